@@ -1,7 +1,8 @@
 /*
  * ssscan.h — C ABI of libssscan.so: the Mamba selective-scan forward and
- * backward, the depthwise causal conv1d backward and the RMSNorm backward,
- * written for NVIDIA GB300 (sm_103a).
+ * backward, the depthwise causal conv1d backward, the RMSNorm backward, linear
+ * attention with a decay for each head and layer norm (each forward and
+ * backward), written for NVIDIA GB300 (sm_103a).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -355,6 +356,99 @@ int ss_scan_step(const void* x, const void* delta, const float* A, const void* B
  */
 int conv1d_causal_step(const void* x, float* conv_state, const float* w, const float* bias, void* out,
                        int B, int D, int d_conv, int silu, int dtype, void* stream);
+
+/*
+ * Linear attention with a decay for each head: the scan's matrix-state form.
+ * Per batch row b, head h and token t, with a state S of [K, V] values,
+ *     S_t = exp(g_t) * S_{t-1} + k_t v_t^T                 (S_{-1} = h0, or 0)
+ *     o_t = scale * S_t^T q_t
+ *   q, k : [B, L, G, K] (dtype), v : [B, L, H, V] (dtype); head h uses q, k of
+ *          group h / (H / G).  ldq, ldk, ldv: elements from one token's row to
+ *          the next (batch rows L * ld apart), so that q, k and v may be column
+ *          ranges of one wider [B, L, W] array; a multiple of 8, at least the
+ *          row's G*K or H*V.
+ *   g    : log decays, fp32: [B, L, H], or with g_per_head [H] (one for each
+ *          head).  Values below -1000 (-inf: forget all) count as -1000.
+ *   lengths : [B] int32 on the device, or NULL: tokens t >= lengths[b] neither
+ *          decay nor add nor read (their inputs may hold anything; o and all
+ *          gradients there are 0); values are clamped to 0 .. L.
+ *   K, V : multiples of 8, at most 128;  H a multiple of G.
+ *   states and their gradients are [B, H, K, V] fp32.
+ * The sequence is worked through in chunks whose inner products are matrix
+ * products; linattn_num_chunks() is their number (the chunk's length goes by
+ * dtype).  Alignment: 16 bytes for every pointer but g, dg and lengths (4).
+ */
+int linattn_num_chunks(int L, int dtype);
+
+/*
+ * linattn_fwd — o [B, L, H, V] (dtype), and where the pointer is given
+ *   ckpt   : [B, H, linattn_num_chunks(L, dtype), K, V] fp32, the state entering
+ *            each chunk, from which linattn_bwd starts (chunks past a row's
+ *            length are not written)
+ *   h_last : [B, H, K, V] fp32, the state after the row's last token
+ * h0 may be NULL (zeros).  workspace: linattn_fwd_workspace_size() bytes (0
+ * when the batch rows and heads fill the GPU by themselves; else a row is cut
+ * in segments whose end states are found first).
+ */
+size_t linattn_fwd_workspace_size(int B, int L, int H, int G, int K, int V, int dtype);
+int linattn_fwd(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv,
+                const float* g, int g_per_head, const float* h0, const int* lengths, void* o, float* ckpt,
+                float* h_last, int B, int L, int H, int G, int K, int V, float scale, int dtype,
+                void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * linattn_bwd — gradient of sum(o * dout) + sum(h_last * dh_last):
+ *   dq, dk : [B, L, G, K], dv : [B, L, H, V] (dtype; overwritten).  They have
+ *            the activations' type, unlike the scan's: the matrix products that
+ *            make them take operands of that type.
+ *   dg     : [B, L, H] fp32, overwritten; with g_per_head [H], accumulated (+=)
+ *   dh0    : [B, H, K, V] fp32, overwritten, or NULL
+ * ckpt: the forward's.  dh_last may be NULL (zero).  With U_t = dL/dS_t =
+ * scale q_t dout_t^T + exp(g_{t+1}) U_{t+1}:
+ *   dq_t = scale S_t dout_t;  dk_t = U_t v_t;  dv_t = U_t^T k_t;
+ *   dg_t = exp(g_t) <S_{t-1}, U_t>;  dh0 = exp(g_0) U_0
+ * (dq, dk summed over the heads of a group).  Sums are in a fixed order: two
+ * identical calls give the same bits.
+ */
+size_t linattn_bwd_workspace_size(int B, int L, int H, int G, int K, int V, int g_per_head, int dtype);
+int linattn_bwd(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv,
+                const float* g, int g_per_head, const int* lengths, const float* ckpt, const void* dout,
+                const float* dh_last, void* dq, void* dk, void* dv, float* dg, float* dh0,
+                int B, int L, int H, int G, int K, int V, float scale, int dtype,
+                void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * linattn_step — one token for B sequences (decode), the state in place:
+ *   q, k : [B, G, K], v, o : [B, H, V] (dtype, dense);  g : [B, H] fp32 (or [H])
+ *   h    : [B, H, K, V] fp32, read and overwritten
+ * Running it L times from h equals linattn_fwd over those tokens from h0 = h
+ * (up to rounding order).
+ */
+int linattn_step(const void* q, const void* k, const void* v, const float* g, int g_per_head, float* h, void* o,
+                 int B, int H, int G, int K, int V, float scale, int dtype, void* stream);
+
+/*
+ * layernorm_fwd — per row of x [rows, dim]:
+ *   mean = mean_i x;  rstd = 1 / sqrt(mean_i (x - mean)^2 + eps)
+ *   y    = (x - mean) * rstd * scale + bias
+ *   x, y : [rows, dim] (dtype; y overwritten, bf16 rounded to nearest even)
+ *   scale, bias : [dim] fp32, bias may be NULL (zero)
+ *   mean, rstd  : [rows] fp32 outputs, each may be NULL
+ * dim a multiple of 8 and at most 32768; eps >= 0; pointers 16-byte aligned.
+ */
+int layernorm_fwd(const void* x, const float* scale, const float* bias, float eps, void* y, float* mean, float* rstd,
+                  int rows, int dim, int dtype, void* stream);
+
+/*
+ * layernorm_bwd — with xh = (x - mean) * rstd and w = dy * scale:
+ *   dx = rstd * (w - mean_i w - xh * mean_i(w * xh))       [rows, dim] fp32, overwritten
+ *   dscale += sum_r dy * xh;  dbias += sum_r dy            [dim] fp32, accumulated
+ * dy, x (dtype); mean, rstd as layernorm_fwd saved them; sizes as there.
+ */
+size_t layernorm_bwd_workspace_size(int rows, int dim);
+int layernorm_bwd(const void* dy, const void* x, const float* scale, const float* mean, const float* rstd,
+                  float* dx, float* dscale, float* dbias, int rows, int dim, int dtype,
+                  void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * ss_count_nonfinite — failure detection: writes to `count` (a device

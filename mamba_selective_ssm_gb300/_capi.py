@@ -25,6 +25,8 @@ SS_BF16 = 1
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
+_ll = ctypes.c_longlong
+_f = ctypes.c_float
 
 # name -> (restype, argtypes), in the order of include/ssscan.h
 SIGNATURES = {
@@ -47,6 +49,15 @@ SIGNATURES = {
     "rmsnorm_fwd": (_i, [_vp, _vp, ctypes.c_float, _vp, _vp, _i, _i, _i, _vp]),
     "ss_scan_step": (_i, [_vp] * 9 + [_i] * 4 + [_vp]),
     "conv1d_causal_step": (_i, [_vp] * 5 + [_i] * 5 + [_vp]),
+    "linattn_num_chunks": (_i, [_i, _i]),
+    "linattn_fwd_workspace_size": (_sz, [_i] * 7),
+    "linattn_fwd": (_i, [_vp, _ll] * 3 + [_vp, _i] + [_vp] * 5 + [_i] * 6 + [_f, _i, _vp, _sz, _vp]),
+    "linattn_bwd_workspace_size": (_sz, [_i] * 8),
+    "linattn_bwd": (_i, [_vp, _ll] * 3 + [_vp, _i] + [_vp] * 9 + [_i] * 6 + [_f, _i, _vp, _sz, _vp]),
+    "linattn_step": (_i, [_vp] * 4 + [_i] + [_vp] * 2 + [_i] * 5 + [_f, _i, _vp]),
+    "layernorm_fwd": (_i, [_vp] * 3 + [_f] + [_vp] * 3 + [_i] * 3 + [_vp]),
+    "layernorm_bwd_workspace_size": (_sz, [_i, _i]),
+    "layernorm_bwd": (_i, [_vp] * 8 + [_i] * 3 + [_vp, _sz, _vp]),
     "ss_count_nonfinite_workspace_size": (_sz, []),
     "ss_count_nonfinite": (_i, [_vp, _sz, _i, _vp, _vp, _sz, _vp]),
     "ss_device_status": (_i, [_vp]),

@@ -1,0 +1,201 @@
+// Shared pieces of the linear attention kernels (linattn_fwd.cu, linattn_bwd.cu,
+// linattn_step.cu): the call's arguments, the decays of a chunk and the plan
+// that cuts a long sequence into segments.
+//
+//   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t       per (batch row, head)
+//
+// A chunk of C tokens with running log decay c_i = g_first + ... + g_i is
+//   o_i   = scale * ( e^{c_i} q_i S_in + sum_{j<=i} e^{c_i - c_j} (q_i.k_j) v_j )
+//   S_out = e^{c_last} S_in + sum_j e^{c_last - c_j} k_j v_j^T
+// so all its products are matrix products and only S passes from chunk to chunk.
+#pragma once
+
+#include "common.cuh"
+
+namespace ssk {
+
+// One call's arguments.  Rows of q, k, v are ld* elements apart (batch rows
+// L * ld*); o, dout and the gradients are dense.
+struct LinAttn {
+  const void *q, *k, *v;
+  long long ldq, ldk, ldv;
+  const float* g;  // [B, L, H], or [H] with g_head
+  int g_head;
+  const int* lengths;  // [B] or null: tokens t >= lengths[b] neither decay nor add nor read
+  int B, L, H, G, K, V;
+  float scale;
+  int nck;        // chunks of a row
+  int nseg, cps;  // segments of a row and chunks per segment
+
+  __device__ __forceinline__ int len(int b) const {
+    if (lengths == nullptr) return L;
+    const int n = lengths[b];
+    return n < 0 ? 0 : n > L ? L : n;
+  }
+  __device__ __forceinline__ float gate(int b, int t, int h) const {
+    return g_head ? g[h] : g[((size_t)b * L + t) * H + h];
+  }
+};
+
+// A log decay in units of log2, as a pair of floats hi + lo.  c_i - c_j of two
+// far tokens is then good to ~2^-45 of c and exp2 of it to the hardware's
+// rounding: a single float c would cost |c| * 2^-24 in the exponent, which after
+// a few strong decays (c = -200) is 1e-5 of every later product.
+struct Dec {
+  float hi, lo;
+};
+__device__ __forceinline__ Dec dec_of(double c) {
+  Dec d;
+  d.hi = (float)c;
+  d.lo = (float)(c - (double)d.hi);
+  return d;
+}
+__device__ __forceinline__ float dec_exp(float hi, float lo) { return ex2(hi) * fmaf(lo, kLn2, 1.0f); }
+// e^{c_i - c_j}
+__device__ __forceinline__ float dec_diff(float hi_i, float lo_i, float hi_j, float lo_j) {
+  return ex2((hi_i - hi_j) + (lo_i - lo_j));
+}
+
+// Log decays below this empty the state in fp32 anyway (e^-1000 = 0); the clamp
+// keeps -inf, a reset, from making c_i - c_j = -inf + inf.
+constexpr float kMinLogDecay = -1000.0f;
+
+// Running log2 decays of the chunk at t0: chi/clo[i] for i < C (a token past
+// the row's end decays by 1).  One warp, C / 32 consecutive tokens a lane.
+template <int C>
+__device__ __forceinline__ void chunk_decays(const LinAttn& p, int b, int h, int t0, int len, int lane, float* chi, float* clo) {
+  constexpr int PER = C / 32;
+  double x[PER];
+  double s = 0.0;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    const int t = t0 + lane * PER + e;
+    float gv = t < len ? p.gate(b, t, h) : 0.0f;
+    if (gv < kMinLogDecay) gv = kMinLogDecay;
+    s += (double)gv * 1.4426950408889634;
+    x[e] = s;
+  }
+  double incl = s;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  const double base = incl - s;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    const Dec d = dec_of(base + x[e]);
+    chi[lane * PER + e] = d.hi;
+    clo[lane * PER + e] = d.lo;
+  }
+}
+
+constexpr int kLinMaxHead = 128;  // widest K, V
+constexpr int kLinChunkF32 = 64;
+
+inline int linattn_chunk(int dtype) { return dtype == SS_F32 ? kLinChunkF32 : 64; }
+
+// Segments: with fewer independent walks (batch rows x heads x column tiles)
+// than the GPU holds at once, a row is cut in `nseg` pieces whose end states
+// are found first.  Each piece costs a second read of its inputs, so no more
+// pieces than fill `slots` walks, and none shorter than four chunks.
+inline void linattn_segments(LinAttn& p, int chunk, long long walks, int slots) {
+  p.nck = (p.L + chunk - 1) / chunk;
+  int n = walks > 0 ? (int)(slots / walks) : 1;
+  if (n > p.nck / 4) n = p.nck / 4;
+  if (n < 1) n = 1;
+  p.cps = (p.nck + n - 1) / n;
+  p.nseg = (p.nck + p.cps - 1) / p.cps;
+}
+
+inline int linattn_validate(int B, int L, int H, int G, int K, int V, int dtype) {
+  if (B <= 0 || L <= 0 || H <= 0 || G <= 0 || K <= 0 || V <= 0) return SS_ERR_DIM;
+  if (dtype != SS_F32 && dtype != SS_BF16) return SS_ERR_UNSUPPORTED;
+  if (H % G != 0) return SS_ERR_DIM;
+  if (K % 8 != 0 || V % 8 != 0) return SS_ERR_ALIGN;
+  if (K > kLinMaxHead || V > kLinMaxHead) return SS_ERR_DIM;
+  return SS_OK;
+}
+
+// a token stride: at least the row it holds, and rows on 16-byte boundaries
+inline int linattn_ld_ok(long long ld, int width) {
+  if (ld < width) return SS_ERR_DIM;
+  return ld % 8 != 0 ? SS_ERR_ALIGN : SS_OK;
+}
+
+// ---------------------------------------------------------------- FP32 tiles
+// C += A B from shared memory on the FMA pipe, 256 threads as 16 x 16: thread
+// (ty, tx) owns rows ty * M/16 + r and columns tx + 16 c of the M x N product.
+// A is stored [M][Kd] (TA false) or [Kd][M]; B is stored [Kd][N] (TB false) or
+// [N][Kd].  Every product of a kernel uses the same ownership, so accumulators
+// of different products combine element by element in registers.
+template <int M, int N, int Kd, bool TA, bool TB, int LDA, int LDB>
+__device__ __forceinline__ void mm(const float* __restrict__ A, const float* __restrict__ B, float (&acc)[M / 16][N / 16], int tid) {
+  constexpr int RM = M / 16, RN = N / 16;
+  const int ty = tid >> 4, tx = tid & 15;
+#pragma unroll 2
+  for (int k = 0; k < Kd; k += 4) {
+    float a[RM][4], b[RN][4];
+#pragma unroll
+    for (int r = 0; r < RM; ++r) {
+      if constexpr (!TA) {
+        const float4 v = *reinterpret_cast<const float4*>(A + (ty * RM + r) * LDA + k);
+        a[r][0] = v.x; a[r][1] = v.y; a[r][2] = v.z; a[r][3] = v.w;
+      }
+    }
+    if constexpr (TA) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int r = 0; r < RM; r += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(A + (k + e) * LDA + ty * RM + r);
+          a[r][e] = v.x; a[r + 1][e] = v.y; a[r + 2][e] = v.z; a[r + 3][e] = v.w;
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < RN; ++c) {
+      if constexpr (TB) {
+        const float4 v = *reinterpret_cast<const float4*>(B + (tx + 16 * c) * LDB + k);
+        b[c][0] = v.x; b[c][1] = v.y; b[c][2] = v.z; b[c][3] = v.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[c][e] = B[(k + e) * LDB + tx + 16 * c];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int r = 0; r < RM; ++r)
+#pragma unroll
+        for (int c = 0; c < RN; ++c) acc[r][c] = fmaf(a[r][e], b[c][e], acc[r][c]);
+  }
+}
+
+template <int R, int Cn>
+__device__ __forceinline__ void zero_acc(float (&acc)[R][Cn]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < Cn; ++c) acc[r][c] = 0.f;
+}
+
+// C tokens x W columns of a strided input into a padded fp32 tile; columns
+// past `width` and tokens past `valid` become zero (their memory is not read).
+template <typename T, int C, int W, int LD>
+__device__ __forceinline__ void load_tile(const T* __restrict__ src, long long ld, int valid, int width, float* dst, int tid) {
+  for (int i = tid; i < C * (W / 8); i += 256) {
+    const int t = i / (W / 8), c = (i % (W / 8)) * 8;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (t < valid && c < width) ActT<T>::ld8(src + (long long)t * ld + c, v);
+    ActT<float>::st8(dst + t * LD + c, v);
+  }
+}
+
+// Row sums of a per-thread [rows][cols] product over the 16 threads of a row.
+__device__ __forceinline__ float row_sum16(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+}  // namespace ssk

@@ -18,6 +18,11 @@ Names and argument order follow include/ssscan.h:
   ``ss_scan_carries(A, delta_sum, summ, init=None, reverse=False)`` -> ``carry``
   (the pieces of a sequence-sharded scan; ``sharded.py`` runs them over ranks)
 * ``conv1d_causal_step(x, conv_state, w, bias=None, silu=False)`` -> ``out`` (state updated in place)
+* ``linattn_fwd(q, k, v, g, h0=None, scale=None, lengths=None)`` -> ``(o, ckpt, h_last)``
+* ``linattn_bwd(q, k, v, g, ckpt, do, dh_last=None, scale=None, lengths=None)`` -> dict of gradients
+* ``linattn_step(q, k, v, g, h, scale=None)`` -> ``o`` (h updated in place)
+* ``layernorm_fwd(x, scale, bias, eps)`` -> ``(y, mean, rstd)``
+* ``layernorm_bwd(dy, x, scale, mean, rstd, dscale=None, dbias=None)`` -> ``(dx, dscale, dbias)``
 
 Activations are ``torch.float32`` or ``torch.bfloat16`` CUDA tensors, contiguous;
 parameters, states and gradients are ``torch.float32``.
@@ -358,6 +363,191 @@ def conv1d_causal_step(x, conv_state, w, bias=None, silu: bool = False):
                                 _stream())
     check(rc, "conv1d_causal_step")
     return out
+
+
+def linattn_num_chunks(L: int, dtype) -> int:
+    """Checkpoints a row of L tokens has (``ckpt`` is [B, H, that, K, V])."""
+    return load().linattn_num_chunks(L, _DT[dtype])
+
+
+def _rows(t, name, shape, dtype, device):
+    """A [B, L, heads, width] input whose tokens may lie further apart than their own rows (a column range of a
+    wider [B, L, W] array): its token stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    B, L, n, w = shape
+    sb, sl, sn, sw = t.stride()
+    if L == 1 and B > 1:
+        sl = sb  # one token a row: rows are the batch's
+    elif L == 1:
+        sl = n * w
+    if (w > 1 and sw != 1) or (n > 1 and sn != w) or (B > 1 and L > 0 and sb != L * sl):
+        raise ValueError(f"{name} must hold each token's heads contiguously and its batch rows L tokens apart, got "
+                         f"strides {t.stride()}")
+    return sl
+
+
+def _linattn_sizes(q, v):
+    if not isinstance(q, torch.Tensor) or not isinstance(v, torch.Tensor):
+        raise TypeError("q, k, v must be torch.Tensor")
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError(f"q, k must be [B, L, G, K] and v [B, L, H, V], got {tuple(q.shape)} and {tuple(v.shape)}")
+    B, L, G, K = q.shape
+    return B, L, v.shape[2], G, K, v.shape[3]
+
+
+def _linattn_gate(g, B, L, H, dev):
+    """1 when g is one log decay for each head, 0 when it has one for each token."""
+    if isinstance(g, torch.Tensor) and g.dim() == 1:
+        _req(g, "g", (H,), torch.float32, dev)
+        return 1
+    _req(g, "g", (B, L, H), torch.float32, dev)
+    return 0
+
+
+def _scratch(workspace, need, dev):
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def linattn_fwd(q, k, v, g, h0=None, scale=None, lengths=None, want_ckpt: bool = True, want_h_last: bool = True,
+                workspace=None):
+    """Linear attention with a decay for each head -> ``(o, ckpt, h_last)``:
+    ``S_t = exp(g_t) S_{t-1} + k_t v_t^T``, ``o_t = scale * S_t^T q_t`` from ``S = h0``.
+
+    ``q, k`` [B, L, G, K] are shared by the H/G heads of a group of ``v`` [B, L, H, V]; each may be a column range of
+    a wider [B, L, W] tensor.  ``g`` are log decays, fp32 [B, L, H] or one for each head [H].  ``lengths`` (int32 [B])
+    ends each row; past it o is 0 and the state stays.  ``scale`` is ``K ** -0.5`` unless given.  ``ckpt`` (None unless
+    ``want_ckpt``) is what ``linattn_bwd`` starts from."""
+    lib = load()
+    B, L, H, G, K, V = _linattn_sizes(q, v)
+    dev, dt = q.device, q.dtype
+    sdt = _act_dtype(q)
+    ldq = _rows(q, "q", (B, L, G, K), dt, dev)
+    ldk = _rows(k, "k", (B, L, G, K), dt, dev)
+    ldv = _rows(v, "v", (B, L, H, V), dt, dev)
+    per_head = _linattn_gate(g, B, L, H, dev)
+    if h0 is not None:
+        _req(h0, "h0", (B, H, K, V), torch.float32, dev)
+    if lengths is not None:
+        _req(lengths, "lengths", (B,), torch.int32, dev)
+    o = torch.empty((B, L, H, V), device=dev, dtype=dt)
+    f32 = dict(device=dev, dtype=torch.float32)
+    ckpt = torch.empty((B, H, lib.linattn_num_chunks(L, sdt), K, V), **f32) if want_ckpt else None
+    h_last = torch.empty((B, H, K, V), **f32) if want_h_last else None
+    workspace, ws_have = _scratch(workspace, lib.linattn_fwd_workspace_size(B, L, H, G, K, V, sdt), dev)
+    rc = lib.linattn_fwd(_p(q), ldq, _p(k), ldk, _p(v), ldv, _p(g), per_head, _p(h0), _p(lengths), _p(o), _p(ckpt),
+                         _p(h_last), B, L, H, G, K, V, K ** -0.5 if scale is None else scale, sdt, _p(workspace), ws_have,
+                         _stream())
+    check(rc, "linattn_fwd")
+    return o, ckpt, h_last
+
+
+def linattn_bwd(q, k, v, g, ckpt, do, dh_last=None, scale=None, lengths=None, dg=None, want_dh0: bool = True,
+                workspace=None):
+    """Gradients of ``sum(o * do)`` (+ ``sum(h_last * dh_last)``) through ``linattn_fwd`` called with the same q, k, v, g,
+    scale and lengths -> dict ``dq, dk, dv`` (q's type), ``dg``, ``dh0`` (fp32).  With one decay for each head ``dg`` [H]
+    accumulates into the given tensor (zeros when None)."""
+    lib = load()
+    B, L, H, G, K, V = _linattn_sizes(q, v)
+    dev, dt = q.device, q.dtype
+    sdt = _act_dtype(q)
+    ldq = _rows(q, "q", (B, L, G, K), dt, dev)
+    ldk = _rows(k, "k", (B, L, G, K), dt, dev)
+    ldv = _rows(v, "v", (B, L, H, V), dt, dev)
+    per_head = _linattn_gate(g, B, L, H, dev)
+    _req(ckpt, "ckpt", (B, H, lib.linattn_num_chunks(L, sdt), K, V), torch.float32, dev)
+    _req(do, "do", (B, L, H, V), dt, dev)
+    if dh_last is not None:
+        _req(dh_last, "dh_last", (B, H, K, V), torch.float32, dev)
+    if lengths is not None:
+        _req(lengths, "lengths", (B,), torch.int32, dev)
+    f32 = dict(device=dev, dtype=torch.float32)
+    if dg is not None:
+        _req(dg, "dg", g.shape, torch.float32, dev)
+    else:
+        dg = torch.zeros((H,), **f32) if per_head else torch.empty((B, L, H), **f32)
+    out = {"dq": torch.empty((B, L, G, K), device=dev, dtype=dt), "dk": torch.empty((B, L, G, K), device=dev, dtype=dt),
+           "dv": torch.empty((B, L, H, V), device=dev, dtype=dt), "dg": dg,
+           "dh0": torch.empty((B, H, K, V), **f32) if want_dh0 else None}
+    workspace, ws_have = _scratch(workspace, lib.linattn_bwd_workspace_size(B, L, H, G, K, V, per_head, sdt), dev)
+    rc = lib.linattn_bwd(_p(q), ldq, _p(k), ldk, _p(v), ldv, _p(g), per_head, _p(lengths), _p(ckpt), _p(do), _p(dh_last),
+                         _p(out["dq"]), _p(out["dk"]), _p(out["dv"]), _p(dg), _p(out["dh0"]), B, L, H, G, K, V,
+                         K ** -0.5 if scale is None else scale, sdt, _p(workspace), ws_have, _stream())
+    check(rc, "linattn_bwd")
+    return out
+
+
+def linattn_step(q, k, v, g, h, scale=None):
+    """One token for B sequences: updates ``h`` [B, H, K, V] in place and returns o [B, H, V].
+    ``q, k`` [B, G, K], ``v`` [B, H, V], ``g`` fp32 [B, H] or [H]."""
+    lib = load()
+    B, G, K = q.shape
+    H, V = v.shape[1:]
+    dev, dt = q.device, q.dtype
+    sdt = _act_dtype(q)
+    _req(q, "q", (B, G, K), dt, dev)
+    _req(k, "k", (B, G, K), dt, dev)
+    _req(v, "v", (B, H, V), dt, dev)
+    per_head = 1 if g.dim() == 1 else 0
+    _req(g, "g", (H,) if per_head else (B, H), torch.float32, dev)
+    _req(h, "h", (B, H, K, V), torch.float32, dev)
+    o = torch.empty_like(v)
+    rc = lib.linattn_step(_p(q), _p(k), _p(v), _p(g), per_head, _p(h), _p(o), B, H, G, K, V,
+                          K ** -0.5 if scale is None else scale, sdt, _stream())
+    check(rc, "linattn_step")
+    return o
+
+
+def layernorm_fwd(x, scale, bias, eps: float, want_stats: bool = True):
+    """Layer norm of the rows of x [rows, dim]: ``(y, mean, rstd)`` with y in x's dtype and the statistics fp32 (None
+    unless ``want_stats``); ``bias`` may be None."""
+    lib = load()
+    R, N = x.shape
+    dev = x.device
+    dt = _act_dtype(x)
+    _req(x, "x", (R, N), x.dtype, dev)
+    _req(scale, "scale", (N,), torch.float32, dev)
+    if bias is not None:
+        _req(bias, "bias", (N,), torch.float32, dev)
+    y = torch.empty_like(x)
+    mean = torch.empty((R,), device=dev, dtype=torch.float32) if want_stats else None
+    rstd = torch.empty((R,), device=dev, dtype=torch.float32) if want_stats else None
+    rc = lib.layernorm_fwd(_p(x), _p(scale), _p(bias), float(eps), _p(y), _p(mean), _p(rstd), R, N, dt, _stream())
+    check(rc, "layernorm_fwd")
+    return y, mean, rstd
+
+
+def layernorm_bwd(dy, x, scale, mean, rstd, dscale=None, dbias=None, workspace=None):
+    """Layer norm backward -> ``(dx, dscale, dbias)``, all fp32; dscale and dbias accumulate into the given tensors
+    (zeros when None)."""
+    lib = load()
+    R, N = x.shape
+    dev = x.device
+    dt = _act_dtype(x)
+    _req(dy, "dy", (R, N), x.dtype, dev)
+    _req(x, "x", (R, N), x.dtype, dev)
+    _req(scale, "scale", (N,), torch.float32, dev)
+    _req(mean, "mean", (R,), torch.float32, dev)
+    _req(rstd, "rstd", (R,), torch.float32, dev)
+    f32 = dict(device=dev, dtype=torch.float32)
+    dscale = torch.zeros((N,), **f32) if dscale is None else _req(dscale, "dscale", (N,), torch.float32, dev)
+    dbias = torch.zeros((N,), **f32) if dbias is None else _req(dbias, "dbias", (N,), torch.float32, dev)
+    dx = torch.empty((R, N), **f32)
+    workspace, ws_have = _scratch(workspace, lib.layernorm_bwd_workspace_size(R, N), dev)
+    rc = lib.layernorm_bwd(_p(dy), _p(x), _p(scale), _p(mean), _p(rstd), _p(dx), _p(dscale), _p(dbias), R, N, dt,
+                           _p(workspace), ws_have, _stream())
+    check(rc, "layernorm_bwd")
+    return dx, dscale, dbias
 
 
 def count_nonfinite(t, workspace=None) -> int:
