@@ -12,11 +12,9 @@
 // the same number, but loses what the sums have in common):
 //   dg_t = sum_{j<t<=i} M_ij + sum_{i>=t} q_i.(scale e^{c_i} S_in do_i)
 //        + sum_{j<t} k_j.(e^{c_last-c_j} U v_j) + e^{c_last} <S_in, U>,   M_ij = P_ij (do_i.v_j)
-#include "linattn_common.cuh"
+#include "linattn_tc.cuh"
 
 namespace {
-
-using namespace ssk;
 
 template <int KP, int VP>
 struct BwdSmem {
@@ -31,10 +29,11 @@ struct BwdOut {
   float* dh0;
 };
 
+// ---------------------------------------------------------------- fp32: FMA pipe
 // A CTA walks the chunks of one (batch row, head, segment) from the last to the
 // first with U in registers.  SUM only finds the segment's U from zero.
-template <typename T, int KP, int VP, bool SUM>
-__global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const T* __restrict__ dout, const float* __restrict__ ckpt,
+template <int KP, int VP, bool SUM>
+__global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const float* __restrict__ dout, const float* __restrict__ ckpt,
                                                           const float* __restrict__ u0, BwdOut out, float* __restrict__ uend,
                                                           double* __restrict__ udec) {
   using Sm = BwdSmem<KP, VP>;
@@ -49,11 +48,11 @@ __global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const T* __
   const int gh = h / (p.H / p.G);
   const int len = p.len(b);
   const long long bh = (long long)b * p.H + h, kv = (long long)p.K * p.V;
-  const T* q = static_cast<const T*>(p.q) + (long long)b * p.L * p.ldq + (long long)gh * p.K;
-  const T* k = static_cast<const T*>(p.k) + (long long)b * p.L * p.ldk + (long long)gh * p.K;
-  const T* v = static_cast<const T*>(p.v) + (long long)b * p.L * p.ldv + (long long)h * p.V;
+  const float* q = static_cast<const float*>(p.q) + (long long)b * p.L * p.ldq + (long long)gh * p.K;
+  const float* k = static_cast<const float*>(p.k) + (long long)b * p.L * p.ldk + (long long)gh * p.K;
+  const float* v = static_cast<const float*>(p.v) + (long long)b * p.L * p.ldv + (long long)h * p.V;
   const long long ldo = (long long)p.H * p.V;
-  const T* d = dout + (long long)b * p.L * ldo + (long long)h * p.V;
+  const float* d = dout + (long long)b * p.L * ldo + (long long)h * p.V;
 
   float U[RK][RV];
   zero_acc(U);
@@ -78,7 +77,7 @@ __global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const T* __
         const long long at = (((long long)b * p.L + t0 + i) * p.H + h) * p.K + kk;
         const float x = i < valid ? a[r][c] : 0.f;
         if (part != nullptr) part[at] = x;
-        else ActT<T>::st1(static_cast<T*>(typed) + at, x);
+        else static_cast<float*>(typed)[at] = x;
       }
   };
   double total = 0.0;
@@ -94,7 +93,7 @@ __global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const T* __
         put_qk(out.dq, out.dqp, t0, rows, 0, z);
         put_qk(out.dk, out.dkp, t0, rows, 0, z);
         for (int i = tid; i < rows * p.V; i += 256)
-          ActT<T>::st1(static_cast<T*>(out.dv) + (((long long)b * p.L + t0 + i / p.V) * p.H + h) * p.V + i % p.V, 0.f);
+          static_cast<float*>(out.dv)[(((long long)b * p.L + t0 + i / p.V) * p.H + h) * p.V + i % p.V] = 0.f;
         if (p.g_head) {
           if (tid == 0) out.dg[((long long)b * p.nck + ck) * p.H + h] = 0.f;
         } else if (tid < rows) {
@@ -103,12 +102,12 @@ __global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const T* __
       }
       continue;
     }
-    if (tid < 32) chunk_decays<C>(p, b, h, t0, len, tid, sm.chi, sm.clo);
-    load_tile<T, C, KP, LK>(q + t0 * p.ldq, p.ldq, valid, p.K, sm.q, tid);
-    load_tile<T, C, VP, LV>(d + t0 * ldo, ldo, valid, p.V, sm.d, tid);
+    if (tid < 32) chunk_decays<C>(p, b, h, t0, len, tid, [&](int i, Dec d) { sm.chi[i] = d.hi; sm.clo[i] = d.lo; });
+    load_tile<C, KP, LK>(q + t0 * p.ldq, p.ldq, valid, p.K, sm.q, tid);
+    load_tile<C, VP, LV>(d + t0 * ldo, ldo, valid, p.V, sm.d, tid);
     if (!SUM) {
-      load_tile<T, C, KP, LK>(k + t0 * p.ldk, p.ldk, valid, p.K, sm.k, tid);
-      load_tile<T, C, VP, LV>(v + t0 * p.ldv, p.ldv, valid, p.V, sm.v, tid);
+      load_tile<C, KP, LK>(k + t0 * p.ldk, p.ldk, valid, p.K, sm.k, tid);
+      load_tile<C, VP, LV>(v + t0 * p.ldv, p.ldv, valid, p.V, sm.v, tid);
       const float* src = ckpt + (bh * p.nck + ck) * kv;
 #pragma unroll
       for (int r = 0; r < RK; ++r)
@@ -193,7 +192,7 @@ __global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const T* __
         for (int c = 0; c < RV; ++c) {
           const int i = ty * 4 + r, vv = tx + 16 * c;
           if (i < rows && vv < p.V)
-            ActT<T>::st1(static_cast<T*>(out.dv) + (((long long)b * p.L + t0 + i) * p.H + h) * p.V + vv, i < valid ? dv[r][c] : 0.f);
+            static_cast<float*>(out.dv)[(((long long)b * p.L + t0 + i) * p.H + h) * p.V + vv] = i < valid ? dv[r][c] : 0.f;
         }
       float ki[4][RK];
       zero_acc(ki);
@@ -308,21 +307,453 @@ __global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const T* __
   if (SUM && tid == 0) udec[bh * p.nseg + seg] = total;
 }
 
-// In place over the segments of a (batch row, head), last to first: the U found
-// from zero becomes the U arriving at the segment's end.
-__global__ void __launch_bounds__(256) linattn_bwd_join_kernel(const float* __restrict__ dh_last, float* __restrict__ st,
-                                                               const double* __restrict__ dec, long long kv, int nseg) {
-  const long long bh = blockIdx.y;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= kv) return;
-  float s = dh_last != nullptr ? dh_last[bh * kv + i] : 0.f;
-  for (int n = nseg - 1; n >= 0; --n) {
-    float* at = st + (bh * nseg + n) * kv + i;
-    const Dec d = dec_of(dec[bh * nseg + n]);
-    const float end = *at;
-    *at = s;
-    s = fmaf(dec_exp(d.hi, d.lo), s, end);
+// ---------------------------------------------------------------- bf16: tensor cores
+// One CTA of 16 warps walks the chunks (128 tokens) of a (batch row, head,
+// segment) from the last to the first.  U stays in registers in fp32 (thread =
+// row d of K and a quarter of the V columns).  Scores are taken transposed
+// (tensor-memory lane = key token j), so that P^T and dP^T are A operands where
+// they are made, and one shared-memory copy of dP^T serves dq.
+//   T0 = k q^T, T1 = v do^T                            -> P^T, dP^T (bf16), M for dg
+//   T2 = do S_in^T (three terms)                       -> * scale e^{c_i}, dotted with q for dg
+//   T0 = k U (one term), T1 = v U^T (three terms)      -> * e^{c_last-c_j}, T1 dotted with k for dg
+//   T0 += P^T do = dv, T1 += dP^T q = dk, T2 += dP k = dq
+//   T3 = q^T (scale e^{c_i} do) (three terms)          -> U
+// What ends in fp32 (dg, dh0, U) takes its fp32 operands as three bf16 terms;
+// a term of dq, dk or dv is rounded to bf16 once on its way.
+constexpr int kBwdThreads = 512;
+
+template <int VP>
+struct BwdTc {
+  static constexpr int vt = kTC * VP * 2;  // bytes of a tile VP columns wide
+  static constexpr int q = 0, k = q + 2 * kPanel, x = k + 2 * kPanel, v = x + 2 * kPanel, d = v + vt, y0 = d + vt, y1 = y0 + vt, dec = y1 + vt;
+  static constexpr int bar = dec + DecTile::bytes, tm = bar + 16, bytes = tm + 8;
+  // in x while it is free: parts of dg
+  static constexpr int a = x, b = a + 4 * kTC * 4, rect = b + 4 * kTC * 4, tot = rect + 4 * kTC * 4, thr = tot + 4 * kTC * 4;
+  static constexpr int T0 = 0, T1 = 128, T2 = 256, T3 = 384, Pb = 384, dPb = 448, cols = 512;
+};
+
+// lane l gets the sum over the warp's lanes of x[l]
+__device__ __forceinline__ float col_sums32(float (&x)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int e = 0; e < o; ++e) {
+      const float give = up ? x[e] : x[e + o], keep = up ? x[e + o] : x[e];
+      x[e] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
   }
+  return x[0];
+}
+
+template <int VP>
+__global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn p, const __nv_bfloat16* __restrict__ dout,
+                                                                       const float* __restrict__ ckpt,
+                                                                       const float* __restrict__ u0, BwdOut out) {
+  using L = BwdTc<VP>;
+  constexpr int VQ = VP / 4, NU = VQ / 8;  // columns and 16-byte units of a thread's quarter of V
+  extern __shared__ __align__(1024) unsigned char raw[];
+  const uint32_t sb = smem_u32(raw);
+  const DecTile dec{sb + L::dec};
+  uint64_t* bar = reinterpret_cast<uint64_t*>(raw + L::bar);
+  uint32_t* tma = reinterpret_cast<uint32_t*>(raw + L::tm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row = (warp & 3) * 32 + lane, cq = warp >> 2;  // tensor-memory lane, quarter of the columns
+  long long id = blockIdx.x;
+  const int seg = (int)(id % p.nseg);
+  id /= p.nseg;
+  const int h = (int)(id % p.H), b = (int)(id / p.H);
+  const int gh = h / (p.H / p.G);
+  const int len = p.len(b);
+  const long long bh = (long long)b * p.H + h, kv = (long long)p.K * p.V, ldo = (long long)p.H * p.V;
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (long long)b * p.L * p.ldq + (long long)gh * p.K;
+  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.k) + (long long)b * p.L * p.ldk + (long long)gh * p.K;
+  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + (long long)b * p.L * p.ldv + (long long)h * p.V;
+  const __nv_bfloat16* d = dout + (long long)b * p.L * ldo + (long long)h * p.V;
+
+  if (tid == 0) {
+    mbar_init(&bar[0], 1);
+    mbar_init(&bar[1], 1);
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tma, L::cols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tm = *tma;
+  const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
+  const int ks = (p.K + 15) / 16, vs = (p.V + 15) / 16;  // contraction steps over K and V
+
+  float U[VQ];
+#pragma unroll
+  for (int e = 0; e < VQ; ++e) U[e] = 0.f;
+  if (u0 != nullptr && row < p.K) {
+    const float* src = u0 + ((p.nseg > 1 ? bh * p.nseg + seg : bh) * p.K + row) * p.V + cq * VQ;
+#pragma unroll
+    for (int e = 0; e < VQ; e += 4)
+      if (cq * VQ + e < p.V) {
+        const float4 x = *reinterpret_cast<const float4*>(src + e);
+        U[e] = x.x; U[e + 1] = x.y; U[e + 2] = x.z; U[e + 3] = x.w;
+      }
+  }
+  auto valid_of = [&](int ck) { const int n = len - ck * kTC; return n < 0 ? 0 : n < kTC ? n : kTC; };
+  auto load_k = [&](int ck) {
+    load_tile_tc<16, kBwdThreads>(k + (long long)ck * kTC * p.ldk, p.ldk, valid_of(ck), p.K, sb + L::k, tid);
+  };
+  auto load_rest = [&](int ck) {
+    const int n = valid_of(ck);
+    const long long t0 = (long long)ck * kTC;
+    load_tile_tc<16, kBwdThreads>(q + t0 * p.ldq, p.ldq, n, p.K, sb + L::q, tid);
+    load_tile_tc<VP / 8, kBwdThreads>(d + t0 * ldo, ldo, n, p.V, sb + L::d, tid);
+    load_tile_tc<VP / 8, kBwdThreads>(v + t0 * p.ldv, p.ldv, n, p.V, sb + L::v, tid);
+    if (warp == 0) chunk_decays<kTC>(p, b, h, ck * kTC, len, lane, [&](int i, Dec e) { dec.put(i, e); });
+  };
+  // 32 gradients of q or k of token row i (columns cq * 32 ...): typed, or this head's fp32 part
+  auto put_qk = [&](void* typed, float* part, int t0, const uint32_t (&r)[32], bool live) {
+    if (t0 + row >= p.L) return;
+    const long long at = (((long long)b * p.L + t0 + row) * p.H + h) * p.K + cq * 32;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (cq * 32 + u * 8 >= p.K) continue;
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = live ? __uint_as_float(r[8 * u + e]) : 0.f;
+      if (part != nullptr) ActT<float>::st8(part + at + 8 * u, x);
+      else ActT<__nv_bfloat16>::st8(static_cast<__nv_bfloat16*>(typed) + at + 8 * u, x);
+    }
+  };
+  // the three terms of a [K][V] fp32 state, this thread's row and quarter
+  auto put_terms = [&](const float (&s)[VQ], uint32_t t0, uint32_t t1, uint32_t t2) {
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = s[8 * u + e];
+      const uint32_t at = tile_at(row, cq * NU + u);
+      sts16(sb + t0 + at, take_term(x));
+      sts16(sb + t1 + at, take_term(x));
+      sts16(sb + t2 + at, take_term(x));
+    }
+  };
+
+  const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
+  int cend = (len + kTC - 1) / kTC;
+  cend = cend < c0 ? c0 : cend < c1 ? cend : c1;
+  for (int ck = cend; ck < c1; ++ck) {  // past the row's end
+    uint32_t z[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) z[e] = 0u;
+    put_qk(out.dq, out.dqp, ck * kTC, z, false);
+    put_qk(out.dk, out.dkp, ck * kTC, z, false);
+    const int rows = p.L - ck * kTC < kTC ? p.L - ck * kTC : kTC;
+    for (int i = tid; i < rows * (p.V / 8); i += kBwdThreads)
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out.dv) + (((long long)b * p.L + ck * kTC + i / (p.V / 8)) * p.H + h) * p.V +
+                                i % (p.V / 8) * 8) = make_uint4(0u, 0u, 0u, 0u);
+    if (p.g_head) {
+      if (tid == 0) out.dg[((long long)b * p.nck + ck) * p.H + h] = 0.f;
+    } else if (tid < rows) {
+      out.dg[((long long)b * p.L + ck * kTC + tid) * p.H + h] = 0.f;
+    }
+  }
+  uint32_t ph0 = 0, ph1 = 0;
+  bool ok = true;
+  auto wait0 = [&]() { ok = mbar_wait_bounded(&bar[0], ph0, kWaitLimitNs); ph0 ^= 1; };
+  auto wait1 = [&]() { ok = mbar_wait_bounded(&bar[1], ph1, kWaitLimitNs); ph1 ^= 1; };
+  if (c0 < cend) {
+    load_k(cend - 1);
+    load_rest(cend - 1);
+  }
+  for (int ck = cend - 1; ck >= c0; --ck) {
+    const int t0 = ck * kTC, valid = valid_of(ck);
+    float through = 0.f;  // <S_in, U>, this thread's part
+    {
+      float S[VQ];
+#pragma unroll
+      for (int e = 0; e < VQ; e += 4) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < p.K && cq * VQ + e < p.V)
+          x = *reinterpret_cast<const float4*>(ckpt + ((bh * p.nck + ck) * p.K + row) * p.V + cq * VQ + e);
+        S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
+      }
+#pragma unroll
+      for (int e = 0; e < VQ; ++e) through = fmaf(S[e], U[e], through);
+      put_terms(S, L::y0, L::y1, L::x);
+    }
+    cp_wait_all();
+    fence_proxy_async_smem();
+    tc_fence_before_sync();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after_sync();
+      const uint32_t id128 = mma_idesc(128, false, false);
+      for (int s = 0; s < ks; ++s) mma_ss(tm + L::T0, desc_rows(sb + L::k, s), desc_rows(sb + L::q, s), id128, s > 0);
+      for (int s = 0; s < vs; ++s) mma_ss(tm + L::T1, desc_rows(sb + L::v, s), desc_rows(sb + L::d, s), id128, s > 0);
+      mma_commit(&bar[0]);
+      for (int t = 2; t >= 0; --t)
+        for (int s = 0; s < vs; ++s)
+          mma_ss(tm + L::T2, desc_rows(sb + L::d, s), desc_rows(sb + (t == 0 ? L::y0 : t == 1 ? L::y1 : L::x), s), id128, t < 2 || s > 0);
+      mma_commit(&bar[1]);
+    }
+    const Dec last = dec.get(kTC - 1), own = dec.get(row);
+    const float elast = dec_exp(last.hi, last.lo), into = p.scale * dec_exp(own.hi, own.lo);
+    const float rest = dec_diff(last.hi, last.lo, own.hi, own.lo);
+    wait0();
+    if (__syncthreads_or(!ok)) break;
+    tc_fence_after_sync();
+    float rect = 0.f, tot = 0.f;
+    if (cq * 32 + 31 >= (row & ~31)) {  // some query token of this quarter is at or after this warp's key tokens
+      float m[32];
+#pragma unroll
+      for (int g = 1; g >= 0; --g) {
+        const int i0 = cq * 32 + g * 16;
+        uint32_t s[16], t[16], w[8], z[8];
+        tmem_ld16(tl + L::T0 + i0, s);
+        tmem_ld16(tl + L::T1 + i0, t);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 14; e >= 0; e -= 2) {
+          const int i = i0 + e;
+          Dec a, c;
+          dec.get2(i, a, c);
+          const float w0 = i >= row ? p.scale * dec_diff(a.hi, a.lo, own.hi, own.lo) : 0.f;
+          const float w1 = i + 1 >= row ? p.scale * dec_diff(c.hi, c.lo, own.hi, own.lo) : 0.f;
+          const float d0 = __uint_as_float(t[e]), d1 = __uint_as_float(t[e + 1]);
+          const float p0 = i >= row ? __uint_as_float(s[e]) * w0 : 0.f, p1 = i + 1 >= row ? __uint_as_float(s[e + 1]) * w1 : 0.f;
+          w[e / 2] = pack_bf16(p0, p1);
+          z[e / 2] = pack_bf16(i >= row ? d0 * w0 : 0.f, i + 1 >= row ? d1 * w1 : 0.f);
+          tot += i + 1 >= row ? p1 * d1 : 0.f;  // paths from j to this query token or a later one of the quarter
+          m[g * 16 + e + 1] = i + 1 > row ? tot : 0.f;
+          tot += i >= row ? p0 * d0 : 0.f;
+          m[g * 16 + e] = i > row ? tot : 0.f;
+        }
+        tmem_st8u(tl + L::Pb + i0 / 2, w);
+        tmem_st8u(tl + L::dPb + i0 / 2, z);
+      }
+      rect = col_sums32(m, lane);
+    } else {
+      uint32_t z[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) z[e] = 0u;
+      tmem_st16(tl + L::Pb + cq * 16, z);
+      tmem_st16(tl + L::dPb + cq * 16, z);
+    }
+    tmem_wait_st();
+    wait1();
+    if (__syncthreads_or(!ok)) break;
+    tc_fence_after_sync();
+    put_terms(U, L::y0, L::y1, L::x);
+    float dot_a = 0.f;
+    {
+      uint32_t r[32];
+      tmem_ld32(tl + L::T2 + cq * 32, r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float x[8];
+        Raw8<__nv_bfloat16>::wide(lds16(sb + L::q + tile_at(row, cq * 4 + u)), x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float y = __uint_as_float(r[8 * u + e]) * into;
+          dot_a = fmaf(x[e], y, dot_a);
+          r[8 * u + e] = __float_as_uint(y);
+        }
+      }
+      tmem_st32(tl + L::T2 + cq * 32, r);
+      tmem_wait_st();
+    }
+    fence_proxy_async_smem();
+    tc_fence_before_sync();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after_sync();
+      const uint32_t id128 = mma_idesc(128, false, false);
+      for (int s = 0; s < ks; ++s) mma_ss(tm + L::T0, desc_rows(sb + L::k, s), desc_cols(sb + L::y0, s), mma_idesc(VP, false, true), s > 0);
+      for (int t = 2; t >= 0; --t)
+        for (int s = 0; s < vs; ++s)
+          mma_ss(tm + L::T1, desc_rows(sb + L::v, s), desc_rows(sb + (t == 0 ? L::y0 : t == 1 ? L::y1 : L::x), s), id128, t < 2 || s > 0);
+      mma_commit(&bar[0]);
+    }
+    wait0();
+    if (__syncthreads_or(!ok)) break;
+    tc_fence_after_sync();
+    // operands of the last products: dP^T in shared memory, scale e^{c_i} do in three terms (the third in v's place)
+    {
+      uint32_t z[16];
+      tmem_ld16(tl + L::dPb + cq * 16, z);
+      tmem_wait_ld();
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        sts16(sb + L::x + tile_at(row, cq * 4 + u), make_uint4(z[4 * u], z[4 * u + 1], z[4 * u + 2], z[4 * u + 3]));
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        const uint32_t at = tile_at(row, cq * NU + u);
+        float x[8];
+        Raw8<__nv_bfloat16>::wide(lds16(sb + L::d + at), x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= into;
+        sts16(sb + L::y0 + at, take_term(x));
+        sts16(sb + L::y1 + at, take_term(x));
+        sts16(sb + L::v + at, take_term(x));
+      }
+    }
+    float dot_b = 0.f;
+    {
+      uint32_t r[32];
+      tmem_ld32(tl + L::T1 + cq * 32, r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float x[8];
+        Raw8<__nv_bfloat16>::wide(lds16(sb + L::k + tile_at(row, cq * 4 + u)), x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float y = __uint_as_float(r[8 * u + e]) * rest;
+          dot_b = fmaf(x[e], y, dot_b);
+          r[8 * u + e] = __float_as_uint(y);
+        }
+      }
+      tmem_st32(tl + L::T1 + cq * 32, r);
+      tmem_scale<VQ>(tl + L::T0 + cq * VQ, rest);
+      tmem_wait_st();
+    }
+    fence_proxy_async_smem();
+    tc_fence_before_sync();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after_sync();
+      for (int s = 0; s < kTC / 16; ++s) mma_ts(tm + L::T0, tm + L::Pb + s * 8, desc_cols(sb + L::d, s), mma_idesc(VP, false, true), true);
+      for (int s = 0; s < kTC / 16; ++s) mma_ts(tm + L::T1, tm + L::dPb + s * 8, desc_cols(sb + L::q, s), mma_idesc(128, false, true), true);
+      for (int s = 0; s < kTC / 16; ++s)
+        mma_ss(tm + L::T2, desc_cols(sb + L::x, s), desc_cols(sb + L::k, s), mma_idesc(128, true, true), true);
+      mma_commit(&bar[1]);
+    }
+    wait1();
+    if (__syncthreads_or(!ok)) break;
+    tc_fence_after_sync();
+    if (tid == 0) {  // into the scores' place, whose readers are done
+      for (int t = 2; t >= 0; --t)
+        for (int s = 0; s < kTC / 16; ++s)
+          mma_ss(tm + L::T3, desc_cols(sb + L::q, s), desc_cols(sb + (t == 0 ? L::y0 : t == 1 ? L::y1 : L::v), s), mma_idesc(VP, true, true),
+                 t < 2 || s > 0);
+      mma_commit(&bar[0]);
+    }
+    if (ck > c0) load_k(ck - 1);
+    {  // what dg is summed from, in x's place
+      float* f = reinterpret_cast<float*>(raw);
+      f[L::a / 4 + cq * kTC + row] = dot_a;
+      f[L::b / 4 + cq * kTC + row] = dot_b;
+      f[L::tot / 4 + cq * kTC + row] = tot;
+      f[L::rect / 4 + (warp & 3) * kTC + cq * 32 + lane] = rect;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) through += __shfl_xor_sync(0xffffffffu, through, o);
+      if (lane == 0) f[L::thr / 4 + warp] = through;
+    }
+    {
+      uint32_t r[32];
+      tmem_ld32(tl + L::T2 + cq * 32, r);
+      tmem_wait_ld();
+      put_qk(out.dq, out.dqp, t0, r, row < valid);
+      tmem_ld32(tl + L::T1 + cq * 32, r);
+      tmem_wait_ld();
+      put_qk(out.dk, out.dkp, t0, r, row < valid);
+    }
+    {
+      uint32_t r[VQ];
+      tmem_ldn(tl + L::T0 + cq * VQ, r);
+      tmem_wait_ld();
+      if (t0 + row < p.L) {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out.dv) + (((long long)b * p.L + t0 + row) * p.H + h) * p.V + cq * VQ;
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+          if (cq * VQ + u * 8 >= p.V) continue;
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = row < valid ? __uint_as_float(r[8 * u + e]) : 0.f;
+          ActT<__nv_bfloat16>::st8(dst + 8 * u, x);
+        }
+      }
+    }
+    wait0();
+    if (__syncthreads_or(!ok)) break;
+    tc_fence_after_sync();
+    if (warp < 4) {  // dg of tokens t = 32 warp + lane
+      const float* f = reinterpret_cast<const float*>(raw);
+      float sa = 0.f, sb_ = 0.f, sl = 0.f;        // sums over the other quarters; then the running sums of this one
+      float oa = 0.f, ob = 0.f, ol = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int at = c * 32 + lane;
+        const float a = (f[L::a / 4 + at] + f[L::a / 4 + kTC + at]) + (f[L::a / 4 + 2 * kTC + at] + f[L::a / 4 + 3 * kTC + at]);
+        const float e = (f[L::b / 4 + at] + f[L::b / 4 + kTC + at]) + (f[L::b / 4 + 2 * kTC + at] + f[L::b / 4 + 3 * kTC + at]);
+        float l = 0.f;  // row at's paths to the quarters after this warp's
+#pragma unroll
+        for (int u = 1; u < 4; ++u) l += u > warp ? f[L::tot / 4 + u * kTC + at] : 0.f;
+        if (c == warp) { oa = a; ob = e; ol = l; }
+        if (c > warp) sa += a;
+        if (c < warp) { sb_ += e; sl += l; }
+      }
+      float ra = oa, rb = ob + ol;
+      sb_ += sl;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        sa += __shfl_xor_sync(0xffffffffu, sa, o);
+        sb_ += __shfl_xor_sync(0xffffffffu, sb_, o);
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float ua = __shfl_down_sync(0xffffffffu, ra, o), ub = __shfl_up_sync(0xffffffffu, rb, o);
+        if (lane + o < 32) ra += ua;
+        if (lane >= o) rb += ub;
+      }
+      float thr = lane < 16 ? f[L::thr / 4 + lane] : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) thr += __shfl_xor_sync(0xffffffffu, thr, o);
+      const int t = warp * 32 + lane;
+      const float in = (f[L::rect / 4 + t] + f[L::rect / 4 + kTC + t]) + (f[L::rect / 4 + 2 * kTC + t] + f[L::rect / 4 + 3 * kTC + t]);
+      const float before = __shfl_up_sync(0xffffffffu, rb, 1);
+      const float g = in + (sa + ra) + (sb_ + (lane > 0 ? before : 0.f)) + elast * thr;
+      float* dst = out.dg;
+      if (p.g_head) {  // the four warps' parts are added by the column sum
+        float s = t < valid ? g : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) reinterpret_cast<float*>(raw)[L::thr / 4 + 16 + warp] = s;
+      } else if (t0 + t < p.L) {
+        dst[((long long)b * p.L + t0 + t) * p.H + h] = t < valid ? g : 0.f;
+      }
+    }
+    uint32_t r[VQ];
+    tmem_ldn(tl + L::T3 + cq * VQ, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < VQ; ++e) U[e] = fmaf(U[e], elast, __uint_as_float(r[e]));
+    tc_fence_before_sync();
+    __syncthreads();  // x and the decays are free
+    if (p.g_head && tid == 0) {
+      const float* s = reinterpret_cast<const float*>(raw) + L::thr / 4 + 16;
+      out.dg[((long long)b * p.nck + ck) * p.H + h] = (s[0] + s[1]) + (s[2] + s[3]);
+    }
+    if (ck > c0) load_rest(ck - 1);
+    if (p.g_head) __syncthreads();  // x is written next
+  }
+  if (!ok) {  // a wait ran out: say so; the outputs are invalid
+    if (tid == 0) atomicOr(&g_lin_err, kErrTmaTimeout);
+    mbar_wait_bounded(&bar[0], ph0 ^ 1, 100000000ull);  // its own MMAs
+    mbar_wait_bounded(&bar[1], ph1 ^ 1, 100000000ull);
+    cp_wait_all();
+  }
+  if (out.dh0 != nullptr && seg == 0 && row < p.K) {
+    float* dst = out.dh0 + (bh * p.K + row) * p.V + cq * VQ;
+#pragma unroll
+    for (int e = 0; e < VQ; e += 4)
+      if (cq * VQ + e < p.V) *reinterpret_cast<float4*>(dst + e) = make_float4(U[e], U[e + 1], U[e + 2], U[e + 3]);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tm, L::cols);
 }
 
 // dq, dk of a shared head: the parts of its R heads added in order, rounded once.
@@ -372,31 +803,24 @@ int bwd_plan(int B, int L, int H, int G, int K, int V, int dtype, int g_head, Bw
   return SS_OK;
 }
 
-template <typename T, int KP, int VP>
-int bwd_launch(const BwdPlan& pl, const void* dout, const float* ckpt, const float* dh_last, BwdOut out, float* dg, char* ws,
-               cudaStream_t s) {
+// The walk (for a row cut in segments after their U), then the sums over heads that share q, k and over chunks.
+template <typename T, typename Sum, typename Walk>
+int bwd_run(const BwdPlan& pl, const float* dh_last, BwdOut out, float* dg, char* ws, cudaStream_t s, Sum sum, Walk walk) {
   const LinAttn& p = pl.p;
-  const size_t smem = sizeof(BwdSmem<KP, VP>);
   float* st = reinterpret_cast<float*>(ws);
   double* dec = reinterpret_cast<double*>(ws + pl.states);
   out.dqp = pl.parts ? reinterpret_cast<float*>(ws + pl.states + pl.decs) : nullptr;
   out.dkp = pl.parts ? reinterpret_cast<float*>(ws + pl.states + pl.decs + pl.parts) : nullptr;
   out.dg = p.g_head ? reinterpret_cast<float*>(ws + pl.states + pl.decs + 2 * pl.parts) : dg;
-  auto run = [&](auto kern, const float* u0, float* uend, double* udec) -> int {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SS_ERR_CUDA;
-    const long long grid = (long long)p.B * p.H * p.nseg;
-    kern<<<(unsigned)grid, 256, smem, s>>>(p, static_cast<const T*>(dout), ckpt, u0, out, uend, udec);
-    return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
-  };
   int rc;
   if (p.nseg == 1) {
-    rc = run(linattn_bwd_kernel<T, KP, VP, false>, dh_last, nullptr, nullptr);
+    rc = walk(dh_last, out);
   } else {
-    if ((rc = run(linattn_bwd_kernel<T, KP, VP, true>, nullptr, st, dec)) != SS_OK) return rc;
+    if ((rc = sum(st, dec, out)) != SS_OK) return rc;
     const long long kv = (long long)p.K * p.V;
-    linattn_bwd_join_kernel<<<dim3((unsigned)((kv + 255) / 256), (unsigned)(p.B * p.H)), 256, 0, s>>>(dh_last, st, dec, kv, p.nseg);
+    linattn_join_kernel<true><<<dim3((unsigned)((kv + 255) / 256), (unsigned)(p.B * p.H)), 256, 0, s>>>(dh_last, st, dec, kv, p.nseg);
     if (cudaGetLastError() != cudaSuccess) return SS_ERR_CUDA;
-    rc = run(linattn_bwd_kernel<T, KP, VP, false>, st, nullptr, nullptr);
+    rc = walk(st, out);
   }
   if (rc != SS_OK) return rc;
   if (pl.parts) {
@@ -409,14 +833,35 @@ int bwd_launch(const BwdPlan& pl, const void* dout, const float* ckpt, const flo
   return SS_OK;
 }
 
-template <typename T>
-int bwd_dispatch(const BwdPlan& pl, const void* dout, const float* ckpt, const float* dh_last, const BwdOut& out, float* dg,
-                 char* ws, cudaStream_t s) {
-  if (pl.p.K <= 64)
-    return pl.p.V <= 64 ? bwd_launch<T, 64, 64>(pl, dout, ckpt, dh_last, out, dg, ws, s)
-                        : bwd_launch<T, 64, 128>(pl, dout, ckpt, dh_last, out, dg, ws, s);
-  return pl.p.V <= 64 ? bwd_launch<T, 128, 64>(pl, dout, ckpt, dh_last, out, dg, ws, s)
-                      : bwd_launch<T, 128, 128>(pl, dout, ckpt, dh_last, out, dg, ws, s);
+template <int KP, int VP>
+int bwd_f32(const BwdPlan& pl, const void* dout, const float* ckpt, const float* dh_last, const BwdOut& out, float* dg, char* ws,
+            cudaStream_t s) {
+  const unsigned grid = (unsigned)pl.p.B * pl.p.H * pl.p.nseg;
+  const size_t smem = sizeof(BwdSmem<KP, VP>);
+  return bwd_run<float>(
+      pl, dh_last, out, dg, ws, s,
+      [&](float* st, double* dec, const BwdOut& o) {
+        return lin_launch(linattn_bwd_kernel<KP, VP, true>, grid, 256, smem, s, pl.p, dout, ckpt, nullptr, o, st, dec);
+      },
+      [&](const float* u0, const BwdOut& o) {
+        return lin_launch(linattn_bwd_kernel<KP, VP, false>, grid, 256, smem, s, pl.p, dout, ckpt, u0, o, nullptr, nullptr);
+      });
+}
+
+template <int VP>
+int bwd_bf16(const BwdPlan& pl, const void* dout, const float* ckpt, const float* dh_last, const BwdOut& out, float* dg, char* ws,
+             cudaStream_t s) {
+  const LinAttn& p = pl.p;
+  const unsigned grid = (unsigned)p.B * p.H * p.nseg;
+  return bwd_run<__nv_bfloat16>(
+      pl, dh_last, out, dg, ws, s,
+      [&](float* st, double* dec, const BwdOut&) {
+        return lin_launch(linattn_sum_tc_kernel<true>, grid * ((p.V + 63) / 64), kTcThreads, SumTc::bytes, s, p, p.q, p.ldq, dout,
+                          (long long)p.H * p.V, st, dec);
+      },
+      [&](const float* u0, const BwdOut& o) {
+        return lin_launch(linattn_bwd_tc_kernel<VP>, grid, kBwdThreads, BwdTc<VP>::bytes, s, p, dout, ckpt, u0, o);
+      });
 }
 
 }  // namespace
@@ -455,6 +900,13 @@ extern "C" int linattn_bwd(const void* q, long long ldq, const void* k, long lon
   BwdOut out = {dq, dk, dv, nullptr, nullptr, nullptr, dh0};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
-  if (dtype == SS_F32) return bwd_dispatch<float>(pl, dout, ckpt, dh_last, out, dg, ws, s);
-  return bwd_dispatch<__nv_bfloat16>(pl, dout, ckpt, dh_last, out, dg, ws, s);
+  if (dtype == SS_BF16)
+    return V <= 64 ? bwd_bf16<64>(pl, dout, ckpt, dh_last, out, dg, ws, s) : bwd_bf16<128>(pl, dout, ckpt, dh_last, out, dg, ws, s);
+  if (K <= 64)
+    return V <= 64 ? bwd_f32<64, 64>(pl, dout, ckpt, dh_last, out, dg, ws, s) : bwd_f32<64, 128>(pl, dout, ckpt, dh_last, out, dg, ws, s);
+  return V <= 64 ? bwd_f32<128, 64>(pl, dout, ckpt, dh_last, out, dg, ws, s) : bwd_f32<128, 128>(pl, dout, ckpt, dh_last, out, dg, ws, s);
 }
+
+namespace ssh {
+int read_clear_linb_err(cudaStream_t s, unsigned* out) { return read_clear_lin_err(s, out); }
+}  // namespace ssh

@@ -10,6 +10,8 @@
 // so all its products are matrix products and only S passes from chunk to chunk.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace ssk {
@@ -60,10 +62,10 @@ __device__ __forceinline__ float dec_diff(float hi_i, float lo_i, float hi_j, fl
 // keeps -inf, a reset, from making c_i - c_j = -inf + inf.
 constexpr float kMinLogDecay = -1000.0f;
 
-// Running log2 decays of the chunk at t0: chi/clo[i] for i < C (a token past
-// the row's end decays by 1).  One warp, C / 32 consecutive tokens a lane.
-template <int C>
-__device__ __forceinline__ void chunk_decays(const LinAttn& p, int b, int h, int t0, int len, int lane, float* chi, float* clo) {
+// Running log2 decays of the chunk at t0, put(i, c_i) for i < C (a token past the
+// row's end decays by 1).  One warp, C / 32 consecutive tokens a lane.
+template <int C, typename Put>
+__device__ __forceinline__ void chunk_decays(const LinAttn& p, int b, int h, int t0, int len, int lane, Put put) {
   constexpr int PER = C / 32;
   double x[PER];
   double s = 0.0;
@@ -83,17 +85,14 @@ __device__ __forceinline__ void chunk_decays(const LinAttn& p, int b, int h, int
   }
   const double base = incl - s;
 #pragma unroll
-  for (int e = 0; e < PER; ++e) {
-    const Dec d = dec_of(base + x[e]);
-    chi[lane * PER + e] = d.hi;
-    clo[lane * PER + e] = d.lo;
-  }
+  for (int e = 0; e < PER; ++e) put(lane * PER + e, dec_of(base + x[e]));
 }
 
 constexpr int kLinMaxHead = 128;  // widest K, V
-constexpr int kLinChunkF32 = 64;
+constexpr int kLinChunkF32 = 64;    // tokens of a chunk: fp32 (FMA pipe)
+constexpr int kLinChunkBf16 = 128;  // bf16 (tensor cores: 128 rows of an MMA)
 
-inline int linattn_chunk(int dtype) { return dtype == SS_F32 ? kLinChunkF32 : 64; }
+inline int linattn_chunk(int dtype) { return dtype == SS_F32 ? kLinChunkF32 : kLinChunkBf16; }
 
 // Segments: with fewer independent walks (batch rows x heads x column tiles)
 // than the GPU holds at once, a row is cut in `nseg` pieces whose end states
@@ -121,6 +120,19 @@ inline int linattn_validate(int B, int L, int H, int G, int K, int V, int dtype)
 inline int linattn_ld_ok(long long ld, int width) {
   if (ld < width) return SS_ERR_DIM;
   return ld % 8 != 0 ? SS_ERR_ALIGN : SS_OK;
+}
+
+// an argument as the kernel takes it (untyped activations become its type)
+template <typename K, typename A>
+inline K lin_arg(A a) {
+  if constexpr (std::is_same_v<A, const void*> && std::is_pointer_v<K>) return static_cast<K>(a);
+  else return a;
+}
+template <typename... KArgs, typename... Args>
+inline int lin_launch(void (*kern)(KArgs...), unsigned grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SS_ERR_CUDA;
+  kern<<<grid, threads, smem, s>>>(lin_arg<KArgs>(args)...);
+  return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------- FP32 tiles
@@ -181,12 +193,12 @@ __device__ __forceinline__ void zero_acc(float (&acc)[R][Cn]) {
 
 // C tokens x W columns of a strided input into a padded fp32 tile; columns
 // past `width` and tokens past `valid` become zero (their memory is not read).
-template <typename T, int C, int W, int LD>
-__device__ __forceinline__ void load_tile(const T* __restrict__ src, long long ld, int valid, int width, float* dst, int tid) {
+template <int C, int W, int LD>
+__device__ __forceinline__ void load_tile(const float* __restrict__ src, long long ld, int valid, int width, float* dst, int tid) {
   for (int i = tid; i < C * (W / 8); i += 256) {
     const int t = i / (W / 8), c = (i % (W / 8)) * 8;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (t < valid && c < width) ActT<T>::ld8(src + (long long)t * ld + c, v);
+    if (t < valid && c < width) ActT<float>::ld8(src + (long long)t * ld + c, v);
     ActT<float>::st8(dst + t * LD + c, v);
   }
 }

@@ -1,11 +1,9 @@
 // Linear attention with a decay for each head, chunked forward (linattn_fwd) for sm_103a.
-#include "linattn_common.cuh"
+#include "linattn_tc.cuh"
 
 namespace {
 
-using namespace ssk;
-
-// FP32 products on the FMA pipe.  A CTA walks the chunks of one (batch row,
+// fp32: products on the FMA pipe.  A CTA walks the chunks of one (batch row,
 // head, 64-column tile of V, segment) in order with the state in registers.
 // SUM only finds the segment's end state from zero and its decay (no q, no o).
 constexpr int kVT = 64;
@@ -16,8 +14,8 @@ struct FwdSmem {
   float q[C * LK], k[C * LK], v[C * LV], s[KP * LV], p[C * LC], chi[C], clo[C];
 };
 
-template <typename T, int KP, bool SUM>
-__global__ void __launch_bounds__(256) linattn_fwd_kernel(LinAttn p, const float* __restrict__ s0, T* __restrict__ o,
+template <int KP, bool SUM>
+__global__ void __launch_bounds__(256) linattn_fwd_kernel(LinAttn p, const float* __restrict__ s0, float* __restrict__ o,
                                                           float* __restrict__ ckpt, float* __restrict__ send,
                                                           double* __restrict__ sdec) {
   using Sm = FwdSmem<KP>;
@@ -35,9 +33,9 @@ __global__ void __launch_bounds__(256) linattn_fwd_kernel(LinAttn p, const float
   const int gh = h / (p.H / p.G), v0 = vt * kVT, vw = p.V - v0 < kVT ? p.V - v0 : kVT;
   const int len = p.len(b);
   const long long bh = (long long)b * p.H + h;
-  const T* q = static_cast<const T*>(p.q) + (long long)b * p.L * p.ldq + (long long)gh * p.K;
-  const T* k = static_cast<const T*>(p.k) + (long long)b * p.L * p.ldk + (long long)gh * p.K;
-  const T* v = static_cast<const T*>(p.v) + (long long)b * p.L * p.ldv + (long long)h * p.V + v0;
+  const float* q = static_cast<const float*>(p.q) + (long long)b * p.L * p.ldq + (long long)gh * p.K;
+  const float* k = static_cast<const float*>(p.k) + (long long)b * p.L * p.ldk + (long long)gh * p.K;
+  const float* v = static_cast<const float*>(p.v) + (long long)b * p.L * p.ldv + (long long)h * p.V + v0;
 
   // the state this segment starts from: what the segments before composed, or h0, or zero
   float S[RK][4];
@@ -61,13 +59,13 @@ __global__ void __launch_bounds__(256) linattn_fwd_kernel(LinAttn p, const float
     if (valid == 0) {  // past the row's end: nothing decays, adds or reads
       if (!SUM)
         for (int i = tid; i < rows * vw; i += 256)
-          ActT<T>::st1(o + (((long long)b * p.L + t0 + i / vw) * p.H + h) * p.V + v0 + i % vw, 0.f);
+          o[(((long long)b * p.L + t0 + i / vw) * p.H + h) * p.V + v0 + i % vw] = 0.f;
       continue;
     }
-    if (tid < 32) chunk_decays<C>(p, b, h, t0, len, tid, sm.chi, sm.clo);
-    if (!SUM) load_tile<T, C, KP, LK>(q + t0 * p.ldq, p.ldq, valid, p.K, sm.q, tid);
-    load_tile<T, C, KP, LK>(k + t0 * p.ldk, p.ldk, valid, p.K, sm.k, tid);
-    load_tile<T, C, kVT, LV>(v + t0 * p.ldv, p.ldv, valid, vw, sm.v, tid);
+    if (tid < 32) chunk_decays<C>(p, b, h, t0, len, tid, [&](int i, Dec d) { sm.chi[i] = d.hi; sm.clo[i] = d.lo; });
+    if (!SUM) load_tile<C, KP, LK>(q + t0 * p.ldq, p.ldq, valid, p.K, sm.q, tid);
+    load_tile<C, KP, LK>(k + t0 * p.ldk, p.ldk, valid, p.K, sm.k, tid);
+    load_tile<C, kVT, LV>(v + t0 * p.ldv, p.ldv, valid, vw, sm.v, tid);
     if (!SUM) {
 #pragma unroll
       for (int r = 0; r < RK; ++r)
@@ -106,7 +104,7 @@ __global__ void __launch_bounds__(256) linattn_fwd_kernel(LinAttn p, const float
         for (int c = 0; c < 4; ++c) {
           const int i = ty * 4 + r, vv = tx + 16 * c;
           if (i < rows && vv < vw)
-            ActT<T>::st1(o + (((long long)b * p.L + t0 + i) * p.H + h) * p.V + v0 + vv, i < valid ? p.scale * a[r][c] : 0.f);
+            o[(((long long)b * p.L + t0 + i) * p.H + h) * p.V + v0 + vv] = i < valid ? p.scale * a[r][c] : 0.f;
         }
     }
     __syncthreads();
@@ -140,25 +138,240 @@ __global__ void __launch_bounds__(256) linattn_fwd_kernel(LinAttn p, const float
   if (SUM && tid == 0 && vt == 0) sdec[bh * p.nseg + seg] = total;
 }
 
-// In place over the segments of a (batch row, head): the end states found from
-// zero become the states entering the segments, S[s+1] = 2^{dec[s]} S[s] + end[s].
-__global__ void __launch_bounds__(256) linattn_fwd_join_kernel(const float* __restrict__ h0, float* __restrict__ st,
-                                                               const double* __restrict__ dec, long long kv, int nseg) {
-  const long long bh = blockIdx.y;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= kv) return;
-  float s = h0 != nullptr ? h0[bh * kv + i] : 0.f;
-  for (int n = 0; n < nseg; ++n) {
-    float* at = st + (bh * nseg + n) * kv + i;
-    const Dec d = dec_of(dec[bh * nseg + n]);
-    const float end = *at;
-    *at = s;
-    s = fmaf(dec_exp(d.hi, d.lo), s, end);
+// ---------------------------------------------------------------- bf16: tensor cores
+// A CTA walks the chunks (128 tokens) of one (batch row, head, 64-column tile of
+// V, segment).  The state stays in registers in fp32 (thread = row d of K and 32
+// of the 64 columns) and goes to shared memory as bf16 for the product with q.
+//   P   = q k^T                 -> scaled by the decays, rounded to bf16, back to tensor memory as an A operand
+//   Oi  = q S_in                (bf16 S_in; the row factor e^{c_i} is applied in fp32)
+//   Oa  = P v
+//   Sn  = k^T (w v),  w_j = e^{c_last - c_j}: w v as three bf16 terms, an fp32-exact product
+// A term of o is rounded to bf16 once on its way (as a score or as a state).
+struct FwdTc {
+  // shared memory: tiles, decays, barrier, tensor-memory address; two CTAs fit an SM
+  static constexpr int q = 0, k = q + 2 * kPanel, v = k + 2 * kPanel, s = v + kPanel, w = s + kPanel, dec = w + kPanel;
+  static constexpr int bar = dec + DecTile::bytes, tm = bar + 8, bytes = tm + 8;
+  // tensor memory columns
+  static constexpr int P = 0, Oa = 0, Sn = 64, Pb = 128, Oi = 192, cols = 256;
+};
+
+__global__ void __launch_bounds__(kTcThreads, 2) linattn_fwd_tc_kernel(LinAttn p, const float* __restrict__ s0,
+                                                                      __nv_bfloat16* __restrict__ o, float* __restrict__ ckpt,
+                                                                      float* __restrict__ send) {
+  using L = FwdTc;
+  extern __shared__ __align__(1024) unsigned char raw[];
+  const uint32_t sb = smem_u32(raw);
+  const DecTile dec{sb + L::dec};
+  uint64_t* bar = reinterpret_cast<uint64_t*>(raw + L::bar);
+  uint32_t* tma = reinterpret_cast<uint32_t*>(raw + L::tm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row = (warp & 3) * 32 + lane, half = warp >> 2;  // tensor-memory lane and half of the columns of this thread
+  const int nvt = (p.V + kVT - 1) / kVT;
+  long long id = blockIdx.x;
+  const int seg = (int)(id % p.nseg);
+  id /= p.nseg;
+  const int vt = (int)(id % nvt);
+  id /= nvt;
+  const int h = (int)(id % p.H), b = (int)(id / p.H);
+  const int gh = h / (p.H / p.G), v0 = vt * kVT, vw = p.V - v0 < kVT ? p.V - v0 : kVT;
+  const int len = p.len(b);
+  const long long bh = (long long)b * p.H + h;
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (long long)b * p.L * p.ldq + (long long)gh * p.K;
+  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.k) + (long long)b * p.L * p.ldk + (long long)gh * p.K;
+  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + (long long)b * p.L * p.ldv + (long long)h * p.V + v0;
+
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    fence_barrier_init();
   }
+  if (warp == 0) {
+    tmem_alloc(tma, L::cols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tm = *tma;
+  const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);  // this warp's lanes
+  const int ks = (p.K + 15) / 16;                                 // contraction steps over K
+
+  float S[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) S[e] = 0.f;
+  if (s0 != nullptr && row < p.K) {
+    const float* src = s0 + ((p.nseg > 1 ? bh * p.nseg + seg : bh) * p.K + row) * p.V + v0 + half * 32;
+#pragma unroll
+    for (int e = 0; e < 32; e += 4)
+      if (half * 32 + e < vw) {
+        const float4 x = *reinterpret_cast<const float4*>(src + e);
+        S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
+      }
+  }
+  auto store_s = [&]() {  // S_in as a bf16 tile
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      sts16(sb + L::s + tile_at(row, half * 4 + u), make_uint4(pack_bf16(S[8 * u], S[8 * u + 1]), pack_bf16(S[8 * u + 2], S[8 * u + 3]),
+                                                             pack_bf16(S[8 * u + 4], S[8 * u + 5]), pack_bf16(S[8 * u + 6], S[8 * u + 7])));
+  };
+  auto valid_of = [&](int ck) { const int n = len - ck * kTC; return n < 0 ? 0 : n < kTC ? n : kTC; };
+  auto load = [&](int ck) {
+    const int n = valid_of(ck);
+    const long long t0 = (long long)ck * kTC;
+    load_tile_tc<16, kTcThreads>(q + t0 * p.ldq, p.ldq, n, p.K, sb + L::q, tid);
+    load_tile_tc<16, kTcThreads>(k + t0 * p.ldk, p.ldk, n, p.K, sb + L::k, tid);
+    load_tile_tc<8, kTcThreads>(v + t0 * p.ldv, p.ldv, n, vw, sb + L::v, tid);
+    if (warp == 0) chunk_decays<kTC>(p, b, h, ck * kTC, len, lane, [&](int i, Dec d) { dec.put(i, d); });
+  };
+  const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
+  int cend = (len + kTC - 1) / kTC;  // chunks that hold a token
+  cend = cend < c0 ? c0 : cend < c1 ? cend : c1;
+  uint32_t phase = 0;
+  bool ok = true;
+  if (c0 < cend) {
+    load(c0);
+    store_s();
+  }
+  for (int ck = c0; ck < cend; ++ck) {
+    const int t0 = ck * kTC, valid = valid_of(ck);
+    cp_wait_all();
+    fence_proxy_async_smem();
+    tc_fence_before_sync();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after_sync();
+      for (int s = 0; s < ks; ++s) mma_ss(tm + L::P, desc_rows(sb + L::q, s), desc_rows(sb + L::k, s), mma_idesc(kTC, false, false), s > 0);
+      for (int s = 0; s < ks; ++s) mma_ss(tm + L::Oi, desc_rows(sb + L::q, s), desc_cols(sb + L::s, s), mma_idesc(kVT, false, true), s > 0);
+      mma_commit(bar);
+    }
+    const Dec last = dec.get(kTC - 1), own = dec.get(row);
+    const float elast = dec_exp(last.hi, last.lo);
+    // w v: row tid / 2, half of the columns; the first term has a tile of its own, the others take q's
+    const int vr = tid >> 1, vh = (tid & 1) * 4;
+    const Dec dr = dec.get(vr);
+    const float wj = dec_diff(last.hi, last.lo, dr.hi, dr.lo);
+    auto wv = [&](int u, float (&x)[8]) {
+      const uint4 a = lds16(sb + L::v + tile_at(vr, vh + u));
+      Raw8<__nv_bfloat16>::wide(a, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= wj;
+    };
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float x[8];
+      wv(u, x);
+      sts16(sb + L::w + tile_at(vr, vh + u), take_term(x));
+    }
+    ok = mbar_wait_bounded(bar, phase, kWaitLimitNs);
+    phase ^= 1;
+    if (__syncthreads_or(!ok)) break;
+    tc_fence_after_sync();
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {  // 32 scores at a time
+      const int j0 = half * 64 + g * 32;
+      uint32_t r[32], w[16];
+      if (j0 <= (row | 31)) {
+        tmem_ld32(tl + L::P + j0, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const int j = j0 + e;
+          Dec a, c;
+          dec.get2(j, a, c);
+          const float d0 = dec_diff(own.hi, own.lo, a.hi, a.lo), d1 = dec_diff(own.hi, own.lo, c.hi, c.lo);
+          w[e / 2] = pack_bf16(j <= row ? __uint_as_float(r[e]) * d0 : 0.f, j + 1 <= row ? __uint_as_float(r[e + 1]) * d1 : 0.f);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e] = 0u;
+      }
+      tmem_st16(tl + L::Pb + j0 / 2, w);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float x[8];
+      wv(u, x);
+      take_term(x);
+      sts16(sb + L::q + tile_at(vr, vh + u), take_term(x));
+      sts16(sb + L::q + kPanel + tile_at(vr, vh + u), take_term(x));
+    }
+    fence_proxy_async_smem();
+    tmem_wait_st();
+    tc_fence_before_sync();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after_sync();
+      for (int s = 0; s < kTC / 16; ++s) mma_ts(tm + L::Oa, tm + L::Pb + s * 8, desc_cols(sb + L::v, s), mma_idesc(kVT, false, true), s > 0);
+      for (int t = 2; t >= 0; --t) {  // the smallest term first
+        const uint32_t w = sb + (t == 0 ? L::w : L::q + (t - 1) * kPanel);
+        for (int s = 0; s < kTC / 16; ++s)
+          mma_ss(tm + L::Sn, desc_cols(sb + L::k, s), desc_cols(w, s), mma_idesc(kVT, true, true), t < 2 || s > 0);
+      }
+      mma_commit(bar);
+    }
+    const float ei = p.scale * dec_exp(own.hi, own.lo);
+    if (ckpt != nullptr && row < p.K) {
+      float* dst = ckpt + ((bh * p.nck + ck) * p.K + row) * p.V + v0 + half * 32;
+#pragma unroll
+      for (int e = 0; e < 32; e += 4)
+        if (half * 32 + e < vw) *reinterpret_cast<float4*>(dst + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+    }
+    ok = mbar_wait_bounded(bar, phase, kWaitLimitNs);
+    phase ^= 1;
+    if (__syncthreads_or(!ok)) break;
+    tc_fence_after_sync();
+    if (ck + 1 < cend) load(ck + 1);
+    uint32_t r[32];
+    tmem_ld32(tl + L::Sn + half * 32, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) S[e] = fmaf(S[e], elast, __uint_as_float(r[e]));
+    if (ck + 1 < cend) store_s();
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      uint32_t a[16], i[16];
+      tmem_ld16(tl + L::Oa + half * 32 + g * 16, a);
+      tmem_ld16(tl + L::Oi + half * 32 + g * 16, i);
+      tmem_wait_ld();
+      if (t0 + row < p.L) {
+        __nv_bfloat16* dst = o + (((long long)b * p.L + t0 + row) * p.H + h) * p.V + v0 + half * 32 + g * 16;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (half * 32 + g * 16 + u * 8 >= vw) continue;
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            x[e] = row < valid ? fmaf(__uint_as_float(i[8 * u + e]), ei, p.scale * __uint_as_float(a[8 * u + e])) : 0.f;
+          ActT<__nv_bfloat16>::st8(dst + 8 * u, x);
+        }
+      }
+    }
+  }
+  if (!ok) {  // a wait ran out: say so; the outputs are invalid
+    if (tid == 0) atomicOr(&g_lin_err, kErrTmaTimeout);
+    mbar_wait_bounded(bar, phase ^ 1, 100000000ull);  // its own MMAs
+    cp_wait_all();
+  } else {
+    for (int ck = cend; ck < c1; ++ck) {  // past the row's end
+      const int rows = p.L - ck * kTC < kTC ? p.L - ck * kTC : kTC;
+      for (int i = tid; i < rows * (vw / 8); i += kTcThreads)
+        *reinterpret_cast<uint4*>(o + (((long long)b * p.L + ck * kTC + i / (vw / 8)) * p.H + h) * p.V + v0 + i % (vw / 8) * 8) =
+            make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  if (send != nullptr && seg == p.nseg - 1 && row < p.K) {
+    float* dst = send + (bh * p.K + row) * p.V + v0 + half * 32;
+#pragma unroll
+    for (int e = 0; e < 32; e += 4)
+      if (half * 32 + e < vw) *reinterpret_cast<float4*>(dst + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tm, L::cols);
 }
 
 struct FwdPlan {
   LinAttn p;
+  long long walks;  // (batch row, head, column tile)
   size_t states, bytes;
 };
 
@@ -167,33 +380,48 @@ int fwd_plan(int B, int L, int H, int G, int K, int V, int dtype, FwdPlan& pl) {
   if (rc != SS_OK) return rc;
   pl.p = LinAttn{};
   pl.p.B = B; pl.p.L = L; pl.p.H = H; pl.p.G = G; pl.p.K = K; pl.p.V = V;
-  const long long walks = (long long)B * H * ((V + kVT - 1) / kVT);
-  if (walks > (1ll << 24)) return SS_ERR_DIM;
-  linattn_segments(pl.p, linattn_chunk(dtype), walks, (K > 64 ? 1 : 2) * 152);
+  pl.walks = (long long)B * H * ((V + kVT - 1) / kVT);
+  if (pl.walks > (1ll << 24)) return SS_ERR_DIM;
+  linattn_segments(pl.p, linattn_chunk(dtype), pl.walks, (dtype == SS_BF16 || K <= 64 ? 2 : 1) * 152);
   pl.states = pl.p.nseg > 1 ? (size_t)B * H * pl.p.nseg * K * V * sizeof(float) : 0;
   pl.bytes = pl.p.nseg > 1 ? pl.states + (size_t)B * H * pl.p.nseg * sizeof(double) : 0;
   return SS_OK;
 }
 
-template <typename T, int KP>
-int fwd_launch(const FwdPlan& pl, const float* h0, void* o, float* ckpt, float* h_last, void* ws, cudaStream_t s) {
+// The walk; for a row cut in segments first their end states, then the states they start from.
+template <typename Sum, typename Walk>
+int fwd_run(const FwdPlan& pl, const float* h0, void* ws, cudaStream_t s, Sum sum, Walk walk) {
   const LinAttn& p = pl.p;
-  const size_t smem = sizeof(FwdSmem<KP>);
-  auto run = [&](auto kern, const float* s0, float* send, double* dec) -> int {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SS_ERR_CUDA;
-    const long long grid = (long long)p.B * p.H * ((p.V + kVT - 1) / kVT) * p.nseg;
-    kern<<<(unsigned)grid, 256, smem, s>>>(p, s0, static_cast<T*>(o), ckpt, send, dec);
-    return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
-  };
-  if (p.nseg == 1) return run(linattn_fwd_kernel<T, KP, false>, h0, h_last, nullptr);
+  if (p.nseg == 1) return walk(h0);
   float* st = static_cast<float*>(ws);
   double* dec = reinterpret_cast<double*>(static_cast<char*>(ws) + pl.states);
-  int rc = run(linattn_fwd_kernel<T, KP, true>, nullptr, st, dec);
+  const int rc = sum(st, dec);
   if (rc != SS_OK) return rc;
   const long long kv = (long long)p.K * p.V;
-  linattn_fwd_join_kernel<<<dim3((unsigned)((kv + 255) / 256), (unsigned)(p.B * p.H)), 256, 0, s>>>(h0, st, dec, kv, p.nseg);
+  linattn_join_kernel<false><<<dim3((unsigned)((kv + 255) / 256), (unsigned)(p.B * p.H)), 256, 0, s>>>(h0, st, dec, kv, p.nseg);
   if (cudaGetLastError() != cudaSuccess) return SS_ERR_CUDA;
-  return run(linattn_fwd_kernel<T, KP, false>, st, h_last, nullptr);
+  return walk(st);
+}
+
+template <int KP>
+int fwd_f32(const FwdPlan& pl, const float* h0, float* o, float* ckpt, float* h_last, void* ws, cudaStream_t s) {
+  const unsigned grid = (unsigned)pl.walks * pl.p.nseg;
+  const size_t smem = sizeof(FwdSmem<KP>);
+  return fwd_run(
+      pl, h0, ws, s,
+      [&](float* st, double* dec) { return lin_launch(linattn_fwd_kernel<KP, true>, grid, 256, smem, s, pl.p, nullptr, o, ckpt, st, dec); },
+      [&](const float* s0) { return lin_launch(linattn_fwd_kernel<KP, false>, grid, 256, smem, s, pl.p, s0, o, ckpt, h_last, nullptr); });
+}
+
+int fwd_bf16(const FwdPlan& pl, const float* h0, __nv_bfloat16* o, float* ckpt, float* h_last, void* ws, cudaStream_t s) {
+  const LinAttn& p = pl.p;
+  const unsigned grid = (unsigned)pl.walks * p.nseg;
+  return fwd_run(
+      pl, h0, ws, s,
+      [&](float* st, double* dec) {
+        return lin_launch(linattn_sum_tc_kernel<false>, grid, kTcThreads, SumTc::bytes, s, p, p.k, p.ldk, p.v, p.ldv, st, dec);
+      },
+      [&](const float* s0) { return lin_launch(linattn_fwd_tc_kernel, grid, kTcThreads, FwdTc::bytes, s, p, s0, o, ckpt, h_last); });
 }
 
 }  // namespace
@@ -236,8 +464,11 @@ extern "C" int linattn_fwd(const void* q, long long ldq, const void* k, long lon
   p.scale = scale;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == SS_F32)
-    return K <= 64 ? fwd_launch<float, 64>(pl, h0, o, ckpt, h_last, workspace, s)
-                   : fwd_launch<float, 128>(pl, h0, o, ckpt, h_last, workspace, s);
-  return K <= 64 ? fwd_launch<__nv_bfloat16, 64>(pl, h0, o, ckpt, h_last, workspace, s)
-                 : fwd_launch<__nv_bfloat16, 128>(pl, h0, o, ckpt, h_last, workspace, s);
+    return K <= 64 ? fwd_f32<64>(pl, h0, static_cast<float*>(o), ckpt, h_last, workspace, s)
+                   : fwd_f32<128>(pl, h0, static_cast<float*>(o), ckpt, h_last, workspace, s);
+  return fwd_bf16(pl, h0, static_cast<__nv_bfloat16*>(o), ckpt, h_last, workspace, s);
 }
+
+namespace ssh {
+int read_clear_linf_err(cudaStream_t s, unsigned* out) { return read_clear_lin_err(s, out); }
+}  // namespace ssh

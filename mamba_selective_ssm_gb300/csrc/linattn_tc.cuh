@@ -1,0 +1,336 @@
+// Tensor-core pieces of the bf16 linear attention kernels: shared-memory tiles
+// in the 128-byte-swizzled layout that tcgen05.mma reads, their descriptors, and
+// tensor-memory access.
+//
+// A tile of R rows x W columns of bf16 is W / 64 panels of R rows of 128 bytes;
+// 16-byte unit u of row r lies at unit u ^ (r & 7) of its row.  One tile serves
+// as an operand whose contraction runs along its columns ("rows" below: M or N
+// are its rows) and as one whose contraction runs down its rows ("cols": M or N
+// are its columns), so q, k, v and do are loaded once for all their products.
+#pragma once
+
+#include "linattn_common.cuh"
+
+namespace ssk {
+
+constexpr int kTC = kLinChunkBf16;        // tokens of a chunk = rows of a tile
+constexpr int kPanel = kTC * 128;         // bytes of a panel of kTC rows
+constexpr int kTcThreads = 256;
+
+// byte offset of 16-byte unit `u` (8 columns) of row r in a tile of kTC rows
+__device__ __forceinline__ uint32_t tile_at(int r, int u) {
+  return (uint32_t)((u >> 3) * kPanel + r * 128 + (((u & 7) ^ (r & 7)) << 4));
+}
+
+// The decays of a chunk in shared memory: hi as floats, lo as bf16 (it only has
+// to bring 8 more bits), so that two CTAs' tiles fit an SM.
+struct DecTile {
+  static constexpr int bytes = kTC * 6;
+  uint32_t base;
+  __device__ __forceinline__ void put(int i, Dec d) const {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + 4 * i), "f"(d.hi) : "memory");
+    const __nv_bfloat16 l = __float2bfloat16_rn(d.lo);
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(base + 4 * kTC + 2 * i), "h"(*reinterpret_cast<const uint16_t*>(&l)) : "memory");
+  }
+  __device__ __forceinline__ Dec get(int i) const {
+    Dec d;
+    uint16_t l;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(d.hi) : "r"(base + 4 * i));
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(l) : "r"(base + 4 * kTC + 2 * i));
+    d.lo = __uint_as_float((uint32_t)l << 16);
+    return d;
+  }
+  // tokens j, j + 1 (j even)
+  __device__ __forceinline__ void get2(int j, Dec& a, Dec& b) const {
+    uint32_t l;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(a.hi), "=f"(b.hi) : "r"(base + 4 * j));
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(l) : "r"(base + 4 * kTC + 2 * j));
+    a.lo = __uint_as_float(l << 16);
+    b.lo = __uint_as_float(l & 0xffff0000u);
+  }
+};
+
+// ---------------------------------------------------------------- descriptors
+// Shared-memory operand descriptor: start address, leading and stride byte
+// offsets (all in 16-byte units), version 1, 128-byte swizzle.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)((lbo >> 4) & 0x3fff) << 16) | ((uint64_t)((sbo >> 4) & 0x3fff) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// contraction along the columns; step s takes columns 16 s .. 16 s + 15
+__device__ __forceinline__ uint64_t desc_rows(uint32_t tile, int s) {
+  return smem_desc(tile + (s >> 2) * kPanel + (s & 3) * 32, 16, 1024);
+}
+// contraction down the rows; step s takes rows 16 s .. 16 s + 15; 64-column panels kPanel apart
+__device__ __forceinline__ uint64_t desc_cols(uint32_t tile, int s) { return smem_desc(tile + s * 2048, kPanel, 1024); }
+
+// bf16 x bf16 -> fp32, M = 128; a_cols / b_cols: that operand's contraction runs down its rows
+__device__ __forceinline__ uint32_t mma_idesc(int n, bool a_cols, bool b_cols) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_cols ? 1u : 0u) << 15) | ((b_cols ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+         ((128u >> 4) << 24);
+}
+
+// D (tensor memory) = A B (+ D); one thread issues
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// the same with A (128 rows, bf16 pairs in columns) in tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// the barrier completes when all MMAs issued before are done
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void tmem_stn(uint32_t taddr, const uint32_t (&r)[32]) { tmem_st32(taddr, r); }
+__device__ __forceinline__ void tmem_stn(uint32_t taddr, const uint32_t (&r)[16]) { tmem_st16(taddr, r); }
+// N columns of this thread's lane times f, in place (the caller waits for the store)
+template <int N>
+__device__ __forceinline__ void tmem_scale(uint32_t taddr, float f) {
+  uint32_t r[N];
+  tmem_ldn(taddr, r);
+  tmem_wait_ld();
+#pragma unroll
+  for (int e = 0; e < N; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+  tmem_stn(taddr, r);
+}
+
+// ---------------------------------------------------------------- tiles
+
+// 16 bytes global -> shared, asynchronously; zeros instead (nothing read) when !ok
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// kTC tokens x (8 * UNITS) columns into a tile; columns past `width` and tokens past `valid` become zero
+template <int UNITS, int THREADS>
+__device__ __forceinline__ void load_tile_tc(const __nv_bfloat16* __restrict__ src, long long ld, int valid, int width, uint32_t tile,
+                                             int tid) {
+#pragma unroll
+  for (int i = 0; i < kTC * UNITS / THREADS; ++i) {
+    const int at = i * THREADS + tid, r = at / UNITS, u = at % UNITS;
+    const bool ok = r < valid && u * 8 < width;
+    cp16(tile + tile_at(r, u), ok ? src + (long long)r * ld + u * 8 : src, ok);
+  }
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) { return ActT<__nv_bfloat16>::pack2(lo, hi); }
+
+// An fp32 value as a sum of three bf16 terms: the first is off by 2^-8 of the
+// value at most, the first two by 2^-16, all three by 2^-24, the half-step of
+// fp32 itself, so that a product of the terms with an exact bf16 operand is an
+// fp32 product.  This takes term n of eight values and leaves what is left.
+__device__ __forceinline__ uint4 take_term(float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    w[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+    x[2 * e] -= __uint_as_float(w[e] << 16);
+    x[2 * e + 1] -= __uint_as_float(w[e] & 0xffff0000u);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+}  // namespace ssk
+
+namespace {
+
+using namespace ssk;
+
+__device__ unsigned g_lin_err;  // this translation unit's error word: a wait for its own MMAs ran out
+
+inline int read_clear_lin_err(cudaStream_t s, unsigned* out) {
+  unsigned zero = 0;
+  if (cudaMemcpyFromSymbolAsync(out, g_lin_err, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess) return SS_ERR_CUDA;
+  if (cudaMemcpyToSymbolAsync(g_lin_err, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s) != cudaSuccess) return SS_ERR_CUDA;
+  return cudaStreamSynchronize(s) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- a segment's state
+// The state a segment reaches from zero and its log decay, for both directions:
+//   forward   S = e^{c_last} S + sum_j k_j (e^{c_last-c_j} v_j)^T      chunks in order
+//   REV       U = e^{c_last} U + sum_i q_i (scale e^{c_i} do_i)^T      chunks from the last
+// A CTA takes 64 columns of y (v or do); the weighted rows of y go through the
+// tensor cores as three bf16 terms.
+struct SumTc {
+  static constexpr int x = 0, y = x + 2 * kPanel, w = y + kPanel, dec = w + 3 * kPanel, bar = dec + DecTile::bytes, tm = bar + 8,
+                       bytes = tm + 8;
+  static constexpr int cols = 64;
+};
+
+template <bool REV>
+__global__ void __launch_bounds__(kTcThreads, 2) linattn_sum_tc_kernel(LinAttn p, const __nv_bfloat16* __restrict__ xs, long long ldx,
+                                                                      const __nv_bfloat16* __restrict__ ys, long long ldy,
+                                                                      float* __restrict__ send, double* __restrict__ sdec) {
+  using L = SumTc;
+  extern __shared__ __align__(1024) unsigned char raw[];
+  const uint32_t sb = smem_u32(raw);
+  const DecTile dec{sb + L::dec};
+  uint64_t* bar = reinterpret_cast<uint64_t*>(raw + L::bar);
+  uint32_t* tma = reinterpret_cast<uint32_t*>(raw + L::tm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, half = warp >> 2;
+  const int nvt = (p.V + 63) / 64;
+  long long id = blockIdx.x;
+  const int seg = (int)(id % p.nseg);
+  id /= p.nseg;
+  const int vt = (int)(id % nvt);
+  id /= nvt;
+  const int h = (int)(id % p.H), b = (int)(id / p.H), gh = h / (p.H / p.G), v0 = vt * 64, vw = p.V - v0 < 64 ? p.V - v0 : 64;
+  const int len = p.len(b);
+  const long long bh = (long long)b * p.H + h;
+  xs += (long long)b * p.L * ldx + (long long)gh * p.K;
+  ys += (long long)b * p.L * ldy + (long long)h * p.V + v0;
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tma, L::cols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tm = *tma, tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
+  float S[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) S[e] = 0.f;
+  const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
+  int cend = (len + kTC - 1) / kTC;
+  cend = cend < c0 ? c0 : cend < c1 ? cend : c1;
+  auto load = [&](int ck) {
+    const int m = len - ck * kTC, n = m < kTC ? m : kTC;
+    const long long t0 = (long long)ck * kTC;
+    load_tile_tc<16, kTcThreads>(xs + t0 * ldx, ldx, n, p.K, sb + L::x, tid);
+    load_tile_tc<8, kTcThreads>(ys + t0 * ldy, ldy, n, vw, sb + L::y, tid);
+    if (warp == 0) chunk_decays<kTC>(p, b, h, ck * kTC, len, lane, [&](int i, Dec d) { dec.put(i, d); });
+  };
+  double total = 0.0;
+  uint32_t phase = 0;
+  bool ok = true;
+  if (c0 < cend) load(REV ? cend - 1 : c0);
+  for (int n = 0; n < cend - c0; ++n) {
+    const int ck = REV ? cend - 1 - n : c0 + n;
+    cp_wait_all();
+    __syncthreads();
+    const Dec last = dec.get(kTC - 1);
+    const float elast = dec_exp(last.hi, last.lo);
+    total += (double)last.hi + (double)last.lo;
+    const int r = tid >> 1, u0 = (tid & 1) * 4;
+    const Dec dr = dec.get(r);
+    const float w = REV ? p.scale * dec_exp(dr.hi, dr.lo) : dec_diff(last.hi, last.lo, dr.hi, dr.lo);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t at = tile_at(r, u0 + u);
+      float x[8];
+      Raw8<__nv_bfloat16>::wide(lds16(sb + L::y + at), x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= w;
+      sts16(sb + L::w + at, take_term(x));
+      sts16(sb + L::w + kPanel + at, take_term(x));
+      sts16(sb + L::w + 2 * kPanel + at, take_term(x));
+    }
+    fence_proxy_async_smem();
+    tc_fence_before_sync();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after_sync();
+      for (int t = 2; t >= 0; --t)
+        for (int s = 0; s < kTC / 16; ++s)
+          mma_ss(tm, desc_cols(sb + L::x, s), desc_cols(sb + L::w + t * kPanel, s), mma_idesc(64, true, true), t < 2 || s > 0);
+      mma_commit(bar);
+    }
+    ok = mbar_wait_bounded(bar, phase, kWaitLimitNs);
+    phase ^= 1;
+    if (__syncthreads_or(!ok)) break;
+    tc_fence_after_sync();
+    if (n + 1 < cend - c0) load(REV ? ck - 1 : ck + 1);
+    uint32_t a[32];
+    tmem_ld32(tl + half * 32, a);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) S[e] = fmaf(S[e], elast, __uint_as_float(a[e]));
+  }
+  if (!ok) {  // a wait ran out: say so; the outputs are invalid
+    if (tid == 0) atomicOr(&g_lin_err, kErrTmaTimeout);
+    mbar_wait_bounded(bar, phase ^ 1, 100000000ull);
+    cp_wait_all();
+  }
+  if (row < p.K) {
+    float* dst = send + ((bh * p.nseg + seg) * p.K + row) * p.V + v0 + half * 32;
+#pragma unroll
+    for (int e = 0; e < 32; e += 4)
+      if (half * 32 + e < vw) *reinterpret_cast<float4*>(dst + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+  }
+  if (tid == 0 && vt == 0) sdec[bh * p.nseg + seg] = total;
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tm, L::cols);
+}
+
+// In place over the segments of a (batch row, head), in walking order: the
+// states found from zero become the states the segments start from,
+// s[next] = 2^{dec} s + end.
+template <bool REV>
+__global__ void __launch_bounds__(256) linattn_join_kernel(const float* __restrict__ first, float* __restrict__ st,
+                                                           const double* __restrict__ dec, long long kv, int nseg) {
+  const long long bh = blockIdx.y;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= kv) return;
+  float s = first != nullptr ? first[bh * kv + i] : 0.f;
+  for (int m = 0; m < nseg; ++m) {
+    const int n = REV ? nseg - 1 - m : m;
+    float* at = st + (bh * nseg + n) * kv + i;
+    const Dec d = dec_of(dec[bh * nseg + n]);
+    const float end = *at;
+    *at = s;
+    s = fmaf(dec_exp(d.hi, d.lo), s, end);
+  }
+}
+
+}  // namespace
