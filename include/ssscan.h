@@ -383,7 +383,8 @@ int linattn_num_chunks(int L, int dtype);
 /*
  * linattn_fwd — o [B, L, H, V] (dtype), and where the pointer is given
  *   ckpt   : [B, H, linattn_num_chunks(L, dtype), K, V] fp32, the state entering
- *            each chunk, from which linattn_bwd starts (chunks past a row's
+ *            each chunk, from which linattn_bwd starts (the order of the K * V
+ *            values within a chunk is the library's own; chunks past a row's
  *            length are not written)
  *   h_last : [B, H, K, V] fp32, the state after the row's last token
  * h0 may be NULL (zeros).  workspace: linattn_fwd_workspace_size() bytes (0
@@ -442,12 +443,14 @@ int layernorm_fwd(const void* x, const float* scale, const float* bias, float ep
 /*
  * layernorm_bwd — with xh = (x - mean) * rstd and w = dy * scale:
  *   dx = rstd * (w - mean_i w - xh * mean_i(w * xh))       [rows, dim] fp32, overwritten
- *   dscale += sum_r dy * xh;  dbias += sum_r dy            [dim] fp32, accumulated
+ *   dscale += sum_r dy * xh;  dbias += sum_r dy            [dim] fp32
+ * accumulate: 1 adds to dscale, 2 to dbias, 3 to both; where its bit is 0 the
+ * array is overwritten (a caller without a sum to add to need not clear one).
  * dy, x (dtype); mean, rstd as layernorm_fwd saved them; sizes as there.
  */
 size_t layernorm_bwd_workspace_size(int rows, int dim);
 int layernorm_bwd(const void* dy, const void* x, const float* scale, const float* mean, const float* rstd,
-                  float* dx, float* dscale, float* dbias, int rows, int dim, int dtype,
+                  float* dx, float* dscale, float* dbias, int accumulate, int rows, int dim, int dtype,
                   void* workspace, size_t ws_bytes, void* stream);
 
 /*

@@ -57,7 +57,7 @@ SIGNATURES = {
     "linattn_step": (_i, [_vp] * 4 + [_i] + [_vp] * 2 + [_i] * 5 + [_f, _i, _vp]),
     "layernorm_fwd": (_i, [_vp] * 3 + [_f] + [_vp] * 3 + [_i] * 3 + [_vp]),
     "layernorm_bwd_workspace_size": (_sz, [_i, _i]),
-    "layernorm_bwd": (_i, [_vp] * 8 + [_i] * 3 + [_vp, _sz, _vp]),
+    "layernorm_bwd": (_i, [_vp] * 8 + [_i] * 4 + [_vp, _sz, _vp]),
     "ss_count_nonfinite_workspace_size": (_sz, []),
     "ss_count_nonfinite": (_i, [_vp, _sz, _i, _vp, _vp, _sz, _vp]),
     "ss_device_status": (_i, [_vp]),

@@ -374,12 +374,12 @@ __global__ void __launch_bounds__(1024) ln_bwd_cols_kernel(const T* __restrict__
   }
 }
 
-struct AddScaleBias {
+struct ScaleBiasOut {
   float *dscale, *dbias;
-  int dim;
+  int dim, add;
   __device__ void put(long long i, float v) const {
-    if (i < dim) dscale[i] += v;
-    else dbias[i - dim] += v;
+    float* out = i < dim ? dscale + i : dbias + (i - dim);
+    *out = (add & (i < dim ? 1 : 2)) ? *out + v : v;
   }
 };
 
@@ -470,7 +470,7 @@ int ln_fwd_launch(const T* x, const float* scale, const float* bias, float eps, 
 
 template <typename T>
 int ln_bwd_launch(const T* dy, const T* x, const float* scale, const float* mean, const float* rstd, float* dx, float* dscale,
-                  float* dbias, int rows, int dim, float* ws, cudaStream_t s) {
+                  float* dbias, int add, int rows, int dim, float* ws, cudaStream_t s) {
   const int grid = ln_bwd_grid(rows, dim);
   if (dim <= 256) {
     const int rc = ln_narrow(ln_lanes(dim), [&](auto tag) -> int {
@@ -486,7 +486,7 @@ int ln_bwd_launch(const T* dy, const T* x, const float* scale, const float* mean
     else ln_bwd_cols_kernel<T, 4><<<grid, threads, 0, s>>>(dy, x, scale, mean, rstd, dx, ws, rows, dim);
     if (cudaGetLastError() != cudaSuccess) return SS_ERR_CUDA;
   }
-  return colsum(ws, 2ll * dim, grid, AddScaleBias{dscale, dbias, dim}, s) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+  return colsum(ws, 2ll * dim, grid, ScaleBiasOut{dscale, dbias, dim, add}, s) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
 }  // namespace
@@ -512,8 +512,8 @@ extern "C" size_t layernorm_bwd_workspace_size(int rows, int dim) {
 }
 
 extern "C" int layernorm_bwd(const void* dy, const void* x, const float* scale, const float* mean, const float* rstd, float* dx,
-                             float* dscale, float* dbias, int rows, int dim, int dtype, void* workspace, size_t ws_bytes,
-                             void* stream) {
+                             float* dscale, float* dbias, int accumulate, int rows, int dim, int dtype, void* workspace,
+                             size_t ws_bytes, void* stream) {
   if (!dy || !x || !scale || !mean || !rstd || !dx || !dscale || !dbias) return SS_ERR_NULL;
   const int v = ln_validate(rows, dim, dtype);
   if (v != SS_OK) return v;
@@ -525,8 +525,8 @@ extern "C" int layernorm_bwd(const void* dy, const void* x, const float* scale, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   float* ws = static_cast<float*>(workspace);
   if (dtype == SS_F32)
-    return ln_bwd_launch(static_cast<const float*>(dy), static_cast<const float*>(x), scale, mean, rstd, dx, dscale, dbias, rows,
-                         dim, ws, s);
+    return ln_bwd_launch(static_cast<const float*>(dy), static_cast<const float*>(x), scale, mean, rstd, dx, dscale, dbias, accumulate,
+                         rows, dim, ws, s);
   return ln_bwd_launch(static_cast<const __nv_bfloat16*>(dy), static_cast<const __nv_bfloat16*>(x), scale, mean, rstd, dx, dscale,
-                       dbias, rows, dim, ws, s);
+                       dbias, accumulate, rows, dim, ws, s);
 }

@@ -35,7 +35,7 @@ struct BwdOut {
 template <int KP, int VP, bool SUM>
 __global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const float* __restrict__ dout, const float* __restrict__ ckpt,
                                                           const float* __restrict__ u0, BwdOut out, float* __restrict__ uend,
-                                                          double* __restrict__ udec) {
+                                                          Dec* __restrict__ udec) {
   using Sm = BwdSmem<KP, VP>;
   constexpr int C = Sm::C, LK = Sm::LK, LV = Sm::LV, LC = Sm::LC, RK = KP / 16, RV = VP / 16;
   extern __shared__ __align__(16) unsigned char raw[];
@@ -80,7 +80,8 @@ __global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const float
         else static_cast<float*>(typed)[at] = x;
       }
   };
-  double total = 0.0;
+  Dec total = {0.f, 0.f};
+  ChunkGates<C> gates;
   const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
   for (int ck = c1 - 1; ck >= c0; --ck) {
     const int t0 = ck * C;
@@ -102,7 +103,10 @@ __global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const float
       }
       continue;
     }
-    if (tid < 32) chunk_decays<C>(p, b, h, t0, len, tid, [&](int i, Dec d) { sm.chi[i] = d.hi; sm.clo[i] = d.lo; });
+    if (tid < 32) {
+      gates.fetch(p, b, h, t0, len, tid);
+      gates.scan(tid, [&](int i, Dec e) { sm.chi[i] = e.hi; sm.clo[i] = e.lo; });
+    }
     load_tile<C, KP, LK>(q + t0 * p.ldq, p.ldq, valid, p.K, sm.q, tid);
     load_tile<C, VP, LV>(d + t0 * ldo, ldo, valid, p.V, sm.d, tid);
     if (!SUM) {
@@ -119,7 +123,7 @@ __global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const float
     }
     __syncthreads();
     const float chi = sm.chi[C - 1], clo = sm.clo[C - 1];
-    total += (double)chi + (double)clo;
+    total = dec_add(total, Dec{chi, clo});
     float m[4][4], pr[4][4];
     if (!SUM) {
       float part = 0.f;  // <S_in, U>
@@ -326,7 +330,7 @@ template <int VP>
 struct BwdTc {
   static constexpr int vt = kTC * VP * 2;  // bytes of a tile VP columns wide
   static constexpr int q = 0, k = q + 2 * kPanel, x = k + 2 * kPanel, v = x + 2 * kPanel, d = v + vt, y0 = d + vt, y1 = y0 + vt, dec = y1 + vt;
-  static constexpr int bar = dec + DecTile::bytes, tm = bar + 16, bytes = tm + 8;
+  static constexpr int bar = dec + DecTile::bytes, tm = bar + 16, hsum = tm + 8, bytes = hsum + 16;
   // in x while it is free: parts of dg
   static constexpr int a = x, b = a + 4 * kTC * 4, rect = b + 4 * kTC * 4, tot = rect + 4 * kTC * 4, thr = tot + 4 * kTC * 4;
   static constexpr int T0 = 0, T1 = 128, T2 = 256, T3 = 384, Pb = 384, dPb = 448, cols = 512;
@@ -357,6 +361,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
   const DecTile dec{sb + L::dec};
   uint64_t* bar = reinterpret_cast<uint64_t*>(raw + L::bar);
   uint32_t* tma = reinterpret_cast<uint32_t*>(raw + L::tm);
+  float* hsum = reinterpret_cast<float*>(raw + L::hsum);  // dg of a chunk, by quarter of its tokens
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = (warp & 3) * 32 + lane, cq = warp >> 2;  // tensor-memory lane, quarter of the columns
   long long id = blockIdx.x;
@@ -403,16 +408,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
   auto load_k = [&](int ck) {
     load_tile_tc<16, kBwdThreads>(k + (long long)ck * kTC * p.ldk, p.ldk, valid_of(ck), p.K, sb + L::k, tid);
   };
+  ChunkGates<kTC> gates;
   auto load_rest = [&](int ck) {
     const int n = valid_of(ck);
     const long long t0 = (long long)ck * kTC;
     load_tile_tc<16, kBwdThreads>(q + t0 * p.ldq, p.ldq, n, p.K, sb + L::q, tid);
     load_tile_tc<VP / 8, kBwdThreads>(d + t0 * ldo, ldo, n, p.V, sb + L::d, tid);
     load_tile_tc<VP / 8, kBwdThreads>(v + t0 * p.ldv, p.ldv, n, p.V, sb + L::v, tid);
-    if (warp == 0) chunk_decays<kTC>(p, b, h, ck * kTC, len, lane, [&](int i, Dec e) { dec.put(i, e); });
+    if (warp == 0) {
+      gates.scan(lane, [&](int i, Dec e) { dec.put(i, e); });
+      gates.fetch(p, b, h, (ck - 1) * kTC, len, lane);
+    }
   };
-  // 32 gradients of q or k of token row i (columns cq * 32 ...): typed, or this head's fp32 part
-  auto put_qk = [&](void* typed, float* part, int t0, const uint32_t (&r)[32], bool live) {
+  // 32 gradients of q or k of this thread's token (columns cq * 32 ...) as this head's fp32 part
+  auto put_part = [&](float* part, int t0, const uint32_t (&r)[32], bool live) {
     if (t0 + row >= p.L) return;
     const long long at = (((long long)b * p.L + t0 + row) * p.H + h) * p.K + cq * 32;
 #pragma unroll
@@ -421,8 +430,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
       float x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = live ? __uint_as_float(r[8 * u + e]) : 0.f;
-      if (part != nullptr) ActT<float>::st8(part + at + 8 * u, x);
-      else ActT<__nv_bfloat16>::st8(static_cast<__nv_bfloat16*>(typed) + at + 8 * u, x);
+      ActT<float>::st8(part + at + 8 * u, x);
     }
   };
   // the three terms of a [K][V] fp32 state, this thread's row and quarter
@@ -443,15 +451,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
   int cend = (len + kTC - 1) / kTC;
   cend = cend < c0 ? c0 : cend < c1 ? cend : c1;
   for (int ck = cend; ck < c1; ++ck) {  // past the row's end
-    uint32_t z[32];
-#pragma unroll
-    for (int e = 0; e < 32; ++e) z[e] = 0u;
-    put_qk(out.dq, out.dqp, ck * kTC, z, false);
-    put_qk(out.dk, out.dkp, ck * kTC, z, false);
     const int rows = p.L - ck * kTC < kTC ? p.L - ck * kTC : kTC;
-    for (int i = tid; i < rows * (p.V / 8); i += kBwdThreads)
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out.dv) + (((long long)b * p.L + ck * kTC + i / (p.V / 8)) * p.H + h) * p.V +
-                                i % (p.V / 8) * 8) = make_uint4(0u, 0u, 0u, 0u);
+    const long long at = ((long long)b * p.L + ck * kTC) * p.H + h;
+    auto clear = [&](void* dst, int width, int esize) {  // rows of `width` elements, H rows apart
+      const int n = width * esize / 16;
+      uint4* to = reinterpret_cast<uint4*>(static_cast<char*>(dst) + at * width * esize);
+      for (int i = tid; i < rows * n; i += kBwdThreads) to[(long long)(i / n) * p.H * n + i % n] = make_uint4(0u, 0u, 0u, 0u);
+    };
+    clear(out.dqp != nullptr ? static_cast<void*>(out.dqp) : out.dq, p.K, out.dqp != nullptr ? 4 : 2);
+    clear(out.dkp != nullptr ? static_cast<void*>(out.dkp) : out.dk, p.K, out.dkp != nullptr ? 4 : 2);
+    clear(out.dv, p.V, 2);
     if (p.g_head) {
       if (tid == 0) out.dg[((long long)b * p.nck + ck) * p.H + h] = 0.f;
     } else if (tid < rows) {
@@ -463,6 +472,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
   auto wait0 = [&]() { ok = mbar_wait_bounded(&bar[0], ph0, kWaitLimitNs); ph0 ^= 1; };
   auto wait1 = [&]() { ok = mbar_wait_bounded(&bar[1], ph1, kWaitLimitNs); ph1 ^= 1; };
   if (c0 < cend) {
+    if (warp == 0) gates.fetch(p, b, h, (cend - 1) * kTC, len, lane);
     load_k(cend - 1);
     load_rest(cend - 1);
   }
@@ -475,7 +485,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
       for (int e = 0; e < VQ; e += 4) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (row < p.K && cq * VQ + e < p.V)
-          x = *reinterpret_cast<const float4*>(ckpt + ((bh * p.nck + ck) * p.K + row) * p.V + cq * VQ + e);
+          x = *(reinterpret_cast<const float4*>(ckpt + (bh * p.nck + ck) * kv) + (long long)((cq * VQ + e) / 4) * p.K + row);
         S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
       }
 #pragma unroll
@@ -640,7 +650,45 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
                  t < 2 || s > 0);
       mma_commit(&bar[0]);
     }
-    if (ck > c0) load_k(ck - 1);
+    // dq, dk, dv: typed through the tiles of k, x and do, whose products are done; fp32 parts as they are
+    const bool shared = out.dqp != nullptr;
+    auto stage = [&](const uint32_t* r, int n, uint32_t tile, int u0) {
+#pragma unroll
+      for (int u = 0; u < n; ++u) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = row < valid ? __uint_as_float(r[8 * u + e]) : 0.f;
+        sts16(sb + tile + tile_at(row, u0 + u), pack8(x));
+      }
+    };
+    {
+      uint32_t r[32];
+      tmem_ld32(tl + L::T2 + cq * 32, r);
+      tmem_wait_ld();
+      if (shared) put_part(out.dqp, t0, r, row < valid);
+      else stage(r, 4, L::k, cq * 4);
+      tmem_ld32(tl + L::T1 + cq * 32, r);
+      tmem_wait_ld();
+      if (shared) put_part(out.dkp, t0, r, row < valid);
+      else stage(r, 4, L::x, cq * 4);
+    }
+    {
+      uint32_t r[VQ];
+      tmem_ldn(tl + L::T0 + cq * VQ, r);
+      tmem_wait_ld();
+      stage(r, NU, L::d, cq * NU);
+    }
+    __syncthreads();
+    if (!shared) {
+      const long long at = (((long long)b * p.L + t0) * p.H + h) * p.K;
+      store_tile_tc<16, kBwdThreads>(sb + L::k, static_cast<__nv_bfloat16*>(out.dq) + at, (long long)p.H * p.K, p.L - t0, p.K, tid);
+      store_tile_tc<16, kBwdThreads>(sb + L::x, static_cast<__nv_bfloat16*>(out.dk) + at, (long long)p.H * p.K, p.L - t0, p.K, tid);
+    }
+    store_tile_tc<VP / 8, kBwdThreads>(sb + L::d, static_cast<__nv_bfloat16*>(out.dv) + (((long long)b * p.L + t0) * p.H + h) * p.V, ldo,
+                                       p.L - t0, p.V, tid);
+    wait0();
+    if (__syncthreads_or(!ok)) break;
+    tc_fence_after_sync();
     {  // what dg is summed from, in x's place
       float* f = reinterpret_cast<float*>(raw);
       f[L::a / 4 + cq * kTC + row] = dot_a;
@@ -652,33 +700,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
       if (lane == 0) f[L::thr / 4 + warp] = through;
     }
     {
-      uint32_t r[32];
-      tmem_ld32(tl + L::T2 + cq * 32, r);
-      tmem_wait_ld();
-      put_qk(out.dq, out.dqp, t0, r, row < valid);
-      tmem_ld32(tl + L::T1 + cq * 32, r);
-      tmem_wait_ld();
-      put_qk(out.dk, out.dkp, t0, r, row < valid);
-    }
-    {
       uint32_t r[VQ];
-      tmem_ldn(tl + L::T0 + cq * VQ, r);
+      tmem_ldn(tl + L::T3 + cq * VQ, r);
       tmem_wait_ld();
-      if (t0 + row < p.L) {
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out.dv) + (((long long)b * p.L + t0 + row) * p.H + h) * p.V + cq * VQ;
 #pragma unroll
-        for (int u = 0; u < NU; ++u) {
-          if (cq * VQ + u * 8 >= p.V) continue;
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = row < valid ? __uint_as_float(r[8 * u + e]) : 0.f;
-          ActT<__nv_bfloat16>::st8(dst + 8 * u, x);
-        }
-      }
+      for (int e = 0; e < VQ; ++e) U[e] = fmaf(U[e], elast, __uint_as_float(r[e]));
     }
-    wait0();
-    if (__syncthreads_or(!ok)) break;
-    tc_fence_after_sync();
+    tc_fence_before_sync();
+    __syncthreads();
+    if (ck > c0) {
+      load_k(ck - 1);
+      load_rest(ck - 1);
+    }
     if (warp < 4) {  // dg of tokens t = 32 warp + lane
       const float* f = reinterpret_cast<const float*>(raw);
       float sa = 0.f, sb_ = 0.f, sl = 0.f;        // sums over the other quarters; then the running sums of this one
@@ -720,24 +753,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
         float s = t < valid ? g : 0.f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) reinterpret_cast<float*>(raw)[L::thr / 4 + 16 + warp] = s;
+        if (lane == 0) hsum[warp] = s;
       } else if (t0 + t < p.L) {
         dst[((long long)b * p.L + t0 + t) * p.H + h] = t < valid ? g : 0.f;
       }
     }
-    uint32_t r[VQ];
-    tmem_ldn(tl + L::T3 + cq * VQ, r);
-    tmem_wait_ld();
-#pragma unroll
-    for (int e = 0; e < VQ; ++e) U[e] = fmaf(U[e], elast, __uint_as_float(r[e]));
-    tc_fence_before_sync();
-    __syncthreads();  // x and the decays are free
-    if (p.g_head && tid == 0) {
-      const float* s = reinterpret_cast<const float*>(raw) + L::thr / 4 + 16;
-      out.dg[((long long)b * p.nck + ck) * p.H + h] = (s[0] + s[1]) + (s[2] + s[3]);
-    }
-    if (ck > c0) load_rest(ck - 1);
-    if (p.g_head) __syncthreads();  // x is written next
+    __syncthreads();  // x is free
+    if (p.g_head && tid == 0) out.dg[((long long)b * p.nck + ck) * p.H + h] = (hsum[0] + hsum[1]) + (hsum[2] + hsum[3]);
   }
   if (!ok) {  // a wait ran out: say so; the outputs are invalid
     if (tid == 0) atomicOr(&g_lin_err, kErrTmaTimeout);
@@ -796,7 +818,7 @@ int bwd_plan(int B, int L, int H, int G, int K, int V, int dtype, int g_head, Bw
   linattn_segments(pl.p, linattn_chunk(dtype), walks, 152);
   const int n = pl.p.nseg;
   pl.states = n > 1 ? (size_t)walks * n * K * V * sizeof(float) : 0;
-  pl.decs = n > 1 ? up16((size_t)walks * n * sizeof(double)) : 0;
+  pl.decs = n > 1 ? up16((size_t)walks * n * sizeof(Dec)) : 0;
   pl.parts = H != G ? (size_t)B * L * H * K * sizeof(float) : 0;
   pl.sums = g_head ? up16((size_t)B * pl.p.nck * H * sizeof(float)) : 0;
   pl.bytes = pl.states + pl.decs + 2 * pl.parts + pl.sums;
@@ -808,7 +830,7 @@ template <typename T, typename Sum, typename Walk>
 int bwd_run(const BwdPlan& pl, const float* dh_last, BwdOut out, float* dg, char* ws, cudaStream_t s, Sum sum, Walk walk) {
   const LinAttn& p = pl.p;
   float* st = reinterpret_cast<float*>(ws);
-  double* dec = reinterpret_cast<double*>(ws + pl.states);
+  Dec* dec = reinterpret_cast<Dec*>(ws + pl.states);
   out.dqp = pl.parts ? reinterpret_cast<float*>(ws + pl.states + pl.decs) : nullptr;
   out.dkp = pl.parts ? reinterpret_cast<float*>(ws + pl.states + pl.decs + pl.parts) : nullptr;
   out.dg = p.g_head ? reinterpret_cast<float*>(ws + pl.states + pl.decs + 2 * pl.parts) : dg;
@@ -840,7 +862,7 @@ int bwd_f32(const BwdPlan& pl, const void* dout, const float* ckpt, const float*
   const size_t smem = sizeof(BwdSmem<KP, VP>);
   return bwd_run<float>(
       pl, dh_last, out, dg, ws, s,
-      [&](float* st, double* dec, const BwdOut& o) {
+      [&](float* st, Dec* dec, const BwdOut& o) {
         return lin_launch(linattn_bwd_kernel<KP, VP, true>, grid, 256, smem, s, pl.p, dout, ckpt, nullptr, o, st, dec);
       },
       [&](const float* u0, const BwdOut& o) {
@@ -855,7 +877,7 @@ int bwd_bf16(const BwdPlan& pl, const void* dout, const float* ckpt, const float
   const unsigned grid = (unsigned)p.B * p.H * p.nseg;
   return bwd_run<__nv_bfloat16>(
       pl, dh_last, out, dg, ws, s,
-      [&](float* st, double* dec, const BwdOut&) {
+      [&](float* st, Dec* dec, const BwdOut&) {
         return lin_launch(linattn_sum_tc_kernel<true>, grid * ((p.V + 63) / 64), kTcThreads, SumTc::bytes, s, p, p.q, p.ldq, dout,
                           (long long)p.H * p.V, st, dec);
       },

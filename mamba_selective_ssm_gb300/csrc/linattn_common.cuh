@@ -39,18 +39,34 @@ struct LinAttn {
   }
 };
 
-// A log decay in units of log2, as a pair of floats hi + lo.  c_i - c_j of two
-// far tokens is then good to ~2^-45 of c and exp2 of it to the hardware's
-// rounding: a single float c would cost |c| * 2^-24 in the exponent, which after
-// a few strong decays (c = -200) is 1e-5 of every later product.
+// A log decay in units of log2, as an unevaluated sum hi + lo of two floats.
+// c_i - c_j of two far tokens is then good to ~2^-45 of c and exp2 of it to the
+// hardware's rounding: a single float c would cost |c| * 2^-24 in the exponent,
+// which after a few strong decays (c = -200) is 1e-5 of every later product.
+// (Two floats, not a double: the running sums of a chunk in fp64 took 8000
+// cycles of one warp that the other warps waited for, in two floats 700.)
 struct Dec {
   float hi, lo;
 };
-__device__ __forceinline__ Dec dec_of(double c) {
-  Dec d;
-  d.hi = (float)c;
-  d.lo = (float)(c - (double)d.hi);
-  return d;
+__device__ __forceinline__ Dec dec_add(Dec a, Dec b) {
+  const float s = __fadd_rn(a.hi, b.hi), t = __fsub_rn(s, a.hi);
+  const float e = __fadd_rn(__fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t)), __fadd_rn(a.lo, b.lo));
+  Dec r;
+  r.hi = __fadd_rn(s, e);
+  r.lo = __fsub_rn(e, __fsub_rn(r.hi, s));
+  return r;
+}
+// Log decays below this empty the state in fp32 anyway (e^-1000 = 0); the clamp
+// keeps -inf, a reset, from making c_i - c_j = -inf + inf.
+constexpr float kMinLogDecay = -1000.0f;
+__device__ __forceinline__ Dec dec_of_log(float g) {  // g log2(e)
+  constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f;
+  if (g < kMinLogDecay) g = kMinLogDecay;
+  const float p = __fmul_rn(g, kHi), e = __fmaf_rn(g, kLo, __fmaf_rn(g, kHi, -p));
+  Dec r;
+  r.hi = __fadd_rn(p, e);
+  r.lo = __fsub_rn(e, __fsub_rn(r.hi, p));
+  return r;
 }
 __device__ __forceinline__ float dec_exp(float hi, float lo) { return ex2(hi) * fmaf(lo, kLn2, 1.0f); }
 // e^{c_i - c_j}
@@ -58,35 +74,44 @@ __device__ __forceinline__ float dec_diff(float hi_i, float lo_i, float hi_j, fl
   return ex2((hi_i - hi_j) + (lo_i - lo_j));
 }
 
-// Log decays below this empty the state in fp32 anyway (e^-1000 = 0); the clamp
-// keeps -inf, a reset, from making c_i - c_j = -inf + inf.
-constexpr float kMinLogDecay = -1000.0f;
-
-// Running log2 decays of the chunk at t0, put(i, c_i) for i < C (a token past the
-// row's end decays by 1).  One warp, C / 32 consecutive tokens a lane.
-template <int C, typename Put>
-__device__ __forceinline__ void chunk_decays(const LinAttn& p, int b, int h, int t0, int len, int lane, Put put) {
-  constexpr int PER = C / 32;
-  double x[PER];
-  double s = 0.0;
+// The running log2 decays of chunks, by one warp: lane l owns C / 32 consecutive
+// tokens.  fetch() reads a chunk's gates (a token past the row's end decays by
+// 1), scan() puts their running sums with put(i, c_i); a caller fetches one
+// chunk ahead, so that no one waits for the loads.
+template <int C>
+struct ChunkGates {
+  static constexpr int PER = C / 32;
+  float g[PER];
+  __device__ __forceinline__ void fetch(const LinAttn& p, int b, int h, int t0, int len, int lane) {
 #pragma unroll
-  for (int e = 0; e < PER; ++e) {
-    const int t = t0 + lane * PER + e;
-    float gv = t < len ? p.gate(b, t, h) : 0.0f;
-    if (gv < kMinLogDecay) gv = kMinLogDecay;
-    s += (double)gv * 1.4426950408889634;
-    x[e] = s;
+    for (int e = 0; e < PER; ++e) {
+      const int t = t0 + lane * PER + e;
+      g[e] = t >= 0 && t < len ? p.gate(b, t, h) : 0.0f;
+    }
   }
-  double incl = s;
+  template <typename Put>
+  __device__ __forceinline__ void scan(int lane, Put put) const {
+    Dec x[PER];
+    x[0] = dec_of_log(g[0]);
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double u = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += u;
+    for (int e = 1; e < PER; ++e) x[e] = dec_add(x[e - 1], dec_of_log(g[e]));
+    Dec incl = x[PER - 1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      Dec u;
+      u.hi = __shfl_up_sync(0xffffffffu, incl.hi, o);
+      u.lo = __shfl_up_sync(0xffffffffu, incl.lo, o);
+      const Dec s = dec_add(incl, u);
+      if (lane >= o) incl = s;
+    }
+    Dec base;
+    base.hi = __shfl_up_sync(0xffffffffu, incl.hi, 1);
+    base.lo = __shfl_up_sync(0xffffffffu, incl.lo, 1);
+    if (lane == 0) base.hi = base.lo = 0.0f;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) put(lane * PER + e, dec_add(base, x[e]));
   }
-  const double base = incl - s;
-#pragma unroll
-  for (int e = 0; e < PER; ++e) put(lane * PER + e, dec_of(base + x[e]));
-}
+};
 
 constexpr int kLinMaxHead = 128;  // widest K, V
 constexpr int kLinChunkF32 = 64;    // tokens of a chunk: fp32 (FMA pipe)

@@ -17,7 +17,7 @@ struct FwdSmem {
 template <int KP, bool SUM>
 __global__ void __launch_bounds__(256) linattn_fwd_kernel(LinAttn p, const float* __restrict__ s0, float* __restrict__ o,
                                                           float* __restrict__ ckpt, float* __restrict__ send,
-                                                          double* __restrict__ sdec) {
+                                                          Dec* __restrict__ sdec) {
   using Sm = FwdSmem<KP>;
   constexpr int C = Sm::C, LK = Sm::LK, LV = Sm::LV, LC = Sm::LC, RK = KP / 16;
   extern __shared__ __align__(16) unsigned char raw[];
@@ -50,7 +50,8 @@ __global__ void __launch_bounds__(256) linattn_fwd_kernel(LinAttn p, const float
         if (kk < p.K && vv < vw) S[r][c] = src[(long long)kk * p.V + v0 + vv];
       }
   }
-  double total = 0.0;
+  Dec total = {0.f, 0.f};
+  ChunkGates<C> gates;
   const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
   for (int ck = c0; ck < c1; ++ck) {
     const int t0 = ck * C;
@@ -62,7 +63,10 @@ __global__ void __launch_bounds__(256) linattn_fwd_kernel(LinAttn p, const float
           o[(((long long)b * p.L + t0 + i / vw) * p.H + h) * p.V + v0 + i % vw] = 0.f;
       continue;
     }
-    if (tid < 32) chunk_decays<C>(p, b, h, t0, len, tid, [&](int i, Dec d) { sm.chi[i] = d.hi; sm.clo[i] = d.lo; });
+    if (tid < 32) {
+      gates.fetch(p, b, h, t0, len, tid);
+      gates.scan(tid, [&](int i, Dec e) { sm.chi[i] = e.hi; sm.clo[i] = e.lo; });
+    }
     if (!SUM) load_tile<C, KP, LK>(q + t0 * p.ldq, p.ldq, valid, p.K, sm.q, tid);
     load_tile<C, KP, LK>(k + t0 * p.ldk, p.ldk, valid, p.K, sm.k, tid);
     load_tile<C, kVT, LV>(v + t0 * p.ldv, p.ldv, valid, vw, sm.v, tid);
@@ -109,7 +113,7 @@ __global__ void __launch_bounds__(256) linattn_fwd_kernel(LinAttn p, const float
     }
     __syncthreads();
     const float chi = sm.chi[C - 1], clo = sm.clo[C - 1];
-    total += (double)chi + (double)clo;
+    total = dec_add(total, Dec{chi, clo});
     for (int i = tid; i < C * KP; i += 256) {  // k_j e^{c_last - c_j}
       const int j = i / KP;
       sm.k[j * LK + i % KP] *= dec_diff(chi, clo, sm.chi[j], sm.clo[j]);
@@ -214,13 +218,17 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_fwd_tc_kernel(LinAttn p
                                                              pack_bf16(S[8 * u + 4], S[8 * u + 5]), pack_bf16(S[8 * u + 6], S[8 * u + 7])));
   };
   auto valid_of = [&](int ck) { const int n = len - ck * kTC; return n < 0 ? 0 : n < kTC ? n : kTC; };
+  ChunkGates<kTC> gates;
   auto load = [&](int ck) {
     const int n = valid_of(ck);
     const long long t0 = (long long)ck * kTC;
     load_tile_tc<16, kTcThreads>(q + t0 * p.ldq, p.ldq, n, p.K, sb + L::q, tid);
     load_tile_tc<16, kTcThreads>(k + t0 * p.ldk, p.ldk, n, p.K, sb + L::k, tid);
     load_tile_tc<8, kTcThreads>(v + t0 * p.ldv, p.ldv, n, vw, sb + L::v, tid);
-    if (warp == 0) chunk_decays<kTC>(p, b, h, ck * kTC, len, lane, [&](int i, Dec d) { dec.put(i, d); });
+    if (warp == 0) {
+      gates.scan(lane, [&](int i, Dec d) { dec.put(i, d); });
+      gates.fetch(p, b, h, (ck + 1) * kTC, len, lane);
+    }
   };
   const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
   int cend = (len + kTC - 1) / kTC;  // chunks that hold a token
@@ -228,6 +236,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_fwd_tc_kernel(LinAttn p
   uint32_t phase = 0;
   bool ok = true;
   if (c0 < cend) {
+    if (warp == 0) gates.fetch(p, b, h, c0 * kTC, len, lane);
     load(c0);
     store_s();
   }
@@ -310,10 +319,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_fwd_tc_kernel(LinAttn p
     }
     const float ei = p.scale * dec_exp(own.hi, own.lo);
     if (ckpt != nullptr && row < p.K) {
-      float* dst = ckpt + ((bh * p.nck + ck) * p.K + row) * p.V + v0 + half * 32;
+      float4* dst = reinterpret_cast<float4*>(ckpt + (bh * p.nck + ck) * p.K * p.V) + row;
 #pragma unroll
       for (int e = 0; e < 32; e += 4)
-        if (half * 32 + e < vw) *reinterpret_cast<float4*>(dst + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+        if (half * 32 + e < vw) dst[(long long)((v0 + half * 32 + e) / 4) * p.K] = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
     }
     ok = mbar_wait_bounded(bar, phase, kWaitLimitNs);
     phase ^= 1;
@@ -332,19 +341,17 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_fwd_tc_kernel(LinAttn p
       tmem_ld16(tl + L::Oa + half * 32 + g * 16, a);
       tmem_ld16(tl + L::Oi + half * 32 + g * 16, i);
       tmem_wait_ld();
-      if (t0 + row < p.L) {
-        __nv_bfloat16* dst = o + (((long long)b * p.L + t0 + row) * p.H + h) * p.V + v0 + half * 32 + g * 16;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (half * 32 + g * 16 + u * 8 >= vw) continue;
-          float x[8];
+      for (int u = 0; u < 2; ++u) {
+        float x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            x[e] = row < valid ? fmaf(__uint_as_float(i[8 * u + e]), ei, p.scale * __uint_as_float(a[8 * u + e])) : 0.f;
-          ActT<__nv_bfloat16>::st8(dst + 8 * u, x);
-        }
+        for (int e = 0; e < 8; ++e)
+          x[e] = row < valid ? fmaf(__uint_as_float(i[8 * u + e]), ei, p.scale * __uint_as_float(a[8 * u + e])) : 0.f;
+        sts16(sb + L::w + tile_at(row, half * 4 + g * 2 + u), pack8(x));
       }
     }
+    __syncthreads();
+    store_tile_tc<8, kTcThreads>(sb + L::w, o + (((long long)b * p.L + t0) * p.H + h) * p.V + v0, (long long)p.H * p.V, p.L - t0, vw, tid);
   }
   if (!ok) {  // a wait ran out: say so; the outputs are invalid
     if (tid == 0) atomicOr(&g_lin_err, kErrTmaTimeout);
@@ -384,7 +391,7 @@ int fwd_plan(int B, int L, int H, int G, int K, int V, int dtype, FwdPlan& pl) {
   if (pl.walks > (1ll << 24)) return SS_ERR_DIM;
   linattn_segments(pl.p, linattn_chunk(dtype), pl.walks, (dtype == SS_BF16 || K <= 64 ? 2 : 1) * 152);
   pl.states = pl.p.nseg > 1 ? (size_t)B * H * pl.p.nseg * K * V * sizeof(float) : 0;
-  pl.bytes = pl.p.nseg > 1 ? pl.states + (size_t)B * H * pl.p.nseg * sizeof(double) : 0;
+  pl.bytes = pl.p.nseg > 1 ? pl.states + (size_t)B * H * pl.p.nseg * sizeof(Dec) : 0;
   return SS_OK;
 }
 
@@ -394,7 +401,7 @@ int fwd_run(const FwdPlan& pl, const float* h0, void* ws, cudaStream_t s, Sum su
   const LinAttn& p = pl.p;
   if (p.nseg == 1) return walk(h0);
   float* st = static_cast<float*>(ws);
-  double* dec = reinterpret_cast<double*>(static_cast<char*>(ws) + pl.states);
+  Dec* dec = reinterpret_cast<Dec*>(static_cast<char*>(ws) + pl.states);
   const int rc = sum(st, dec);
   if (rc != SS_OK) return rc;
   const long long kv = (long long)p.K * p.V;
@@ -409,7 +416,7 @@ int fwd_f32(const FwdPlan& pl, const float* h0, float* o, float* ckpt, float* h_
   const size_t smem = sizeof(FwdSmem<KP>);
   return fwd_run(
       pl, h0, ws, s,
-      [&](float* st, double* dec) { return lin_launch(linattn_fwd_kernel<KP, true>, grid, 256, smem, s, pl.p, nullptr, o, ckpt, st, dec); },
+      [&](float* st, Dec* dec) { return lin_launch(linattn_fwd_kernel<KP, true>, grid, 256, smem, s, pl.p, nullptr, o, ckpt, st, dec); },
       [&](const float* s0) { return lin_launch(linattn_fwd_kernel<KP, false>, grid, 256, smem, s, pl.p, s0, o, ckpt, h_last, nullptr); });
 }
 
@@ -418,7 +425,7 @@ int fwd_bf16(const FwdPlan& pl, const float* h0, __nv_bfloat16* o, float* ckpt, 
   const unsigned grid = (unsigned)pl.walks * p.nseg;
   return fwd_run(
       pl, h0, ws, s,
-      [&](float* st, double* dec) {
+      [&](float* st, Dec* dec) {
         return lin_launch(linattn_sum_tc_kernel<false>, grid, kTcThreads, SumTc::bytes, s, p, p.k, p.ldk, p.v, p.ldv, st, dec);
       },
       [&](const float* s0) { return lin_launch(linattn_fwd_tc_kernel, grid, kTcThreads, FwdTc::bytes, s, p, s0, o, ckpt, h_last); });

@@ -161,6 +161,23 @@ __device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) { return ActT<__nv_bfloat16>::pack2(lo, hi); }
 
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+
+// A tile's first `rows` rows and `width` columns to global memory.  A lane's
+// accumulators are one row, so storing them as they are would touch 32 rows with
+// each instruction; through a tile a warp stores whole rows (the backward's three
+// outputs: 9000 -> 2000 cycles a chunk).
+template <int UNITS, int THREADS>
+__device__ __forceinline__ void store_tile_tc(uint32_t tile, __nv_bfloat16* __restrict__ dst, long long ld, int rows, int width, int tid) {
+#pragma unroll
+  for (int i = 0; i < kTC * UNITS / THREADS; ++i) {
+    const int at = i * THREADS + tid, r = at / UNITS, u = at % UNITS;
+    if (r < rows && u * 8 < width) *reinterpret_cast<uint4*>(dst + (long long)r * ld + u * 8) = lds16(tile + tile_at(r, u));
+  }
+}
+
 // An fp32 value as a sum of three bf16 terms: the first is off by 2^-8 of the
 // value at most, the first two by 2^-16, all three by 2^-24, the half-step of
 // fp32 itself, so that a product of the terms with an exact bf16 operand is an
@@ -206,7 +223,7 @@ struct SumTc {
 template <bool REV>
 __global__ void __launch_bounds__(kTcThreads, 2) linattn_sum_tc_kernel(LinAttn p, const __nv_bfloat16* __restrict__ xs, long long ldx,
                                                                       const __nv_bfloat16* __restrict__ ys, long long ldy,
-                                                                      float* __restrict__ send, double* __restrict__ sdec) {
+                                                                      float* __restrict__ send, Dec* __restrict__ sdec) {
   using L = SumTc;
   extern __shared__ __align__(1024) unsigned char raw[];
   const uint32_t sb = smem_u32(raw);
@@ -243,24 +260,31 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_sum_tc_kernel(LinAttn p
   const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
   int cend = (len + kTC - 1) / kTC;
   cend = cend < c0 ? c0 : cend < c1 ? cend : c1;
+  ChunkGates<kTC> gates;
   auto load = [&](int ck) {
     const int m = len - ck * kTC, n = m < kTC ? m : kTC;
     const long long t0 = (long long)ck * kTC;
     load_tile_tc<16, kTcThreads>(xs + t0 * ldx, ldx, n, p.K, sb + L::x, tid);
     load_tile_tc<8, kTcThreads>(ys + t0 * ldy, ldy, n, vw, sb + L::y, tid);
-    if (warp == 0) chunk_decays<kTC>(p, b, h, ck * kTC, len, lane, [&](int i, Dec d) { dec.put(i, d); });
+    if (warp == 0) {
+      gates.scan(lane, [&](int i, Dec d) { dec.put(i, d); });
+      gates.fetch(p, b, h, (REV ? ck - 1 : ck + 1) * kTC, len, lane);
+    }
   };
-  double total = 0.0;
+  Dec total = {0.f, 0.f};
   uint32_t phase = 0;
   bool ok = true;
-  if (c0 < cend) load(REV ? cend - 1 : c0);
+  if (c0 < cend) {
+    if (warp == 0) gates.fetch(p, b, h, (REV ? cend - 1 : c0) * kTC, len, lane);
+    load(REV ? cend - 1 : c0);
+  }
   for (int n = 0; n < cend - c0; ++n) {
     const int ck = REV ? cend - 1 - n : c0 + n;
     cp_wait_all();
     __syncthreads();
     const Dec last = dec.get(kTC - 1);
     const float elast = dec_exp(last.hi, last.lo);
-    total += (double)last.hi + (double)last.lo;
+    total = dec_add(total, last);
     const int r = tid >> 1, u0 = (tid & 1) * 4;
     const Dec dr = dec.get(r);
     const float w = REV ? p.scale * dec_exp(dr.hi, dr.lo) : dec_diff(last.hi, last.lo, dr.hi, dr.lo);
@@ -318,7 +342,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_sum_tc_kernel(LinAttn p
 // s[next] = 2^{dec} s + end.
 template <bool REV>
 __global__ void __launch_bounds__(256) linattn_join_kernel(const float* __restrict__ first, float* __restrict__ st,
-                                                           const double* __restrict__ dec, long long kv, int nseg) {
+                                                           const Dec* __restrict__ dec, long long kv, int nseg) {
   const long long bh = blockIdx.y;
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   if (i >= kv) return;
@@ -326,7 +350,7 @@ __global__ void __launch_bounds__(256) linattn_join_kernel(const float* __restri
   for (int m = 0; m < nseg; ++m) {
     const int n = REV ? nseg - 1 - m : m;
     float* at = st + (bh * nseg + n) * kv + i;
-    const Dec d = dec_of(dec[bh * nseg + n]);
+    const Dec d = dec[bh * nseg + n];
     const float end = *at;
     *at = s;
     s = fmaf(dec_exp(d.hi, d.lo), s, end);

@@ -31,6 +31,7 @@ parameters, states and gradients are ``torch.float32``.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -370,29 +371,64 @@ def linattn_num_chunks(L: int, dtype) -> int:
     return load().linattn_num_chunks(L, _DT[dtype])
 
 
-def _rows(t, name, shape, dtype, device):
+# The calls below take a few microseconds on the GPU at their smallest, so their Python is kept short: a tensor
+# that is as expected passes one test, sizes of scratch are kept by the sizes they follow from, and pointers and the
+# stream go to ctypes as integers.
+
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _at(t, name, shape, dtype, dev):
+    """The address of a dense tensor of this shape, type and device (``_req``'s errors for any other)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_cuda
+            and t.is_contiguous()):
+        _req(t, name, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def _opt_at(t, name, shape, dtype, dev):
+    return None if t is None else _at(t, name, shape, dtype, dev)
+
+
+def _rows(t, name, shape, dtype, dev):
     """A [B, L, heads, width] input whose tokens may lie further apart than their own rows (a column range of a
-    wider [B, L, W] array): its token stride in elements."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    wider [B, L, W] array): its address and its token stride in elements."""
     B, L, n, w = shape
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_cuda:
+        if t.is_contiguous():
+            return t.data_ptr(), n * w
+    elif not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    elif not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    elif t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    elif t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    else:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
     sb, sl, sn, sw = t.stride()
-    if L == 1 and B > 1:
-        sl = sb  # one token a row: rows are the batch's
-    elif L == 1:
-        sl = n * w
+    if L == 1:
+        sl = sb if B > 1 else n * w  # one token a row: rows are the batch's
     if (w > 1 and sw != 1) or (n > 1 and sn != w) or (B > 1 and L > 0 and sb != L * sl):
         raise ValueError(f"{name} must hold each token's heads contiguously and its batch rows L tokens apart, got "
                          f"strides {t.stride()}")
-    return sl
+    return t.data_ptr(), sl
+
+
+@functools.lru_cache(maxsize=1024)
+def _linattn_plan(B, L, H, G, K, V, per_head, sdt):
+    """(chunks, forward scratch, backward scratch) of a call's sizes."""
+    lib = load()
+    return (lib.linattn_num_chunks(L, sdt), lib.linattn_fwd_workspace_size(B, L, H, G, K, V, sdt),
+            lib.linattn_bwd_workspace_size(B, L, H, G, K, V, per_head, sdt))
+
+
+@functools.lru_cache(maxsize=1024)
+def _layernorm_plan(R, N):
+    return load().layernorm_bwd_workspace_size(R, N)
 
 
 def _linattn_sizes(q, v):
@@ -405,18 +441,19 @@ def _linattn_sizes(q, v):
 
 
 def _linattn_gate(g, B, L, H, dev):
-    """1 when g is one log decay for each head, 0 when it has one for each token."""
+    """The address of g, and 1 when it has one log decay for each head, 0 when one for each token."""
     if isinstance(g, torch.Tensor) and g.dim() == 1:
-        _req(g, "g", (H,), torch.float32, dev)
-        return 1
-    _req(g, "g", (B, L, H), torch.float32, dev)
-    return 0
+        return _at(g, "g", (H,), torch.float32, dev), 1
+    return _at(g, "g", (B, L, H), torch.float32, dev), 0
 
 
 def _scratch(workspace, need, dev):
-    if workspace is None and need > 0:
+    if workspace is None:
+        if need == 0:
+            return None, 0
         workspace = torch.empty(need, device=dev, dtype=torch.uint8)
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+        return workspace.data_ptr(), need
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def linattn_fwd(q, k, v, g, h0=None, scale=None, lengths=None, want_ckpt: bool = True, want_h_last: bool = True,
@@ -428,27 +465,25 @@ def linattn_fwd(q, k, v, g, h0=None, scale=None, lengths=None, want_ckpt: bool =
     a wider [B, L, W] tensor.  ``g`` are log decays, fp32 [B, L, H] or one for each head [H].  ``lengths`` (int32 [B])
     ends each row; past it o is 0 and the state stays.  ``scale`` is ``K ** -0.5`` unless given.  ``ckpt`` (None unless
     ``want_ckpt``) is what ``linattn_bwd`` starts from."""
-    lib = load()
     B, L, H, G, K, V = _linattn_sizes(q, v)
-    dev, dt = q.device, q.dtype
+    dev, dt, f32 = q.device, q.dtype, torch.float32
     sdt = _act_dtype(q)
-    ldq = _rows(q, "q", (B, L, G, K), dt, dev)
-    ldk = _rows(k, "k", (B, L, G, K), dt, dev)
-    ldv = _rows(v, "v", (B, L, H, V), dt, dev)
-    per_head = _linattn_gate(g, B, L, H, dev)
-    if h0 is not None:
-        _req(h0, "h0", (B, H, K, V), torch.float32, dev)
-    if lengths is not None:
-        _req(lengths, "lengths", (B,), torch.int32, dev)
+    pq, ldq = _rows(q, "q", (B, L, G, K), dt, dev)
+    pk, ldk = _rows(k, "k", (B, L, G, K), dt, dev)
+    pv, ldv = _rows(v, "v", (B, L, H, V), dt, dev)
+    pg, per_head = _linattn_gate(g, B, L, H, dev)
+    ph = _opt_at(h0, "h0", (B, H, K, V), f32, dev)
+    pn = _opt_at(lengths, "lengths", (B,), torch.int32, dev)
+    chunks, need, _ = _linattn_plan(B, L, H, G, K, V, 0, sdt)
     o = torch.empty((B, L, H, V), device=dev, dtype=dt)
-    f32 = dict(device=dev, dtype=torch.float32)
-    ckpt = torch.empty((B, H, lib.linattn_num_chunks(L, sdt), K, V), **f32) if want_ckpt else None
-    h_last = torch.empty((B, H, K, V), **f32) if want_h_last else None
-    workspace, ws_have = _scratch(workspace, lib.linattn_fwd_workspace_size(B, L, H, G, K, V, sdt), dev)
-    rc = lib.linattn_fwd(_p(q), ldq, _p(k), ldk, _p(v), ldv, _p(g), per_head, _p(h0), _p(lengths), _p(o), _p(ckpt),
-                         _p(h_last), B, L, H, G, K, V, K ** -0.5 if scale is None else scale, sdt, _p(workspace), ws_have,
-                         _stream())
-    check(rc, "linattn_fwd")
+    ckpt = torch.empty((B, H, chunks, K, V), device=dev, dtype=f32) if want_ckpt else None
+    h_last = torch.empty((B, H, K, V), device=dev, dtype=f32) if want_h_last else None
+    pw, have = _scratch(workspace, need, dev)
+    rc = load().linattn_fwd(pq, ldq, pk, ldk, pv, ldv, pg, per_head, ph, pn, o.data_ptr(),
+                            ckpt.data_ptr() if want_ckpt else None, h_last.data_ptr() if want_h_last else None, B, L, H, G, K, V,
+                            K ** -0.5 if scale is None else scale, sdt, pw, have, _raw_stream(dev))
+    if rc:
+        check(rc, "linattn_fwd")
     return o, ckpt, h_last
 
 
@@ -457,96 +492,90 @@ def linattn_bwd(q, k, v, g, ckpt, do, dh_last=None, scale=None, lengths=None, dg
     """Gradients of ``sum(o * do)`` (+ ``sum(h_last * dh_last)``) through ``linattn_fwd`` called with the same q, k, v, g,
     scale and lengths -> dict ``dq, dk, dv`` (q's type), ``dg``, ``dh0`` (fp32).  With one decay for each head ``dg`` [H]
     accumulates into the given tensor (zeros when None)."""
-    lib = load()
     B, L, H, G, K, V = _linattn_sizes(q, v)
-    dev, dt = q.device, q.dtype
+    dev, dt, f32 = q.device, q.dtype, torch.float32
     sdt = _act_dtype(q)
-    ldq = _rows(q, "q", (B, L, G, K), dt, dev)
-    ldk = _rows(k, "k", (B, L, G, K), dt, dev)
-    ldv = _rows(v, "v", (B, L, H, V), dt, dev)
-    per_head = _linattn_gate(g, B, L, H, dev)
-    _req(ckpt, "ckpt", (B, H, lib.linattn_num_chunks(L, sdt), K, V), torch.float32, dev)
-    _req(do, "do", (B, L, H, V), dt, dev)
-    if dh_last is not None:
-        _req(dh_last, "dh_last", (B, H, K, V), torch.float32, dev)
-    if lengths is not None:
-        _req(lengths, "lengths", (B,), torch.int32, dev)
-    f32 = dict(device=dev, dtype=torch.float32)
-    if dg is not None:
-        _req(dg, "dg", g.shape, torch.float32, dev)
-    else:
-        dg = torch.zeros((H,), **f32) if per_head else torch.empty((B, L, H), **f32)
-    out = {"dq": torch.empty((B, L, G, K), device=dev, dtype=dt), "dk": torch.empty((B, L, G, K), device=dev, dtype=dt),
-           "dv": torch.empty((B, L, H, V), device=dev, dtype=dt), "dg": dg,
-           "dh0": torch.empty((B, H, K, V), **f32) if want_dh0 else None}
-    workspace, ws_have = _scratch(workspace, lib.linattn_bwd_workspace_size(B, L, H, G, K, V, per_head, sdt), dev)
-    rc = lib.linattn_bwd(_p(q), ldq, _p(k), ldk, _p(v), ldv, _p(g), per_head, _p(lengths), _p(ckpt), _p(do), _p(dh_last),
-                         _p(out["dq"]), _p(out["dk"]), _p(out["dv"]), _p(dg), _p(out["dh0"]), B, L, H, G, K, V,
-                         K ** -0.5 if scale is None else scale, sdt, _p(workspace), ws_have, _stream())
-    check(rc, "linattn_bwd")
-    return out
+    pq, ldq = _rows(q, "q", (B, L, G, K), dt, dev)
+    pk, ldk = _rows(k, "k", (B, L, G, K), dt, dev)
+    pv, ldv = _rows(v, "v", (B, L, H, V), dt, dev)
+    pg, per_head = _linattn_gate(g, B, L, H, dev)
+    chunks, _, need = _linattn_plan(B, L, H, G, K, V, per_head, sdt)
+    pc = _at(ckpt, "ckpt", (B, H, chunks, K, V), f32, dev)
+    pd = _at(do, "do", (B, L, H, V), dt, dev)
+    pl = _opt_at(dh_last, "dh_last", (B, H, K, V), f32, dev)
+    pn = _opt_at(lengths, "lengths", (B,), torch.int32, dev)
+    if dg is None:
+        dg = torch.zeros((H,), device=dev, dtype=f32) if per_head else torch.empty((B, L, H), device=dev, dtype=f32)
+    dq = torch.empty((B, L, G, K), device=dev, dtype=dt)
+    dk = torch.empty((B, L, G, K), device=dev, dtype=dt)
+    dv = torch.empty((B, L, H, V), device=dev, dtype=dt)
+    dh0 = torch.empty((B, H, K, V), device=dev, dtype=f32) if want_dh0 else None
+    pw, have = _scratch(workspace, need, dev)
+    rc = load().linattn_bwd(pq, ldq, pk, ldk, pv, ldv, pg, per_head, pn, pc, pd, pl, dq.data_ptr(), dk.data_ptr(),
+                            dv.data_ptr(), _at(dg, "dg", g.shape, f32, dev), dh0.data_ptr() if want_dh0 else None, B, L, H, G, K, V,
+                            K ** -0.5 if scale is None else scale, sdt, pw, have, _raw_stream(dev))
+    if rc:
+        check(rc, "linattn_bwd")
+    return {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dh0": dh0}
 
 
 def linattn_step(q, k, v, g, h, scale=None):
     """One token for B sequences: updates ``h`` [B, H, K, V] in place and returns o [B, H, V].
     ``q, k`` [B, G, K], ``v`` [B, H, V], ``g`` fp32 [B, H] or [H]."""
-    lib = load()
     B, G, K = q.shape
-    H, V = v.shape[1:]
-    dev, dt = q.device, q.dtype
+    _, H, V = v.shape
+    dev, dt, f32 = q.device, q.dtype, torch.float32
     sdt = _act_dtype(q)
-    _req(q, "q", (B, G, K), dt, dev)
-    _req(k, "k", (B, G, K), dt, dev)
-    _req(v, "v", (B, H, V), dt, dev)
+    pq, pk = _at(q, "q", (B, G, K), dt, dev), _at(k, "k", (B, G, K), dt, dev)
+    pv, ph = _at(v, "v", (B, H, V), dt, dev), _at(h, "h", (B, H, K, V), f32, dev)
     per_head = 1 if g.dim() == 1 else 0
-    _req(g, "g", (H,) if per_head else (B, H), torch.float32, dev)
-    _req(h, "h", (B, H, K, V), torch.float32, dev)
+    pg = _at(g, "g", (H,) if per_head else (B, H), f32, dev)
     o = torch.empty_like(v)
-    rc = lib.linattn_step(_p(q), _p(k), _p(v), _p(g), per_head, _p(h), _p(o), B, H, G, K, V,
-                          K ** -0.5 if scale is None else scale, sdt, _stream())
-    check(rc, "linattn_step")
+    rc = load().linattn_step(pq, pk, pv, pg, per_head, ph, o.data_ptr(), B, H, G, K, V, K ** -0.5 if scale is None else scale,
+                             sdt, _raw_stream(dev))
+    if rc:
+        check(rc, "linattn_step")
     return o
 
 
 def layernorm_fwd(x, scale, bias, eps: float, want_stats: bool = True):
     """Layer norm of the rows of x [rows, dim]: ``(y, mean, rstd)`` with y in x's dtype and the statistics fp32 (None
     unless ``want_stats``); ``bias`` may be None."""
-    lib = load()
     R, N = x.shape
-    dev = x.device
+    dev, f32 = x.device, torch.float32
     dt = _act_dtype(x)
-    _req(x, "x", (R, N), x.dtype, dev)
-    _req(scale, "scale", (N,), torch.float32, dev)
-    if bias is not None:
-        _req(bias, "bias", (N,), torch.float32, dev)
+    px, ps = _at(x, "x", (R, N), x.dtype, dev), _at(scale, "scale", (N,), f32, dev)
+    pb = _opt_at(bias, "bias", (N,), f32, dev)
     y = torch.empty_like(x)
-    mean = torch.empty((R,), device=dev, dtype=torch.float32) if want_stats else None
-    rstd = torch.empty((R,), device=dev, dtype=torch.float32) if want_stats else None
-    rc = lib.layernorm_fwd(_p(x), _p(scale), _p(bias), float(eps), _p(y), _p(mean), _p(rstd), R, N, dt, _stream())
-    check(rc, "layernorm_fwd")
+    mean = torch.empty((R,), device=dev, dtype=f32) if want_stats else None
+    rstd = torch.empty((R,), device=dev, dtype=f32) if want_stats else None
+    rc = load().layernorm_fwd(px, ps, pb, eps, y.data_ptr(), mean.data_ptr() if want_stats else None,
+                              rstd.data_ptr() if want_stats else None, R, N, dt, _raw_stream(dev))
+    if rc:
+        check(rc, "layernorm_fwd")
     return y, mean, rstd
 
 
 def layernorm_bwd(dy, x, scale, mean, rstd, dscale=None, dbias=None, workspace=None):
     """Layer norm backward -> ``(dx, dscale, dbias)``, all fp32; dscale and dbias accumulate into the given tensors
-    (zeros when None)."""
-    lib = load()
+    and are made when None."""
     R, N = x.shape
-    dev = x.device
+    dev, f32 = x.device, torch.float32
     dt = _act_dtype(x)
-    _req(dy, "dy", (R, N), x.dtype, dev)
-    _req(x, "x", (R, N), x.dtype, dev)
-    _req(scale, "scale", (N,), torch.float32, dev)
-    _req(mean, "mean", (R,), torch.float32, dev)
-    _req(rstd, "rstd", (R,), torch.float32, dev)
-    f32 = dict(device=dev, dtype=torch.float32)
-    dscale = torch.zeros((N,), **f32) if dscale is None else _req(dscale, "dscale", (N,), torch.float32, dev)
-    dbias = torch.zeros((N,), **f32) if dbias is None else _req(dbias, "dbias", (N,), torch.float32, dev)
-    dx = torch.empty((R, N), **f32)
-    workspace, ws_have = _scratch(workspace, lib.layernorm_bwd_workspace_size(R, N), dev)
-    rc = lib.layernorm_bwd(_p(dy), _p(x), _p(scale), _p(mean), _p(rstd), _p(dx), _p(dscale), _p(dbias), R, N, dt,
-                           _p(workspace), ws_have, _stream())
-    check(rc, "layernorm_bwd")
+    py, px = _at(dy, "dy", (R, N), x.dtype, dev), _at(x, "x", (R, N), x.dtype, dev)
+    ps = _at(scale, "scale", (N,), f32, dev)
+    pm, pr = _at(mean, "mean", (R,), f32, dev), _at(rstd, "rstd", (R,), f32, dev)
+    add = (1 if dscale is not None else 0) | (2 if dbias is not None else 0)
+    if dscale is None:
+        dscale = torch.empty((N,), device=dev, dtype=f32)
+    if dbias is None:
+        dbias = torch.empty((N,), device=dev, dtype=f32)
+    dx = torch.empty((R, N), device=dev, dtype=f32)
+    pw, have = _scratch(workspace, _layernorm_plan(R, N), dev)
+    rc = load().layernorm_bwd(py, px, ps, pm, pr, dx.data_ptr(), _at(dscale, "dscale", (N,), f32, dev),
+                              _at(dbias, "dbias", (N,), f32, dev), add, R, N, dt, pw, have, _raw_stream(dev))
+    if rc:
+        check(rc, "layernorm_bwd")
     return dx, dscale, dbias
 
 

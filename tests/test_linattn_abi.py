@@ -136,7 +136,7 @@ def test_layernorm_refusals(lib):
     assert fwd(q) == c.SS_ERR_ALIGN
     need = lib.layernorm_bwd_workspace_size(100, 768)
     assert need > 0 and lib.layernorm_bwd_workspace_size(100, 770) == 0
-    bwd = lambda p=P, R=100, N=768, dt=c.SS_BF16, ws=WS, wsz=need: lib.layernorm_bwd(*p[:8], R, N, dt, ws, wsz, None)
+    bwd = lambda p=P, R=100, N=768, dt=c.SS_BF16, ws=WS, wsz=need: lib.layernorm_bwd(*p[:8], 0, R, N, dt, ws, wsz, None)
     for at in range(8):
         q = list(P)
         q[at] = None
