@@ -368,7 +368,8 @@ int conv1d_causal_step(const void* x, float* conv_state, const float* w, const f
  *          ranges of one wider [B, L, W] array; a multiple of 8, at least the
  *          row's G*K or H*V.
  *   g    : log decays, fp32: [B, L, H], or with g_per_head [H] (one for each
- *          head).  Values below -1000 (-inf: forget all) count as -1000.
+ *          head).  Values below -160 (-inf: forget all) count as -160, whose
+ *          exponential is 0 in fp32.
  *   lengths : [B] int32 on the device, or NULL: tokens t >= lengths[b] neither
  *          decay nor add nor read (their inputs may hold anything; o and all
  *          gradients there are 0); values are clamped to 0 .. L.

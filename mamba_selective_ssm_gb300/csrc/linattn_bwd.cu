@@ -330,7 +330,7 @@ template <int VP>
 struct BwdTc {
   static constexpr int vt = kTC * VP * 2;  // bytes of a tile VP columns wide
   static constexpr int q = 0, k = q + 2 * kPanel, x = k + 2 * kPanel, v = x + 2 * kPanel, d = v + vt, y0 = d + vt, y1 = y0 + vt, dec = y1 + vt;
-  static constexpr int bar = dec + DecTile::bytes, tm = bar + 16, hsum = tm + 8, bytes = hsum + 16;
+  static constexpr int bar = dec + DecTile::bytes, tm = bar + 16, hsum = tm + 8, into = hsum + 16, bytes = into + kTC * 4;
   // in x while it is free: parts of dg
   static constexpr int a = x, b = a + 4 * kTC * 4, rect = b + 4 * kTC * 4, tot = rect + 4 * kTC * 4, thr = tot + 4 * kTC * 4;
   static constexpr int T0 = 0, T1 = 128, T2 = 256, T3 = 384, Pb = 384, dPb = 448, cols = 512;
@@ -361,8 +361,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
   const DecTile dec{sb + L::dec};
   uint64_t* bar = reinterpret_cast<uint64_t*>(raw + L::bar);
   uint32_t* tma = reinterpret_cast<uint32_t*>(raw + L::tm);
+  float* into_block = reinterpret_cast<float*>(raw + L::into);  // scale e^{c_i - c of the end of the block of 32 before}
   float* hsum = reinterpret_cast<float*>(raw + L::hsum);  // dg of a chunk, by quarter of its tokens
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the MMAs' issuing thread: warp 3 has no score to scale (its key tokens come after its query tokens); the decays'
+  // warp: not one of those that sum dg
+  constexpr int kIssue = 96, kScan = 15;
   const int row = (warp & 3) * 32 + lane, cq = warp >> 2;  // tensor-memory lane, quarter of the columns
   long long id = blockIdx.x;
   const int seg = (int)(id % p.nseg);
@@ -415,8 +419,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
     load_tile_tc<16, kBwdThreads>(q + t0 * p.ldq, p.ldq, n, p.K, sb + L::q, tid);
     load_tile_tc<VP / 8, kBwdThreads>(d + t0 * ldo, ldo, n, p.V, sb + L::d, tid);
     load_tile_tc<VP / 8, kBwdThreads>(v + t0 * p.ldv, p.ldv, n, p.V, sb + L::v, tid);
-    if (warp == 0) {
-      gates.scan(lane, [&](int i, Dec e) { dec.put(i, e); });
+    if (warp == kScan) {
+      put_decays(gates, dec, lane);
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < kTC; e += 32) into_block[e + lane] = p.scale * dec_exp(dec.rel(e + lane));
       gates.fetch(p, b, h, (ck - 1) * kTC, len, lane);
     }
   };
@@ -472,7 +479,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
   auto wait0 = [&]() { ok = mbar_wait_bounded(&bar[0], ph0, kWaitLimitNs); ph0 ^= 1; };
   auto wait1 = [&]() { ok = mbar_wait_bounded(&bar[1], ph1, kWaitLimitNs); ph1 ^= 1; };
   if (c0 < cend) {
-    if (warp == 0) gates.fetch(p, b, h, (cend - 1) * kTC, len, lane);
+    if (warp == kScan) gates.fetch(p, b, h, (cend - 1) * kTC, len, lane);
     load_k(cend - 1);
     load_rest(cend - 1);
   }
@@ -496,26 +503,41 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
     fence_proxy_async_smem();
     tc_fence_before_sync();
     __syncthreads();
-    if (tid == 0) {
+    if (tid == kIssue) {
       tc_fence_after_sync();
       const uint32_t id128 = mma_idesc(128, false, false);
-      for (int s = 0; s < ks; ++s) mma_ss(tm + L::T0, desc_rows(sb + L::k, s), desc_rows(sb + L::q, s), id128, s > 0);
-      for (int s = 0; s < vs; ++s) mma_ss(tm + L::T1, desc_rows(sb + L::v, s), desc_rows(sb + L::d, s), id128, s > 0);
+      mma_steps(tm + L::T0, Rows{sb + L::k}, Rows{sb + L::q}, id128, ks, false);
+      mma_steps(tm + L::T1, Rows{sb + L::v}, Rows{sb + L::d}, id128, vs, false);
       mma_commit(&bar[0]);
-      for (int t = 2; t >= 0; --t)
-        for (int s = 0; s < vs; ++s)
-          mma_ss(tm + L::T2, desc_rows(sb + L::d, s), desc_rows(sb + (t == 0 ? L::y0 : t == 1 ? L::y1 : L::x), s), id128, t < 2 || s > 0);
+#pragma unroll
+      for (int t = 2; t >= 0; --t)  // the smallest term first
+        mma_steps(tm + L::T2, Rows{sb + L::d}, Rows{sb + (t == 0 ? L::y0 : t == 1 ? L::y1 : L::x)}, id128, vs, t < 2);
       mma_commit(&bar[1]);
     }
     const Dec last = dec.get(kTC - 1), own = dec.get(row);
-    const float elast = dec_exp(last.hi, last.lo), into = p.scale * dec_exp(own.hi, own.lo);
-    const float rest = dec_diff(last.hi, last.lo, own.hi, own.lo);
+    const float elast = dec_exp(last), into = p.scale * dec_exp(own), rest = dec_exp(dec_sub(last, own));
+    if (ck > c0) {  // the chunk before it towards L2
+      const long long n0 = t0 - kTC;
+      const int half = tid >> 8, lt = tid & 255;
+      const float* c = ckpt + (bh * p.nck + ck - 1) * kv;
+      if (half) {
+        prefetch_rows(q + n0 * p.ldq, p.ldq, kTC, p.K, lt);
+        prefetch_rows(k + n0 * p.ldk, p.ldk, kTC, p.K, lt);
+      } else {
+        prefetch_rows(v + n0 * p.ldv, p.ldv, kTC, p.V, lt);
+        prefetch_rows(d + n0 * ldo, ldo, kTC, p.V, lt);
+      }
+      if (tid * 32 < kv) prefetch_l2(c + tid * 32);
+    }
     wait0();
     if (__syncthreads_or(!ok)) break;
     tc_fence_after_sync();
     float rect = 0.f, tot = 0.f;
-    if (cq * 32 + 31 >= (row & ~31)) {  // some query token of this quarter is at or after this warp's key tokens
+    if (cq >= (warp & 3)) {  // query tokens of this quarter at or after this warp's key tokens
       float m[32];
+      const bool diag = cq == (warp & 3);
+      const float from = diag ? 0.f : dec_exp(dec_sub(dec.base(cq), own));  // off the diagonal a decay is a product of two
+      const Dec orel = dec.rel(row);
 #pragma unroll
       for (int g = 1; g >= 0; --g) {
         const int i0 = cq * 32 + g * 16;
@@ -523,21 +545,36 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
         tmem_ld16(tl + L::T0 + i0, s);
         tmem_ld16(tl + L::T1 + i0, t);
         tmem_wait_ld();
+        if (!diag) {
 #pragma unroll
-        for (int e = 14; e >= 0; e -= 2) {
-          const int i = i0 + e;
-          Dec a, c;
-          dec.get2(i, a, c);
-          const float w0 = i >= row ? p.scale * dec_diff(a.hi, a.lo, own.hi, own.lo) : 0.f;
-          const float w1 = i + 1 >= row ? p.scale * dec_diff(c.hi, c.lo, own.hi, own.lo) : 0.f;
-          const float d0 = __uint_as_float(t[e]), d1 = __uint_as_float(t[e + 1]);
-          const float p0 = i >= row ? __uint_as_float(s[e]) * w0 : 0.f, p1 = i + 1 >= row ? __uint_as_float(s[e + 1]) * w1 : 0.f;
-          w[e / 2] = pack_bf16(p0, p1);
-          z[e / 2] = pack_bf16(i >= row ? d0 * w0 : 0.f, i + 1 >= row ? d1 * w1 : 0.f);
-          tot += i + 1 >= row ? p1 * d1 : 0.f;  // paths from j to this query token or a later one of the quarter
-          m[g * 16 + e + 1] = i + 1 > row ? tot : 0.f;
-          tot += i >= row ? p0 * d0 : 0.f;
-          m[g * 16 + e] = i > row ? tot : 0.f;
+          for (int e = 14; e >= 0; e -= 2) {
+            const float2 f = *reinterpret_cast<const float2*>(into_block + i0 + e);
+            const float w0 = f.x * from, w1 = f.y * from;
+            const float d0 = __uint_as_float(t[e]), d1 = __uint_as_float(t[e + 1]);
+            const float p0 = __uint_as_float(s[e]) * w0, p1 = __uint_as_float(s[e + 1]) * w1;
+            w[e / 2] = pack_bf16(p0, p1);
+            z[e / 2] = pack_bf16(d0 * w0, d1 * w1);
+            tot = fmaf(p1, d1, tot);  // paths from j to this query token or a later one of the quarter
+            m[g * 16 + e + 1] = tot;
+            tot = fmaf(p0, d0, tot);
+            m[g * 16 + e] = tot;
+          }
+        } else {
+#pragma unroll
+          for (int e = 14; e >= 0; e -= 2) {
+            const int i = g * 16 + e;
+            const Dec a = dec.rel(i0 + e), c = dec.rel(i0 + e + 1);
+            const float w0 = i >= lane ? p.scale * dec_diff(a.hi, a.lo, orel.hi, orel.lo) : 0.f;
+            const float w1 = i + 1 >= lane ? p.scale * dec_diff(c.hi, c.lo, orel.hi, orel.lo) : 0.f;
+            const float d0 = i >= lane ? __uint_as_float(t[e]) : 0.f, d1 = i + 1 >= lane ? __uint_as_float(t[e + 1]) : 0.f;
+            const float p0 = i >= lane ? __uint_as_float(s[e]) * w0 : 0.f, p1 = i + 1 >= lane ? __uint_as_float(s[e + 1]) * w1 : 0.f;
+            w[e / 2] = pack_bf16(p0, p1);
+            z[e / 2] = pack_bf16(d0 * w0, d1 * w1);
+            tot = fmaf(p1, d1, tot);
+            m[i + 1] = i + 1 > lane ? tot : 0.f;
+            tot = fmaf(p0, d0, tot);
+            m[i] = i > lane ? tot : 0.f;
+          }
         }
         tmem_st8u(tl + L::Pb + i0 / 2, w);
         tmem_st8u(tl + L::dPb + i0 / 2, z);
@@ -577,13 +614,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
     fence_proxy_async_smem();
     tc_fence_before_sync();
     __syncthreads();
-    if (tid == 0) {
+    if (tid == kIssue) {
       tc_fence_after_sync();
-      const uint32_t id128 = mma_idesc(128, false, false);
-      for (int s = 0; s < ks; ++s) mma_ss(tm + L::T0, desc_rows(sb + L::k, s), desc_cols(sb + L::y0, s), mma_idesc(VP, false, true), s > 0);
+      mma_steps(tm + L::T0, Rows{sb + L::k}, Cols{sb + L::y0}, mma_idesc(VP, false, true), ks, false);
+#pragma unroll
       for (int t = 2; t >= 0; --t)
-        for (int s = 0; s < vs; ++s)
-          mma_ss(tm + L::T1, desc_rows(sb + L::v, s), desc_rows(sb + (t == 0 ? L::y0 : t == 1 ? L::y1 : L::x), s), id128, t < 2 || s > 0);
+        mma_steps(tm + L::T1, Rows{sb + L::v}, Rows{sb + (t == 0 ? L::y0 : t == 1 ? L::y1 : L::x)}, mma_idesc(128, false, false), vs, t < 2);
       mma_commit(&bar[0]);
     }
     wait0();
@@ -632,22 +668,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
     fence_proxy_async_smem();
     tc_fence_before_sync();
     __syncthreads();
-    if (tid == 0) {
+    if (tid == kIssue) {
       tc_fence_after_sync();
+#pragma unroll
       for (int s = 0; s < kTC / 16; ++s) mma_ts(tm + L::T0, tm + L::Pb + s * 8, desc_cols(sb + L::d, s), mma_idesc(VP, false, true), true);
+#pragma unroll
       for (int s = 0; s < kTC / 16; ++s) mma_ts(tm + L::T1, tm + L::dPb + s * 8, desc_cols(sb + L::q, s), mma_idesc(128, false, true), true);
-      for (int s = 0; s < kTC / 16; ++s)
-        mma_ss(tm + L::T2, desc_cols(sb + L::x, s), desc_cols(sb + L::k, s), mma_idesc(128, true, true), true);
+      mma_steps(tm + L::T2, Cols{sb + L::x}, Cols{sb + L::k}, mma_idesc(128, true, true), kTC / 16, true);
       mma_commit(&bar[1]);
     }
     wait1();
     if (__syncthreads_or(!ok)) break;
     tc_fence_after_sync();
-    if (tid == 0) {  // into the scores' place, whose readers are done
+    if (tid == kIssue) {  // into the scores' place, whose readers are done
+#pragma unroll
       for (int t = 2; t >= 0; --t)
-        for (int s = 0; s < kTC / 16; ++s)
-          mma_ss(tm + L::T3, desc_cols(sb + L::q, s), desc_cols(sb + (t == 0 ? L::y0 : t == 1 ? L::y1 : L::v), s), mma_idesc(VP, true, true),
-                 t < 2 || s > 0);
+        mma_steps(tm + L::T3, Cols{sb + L::q}, Cols{sb + (t == 0 ? L::y0 : t == 1 ? L::y1 : L::v)}, mma_idesc(VP, true, true), kTC / 16, t < 2);
       mma_commit(&bar[0]);
     }
     // dq, dk, dv: typed through the tiles of k, x and do, whose products are done; fp32 parts as they are

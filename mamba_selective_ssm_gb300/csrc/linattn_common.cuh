@@ -56,9 +56,9 @@ __device__ __forceinline__ Dec dec_add(Dec a, Dec b) {
   r.lo = __fsub_rn(e, __fsub_rn(r.hi, s));
   return r;
 }
-// Log decays below this empty the state in fp32 anyway (e^-1000 = 0); the clamp
+// Log decays below this empty the state in fp32 anyway (e^-160 = 0); the clamp
 // keeps -inf, a reset, from making c_i - c_j = -inf + inf.
-constexpr float kMinLogDecay = -1000.0f;
+constexpr float kMinLogDecay = -160.0f;
 __device__ __forceinline__ Dec dec_of_log(float g) {  // g log2(e)
   constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f;
   if (g < kMinLogDecay) g = kMinLogDecay;
@@ -89,27 +89,50 @@ struct ChunkGates {
       g[e] = t >= 0 && t < len ? p.gate(b, t, h) : 0.0f;
     }
   }
-  template <typename Put>
-  __device__ __forceinline__ void scan(int lane, Put put) const {
-    Dec x[PER];
+  // Running sums within groups of `lanes` lanes: x[e] becomes that of the lane's own tokens, `before` that of the
+  // group's lanes before it, the result that through the lane's last token.
+  __device__ __forceinline__ Dec sums(int lane, int lanes, Dec (&x)[PER], Dec& before) const {
     x[0] = dec_of_log(g[0]);
 #pragma unroll
     for (int e = 1; e < PER; ++e) x[e] = dec_add(x[e - 1], dec_of_log(g[e]));
     Dec incl = x[PER - 1];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+    for (int o = 1; o < lanes; o <<= 1) {
       Dec u;
       u.hi = __shfl_up_sync(0xffffffffu, incl.hi, o);
       u.lo = __shfl_up_sync(0xffffffffu, incl.lo, o);
       const Dec s = dec_add(incl, u);
-      if (lane >= o) incl = s;
+      if ((lane & (lanes - 1)) >= o) incl = s;
     }
-    Dec base;
-    base.hi = __shfl_up_sync(0xffffffffu, incl.hi, 1);
-    base.lo = __shfl_up_sync(0xffffffffu, incl.lo, 1);
-    if (lane == 0) base.hi = base.lo = 0.0f;
+    before.hi = __shfl_up_sync(0xffffffffu, incl.hi, 1);
+    before.lo = __shfl_up_sync(0xffffffffu, incl.lo, 1);
+    if ((lane & (lanes - 1)) == 0) before.hi = before.lo = 0.0f;
+    return incl;
+  }
+  template <typename Put>
+  __device__ __forceinline__ void scan(int lane, Put put) const {
+    Dec x[PER], before;
+    sums(lane, 32, x, before);
 #pragma unroll
-    for (int e = 0; e < PER; ++e) put(lane * PER + e, dec_add(base, x[e]));
+    for (int e = 0; e < PER; ++e) put(lane * PER + e, dec_add(before, x[e]));
+  }
+  // Running sums within blocks of 32 tokens, put(i, r_i), and the sum before each block, put_base(n, c).
+  template <typename Put, typename Base>
+  __device__ __forceinline__ void scan_rel(int lane, Put put, Base put_base) const {
+    constexpr int LB = 32 / PER;  // lanes of a block
+    Dec x[PER], before;
+    const Dec incl = sums(lane, LB, x, before);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) put(lane * PER + e, dec_add(before, x[e]));
+    Dec base = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < 32 / LB; ++n) {
+      if (lane == 0) put_base(n, base);
+      Dec u;
+      u.hi = __shfl_sync(0xffffffffu, incl.hi, n * LB + LB - 1);
+      u.lo = __shfl_sync(0xffffffffu, incl.lo, n * LB + LB - 1);
+      base = dec_add(base, u);
+    }
   }
 };
 

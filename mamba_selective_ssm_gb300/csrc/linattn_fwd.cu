@@ -169,6 +169,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_fwd_tc_kernel(LinAttn p
   uint64_t* bar = reinterpret_cast<uint64_t*>(raw + L::bar);
   uint32_t* tma = reinterpret_cast<uint32_t*>(raw + L::tm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kIssue = 128;  // the MMAs' issuing thread: warp 4 has no score to scale (its tokens come before its key tokens)
   const int row = (warp & 3) * 32 + lane, half = warp >> 2;  // tensor-memory lane and half of the columns of this thread
   const int nvt = (p.V + kVT - 1) / kVT;
   long long id = blockIdx.x;
@@ -217,6 +218,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_fwd_tc_kernel(LinAttn p
       sts16(sb + L::s + tile_at(row, half * 4 + u), make_uint4(pack_bf16(S[8 * u], S[8 * u + 1]), pack_bf16(S[8 * u + 2], S[8 * u + 3]),
                                                              pack_bf16(S[8 * u + 4], S[8 * u + 5]), pack_bf16(S[8 * u + 6], S[8 * u + 7])));
   };
+  const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
+  int cend = (len + kTC - 1) / kTC;  // chunks that hold a token
+  cend = cend < c0 ? c0 : cend < c1 ? cend : c1;
   auto valid_of = [&](int ck) { const int n = len - ck * kTC; return n < 0 ? 0 : n < kTC ? n : kTC; };
   ChunkGates<kTC> gates;
   auto load = [&](int ck) {
@@ -226,13 +230,16 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_fwd_tc_kernel(LinAttn p
     load_tile_tc<16, kTcThreads>(k + t0 * p.ldk, p.ldk, n, p.K, sb + L::k, tid);
     load_tile_tc<8, kTcThreads>(v + t0 * p.ldv, p.ldv, n, vw, sb + L::v, tid);
     if (warp == 0) {
-      gates.scan(lane, [&](int i, Dec d) { dec.put(i, d); });
+      put_decays(gates, dec, lane);
       gates.fetch(p, b, h, (ck + 1) * kTC, len, lane);
     }
+    if (ck + 1 < cend) {  // the chunk after it towards L2
+      const int left = len - (ck + 1) * kTC;
+      prefetch_rows(q + (t0 + kTC) * p.ldq, p.ldq, left, p.K, tid);
+      prefetch_rows(k + (t0 + kTC) * p.ldk, p.ldk, left, p.K, tid);
+      if (!(tid & 1)) prefetch_rows(v + (t0 + kTC) * p.ldv, p.ldv, left, vw, tid);
+    }
   };
-  const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
-  int cend = (len + kTC - 1) / kTC;  // chunks that hold a token
-  cend = cend < c0 ? c0 : cend < c1 ? cend : c1;
   uint32_t phase = 0;
   bool ok = true;
   if (c0 < cend) {
@@ -246,18 +253,18 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_fwd_tc_kernel(LinAttn p
     fence_proxy_async_smem();
     tc_fence_before_sync();
     __syncthreads();
-    if (tid == 0) {
+    if (tid == kIssue) {
       tc_fence_after_sync();
-      for (int s = 0; s < ks; ++s) mma_ss(tm + L::P, desc_rows(sb + L::q, s), desc_rows(sb + L::k, s), mma_idesc(kTC, false, false), s > 0);
-      for (int s = 0; s < ks; ++s) mma_ss(tm + L::Oi, desc_rows(sb + L::q, s), desc_cols(sb + L::s, s), mma_idesc(kVT, false, true), s > 0);
+      mma_steps(tm + L::P, Rows{sb + L::q}, Rows{sb + L::k}, mma_idesc(kTC, false, false), ks, false);
+      mma_steps(tm + L::Oi, Rows{sb + L::q}, Cols{sb + L::s}, mma_idesc(kVT, false, true), ks, false);
       mma_commit(bar);
     }
     const Dec last = dec.get(kTC - 1), own = dec.get(row);
-    const float elast = dec_exp(last.hi, last.lo);
+    const float elast = dec_exp(last);
     // w v: row tid / 2, half of the columns; the first term has a tile of its own, the others take q's
     const int vr = tid >> 1, vh = (tid & 1) * 4;
     const Dec dr = dec.get(vr);
-    const float wj = dec_diff(last.hi, last.lo, dr.hi, dr.lo);
+    const float wj = dec_exp(dec_sub(last, dr));
     auto wv = [&](int u, float (&x)[8]) {
       const uint4 a = lds16(sb + L::v + tile_at(vr, vh + u));
       Raw8<__nv_bfloat16>::wide(a, x);
@@ -275,25 +282,36 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_fwd_tc_kernel(LinAttn p
     if (__syncthreads_or(!ok)) break;
     tc_fence_after_sync();
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {  // 32 scores at a time
-      const int j0 = half * 64 + g * 32;
-      uint32_t r[32], w[16];
-      if (j0 <= (row | 31)) {
-        tmem_ld32(tl + L::P + j0, r);
+    for (int g = 0; g < 2; ++g) {  // 32 key tokens at a time: all before this warp's tokens, among them, or after them
+      const int jb = half * 2 + g;
+      uint32_t w[16];
+      if (jb <= (warp & 3)) {
+        uint32_t r[32];
+        tmem_ld32(tl + L::P + jb * 32, r);
+        const Dec d = dec_sub(own, dec.base(jb));
+        const float x = d.hi + d.lo;
         tmem_wait_ld();
+        if (jb < (warp & 3)) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const int j = j0 + e;
-          Dec a, c;
-          dec.get2(j, a, c);
-          const float d0 = dec_diff(own.hi, own.lo, a.hi, a.lo), d1 = dec_diff(own.hi, own.lo, c.hi, c.lo);
-          w[e / 2] = pack_bf16(j <= row ? __uint_as_float(r[e]) * d0 : 0.f, j + 1 <= row ? __uint_as_float(r[e + 1]) * d1 : 0.f);
+          for (int e = 0; e < 32; e += 4) {
+            const float4 c = dec.r4(jb * 32 + e);
+            w[e / 2] = pack_bf16(__uint_as_float(r[e]) * ex2(x - c.x), __uint_as_float(r[e + 1]) * ex2(x - c.y));
+            w[e / 2 + 1] = pack_bf16(__uint_as_float(r[e + 2]) * ex2(x - c.z), __uint_as_float(r[e + 3]) * ex2(x - c.w));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 c = dec.r4(jb * 32 + e);
+            w[e / 2] = pack_bf16(e <= lane ? __uint_as_float(r[e]) * ex2(x - c.x) : 0.f, e + 1 <= lane ? __uint_as_float(r[e + 1]) * ex2(x - c.y) : 0.f);
+            w[e / 2 + 1] = pack_bf16(e + 2 <= lane ? __uint_as_float(r[e + 2]) * ex2(x - c.z) : 0.f,
+                                     e + 3 <= lane ? __uint_as_float(r[e + 3]) * ex2(x - c.w) : 0.f);
+          }
         }
       } else {
 #pragma unroll
         for (int e = 0; e < 16; ++e) w[e] = 0u;
       }
-      tmem_st16(tl + L::Pb + j0 / 2, w);
+      tmem_st16(tl + L::Pb + jb * 16, w);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -307,17 +325,17 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_fwd_tc_kernel(LinAttn p
     tmem_wait_st();
     tc_fence_before_sync();
     __syncthreads();
-    if (tid == 0) {
+    if (tid == kIssue) {
       tc_fence_after_sync();
+#pragma unroll
       for (int s = 0; s < kTC / 16; ++s) mma_ts(tm + L::Oa, tm + L::Pb + s * 8, desc_cols(sb + L::v, s), mma_idesc(kVT, false, true), s > 0);
-      for (int t = 2; t >= 0; --t) {  // the smallest term first
-        const uint32_t w = sb + (t == 0 ? L::w : L::q + (t - 1) * kPanel);
-        for (int s = 0; s < kTC / 16; ++s)
-          mma_ss(tm + L::Sn, desc_cols(sb + L::k, s), desc_cols(w, s), mma_idesc(kVT, true, true), t < 2 || s > 0);
-      }
+#pragma unroll
+      for (int t = 2; t >= 0; --t)  // the smallest term first
+        mma_steps(tm + L::Sn, Cols{sb + L::k}, Cols{sb + (t == 0 ? L::w : L::q + (t - 1) * kPanel)}, mma_idesc(kVT, true, true), kTC / 16,
+                  t < 2);
       mma_commit(bar);
     }
-    const float ei = p.scale * dec_exp(own.hi, own.lo);
+    const float ei = p.scale * dec_exp(own);
     if (ckpt != nullptr && row < p.K) {
       float4* dst = reinterpret_cast<float4*>(ckpt + (bh * p.nck + ck) * p.K * p.V) + row;
 #pragma unroll

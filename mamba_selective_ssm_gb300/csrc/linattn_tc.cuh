@@ -22,47 +22,77 @@ __device__ __forceinline__ uint32_t tile_at(int r, int u) {
   return (uint32_t)((u >> 3) * kPanel + r * 128 + (((u & 7) ^ (r & 7)) << 4));
 }
 
-// The decays of a chunk in shared memory: hi as floats, lo as bf16 (it only has
-// to bring 8 more bits), so that two CTAs' tiles fit an SM.
+// The decays of a chunk in shared memory, each token's c_i relative to the end of
+// the 32 tokens before its own 32 (base): r_i = c_i - base as a float and, in
+// bf16, what that leaves.  Against tokens of one block of 32 a score's decay is
+// 2^(x - r_j) with x = c_i - base taken once, good to 2^-24 |r_j|.
 struct DecTile {
-  static constexpr int bytes = kTC * 6;
-  uint32_t base;
-  __device__ __forceinline__ void put(int i, Dec d) const {
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + 4 * i), "f"(d.hi) : "memory");
-    const __nv_bfloat16 l = __float2bfloat16_rn(d.lo);
-    asm volatile("st.shared.b16 [%0], %1;" ::"r"(base + 4 * kTC + 2 * i), "h"(*reinterpret_cast<const uint16_t*>(&l)) : "memory");
+  static constexpr int bytes = kTC * 6 + 32;
+  uint32_t at;
+  __device__ __forceinline__ static float ldf(uint32_t a) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(a));
+    return x;
   }
-  __device__ __forceinline__ Dec get(int i) const {
+  // one warp; incl: the running sum through this lane's four tokens, x[e] that of its own first tokens
+  __device__ __forceinline__ void put(int i, Dec r) const {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 4 * i), "f"(r.hi) : "memory");
+    const __nv_bfloat16 l = __float2bfloat16_rn(r.lo);
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 4 * kTC + 2 * i), "h"(*reinterpret_cast<const uint16_t*>(&l)) : "memory");
+  }
+  __device__ __forceinline__ void put_base(int n, Dec b) const {
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at + 6 * kTC + 8 * n), "f"(b.hi), "f"(b.lo) : "memory");
+  }
+  __device__ __forceinline__ Dec base(int n) const {
+    Dec b;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(b.hi), "=f"(b.lo) : "r"(at + 6 * kTC + 8 * n));
+    return b;
+  }
+  __device__ __forceinline__ Dec rel(int i) const {
     Dec d;
     uint16_t l;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(d.hi) : "r"(base + 4 * i));
-    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(l) : "r"(base + 4 * kTC + 2 * i));
+    d.hi = ldf(at + 4 * i);
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(l) : "r"(at + 4 * kTC + 2 * i));
     d.lo = __uint_as_float((uint32_t)l << 16);
     return d;
   }
-  // tokens j, j + 1 (j even)
-  __device__ __forceinline__ void get2(int j, Dec& a, Dec& b) const {
-    uint32_t l;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(a.hi), "=f"(b.hi) : "r"(base + 4 * j));
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(l) : "r"(base + 4 * kTC + 2 * j));
-    a.lo = __uint_as_float(l << 16);
-    b.lo = __uint_as_float(l & 0xffff0000u);
+  __device__ __forceinline__ Dec get(int i) const { return dec_add(base(i >> 5), rel(i)); }
+  // r of tokens j .. j + 3 (j a multiple of 4)
+  __device__ __forceinline__ float4 r4(int j) const {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at + 4 * j));
+    return v;
   }
 };
+__device__ __forceinline__ Dec dec_sub(Dec a, Dec b) { return dec_add(a, Dec{-b.hi, -b.lo}); }
+__device__ __forceinline__ float dec_exp(Dec d) { return dec_exp(d.hi, d.lo); }
+
+// A chunk's decays into shared memory (one warp).
+__device__ __forceinline__ void put_decays(const ChunkGates<kTC>& g, const DecTile& t, int lane) {
+  g.scan_rel(lane, [&](int i, Dec r) { t.put(i, r); }, [&](int n, Dec b) { t.put_base(n, b); });
+}
+
+// One 128-byte line into L2, ahead of the loads that will want it.
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+// kTC rows of `width` bf16 (at most 128: two lines and an odd start) from row t0: a lane per row and line
+__device__ __forceinline__ void prefetch_rows(const __nv_bfloat16* src, long long ld, int valid, int width, int tid) {
+  const int r = tid >> 1, c = (tid & 1) * 64;
+  if (r < valid && c < width) prefetch_l2(src + (long long)r * ld + c);
+}
 
 // ---------------------------------------------------------------- descriptors
 // Shared-memory operand descriptor: start address, leading and stride byte
-// offsets (all in 16-byte units), version 1, 128-byte swizzle.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)((lbo >> 4) & 0x3fff) << 16) | ((uint64_t)((sbo >> 4) & 0x3fff) << 32) |
-         (1ull << 46) | (2ull << 61);
-}
+// offsets (all in 16-byte units), version 1, 128-byte swizzle; 8-row groups are
+// 1024 bytes apart.  Only the low word changes from step to step of a product.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t lo) { return ((uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32) | lo; }
 // contraction along the columns; step s takes columns 16 s .. 16 s + 15
 __device__ __forceinline__ uint64_t desc_rows(uint32_t tile, int s) {
-  return smem_desc(tile + (s >> 2) * kPanel + (s & 3) * 32, 16, 1024);
+  return smem_desc((tile >> 4) + (s >> 2) * (kPanel >> 4) + (s & 3) * 2 + (1u << 16));
 }
 // contraction down the rows; step s takes rows 16 s .. 16 s + 15; 64-column panels kPanel apart
-__device__ __forceinline__ uint64_t desc_cols(uint32_t tile, int s) { return smem_desc(tile + s * 2048, kPanel, 1024); }
+__device__ __forceinline__ uint64_t desc_cols(uint32_t tile, int s) {
+  return smem_desc((tile >> 4) + s * 128 + ((uint32_t)(kPanel >> 4) << 16));
+}
 
 // bf16 x bf16 -> fp32, M = 128; a_cols / b_cols: that operand's contraction runs down its rows
 __device__ __forceinline__ uint32_t mma_idesc(int n, bool a_cols, bool b_cols) {
@@ -86,6 +116,22 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
+// A product of n steps of 16 (n <= 8), unrolled, so that a step costs its issuing thread a few instructions:
+// the operands' descriptors as functions of the step
+template <typename A, typename B>
+__device__ __forceinline__ void mma_steps(uint32_t d, A a, B b, uint32_t idesc, int n, bool add) {
+#pragma unroll
+  for (int s = 0; s < 8; ++s)
+    if (s < n) mma_ss(d, a(s), b(s), idesc, add || s > 0);
+}
+struct Rows {  // an operand whose contraction runs along the tile's columns
+  uint32_t tile;
+  __device__ __forceinline__ uint64_t operator()(int s) const { return desc_rows(tile, s); }
+};
+struct Cols {  // ... down its rows
+  uint32_t tile;
+  __device__ __forceinline__ uint64_t operator()(int s) const { return desc_cols(tile, s); }
+};
 // the barrier completes when all MMAs issued before are done
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -267,8 +313,14 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_sum_tc_kernel(LinAttn p
     load_tile_tc<16, kTcThreads>(xs + t0 * ldx, ldx, n, p.K, sb + L::x, tid);
     load_tile_tc<8, kTcThreads>(ys + t0 * ldy, ldy, n, vw, sb + L::y, tid);
     if (warp == 0) {
-      gates.scan(lane, [&](int i, Dec d) { dec.put(i, d); });
+      put_decays(gates, dec, lane);
       gates.fetch(p, b, h, (REV ? ck - 1 : ck + 1) * kTC, len, lane);
+    }
+    const int nx = REV ? ck - 1 : ck + 1;  // the chunk after it
+    if (nx >= c0 && nx < cend) {
+      const int left = len - nx * kTC;
+      prefetch_rows(xs + (long long)nx * kTC * ldx, ldx, left, p.K, tid);
+      if (!(tid & 1)) prefetch_rows(ys + (long long)nx * kTC * ldy, ldy, left, vw, tid);
     }
   };
   Dec total = {0.f, 0.f};
@@ -283,11 +335,11 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_sum_tc_kernel(LinAttn p
     cp_wait_all();
     __syncthreads();
     const Dec last = dec.get(kTC - 1);
-    const float elast = dec_exp(last.hi, last.lo);
+    const float elast = dec_exp(last);
     total = dec_add(total, last);
     const int r = tid >> 1, u0 = (tid & 1) * 4;
     const Dec dr = dec.get(r);
-    const float w = REV ? p.scale * dec_exp(dr.hi, dr.lo) : dec_diff(last.hi, last.lo, dr.hi, dr.lo);
+    const float w = REV ? p.scale * dec_exp(dr) : dec_exp(dec_sub(last, dr));
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const uint32_t at = tile_at(r, u0 + u);
@@ -304,9 +356,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_sum_tc_kernel(LinAttn p
     __syncthreads();
     if (tid == 0) {
       tc_fence_after_sync();
-      for (int t = 2; t >= 0; --t)
-        for (int s = 0; s < kTC / 16; ++s)
-          mma_ss(tm, desc_cols(sb + L::x, s), desc_cols(sb + L::w + t * kPanel, s), mma_idesc(64, true, true), t < 2 || s > 0);
+#pragma unroll
+      for (int t = 2; t >= 0; --t)  // the smallest term first
+        mma_steps(tm, Cols{sb + L::x}, Cols{sb + L::w + t * kPanel}, mma_idesc(64, true, true), kTC / 16, t < 2);
       mma_commit(bar);
     }
     ok = mbar_wait_bounded(bar, phase, kWaitLimitNs);
