@@ -151,17 +151,31 @@ __global__ void __launch_bounds__(256) linattn_fwd_kernel(LinAttn p, const float
 //   Oa  = P v
 //   Sn  = k^T (w v),  w_j = e^{c_last - c_j}: w v as three bf16 terms, an fp32-exact product
 // A term of o is rounded to bf16 once on its way (as a score or as a state).
+//
+// Eight warps compute; a ninth issues: the TMA loads, the MMAs (whose issue
+// blocks while the tensor cores are behind) and the decays of the next chunk.
+// They meet at mbarriers only, so a warp waits for what it needs and not for the
+// CTA.  Two CTAs share an SM and fill each other's waits.
 struct FwdTc {
-  // shared memory: tiles, decays, barrier, tensor-memory address; two CTAs fit an SM
+  // shared memory: tiles, decays, barriers, tensor-memory address; two CTAs fit an SM
   static constexpr int q = 0, k = q + 2 * kPanel, v = k + 2 * kPanel, s = v + kPanel, w = s + kPanel, dec = w + kPanel;
-  static constexpr int bar = dec + DecTile::bytes, tm = bar + 8, bytes = tm + 8;
+  static constexpr int bar = dec + DecTile::bytes, tm = bar + 5 * 8, bytes = tm + 8;
+  static_assert(2 * (bytes + 1024) <= 228 * 1024, "two CTAs an SM");
+  // barriers: chunk landed; state tile stored (and accumulators read); scores stored; first and second products done
+  static constexpr int kLd = 0, kSt = 1, kSc = 2, kM0 = 3, kM1 = 4;
   // tensor memory columns
   static constexpr int P = 0, Oa = 0, Sn = 64, Pb = 128, Oi = 192, cols = 256;
+  static constexpr int warps = 8, threads = 32 * (warps + 1);
+  static constexpr uint32_t tx = 5 * kPanel;
 };
 
-__global__ void __launch_bounds__(kTcThreads, 2) linattn_fwd_tc_kernel(LinAttn p, const float* __restrict__ s0,
-                                                                      __nv_bfloat16* __restrict__ o, float* __restrict__ ckpt,
-                                                                      float* __restrict__ send) {
+struct FwdMaps {
+  CUtensorMap q, k, v;
+};
+
+__global__ void __launch_bounds__(FwdTc::threads, 2) linattn_fwd_tc_kernel(LinAttn p, const __grid_constant__ FwdMaps maps,
+                                                                           const float* __restrict__ s0, __nv_bfloat16* __restrict__ o,
+                                                                           float* __restrict__ ckpt, float* __restrict__ send) {
   using L = FwdTc;
   extern __shared__ __align__(1024) unsigned char raw[];
   const uint32_t sb = smem_u32(raw);
@@ -169,8 +183,6 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_fwd_tc_kernel(LinAttn p
   uint64_t* bar = reinterpret_cast<uint64_t*>(raw + L::bar);
   uint32_t* tma = reinterpret_cast<uint32_t*>(raw + L::tm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kIssue = 128;  // the MMAs' issuing thread: warp 4 has no score to scale (its tokens come before its key tokens)
-  const int row = (warp & 3) * 32 + lane, half = warp >> 2;  // tensor-memory lane and half of the columns of this thread
   const int nvt = (p.V + kVT - 1) / kVT;
   long long id = blockIdx.x;
   const int seg = (int)(id % p.nseg);
@@ -181,12 +193,16 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_fwd_tc_kernel(LinAttn p
   const int gh = h / (p.H / p.G), v0 = vt * kVT, vw = p.V - v0 < kVT ? p.V - v0 : kVT;
   const int len = p.len(b);
   const long long bh = (long long)b * p.H + h;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (long long)b * p.L * p.ldq + (long long)gh * p.K;
-  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.k) + (long long)b * p.L * p.ldk + (long long)gh * p.K;
-  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + (long long)b * p.L * p.ldv + (long long)h * p.V + v0;
+  const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
+  int cend = (len + kTC - 1) / kTC;  // chunks that hold a token
+  cend = cend < c0 ? c0 : cend < c1 ? cend : c1;
 
   if (tid == 0) {
-    mbar_init(bar, 1);
+    mbar_init(&bar[L::kLd], 1);
+    mbar_init(&bar[L::kSt], L::warps);
+    mbar_init(&bar[L::kSc], L::warps);
+    mbar_init(&bar[L::kM0], 1);
+    mbar_init(&bar[L::kM1], 1);
     fence_barrier_init();
   }
   if (warp == 0) {
@@ -197,200 +213,223 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_fwd_tc_kernel(LinAttn p
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tm = *tma;
-  const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);  // this warp's lanes
-  const int ks = (p.K + 15) / 16;                                 // contraction steps over K
-
-  float S[32];
-#pragma unroll
-  for (int e = 0; e < 32; ++e) S[e] = 0.f;
-  if (s0 != nullptr && row < p.K) {
-    const float* src = s0 + ((p.nseg > 1 ? bh * p.nseg + seg : bh) * p.K + row) * p.V + v0 + half * 32;
-#pragma unroll
-    for (int e = 0; e < 32; e += 4)
-      if (half * 32 + e < vw) {
-        const float4 x = *reinterpret_cast<const float4*>(src + e);
-        S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
-      }
-  }
-  auto store_s = [&]() {  // S_in as a bf16 tile
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      sts16(sb + L::s + tile_at(row, half * 4 + u), make_uint4(pack_bf16(S[8 * u], S[8 * u + 1]), pack_bf16(S[8 * u + 2], S[8 * u + 3]),
-                                                             pack_bf16(S[8 * u + 4], S[8 * u + 5]), pack_bf16(S[8 * u + 6], S[8 * u + 7])));
-  };
-  const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
-  int cend = (len + kTC - 1) / kTC;  // chunks that hold a token
-  cend = cend < c0 ? c0 : cend < c1 ? cend : c1;
-  auto valid_of = [&](int ck) { const int n = len - ck * kTC; return n < 0 ? 0 : n < kTC ? n : kTC; };
-  ChunkGates<kTC> gates;
-  auto load = [&](int ck) {
-    const int n = valid_of(ck);
-    const long long t0 = (long long)ck * kTC;
-    load_tile_tc<16, kTcThreads>(q + t0 * p.ldq, p.ldq, n, p.K, sb + L::q, tid);
-    load_tile_tc<16, kTcThreads>(k + t0 * p.ldk, p.ldk, n, p.K, sb + L::k, tid);
-    load_tile_tc<8, kTcThreads>(v + t0 * p.ldv, p.ldv, n, vw, sb + L::v, tid);
-    if (warp == 0) {
-      put_decays(gates, dec, lane);
-      gates.fetch(p, b, h, (ck + 1) * kTC, len, lane);
-    }
-    if (ck + 1 < cend) {  // the chunk after it towards L2
-      const int left = len - (ck + 1) * kTC;
-      prefetch_rows(q + (t0 + kTC) * p.ldq, p.ldq, left, p.K, tid);
-      prefetch_rows(k + (t0 + kTC) * p.ldk, p.ldk, left, p.K, tid);
-      if (!(tid & 1)) prefetch_rows(v + (t0 + kTC) * p.ldv, p.ldv, left, vw, tid);
-    }
-  };
-  uint32_t phase = 0;
   bool ok = true;
-  if (c0 < cend) {
-    if (warp == 0) gates.fetch(p, b, h, c0 * kTC, len, lane);
-    load(c0);
-    store_s();
-  }
-  for (int ck = c0; ck < cend; ++ck) {
-    const int t0 = ck * kTC, valid = valid_of(ck);
-    cp_wait_all();
-    fence_proxy_async_smem();
-    tc_fence_before_sync();
-    __syncthreads();
-    if (tid == kIssue) {
-      tc_fence_after_sync();
-      mma_steps(tm + L::P, Rows{sb + L::q}, Rows{sb + L::k}, mma_idesc(kTC, false, false), ks, false);
-      mma_steps(tm + L::Oi, Rows{sb + L::q}, Cols{sb + L::s}, mma_idesc(kVT, false, true), ks, false);
-      mma_commit(bar);
-    }
-    const Dec last = dec.get(kTC - 1), own = dec.get(row);
-    const float elast = dec_exp(last);
-    // w v: row tid / 2, half of the columns; the first term has a tile of its own, the others take q's
-    const int vr = tid >> 1, vh = (tid & 1) * 4;
-    const Dec dr = dec.get(vr);
-    const float wj = dec_exp(dec_sub(last, dr));
-    auto wv = [&](int u, float (&x)[8]) {
-      const uint4 a = lds16(sb + L::v + tile_at(vr, vh + u));
-      Raw8<__nv_bfloat16>::wide(a, x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= wj;
+  auto wait = [&](int i, uint32_t par) { return ok = mbar_wait_bounded(&bar[i], par, kWaitLimitNs); };
+
+  if (warp == L::warps) {  // ---- the issuing warp
+    const int ks = (p.K + 15) / 16;  // contraction steps over K
+    ChunkGates<kTC> gates;
+    auto load = [&](int ck) {  // a chunk's decays and tiles; its readers have passed a barrier that this warp has waited for
+      put_decays(gates, dec, lane);
+      __syncwarp();
+      if (lane == 0) {
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(&bar[L::kLd], L::tx);
+        load_panels(sb + L::q, 2, &maps.q, &bar[L::kLd], 0, gh, ck * kTC, b);
+        load_panels(sb + L::k, 2, &maps.k, &bar[L::kLd], 0, gh, ck * kTC, b);
+        load_panels(sb + L::v, 1, &maps.v, &bar[L::kLd], v0, h, ck * kTC, b);
+        if (ck + 1 < cend) {
+          prefetch_panels((p.K + 63) / 64, &maps.q, 0, gh, (ck + 1) * kTC, b);
+          prefetch_panels((p.K + 63) / 64, &maps.k, 0, gh, (ck + 1) * kTC, b);
+          prefetch_panels(1, &maps.v, v0, h, (ck + 1) * kTC, b);
+        }
+      }
+      gates.fetch(p, b, h, (ck + 1) * kTC, len, lane);
     };
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float x[8];
-      wv(u, x);
-      sts16(sb + L::w + tile_at(vr, vh + u), take_term(x));
+    if (c0 < cend) {
+      gates.fetch(p, b, h, c0 * kTC, len, lane);
+      load(c0);
     }
-    ok = mbar_wait_bounded(bar, phase, kWaitLimitNs);
-    phase ^= 1;
-    if (__syncthreads_or(!ok)) break;
-    tc_fence_after_sync();
+    for (int ck = c0; ck < cend; ++ck) {
+      const uint32_t par = (uint32_t)(ck - c0) & 1u;
+      if (!wait(L::kLd, par)) break;
+      const int valid = len - ck * kTC;
+      if (valid < kTC && ck * kTC + valid < p.L) {  // the row ends inside the tensor: what follows is not its own
+        zero_rows(sb + L::q, 5, valid, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (!wait(L::kSt, par)) break;
+      if (lane == 0) {
+        tc_fence_after_sync();
+        mma_steps(tm + L::P, Rows{sb + L::q}, Rows{sb + L::k}, mma_idesc(kTC, false, false), ks, false);
+        mma_steps(tm + L::Oi, Rows{sb + L::q}, Cols{sb + L::s}, mma_idesc(kVT, false, true), ks, false);
+        mma_commit(&bar[L::kM0]);
+      }
+      if (!wait(L::kSc, par)) break;
+      if (lane == 0) {
+        tc_fence_after_sync();
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {  // 32 key tokens at a time: all before this warp's tokens, among them, or after them
-      const int jb = half * 2 + g;
-      uint32_t w[16];
-      if (jb <= (warp & 3)) {
-        uint32_t r[32];
-        tmem_ld32(tl + L::P + jb * 32, r);
-        const Dec d = dec_sub(own, dec.base(jb));
-        const float x = d.hi + d.lo;
-        tmem_wait_ld();
-        if (jb < (warp & 3)) {
+        for (int s = 0; s < kTC / 16; ++s)
+          mma_ts(tm + L::Oa, tm + L::Pb + s * 8, desc_cols(sb + L::v, s), mma_idesc(kVT, false, true), s > 0);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 c = dec.r4(jb * 32 + e);
-            w[e / 2] = pack_bf16(__uint_as_float(r[e]) * ex2(x - c.x), __uint_as_float(r[e + 1]) * ex2(x - c.y));
-            w[e / 2 + 1] = pack_bf16(__uint_as_float(r[e + 2]) * ex2(x - c.z), __uint_as_float(r[e + 3]) * ex2(x - c.w));
+        for (int t = 2; t >= 0; --t)  // the smallest term first
+          mma_steps(tm + L::Sn, Cols{sb + L::k}, Cols{sb + (t == 0 ? L::w : L::q + (t - 1) * kPanel)}, mma_idesc(kVT, true, true),
+                    kTC / 16, t < 2);
+        mma_commit(&bar[L::kM1]);
+      }
+      __syncwarp();
+      if (ck + 1 < cend) {
+        if (!wait(L::kM1, par)) break;
+        load(ck + 1);
+      }
+    }
+  } else {  // ---- a computing warp
+    const int row = (warp & 3) * 32 + lane, half = warp >> 2;  // tensor-memory lane and half of the columns of this thread
+    const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    float S[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) S[e] = 0.f;
+    if (s0 != nullptr && row < p.K) {
+      const float* src = s0 + ((p.nseg > 1 ? bh * p.nseg + seg : bh) * p.K + row) * p.V + v0 + half * 32;
+#pragma unroll
+      for (int e = 0; e < 32; e += 4)
+        if (half * 32 + e < vw) {
+          const float4 x = *reinterpret_cast<const float4*>(src + e);
+          S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
+        }
+    }
+    auto arrive = [&](int i) {  // this warp's shared- and tensor-memory accesses before are over
+      fence_proxy_async_smem();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[i]);
+    };
+    auto store_s = [&]() {  // S_in as a bf16 tile
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float x[8] = {S[8 * u], S[8 * u + 1], S[8 * u + 2], S[8 * u + 3], S[8 * u + 4], S[8 * u + 5], S[8 * u + 6], S[8 * u + 7]};
+        sts16(sb + L::s + tile_at(row, half * 4 + u), pack8(x));
+      }
+    };
+    if (c0 < cend) {
+      store_s();
+      arrive(L::kSt);
+    }
+    for (int ck = c0; ck < cend; ++ck) {
+      const uint32_t par = (uint32_t)(ck - c0) & 1u;
+      const int t0 = ck * kTC, valid = len - t0;
+      if (!wait(L::kLd, par)) break;
+      const Dec last = dec.get(kTC - 1), own = dec.get(row);
+      const float elast = dec_exp(last), wj = dec_exp(dec_sub(last, own));
+      // w v of this thread's token and half of the columns, eight at a time
+      auto wv = [&](int u, float (&x)[8]) {
+        Raw8<__nv_bfloat16>::wide(lds16(sb + L::v + tile_at(row, half * 4 + u)), x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = row < valid ? x[e] * wj : 0.f;
+      };
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {  // the first term has a tile of its own, the others take q's
+        float x[8];
+        wv(u, x);
+        sts16(sb + L::w + tile_at(row, half * 4 + u), take_term(x));
+      }
+      if (!wait(L::kM0, par)) break;
+      tc_fence_after_sync();
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float x[8];
+        wv(u, x);
+        take_term(x);
+        sts16(sb + L::q + tile_at(row, half * 4 + u), take_term(x));
+        sts16(sb + L::q + kPanel + tile_at(row, half * 4 + u), take_term(x));
+      }
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {  // 32 key tokens at a time: all before this warp's tokens, among them, or after them
+        const int jb = half * 2 + g;
+        uint32_t w[16];
+        if (jb <= (warp & 3)) {
+          uint32_t r[32];
+          tmem_ld32(tl + L::P + jb * 32, r);
+          const Dec d = dec_sub(own, dec.base(jb));
+          const float x = d.hi + d.lo;
+          tmem_wait_ld();
+          if (jb < (warp & 3)) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 c = dec.r4(jb * 32 + e);
+              w[e / 2] = pack_bf16(__uint_as_float(r[e]) * ex2(x - c.x), __uint_as_float(r[e + 1]) * ex2(x - c.y));
+              w[e / 2 + 1] = pack_bf16(__uint_as_float(r[e + 2]) * ex2(x - c.z), __uint_as_float(r[e + 3]) * ex2(x - c.w));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 c = dec.r4(jb * 32 + e);
+              w[e / 2] = pack_bf16(e <= lane ? __uint_as_float(r[e]) * ex2(x - c.x) : 0.f,
+                                   e + 1 <= lane ? __uint_as_float(r[e + 1]) * ex2(x - c.y) : 0.f);
+              w[e / 2 + 1] = pack_bf16(e + 2 <= lane ? __uint_as_float(r[e + 2]) * ex2(x - c.z) : 0.f,
+                                       e + 3 <= lane ? __uint_as_float(r[e + 3]) * ex2(x - c.w) : 0.f);
+            }
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 c = dec.r4(jb * 32 + e);
-            w[e / 2] = pack_bf16(e <= lane ? __uint_as_float(r[e]) * ex2(x - c.x) : 0.f, e + 1 <= lane ? __uint_as_float(r[e + 1]) * ex2(x - c.y) : 0.f);
-            w[e / 2 + 1] = pack_bf16(e + 2 <= lane ? __uint_as_float(r[e + 2]) * ex2(x - c.z) : 0.f,
-                                     e + 3 <= lane ? __uint_as_float(r[e + 3]) * ex2(x - c.w) : 0.f);
-          }
+          for (int e = 0; e < 16; ++e) w[e] = 0u;
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = 0u;
+        tmem_st16(tl + L::Pb + jb * 16, w);
       }
-      tmem_st16(tl + L::Pb + jb * 16, w);
-    }
+      tmem_wait_st();
+      arrive(L::kSc);
+      if (ckpt != nullptr && row < p.K) {
+        float4* dst = reinterpret_cast<float4*>(ckpt + (bh * p.nck + ck) * p.K * p.V) + row;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float x[8];
-      wv(u, x);
-      take_term(x);
-      sts16(sb + L::q + tile_at(vr, vh + u), take_term(x));
-      sts16(sb + L::q + kPanel + tile_at(vr, vh + u), take_term(x));
-    }
-    fence_proxy_async_smem();
-    tmem_wait_st();
-    tc_fence_before_sync();
-    __syncthreads();
-    if (tid == kIssue) {
+        for (int e = 0; e < 32; e += 4)
+          if (half * 32 + e < vw) dst[(long long)((v0 + half * 32 + e) / 4) * p.K] = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+      }
+      const float ei = p.scale * dec_exp(own);
+      if (!wait(L::kM1, par)) break;
       tc_fence_after_sync();
+      {
+        uint32_t r[32];
+        tmem_ld32(tl + L::Sn + half * 32, r);
+        tmem_wait_ld();
 #pragma unroll
-      for (int s = 0; s < kTC / 16; ++s) mma_ts(tm + L::Oa, tm + L::Pb + s * 8, desc_cols(sb + L::v, s), mma_idesc(kVT, false, true), s > 0);
+        for (int e = 0; e < 32; ++e) S[e] = fmaf(S[e], elast, __uint_as_float(r[e]));
+      }
+      if (ck + 1 < cend) store_s();
+      // o through this warp's part of the first term's tile: a lane's accumulators are one row, whole rows leave
+      __syncwarp();
 #pragma unroll
-      for (int t = 2; t >= 0; --t)  // the smallest term first
-        mma_steps(tm + L::Sn, Cols{sb + L::k}, Cols{sb + (t == 0 ? L::w : L::q + (t - 1) * kPanel)}, mma_idesc(kVT, true, true), kTC / 16,
-                  t < 2);
-      mma_commit(bar);
+      for (int g = 0; g < 2; ++g) {
+        uint32_t a[16], i[16];
+        tmem_ld16(tl + L::Oa + half * 32 + g * 16, a);
+        tmem_ld16(tl + L::Oi + half * 32 + g * 16, i);
+        tmem_wait_ld();
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            x[e] = row < valid ? fmaf(__uint_as_float(i[8 * u + e]), ei, p.scale * __uint_as_float(a[8 * u + e])) : 0.f;
+          sts16(sb + L::w + tile_at(row, half * 4 + g * 2 + u), pack8(x));
+        }
+      }
+      if (ck + 1 < cend) arrive(L::kSt);
+      else __syncwarp();
+      store_rows(sb + L::w, o + (((long long)b * p.L + t0) * p.H + h) * p.V + v0, (long long)p.H * p.V, (warp & 3) * 32, half * 4,
+                 p.L - t0, vw, lane);
+      __syncwarp();
     }
-    const float ei = p.scale * dec_exp(own);
-    if (ckpt != nullptr && row < p.K) {
-      float4* dst = reinterpret_cast<float4*>(ckpt + (bh * p.nck + ck) * p.K * p.V) + row;
+    if (ok) {
+      for (int ck = cend; ck < c1; ++ck) {  // past the row's end
+        const int rows = p.L - ck * kTC < kTC ? p.L - ck * kTC : kTC;
+        for (int i = tid; i < rows * (vw / 8); i += 32 * L::warps)
+          *reinterpret_cast<uint4*>(o + (((long long)b * p.L + ck * kTC + i / (vw / 8)) * p.H + h) * p.V + v0 + i % (vw / 8) * 8) =
+              make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    if (send != nullptr && seg == p.nseg - 1 && row < p.K) {
+      float* dst = send + (bh * p.K + row) * p.V + v0 + half * 32;
 #pragma unroll
       for (int e = 0; e < 32; e += 4)
-        if (half * 32 + e < vw) dst[(long long)((v0 + half * 32 + e) / 4) * p.K] = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
-    }
-    ok = mbar_wait_bounded(bar, phase, kWaitLimitNs);
-    phase ^= 1;
-    if (__syncthreads_or(!ok)) break;
-    tc_fence_after_sync();
-    if (ck + 1 < cend) load(ck + 1);
-    uint32_t r[32];
-    tmem_ld32(tl + L::Sn + half * 32, r);
-    tmem_wait_ld();
-#pragma unroll
-    for (int e = 0; e < 32; ++e) S[e] = fmaf(S[e], elast, __uint_as_float(r[e]));
-    if (ck + 1 < cend) store_s();
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      uint32_t a[16], i[16];
-      tmem_ld16(tl + L::Oa + half * 32 + g * 16, a);
-      tmem_ld16(tl + L::Oi + half * 32 + g * 16, i);
-      tmem_wait_ld();
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          x[e] = row < valid ? fmaf(__uint_as_float(i[8 * u + e]), ei, p.scale * __uint_as_float(a[8 * u + e])) : 0.f;
-        sts16(sb + L::w + tile_at(row, half * 4 + g * 2 + u), pack8(x));
-      }
-    }
-    __syncthreads();
-    store_tile_tc<8, kTcThreads>(sb + L::w, o + (((long long)b * p.L + t0) * p.H + h) * p.V + v0, (long long)p.H * p.V, p.L - t0, vw, tid);
-  }
-  if (!ok) {  // a wait ran out: say so; the outputs are invalid
-    if (tid == 0) atomicOr(&g_lin_err, kErrTmaTimeout);
-    mbar_wait_bounded(bar, phase ^ 1, 100000000ull);  // its own MMAs
-    cp_wait_all();
-  } else {
-    for (int ck = cend; ck < c1; ++ck) {  // past the row's end
-      const int rows = p.L - ck * kTC < kTC ? p.L - ck * kTC : kTC;
-      for (int i = tid; i < rows * (vw / 8); i += kTcThreads)
-        *reinterpret_cast<uint4*>(o + (((long long)b * p.L + ck * kTC + i / (vw / 8)) * p.H + h) * p.V + v0 + i % (vw / 8) * 8) =
-            make_uint4(0u, 0u, 0u, 0u);
+        if (half * 32 + e < vw) *reinterpret_cast<float4*>(dst + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
     }
   }
-  if (send != nullptr && seg == p.nseg - 1 && row < p.K) {
-    float* dst = send + (bh * p.K + row) * p.V + v0 + half * 32;
-#pragma unroll
-    for (int e = 0; e < 32; e += 4)
-      if (half * 32 + e < vw) *reinterpret_cast<float4*>(dst + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
-  }
+  if (!ok && lane == 0) atomicOr(&g_lin_err, kErrTmaTimeout);  // a wait ran out: the outputs are invalid
   tc_fence_before_sync();
-  __syncthreads();
+  if (__syncthreads_or(!ok) && warp == 0) {  // whatever this CTA still has in flight: limited waits for both phases
+    for (int i = 0; i < 5; ++i)
+      for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(&bar[i], ph, 20000000ull);
+  }
   if (warp == 0) tmem_dealloc(tm, L::cols);
 }
 
@@ -441,12 +480,16 @@ int fwd_f32(const FwdPlan& pl, const float* h0, float* o, float* ckpt, float* h_
 int fwd_bf16(const FwdPlan& pl, const float* h0, __nv_bfloat16* o, float* ckpt, float* h_last, void* ws, cudaStream_t s) {
   const LinAttn& p = pl.p;
   const unsigned grid = (unsigned)pl.walks * p.nseg;
+  FwdMaps maps;
+  if (!lin_map(&maps.q, p.q, p.ldq, p.B, p.L, p.G, p.K) || !lin_map(&maps.k, p.k, p.ldk, p.B, p.L, p.G, p.K) ||
+      !lin_map(&maps.v, p.v, p.ldv, p.B, p.L, p.H, p.V))
+    return SS_ERR_CUDA;
   return fwd_run(
       pl, h0, ws, s,
       [&](float* st, Dec* dec) {
         return lin_launch(linattn_sum_tc_kernel<false>, grid, kTcThreads, SumTc::bytes, s, p, p.k, p.ldk, p.v, p.ldv, st, dec);
       },
-      [&](const float* s0) { return lin_launch(linattn_fwd_tc_kernel, grid, kTcThreads, FwdTc::bytes, s, p, s0, o, ckpt, h_last); });
+      [&](const float* s0) { return lin_launch(linattn_fwd_tc_kernel, grid, FwdTc::threads, FwdTc::bytes, s, p, maps, s0, o, ckpt, h_last); });
 }
 
 }  // namespace

@@ -179,6 +179,29 @@ __device__ __forceinline__ void tmem_scale(uint32_t taddr, float f) {
 
 // ---------------------------------------------------------------- tiles
 
+// [B, L, heads, width] bf16 with `ld` elements from token to token, as boxes of one panel (64 columns of one head
+// x kTC tokens); columns past `width` and tokens past L read as zero
+inline bool lin_map(CUtensorMap* m, const void* base, long long ld, int B, int L, int heads, int width) {
+  const uint64_t dims[4] = {(uint64_t)width, (uint64_t)heads, (uint64_t)L, (uint64_t)B};
+  const uint64_t strides[3] = {(uint64_t)width * 2, (uint64_t)ld * 2, (uint64_t)ld * 2 * (uint64_t)L};
+  const uint32_t box[4] = {64, 1, (uint32_t)kTC, 1};
+  return ssh::encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, true);
+}
+// the panels of a tile of `n` panels
+__device__ __forceinline__ void load_panels(uint32_t tile, int n, const CUtensorMap* m, uint64_t* bar, int c, int head, int t0, int b) {
+  for (int i = 0; i < n; ++i) tma_load_4d(tile + i * kPanel, m, bar, c + i * 64, head, t0, b);
+}
+__device__ __forceinline__ void prefetch_panels(int n, const CUtensorMap* m, int c, int head, int t0, int b) {
+  for (int i = 0; i < n; ++i) tma_prefetch_4d(m, c + i * 64, head, t0, b);
+}
+// rows from `valid` on of `panels` panels become zero (one warp): a row that ends inside the tensor
+__device__ __forceinline__ void zero_rows(uint32_t tile, int panels, int valid, int lane) {
+  for (int i = lane; i < panels * (kTC - valid) * 8; i += 32) {
+    const int n = i / ((kTC - valid) * 8), at = i % ((kTC - valid) * 8);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + n * kPanel + valid * 128 + at * 16), "r"(0) : "memory");
+  }
+}
+
 // 16 bytes global -> shared, asynchronously; zeros instead (nothing read) when !ok
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
@@ -211,10 +234,19 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-// A tile's first `rows` rows and `width` columns to global memory.  A lane's
-// accumulators are one row, so storing them as they are would touch 32 rows with
-// each instruction; through a tile a warp stores whole rows (the backward's three
+// A warp's part of a tile (32 rows from r0, four 16-byte units from u0) to
+// global memory, up to `rows` rows and `width` columns.  A lane's accumulators
+// are one row, so storing them as they are would touch 32 rows with each
+// instruction; through the tile four lanes share a row (the backward's three
 // outputs: 9000 -> 2000 cycles a chunk).
+__device__ __forceinline__ void store_rows(uint32_t tile, __nv_bfloat16* __restrict__ dst, long long ld, int r0, int u0, int rows, int width,
+                                           int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + i * 8 + (lane >> 2), u = u0 + (lane & 3);
+    if (r < rows && u * 8 < width) *reinterpret_cast<uint4*>(dst + (long long)r * ld + u * 8) = lds16(tile + tile_at(r, u));
+  }
+}
 template <int UNITS, int THREADS>
 __device__ __forceinline__ void store_tile_tc(uint32_t tile, __nv_bfloat16* __restrict__ dst, long long ld, int rows, int width, int tid) {
 #pragma unroll
@@ -399,13 +431,24 @@ __global__ void __launch_bounds__(256) linattn_join_kernel(const float* __restri
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   if (i >= kv) return;
   float s = first != nullptr ? first[bh * kv + i] : 0.f;
-  for (int m = 0; m < nseg; ++m) {
-    const int n = REV ? nseg - 1 - m : m;
-    float* at = st + (bh * nseg + n) * kv + i;
-    const Dec d = dec[bh * nseg + n];
-    const float end = *at;
-    *at = s;
-    s = fmaf(dec_exp(d.hi, d.lo), s, end);
+  constexpr int U = 8;  // end states in flight
+  for (int m = 0; m < nseg; m += U) {
+    float end[U];
+    Dec d[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (m + u >= nseg) break;
+      const int n = REV ? nseg - 1 - m - u : m + u;
+      end[u] = st[(bh * nseg + n) * kv + i];
+      d[u] = dec[bh * nseg + n];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (m + u >= nseg) break;
+      const int n = REV ? nseg - 1 - m - u : m + u;
+      st[(bh * nseg + n) * kv + i] = s;
+      s = fmaf(dec_exp(d[u]), s, end[u]);
+    }
   }
 }
 
