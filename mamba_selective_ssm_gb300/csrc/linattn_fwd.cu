@@ -143,54 +143,53 @@ __global__ void __launch_bounds__(256) linattn_fwd_kernel(LinAttn p, const float
 }
 
 // ---------------------------------------------------------------- bf16: tensor cores
-// A CTA walks the chunks (128 tokens) of one (batch row, head, 64-column tile of
-// V, segment).  The state stays in registers in fp32 (thread = row d of K and 32
-// of the 64 columns) and goes to shared memory as bf16 for the product with q.
-//   P   = q k^T                 -> scaled by the decays, rounded to bf16, back to tensor memory as an A operand
-//   Oi  = q S_in                (bf16 S_in; the row factor e^{c_i} is applied in fp32)
-//   Oa  = P v
-//   Sn  = k^T (w v),  w_j = e^{c_last - c_j}: w v as three bf16 terms, an fp32-exact product
+// A CTA walks the chunks (128 tokens) of one (batch row, head, segment).  The
+// state stays in registers in fp32 (thread = row d of K and a quarter of the V
+// columns) and goes to shared memory as bf16 for the product with q.
+//   P  = q k^T               -> scaled by the decays, rounded to bf16, back to tensor memory as an A operand
+//   O  = q S_in              -> * e^{c_i} in fp32 (bf16 S_in)
+//   Sn = k^T (w v),  w_j = e^{c_last - c_j}: w v as three bf16 terms, an fp32-exact product
+//   O += P v
 // A term of o is rounded to bf16 once on its way (as a score or as a state).
 //
-// Eight warps compute; a ninth issues: the TMA loads, the MMAs (whose issue
+// Sixteen warps compute; one more issues: the TMA loads, the MMAs (whose issue
 // blocks while the tensor cores are behind) and the decays of the next chunk.
-// They meet at mbarriers only, so a warp waits for what it needs and not for the
-// CTA.  Two CTAs share an SM and fill each other's waits.
+// They meet at mbarriers only, so that the products of the state run under the
+// scaling of the scores, and the next chunk's loads under this one's output.
+// All of V in one CTA: with 64 columns a CTA and two CTAs an SM the scores were
+// made and scaled twice and the narrow products waited for shared memory
+// (1.4B-shaped prefill 114 us).
+template <int VP>
 struct FwdTc {
-  // shared memory: tiles, decays, barriers, tensor-memory address; two CTAs fit an SM
-  static constexpr int q = 0, k = q + 2 * kPanel, v = k + 2 * kPanel, s = v + kPanel, w = s + kPanel, dec = w + kPanel;
-  static constexpr int bar = dec + DecTile::bytes, tm = bar + 5 * 8, bytes = tm + 8;
-  static_assert(2 * (bytes + 1024) <= 228 * 1024, "two CTAs an SM");
-  // barriers: chunk landed; state tile stored (and accumulators read); scores stored; first and second products done
-  static constexpr int kLd = 0, kSt = 1, kSc = 2, kM0 = 3, kM1 = 4;
-  // tensor memory columns
-  static constexpr int P = 0, Oa = 0, Sn = 64, Pb = 128, Oi = 192, cols = 256;
-  static constexpr int warps = 8, threads = 32 * (warps + 1);
-  static constexpr uint32_t tx = 5 * kPanel;
+  static constexpr int vt = kTC * VP * 2;  // bytes of a tile VP columns wide
+  static constexpr int q = 0, k = q + 2 * kPanel, v = k + 2 * kPanel, s = v + vt, w = s + vt, dec = w + 3 * vt;
+  // barriers: chunk landed; w v stored; scores stored and O scaled; state tile stored; O read; P, O, Sn, O + P v done
+  static constexpr int kLd = 0, kW = 1, kSc = 2, kSt = 3, kRd = 4, kMp = 5, kMo = 6, kMs = 7, kM1 = 8, nbar = 9;
+  static constexpr int bar = dec + DecTile::bytes, tm = bar + nbar * 8, bytes = tm + 8;
+  static constexpr int P = 0, Pb = 128, O = 192, Sn = 192 + VP, cols = 512;  // tensor memory columns
+  static constexpr uint32_t tx = 4 * kPanel + vt;
 };
 
 struct FwdMaps {
   CUtensorMap q, k, v;
 };
 
-__global__ void __launch_bounds__(FwdTc::threads, 2) linattn_fwd_tc_kernel(LinAttn p, const __grid_constant__ FwdMaps maps,
-                                                                           const float* __restrict__ s0, __nv_bfloat16* __restrict__ o,
-                                                                           float* __restrict__ ckpt, float* __restrict__ send) {
-  using L = FwdTc;
+template <int VP>
+__global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn p, const __grid_constant__ FwdMaps maps,
+                                                                        const float* __restrict__ s0, __nv_bfloat16* __restrict__ o,
+                                                                        float* __restrict__ ckpt, float* __restrict__ send) {
+  using L = FwdTc<VP>;
+  constexpr int VQ = VP / 4, NU = VQ / 8;  // columns and 16-byte units of a thread's quarter of V
   extern __shared__ __align__(1024) unsigned char raw[];
   const uint32_t sb = smem_u32(raw);
   const DecTile dec{sb + L::dec};
   uint64_t* bar = reinterpret_cast<uint64_t*>(raw + L::bar);
   uint32_t* tma = reinterpret_cast<uint32_t*>(raw + L::tm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nvt = (p.V + kVT - 1) / kVT;
   long long id = blockIdx.x;
   const int seg = (int)(id % p.nseg);
   id /= p.nseg;
-  const int vt = (int)(id % nvt);
-  id /= nvt;
-  const int h = (int)(id % p.H), b = (int)(id / p.H);
-  const int gh = h / (p.H / p.G), v0 = vt * kVT, vw = p.V - v0 < kVT ? p.V - v0 : kVT;
+  const int h = (int)(id % p.H), b = (int)(id / p.H), gh = h / (p.H / p.G);
   const int len = p.len(b);
   const long long bh = (long long)b * p.H + h;
   const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
@@ -198,11 +197,7 @@ __global__ void __launch_bounds__(FwdTc::threads, 2) linattn_fwd_tc_kernel(LinAt
   cend = cend < c0 ? c0 : cend < c1 ? cend : c1;
 
   if (tid == 0) {
-    mbar_init(&bar[L::kLd], 1);
-    mbar_init(&bar[L::kSt], L::warps);
-    mbar_init(&bar[L::kSc], L::warps);
-    mbar_init(&bar[L::kM0], 1);
-    mbar_init(&bar[L::kM1], 1);
+    for (int i = 0; i < L::nbar; ++i) mbar_init(&bar[i], i >= L::kW && i <= L::kRd ? kLinWarps : 1);
     fence_barrier_init();
   }
   if (warp == 0) {
@@ -216,10 +211,10 @@ __global__ void __launch_bounds__(FwdTc::threads, 2) linattn_fwd_tc_kernel(LinAt
   bool ok = true;
   auto wait = [&](int i, uint32_t par) { return ok = mbar_wait_bounded(&bar[i], par, kWaitLimitNs); };
 
-  if (warp == L::warps) {  // ---- the issuing warp
+  if (warp == kLinWarps) {  // ---- the issuing warp
     const int ks = (p.K + 15) / 16;  // contraction steps over K
     ChunkGates<kTC> gates;
-    auto load = [&](int ck) {  // a chunk's decays and tiles; its readers have passed a barrier that this warp has waited for
+    auto load = [&](int ck) {  // a chunk's decays and tiles; their readers have passed a barrier that this warp has waited for
       put_decays(gates, dec, lane);
       __syncwarp();
       if (lane == 0) {
@@ -227,11 +222,11 @@ __global__ void __launch_bounds__(FwdTc::threads, 2) linattn_fwd_tc_kernel(LinAt
         mbar_arrive_expect_tx(&bar[L::kLd], L::tx);
         load_panels(sb + L::q, 2, &maps.q, &bar[L::kLd], 0, gh, ck * kTC, b);
         load_panels(sb + L::k, 2, &maps.k, &bar[L::kLd], 0, gh, ck * kTC, b);
-        load_panels(sb + L::v, 1, &maps.v, &bar[L::kLd], v0, h, ck * kTC, b);
+        load_panels(sb + L::v, VP / 64, &maps.v, &bar[L::kLd], 0, h, ck * kTC, b);
         if (ck + 1 < cend) {
           prefetch_panels((p.K + 63) / 64, &maps.q, 0, gh, (ck + 1) * kTC, b);
           prefetch_panels((p.K + 63) / 64, &maps.k, 0, gh, (ck + 1) * kTC, b);
-          prefetch_panels(1, &maps.v, v0, h, (ck + 1) * kTC, b);
+          prefetch_panels((p.V + 63) / 64, &maps.v, 0, h, (ck + 1) * kTC, b);
         }
       }
       gates.fetch(p, b, h, (ck + 1) * kTC, len, lane);
@@ -245,27 +240,35 @@ __global__ void __launch_bounds__(FwdTc::threads, 2) linattn_fwd_tc_kernel(LinAt
       if (!wait(L::kLd, par)) break;
       const int valid = len - ck * kTC;
       if (valid < kTC && ck * kTC + valid < p.L) {  // the row ends inside the tensor: what follows is not its own
-        zero_rows(sb + L::q, 5, valid, lane);
+        zero_rows(sb + L::q, 4 + VP / 64, valid, lane);
         fence_proxy_async_smem();
         __syncwarp();
       }
-      if (!wait(L::kSt, par)) break;
-      if (lane == 0) {
+      if (lane == 0) {  // the scores of the chunk before have been read: its kM1 has been waited for
         tc_fence_after_sync();
         mma_steps(tm + L::P, Rows{sb + L::q}, Rows{sb + L::k}, mma_idesc(kTC, false, false), ks, false);
-        mma_steps(tm + L::Oi, Rows{sb + L::q}, Cols{sb + L::s}, mma_idesc(kVT, false, true), ks, false);
-        mma_commit(&bar[L::kM0]);
+        mma_commit(&bar[L::kMp]);
+      }
+      if (!wait(L::kSt, par) || !wait(L::kRd, par)) break;
+      if (lane == 0) {
+        tc_fence_after_sync();
+        mma_steps(tm + L::O, Rows{sb + L::q}, Cols{sb + L::s}, mma_idesc(VP, false, true), ks, false);
+        mma_commit(&bar[L::kMo]);
+      }
+      if (!wait(L::kW, par)) break;
+      if (lane == 0) {
+        tc_fence_after_sync();
+#pragma unroll
+        for (int t = 2; t >= 0; --t)  // the smallest term first
+          mma_steps(tm + L::Sn, Cols{sb + L::k}, Cols{sb + L::w + t * L::vt}, mma_idesc(VP, true, true), kTC / 16, t < 2);
+        mma_commit(&bar[L::kMs]);
       }
       if (!wait(L::kSc, par)) break;
       if (lane == 0) {
         tc_fence_after_sync();
 #pragma unroll
         for (int s = 0; s < kTC / 16; ++s)
-          mma_ts(tm + L::Oa, tm + L::Pb + s * 8, desc_cols(sb + L::v, s), mma_idesc(kVT, false, true), s > 0);
-#pragma unroll
-        for (int t = 2; t >= 0; --t)  // the smallest term first
-          mma_steps(tm + L::Sn, Cols{sb + L::k}, Cols{sb + (t == 0 ? L::w : L::q + (t - 1) * kPanel)}, mma_idesc(kVT, true, true),
-                    kTC / 16, t < 2);
+          mma_ts(tm + L::O, tm + L::Pb + s * 8, desc_cols(sb + L::v, s), mma_idesc(VP, false, true), true);
         mma_commit(&bar[L::kM1]);
       }
       __syncwarp();
@@ -274,17 +277,17 @@ __global__ void __launch_bounds__(FwdTc::threads, 2) linattn_fwd_tc_kernel(LinAt
         load(ck + 1);
       }
     }
-  } else {  // ---- a computing warp
-    const int row = (warp & 3) * 32 + lane, half = warp >> 2;  // tensor-memory lane and half of the columns of this thread
+  } else if (warp < kLinWarps) {  // ---- a computing warp
+    const int row = (warp & 3) * 32 + lane, cq = warp >> 2;  // tensor-memory lane and quarter of the columns of this thread
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
-    float S[32];
+    float S[VQ];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) S[e] = 0.f;
+    for (int e = 0; e < VQ; ++e) S[e] = 0.f;
     if (s0 != nullptr && row < p.K) {
-      const float* src = s0 + ((p.nseg > 1 ? bh * p.nseg + seg : bh) * p.K + row) * p.V + v0 + half * 32;
+      const float* src = s0 + ((p.nseg > 1 ? bh * p.nseg + seg : bh) * p.K + row) * p.V + cq * VQ;
 #pragma unroll
-      for (int e = 0; e < 32; e += 4)
-        if (half * 32 + e < vw) {
+      for (int e = 0; e < VQ; e += 4)
+        if (cq * VQ + e < p.V) {
           const float4 x = *reinterpret_cast<const float4*>(src + e);
           S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
         }
@@ -297,64 +300,58 @@ __global__ void __launch_bounds__(FwdTc::threads, 2) linattn_fwd_tc_kernel(LinAt
     };
     auto store_s = [&]() {  // S_in as a bf16 tile
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < NU; ++u) {
         const float x[8] = {S[8 * u], S[8 * u + 1], S[8 * u + 2], S[8 * u + 3], S[8 * u + 4], S[8 * u + 5], S[8 * u + 6], S[8 * u + 7]};
-        sts16(sb + L::s + tile_at(row, half * 4 + u), pack8(x));
+        sts16(sb + L::s + tile_at(row, cq * NU + u), pack8(x));
       }
     };
     if (c0 < cend) {
       store_s();
       arrive(L::kSt);
+      arrive(L::kRd);
     }
     for (int ck = c0; ck < cend; ++ck) {
       const uint32_t par = (uint32_t)(ck - c0) & 1u;
       const int t0 = ck * kTC, valid = len - t0;
       if (!wait(L::kLd, par)) break;
       const Dec last = dec.get(kTC - 1), own = dec.get(row);
-      const float elast = dec_exp(last), wj = dec_exp(dec_sub(last, own));
-      // w v of this thread's token and half of the columns, eight at a time
-      auto wv = [&](int u, float (&x)[8]) {
-        Raw8<__nv_bfloat16>::wide(lds16(sb + L::v + tile_at(row, half * 4 + u)), x);
+      const float elast = dec_exp(last);
+      {
+        const float wj = dec_exp(dec_sub(last, own));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = row < valid ? x[e] * wj : 0.f;
-      };
+        for (int u = 0; u < NU; ++u) {  // w v of this thread's token
+          const uint32_t at = tile_at(row, cq * NU + u);
+          float x[8];
+          Raw8<__nv_bfloat16>::wide(row < valid ? lds16(sb + L::v + at) : make_uint4(0u, 0u, 0u, 0u), x);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {  // the first term has a tile of its own, the others take q's
-        float x[8];
-        wv(u, x);
-        sts16(sb + L::w + tile_at(row, half * 4 + u), take_term(x));
+          for (int e = 0; e < 8; ++e) x[e] *= wj;
+          sts16(sb + L::w + at, take_term(x));
+          sts16(sb + L::w + L::vt + at, take_term(x));
+          sts16(sb + L::w + 2 * L::vt + at, last_term(x));
+        }
+        arrive(L::kW);
       }
-      if (!wait(L::kM0, par)) break;
+      if (!wait(L::kMp, par)) break;
       tc_fence_after_sync();
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        float x[8];
-        wv(u, x);
-        take_term(x);
-        sts16(sb + L::q + tile_at(row, half * 4 + u), take_term(x));
-        sts16(sb + L::q + kPanel + tile_at(row, half * 4 + u), take_term(x));
-      }
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {  // 32 key tokens at a time: all before this warp's tokens, among them, or after them
-        const int jb = half * 2 + g;
+      {  // 32 key tokens: all before this warp's tokens, among them, or after them
         uint32_t w[16];
-        if (jb <= (warp & 3)) {
+        if (cq <= (warp & 3)) {
           uint32_t r[32];
-          tmem_ld32(tl + L::P + jb * 32, r);
-          const Dec d = dec_sub(own, dec.base(jb));
+          tmem_ld32(tl + L::P + cq * 32, r);
+          const Dec d = dec_sub(own, dec.base(cq));
           const float x = d.hi + d.lo;
           tmem_wait_ld();
-          if (jb < (warp & 3)) {
+          if (cq < (warp & 3)) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const float4 c = dec.r4(jb * 32 + e);
+              const float4 c = dec.r4(cq * 32 + e);
               w[e / 2] = pack_bf16(__uint_as_float(r[e]) * ex2(x - c.x), __uint_as_float(r[e + 1]) * ex2(x - c.y));
               w[e / 2 + 1] = pack_bf16(__uint_as_float(r[e + 2]) * ex2(x - c.z), __uint_as_float(r[e + 3]) * ex2(x - c.w));
             }
           } else {
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const float4 c = dec.r4(jb * 32 + e);
+              const float4 c = dec.r4(cq * 32 + e);
               w[e / 2] = pack_bf16(e <= lane ? __uint_as_float(r[e]) * ex2(x - c.x) : 0.f,
                                    e + 1 <= lane ? __uint_as_float(r[e + 1]) * ex2(x - c.y) : 0.f);
               w[e / 2 + 1] = pack_bf16(e + 2 <= lane ? __uint_as_float(r[e + 2]) * ex2(x - c.z) : 0.f,
@@ -365,77 +362,72 @@ __global__ void __launch_bounds__(FwdTc::threads, 2) linattn_fwd_tc_kernel(LinAt
 #pragma unroll
           for (int e = 0; e < 16; ++e) w[e] = 0u;
         }
-        tmem_st16(tl + L::Pb + jb * 16, w);
+        tmem_st16(tl + L::Pb + cq * 16, w);
       }
+      if (!wait(L::kMo, par)) break;
+      tc_fence_after_sync();
+      tmem_scale<VQ>(tl + L::O + cq * VQ, dec_exp(own));
       tmem_wait_st();
       arrive(L::kSc);
       if (ckpt != nullptr && row < p.K) {
         float4* dst = reinterpret_cast<float4*>(ckpt + (bh * p.nck + ck) * p.K * p.V) + row;
 #pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          if (half * 32 + e < vw) dst[(long long)((v0 + half * 32 + e) / 4) * p.K] = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+        for (int e = 0; e < VQ; e += 4)
+          if (cq * VQ + e < p.V) dst[(long long)((cq * VQ + e) / 4) * p.K] = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
       }
-      const float ei = p.scale * dec_exp(own);
-      if (!wait(L::kM1, par)) break;
+      if (!wait(L::kMs, par)) break;
       tc_fence_after_sync();
       {
-        uint32_t r[32];
-        tmem_ld32(tl + L::Sn + half * 32, r);
+        uint32_t r[VQ];
+        tmem_ldn(tl + L::Sn + cq * VQ, r);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) S[e] = fmaf(S[e], elast, __uint_as_float(r[e]));
+        for (int e = 0; e < VQ; ++e) S[e] = fmaf(S[e], elast, __uint_as_float(r[e]));
       }
-      if (ck + 1 < cend) store_s();
-      // o through this warp's part of the first term's tile: a lane's accumulators are one row, whole rows leave
-      __syncwarp();
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint32_t a[16], i[16];
-        tmem_ld16(tl + L::Oa + half * 32 + g * 16, a);
-        tmem_ld16(tl + L::Oi + half * 32 + g * 16, i);
+      if (ck + 1 < cend) {
+        store_s();
+        arrive(L::kSt);
+      }
+      if (!wait(L::kM1, par)) break;
+      tc_fence_after_sync();
+      {  // o through this warp's part of the first term's tile: a lane's accumulators are one row, whole rows leave
+        uint32_t r[VQ];
+        tmem_ldn(tl + L::O + cq * VQ, r);
         tmem_wait_ld();
+        if (ck + 1 < cend) arrive(L::kRd);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < NU; ++u) {
           float x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            x[e] = row < valid ? fmaf(__uint_as_float(i[8 * u + e]), ei, p.scale * __uint_as_float(a[8 * u + e])) : 0.f;
-          sts16(sb + L::w + tile_at(row, half * 4 + g * 2 + u), pack8(x));
+          for (int e = 0; e < 8; ++e) x[e] = row < valid ? p.scale * __uint_as_float(r[8 * u + e]) : 0.f;
+          sts16(sb + L::w + tile_at(row, cq * NU + u), pack8(x));
         }
+        __syncwarp();
+        store_rows<NU>(sb + L::w, o + (((long long)b * p.L + t0) * p.H + h) * p.V, (long long)p.H * p.V, (warp & 3) * 32, cq * NU,
+                       p.L - t0, p.V, lane);
+        __syncwarp();
       }
-      if (ck + 1 < cend) arrive(L::kSt);
-      else __syncwarp();
-      store_rows(sb + L::w, o + (((long long)b * p.L + t0) * p.H + h) * p.V + v0, (long long)p.H * p.V, (warp & 3) * 32, half * 4,
-                 p.L - t0, vw, lane);
-      __syncwarp();
     }
     if (ok) {
       for (int ck = cend; ck < c1; ++ck) {  // past the row's end
-        const int rows = p.L - ck * kTC < kTC ? p.L - ck * kTC : kTC;
-        for (int i = tid; i < rows * (vw / 8); i += 32 * L::warps)
-          *reinterpret_cast<uint4*>(o + (((long long)b * p.L + ck * kTC + i / (vw / 8)) * p.H + h) * p.V + v0 + i % (vw / 8) * 8) =
-              make_uint4(0u, 0u, 0u, 0u);
+        const int rows = p.L - ck * kTC < kTC ? p.L - ck * kTC : kTC, n = p.V / 8;
+        for (int i = tid; i < rows * n; i += 32 * kLinWarps)
+          *reinterpret_cast<uint4*>(o + (((long long)b * p.L + ck * kTC + i / n) * p.H + h) * p.V + i % n * 8) = make_uint4(0u, 0u, 0u, 0u);
       }
     }
     if (send != nullptr && seg == p.nseg - 1 && row < p.K) {
-      float* dst = send + (bh * p.K + row) * p.V + v0 + half * 32;
+      float* dst = send + (bh * p.K + row) * p.V + cq * VQ;
 #pragma unroll
-      for (int e = 0; e < 32; e += 4)
-        if (half * 32 + e < vw) *reinterpret_cast<float4*>(dst + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+      for (int e = 0; e < VQ; e += 4)
+        if (cq * VQ + e < p.V) *reinterpret_cast<float4*>(dst + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
     }
   }
-  if (!ok && lane == 0) atomicOr(&g_lin_err, kErrTmaTimeout);  // a wait ran out: the outputs are invalid
-  tc_fence_before_sync();
-  if (__syncthreads_or(!ok) && warp == 0) {  // whatever this CTA still has in flight: limited waits for both phases
-    for (int i = 0; i < 5; ++i)
-      for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(&bar[i], ph, 20000000ull);
-  }
-  if (warp == 0) tmem_dealloc(tm, L::cols);
+  lin_leave(ok, bar, L::nbar, tm, L::cols, warp, lane);
 }
 
 struct FwdPlan {
   LinAttn p;
-  long long walks;  // (batch row, head, column tile)
+  long long walks;  // (batch row, head) and for fp32 column tile
   size_t states, bytes;
 };
 
@@ -444,9 +436,9 @@ int fwd_plan(int B, int L, int H, int G, int K, int V, int dtype, FwdPlan& pl) {
   if (rc != SS_OK) return rc;
   pl.p = LinAttn{};
   pl.p.B = B; pl.p.L = L; pl.p.H = H; pl.p.G = G; pl.p.K = K; pl.p.V = V;
-  pl.walks = (long long)B * H * ((V + kVT - 1) / kVT);
+  pl.walks = (long long)B * H * (dtype == SS_F32 ? (V + kVT - 1) / kVT : 1);
   if (pl.walks > (1ll << 24)) return SS_ERR_DIM;
-  linattn_segments(pl.p, linattn_chunk(dtype), pl.walks, (dtype == SS_BF16 || K <= 64 ? 2 : 1) * 152);
+  linattn_segments(pl.p, linattn_chunk(dtype), pl.walks, (dtype == SS_F32 && K <= 64 ? 2 : 1) * 152);
   pl.states = pl.p.nseg > 1 ? (size_t)B * H * pl.p.nseg * K * V * sizeof(float) : 0;
   pl.bytes = pl.p.nseg > 1 ? pl.states + (size_t)B * H * pl.p.nseg * sizeof(Dec) : 0;
   return SS_OK;
@@ -477,6 +469,7 @@ int fwd_f32(const FwdPlan& pl, const float* h0, float* o, float* ckpt, float* h_
       [&](const float* s0) { return lin_launch(linattn_fwd_kernel<KP, false>, grid, 256, smem, s, pl.p, s0, o, ckpt, h_last, nullptr); });
 }
 
+template <int VP>
 int fwd_bf16(const FwdPlan& pl, const float* h0, __nv_bfloat16* o, float* ckpt, float* h_last, void* ws, cudaStream_t s) {
   const LinAttn& p = pl.p;
   const unsigned grid = (unsigned)pl.walks * p.nseg;
@@ -487,9 +480,9 @@ int fwd_bf16(const FwdPlan& pl, const float* h0, __nv_bfloat16* o, float* ckpt, 
   return fwd_run(
       pl, h0, ws, s,
       [&](float* st, Dec* dec) {
-        return lin_launch(linattn_sum_tc_kernel<false>, grid, kTcThreads, SumTc::bytes, s, p, p.k, p.ldk, p.v, p.ldv, st, dec);
+        return lin_launch(linattn_sum_tc_kernel<false>, grid * ((p.V + 63) / 64), kTcThreads, SumTc::bytes, s, p, p.k, p.ldk, p.v, p.ldv, st, dec);
       },
-      [&](const float* s0) { return lin_launch(linattn_fwd_tc_kernel, grid, FwdTc::threads, FwdTc::bytes, s, p, maps, s0, o, ckpt, h_last); });
+      [&](const float* s0) { return lin_launch(linattn_fwd_tc_kernel<VP>, grid, kLinThreads, FwdTc<VP>::bytes, s, p, maps, s0, o, ckpt, h_last); });
 }
 
 }  // namespace
@@ -534,7 +527,8 @@ extern "C" int linattn_fwd(const void* q, long long ldq, const void* k, long lon
   if (dtype == SS_F32)
     return K <= 64 ? fwd_f32<64>(pl, h0, static_cast<float*>(o), ckpt, h_last, workspace, s)
                    : fwd_f32<128>(pl, h0, static_cast<float*>(o), ckpt, h_last, workspace, s);
-  return fwd_bf16(pl, h0, static_cast<__nv_bfloat16*>(o), ckpt, h_last, workspace, s);
+  return V <= 64 ? fwd_bf16<64>(pl, h0, static_cast<__nv_bfloat16*>(o), ckpt, h_last, workspace, s)
+                 : fwd_bf16<128>(pl, h0, static_cast<__nv_bfloat16*>(o), ckpt, h_last, workspace, s);
 }
 
 namespace ssh {

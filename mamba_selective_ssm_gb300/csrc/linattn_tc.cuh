@@ -16,6 +16,7 @@ namespace ssk {
 constexpr int kTC = kLinChunkBf16;        // tokens of a chunk = rows of a tile
 constexpr int kPanel = kTC * 128;         // bytes of a panel of kTC rows
 constexpr int kTcThreads = 256;
+constexpr int kLinWarps = 16, kLinThreads = 32 * (kLinWarps + 1);  // computing warps, and one that issues
 
 // byte offset of 16-byte unit `u` (8 columns) of row r in a tile of kTC rows
 __device__ __forceinline__ uint32_t tile_at(int r, int u) {
@@ -234,16 +235,17 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-// A warp's part of a tile (32 rows from r0, four 16-byte units from u0) to
+// A warp's part of a tile (32 rows from r0, NU 16-byte units from u0) to
 // global memory, up to `rows` rows and `width` columns.  A lane's accumulators
 // are one row, so storing them as they are would touch 32 rows with each
 // instruction; through the tile four lanes share a row (the backward's three
 // outputs: 9000 -> 2000 cycles a chunk).
+template <int NU>  // NU units of each row: 4 or 2
 __device__ __forceinline__ void store_rows(uint32_t tile, __nv_bfloat16* __restrict__ dst, long long ld, int r0, int u0, int rows, int width,
                                            int lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + i * 8 + (lane >> 2), u = u0 + (lane & 3);
+  for (int i = 0; i < NU; ++i) {
+    const int r = r0 + i * (32 / NU) + lane / NU, u = u0 + lane % NU;
     if (r < rows && u * 8 < width) *reinterpret_cast<uint4*>(dst + (long long)r * ld + u * 8) = lds16(tile + tile_at(r, u));
   }
 }
@@ -271,6 +273,8 @@ __device__ __forceinline__ uint4 take_term(float (&x)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+__device__ __forceinline__ uint4 last_term(const float (&x)[8]) { return pack8(x); }
+
 }  // namespace ssk
 
 namespace {
@@ -284,6 +288,19 @@ inline int read_clear_lin_err(cudaStream_t s, unsigned* out) {
   if (cudaMemcpyFromSymbolAsync(out, g_lin_err, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess) return SS_ERR_CUDA;
   if (cudaMemcpyToSymbolAsync(g_lin_err, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s) != cudaSuccess) return SS_ERR_CUDA;
   return cudaStreamSynchronize(s) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+// The end of a kernel of kLinThreads: a wait that ran out is told (the outputs
+// are invalid) and whatever is still in flight gets a limited wait, then the
+// tensor memory is returned.
+__device__ __forceinline__ void lin_leave(bool ok, uint64_t* bar, int nbar, uint32_t tm, uint32_t cols, int warp, int lane) {
+  if (!ok && lane == 0) atomicOr(&g_lin_err, kErrTmaTimeout);
+  tc_fence_before_sync();
+  if (__syncthreads_or(!ok) && warp == 0) {
+    for (int i = 0; i < nbar; ++i)
+      for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(&bar[i], ph, 20000000ull);
+  }
+  if (warp == 0) tmem_dealloc(tm, cols);
 }
 
 // ---------------------------------------------------------------- a segment's state
