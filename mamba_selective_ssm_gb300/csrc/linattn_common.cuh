@@ -116,23 +116,23 @@ struct ChunkGates {
 #pragma unroll
     for (int e = 0; e < PER; ++e) put(lane * PER + e, dec_add(before, x[e]));
   }
-  // Running sums within blocks of 32 tokens, put(i, r_i), and the sum before each block, put_base(n, c).
-  template <typename Put, typename Base>
-  __device__ __forceinline__ void scan_rel(int lane, Put put, Base put_base) const {
+  // Running sums within blocks of 32 tokens, rel[e] of the lane's own tokens, and in lane n the sum before block n.
+  __device__ __forceinline__ Dec scan_rel(int lane, Dec (&rel)[PER]) const {
     constexpr int LB = 32 / PER;  // lanes of a block
-    Dec x[PER], before;
-    const Dec incl = sums(lane, LB, x, before);
+    Dec before;
+    const Dec incl = sums(lane, LB, rel, before);
 #pragma unroll
-    for (int e = 0; e < PER; ++e) put(lane * PER + e, dec_add(before, x[e]));
-    Dec base = {0.f, 0.f};
+    for (int e = 0; e < PER; ++e) rel[e] = dec_add(before, rel[e]);
+    Dec base = {0.f, 0.f}, own = base;
 #pragma unroll
     for (int n = 0; n < 32 / LB; ++n) {
-      if (lane == 0) put_base(n, base);
+      if (lane == n) own = base;
       Dec u;
       u.hi = __shfl_sync(0xffffffffu, incl.hi, n * LB + LB - 1);
       u.lo = __shfl_sync(0xffffffffu, incl.lo, n * LB + LB - 1);
       base = dec_add(base, u);
     }
+    return own;
   }
 };
 

@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(256) linattn_fwd_kernel(LinAttn p, const float
 //   O += P v
 // A term of o is rounded to bf16 once on its way (as a score or as a state).
 //
-// Sixteen warps compute; one more issues: the TMA loads, the MMAs (whose issue
-// blocks while the tensor cores are behind) and the decays of the next chunk.
+// Sixteen warps compute; one issues the TMA loads and the MMAs (whose issue
+// blocks while the tensor cores are behind), one finds the next chunk's decays.
 // They meet at mbarriers only, so that the products of the state run under the
 // scaling of the scores, and the next chunk's loads under this one's output.
 // All of V in one CTA: with 64 columns a CTA and two CTAs an SM the scores were
@@ -163,11 +163,11 @@ template <int VP>
 struct FwdTc {
   static constexpr int vt = kTC * VP * 2;  // bytes of a tile VP columns wide
   static constexpr int q = 0, k = q + 2 * kPanel, v = k + 2 * kPanel, s = v + vt, w = s + vt, dec = w + 3 * vt;
-  // barriers: chunk landed; w v stored; scores stored and O scaled; state tile stored; O read; P, O, Sn, O + P v done
-  static constexpr int kLd = 0, kW = 1, kSc = 2, kSt = 3, kRd = 4, kMp = 5, kMo = 6, kMs = 7, kM1 = 8, nbar = 9;
+  // barriers: v landed, q and k landed, decays stored; w v stored; scores stored and O scaled; state tile stored; O read;
+  // P, O, Sn, O + P v done
+  static constexpr int kLd = 0, kW = 1, kSc = 2, kSt = 3, kRd = 4, kMp = 5, kMo = 6, kMs = 7, kM1 = 8, kLq = 9, kDc = 10, nbar = 11;
   static constexpr int bar = dec + DecTile::bytes, tm = bar + nbar * 8, bytes = tm + 8;
   static constexpr int P = 0, Pb = 128, O = 192, Sn = 192 + VP, cols = 512;  // tensor memory columns
-  static constexpr uint32_t tx = 4 * kPanel + vt;
 };
 
 struct FwdMaps {
@@ -213,38 +213,37 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
 
   if (warp == kLinWarps) {  // ---- the issuing warp
     const int ks = (p.K + 15) / 16;  // contraction steps over K
-    ChunkGates<kTC> gates;
-    auto load = [&](int ck) {  // a chunk's decays and tiles; their readers have passed a barrier that this warp has waited for
-      put_decays(gates, dec, lane);
-      __syncwarp();
+    // a chunk's tiles; their readers have passed a barrier that this warp has waited for, with a proxy fence before it
+    auto load_qk = [&](int ck) {
       if (lane == 0) {
-        fence_proxy_async_smem();
-        mbar_arrive_expect_tx(&bar[L::kLd], L::tx);
-        load_panels(sb + L::q, 2, &maps.q, &bar[L::kLd], 0, gh, ck * kTC, b);
-        load_panels(sb + L::k, 2, &maps.k, &bar[L::kLd], 0, gh, ck * kTC, b);
-        load_panels(sb + L::v, VP / 64, &maps.v, &bar[L::kLd], 0, h, ck * kTC, b);
-        if (ck + 1 < cend) {
-          prefetch_panels((p.K + 63) / 64, &maps.q, 0, gh, (ck + 1) * kTC, b);
-          prefetch_panels((p.K + 63) / 64, &maps.k, 0, gh, (ck + 1) * kTC, b);
-          prefetch_panels((p.V + 63) / 64, &maps.v, 0, h, (ck + 1) * kTC, b);
-        }
+        mbar_arrive_expect_tx(&bar[L::kLq], 4 * kPanel);
+        load_panels(sb + L::q, 2, &maps.q, &bar[L::kLq], 0, gh, ck * kTC, b);
+        load_panels(sb + L::k, 2, &maps.k, &bar[L::kLq], 0, gh, ck * kTC, b);
       }
-      gates.fetch(p, b, h, (ck + 1) * kTC, len, lane);
+      __syncwarp();
+    };
+    auto load_v = [&](int ck) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bar[L::kLd], L::vt);
+        load_panels(sb + L::v, VP / 64, &maps.v, &bar[L::kLd], 0, h, ck * kTC, b);
+      }
+      __syncwarp();
     };
     if (c0 < cend) {
-      gates.fetch(p, b, h, c0 * kTC, len, lane);
-      load(c0);
+      load_qk(c0);
+      load_v(c0);
     }
     for (int ck = c0; ck < cend; ++ck) {
       const uint32_t par = (uint32_t)(ck - c0) & 1u;
-      if (!wait(L::kLd, par)) break;
       const int valid = len - ck * kTC;
-      if (valid < kTC && ck * kTC + valid < p.L) {  // the row ends inside the tensor: what follows is not its own
-        zero_rows(sb + L::q, 4 + VP / 64, valid, lane);
+      const bool more = ck + 1 < cend, cut = valid < kTC && ck * kTC + valid < p.L;
+      if (!wait(L::kLq, par)) break;
+      if (cut) {  // the row ends inside the tensor: what follows is not its own
+        zero_rows(sb + L::q, 4, valid, lane);
         fence_proxy_async_smem();
         __syncwarp();
       }
-      if (lane == 0) {  // the scores of the chunk before have been read: its kM1 has been waited for
+      if (lane == 0) {  // the scores of the chunk before have been read: its kSc has been waited for
         tc_fence_after_sync();
         mma_steps(tm + L::P, Rows{sb + L::q}, Rows{sb + L::k}, mma_idesc(kTC, false, false), ks, false);
         mma_commit(&bar[L::kMp]);
@@ -254,8 +253,19 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
         tc_fence_after_sync();
         mma_steps(tm + L::O, Rows{sb + L::q}, Cols{sb + L::s}, mma_idesc(VP, false, true), ks, false);
         mma_commit(&bar[L::kMo]);
+        if (more) {  // the next chunk towards L2
+          prefetch_panels((p.K + 63) / 64, &maps.q, 0, gh, (ck + 1) * kTC, b);
+          prefetch_panels((p.K + 63) / 64, &maps.k, 0, gh, (ck + 1) * kTC, b);
+          prefetch_panels((p.V + 63) / 64, &maps.v, 0, h, (ck + 1) * kTC, b);
+        }
       }
+      __syncwarp();
       if (!wait(L::kW, par)) break;
+      if (cut) {  // (the v tile's other readers take its dead rows as zero)
+        zero_rows(sb + L::v, VP / 64, valid, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
       if (lane == 0) {
         tc_fence_after_sync();
 #pragma unroll
@@ -272,12 +282,25 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
         mma_commit(&bar[L::kM1]);
       }
       __syncwarp();
-      if (ck + 1 < cend) {
+      if (more) {
+        if (!wait(L::kMs, par)) break;
+        load_qk(ck + 1);
         if (!wait(L::kM1, par)) break;
-        load(ck + 1);
+        load_v(ck + 1);
       }
     }
-  } else if (warp < kLinWarps) {  // ---- a computing warp
+  } else if (warp > kLinWarps) {  // ---- the decays' warp: a chunk ahead, stored when the chunk before has read its own
+    DecStage ds;
+    ds.g.fetch(p, b, h, c0 * kTC, len, lane);
+    for (int ck = c0; ck < cend; ++ck) {
+      ds.scan(lane);
+      if (ck > c0 && !wait(L::kSc, (uint32_t)(ck - 1 - c0) & 1u)) break;
+      ds.put(dec, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[L::kDc]);
+      ds.g.fetch(p, b, h, (ck + 1) * kTC, len, lane);
+    }
+  } else {  // ---- a computing warp
     const int row = (warp & 3) * 32 + lane, cq = warp >> 2;  // tensor-memory lane and quarter of the columns of this thread
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
     float S[VQ];
@@ -313,7 +336,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
     for (int ck = c0; ck < cend; ++ck) {
       const uint32_t par = (uint32_t)(ck - c0) & 1u;
       const int t0 = ck * kTC, valid = len - t0;
-      if (!wait(L::kLd, par)) break;
+      if (!wait(L::kDc, par) || !wait(L::kLd, par)) break;
       const Dec last = dec.get(kTC - 1), own = dec.get(row);
       const float elast = dec_exp(last);
       {

@@ -16,7 +16,7 @@ namespace ssk {
 constexpr int kTC = kLinChunkBf16;        // tokens of a chunk = rows of a tile
 constexpr int kPanel = kTC * 128;         // bytes of a panel of kTC rows
 constexpr int kTcThreads = 256;
-constexpr int kLinWarps = 16, kLinThreads = 32 * (kLinWarps + 1);  // computing warps, and one that issues
+constexpr int kLinWarps = 16, kLinThreads = 32 * (kLinWarps + 2);  // computing warps, one that issues, one for the decays
 
 // byte offset of 16-byte unit `u` (8 columns) of row r in a tile of kTC rows
 __device__ __forceinline__ uint32_t tile_at(int r, int u) {
@@ -68,9 +68,22 @@ struct DecTile {
 __device__ __forceinline__ Dec dec_sub(Dec a, Dec b) { return dec_add(a, Dec{-b.hi, -b.lo}); }
 __device__ __forceinline__ float dec_exp(Dec d) { return dec_exp(d.hi, d.lo); }
 
-// A chunk's decays into shared memory (one warp).
+// A chunk's decays, in one warp: take() reads the gates ahead and finds the sums
+// in registers, put() stores them once the tile's readers are done.
+struct DecStage {
+  ChunkGates<kTC> g;
+  Dec rel[ChunkGates<kTC>::PER], base;
+  __device__ __forceinline__ void scan(int lane) { base = g.scan_rel(lane, rel); }
+  __device__ __forceinline__ void put(const DecTile& t, int lane) const {
+#pragma unroll
+    for (int e = 0; e < ChunkGates<kTC>::PER; ++e) t.put(lane * ChunkGates<kTC>::PER + e, rel[e]);
+    if (lane < kTC / 32) t.put_base(lane, base);
+  }
+};
 __device__ __forceinline__ void put_decays(const ChunkGates<kTC>& g, const DecTile& t, int lane) {
-  g.scan_rel(lane, [&](int i, Dec r) { t.put(i, r); }, [&](int n, Dec b) { t.put_base(n, b); });
+  DecStage s;
+  s.base = g.scan_rel(lane, s.rel);
+  s.put(t, lane);
 }
 
 // One 128-byte line into L2, ahead of the loads that will want it.
@@ -267,8 +280,8 @@ __device__ __forceinline__ uint4 take_term(float (&x)[8]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     w[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
-    x[2 * e] -= __uint_as_float(w[e] << 16);
-    x[2 * e + 1] -= __uint_as_float(w[e] & 0xffff0000u);
+    x[2 * e] -= bf16_lo(w[e]);
+    x[2 * e + 1] -= bf16_hi(w[e]);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
