@@ -911,11 +911,12 @@ int bwd_bf16(const BwdPlan& pl, const void* dout, const float* ckpt, const float
              cudaStream_t s) {
   const LinAttn& p = pl.p;
   const unsigned grid = (unsigned)p.B * p.H * p.nseg;
+  CUtensorMap mq, md;
+  if (!lin_map(&mq, p.q, p.ldq, p.B, p.L, p.G, p.K) || !lin_map(&md, dout, (long long)p.H * p.V, p.B, p.L, p.H, p.V)) return SS_ERR_CUDA;
   return bwd_run<__nv_bfloat16>(
       pl, dh_last, out, dg, ws, s,
       [&](float* st, Dec* dec, const BwdOut&) {
-        return lin_launch(linattn_sum_tc_kernel<true>, grid * ((p.V + 63) / 64), kTcThreads, SumTc::bytes, s, p, p.q, p.ldq, dout,
-                          (long long)p.H * p.V, st, dec);
+        return lin_launch(linattn_sum_tc_kernel<true>, grid * ((p.V + 63) / 64), kLinThreads, SumTc::bytes, s, p, mq, md, st, dec);
       },
       [&](const float* u0, const BwdOut& o) {
         return lin_launch(linattn_bwd_tc_kernel<VP>, grid, kBwdThreads, BwdTc<VP>::bytes, s, p, dout, ckpt, u0, o);

@@ -503,7 +503,7 @@ int fwd_bf16(const FwdPlan& pl, const float* h0, __nv_bfloat16* o, float* ckpt, 
   return fwd_run(
       pl, h0, ws, s,
       [&](float* st, Dec* dec) {
-        return lin_launch(linattn_sum_tc_kernel<false>, grid * ((p.V + 63) / 64), kTcThreads, SumTc::bytes, s, p, p.k, p.ldk, p.v, p.ldv, st, dec);
+        return lin_launch(linattn_sum_tc_kernel<false>, grid * ((p.V + 63) / 64), kLinThreads, SumTc::bytes, s, p, maps.k, maps.v, st, dec);
       },
       [&](const float* s0) { return lin_launch(linattn_fwd_tc_kernel<VP>, grid, kLinThreads, FwdTc<VP>::bytes, s, p, maps, s0, o, ckpt, h_last); });
 }

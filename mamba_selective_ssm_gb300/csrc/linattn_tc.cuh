@@ -172,12 +172,20 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
                : "memory");
 }
+__device__ __forceinline__ void tmem_ld8u(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
                : "memory");
 }
 __device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
 __device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[8]) { tmem_ld8u(taddr, r); }
+__device__ __forceinline__ void tmem_stn(uint32_t taddr, const uint32_t (&r)[8]) { tmem_st8u(taddr, r); }
 __device__ __forceinline__ void tmem_stn(uint32_t taddr, const uint32_t (&r)[32]) { tmem_st32(taddr, r); }
 __device__ __forceinline__ void tmem_stn(uint32_t taddr, const uint32_t (&r)[16]) { tmem_st16(taddr, r); }
 // N columns of this thread's lane times f, in place (the caller waits for the store)
@@ -320,25 +328,26 @@ __device__ __forceinline__ void lin_leave(bool ok, uint64_t* bar, int nbar, uint
 // The state a segment reaches from zero and its log decay, for both directions:
 //   forward   S = e^{c_last} S + sum_j k_j (e^{c_last-c_j} v_j)^T      chunks in order
 //   REV       U = e^{c_last} U + sum_i q_i (scale e^{c_i} do_i)^T      chunks from the last
-// A CTA takes 64 columns of y (v or do); the weighted rows of y go through the
-// tensor cores as three bf16 terms.
+// A CTA takes 64 columns of y (v or do).  The weighted rows of y, as three bf16
+// terms side by side, are one product of 192 columns, so that x is read once;
+// every tile has two places, and a chunk's weights are under the product before.
 struct SumTc {
-  static constexpr int x = 0, y = x + 2 * kPanel, w = y + kPanel, dec = w + 3 * kPanel, bar = dec + DecTile::bytes, tm = bar + 8,
-                       bytes = tm + 8;
-  static constexpr int cols = 64;
+  static constexpr int x = 0, y = x + 4 * kPanel, w = y + 2 * kPanel, dec = w + 6 * kPanel, bar = dec + 2 * ((DecTile::bytes + 15) / 16 * 16);
+  // barriers, two each: tiles landed, decays stored, product done, terms stored
+  static constexpr int kLd = 0, kDc = 2, kM = 4, kW = 6, nbar = 8;
+  static constexpr int tm = bar + nbar * 8, bytes = tm + 8, cols = 512;
 };
 
 template <bool REV>
-__global__ void __launch_bounds__(kTcThreads, 2) linattn_sum_tc_kernel(LinAttn p, const __nv_bfloat16* __restrict__ xs, long long ldx,
-                                                                      const __nv_bfloat16* __restrict__ ys, long long ldy,
-                                                                      float* __restrict__ send, Dec* __restrict__ sdec) {
+__global__ void __launch_bounds__(kLinThreads, 1) linattn_sum_tc_kernel(LinAttn p, const __grid_constant__ CUtensorMap mx,
+                                                                        const __grid_constant__ CUtensorMap my,
+                                                                        float* __restrict__ send, Dec* __restrict__ sdec) {
   using L = SumTc;
   extern __shared__ __align__(1024) unsigned char raw[];
   const uint32_t sb = smem_u32(raw);
-  const DecTile dec{sb + L::dec};
   uint64_t* bar = reinterpret_cast<uint64_t*>(raw + L::bar);
   uint32_t* tma = reinterpret_cast<uint32_t*>(raw + L::tm);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = (warp & 3) * 32 + lane, half = warp >> 2;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nvt = (p.V + 63) / 64;
   long long id = blockIdx.x;
   const int seg = (int)(id % p.nseg);
@@ -348,10 +357,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_sum_tc_kernel(LinAttn p
   const int h = (int)(id % p.H), b = (int)(id / p.H), gh = h / (p.H / p.G), v0 = vt * 64, vw = p.V - v0 < 64 ? p.V - v0 : 64;
   const int len = p.len(b);
   const long long bh = (long long)b * p.H + h;
-  xs += (long long)b * p.L * ldx + (long long)gh * p.K;
-  ys += (long long)b * p.L * ldy + (long long)h * p.V + v0;
+  const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
+  int cend = (len + kTC - 1) / kTC;
+  cend = cend < c0 ? c0 : cend < c1 ? cend : c1;
+  const int n = cend - c0;
+  auto chunk = [&](int i) { return REV ? cend - 1 - i : c0 + i; };  // the i-th chunk walked
   if (tid == 0) {
-    mbar_init(bar, 1);
+    for (int i = 0; i < L::nbar; ++i) mbar_init(&bar[i], i >= L::kW ? kLinWarps : 1);
     fence_barrier_init();
   }
   if (warp == 0) {
@@ -361,94 +373,116 @@ __global__ void __launch_bounds__(kTcThreads, 2) linattn_sum_tc_kernel(LinAttn p
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tm = *tma, tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
-  float S[32];
-#pragma unroll
-  for (int e = 0; e < 32; ++e) S[e] = 0.f;
-  const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
-  int cend = (len + kTC - 1) / kTC;
-  cend = cend < c0 ? c0 : cend < c1 ? cend : c1;
-  ChunkGates<kTC> gates;
-  auto load = [&](int ck) {
-    const int m = len - ck * kTC, n = m < kTC ? m : kTC;
-    const long long t0 = (long long)ck * kTC;
-    load_tile_tc<16, kTcThreads>(xs + t0 * ldx, ldx, n, p.K, sb + L::x, tid);
-    load_tile_tc<8, kTcThreads>(ys + t0 * ldy, ldy, n, vw, sb + L::y, tid);
-    if (warp == 0) {
-      put_decays(gates, dec, lane);
-      gates.fetch(p, b, h, (REV ? ck - 1 : ck + 1) * kTC, len, lane);
-    }
-    const int nx = REV ? ck - 1 : ck + 1;  // the chunk after it
-    if (nx >= c0 && nx < cend) {
-      const int left = len - nx * kTC;
-      prefetch_rows(xs + (long long)nx * kTC * ldx, ldx, left, p.K, tid);
-      if (!(tid & 1)) prefetch_rows(ys + (long long)nx * kTC * ldy, ldy, left, vw, tid);
-    }
-  };
-  Dec total = {0.f, 0.f};
-  uint32_t phase = 0;
+  const uint32_t tm = *tma;
   bool ok = true;
-  if (c0 < cend) {
-    if (warp == 0) gates.fetch(p, b, h, (REV ? cend - 1 : c0) * kTC, len, lane);
-    load(REV ? cend - 1 : c0);
-  }
-  for (int n = 0; n < cend - c0; ++n) {
-    const int ck = REV ? cend - 1 - n : c0 + n;
-    cp_wait_all();
-    __syncthreads();
-    const Dec last = dec.get(kTC - 1);
-    const float elast = dec_exp(last);
-    total = dec_add(total, last);
-    const int r = tid >> 1, u0 = (tid & 1) * 4;
-    const Dec dr = dec.get(r);
-    const float w = REV ? p.scale * dec_exp(dr) : dec_exp(dec_sub(last, dr));
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t at = tile_at(r, u0 + u);
-      float x[8];
-      Raw8<__nv_bfloat16>::wide(lds16(sb + L::y + at), x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= w;
-      sts16(sb + L::w + at, take_term(x));
-      sts16(sb + L::w + kPanel + at, take_term(x));
-      sts16(sb + L::w + 2 * kPanel + at, take_term(x));
+  // barrier pair `i` for its place's turn m: the places take turns, so place m & 1 is at phase (m >> 1) & 1
+  auto wait = [&](int i, int m) { return ok = mbar_wait_bounded(&bar[i + (m & 1)], (uint32_t)(m >> 1) & 1u, kWaitLimitNs); };
+
+  if (warp == kLinWarps) {  // ---- the issuing warp
+    auto load = [&](int i) {
+      if (lane == 0) {
+        uint64_t* bl = &bar[L::kLd + (i & 1)];
+        mbar_arrive_expect_tx(bl, 3 * kPanel);
+        load_panels(sb + L::x + (i & 1) * 2 * kPanel, 2, &mx, bl, 0, gh, chunk(i) * kTC, b);
+        load_panels(sb + L::y + (i & 1) * kPanel, 1, &my, bl, v0, h, chunk(i) * kTC, b);
+      }
+      __syncwarp();
+    };
+    if (n > 0) load(0);
+    if (n > 1) load(1);
+    for (int i = 0; i < n; ++i) {
+      const uint32_t x = sb + L::x + (i & 1) * 2 * kPanel;
+      if (!wait(L::kLd, i)) break;
+      const int valid = len - chunk(i) * kTC;
+      if (valid < kTC && chunk(i) * kTC + valid < p.L) {  // the row ends inside the tensor (y's readers take dead rows as zero)
+        zero_rows(x, 2, valid, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (!wait(L::kW, i)) break;
+      if (lane == 0) {
+        tc_fence_after_sync();
+        mma_steps(tm + (i & 1) * 256, Cols{x}, Cols{sb + L::w + (i & 1) * 3 * kPanel}, mma_idesc(192, true, true), kTC / 16, false);
+        mma_commit(&bar[L::kM + (i & 1)]);
+      }
+      __syncwarp();
+      if (i + 2 < n) {
+        if (!wait(L::kM, i)) break;
+        load(i + 2);
+      }
     }
-    fence_proxy_async_smem();
-    tc_fence_before_sync();
-    __syncthreads();
-    if (tid == 0) {
+  } else if (warp > kLinWarps) {  // ---- the decays' warp
+    DecStage ds;
+    Dec total = {0.f, 0.f};
+    if (n > 0) ds.g.fetch(p, b, h, chunk(0) * kTC, len, lane);
+    for (int i = 0; i < n; ++i) {
+      ds.scan(lane);
+      if (i + 1 < n) ds.g.fetch(p, b, h, chunk(i + 1) * kTC, len, lane);
+      if (i > 1 && !wait(L::kM, i - 2)) break;  // its readers had stored their terms
+      const DecTile dec{sb + L::dec + (i & 1) * ((DecTile::bytes + 15) / 16 * 16)};
+      ds.put(dec, lane);
+      __syncwarp();
+      total = dec_add(total, dec.get(kTC - 1));
+      if (lane == 0) mbar_arrive(&bar[L::kDc + (i & 1)]);
+    }
+    if (lane == 0 && vt == 0) sdec[bh * p.nseg + seg] = total;
+  } else {  // ---- a computing warp
+    const int row = (warp & 3) * 32 + lane, cq = warp >> 2;
+    const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    float S[16], elast = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) S[e] = 0.f;
+    auto add = [&](int i, float f) {  // S = f S + the product of chunk i
+      uint32_t a[16], c[16], d[16];
+      tmem_ld16(tl + (i & 1) * 256 + cq * 16, a);
+      tmem_ld16(tl + (i & 1) * 256 + 64 + cq * 16, c);
+      tmem_ld16(tl + (i & 1) * 256 + 128 + cq * 16, d);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        S[e] = fmaf(S[e], f, __uint_as_float(a[e]) + (__uint_as_float(c[e]) + __uint_as_float(d[e])));
+    };
+    for (int i = 0; i < n; ++i) {
+      if (!wait(L::kDc, i) || !wait(L::kLd, i)) break;
+      const DecTile dec{sb + L::dec + (i & 1) * ((DecTile::bytes + 15) / 16 * 16)};
+      const Dec last = dec.get(kTC - 1), own = dec.get(row);
+      const float w = REV ? p.scale * dec_exp(own) : dec_exp(dec_sub(last, own));
+      const bool live = row < len - chunk(i) * kTC;
+      const uint32_t wt = sb + L::w + (i & 1) * 3 * kPanel;  // read by product i - 2, whose sum has been taken
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t at = tile_at(row, cq * 2 + u);
+        float x[8];
+        Raw8<__nv_bfloat16>::wide(live ? lds16(sb + L::y + (i & 1) * kPanel + at) : make_uint4(0u, 0u, 0u, 0u), x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= w;
+        sts16(wt + at, take_term(x));
+        sts16(wt + kPanel + at, take_term(x));
+        sts16(wt + 2 * kPanel + at, last_term(x));
+      }
+      fence_proxy_async_smem();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[L::kW + (i & 1)]);
+      if (i > 0) {  // the product before, under this one
+        if (!wait(L::kM, i - 1)) break;
+        tc_fence_after_sync();
+        add(i - 1, elast);
+      }
+      elast = dec_exp(last);
+    }
+    if (ok && n > 0 && wait(L::kM, n - 1)) {
       tc_fence_after_sync();
-#pragma unroll
-      for (int t = 2; t >= 0; --t)  // the smallest term first
-        mma_steps(tm, Cols{sb + L::x}, Cols{sb + L::w + t * kPanel}, mma_idesc(64, true, true), kTC / 16, t < 2);
-      mma_commit(bar);
+      add(n - 1, elast);
     }
-    ok = mbar_wait_bounded(bar, phase, kWaitLimitNs);
-    phase ^= 1;
-    if (__syncthreads_or(!ok)) break;
-    tc_fence_after_sync();
-    if (n + 1 < cend - c0) load(REV ? ck - 1 : ck + 1);
-    uint32_t a[32];
-    tmem_ld32(tl + half * 32, a);
-    tmem_wait_ld();
+    if (row < p.K) {
+      float* dst = send + ((bh * p.nseg + seg) * p.K + row) * p.V + v0 + cq * 16;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) S[e] = fmaf(S[e], elast, __uint_as_float(a[e]));
+      for (int e = 0; e < 16; e += 4)
+        if (cq * 16 + e < vw) *reinterpret_cast<float4*>(dst + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+    }
   }
-  if (!ok) {  // a wait ran out: say so; the outputs are invalid
-    if (tid == 0) atomicOr(&g_lin_err, kErrTmaTimeout);
-    mbar_wait_bounded(bar, phase ^ 1, 100000000ull);
-    cp_wait_all();
-  }
-  if (row < p.K) {
-    float* dst = send + ((bh * p.nseg + seg) * p.K + row) * p.V + v0 + half * 32;
-#pragma unroll
-    for (int e = 0; e < 32; e += 4)
-      if (half * 32 + e < vw) *reinterpret_cast<float4*>(dst + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
-  }
-  if (tid == 0 && vt == 0) sdec[bh * p.nseg + seg] = total;
-  tc_fence_before_sync();
-  __syncthreads();
-  if (warp == 0) tmem_dealloc(tm, L::cols);
+  lin_leave(ok, bar, L::nbar, tm, L::cols, warp, lane);
 }
 
 // In place over the segments of a (batch row, head), in walking order: the
