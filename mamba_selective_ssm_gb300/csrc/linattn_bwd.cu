@@ -265,17 +265,19 @@ __global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const float
         for (int w = 0; w < 8; ++w) through += sm.red[w];
         through *= dec_exp(chi, clo);
         const float a0 = sm.a[2 * tid], a1 = sm.a[2 * tid + 1], b0 = sm.b[2 * tid], b1 = sm.b[2 * tid + 1];
-        double sa = (double)a0 + a1, sb = (double)b0 + b1;
-        const double sb_own = sb;
+        float sa = a0 + a1, sb = b0 + b1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const double ua = __shfl_down_sync(0xffffffffu, sa, o), ub = __shfl_up_sync(0xffffffffu, sb, o);
+          const float ua = __shfl_down_sync(0xffffffffu, sa, o), ub = __shfl_up_sync(0xffffffffu, sb, o);
           if (tid + o < 32) sa += ua;
           if (tid >= o) sb += ub;
         }
-        const double before = sb - sb_own;
-        float g0 = (float)(sa + before + through + sm.rect[2 * tid]);
-        float g1 = (float)((sa - a0) + (before + b0) + through + sm.rect[2 * tid + 1]);
+        // sums over the tokens after this lane's two, and before them
+        float after = __shfl_down_sync(0xffffffffu, sa, 1), before = __shfl_up_sync(0xffffffffu, sb, 1);
+        if (tid == 31) after = 0.f;
+        if (tid == 0) before = 0.f;
+        const float g0 = (after + (a0 + a1)) + before + through + sm.rect[2 * tid];
+        const float g1 = (after + a1) + (before + b0) + through + sm.rect[2 * tid + 1];
         if (p.g_head) {
           float s = (2 * tid < valid ? g0 : 0.f) + (2 * tid + 1 < valid ? g1 : 0.f);
 #pragma unroll
@@ -312,11 +314,11 @@ __global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const float
 }
 
 // ---------------------------------------------------------------- bf16: tensor cores
-// One CTA of 16 warps walks the chunks (128 tokens) of a (batch row, head,
-// segment) from the last to the first.  U stays in registers in fp32 (thread =
-// row d of K and a quarter of the V columns).  Scores are taken transposed
-// (tensor-memory lane = key token j), so that P^T and dP^T are A operands where
-// they are made, and one shared-memory copy of dP^T serves dq.
+// A CTA walks the chunks (128 tokens) of a (batch row, head, segment) from the
+// last to the first.  U stays in registers in fp32 (thread = row d of K and a
+// quarter of the V columns).  Scores are taken transposed (tensor-memory lane =
+// key token j), so that P^T and dP^T are A operands where they are made, and one
+// shared-memory copy of dP^T serves dq.
 //   T0 = k q^T, T1 = v do^T                            -> P^T, dP^T (bf16), M for dg
 //   T2 = do S_in^T (three terms)                       -> * scale e^{c_i}, dotted with q for dg
 //   T0 = k U (one term), T1 = v U^T (three terms)      -> * e^{c_last-c_j}, T1 dotted with k for dg
@@ -324,22 +326,36 @@ __global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const float
 //   T3 = q^T (scale e^{c_i} do) (three terms)          -> U
 // What ends in fp32 (dg, dh0, U) takes its fp32 operands as three bf16 terms;
 // a term of dq, dk or dv is rounded to bf16 once on its way.
-constexpr int kBwdThreads = 512;
-
+//
+// Sixteen warps compute, one issues the TMA loads and the MMAs, one finds the
+// decays; they meet at mbarriers, as in the forward.
 template <int VP>
 struct BwdTc {
   static constexpr int vt = kTC * VP * 2;  // bytes of a tile VP columns wide
-  static constexpr int q = 0, k = q + 2 * kPanel, x = k + 2 * kPanel, v = x + 2 * kPanel, d = v + vt, y0 = d + vt, y1 = y0 + vt, dec = y1 + vt;
-  static constexpr int bar = dec + DecTile::bytes, tm = bar + 16, hsum = tm + 8, into = hsum + 16, bytes = into + kTC * 4;
-  // in x while it is free: parts of dg
-  static constexpr int a = x, b = a + 4 * kTC * 4, rect = b + 4 * kTC * 4, tot = rect + 4 * kTC * 4, thr = tot + 4 * kTC * 4;
+  static constexpr int q = 0, k = q + 2 * kPanel, x = k + 2 * kPanel, v = x + 2 * kPanel, d = v + vt, y0 = d + vt, y1 = y0 + vt;
+  // the third term of a state: a tile of its own, or x, which is free then
+  static constexpr int y2 = VP == 64 ? y1 + vt : x, dec = VP == 64 ? y2 + vt : y1 + vt;
+  // scale e^{c_i - c of the end of the block of 32 before}; column sums of M by (quarter, block of rows up to it); <S_in, U> by
+  // warp; dg of a chunk by quarter
+  static constexpr int into = dec + DecTile::bytes, rect = into + kTC * 4, thr = rect + 10 * 32 * 4, hsum = thr + kLinWarps * 4;
+  // barriers: tiles landed, decays stored; MMA groups done; S terms, U terms and scores, last operands stored; outputs out;
+  // U read
+  static constexpr int kLd = 0, kDc = 1, kM0 = 2, kM1 = 3, kM2 = 4, kM3 = 5, kM4 = 6, kR1 = 7, kR3 = 8, kR4 = 9, kR5 = 10, kR6 = 11, nbar = 12;
+  static constexpr int bar = hsum + 64, tm = bar + nbar * 8, bytes = tm + 8;
+  static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
   static constexpr int T0 = 0, T1 = 128, T2 = 256, T3 = 384, Pb = 384, dPb = 448, cols = 512;
 };
 
-// lane l gets the sum over the warp's lanes of x[l]
-__device__ __forceinline__ float col_sums32(float (&x)[32], int lane) {
+struct BwdMaps {
+  CUtensorMap q, k, v, d;
+};
+
+// the sum over the warp's lanes of x[l & 15], in lane l
+__device__ __forceinline__ float col_sums16(float (&x)[16], int lane) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int e = 0; e < 16; ++e) x[e] += __shfl_xor_sync(0xffffffffu, x[e], 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int e = 0; e < o; ++e) {
@@ -351,7 +367,7 @@ __device__ __forceinline__ float col_sums32(float (&x)[32], int lane) {
 }
 
 template <int VP>
-__global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn p, const __nv_bfloat16* __restrict__ dout,
+__global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn p, const __grid_constant__ BwdMaps maps,
                                                                        const float* __restrict__ ckpt,
                                                                        const float* __restrict__ u0, BwdOut out) {
   using L = BwdTc<VP>;
@@ -361,28 +377,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
   const DecTile dec{sb + L::dec};
   uint64_t* bar = reinterpret_cast<uint64_t*>(raw + L::bar);
   uint32_t* tma = reinterpret_cast<uint32_t*>(raw + L::tm);
-  float* into_block = reinterpret_cast<float*>(raw + L::into);  // scale e^{c_i - c of the end of the block of 32 before}
-  float* hsum = reinterpret_cast<float*>(raw + L::hsum);  // dg of a chunk, by quarter of its tokens
+  float* into_block = reinterpret_cast<float*>(raw + L::into);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // the MMAs' issuing thread: warp 3 has no score to scale (its key tokens come after its query tokens); the decays'
-  // warp: not one of those that sum dg
-  constexpr int kIssue = 96, kScan = 15;
-  const int row = (warp & 3) * 32 + lane, cq = warp >> 2;  // tensor-memory lane, quarter of the columns
   long long id = blockIdx.x;
   const int seg = (int)(id % p.nseg);
   id /= p.nseg;
-  const int h = (int)(id % p.H), b = (int)(id / p.H);
-  const int gh = h / (p.H / p.G);
+  const int h = (int)(id % p.H), b = (int)(id / p.H), gh = h / (p.H / p.G);
   const int len = p.len(b);
-  const long long bh = (long long)b * p.H + h, kv = (long long)p.K * p.V, ldo = (long long)p.H * p.V;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (long long)b * p.L * p.ldq + (long long)gh * p.K;
-  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.k) + (long long)b * p.L * p.ldk + (long long)gh * p.K;
-  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + (long long)b * p.L * p.ldv + (long long)h * p.V;
-  const __nv_bfloat16* d = dout + (long long)b * p.L * ldo + (long long)h * p.V;
+  const long long bh = (long long)b * p.H + h, kv = (long long)p.K * p.V;
+  const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
+  int cend = (len + kTC - 1) / kTC;
+  cend = cend < c0 ? c0 : cend < c1 ? cend : c1;
 
   if (tid == 0) {
-    mbar_init(&bar[0], 1);
-    mbar_init(&bar[1], 1);
+    for (int i = 0; i < L::nbar; ++i) mbar_init(&bar[i], i >= L::kR1 ? kLinWarps : 1);
     fence_barrier_init();
   }
   if (warp == 0) {
@@ -393,443 +401,495 @@ __global__ void __launch_bounds__(kBwdThreads, 1) linattn_bwd_tc_kernel(LinAttn 
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tm = *tma;
-  const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
-  const int ks = (p.K + 15) / 16, vs = (p.V + 15) / 16;  // contraction steps over K and V
+  bool ok = true;
+  auto wait = [&](int i, uint32_t par) { return ok = mbar_wait_bounded(&bar[i], par, kWaitLimitNs); };
 
-  float U[VQ];
-#pragma unroll
-  for (int e = 0; e < VQ; ++e) U[e] = 0.f;
-  if (u0 != nullptr && row < p.K) {
-    const float* src = u0 + ((p.nseg > 1 ? bh * p.nseg + seg : bh) * p.K + row) * p.V + cq * VQ;
-#pragma unroll
-    for (int e = 0; e < VQ; e += 4)
-      if (cq * VQ + e < p.V) {
-        const float4 x = *reinterpret_cast<const float4*>(src + e);
-        U[e] = x.x; U[e + 1] = x.y; U[e + 2] = x.z; U[e + 3] = x.w;
+  if (warp == kLinWarps) {  // ---- the issuing warp
+    const int ks = (p.K + 15) / 16, vs = (p.V + 15) / 16;  // contraction steps over K and V
+    const uint32_t id128 = mma_idesc(128, false, false);
+    // a chunk's tiles; their readers have passed a barrier that this warp has waited for, with a proxy fence before it
+    auto load = [&](int ck) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bar[L::kLd], 4 * kPanel + 2 * L::vt);
+        load_panels(sb + L::q, 2, &maps.q, &bar[L::kLd], 0, gh, ck * kTC, b);
+        load_panels(sb + L::k, 2, &maps.k, &bar[L::kLd], 0, gh, ck * kTC, b);
+        load_panels(sb + L::v, VP / 64, &maps.v, &bar[L::kLd], 0, h, ck * kTC, b);
+        load_panels(sb + L::d, VP / 64, &maps.d, &bar[L::kLd], 0, h, ck * kTC, b);
       }
-  }
-  auto valid_of = [&](int ck) { const int n = len - ck * kTC; return n < 0 ? 0 : n < kTC ? n : kTC; };
-  auto load_k = [&](int ck) {
-    load_tile_tc<16, kBwdThreads>(k + (long long)ck * kTC * p.ldk, p.ldk, valid_of(ck), p.K, sb + L::k, tid);
-  };
-  ChunkGates<kTC> gates;
-  auto load_rest = [&](int ck) {
-    const int n = valid_of(ck);
-    const long long t0 = (long long)ck * kTC;
-    load_tile_tc<16, kBwdThreads>(q + t0 * p.ldq, p.ldq, n, p.K, sb + L::q, tid);
-    load_tile_tc<VP / 8, kBwdThreads>(d + t0 * ldo, ldo, n, p.V, sb + L::d, tid);
-    load_tile_tc<VP / 8, kBwdThreads>(v + t0 * p.ldv, p.ldv, n, p.V, sb + L::v, tid);
-    if (warp == kScan) {
-      put_decays(gates, dec, lane);
+      __syncwarp();
+    };
+    if (c0 < cend) load(cend - 1);
+    for (int ck = cend - 1; ck >= c0; --ck) {
+      const uint32_t par = (uint32_t)(cend - 1 - ck) & 1u;
+      const int valid = len - ck * kTC;
+      if (!wait(L::kLd, par)) break;
+      if (valid < kTC && ck * kTC + valid < p.L) {  // the row ends inside the tensor: what follows is not its own
+        zero_rows(sb + L::q, 4, valid, lane);         // (the tiles' other readers take dead rows as zero)
+        zero_rows(sb + L::v, 2 * VP / 64, valid, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (ck < cend - 1 && !wait(L::kR6, par ^ 1u)) break;  // U's place takes scores next
+      if (lane == 0) {
+        tc_fence_after_sync();
+        mma_steps(tm + L::T0, Rows{sb + L::k}, Rows{sb + L::q}, id128, ks, false);
+        mma_steps(tm + L::T1, Rows{sb + L::v}, Rows{sb + L::d}, id128, vs, false);
+        mma_commit(&bar[L::kM0]);
+        if (ck > c0) {  // the next chunk towards L2
+          prefetch_panels((p.K + 63) / 64, &maps.q, 0, gh, (ck - 1) * kTC, b);
+          prefetch_panels((p.K + 63) / 64, &maps.k, 0, gh, (ck - 1) * kTC, b);
+          prefetch_panels((p.V + 63) / 64, &maps.v, 0, h, (ck - 1) * kTC, b);
+          prefetch_panels((p.V + 63) / 64, &maps.d, 0, h, (ck - 1) * kTC, b);
+        }
+      }
+      __syncwarp();
+      if (!wait(L::kR1, par)) break;
+      if (lane == 0) {
+        tc_fence_after_sync();
+#pragma unroll
+        for (int t = 2; t >= 0; --t)  // the smallest term first
+          mma_steps(tm + L::T2, Rows{sb + L::d}, Rows{sb + (t == 0 ? L::y0 : t == 1 ? L::y1 : L::y2)}, id128, vs, t < 2);
+        mma_commit(&bar[L::kM1]);
+      }
+      __syncwarp();
+      if (!wait(L::kR3, par)) break;
+      if (lane == 0) {
+        tc_fence_after_sync();
+        mma_steps(tm + L::T0, Rows{sb + L::k}, Cols{sb + L::y0}, mma_idesc(VP, false, true), ks, false);
+#pragma unroll
+        for (int t = 2; t >= 0; --t)
+          mma_steps(tm + L::T1, Rows{sb + L::v}, Rows{sb + (t == 0 ? L::y0 : t == 1 ? L::y1 : L::y2)}, id128, vs, t < 2);
+        mma_commit(&bar[L::kM2]);
+      }
+      __syncwarp();
+      if (!wait(L::kR4, par)) break;
+      if (lane == 0) {
+        tc_fence_after_sync();
+#pragma unroll
+        for (int s = 0; s < kTC / 16; ++s) mma_ts(tm + L::T0, tm + L::Pb + s * 8, desc_cols(sb + L::d, s), mma_idesc(VP, false, true), true);
+#pragma unroll
+        for (int s = 0; s < kTC / 16; ++s) mma_ts(tm + L::T1, tm + L::dPb + s * 8, desc_cols(sb + L::q, s), mma_idesc(128, false, true), true);
+        mma_steps(tm + L::T2, Cols{sb + L::x}, Cols{sb + L::k}, mma_idesc(128, true, true), kTC / 16, true);
+        mma_commit(&bar[L::kM3]);
+      }
+      __syncwarp();
+      if (!wait(L::kM3, par)) break;
+      if (lane == 0) {  // into the scores' place, whose readers are done
+        tc_fence_after_sync();
+#pragma unroll
+        for (int t = 2; t >= 0; --t)
+          mma_steps(tm + L::T3, Cols{sb + L::q}, Cols{sb + (t == 0 ? L::y0 : t == 1 ? L::y1 : L::v)}, mma_idesc(VP, true, true), kTC / 16, t < 2);
+        mma_commit(&bar[L::kM4]);
+      }
+      __syncwarp();
+      if (ck > c0) {
+        if (!wait(L::kR5, par) || !wait(L::kM4, par)) break;
+        load(ck - 1);
+      }
+    }
+  } else if (warp > kLinWarps) {  // ---- the decays' warp
+    DecStage ds;
+    ds.g.fetch(p, b, h, (cend - 1) * kTC, len, lane);
+    for (int ck = cend - 1; ck >= c0; --ck) {
+      ds.scan(lane);
+      if (ck < cend - 1 && !wait(L::kR3, (uint32_t)(cend - 2 - ck) & 1u)) break;  // the chunk before is done with its own
+      ds.put(dec, lane);
       __syncwarp();
 #pragma unroll
       for (int e = 0; e < kTC; e += 32) into_block[e + lane] = p.scale * dec_exp(dec.rel(e + lane));
-      gates.fetch(p, b, h, (ck - 1) * kTC, len, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[L::kDc]);
+      if (ck > c0) {
+        ds.g.fetch(p, b, h, (ck - 1) * kTC, len, lane);
+        const float* c = ckpt + (bh * p.nck + ck - 1) * kv;
+        for (long long i = lane * 32; i < kv; i += 32 * 32) prefetch_l2(c + i);
+      }
     }
-  };
-  // 32 gradients of q or k of this thread's token (columns cq * 32 ...) as this head's fp32 part
-  auto put_part = [&](float* part, int t0, const uint32_t (&r)[32], bool live) {
-    if (t0 + row >= p.L) return;
-    const long long at = (((long long)b * p.L + t0 + row) * p.H + h) * p.K + cq * 32;
+  } else {  // ---- a computing warp
+    const int row = (warp & 3) * 32 + lane, cq = warp >> 2;  // tensor-memory lane, quarter of the columns
+    const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    float* rect = reinterpret_cast<float*>(raw + L::rect);
+    float* thr = reinterpret_cast<float*>(raw + L::thr);
+    float U[VQ];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (cq * 32 + u * 8 >= p.K) continue;
-      float x[8];
+    for (int e = 0; e < VQ; ++e) U[e] = 0.f;
+    if (u0 != nullptr && row < p.K) {
+      const float* src = u0 + ((p.nseg > 1 ? bh * p.nseg + seg : bh) * p.K + row) * p.V + cq * VQ;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = live ? __uint_as_float(r[8 * u + e]) : 0.f;
-      ActT<float>::st8(part + at + 8 * u, x);
+      for (int e = 0; e < VQ; e += 4)
+        if (cq * VQ + e < p.V) {
+          const float4 x = *reinterpret_cast<const float4*>(src + e);
+          U[e] = x.x; U[e + 1] = x.y; U[e + 2] = x.z; U[e + 3] = x.w;
+        }
     }
-  };
-  // the three terms of a [K][V] fp32 state, this thread's row and quarter
-  auto put_terms = [&](const float (&s)[VQ], uint32_t t0, uint32_t t1, uint32_t t2) {
-#pragma unroll
-    for (int u = 0; u < NU; ++u) {
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = s[8 * u + e];
-      const uint32_t at = tile_at(row, cq * NU + u);
-      sts16(sb + t0 + at, take_term(x));
-      sts16(sb + t1 + at, take_term(x));
-      sts16(sb + t2 + at, take_term(x));
-    }
-  };
-
-  const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
-  int cend = (len + kTC - 1) / kTC;
-  cend = cend < c0 ? c0 : cend < c1 ? cend : c1;
-  for (int ck = cend; ck < c1; ++ck) {  // past the row's end
-    const int rows = p.L - ck * kTC < kTC ? p.L - ck * kTC : kTC;
-    const long long at = ((long long)b * p.L + ck * kTC) * p.H + h;
-    auto clear = [&](void* dst, int width, int esize) {  // rows of `width` elements, H rows apart
-      const int n = width * esize / 16;
-      uint4* to = reinterpret_cast<uint4*>(static_cast<char*>(dst) + at * width * esize);
-      for (int i = tid; i < rows * n; i += kBwdThreads) to[(long long)(i / n) * p.H * n + i % n] = make_uint4(0u, 0u, 0u, 0u);
+    auto arrive = [&](int i) {  // this warp's shared- and tensor-memory accesses before are over
+      fence_proxy_async_smem();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[i]);
     };
-    clear(out.dqp != nullptr ? static_cast<void*>(out.dqp) : out.dq, p.K, out.dqp != nullptr ? 4 : 2);
-    clear(out.dkp != nullptr ? static_cast<void*>(out.dkp) : out.dk, p.K, out.dkp != nullptr ? 4 : 2);
-    clear(out.dv, p.V, 2);
-    if (p.g_head) {
-      if (tid == 0) out.dg[((long long)b * p.nck + ck) * p.H + h] = 0.f;
-    } else if (tid < rows) {
-      out.dg[((long long)b * p.L + ck * kTC + tid) * p.H + h] = 0.f;
-    }
-  }
-  uint32_t ph0 = 0, ph1 = 0;
-  bool ok = true;
-  auto wait0 = [&]() { ok = mbar_wait_bounded(&bar[0], ph0, kWaitLimitNs); ph0 ^= 1; };
-  auto wait1 = [&]() { ok = mbar_wait_bounded(&bar[1], ph1, kWaitLimitNs); ph1 ^= 1; };
-  if (c0 < cend) {
-    if (warp == kScan) gates.fetch(p, b, h, (cend - 1) * kTC, len, lane);
-    load_k(cend - 1);
-    load_rest(cend - 1);
-  }
-  for (int ck = cend - 1; ck >= c0; --ck) {
-    const int t0 = ck * kTC, valid = valid_of(ck);
-    float through = 0.f;  // <S_in, U>, this thread's part
-    {
-      float S[VQ];
+    // 32 gradients of q or k of this thread's token (columns cq * 32 ...) as this head's fp32 part, [K/4][token][4]
+    auto put_part = [&](float* part, int ck, const uint32_t (&r)[32], bool live) {
+      float4* dst = reinterpret_cast<float4*>(part) + (((long long)b * p.nck + ck) * p.H + h) * (p.K / 4) * kTC + row;
 #pragma unroll
-      for (int e = 0; e < VQ; e += 4) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (row < p.K && cq * VQ + e < p.V)
-          x = *(reinterpret_cast<const float4*>(ckpt + (bh * p.nck + ck) * kv) + (long long)((cq * VQ + e) / 4) * p.K + row);
-        S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
+      for (int u = 0; u < 8; ++u) {
+        if (cq * 32 + u * 4 >= p.K) continue;
+        dst[(cq * 8 + u) * kTC] = live ? make_float4(__uint_as_float(r[4 * u]), __uint_as_float(r[4 * u + 1]), __uint_as_float(r[4 * u + 2]),
+                                                     __uint_as_float(r[4 * u + 3]))
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-#pragma unroll
-      for (int e = 0; e < VQ; ++e) through = fmaf(S[e], U[e], through);
-      put_terms(S, L::y0, L::y1, L::x);
-    }
-    cp_wait_all();
-    fence_proxy_async_smem();
-    tc_fence_before_sync();
-    __syncthreads();
-    if (tid == kIssue) {
-      tc_fence_after_sync();
-      const uint32_t id128 = mma_idesc(128, false, false);
-      mma_steps(tm + L::T0, Rows{sb + L::k}, Rows{sb + L::q}, id128, ks, false);
-      mma_steps(tm + L::T1, Rows{sb + L::v}, Rows{sb + L::d}, id128, vs, false);
-      mma_commit(&bar[0]);
-#pragma unroll
-      for (int t = 2; t >= 0; --t)  // the smallest term first
-        mma_steps(tm + L::T2, Rows{sb + L::d}, Rows{sb + (t == 0 ? L::y0 : t == 1 ? L::y1 : L::x)}, id128, vs, t < 2);
-      mma_commit(&bar[1]);
-    }
-    const Dec last = dec.get(kTC - 1), own = dec.get(row);
-    const float elast = dec_exp(last), into = p.scale * dec_exp(own), rest = dec_exp(dec_sub(last, own));
-    if (ck > c0) {  // the chunk before it towards L2
-      const long long n0 = t0 - kTC;
-      const int half = tid >> 8, lt = tid & 255;
-      const float* c = ckpt + (bh * p.nck + ck - 1) * kv;
-      if (half) {
-        prefetch_rows(q + n0 * p.ldq, p.ldq, kTC, p.K, lt);
-        prefetch_rows(k + n0 * p.ldk, p.ldk, kTC, p.K, lt);
-      } else {
-        prefetch_rows(v + n0 * p.ldv, p.ldv, kTC, p.V, lt);
-        prefetch_rows(d + n0 * ldo, ldo, kTC, p.V, lt);
-      }
-      if (tid * 32 < kv) prefetch_l2(c + tid * 32);
-    }
-    wait0();
-    if (__syncthreads_or(!ok)) break;
-    tc_fence_after_sync();
-    float rect = 0.f, tot = 0.f;
-    if (cq >= (warp & 3)) {  // query tokens of this quarter at or after this warp's key tokens
-      float m[32];
-      const bool diag = cq == (warp & 3);
-      const float from = diag ? 0.f : dec_exp(dec_sub(dec.base(cq), own));  // off the diagonal a decay is a product of two
-      const Dec orel = dec.rel(row);
-#pragma unroll
-      for (int g = 1; g >= 0; --g) {
-        const int i0 = cq * 32 + g * 16;
-        uint32_t s[16], t[16], w[8], z[8];
-        tmem_ld16(tl + L::T0 + i0, s);
-        tmem_ld16(tl + L::T1 + i0, t);
-        tmem_wait_ld();
-        if (!diag) {
-#pragma unroll
-          for (int e = 14; e >= 0; e -= 2) {
-            const float2 f = *reinterpret_cast<const float2*>(into_block + i0 + e);
-            const float w0 = f.x * from, w1 = f.y * from;
-            const float d0 = __uint_as_float(t[e]), d1 = __uint_as_float(t[e + 1]);
-            const float p0 = __uint_as_float(s[e]) * w0, p1 = __uint_as_float(s[e + 1]) * w1;
-            w[e / 2] = pack_bf16(p0, p1);
-            z[e / 2] = pack_bf16(d0 * w0, d1 * w1);
-            tot = fmaf(p1, d1, tot);  // paths from j to this query token or a later one of the quarter
-            m[g * 16 + e + 1] = tot;
-            tot = fmaf(p0, d0, tot);
-            m[g * 16 + e] = tot;
-          }
-        } else {
-#pragma unroll
-          for (int e = 14; e >= 0; e -= 2) {
-            const int i = g * 16 + e;
-            const Dec a = dec.rel(i0 + e), c = dec.rel(i0 + e + 1);
-            const float w0 = i >= lane ? p.scale * dec_diff(a.hi, a.lo, orel.hi, orel.lo) : 0.f;
-            const float w1 = i + 1 >= lane ? p.scale * dec_diff(c.hi, c.lo, orel.hi, orel.lo) : 0.f;
-            const float d0 = i >= lane ? __uint_as_float(t[e]) : 0.f, d1 = i + 1 >= lane ? __uint_as_float(t[e + 1]) : 0.f;
-            const float p0 = i >= lane ? __uint_as_float(s[e]) * w0 : 0.f, p1 = i + 1 >= lane ? __uint_as_float(s[e + 1]) * w1 : 0.f;
-            w[e / 2] = pack_bf16(p0, p1);
-            z[e / 2] = pack_bf16(d0 * w0, d1 * w1);
-            tot = fmaf(p1, d1, tot);
-            m[i + 1] = i + 1 > lane ? tot : 0.f;
-            tot = fmaf(p0, d0, tot);
-            m[i] = i > lane ? tot : 0.f;
-          }
-        }
-        tmem_st8u(tl + L::Pb + i0 / 2, w);
-        tmem_st8u(tl + L::dPb + i0 / 2, z);
-      }
-      rect = col_sums32(m, lane);
-    } else {
-      uint32_t z[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) z[e] = 0u;
-      tmem_st16(tl + L::Pb + cq * 16, z);
-      tmem_st16(tl + L::dPb + cq * 16, z);
-    }
-    tmem_wait_st();
-    wait1();
-    if (__syncthreads_or(!ok)) break;
-    tc_fence_after_sync();
-    put_terms(U, L::y0, L::y1, L::x);
-    float dot_a = 0.f;
-    {
-      uint32_t r[32];
-      tmem_ld32(tl + L::T2 + cq * 32, r);
-      tmem_wait_ld();
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        float x[8];
-        Raw8<__nv_bfloat16>::wide(lds16(sb + L::q + tile_at(row, cq * 4 + u)), x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float y = __uint_as_float(r[8 * u + e]) * into;
-          dot_a = fmaf(x[e], y, dot_a);
-          r[8 * u + e] = __float_as_uint(y);
-        }
-      }
-      tmem_st32(tl + L::T2 + cq * 32, r);
-      tmem_wait_st();
-    }
-    fence_proxy_async_smem();
-    tc_fence_before_sync();
-    __syncthreads();
-    if (tid == kIssue) {
-      tc_fence_after_sync();
-      mma_steps(tm + L::T0, Rows{sb + L::k}, Cols{sb + L::y0}, mma_idesc(VP, false, true), ks, false);
-#pragma unroll
-      for (int t = 2; t >= 0; --t)
-        mma_steps(tm + L::T1, Rows{sb + L::v}, Rows{sb + (t == 0 ? L::y0 : t == 1 ? L::y1 : L::x)}, mma_idesc(128, false, false), vs, t < 2);
-      mma_commit(&bar[0]);
-    }
-    wait0();
-    if (__syncthreads_or(!ok)) break;
-    tc_fence_after_sync();
-    // operands of the last products: dP^T in shared memory, scale e^{c_i} do in three terms (the third in v's place)
-    {
-      uint32_t z[16];
-      tmem_ld16(tl + L::dPb + cq * 16, z);
-      tmem_wait_ld();
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        sts16(sb + L::x + tile_at(row, cq * 4 + u), make_uint4(z[4 * u], z[4 * u + 1], z[4 * u + 2], z[4 * u + 3]));
+    };
+    // the three terms of a [K][V] fp32 state, this thread's row and quarter
+    auto put_terms = [&](const float (&s)[VQ]) {
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
-        const uint32_t at = tile_at(row, cq * NU + u);
         float x[8];
-        Raw8<__nv_bfloat16>::wide(lds16(sb + L::d + at), x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= into;
+        for (int e = 0; e < 8; ++e) x[e] = s[8 * u + e];
+        const uint32_t at = tile_at(row, cq * NU + u);
         sts16(sb + L::y0 + at, take_term(x));
         sts16(sb + L::y1 + at, take_term(x));
-        sts16(sb + L::v + at, take_term(x));
+        sts16(sb + L::y2 + at, last_term(x));
       }
-    }
-    float dot_b = 0.f;
-    {
+    };
+    // N columns of tensor memory times f, in place, dotted with this token's row of a tile of 128 columns
+    auto scale_dot = [&](uint32_t t, uint32_t tile, float f, bool live) {
       uint32_t r[32];
-      tmem_ld32(tl + L::T1 + cq * 32, r);
+      tmem_ld32(tl + t + cq * 32, r);
       tmem_wait_ld();
+      float dot = 0.f;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         float x[8];
-        Raw8<__nv_bfloat16>::wide(lds16(sb + L::k + tile_at(row, cq * 4 + u)), x);
+        Raw8<__nv_bfloat16>::wide(live ? lds16(sb + tile + tile_at(row, cq * 4 + u)) : make_uint4(0u, 0u, 0u, 0u), x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float y = __uint_as_float(r[8 * u + e]) * rest;
-          dot_b = fmaf(x[e], y, dot_b);
+          const float y = __uint_as_float(r[8 * u + e]) * f;
+          dot = fmaf(x[e], y, dot);
           r[8 * u + e] = __float_as_uint(y);
         }
       }
-      tmem_st32(tl + L::T1 + cq * 32, r);
-      tmem_scale<VQ>(tl + L::T0 + cq * VQ, rest);
-      tmem_wait_st();
-    }
-    fence_proxy_async_smem();
-    tc_fence_before_sync();
-    __syncthreads();
-    if (tid == kIssue) {
-      tc_fence_after_sync();
-#pragma unroll
-      for (int s = 0; s < kTC / 16; ++s) mma_ts(tm + L::T0, tm + L::Pb + s * 8, desc_cols(sb + L::d, s), mma_idesc(VP, false, true), true);
-#pragma unroll
-      for (int s = 0; s < kTC / 16; ++s) mma_ts(tm + L::T1, tm + L::dPb + s * 8, desc_cols(sb + L::q, s), mma_idesc(128, false, true), true);
-      mma_steps(tm + L::T2, Cols{sb + L::x}, Cols{sb + L::k}, mma_idesc(128, true, true), kTC / 16, true);
-      mma_commit(&bar[1]);
-    }
-    wait1();
-    if (__syncthreads_or(!ok)) break;
-    tc_fence_after_sync();
-    if (tid == kIssue) {  // into the scores' place, whose readers are done
-#pragma unroll
-      for (int t = 2; t >= 0; --t)
-        mma_steps(tm + L::T3, Cols{sb + L::q}, Cols{sb + (t == 0 ? L::y0 : t == 1 ? L::y1 : L::v)}, mma_idesc(VP, true, true), kTC / 16, t < 2);
-      mma_commit(&bar[0]);
-    }
-    // dq, dk, dv: typed through the tiles of k, x and do, whose products are done; fp32 parts as they are
-    const bool shared = out.dqp != nullptr;
-    auto stage = [&](const uint32_t* r, int n, uint32_t tile, int u0) {
+      __syncwarp();
+      tmem_st32(tl + t + cq * 32, r);
+      return dot;
+    };
+    // typed gradients through this warp's part of a tile whose product is done
+    auto stage = [&](const uint32_t* r, int u0, int n, uint32_t tile, bool live) {
 #pragma unroll
       for (int u = 0; u < n; ++u) {
         float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = row < valid ? __uint_as_float(r[8 * u + e]) : 0.f;
+        for (int e = 0; e < 8; ++e) x[e] = live ? __uint_as_float(r[8 * u + e]) : 0.f;
         sts16(sb + tile + tile_at(row, u0 + u), pack8(x));
       }
+      __syncwarp();
     };
-    {
-      uint32_t r[32];
-      tmem_ld32(tl + L::T2 + cq * 32, r);
-      tmem_wait_ld();
-      if (shared) put_part(out.dqp, t0, r, row < valid);
-      else stage(r, 4, L::k, cq * 4);
-      tmem_ld32(tl + L::T1 + cq * 32, r);
-      tmem_wait_ld();
-      if (shared) put_part(out.dkp, t0, r, row < valid);
-      else stage(r, 4, L::x, cq * 4);
+
+    for (int ck = cend; ck < c1; ++ck) {  // past the row's end
+      const int rows = p.L - ck * kTC < kTC ? p.L - ck * kTC : kTC;
+      const long long at = ((long long)b * p.L + ck * kTC) * p.H + h;
+      auto clear = [&](void* dst, int width) {  // rows of `width` bf16, H rows apart
+        const int n = width / 8;
+        uint4* to = static_cast<uint4*>(dst) + at * n;
+        for (int i = tid; i < rows * n; i += 32 * kLinWarps) to[(long long)(i / n) * p.H * n + i % n] = make_uint4(0u, 0u, 0u, 0u);
+      };
+      if (out.dqp != nullptr) {
+        const long long n = (long long)(p.K / 4) * kTC, to = (((long long)b * p.nck + ck) * p.H + h) * n;
+        for (int i = tid; i < n; i += 32 * kLinWarps)
+          reinterpret_cast<float4*>(out.dqp)[to + i] = reinterpret_cast<float4*>(out.dkp)[to + i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      } else {
+        clear(out.dq, p.K);
+        clear(out.dk, p.K);
+      }
+      clear(out.dv, p.V);
+      if (p.g_head) {
+        if (tid == 0) out.dg[((long long)b * p.nck + ck) * p.H + h] = 0.f;
+      } else if (tid < rows) {
+        out.dg[((long long)b * p.L + ck * kTC + tid) * p.H + h] = 0.f;
+      }
     }
-    {
-      uint32_t r[VQ];
-      tmem_ldn(tl + L::T0 + cq * VQ, r);
-      tmem_wait_ld();
-      stage(r, NU, L::d, cq * NU);
-    }
-    __syncthreads();
-    if (!shared) {
-      const long long at = (((long long)b * p.L + t0) * p.H + h) * p.K;
-      store_tile_tc<16, kBwdThreads>(sb + L::k, static_cast<__nv_bfloat16*>(out.dq) + at, (long long)p.H * p.K, p.L - t0, p.K, tid);
-      store_tile_tc<16, kBwdThreads>(sb + L::x, static_cast<__nv_bfloat16*>(out.dk) + at, (long long)p.H * p.K, p.L - t0, p.K, tid);
-    }
-    store_tile_tc<VP / 8, kBwdThreads>(sb + L::d, static_cast<__nv_bfloat16*>(out.dv) + (((long long)b * p.L + t0) * p.H + h) * p.V, ldo,
-                                       p.L - t0, p.V, tid);
-    wait0();
-    if (__syncthreads_or(!ok)) break;
-    tc_fence_after_sync();
-    {  // what dg is summed from, in x's place
-      float* f = reinterpret_cast<float*>(raw);
-      f[L::a / 4 + cq * kTC + row] = dot_a;
-      f[L::b / 4 + cq * kTC + row] = dot_b;
-      f[L::tot / 4 + cq * kTC + row] = tot;
-      f[L::rect / 4 + (warp & 3) * kTC + cq * 32 + lane] = rect;
+    for (int ck = cend - 1; ck >= c0; --ck) {
+      const uint32_t par = (uint32_t)(cend - 1 - ck) & 1u;
+      const int t0 = ck * kTC, valid = len - t0;
+      const bool live = row < valid;
+      float through = 0.f;  // <S_in, U>, this thread's part
+      {
+        float S[VQ];
+        const float4* src = reinterpret_cast<const float4*>(ckpt + (bh * p.nck + ck) * kv) + row;
+#pragma unroll
+        for (int e = 0; e < VQ; e += 4) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (row < p.K && cq * VQ + e < p.V) x = src[(long long)((cq * VQ + e) / 4) * p.K];
+          S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
+        }
+#pragma unroll
+        for (int e = 0; e < VQ; ++e) through = fmaf(S[e], U[e], through);
+        put_terms(S);
+      }
+      arrive(L::kR1);
+      if (!wait(L::kDc, par) || !wait(L::kLd, par)) break;
+      const Dec last = dec.get(kTC - 1), own = dec.get(row);
+      const float elast = dec_exp(last), into = p.scale * dec_exp(own), rest = dec_exp(dec_sub(last, own));
+      if (!wait(L::kM0, par)) break;
+      tc_fence_after_sync();
+      float tot = 0.f;
+      if (cq >= (warp & 3)) {  // query tokens of this quarter at or after this warp's key tokens
+        const bool diag = cq == (warp & 3);
+        const float from = diag ? 0.f : dec_exp(dec_sub(dec.base(cq), own));  // off the diagonal a decay is a product of two
+        const Dec orel = dec.rel(row);
+        float sums[2];
+#pragma unroll
+        for (int g = 1; g >= 0; --g) {
+          const int i0 = cq * 32 + g * 16;
+          uint32_t s[16], t[16], w[8], z[8];
+          float m[16];
+          tmem_ld16(tl + L::T0 + i0, s);
+          tmem_ld16(tl + L::T1 + i0, t);
+          tmem_wait_ld();
+          if (!diag) {
+#pragma unroll
+            for (int e = 14; e >= 0; e -= 2) {
+              const float2 f = *reinterpret_cast<const float2*>(into_block + i0 + e);
+              const float w0 = f.x * from, w1 = f.y * from;
+              const float d0 = __uint_as_float(t[e]), d1 = __uint_as_float(t[e + 1]);
+              const float p0 = __uint_as_float(s[e]) * w0, p1 = __uint_as_float(s[e + 1]) * w1;
+              w[e / 2] = pack_bf16(p0, p1);
+              z[e / 2] = pack_bf16(d0 * w0, d1 * w1);
+              tot = fmaf(p1, d1, tot);  // paths from j to this query token or a later one of the quarter
+              m[e + 1] = tot;
+              tot = fmaf(p0, d0, tot);
+              m[e] = tot;
+            }
+          } else {
+#pragma unroll
+            for (int e = 14; e >= 0; e -= 2) {
+              const int i = g * 16 + e;
+              const Dec a = dec.rel(i0 + e), c = dec.rel(i0 + e + 1);
+              const float w0 = i >= lane ? p.scale * dec_diff(a.hi, a.lo, orel.hi, orel.lo) : 0.f;
+              const float w1 = i + 1 >= lane ? p.scale * dec_diff(c.hi, c.lo, orel.hi, orel.lo) : 0.f;
+              const float d0 = i >= lane ? __uint_as_float(t[e]) : 0.f, d1 = i + 1 >= lane ? __uint_as_float(t[e + 1]) : 0.f;
+              const float p0 = i >= lane ? __uint_as_float(s[e]) * w0 : 0.f, p1 = i + 1 >= lane ? __uint_as_float(s[e + 1]) * w1 : 0.f;
+              w[e / 2] = pack_bf16(p0, p1);
+              z[e / 2] = pack_bf16(d0 * w0, d1 * w1);
+              tot = fmaf(p1, d1, tot);
+              m[e + 1] = i + 1 > lane ? tot : 0.f;
+              tot = fmaf(p0, d0, tot);
+              m[e] = i > lane ? tot : 0.f;
+            }
+          }
+          tmem_st8u(tl + L::Pb + i0 / 2, w);
+          tmem_st8u(tl + L::dPb + i0 / 2, z);
+          sums[g] = col_sums16(m, lane);
+        }
+        rect[(cq * (cq + 1) / 2 + (warp & 3)) * 32 + lane] = lane < 16 ? sums[0] : sums[1];
+      } else {
+        uint32_t z[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) z[e] = 0u;
+        tmem_st16(tl + L::Pb + cq * 16, z);
+        tmem_st16(tl + L::dPb + cq * 16, z);
+      }
+      if (!wait(L::kM1, par)) break;
+      tc_fence_after_sync();
+      put_terms(U);
+      const float dot_a = scale_dot(L::T2, L::q, into, live);
+      tmem_wait_st();
+      arrive(L::kR3);
+      if (!wait(L::kM2, par)) break;
+      tc_fence_after_sync();
+      // operands of the last products: dP^T in shared memory, scale e^{c_i} do in three terms (the third in v's place)
+      {
+        uint32_t z[16];
+        tmem_ld16(tl + L::dPb + cq * 16, z);
+        tmem_wait_ld();
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          sts16(sb + L::x + tile_at(row, cq * 4 + u), make_uint4(z[4 * u], z[4 * u + 1], z[4 * u + 2], z[4 * u + 3]));
+      }
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        const uint32_t at = tile_at(row, cq * NU + u);
+        float x[8];
+        Raw8<__nv_bfloat16>::wide(live ? lds16(sb + L::d + at) : make_uint4(0u, 0u, 0u, 0u), x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= into;
+        sts16(sb + L::y0 + at, take_term(x));
+        sts16(sb + L::y1 + at, take_term(x));
+        sts16(sb + L::v + at, last_term(x));
+      }
+      __syncwarp();
+      const float dot_b = scale_dot(L::T1, L::k, rest, live);
+      tmem_scale<VQ>(tl + L::T0 + cq * VQ, rest);
+      tmem_wait_st();
+      arrive(L::kR4);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) through += __shfl_xor_sync(0xffffffffu, through, o);
-      if (lane == 0) f[L::thr / 4 + warp] = through;
-    }
-    {
-      uint32_t r[VQ];
-      tmem_ldn(tl + L::T3 + cq * VQ, r);
-      tmem_wait_ld();
-#pragma unroll
-      for (int e = 0; e < VQ; ++e) U[e] = fmaf(U[e], elast, __uint_as_float(r[e]));
-    }
-    tc_fence_before_sync();
-    __syncthreads();
-    if (ck > c0) {
-      load_k(ck - 1);
-      load_rest(ck - 1);
-    }
-    if (warp < 4) {  // dg of tokens t = 32 warp + lane
-      const float* f = reinterpret_cast<const float*>(raw);
-      float sa = 0.f, sb_ = 0.f, sl = 0.f;        // sums over the other quarters; then the running sums of this one
-      float oa = 0.f, ob = 0.f, ol = 0.f;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int at = c * 32 + lane;
-        const float a = (f[L::a / 4 + at] + f[L::a / 4 + kTC + at]) + (f[L::a / 4 + 2 * kTC + at] + f[L::a / 4 + 3 * kTC + at]);
-        const float e = (f[L::b / 4 + at] + f[L::b / 4 + kTC + at]) + (f[L::b / 4 + 2 * kTC + at] + f[L::b / 4 + 3 * kTC + at]);
-        float l = 0.f;  // row at's paths to the quarters after this warp's
-#pragma unroll
-        for (int u = 1; u < 4; ++u) l += u > warp ? f[L::tot / 4 + u * kTC + at] : 0.f;
-        if (c == warp) { oa = a; ob = e; ol = l; }
-        if (c > warp) sa += a;
-        if (c < warp) { sb_ += e; sl += l; }
+      if (lane == 0) thr[warp] = through;
+      if (!wait(L::kM3, par)) break;
+      tc_fence_after_sync();
+      {
+        const bool shared = out.dqp != nullptr;
+        const long long at = (((long long)b * p.L + t0) * p.H + h) * p.K;
+        uint32_t r[32];
+        tmem_ld32(tl + L::T2 + cq * 32, r);
+        tmem_wait_ld();
+        if (shared) {
+          put_part(out.dqp, ck, r, live);
+        } else {
+          stage(r, cq * 4, 4, L::k, live);
+          store_rows<4>(sb + L::k, static_cast<__nv_bfloat16*>(out.dq) + at, (long long)p.H * p.K, (warp & 3) * 32, cq * 4, p.L - t0, p.K, lane);
+        }
+        __syncwarp();
+        {  // this token's parts of dg to the warps that sum it, in the place just read
+          const uint32_t e[8] = {__float_as_uint(dot_a), __float_as_uint(dot_b), __float_as_uint(tot), 0u, 0u, 0u, 0u, 0u};
+          tmem_st8u(tl + L::T2 + cq * 32, e);
+        }
+        tmem_ld32(tl + L::T1 + cq * 32, r);
+        tmem_wait_ld();
+        if (shared) {
+          put_part(out.dkp, ck, r, live);
+        } else {
+          stage(r, cq * 4, 4, L::x, live);
+          store_rows<4>(sb + L::x, static_cast<__nv_bfloat16*>(out.dk) + at, (long long)p.H * p.K, (warp & 3) * 32, cq * 4, p.L - t0, p.K, lane);
+        }
+        __syncwarp();
       }
-      float ra = oa, rb = ob + ol;
-      sb_ += sl;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        sa += __shfl_xor_sync(0xffffffffu, sa, o);
-        sb_ += __shfl_xor_sync(0xffffffffu, sb_, o);
+      {
+        uint32_t r[VQ];
+        tmem_ldn(tl + L::T0 + cq * VQ, r);
+        tmem_wait_ld();
+        stage(r, cq * NU, NU, L::d, live);
+        store_rows<NU>(sb + L::d, static_cast<__nv_bfloat16*>(out.dv) + (((long long)b * p.L + t0) * p.H + h) * p.V, (long long)p.H * p.V,
+                       (warp & 3) * 32, cq * NU, p.L - t0, p.V, lane);
+        __syncwarp();
       }
+      tmem_wait_st();
+      tc_fence_before_sync();
+      if (warp >= 4) {
+        asm volatile("bar.arrive 1, 512;" ::: "memory");
+        arrive(L::kR5);
+      } else {  // dg of tokens t = 32 warp + lane
+        asm volatile("bar.sync 1, 512;" ::: "memory");
+        tc_fence_after_sync();
+        float in = 0.f;  // the blocks of rows up to this quarter
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float ua = __shfl_down_sync(0xffffffffu, ra, o), ub = __shfl_up_sync(0xffffffffu, rb, o);
-        if (lane + o < 32) ra += ua;
-        if (lane >= o) rb += ub;
+        for (int w = 0; w < 4; ++w)
+          if (w <= warp) in += rect[(warp * (warp + 1) / 2 + w) * 32 + lane];
+        float th = lane < kLinWarps ? thr[lane] : 0.f;
+        arrive(L::kR5);
+        uint32_t e[4][8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld8u(tl + L::T2 + c * 32, e[c]);
+        tmem_wait_ld();
+        // token `row`'s sums over the quarters of the columns; its paths to the quarters after its own and, for the quarters'
+        // boundaries, to those after quarter c
+        const float fa = (__uint_as_float(e[0][0]) + __uint_as_float(e[1][0])) + (__uint_as_float(e[2][0]) + __uint_as_float(e[3][0]));
+        const float fb = (__uint_as_float(e[0][1]) + __uint_as_float(e[1][1])) + (__uint_as_float(e[2][1]) + __uint_as_float(e[3][1]));
+        const float q3 = __uint_as_float(e[3][2]), q2 = q3 + __uint_as_float(e[2][2]), q1 = q2 + __uint_as_float(e[1][2]);
+        float ra = fa, rb = fb + (warp == 0 ? q1 : warp == 1 ? q2 : warp == 2 ? q3 : 0.f);  // running sums within the warp's tokens
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float ua = __shfl_down_sync(0xffffffffu, ra, o), ub = __shfl_up_sync(0xffffffffu, rb, o);
+          if (lane + o < 32) ra += ua;
+          if (lane >= o) rb += ub;
+        }
+        // what other quarters of tokens need of this one: its sum of fa (for those before), of fb and of the paths to quarters after c
+        // (for quarter c after it)
+        float sa = fa, s2 = fb + q2, s3 = fb + q3, s4 = fb;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          sa += __shfl_xor_sync(0xffffffffu, sa, o);
+          s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+          s3 += __shfl_xor_sync(0xffffffffu, s3, o);
+          s4 += __shfl_xor_sync(0xffffffffu, s4, o);
+          th += __shfl_xor_sync(0xffffffffu, th, o);
+        }
+        float* ex = reinterpret_cast<float*>(raw + L::hsum);  // [quarter][4]
+        if (lane == 0) {
+          ex[warp * 4] = sa; ex[warp * 4 + 1] = s2; ex[warp * 4 + 2] = s3; ex[warp * 4 + 3] = s4;
+        }
+        asm volatile("bar.sync 2, 128;" ::: "memory");
+        float after = 0.f, before = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          if (w > warp) after += ex[w * 4];
+          if (w < warp) before += ex[w * 4 + warp];  // warp 1, 2, 3: the paths that cross into it
+        }
+        const float up = __shfl_up_sync(0xffffffffu, rb, 1);
+        const float g = in + (after + ra) + (before + (lane > 0 ? up : 0.f)) + elast * th;
+        if (!p.g_head) {
+          if (t0 + row < p.L) out.dg[((long long)b * p.L + t0 + row) * p.H + h] = live ? g : 0.f;
+          asm volatile("bar.sync 2, 128;" ::: "memory");
+        } else {
+          float s = live ? g : 0.f;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          asm volatile("bar.sync 2, 128;" ::: "memory");
+          if (lane == 0) ex[warp] = s;
+          asm volatile("bar.sync 2, 128;" ::: "memory");
+          if (tid == 0) out.dg[((long long)b * p.nck + ck) * p.H + h] = (ex[0] + ex[1]) + (ex[2] + ex[3]);
+          asm volatile("bar.sync 2, 128;" ::: "memory");
+        }
       }
-      float thr = lane < 16 ? f[L::thr / 4 + lane] : 0.f;
+      if (!wait(L::kM4, par)) break;
+      tc_fence_after_sync();
+      {
+        uint32_t r[VQ];
+        tmem_ldn(tl + L::T3 + cq * VQ, r);
+        tmem_wait_ld();
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) thr += __shfl_xor_sync(0xffffffffu, thr, o);
-      const int t = warp * 32 + lane;
-      const float in = (f[L::rect / 4 + t] + f[L::rect / 4 + kTC + t]) + (f[L::rect / 4 + 2 * kTC + t] + f[L::rect / 4 + 3 * kTC + t]);
-      const float before = __shfl_up_sync(0xffffffffu, rb, 1);
-      const float g = in + (sa + ra) + (sb_ + (lane > 0 ? before : 0.f)) + elast * thr;
-      float* dst = out.dg;
-      if (p.g_head) {  // the four warps' parts are added by the column sum
-        float s = t < valid ? g : 0.f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) hsum[warp] = s;
-      } else if (t0 + t < p.L) {
-        dst[((long long)b * p.L + t0 + t) * p.H + h] = t < valid ? g : 0.f;
+        for (int e = 0; e < VQ; ++e) U[e] = fmaf(U[e], elast, __uint_as_float(r[e]));
       }
+      arrive(L::kR6);
     }
-    __syncthreads();  // x is free
-    if (p.g_head && tid == 0) out.dg[((long long)b * p.nck + ck) * p.H + h] = (hsum[0] + hsum[1]) + (hsum[2] + hsum[3]);
+    if (out.dh0 != nullptr && seg == 0 && row < p.K) {
+      float* dst = out.dh0 + (bh * p.K + row) * p.V + cq * VQ;
+#pragma unroll
+      for (int e = 0; e < VQ; e += 4)
+        if (cq * VQ + e < p.V) *reinterpret_cast<float4*>(dst + e) = make_float4(U[e], U[e + 1], U[e + 2], U[e + 3]);
+    }
   }
-  if (!ok) {  // a wait ran out: say so; the outputs are invalid
-    if (tid == 0) atomicOr(&g_lin_err, kErrTmaTimeout);
-    mbar_wait_bounded(&bar[0], ph0 ^ 1, 100000000ull);  // its own MMAs
-    mbar_wait_bounded(&bar[1], ph1 ^ 1, 100000000ull);
-    cp_wait_all();
-  }
-  if (out.dh0 != nullptr && seg == 0 && row < p.K) {
-    float* dst = out.dh0 + (bh * p.K + row) * p.V + cq * VQ;
-#pragma unroll
-    for (int e = 0; e < VQ; e += 4)
-      if (cq * VQ + e < p.V) *reinterpret_cast<float4*>(dst + e) = make_float4(U[e], U[e + 1], U[e + 2], U[e + 3]);
-  }
-  tc_fence_before_sync();
-  __syncthreads();
-  if (warp == 0) tmem_dealloc(tm, L::cols);
+  lin_leave(ok, bar, L::nbar, tm, L::cols, warp, lane);
 }
 
 // dq, dk of a shared head: the parts of its R heads added in order, rounded once.
-template <typename T>
 __global__ void __launch_bounds__(256) linattn_share_kernel(const float* __restrict__ pq, const float* __restrict__ pk,
-                                                            T* __restrict__ dq, T* __restrict__ dk, long long n, int R, int K) {
+                                                            float* __restrict__ dq, float* __restrict__ dk, long long n, int R, int K) {
   const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;  // K is a multiple of 8: four elements of one head
   if (i >= n) return;
   const float* src = blockIdx.y ? pk : pq;
-  T* dst = blockIdx.y ? dk : dq;
+  float* dst = blockIdx.y ? dk : dq;
   const long long row = i / K, at = row * R * K + i % K;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int r = 0; r < R; ++r) {
     const float4 x = *reinterpret_cast<const float4*>(src + at + (long long)r * K);
     a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
   }
-  ActT<T>::st2(dst + i, a.x, a.y);
-  ActT<T>::st2(dst + i + 2, a.z, a.w);
+  *reinterpret_cast<float4*>(dst + i) = a;
+}
+
+// The same from parts in blocks of kTC tokens, [K/4][token][4] (the tensor-core kernel's): a warp reads eight tokens of four
+// groups of columns, 128 bytes each.
+__global__ void __launch_bounds__(256) linattn_share_tc_kernel(const float* __restrict__ pq, const float* __restrict__ pk,
+                                                               __nv_bfloat16* __restrict__ dq, __nv_bfloat16* __restrict__ dk, int L,
+                                                               int nck, int H, int G, int K) {
+  const float4* src = reinterpret_cast<const float4*>(blockIdx.y ? pk : pq);
+  __nv_bfloat16* dst = blockIdx.y ? dk : dq;
+  const int R = H / G, g = (int)(blockIdx.x % G);
+  const long long bc = blockIdx.x / G, b = bc / nck;
+  const int ck = (int)(bc % nck), lane = threadIdx.x & 31, n4 = K / 4;
+  const long long block = (long long)n4 * kTC;
+  for (int i = threadIdx.x >> 5; i < (n4 + 3) / 4 * (kTC / 8); i += 8) {
+    const int c4 = i / (kTC / 8) * 4 + (lane >> 3), t = i % (kTC / 8) * 8 + (lane & 7);
+    if (c4 >= n4 || ck * kTC + t >= L) continue;
+    const float4* at = src + (bc * H + (long long)g * R) * block + (long long)c4 * kTC + t;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = 0; r < R; ++r) {
+      const float4 x = at[r * block];
+      a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+    }
+    *reinterpret_cast<uint2*>(dst + ((b * L + ck * kTC + t) * G + g) * K + c4 * 4) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
+  }
 }
 
 struct AddDg {
@@ -855,7 +915,7 @@ int bwd_plan(int B, int L, int H, int G, int K, int V, int dtype, int g_head, Bw
   const int n = pl.p.nseg;
   pl.states = n > 1 ? (size_t)walks * n * K * V * sizeof(float) : 0;
   pl.decs = n > 1 ? up16((size_t)walks * n * sizeof(Dec)) : 0;
-  pl.parts = H != G ? (size_t)B * L * H * K * sizeof(float) : 0;
+  pl.parts = H != G ? (size_t)B * (dtype == SS_F32 ? (size_t)L : (size_t)pl.p.nck * kTC) * H * K * sizeof(float) : 0;
   pl.sums = g_head ? up16((size_t)B * pl.p.nck * H * sizeof(float)) : 0;
   pl.bytes = pl.states + pl.decs + 2 * pl.parts + pl.sums;
   return SS_OK;
@@ -881,10 +941,14 @@ int bwd_run(const BwdPlan& pl, const float* dh_last, BwdOut out, float* dg, char
     rc = walk(st, out);
   }
   if (rc != SS_OK) return rc;
-  if (pl.parts) {
+  if (pl.parts && std::is_same_v<T, __nv_bfloat16>) {
+    linattn_share_tc_kernel<<<dim3((unsigned)((long long)p.B * p.nck * p.G), 2), 256, 0, s>>>(
+        out.dqp, out.dkp, static_cast<__nv_bfloat16*>(out.dq), static_cast<__nv_bfloat16*>(out.dk), p.L, p.nck, p.H, p.G, p.K);
+    if (cudaGetLastError() != cudaSuccess) return SS_ERR_CUDA;
+  } else if (pl.parts) {
     const long long n = (long long)p.B * p.L * p.G * p.K;
-    linattn_share_kernel<T><<<dim3((unsigned)((n / 4 + 255) / 256), 2), 256, 0, s>>>(out.dqp, out.dkp, static_cast<T*>(out.dq),
-                                                                                 static_cast<T*>(out.dk), n, p.H / p.G, p.K);
+    linattn_share_kernel<<<dim3((unsigned)((n / 4 + 255) / 256), 2), 256, 0, s>>>(out.dqp, out.dkp, static_cast<float*>(out.dq),
+                                                                              static_cast<float*>(out.dk), n, p.H / p.G, p.K);
     if (cudaGetLastError() != cudaSuccess) return SS_ERR_CUDA;
   }
   if (p.g_head && colsum(out.dg, p.H, p.B * p.nck, AddDg{dg}, s) != cudaSuccess) return SS_ERR_CUDA;
@@ -911,15 +975,17 @@ int bwd_bf16(const BwdPlan& pl, const void* dout, const float* ckpt, const float
              cudaStream_t s) {
   const LinAttn& p = pl.p;
   const unsigned grid = (unsigned)p.B * p.H * p.nseg;
-  CUtensorMap mq, md;
-  if (!lin_map(&mq, p.q, p.ldq, p.B, p.L, p.G, p.K) || !lin_map(&md, dout, (long long)p.H * p.V, p.B, p.L, p.H, p.V)) return SS_ERR_CUDA;
+  BwdMaps maps;
+  if (!lin_map(&maps.q, p.q, p.ldq, p.B, p.L, p.G, p.K) || !lin_map(&maps.k, p.k, p.ldk, p.B, p.L, p.G, p.K) ||
+      !lin_map(&maps.v, p.v, p.ldv, p.B, p.L, p.H, p.V) || !lin_map(&maps.d, dout, (long long)p.H * p.V, p.B, p.L, p.H, p.V))
+    return SS_ERR_CUDA;
   return bwd_run<__nv_bfloat16>(
       pl, dh_last, out, dg, ws, s,
       [&](float* st, Dec* dec, const BwdOut&) {
-        return lin_launch(linattn_sum_tc_kernel<true>, grid * ((p.V + 63) / 64), kLinThreads, SumTc::bytes, s, p, mq, md, st, dec);
+        return lin_launch(linattn_sum_tc_kernel<true>, grid * ((p.V + 63) / 64), kLinThreads, SumTc::bytes, s, p, maps.q, maps.d, st, dec);
       },
       [&](const float* u0, const BwdOut& o) {
-        return lin_launch(linattn_bwd_tc_kernel<VP>, grid, kBwdThreads, BwdTc<VP>::bytes, s, p, dout, ckpt, u0, o);
+        return lin_launch(linattn_bwd_tc_kernel<VP>, grid, kLinThreads, BwdTc<VP>::bytes, s, p, maps, ckpt, u0, o);
       });
 }
 
