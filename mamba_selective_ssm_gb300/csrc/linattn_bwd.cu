@@ -338,9 +338,9 @@ struct BwdTc {
   // scale e^{c_i - c of the end of the block of 32 before}; column sums of M by (quarter, block of rows up to it); <S_in, U> by
   // warp; dg of a chunk by quarter
   static constexpr int into = dec + DecTile::bytes, rect = into + kTC * 4, thr = rect + 10 * 32 * 4, hsum = thr + kLinWarps * 4;
-  // barriers: tiles landed, decays stored; MMA groups done; S terms, U terms and scores, last operands stored; outputs out;
-  // U read
-  static constexpr int kLd = 0, kDc = 1, kM0 = 2, kM1 = 3, kM2 = 4, kM3 = 5, kM4 = 6, kR1 = 7, kR3 = 8, kR4 = 9, kR5 = 10, kR6 = 11, nbar = 12;
+  // barriers: tiles landed, decays stored; MMA groups done; S terms, U terms and scores, last operands stored; the tiles of do
+  // and of k out; accumulators read
+  static constexpr int kLd = 0, kDc = 1, kM0 = 2, kM1 = 3, kM2 = 4, kM3 = 5, kM4 = 6, kR1 = 7, kR3 = 8, kR4 = 9, kRd = 10, kRk = 11, kR6 = 12, nbar = 13;
   static constexpr int bar = hsum + 64, tm = bar + nbar * 8, bytes = tm + 8;
   static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
   static constexpr int T0 = 0, T1 = 128, T2 = 256, T3 = 384, Pb = 384, dPb = 448, cols = 512;
@@ -408,17 +408,27 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
     const int ks = (p.K + 15) / 16, vs = (p.V + 15) / 16;  // contraction steps over K and V
     const uint32_t id128 = mma_idesc(128, false, false);
     // a chunk's tiles; their readers have passed a barrier that this warp has waited for, with a proxy fence before it
-    auto load = [&](int ck) {
+    auto load_qv = [&](int ck) {
       if (lane == 0) {
-        mbar_arrive_expect_tx(&bar[L::kLd], 4 * kPanel + 2 * L::vt);
+        mbar_arrive_expect_tx(&bar[L::kLd], 4 * kPanel + 2 * L::vt);  // k and do follow
         load_panels(sb + L::q, 2, &maps.q, &bar[L::kLd], 0, gh, ck * kTC, b);
-        load_panels(sb + L::k, 2, &maps.k, &bar[L::kLd], 0, gh, ck * kTC, b);
         load_panels(sb + L::v, VP / 64, &maps.v, &bar[L::kLd], 0, h, ck * kTC, b);
-        load_panels(sb + L::d, VP / 64, &maps.d, &bar[L::kLd], 0, h, ck * kTC, b);
       }
       __syncwarp();
     };
-    if (c0 < cend) load(cend - 1);
+    auto load_d = [&](int ck) {
+      if (lane == 0) load_panels(sb + L::d, VP / 64, &maps.d, &bar[L::kLd], 0, h, ck * kTC, b);
+      __syncwarp();
+    };
+    auto load_k = [&](int ck) {
+      if (lane == 0) load_panels(sb + L::k, 2, &maps.k, &bar[L::kLd], 0, gh, ck * kTC, b);
+      __syncwarp();
+    };
+    if (c0 < cend) {
+      load_qv(cend - 1);
+      load_d(cend - 1);
+      load_k(cend - 1);
+    }
     for (int ck = cend - 1; ck >= c0; --ck) {
       const uint32_t par = (uint32_t)(cend - 1 - ck) & 1u;
       const int valid = len - ck * kTC;
@@ -429,7 +439,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
         fence_proxy_async_smem();
         __syncwarp();
       }
-      if (ck < cend - 1 && !wait(L::kR6, par ^ 1u)) break;  // U's place takes scores next
+      if (ck < cend - 1 && !wait(L::kR6, par ^ 1u)) break;  // the accumulators' places take scores next
       if (lane == 0) {
         tc_fence_after_sync();
         mma_steps(tm + L::T0, Rows{sb + L::k}, Rows{sb + L::q}, id128, ks, false);
@@ -483,8 +493,12 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
       }
       __syncwarp();
       if (ck > c0) {
-        if (!wait(L::kR5, par) || !wait(L::kM4, par)) break;
-        load(ck - 1);
+        if (!wait(L::kM4, par)) break;
+        load_qv(ck - 1);
+        if (!wait(L::kRd, par)) break;
+        load_d(ck - 1);
+        if (!wait(L::kRk, par)) break;
+        load_k(ck - 1);
       }
     }
   } else if (warp > kLinWarps) {  // ---- the decays' warp
@@ -692,9 +706,9 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
       if (!wait(L::kM1, par)) break;
       tc_fence_after_sync();
       put_terms(U);
-      const float dot_a = scale_dot(L::T2, L::q, into, live);
       tmem_wait_st();
       arrive(L::kR3);
+      const float dot_a = scale_dot(L::T2, L::q, into, live);  // under the products of U
       if (!wait(L::kM2, par)) break;
       tc_fence_after_sync();
       // operands of the last products: dP^T in shared memory, scale e^{c_i} do in three terms (the third in v's place)
@@ -727,8 +741,17 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
       if (lane == 0) thr[warp] = through;
       if (!wait(L::kM3, par)) break;
       tc_fence_after_sync();
+      const bool shared = out.dqp != nullptr;
       {
-        const bool shared = out.dqp != nullptr;
+        uint32_t r[VQ];
+        tmem_ldn(tl + L::T0 + cq * VQ, r);
+        tmem_wait_ld();
+        stage(r, cq * NU, NU, L::d, live);
+        store_rows<NU>(sb + L::d, static_cast<__nv_bfloat16*>(out.dv) + (((long long)b * p.L + t0) * p.H + h) * p.V, (long long)p.H * p.V,
+                       (warp & 3) * 32, cq * NU, p.L - t0, p.V, lane);
+      }
+      arrive(L::kRd);
+      {
         const long long at = (((long long)b * p.L + t0) * p.H + h) * p.K;
         uint32_t r[32];
         tmem_ld32(tl + L::T2 + cq * 32, r);
@@ -739,13 +762,16 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
           stage(r, cq * 4, 4, L::k, live);
           store_rows<4>(sb + L::k, static_cast<__nv_bfloat16*>(out.dq) + at, (long long)p.H * p.K, (warp & 3) * 32, cq * 4, p.L - t0, p.K, lane);
         }
-        __syncwarp();
+        arrive(L::kRk);
         {  // this token's parts of dg to the warps that sum it, in the place just read
           const uint32_t e[8] = {__float_as_uint(dot_a), __float_as_uint(dot_b), __float_as_uint(tot), 0u, 0u, 0u, 0u, 0u};
           tmem_st8u(tl + L::T2 + cq * 32, e);
         }
         tmem_ld32(tl + L::T1 + cq * 32, r);
         tmem_wait_ld();
+        tmem_wait_st();
+        tc_fence_before_sync();
+        if (warp >= 4) asm volatile("bar.arrive 1, 512;" ::: "memory");
         if (shared) {
           put_part(out.dkp, ck, r, live);
         } else {
@@ -754,38 +780,37 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
         }
         __syncwarp();
       }
-      {
-        uint32_t r[VQ];
-        tmem_ldn(tl + L::T0 + cq * VQ, r);
-        tmem_wait_ld();
-        stage(r, cq * NU, NU, L::d, live);
-        store_rows<NU>(sb + L::d, static_cast<__nv_bfloat16*>(out.dv) + (((long long)b * p.L + t0) * p.H + h) * p.V, (long long)p.H * p.V,
-                       (warp & 3) * 32, cq * NU, p.L - t0, p.V, lane);
-        __syncwarp();
-      }
-      tmem_wait_st();
-      tc_fence_before_sync();
-      if (warp >= 4) {
-        asm volatile("bar.arrive 1, 512;" ::: "memory");
-        arrive(L::kR5);
-      } else {  // dg of tokens t = 32 warp + lane
+      // dg of tokens t = 32 warp + lane (warps 0 .. 3): what it is summed from now, the sums when the accumulators are free
+      float in = 0.f, th = 0.f, fa = 0.f, fb = 0.f, q1 = 0.f, q2 = 0.f, q3 = 0.f;
+      if (warp < 4) {
         asm volatile("bar.sync 1, 512;" ::: "memory");
         tc_fence_after_sync();
-        float in = 0.f;  // the blocks of rows up to this quarter
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
+        for (int w = 0; w < 4; ++w)  // the blocks of rows up to this quarter
           if (w <= warp) in += rect[(warp * (warp + 1) / 2 + w) * 32 + lane];
-        float th = lane < kLinWarps ? thr[lane] : 0.f;
-        arrive(L::kR5);
+        th = lane < kLinWarps ? thr[lane] : 0.f;
         uint32_t e[4][8];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld8u(tl + L::T2 + c * 32, e[c]);
         tmem_wait_ld();
-        // token `row`'s sums over the quarters of the columns; its paths to the quarters after its own and, for the quarters'
-        // boundaries, to those after quarter c
-        const float fa = (__uint_as_float(e[0][0]) + __uint_as_float(e[1][0])) + (__uint_as_float(e[2][0]) + __uint_as_float(e[3][0]));
-        const float fb = (__uint_as_float(e[0][1]) + __uint_as_float(e[1][1])) + (__uint_as_float(e[2][1]) + __uint_as_float(e[3][1]));
-        const float q3 = __uint_as_float(e[3][2]), q2 = q3 + __uint_as_float(e[2][2]), q1 = q2 + __uint_as_float(e[1][2]);
+        // token `row`'s sums over the quarters of the columns, and its paths to the quarters after 0, 1, 2
+        fa = (__uint_as_float(e[0][0]) + __uint_as_float(e[1][0])) + (__uint_as_float(e[2][0]) + __uint_as_float(e[3][0]));
+        fb = (__uint_as_float(e[0][1]) + __uint_as_float(e[1][1])) + (__uint_as_float(e[2][1]) + __uint_as_float(e[3][1]));
+        q3 = __uint_as_float(e[3][2]);
+        q2 = q3 + __uint_as_float(e[2][2]);
+        q1 = q2 + __uint_as_float(e[1][2]);
+      }
+      if (!wait(L::kM4, par)) break;
+      tc_fence_after_sync();
+      {
+        uint32_t r[VQ];
+        tmem_ldn(tl + L::T3 + cq * VQ, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < VQ; ++e) U[e] = fmaf(U[e], elast, __uint_as_float(r[e]));
+      }
+      arrive(L::kR6);
+      if (warp < 4) {
         float ra = fa, rb = fb + (warp == 0 ? q1 : warp == 1 ? q2 : warp == 2 ? q3 : 0.f);  // running sums within the warp's tokens
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -831,16 +856,6 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
           asm volatile("bar.sync 2, 128;" ::: "memory");
         }
       }
-      if (!wait(L::kM4, par)) break;
-      tc_fence_after_sync();
-      {
-        uint32_t r[VQ];
-        tmem_ldn(tl + L::T3 + cq * VQ, r);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < VQ; ++e) U[e] = fmaf(U[e], elast, __uint_as_float(r[e]));
-      }
-      arrive(L::kR6);
     }
     if (out.dh0 != nullptr && seg == 0 && row < p.K) {
       float* dst = out.dh0 + (bh * p.K + row) * p.V + cq * VQ;
