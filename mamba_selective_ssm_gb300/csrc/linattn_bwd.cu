@@ -18,8 +18,10 @@ namespace {
 
 template <int KP, int VP>
 struct BwdSmem {
+  static constexpr int NT = KP == 64 && VP == 64 ? 128 : 256;  // threads
   static constexpr int C = kLinChunkF32, LK = KP + 4, LV = VP + 4, LC = C + 4;
-  float q[C * LK], k[C * LK], v[C * LV], d[C * LV], s[KP * LV], p[C * LC], chi[C], clo[C], a[C], b[C], rect[C], red[8];
+  float q[C * LK], k[C * LK], v[C * LV], d[C * LV], s[KP * LV], p[C * LC], chi[C], clo[C], into[C], rest[C];
+  float a[4 * C], b[4 * C], rect[C], red[8];  // a, b: by the warp columns of a C x KP product
 };
 
 struct BwdOut {
@@ -29,18 +31,18 @@ struct BwdOut {
   float* dh0;
 };
 
-// ---------------------------------------------------------------- fp32: FMA pipe
+// ---------------------------------------------------------------- fp32: three-product tf32
 // A CTA walks the chunks of one (batch row, head, segment) from the last to the
 // first with U in registers.  SUM only finds the segment's U from zero.
 template <int KP, int VP, bool SUM>
-__global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const float* __restrict__ dout, const float* __restrict__ ckpt,
-                                                          const float* __restrict__ u0, BwdOut out, float* __restrict__ uend,
-                                                          Dec* __restrict__ udec) {
+__global__ void __launch_bounds__(BwdSmem<KP, VP>::NT) linattn_bwd_kernel(LinAttn p, const float* __restrict__ dout,
+                                                                          const float* __restrict__ ckpt, const float* __restrict__ u0,
+                                                                          BwdOut out, float* __restrict__ uend, Dec* __restrict__ udec) {
   using Sm = BwdSmem<KP, VP>;
-  constexpr int C = Sm::C, LK = Sm::LK, LV = Sm::LV, LC = Sm::LC, RK = KP / 16, RV = VP / 16;
+  constexpr int C = Sm::C, LK = Sm::LK, LV = Sm::LV, LC = Sm::LC, NT = Sm::NT;
   extern __shared__ __align__(16) unsigned char raw[];
   Sm& sm = *reinterpret_cast<Sm*>(raw);
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const int tid = threadIdx.x;
   long long id = blockIdx.x;
   const int seg = (int)(id % p.nseg);
   id /= p.nseg;
@@ -54,46 +56,56 @@ __global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const float
   const long long ldo = (long long)p.H * p.V;
   const float* d = dout + (long long)b * p.L * ldo + (long long)h * p.V;
 
-  float U[RK][RV];
-  zero_acc(U);
+  using State = Own<NT, KP, VP>;
+  using TokK = Own<NT, C, KP>;
+  using TokV = Own<NT, C, VP>;
+  using Score = Own<NT, C, C>;
+  State U;
+  U.zero();
   if (u0 != nullptr && !SUM) {
     const float* src = u0 + (p.nseg > 1 ? bh * p.nseg + seg : bh) * kv;
-#pragma unroll
-    for (int r = 0; r < RK; ++r)
-#pragma unroll
-      for (int c = 0; c < RV; ++c) {
-        const int kk = ty * RK + r, vv = tx + 16 * c;
-        if (kk < p.K && vv < p.V) U[r][c] = src[(long long)kk * p.V + vv];
+    U.pairs(tid, [&](int kk, int vv, float& x, float& y) {
+      if (kk < p.K && vv < p.V) {
+        x = src[(long long)kk * p.V + vv];
+        y = src[(long long)kk * p.V + vv + 1];
       }
+    });
   }
-  // gradients of q or k of token row i: typed when each head has its own, else this head's fp32 part
-  auto put_qk = [&](void* typed, float* part, int t0, int rows, int valid, const float (&a)[4][RK]) {
+  // gradients of q or k: typed when each head has its own, else this head's fp32 part
+  auto put_qk = [&](void* typed, float* part, int t0, int rows, int valid, TokK& a) {
+    float* dst = part != nullptr ? part : static_cast<float*>(typed);
+    a.pairs(tid, [&](int i, int kk, float& x, float& y) {
+      if (i < rows && kk < p.K)
+        st_pair(dst + (((long long)b * p.L + t0 + i) * p.H + h) * p.K + kk, i < valid ? x : 0.f, i < valid ? y : 0.f);
+    });
+  };
+  // a C x KP product's rows dotted with those of a tile, by warp column
+  auto row_dots = [&](TokK& a, const float* tile, float* to) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < TokK::RM; ++r) {
+      const int i = TokK::row(tid, r);
+      float s = 0.f;
 #pragma unroll
-      for (int c = 0; c < RK; ++c) {
-        const int i = ty * 4 + r, kk = tx + 16 * c;
-        if (i >= rows || kk >= p.K) continue;
-        const long long at = (((long long)b * p.L + t0 + i) * p.H + h) * p.K + kk;
-        const float x = i < valid ? a[r][c] : 0.f;
-        if (part != nullptr) part[at] = x;
-        else static_cast<float*>(typed)[at] = x;
-      }
+      for (int c = 0; c < TokK::RN; ++c) s = fmaf(tile[i * LK + TokK::col(tid, c)], a.v[r][c], s);
+      s = row_sum4(s);
+      if ((tid & 3) == 0) to[TokK::wn(tid) * C + i] = s;
+    }
   };
   Dec total = {0.f, 0.f};
   ChunkGates<C> gates;
   const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
+  if (tid < 32) gates.fetch(p, b, h, (c1 - 1) * C, len, tid);
   for (int ck = c1 - 1; ck >= c0; --ck) {
     const int t0 = ck * C;
     const int rows = p.L - t0 < C ? p.L - t0 : C;
     const int valid = len - t0 < 0 ? 0 : len - t0 < C ? len - t0 : C;
     if (valid == 0) {
       if (!SUM) {
-        float z[4][RK];
-        zero_acc(z);
+        TokK z;
+        z.zero();
         put_qk(out.dq, out.dqp, t0, rows, 0, z);
         put_qk(out.dk, out.dkp, t0, rows, 0, z);
-        for (int i = tid; i < rows * p.V; i += 256)
+        for (int i = tid; i < rows * p.V; i += NT)
           static_cast<float*>(out.dv)[(((long long)b * p.L + t0 + i / p.V) * p.H + h) * p.V + i % p.V] = 0.f;
         if (p.g_head) {
           if (tid == 0) out.dg[((long long)b * p.nck + ck) * p.H + h] = 0.f;
@@ -101,170 +113,161 @@ __global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const float
           out.dg[((long long)b * p.L + t0 + tid) * p.H + h] = 0.f;
         }
       }
+      if (tid < 32) gates.fetch(p, b, h, t0 - C, len, tid);
       continue;
     }
-    if (tid < 32) {
-      gates.fetch(p, b, h, t0, len, tid);
-      gates.scan(tid, [&](int i, Dec e) { sm.chi[i] = e.hi; sm.clo[i] = e.lo; });
-    }
-    load_tile<C, KP, LK>(q + t0 * p.ldq, p.ldq, valid, p.K, sm.q, tid);
-    load_tile<C, VP, LV>(d + t0 * ldo, ldo, valid, p.V, sm.d, tid);
+    load_tile<NT, C, KP, LK>(q + t0 * p.ldq, p.ldq, valid, p.K, sm.q, tid);
+    load_tile<NT, C, VP, LV>(d + t0 * ldo, ldo, valid, p.V, sm.d, tid);
     if (!SUM) {
-      load_tile<C, KP, LK>(k + t0 * p.ldk, p.ldk, valid, p.K, sm.k, tid);
-      load_tile<C, VP, LV>(v + t0 * p.ldv, p.ldv, valid, p.V, sm.v, tid);
+      load_tile<NT, C, KP, LK>(k + t0 * p.ldk, p.ldk, valid, p.K, sm.k, tid);
+      load_tile<NT, C, VP, LV>(v + t0 * p.ldv, p.ldv, valid, p.V, sm.v, tid);
       const float* src = ckpt + (bh * p.nck + ck) * kv;
-#pragma unroll
-      for (int r = 0; r < RK; ++r)
-#pragma unroll
-        for (int c = 0; c < RV; ++c) {
-          const int kk = ty * RK + r, vv = tx + 16 * c;
-          sm.s[kk * LV + vv] = kk < p.K && vv < p.V ? src[(long long)kk * p.V + vv] : 0.f;
-        }
+      for (int i = tid; i < KP * (VP / 4); i += NT) {
+        const int kk = i / (VP / 4), vv = i % (VP / 4) * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (kk < p.K && vv < p.V) x = *reinterpret_cast<const float4*>(src + (long long)kk * p.V + vv);
+        *reinterpret_cast<float4*>(sm.s + kk * LV + vv) = x;
+      }
+    }
+    if (tid < 32) {
+      gates.scan(tid, [&](int i, Dec e) { sm.chi[i] = e.hi; sm.clo[i] = e.lo; });
+      __syncwarp();
+      for (int i = tid; i < C; i += 32) {
+        sm.into[i] = p.scale * dec_exp(sm.chi[i], sm.clo[i]);
+        sm.rest[i] = dec_diff(sm.chi[C - 1], sm.clo[C - 1], sm.chi[i], sm.clo[i]);
+      }
+      gates.fetch(p, b, h, t0 - C, len, tid);
     }
     __syncthreads();
     const float chi = sm.chi[C - 1], clo = sm.clo[C - 1];
     total = dec_add(total, Dec{chi, clo});
-    float m[4][4], pr[4][4];
+    Score m;  // what dg's rectangle sums are taken from
     if (!SUM) {
       float part = 0.f;  // <S_in, U>
-#pragma unroll
-      for (int r = 0; r < RK; ++r)
-#pragma unroll
-        for (int c = 0; c < RV; ++c) part = fmaf(sm.s[(ty * RK + r) * LV + tx + 16 * c], U[r][c], part);
+      U.pairs(tid, [&](int kk, int vv, float& x, float& y) {
+        const float2 s = *reinterpret_cast<const float2*>(sm.s + kk * LV + vv);
+        part = fmaf(s.x, x, fmaf(s.y, y, part));
+      });
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
       if ((tid & 31) == 0) sm.red[tid >> 5] = part;
-      float dq[4][RK];
-      zero_acc(dq);
-      mm<C, KP, VP, false, true, LV, LV>(sm.d, sm.s, dq, tid);
+      TokK dq;
+      dq.zero();
+      mm<false, true, LV, LV, VP>(sm.d, sm.s, dq, tid);
+      dq.scale_rows(tid, [&](int i) { return sm.into[i]; });
+      row_dots(dq, sm.q, sm.a);
+      Score pr;
+      m.zero();
+      pr.zero();
+      mm<false, true, LV, LV, VP>(sm.d, sm.v, m, tid);
+      mm<false, true, LK, LK, KP>(sm.q, sm.k, pr, tid);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = ty * 4 + r;
-        const float e = p.scale * dec_exp(sm.chi[i], sm.clo[i]);
-        float s = 0.f;
+      for (int r = 0; r < Score::RM; ++r) {
+        const int i = Score::row(tid, r);
+        const float hi = sm.chi[i], lo = sm.clo[i];
 #pragma unroll
-        for (int c = 0; c < RK; ++c) {
-          dq[r][c] *= e;
-          s = fmaf(sm.q[i * LK + tx + 16 * c], dq[r][c], s);
+        for (int c = 0; c < Score::RN; c += 2) {
+          const int j = Score::col(tid, c);
+          float dp[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const bool in = j + e <= i;
+            const float w = in ? p.scale * dec_diff(hi, lo, sm.chi[j + e], sm.clo[j + e]) : 0.f;
+            float &x = m.v[r][c + e], &y = pr.v[r][c + e];
+            y = in ? y * w : 0.f;
+            dp[e] = in ? x * w : 0.f;
+            x = in ? x * y : 0.f;
+          }
+          st_pair(sm.p + i * LC + j, dp[0], dp[1]);
         }
-        s = row_sum16(s);
-        if (tx == 0) sm.a[i] = s;
       }
-      zero_acc(m);
-      zero_acc(pr);
-      mm<C, C, VP, false, true, LV, LV>(sm.d, sm.v, m, tid);
-      mm<C, C, KP, false, true, LK, LK>(sm.q, sm.k, pr, tid);
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int i = ty * 4 + r, j = tx + 16 * c;
-          const float w = j <= i ? p.scale * dec_diff(sm.chi[i], sm.clo[i], sm.chi[j], sm.clo[j]) : 0.f;
-          pr[r][c] = j <= i ? pr[r][c] * w : 0.f;
-          sm.p[i * LC + j] = j <= i ? m[r][c] * w : 0.f;
-          m[r][c] = j <= i ? m[r][c] * pr[r][c] : 0.f;
-        }
       __syncthreads();
-      mm<C, KP, C, false, false, LC, LK>(sm.p, sm.k, dq, tid);
+      mm<false, false, LC, LK, C>(sm.p, sm.k, dq, tid);
       put_qk(out.dq, out.dqp, t0, rows, valid, dq);
-      float dk[4][RK];
-      zero_acc(dk);
-      mm<C, KP, C, true, false, LC, LK>(sm.p, sm.q, dk, tid);
+      TokK dk;
+      dk.zero();
+      mm<true, false, LC, LK, C>(sm.p, sm.q, dk, tid);
       __syncthreads();
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sm.p[(ty * 4 + r) * LC + tx + 16 * c] = pr[r][c];
-#pragma unroll
-      for (int r = 0; r < RK; ++r)
-#pragma unroll
-        for (int c = 0; c < RV; ++c) sm.s[(ty * RK + r) * LV + tx + 16 * c] = U[r][c];
+      pr.pairs(tid, [&](int i, int j, float& x, float& y) { st_pair(sm.p + i * LC + j, x, y); });
+      U.pairs(tid, [&](int kk, int vv, float& x, float& y) { st_pair(sm.s + kk * LV + vv, x, y); });
       __syncthreads();
-      float dv[4][RV], rest[4];
-      zero_acc(dv);
-      mm<C, VP, KP, false, false, LK, LV>(sm.k, sm.s, dv, tid);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        rest[r] = dec_diff(chi, clo, sm.chi[ty * 4 + r], sm.clo[ty * 4 + r]);
-#pragma unroll
-        for (int c = 0; c < RV; ++c) dv[r][c] *= rest[r];
-      }
-      mm<C, VP, C, true, false, LC, LV>(sm.p, sm.d, dv, tid);
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int c = 0; c < RV; ++c) {
-          const int i = ty * 4 + r, vv = tx + 16 * c;
-          if (i < rows && vv < p.V)
-            static_cast<float*>(out.dv)[(((long long)b * p.L + t0 + i) * p.H + h) * p.V + vv] = i < valid ? dv[r][c] : 0.f;
-        }
-      float ki[4][RK];
-      zero_acc(ki);
-      mm<C, KP, VP, false, true, LV, LV>(sm.v, sm.s, ki, tid);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int j = ty * 4 + r;
-        float s = 0.f;
-#pragma unroll
-        for (int c = 0; c < RK; ++c) {
-          const float x = ki[r][c] * rest[r];
-          s = fmaf(sm.k[j * LK + tx + 16 * c], x, s);
-          dk[r][c] += x;
-        }
-        s = row_sum16(s);
-        if (tx == 0) sm.b[j] = s;
-      }
-      put_qk(out.dk, out.dkp, t0, rows, valid, dk);
-    }
-    __syncthreads();
-    if (!SUM) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sm.p[(ty * 4 + r) * LC + tx + 16 * c] = m[r][c];
-    }
-    for (int i = tid; i < C * KP; i += 256) {  // scale e^{c_i} q_i
-      const int t = i / KP;
-      sm.q[t * LK + i % KP] *= p.scale * dec_exp(sm.chi[t], sm.clo[t]);
-    }
-    __syncthreads();
-    if (!SUM) {
-      // row r of M becomes its running sum over j < t, for t <= r; 4 lanes a row, 16 columns each
       {
-        const int r = tid >> 2, s4 = tid & 3;
-        float* row = sm.p + r * LC + s4 * 16;
-        float x[16], run = 0.f;
+        TokV dv;
+        dv.zero();
+        mm<false, false, LK, LV, KP>(sm.k, sm.s, dv, tid);
+        dv.scale_rows(tid, [&](int i) { return sm.rest[i]; });
+        mm<true, false, LC, LV, C>(sm.p, sm.d, dv, tid);
+        dv.pairs(tid, [&](int i, int vv, float& x, float& y) {
+          if (i < rows && vv < p.V)
+            st_pair(static_cast<float*>(out.dv) + (((long long)b * p.L + t0 + i) * p.H + h) * p.V + vv, i < valid ? x : 0.f, i < valid ? y : 0.f);
+        });
+      }
+      TokK ki;
+      ki.zero();
+      mm<false, true, LV, LV, VP>(sm.v, sm.s, ki, tid);
+      ki.scale_rows(tid, [&](int i) { return sm.rest[i]; });
+      row_dots(ki, sm.k, sm.b);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          x[e] = run;
-          run += row[e];
-        }
+      for (int r = 0; r < TokK::RM; ++r)
+#pragma unroll
+        for (int c = 0; c < TokK::RN; ++c) dk.v[r][c] += ki.v[r][c];
+      put_qk(out.dk, out.dkp, t0, rows, valid, dk);
+      __syncthreads();
+      m.pairs(tid, [&](int i, int j, float& x, float& y) { st_pair(sm.p + i * LC + j, x, y); });
+    }
+    for (int i = tid; i < C * (KP / 4); i += NT) {  // scale e^{c_i} q_i
+      float4* at = reinterpret_cast<float4*>(sm.q + i / (KP / 4) * LK) + i % (KP / 4);
+      const float w = sm.into[i / (KP / 4)];
+      float4 x = *at;
+      x.x *= w; x.y *= w; x.z *= w; x.w *= w;
+      *at = x;
+    }
+    __syncthreads();
+    if (!SUM) {
+      // row r of M becomes its running sum over j < t, for t <= r; LR lanes a row, CW columns each
+      constexpr int LR = NT / C, CW = C / LR;
+      const int r = tid / LR, part = tid % LR;
+      {
+        float* row = sm.p + r * LC + part * CW;
+        float run = 0.f;
+#pragma unroll
+        for (int e = 0; e < CW; ++e) run += row[e];
         float base = 0.f;
 #pragma unroll
-        for (int o = 1; o < 4; ++o) {
-          const float u = __shfl_up_sync(0xffffffffu, run, o, 4);
-          if (s4 >= o) base += u;
+        for (int o = 1; o < LR; ++o) {
+          const float u = __shfl_up_sync(0xffffffffu, run, o, LR);
+          if (part >= o) base += u;
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) row[e] = s4 * 16 + e <= r ? base + x[e] : 0.f;
+        for (int e = 0; e < CW; ++e) {
+          const float x = row[e];
+          row[e] = part * CW + e <= r ? base : 0.f;
+          base += x;
+        }
       }
       __syncthreads();
       {  // column sums: every path from before t to t or later
-        const int t = tid >> 2, s4 = tid & 3;
         float s = 0.f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s += sm.p[(s4 * 16 + e) * LC + t];
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        if (s4 == 0) sm.rect[t] = s;
+        for (int e = 0; e < CW; ++e) s += sm.p[(part * CW + e) * LC + r];
+#pragma unroll
+        for (int o = 1; o < LR; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (part == 0) sm.rect[r] = s;
       }
       __syncthreads();
       if (tid < 32) {  // two consecutive tokens a lane
         float through = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) through += sm.red[w];
+        for (int w = 0; w < NT / 32; ++w) through += sm.red[w];
         through *= dec_exp(chi, clo);
-        const float a0 = sm.a[2 * tid], a1 = sm.a[2 * tid + 1], b0 = sm.b[2 * tid], b1 = sm.b[2 * tid + 1];
+        float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < TokK::WN; ++w) {
+          a0 += sm.a[w * C + 2 * tid];
+          a1 += sm.a[w * C + 2 * tid + 1];
+          b0 += sm.b[w * C + 2 * tid];
+          b1 += sm.b[w * C + 2 * tid + 1];
+        }
         float sa = a0 + a1, sb = b0 + b1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -291,25 +294,17 @@ __global__ void __launch_bounds__(256) linattn_bwd_kernel(LinAttn p, const float
       }
     }
     const float e = dec_exp(chi, clo);
-#pragma unroll
-    for (int r = 0; r < RK; ++r)
-#pragma unroll
-      for (int c = 0; c < RV; ++c) U[r][c] *= e;
-    mm<KP, VP, C, true, false, LK, LV>(sm.q, sm.d, U, tid);
+    U.scale_rows(tid, [&](int) { return e; });
+    mm<true, false, LK, LV, C>(sm.q, sm.d, U, tid);
     __syncthreads();
   }
   float* dst = nullptr;
   if (SUM) dst = uend + (bh * p.nseg + seg) * kv;
   else if (out.dh0 != nullptr && seg == 0) dst = out.dh0 + bh * kv;
-  if (dst != nullptr) {
-#pragma unroll
-    for (int r = 0; r < RK; ++r)
-#pragma unroll
-      for (int c = 0; c < RV; ++c) {
-        const int kk = ty * RK + r, vv = tx + 16 * c;
-        if (kk < p.K && vv < p.V) dst[(long long)kk * p.V + vv] = U[r][c];
-      }
-  }
+  if (dst != nullptr)
+    U.pairs(tid, [&](int kk, int vv, float& x, float& y) {
+      if (kk < p.K && vv < p.V) st_pair(dst + (long long)kk * p.V + vv, x, y);
+    });
   if (SUM && tid == 0) udec[bh * p.nseg + seg] = total;
 }
 
@@ -926,7 +921,7 @@ int bwd_plan(int B, int L, int H, int G, int K, int V, int dtype, int g_head, Bw
   pl.p.B = B; pl.p.L = L; pl.p.H = H; pl.p.G = G; pl.p.K = K; pl.p.V = V;
   const long long walks = (long long)B * H;
   if (walks > (1ll << 24)) return SS_ERR_DIM;
-  linattn_segments(pl.p, linattn_chunk(dtype), walks, 152);
+  linattn_segments(pl.p, dtype, walks);
   const int n = pl.p.nseg;
   pl.states = n > 1 ? (size_t)walks * n * K * V * sizeof(float) : 0;
   pl.decs = n > 1 ? up16((size_t)walks * n * sizeof(Dec)) : 0;
@@ -978,10 +973,10 @@ int bwd_f32(const BwdPlan& pl, const void* dout, const float* ckpt, const float*
   return bwd_run<float>(
       pl, dh_last, out, dg, ws, s,
       [&](float* st, Dec* dec, const BwdOut& o) {
-        return lin_launch(linattn_bwd_kernel<KP, VP, true>, grid, 256, smem, s, pl.p, dout, ckpt, nullptr, o, st, dec);
+        return lin_launch(linattn_bwd_kernel<KP, VP, true>, grid, BwdSmem<KP, VP>::NT, smem, s, pl.p, dout, ckpt, nullptr, o, st, dec);
       },
       [&](const float* u0, const BwdOut& o) {
-        return lin_launch(linattn_bwd_kernel<KP, VP, false>, grid, 256, smem, s, pl.p, dout, ckpt, u0, o, nullptr, nullptr);
+        return lin_launch(linattn_bwd_kernel<KP, VP, false>, grid, BwdSmem<KP, VP>::NT, smem, s, pl.p, dout, ckpt, u0, o, nullptr, nullptr);
       });
 }
 

@@ -142,16 +142,21 @@ constexpr int kLinChunkBf16 = 128;  // bf16 (tensor cores: 128 rows of an MMA)
 
 inline int linattn_chunk(int dtype) { return dtype == SS_F32 ? kLinChunkF32 : kLinChunkBf16; }
 
-// Segments: with fewer independent walks (batch rows x heads x column tiles)
-// than the GPU holds at once, a row is cut in `nseg` pieces whose end states
-// are found first.  Each piece costs a second read of its inputs, so no more
-// pieces than fill `slots` walks, and none shorter than four chunks.
-inline void linattn_segments(LinAttn& p, int chunk, long long walks, int slots) {
+// Segments: with fewer independent walks (batch rows x heads, x column tiles
+// for the fp32 forward) than fill the GPU, a row is cut in pieces of at least
+// four chunks whose end states are found first, at the price of a second read of
+// half the inputs.  The tensor-core kernels hold an SM each: as many pieces as
+// leave every one of them its own.  The fp32 kernels share an SM (three forward,
+// two backward) and their time is arithmetic: below three CTAs an SM, enough
+// pieces for five, so that no SM is left with far more than its share (192 walks
+// of the 130M layer: XXX us for four pieces, YYY for one).
+inline void linattn_segments(LinAttn& p, int dtype, long long walks) {
+  const int chunk = linattn_chunk(dtype);
   p.nck = (p.L + chunk - 1) / chunk;
-  int n = walks > 0 ? (int)(slots / walks) : 1;
+  long long n = dtype == SS_F32 ? (walks >= 3 * 152 ? 1 : (5 * 152 + walks - 1) / walks) : 152 / walks;
   if (n > p.nck / 4) n = p.nck / 4;
   if (n < 1) n = 1;
-  p.cps = (p.nck + n - 1) / n;
+  p.cps = (int)((p.nck + n - 1) / n);
   p.nseg = (p.nck + p.cps - 1) / p.cps;
 }
 
@@ -184,66 +189,112 @@ inline int lin_launch(void (*kern)(KArgs...), unsigned grid, int threads, size_t
 }
 
 // ---------------------------------------------------------------- FP32 tiles
-// C += A B from shared memory on the FMA pipe, 256 threads as 16 x 16: thread
-// (ty, tx) owns rows ty * M/16 + r and columns tx + 16 c of the M x N product.
-// A is stored [M][Kd] (TA false) or [Kd][M]; B is stored [Kd][N] (TB false) or
-// [N][Kd].  Every product of a kernel uses the same ownership, so accumulators
-// of different products combine element by element in registers.
-template <int M, int N, int Kd, bool TA, bool TB, int LDA, int LDB>
-__device__ __forceinline__ void mm(const float* __restrict__ A, const float* __restrict__ B, float (&acc)[M / 16][N / 16], int tid) {
-  constexpr int RM = M / 16, RN = N / 16;
-  const int ty = tid >> 4, tx = tid & 15;
-#pragma unroll 2
-  for (int k = 0; k < Kd; k += 4) {
-    float a[RM][4], b[RN][4];
+// fp32 products from shared memory on the tensor cores: each operand is split
+// in registers into a tf32 value and the tf32 of what that leaves (22 bits), and
+// the three products that matter are summed in fp32, the smallest first; what is
+// dropped is 2^-22 of a term.  Each step of 8 is summed by itself and added with a
+// rounding: the tensor core cuts its sums, which into a state carried over 32
+// chunks added up to 1e-5 of it.  These take operands from registers (mma.sync), so
+// that a tile lies in shared memory once and in fp32: tcgen05 reads its operands
+// there, and both halves of q, k, v, do and the states would not fit.  (On the
+// FMA pipe the same kernels were bound by shared memory: 8 x 4 products a thread
+// read 16 vectors for every 128 multiplies.)
+//
+// Warps tile the M x N product; a thread's accumulators acc[r][c] are rows row(r)
+// and columns col(c), columns in neighbouring pairs.  Products of the same shape
+// have the same owners, so they combine element by element in registers.
+template <int NT, int M, int N>
+struct Own {
+  static constexpr int TM = NT == 256 && M == 64 && N == 64 ? 16 : 32, WM = M / TM, WN = NT / 32 / WM, TN = N / WN;
+  static constexpr int RM = TM / 8, RN = TN / 4;
+  static_assert(WM * WN * 32 == NT && WN * TN == N, "warps tile the product");
+  __device__ __forceinline__ static int wn(int tid) { return (tid >> 5) % WN; }
+  __device__ __forceinline__ static int row(int tid, int r) {
+    return (tid >> 5) / WN * TM + (r >> 1) * 16 + (r & 1) * 8 + ((tid & 31) >> 2);
+  }
+  __device__ __forceinline__ static int col(int tid, int c) { return wn(tid) * TN + (c >> 1) * 8 + (tid & 3) * 2 + (c & 1); }
+  float v[RM][RN];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int r = 0; r < RM; ++r)
+#pragma unroll
+      for (int c = 0; c < RN; ++c) v[r][c] = 0.f;
+  }
+  // f(row, column, value pair) over neighbouring columns
+  template <typename F>
+  __device__ __forceinline__ void pairs(int tid, F f) {
+#pragma unroll
+    for (int r = 0; r < RM; ++r)
+#pragma unroll
+      for (int c = 0; c < RN; c += 2) f(row(tid, r), col(tid, c), v[r][c], v[r][c + 1]);
+  }
+  // every row times f(row)
+  template <typename F>
+  __device__ __forceinline__ void scale_rows(int tid, F f) {
 #pragma unroll
     for (int r = 0; r < RM; ++r) {
-      if constexpr (!TA) {
-        const float4 v = *reinterpret_cast<const float4*>(A + (ty * RM + r) * LDA + k);
-        a[r][0] = v.x; a[r][1] = v.y; a[r][2] = v.z; a[r][3] = v.w;
-      }
+      const float e = f(row(tid, r));
+#pragma unroll
+      for (int c = 0; c < RN; ++c) v[r][c] *= e;
     }
-    if constexpr (TA) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int r = 0; r < RM; r += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(A + (k + e) * LDA + ty * RM + r);
-          a[r][e] = v.x; a[r + 1][e] = v.y; a[r + 2][e] = v.z; a[r + 3][e] = v.w;
-        }
-    }
-#pragma unroll
-    for (int c = 0; c < RN; ++c) {
-      if constexpr (TB) {
-        const float4 v = *reinterpret_cast<const float4*>(B + (tx + 16 * c) * LDB + k);
-        b[c][0] = v.x; b[c][1] = v.y; b[c][2] = v.z; b[c][3] = v.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) b[c][e] = B[(k + e) * LDB + tx + 16 * c];
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-      for (int r = 0; r < RM; ++r)
-#pragma unroll
-        for (int c = 0; c < RN; ++c) acc[r][c] = fmaf(a[r][e], b[c][e], acc[r][c]);
   }
+};
+
+__device__ __forceinline__ void tf32_split(float x, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float& c0, float& c1, float& c2, float& c3, const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c0), "+f"(c1), "+f"(c2), "+f"(c3)
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-template <int R, int Cn>
-__device__ __forceinline__ void zero_acc(float (&acc)[R][Cn]) {
+// acc += A B.  A is stored [M][Kd] (TA false) or [Kd][M]; B is stored [Kd][N] (TB false) or [N][Kd].
+template <bool TA, bool TB, int LDA, int LDB, int Kd, int NT, int M, int N>
+__device__ __forceinline__ void mm(const float* __restrict__ A, const float* __restrict__ B, Own<NT, M, N>& acc, int tid) {
+  using O = Own<NT, M, N>;
+  constexpr int MT = O::RM / 2, NL = O::RN / 2;
+  const int lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int m0 = (tid >> 5) / O::WN * O::TM + g, n0 = O::wn(tid) * O::TN + g;
+#pragma unroll 2
+  for (int k = 0; k < Kd; k += 8) {
+    uint32_t ah[MT][4], al[MT][4];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int c = 0; c < Cn; ++c) acc[r][c] = 0.f;
+      for (int e = 0; e < 4; ++e) {
+        const int i = m0 + m * 16 + (e & 1) * 8, kk = k + t + (e >> 1) * 4;
+        tf32_split(TA ? A[kk * LDA + i] : A[i * LDA + kk], ah[m][e], al[m][e]);
+      }
+#pragma unroll
+    for (int n = 0; n < NL; ++n) {
+      uint32_t bh[2], bl[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = n0 + n * 8, kk = k + t + e * 4;
+        tf32_split(TB ? B[j * LDB + kk] : B[kk * LDB + j], bh[e], bl[e]);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        float c0 = 0.f, c1 = 0.f, c2 = 0.f, c3 = 0.f;
+        mma_tf32(c0, c1, c2, c3, al[m], bh);
+        mma_tf32(c0, c1, c2, c3, ah[m], bl);
+        mma_tf32(c0, c1, c2, c3, ah[m], bh);
+        acc.v[2 * m][2 * n] += c0;
+        acc.v[2 * m][2 * n + 1] += c1;
+        acc.v[2 * m + 1][2 * n] += c2;
+        acc.v[2 * m + 1][2 * n + 1] += c3;
+      }
+    }
+  }
 }
 
 // C tokens x W columns of a strided input into a padded fp32 tile; columns
 // past `width` and tokens past `valid` become zero (their memory is not read).
-template <int C, int W, int LD>
+template <int NT, int C, int W, int LD>
 __device__ __forceinline__ void load_tile(const float* __restrict__ src, long long ld, int valid, int width, float* dst, int tid) {
-  for (int i = tid; i < C * (W / 8); i += 256) {
+  for (int i = tid; i < C * (W / 8); i += NT) {
     const int t = i / (W / 8), c = (i % (W / 8)) * 8;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (t < valid && c < width) ActT<float>::ld8(src + (long long)t * ld + c, v);
@@ -251,11 +302,11 @@ __device__ __forceinline__ void load_tile(const float* __restrict__ src, long lo
   }
 }
 
-// Row sums of a per-thread [rows][cols] product over the 16 threads of a row.
-__device__ __forceinline__ float row_sum16(float v) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+// Sum over the four threads of a warp that share a row of an Own<>.
+__device__ __forceinline__ float row_sum4(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
+__device__ __forceinline__ void st_pair(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
 
 }  // namespace ssk

@@ -3,26 +3,27 @@
 
 namespace {
 
-// fp32: products on the FMA pipe.  A CTA walks the chunks of one (batch row,
+// fp32: three-product tf32 (see Own).  A CTA walks the chunks of one (batch row,
 // head, 64-column tile of V, segment) in order with the state in registers.
 // SUM only finds the segment's end state from zero and its decay (no q, no o).
 constexpr int kVT = 64;
 
 template <int KP>
 struct FwdSmem {
+  static constexpr int NT = KP == 64 ? 128 : 256;  // threads
   static constexpr int C = kLinChunkF32, LK = KP + 4, LV = kVT + 4, LC = C + 4;
-  float q[C * LK], k[C * LK], v[C * LV], s[KP * LV], p[C * LC], chi[C], clo[C];
+  float q[C * LK], k[C * LK], v[C * LV], s[KP * LV], chi[C], clo[C], rest[C];  // the scores take q's place
 };
 
 template <int KP, bool SUM>
-__global__ void __launch_bounds__(256) linattn_fwd_kernel(LinAttn p, const float* __restrict__ s0, float* __restrict__ o,
-                                                          float* __restrict__ ckpt, float* __restrict__ send,
-                                                          Dec* __restrict__ sdec) {
+__global__ void __launch_bounds__(FwdSmem<KP>::NT) linattn_fwd_kernel(LinAttn p, const float* __restrict__ s0, float* __restrict__ o,
+                                                                      float* __restrict__ ckpt, float* __restrict__ send,
+                                                                      Dec* __restrict__ sdec) {
   using Sm = FwdSmem<KP>;
-  constexpr int C = Sm::C, LK = Sm::LK, LV = Sm::LV, LC = Sm::LC, RK = KP / 16;
+  constexpr int C = Sm::C, LK = Sm::LK, LV = Sm::LV, LC = Sm::LC, NT = Sm::NT;
   extern __shared__ __align__(16) unsigned char raw[];
   Sm& sm = *reinterpret_cast<Sm*>(raw);
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const int tid = threadIdx.x;
   const int nvt = (p.V + kVT - 1) / kVT;
   long long id = blockIdx.x;
   const int seg = (int)(id % p.nseg);
@@ -38,107 +39,90 @@ __global__ void __launch_bounds__(256) linattn_fwd_kernel(LinAttn p, const float
   const float* v = static_cast<const float*>(p.v) + (long long)b * p.L * p.ldv + (long long)h * p.V + v0;
 
   // the state this segment starts from: what the segments before composed, or h0, or zero
-  float S[RK][4];
-  zero_acc(S);
+  Own<NT, KP, kVT> S;
+  S.zero();
   if (s0 != nullptr && !SUM) {
-    const float* src = s0 + (p.nseg > 1 ? bh * p.nseg + seg : bh) * p.K * p.V;
-#pragma unroll
-    for (int r = 0; r < RK; ++r)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int kk = ty * RK + r, vv = tx + 16 * c;
-        if (kk < p.K && vv < vw) S[r][c] = src[(long long)kk * p.V + v0 + vv];
+    const float* src = s0 + (p.nseg > 1 ? bh * p.nseg + seg : bh) * p.K * p.V + v0;
+    S.pairs(tid, [&](int kk, int vv, float& x, float& y) {
+      if (kk < p.K && vv < vw) {
+        x = src[(long long)kk * p.V + vv];
+        y = src[(long long)kk * p.V + vv + 1];
       }
+    });
   }
   Dec total = {0.f, 0.f};
   ChunkGates<C> gates;
   const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nck ? c0 + p.cps : p.nck;
+  if (tid < 32) gates.fetch(p, b, h, c0 * C, len, tid);
   for (int ck = c0; ck < c1; ++ck) {
     const int t0 = ck * C;
     const int rows = p.L - t0 < C ? p.L - t0 : C;
     const int valid = len - t0 < 0 ? 0 : len - t0 < C ? len - t0 : C;
     if (valid == 0) {  // past the row's end: nothing decays, adds or reads
       if (!SUM)
-        for (int i = tid; i < rows * vw; i += 256)
+        for (int i = tid; i < rows * vw; i += NT)
           o[(((long long)b * p.L + t0 + i / vw) * p.H + h) * p.V + v0 + i % vw] = 0.f;
       continue;
     }
+    if (!SUM) load_tile<NT, C, KP, LK>(q + t0 * p.ldq, p.ldq, valid, p.K, sm.q, tid);
+    load_tile<NT, C, KP, LK>(k + t0 * p.ldk, p.ldk, valid, p.K, sm.k, tid);
+    load_tile<NT, C, kVT, LV>(v + t0 * p.ldv, p.ldv, valid, vw, sm.v, tid);
     if (tid < 32) {
-      gates.fetch(p, b, h, t0, len, tid);
       gates.scan(tid, [&](int i, Dec e) { sm.chi[i] = e.hi; sm.clo[i] = e.lo; });
+      __syncwarp();
+      for (int i = tid; i < C; i += 32) sm.rest[i] = dec_diff(sm.chi[C - 1], sm.clo[C - 1], sm.chi[i], sm.clo[i]);
+      gates.fetch(p, b, h, t0 + C, len, tid);
     }
-    if (!SUM) load_tile<C, KP, LK>(q + t0 * p.ldq, p.ldq, valid, p.K, sm.q, tid);
-    load_tile<C, KP, LK>(k + t0 * p.ldk, p.ldk, valid, p.K, sm.k, tid);
-    load_tile<C, kVT, LV>(v + t0 * p.ldv, p.ldv, valid, vw, sm.v, tid);
-    if (!SUM) {
-#pragma unroll
-      for (int r = 0; r < RK; ++r)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int kk = ty * RK + r, vv = tx + 16 * c;
-          sm.s[kk * LV + vv] = S[r][c];
-          if (ckpt != nullptr && kk < p.K && vv < vw) ckpt[((bh * p.nck + ck) * p.K + kk) * p.V + v0 + vv] = S[r][c];
-        }
-    }
+    if (!SUM)
+      S.pairs(tid, [&](int kk, int vv, float& x, float& y) {
+        st_pair(sm.s + kk * LV + vv, x, y);
+        if (ckpt != nullptr && kk < p.K && vv < vw) st_pair(ckpt + ((bh * p.nck + ck) * p.K + kk) * p.V + v0 + vv, x, y);
+      });
     __syncthreads();
     if (!SUM) {
-      float a[4][4];
-      zero_acc(a);
-      mm<C, C, KP, false, true, LK, LK>(sm.q, sm.k, a, tid);
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int i = ty * 4 + r, j = tx + 16 * c;
-          sm.p[i * LC + j] = j <= i ? a[r][c] * dec_diff(sm.chi[i], sm.clo[i], sm.chi[j], sm.clo[j]) : 0.f;
-        }
-      zero_acc(a);
-      mm<C, kVT, KP, false, false, LK, LV>(sm.q, sm.s, a, tid);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float e = dec_exp(sm.chi[ty * 4 + r], sm.clo[ty * 4 + r]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) a[r][c] *= e;
-      }
+      Own<NT, C, C> pr;
+      Own<NT, C, kVT> a;
+      pr.zero();
+      mm<false, true, LK, LK, KP>(sm.q, sm.k, pr, tid);
+      a.zero();
+      mm<false, false, LK, LV, KP>(sm.q, sm.s, a, tid);
       __syncthreads();
-      mm<C, kVT, C, false, false, LC, LV>(sm.p, sm.v, a, tid);
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int i = ty * 4 + r, vv = tx + 16 * c;
-          if (i < rows && vv < vw)
-            o[(((long long)b * p.L + t0 + i) * p.H + h) * p.V + v0 + vv] = i < valid ? p.scale * a[r][c] : 0.f;
-        }
+      float* sp = sm.q;
+      pr.pairs(tid, [&](int i, int j, float& x, float& y) {
+        const float hi = sm.chi[i], lo = sm.clo[i];
+        st_pair(sp + i * LC + j, j <= i ? x * dec_diff(hi, lo, sm.chi[j], sm.clo[j]) : 0.f,
+                j + 1 <= i ? y * dec_diff(hi, lo, sm.chi[j + 1], sm.clo[j + 1]) : 0.f);
+      });
+      a.scale_rows(tid, [&](int i) { return dec_exp(sm.chi[i], sm.clo[i]); });
+      __syncthreads();
+      mm<false, false, LC, LV, C>(sp, sm.v, a, tid);
+      a.pairs(tid, [&](int i, int vv, float& x, float& y) {
+        if (i < rows && vv < vw)
+          st_pair(o + (((long long)b * p.L + t0 + i) * p.H + h) * p.V + v0 + vv, i < valid ? p.scale * x : 0.f, i < valid ? p.scale * y : 0.f);
+      });
     }
-    __syncthreads();
     const float chi = sm.chi[C - 1], clo = sm.clo[C - 1];
     total = dec_add(total, Dec{chi, clo});
-    for (int i = tid; i < C * KP; i += 256) {  // k_j e^{c_last - c_j}
-      const int j = i / KP;
-      sm.k[j * LK + i % KP] *= dec_diff(chi, clo, sm.chi[j], sm.clo[j]);
+    for (int i = tid; i < C * (KP / 4); i += NT) {  // k_j e^{c_last - c_j}
+      float4* at = reinterpret_cast<float4*>(sm.k + i / (KP / 4) * LK) + i % (KP / 4);
+      const float w = sm.rest[i / (KP / 4)];
+      float4 x = *at;
+      x.x *= w; x.y *= w; x.z *= w; x.w *= w;
+      *at = x;
     }
     const float e = dec_exp(chi, clo);
-#pragma unroll
-    for (int r = 0; r < RK; ++r)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) S[r][c] *= e;
+    S.scale_rows(tid, [&](int) { return e; });
     __syncthreads();
-    mm<KP, kVT, C, true, false, LK, LV>(sm.k, sm.v, S, tid);
+    mm<true, false, LK, LV, C>(sm.k, sm.v, S, tid);
     __syncthreads();
   }
   float* dst = nullptr;
   if (SUM) dst = send + (bh * p.nseg + seg) * p.K * p.V;
   else if (send != nullptr && seg == p.nseg - 1) dst = send + bh * p.K * p.V;
-  if (dst != nullptr) {
-#pragma unroll
-    for (int r = 0; r < RK; ++r)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int kk = ty * RK + r, vv = tx + 16 * c;
-        if (kk < p.K && vv < vw) dst[(long long)kk * p.V + v0 + vv] = S[r][c];
-      }
-  }
+  if (dst != nullptr)
+    S.pairs(tid, [&](int kk, int vv, float& x, float& y) {
+      if (kk < p.K && vv < vw) st_pair(dst + (long long)kk * p.V + v0 + vv, x, y);
+    });
   if (SUM && tid == 0 && vt == 0) sdec[bh * p.nseg + seg] = total;
 }
 
@@ -461,7 +445,7 @@ int fwd_plan(int B, int L, int H, int G, int K, int V, int dtype, FwdPlan& pl) {
   pl.p.B = B; pl.p.L = L; pl.p.H = H; pl.p.G = G; pl.p.K = K; pl.p.V = V;
   pl.walks = (long long)B * H * (dtype == SS_F32 ? (V + kVT - 1) / kVT : 1);
   if (pl.walks > (1ll << 24)) return SS_ERR_DIM;
-  linattn_segments(pl.p, linattn_chunk(dtype), pl.walks, (dtype == SS_F32 && K <= 64 ? 2 : 1) * 152);
+  linattn_segments(pl.p, dtype, pl.walks);
   pl.states = pl.p.nseg > 1 ? (size_t)B * H * pl.p.nseg * K * V * sizeof(float) : 0;
   pl.bytes = pl.p.nseg > 1 ? pl.states + (size_t)B * H * pl.p.nseg * sizeof(Dec) : 0;
   return SS_OK;
@@ -488,8 +472,8 @@ int fwd_f32(const FwdPlan& pl, const float* h0, float* o, float* ckpt, float* h_
   const size_t smem = sizeof(FwdSmem<KP>);
   return fwd_run(
       pl, h0, ws, s,
-      [&](float* st, Dec* dec) { return lin_launch(linattn_fwd_kernel<KP, true>, grid, 256, smem, s, pl.p, nullptr, o, ckpt, st, dec); },
-      [&](const float* s0) { return lin_launch(linattn_fwd_kernel<KP, false>, grid, 256, smem, s, pl.p, s0, o, ckpt, h_last, nullptr); });
+      [&](float* st, Dec* dec) { return lin_launch(linattn_fwd_kernel<KP, true>, grid, FwdSmem<KP>::NT, smem, s, pl.p, nullptr, o, ckpt, st, dec); },
+      [&](const float* s0) { return lin_launch(linattn_fwd_kernel<KP, false>, grid, FwdSmem<KP>::NT, smem, s, pl.p, s0, o, ckpt, h_last, nullptr); });
 }
 
 template <int VP>
