@@ -12,15 +12,18 @@
 // the same number, but loses what the sums have in common):
 //   dg_t = sum_{j<t<=i} M_ij + sum_{i>=t} q_i.(scale e^{c_i} S_in do_i)
 //        + sum_{j<t} k_j.(e^{c_last-c_j} U v_j) + e^{c_last} <S_in, U>,   M_ij = P_ij (do_i.v_j)
+#include <stddef.h>
+
 #include "linattn_tc.cuh"
 
 namespace {
 
 template <int KP, int VP>
 struct BwdSmem {
-  static constexpr int NT = KP == 64 && VP == 64 ? 128 : 256;  // threads
+  static constexpr int NT = 256;  // threads
   static constexpr int C = kLinChunkF32, LK = KP + 4, LV = VP + 4, LC = C + 4;
-  float q[C * LK], k[C * LK], v[C * LV], d[C * LV], s[KP * LV], p[C * LC], chi[C], clo[C], into[C], rest[C];
+  float q[C * LK], d[C * LV], chi[C], clo[C], into[C], rest[C];
+  float k[C * LK], v[C * LV], s[KP * LV], p[C * LC];  // (these not for a sum)
   float a[4 * C], b[4 * C], rect[C], red[8];  // a, b: by the warp columns of a C x KP product
 };
 
@@ -35,7 +38,7 @@ struct BwdOut {
 // A CTA walks the chunks of one (batch row, head, segment) from the last to the
 // first with U in registers.  SUM only finds the segment's U from zero.
 template <int KP, int VP, bool SUM>
-__global__ void __launch_bounds__(BwdSmem<KP, VP>::NT) linattn_bwd_kernel(LinAttn p, const float* __restrict__ dout,
+__global__ void __launch_bounds__(256, KP == 64 && VP == 64 ? 2 : 1) linattn_bwd_kernel(LinAttn p, const float* __restrict__ dout,
                                                                           const float* __restrict__ ckpt, const float* __restrict__ u0,
                                                                           BwdOut out, float* __restrict__ uend, Dec* __restrict__ udec) {
   using Sm = BwdSmem<KP, VP>;
@@ -969,11 +972,12 @@ template <int KP, int VP>
 int bwd_f32(const BwdPlan& pl, const void* dout, const float* ckpt, const float* dh_last, const BwdOut& out, float* dg, char* ws,
             cudaStream_t s) {
   const unsigned grid = (unsigned)pl.p.B * pl.p.H * pl.p.nseg;
-  const size_t smem = sizeof(BwdSmem<KP, VP>);
+  using Sm = BwdSmem<KP, VP>;
+  const size_t smem = sizeof(Sm);
   return bwd_run<float>(
       pl, dh_last, out, dg, ws, s,
       [&](float* st, Dec* dec, const BwdOut& o) {
-        return lin_launch(linattn_bwd_kernel<KP, VP, true>, grid, BwdSmem<KP, VP>::NT, smem, s, pl.p, dout, ckpt, nullptr, o, st, dec);
+        return lin_launch(linattn_bwd_kernel<KP, VP, true>, grid, BwdSmem<KP, VP>::NT, offsetof(Sm, k), s, pl.p, dout, ckpt, nullptr, o, st, dec);
       },
       [&](const float* u0, const BwdOut& o) {
         return lin_launch(linattn_bwd_kernel<KP, VP, false>, grid, BwdSmem<KP, VP>::NT, smem, s, pl.p, dout, ckpt, u0, o, nullptr, nullptr);

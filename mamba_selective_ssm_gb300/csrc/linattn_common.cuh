@@ -147,13 +147,14 @@ inline int linattn_chunk(int dtype) { return dtype == SS_F32 ? kLinChunkF32 : kL
 // four chunks whose end states are found first, at the price of a second read of
 // half the inputs.  The tensor-core kernels hold an SM each: as many pieces as
 // leave every one of them its own.  The fp32 kernels share an SM (three forward,
-// two backward) and their time is arithmetic: below three CTAs an SM, enough
-// pieces for five, so that no SM is left with far more than its share (192 walks
-// of the 130M layer: XXX us for four pieces, YYY for one).
+// two backward) and their time is arithmetic: pieces
+// for three CTAs an SM, so that no SM is left with far more than its share (a
+// training step of the 130M layer, 192 walks: 1458 us for three pieces, 1594 for
+// six, 1862 for two).
 inline void linattn_segments(LinAttn& p, int dtype, long long walks) {
   const int chunk = linattn_chunk(dtype);
   p.nck = (p.L + chunk - 1) / chunk;
-  long long n = dtype == SS_F32 ? (walks >= 3 * 152 ? 1 : (5 * 152 + walks - 1) / walks) : 152 / walks;
+  long long n = dtype == SS_F32 ? (3 * 152 + walks - 1) / walks : 152 / walks;
   if (n > p.nck / 4) n = p.nck / 4;
   if (n < 1) n = 1;
   p.cps = (int)((p.nck + n - 1) / n);
@@ -205,7 +206,7 @@ inline int lin_launch(void (*kern)(KArgs...), unsigned grid, int threads, size_t
 // have the same owners, so they combine element by element in registers.
 template <int NT, int M, int N>
 struct Own {
-  static constexpr int TM = NT == 256 && M == 64 && N == 64 ? 16 : 32, WM = M / TM, WN = NT / 32 / WM, TN = N / WN;
+  static constexpr int TM = M * N == 64 * 64 ? 16 : 32, WM = M / TM, WN = NT / 32 / WM, TN = N / WN;
   static constexpr int RM = TM / 8, RN = TN / 4;
   static_assert(WM * WN * 32 == NT && WN * TN == N, "warps tile the product");
   __device__ __forceinline__ static int wn(int tid) { return (tid >> 5) % WN; }

@@ -1,4 +1,6 @@
 // Linear attention with a decay for each head, chunked forward (linattn_fwd) for sm_103a.
+#include <stddef.h>
+
 #include "linattn_tc.cuh"
 
 namespace {
@@ -10,9 +12,10 @@ constexpr int kVT = 64;
 
 template <int KP>
 struct FwdSmem {
-  static constexpr int NT = KP == 64 ? 128 : 256;  // threads
+  static constexpr int NT = 256;  // threads
   static constexpr int C = kLinChunkF32, LK = KP + 4, LV = kVT + 4, LC = C + 4;
-  float q[C * LK], k[C * LK], v[C * LV], s[KP * LV], chi[C], clo[C], rest[C];  // the scores take q's place
+  float k[C * LK], v[C * LV], chi[C], clo[C], rest[C];
+  float q[C * LK], s[KP * LV];  // (not for a sum) the scores take q's place
 };
 
 template <int KP, bool SUM>
@@ -472,7 +475,7 @@ int fwd_f32(const FwdPlan& pl, const float* h0, float* o, float* ckpt, float* h_
   const size_t smem = sizeof(FwdSmem<KP>);
   return fwd_run(
       pl, h0, ws, s,
-      [&](float* st, Dec* dec) { return lin_launch(linattn_fwd_kernel<KP, true>, grid, FwdSmem<KP>::NT, smem, s, pl.p, nullptr, o, ckpt, st, dec); },
+      [&](float* st, Dec* dec) { return lin_launch(linattn_fwd_kernel<KP, true>, grid, FwdSmem<KP>::NT, offsetof(FwdSmem<KP>, q), s, pl.p, nullptr, o, ckpt, st, dec); },
       [&](const float* s0) { return lin_launch(linattn_fwd_kernel<KP, false>, grid, FwdSmem<KP>::NT, smem, s, pl.p, s0, o, ckpt, h_last, nullptr); });
 }
 

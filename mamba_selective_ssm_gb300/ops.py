@@ -382,7 +382,7 @@ def _raw_stream(dev):
 
 def _at(t, name, shape, dtype, dev):
     """The address of a dense tensor of this shape, type and device (``_req``'s errors for any other)."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_cuda
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev.index
             and t.is_contiguous()):
         _req(t, name, shape, dtype, dev)
     return t.data_ptr()
@@ -396,7 +396,7 @@ def _rows(t, name, shape, dtype, dev):
     """A [B, L, heads, width] input whose tokens may lie further apart than their own rows (a column range of a
     wider [B, L, W] array): its address and its token stride in elements."""
     B, L, n, w = shape
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_cuda:
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.get_device() == dev.index:
         if t.is_contiguous():
             return t.data_ptr(), n * w
     elif not isinstance(t, torch.Tensor):
