@@ -218,10 +218,9 @@ __device__ __forceinline__ void prefetch_panels(int n, const CUtensorMap* m, int
 }
 // rows from `valid` on of `panels` panels become zero (one warp): a row that ends inside the tensor
 __device__ __forceinline__ void zero_rows(uint32_t tile, int panels, int valid, int lane) {
-  for (int i = lane; i < panels * (kTC - valid) * 8; i += 32) {
-    const int n = i / ((kTC - valid) * 8), at = i % ((kTC - valid) * 8);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + n * kPanel + valid * 128 + at * 16), "r"(0) : "memory");
-  }
+  for (int n = 0; n < panels; ++n)
+    for (int r = valid + (lane >> 3); r < kTC; r += 4)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + n * kPanel + r * 128 + (lane & 7) * 16), "r"(0) : "memory");
 }
 
 // 16 bytes global -> shared, asynchronously; zeros instead (nothing read) when !ok
