@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
   tc_fence_after_sync();
   const uint32_t tm = *tma;
   bool ok = true;
-  auto wait = [&](int i, uint32_t par) { return ok = mbar_wait_bounded(&bar[i], par, kWaitLimitNs); };
+  auto wait = [&](int i, uint32_t par) { return ok = lin_wait(&bar[i], par); };
 
   if (warp == kLinWarps) {  // ---- the issuing warp
     const int ks = (p.K + 15) / 16, vs = (p.V + 15) / 16;  // contraction steps over K and V

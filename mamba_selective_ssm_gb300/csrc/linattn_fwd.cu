@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
   tc_fence_after_sync();
   const uint32_t tm = *tma;
   bool ok = true;
-  auto wait = [&](int i, uint32_t par) { return ok = mbar_wait_bounded(&bar[i], par, kWaitLimitNs); };
+  auto wait = [&](int i, uint32_t par) { return ok = lin_wait(&bar[i], par); };
 
   if (warp == kLinWarps) {  // ---- the issuing warp
     const int ks = (p.K + 15) / 16;  // contraction steps over K
@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
         mma_steps(tm + L::P, Rows{sb + L::q}, Rows{sb + L::k}, mma_idesc(kTC, false, false), ks, false);
         mma_commit(&bar[L::kMp]);
       }
+      __syncwarp();
       if (!wait(L::kSt, par) || !wait(L::kRd, par)) break;
       if (lane == 0) {
         tc_fence_after_sync();
@@ -260,6 +261,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
           mma_steps(tm + L::Sn, Cols{sb + L::k}, Cols{sb + L::w + t * L::vt}, mma_idesc(VP, true, true), kTC / 16, t < 2);
         mma_commit(&bar[L::kMs]);
       }
+      __syncwarp();
       if (!wait(L::kSc, par)) break;
       if (lane == 0) {
         tc_fence_after_sync();

@@ -310,6 +310,14 @@ inline int read_clear_lin_err(cudaStream_t s, unsigned* out) {
   return cudaStreamSynchronize(s) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
+// A whole warp waits for a phase of a barrier, and leaves together: tensor-memory
+// accesses want the warp converged, and a warp's uniform registers (an MMA's
+// descriptors, a copy's coordinates) are not a lane's own, so no lane may run on
+// while another issues; every block that one lane issues ends with __syncwarp().
+__device__ __forceinline__ bool lin_wait(uint64_t* bar, uint32_t par) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, par, kWaitLimitNs));
+}
+
 // The end of a kernel of kLinThreads: a wait that ran out is told (the outputs
 // are invalid) and whatever is still in flight gets a limited wait, then the
 // tensor memory is returned.
@@ -375,7 +383,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_sum_tc_kernel(LinAttn 
   const uint32_t tm = *tma;
   bool ok = true;
   // barrier pair `i` for its place's turn m: the places take turns, so place m & 1 is at phase (m >> 1) & 1
-  auto wait = [&](int i, int m) { return ok = mbar_wait_bounded(&bar[i + (m & 1)], (uint32_t)(m >> 1) & 1u, kWaitLimitNs); };
+  auto wait = [&](int i, int m) { return ok = lin_wait(&bar[i + (m & 1)], (uint32_t)(m >> 1) & 1u); };
 
   if (warp == kLinWarps) {  // ---- the issuing warp
     auto load = [&](int i) {
