@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
     const uint32_t id128 = mma_idesc(128, false, false);
     // a chunk's tiles; their readers have passed a barrier that this warp has waited for, with a proxy fence before it
     auto load_qv = [&](int ck) {
-      if (lane == 0) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(&bar[L::kLd], 4 * kPanel + 2 * L::vt);  // k and do follow
         load_panels(sb + L::q, 2, &maps.q, &bar[L::kLd], 0, gh, ck * kTC, b);
         load_panels(sb + L::v, VP / 64, &maps.v, &bar[L::kLd], 0, h, ck * kTC, b);
@@ -415,11 +415,11 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
       __syncwarp();
     };
     auto load_d = [&](int ck) {
-      if (lane == 0) load_panels(sb + L::d, VP / 64, &maps.d, &bar[L::kLd], 0, h, ck * kTC, b);
+      if (elect_one()) load_panels(sb + L::d, VP / 64, &maps.d, &bar[L::kLd], 0, h, ck * kTC, b);
       __syncwarp();
     };
     auto load_k = [&](int ck) {
-      if (lane == 0) load_panels(sb + L::k, 2, &maps.k, &bar[L::kLd], 0, gh, ck * kTC, b);
+      if (elect_one()) load_panels(sb + L::k, 2, &maps.k, &bar[L::kLd], 0, gh, ck * kTC, b);
       __syncwarp();
     };
     if (c0 < cend) {
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
         __syncwarp();
       }
       if (ck < cend - 1 && !wait(L::kR6, par ^ 1u)) break;  // the accumulators' places take scores next
-      if (lane == 0) {
+      if (elect_one()) {
         tc_fence_after_sync();
         mma_steps(tm + L::T0, Rows{sb + L::k}, Rows{sb + L::q}, id128, ks, false);
         mma_steps(tm + L::T1, Rows{sb + L::v}, Rows{sb + L::d}, id128, vs, false);
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
       }
       __syncwarp();
       if (!wait(L::kR1, par)) break;
-      if (lane == 0) {
+      if (elect_one()) {
         tc_fence_after_sync();
 #pragma unroll
         for (int t = 2; t >= 0; --t)  // the smallest term first
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
       }
       __syncwarp();
       if (!wait(L::kR3, par)) break;
-      if (lane == 0) {
+      if (elect_one()) {
         tc_fence_after_sync();
         mma_steps(tm + L::T0, Rows{sb + L::k}, Cols{sb + L::y0}, mma_idesc(VP, false, true), ks, false);
 #pragma unroll
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
       }
       __syncwarp();
       if (!wait(L::kR4, par)) break;
-      if (lane == 0) {
+      if (elect_one()) {
         tc_fence_after_sync();
 #pragma unroll
         for (int s = 0; s < kTC / 16; ++s) mma_ts(tm + L::T0, tm + L::Pb + s * 8, desc_cols(sb + L::d, s), mma_idesc(VP, false, true), true);

@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
     const int ks = (p.K + 15) / 16;  // contraction steps over K
     // a chunk's tiles; their readers have passed a barrier that this warp has waited for, with a proxy fence before it
     auto load_qk = [&](int ck) {
-      if (lane == 0) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(&bar[L::kLq], 4 * kPanel);
         load_panels(sb + L::q, 2, &maps.q, &bar[L::kLq], 0, gh, ck * kTC, b);
         load_panels(sb + L::k, 2, &maps.k, &bar[L::kLq], 0, gh, ck * kTC, b);
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
       __syncwarp();
     };
     auto load_v = [&](int ck) {
-      if (lane == 0) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(&bar[L::kLd], L::vt);
         load_panels(sb + L::v, VP / 64, &maps.v, &bar[L::kLd], 0, h, ck * kTC, b);
       }
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
       }
       __syncwarp();
       if (!wait(L::kSt, par) || !wait(L::kRd, par)) break;
-      if (lane == 0) {
+      if (elect_one()) {
         tc_fence_after_sync();
         mma_steps(tm + L::O, Rows{sb + L::q}, Cols{sb + L::s}, mma_idesc(VP, false, true), ks, false);
         mma_commit(&bar[L::kMo]);
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
         fence_proxy_async_smem();
         __syncwarp();
       }
-      if (lane == 0) {
+      if (elect_one()) {
         tc_fence_after_sync();
 #pragma unroll
         for (int t = 2; t >= 0; --t)  // the smallest term first
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
       }
       __syncwarp();
       if (!wait(L::kSc, par)) break;
-      if (lane == 0) {
+      if (elect_one()) {
         tc_fence_after_sync();
 #pragma unroll
         for (int s = 0; s < kTC / 16; ++s)

@@ -114,6 +114,15 @@ __device__ __forceinline__ uint32_t mma_idesc(int n, bool a_cols, bool b_cols) {
          ((128u >> 4) << 24);
 }
 
+// True in one thread of a converged warp.  What that thread then issues takes its
+// operands from the warp's uniform registers; behind a test of the lane's number
+// the compiler cannot know that one thread is left (an MMA took 100 cycles to issue).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // D (tensor memory) = A B (+ D); one thread issues
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
@@ -387,7 +396,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_sum_tc_kernel(LinAttn 
 
   if (warp == kLinWarps) {  // ---- the issuing warp
     auto load = [&](int i) {
-      if (lane == 0) {
+      if (elect_one()) {
         uint64_t* bl = &bar[L::kLd + (i & 1)];
         mbar_arrive_expect_tx(bl, 3 * kPanel);
         load_panels(sb + L::x + (i & 1) * 2 * kPanel, 2, &mx, bl, 0, gh, chunk(i) * kTC, b);
@@ -407,7 +416,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_sum_tc_kernel(LinAttn 
         __syncwarp();
       }
       if (!wait(L::kW, i)) break;
-      if (lane == 0) {
+      if (elect_one()) {
         tc_fence_after_sync();
         mma_steps(tm + (i & 1) * 256, Cols{x}, Cols{sb + L::w + (i & 1) * 3 * kPanel}, mma_idesc(192, true, true), kTC / 16, false);
         mma_commit(&bar[L::kM + (i & 1)]);
