@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
       }
       __syncwarp();
       if (!wait(L::kM3, par)) break;
-      if (lane == 0) {  // into the scores' place, whose readers are done
+      if (elect_one()) {  // into the scores' place, whose readers are done
         tc_fence_after_sync();
 #pragma unroll
         for (int t = 2; t >= 0; --t)

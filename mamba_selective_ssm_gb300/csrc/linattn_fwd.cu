@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
         fence_proxy_async_smem();
         __syncwarp();
       }
-      if (lane == 0) {  // the scores of the chunk before have been read: its kSc has been waited for
+      if (elect_one()) {  // the scores of the chunk before have been read: its kSc has been waited for
         tc_fence_after_sync();
         mma_steps(tm + L::P, Rows{sb + L::q}, Rows{sb + L::k}, mma_idesc(kTC, false, false), ks, false);
         mma_commit(&bar[L::kMp]);
