@@ -141,24 +141,31 @@ __global__ void __launch_bounds__(FwdSmem<KP>::NT) linattn_fwd_kernel(LinAttn p,
 //
 // Sixteen warps compute; one issues the TMA loads and the MMAs (whose issue
 // blocks while the tensor cores are behind), one finds the next chunk's decays.
-// They meet at mbarriers only, so that the products of the state run under the
-// scaling of the scores, and the next chunk's loads under this one's output.
-// All of V in one CTA: with 64 columns a CTA and two CTAs an SM the scores were
-// made and scaled twice and the narrow products waited for shared memory
-// (1.4B-shaped prefill 114 us).
+// They meet at mbarriers only: the products of the state run under the scaling
+// of the scores, v has two tiles so that the next chunk's w v begins under this
+// one's output, and the third term of w v waits in tensor memory for the state's
+// tile to be free.  o is staged in the chunk's tile of v and sent from there by
+// TMA, behind the next chunk's products (copied out by the computing warps it
+// held up the state: 2700 of a chunk's 9100 cycles).
+// Measured: 75 us for 4 x 2048 tokens of 32 heads of 128 x 128 with 32 heads of k,
+// 54 % of the copy bandwidth; a chunk takes 9100 cycles of which the chain
+// w v -> Sn -> S -> its tile -> q S -> o binds 6400.  All of V in one CTA: with 64 columns a CTA and two CTAs an SM
+// the scores were made and scaled twice and the narrow products waited for
+// shared memory (114 us).
 template <int VP>
 struct FwdTc {
   static constexpr int vt = kTC * VP * 2;  // bytes of a tile VP columns wide
-  static constexpr int q = 0, k = q + 2 * kPanel, v = k + 2 * kPanel, s = v + vt, w = s + vt, dec = w + 3 * vt;
-  // barriers: v landed, q and k landed, decays stored; w v stored; scores stored and O scaled; state tile stored; O read;
-  // P, O, Sn, O + P v done
-  static constexpr int kLd = 0, kW = 1, kSc = 2, kSt = 3, kRd = 4, kMp = 5, kMo = 6, kMs = 7, kM1 = 8, kLq = 9, kDc = 10, nbar = 11;
+  static constexpr int q = 0, k = q + 2 * kPanel, v = k + 2 * kPanel, w = v + 2 * vt, s = w + 2 * vt, dec = s + vt;
+  // barriers: v (two tiles), q, k landed, decays stored; two terms of w v stored; scores and third term stored and O scaled;
+  // state tile stored; O read; P, O, Sn, O + P v done
+  static constexpr int kLv = 0, kLq = 2, kLk = 3, kDc = 4, kMp = 5, kMo = 6, kMs = 7, kM1 = 8, kW = 9, kSc = 10, kSt = 11, kRd = 12, nbar = 13;
   static constexpr int bar = dec + DecTile::bytes, tm = bar + nbar * 8, bytes = tm + 8;
-  static constexpr int P = 0, Pb = 128, O = 192, Sn = 192 + VP, cols = 512;  // tensor memory columns
+  // tensor memory columns.  VP = 64: the first two terms side by side are one product of 128 columns, Sn has three parts
+  static constexpr int P = 0, Pb = 128, O = 192, Sn = 192 + VP, Wp = VP == 64 ? Sn + 192 : Sn + 128, cols = 512;
 };
 
 struct FwdMaps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o;
 };
 
 template <int VP>
@@ -184,7 +191,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
   cend = cend < c0 ? c0 : cend < c1 ? cend : c1;
 
   if (tid == 0) {
-    for (int i = 0; i < L::nbar; ++i) mbar_init(&bar[i], i >= L::kW && i <= L::kRd ? kLinWarps : 1);
+    for (int i = 0; i < L::nbar; ++i) mbar_init(&bar[i], i >= L::kW ? kLinWarps : 1);
     fence_barrier_init();
   }
   if (warp == 0) {
@@ -201,30 +208,48 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
   if (warp == kLinWarps) {  // ---- the issuing warp
     const int ks = (p.K + 15) / 16;  // contraction steps over K
     // a chunk's tiles; their readers have passed a barrier that this warp has waited for, with a proxy fence before it
-    auto load_qk = [&](int ck) {
+    auto load_q = [&](int ck) {
       if (elect_one()) {
-        mbar_arrive_expect_tx(&bar[L::kLq], 4 * kPanel);
+        mbar_arrive_expect_tx(&bar[L::kLq], 2 * kPanel);
         load_panels(sb + L::q, 2, &maps.q, &bar[L::kLq], 0, gh, ck * kTC, b);
-        load_panels(sb + L::k, 2, &maps.k, &bar[L::kLq], 0, gh, ck * kTC, b);
+      }
+      __syncwarp();
+    };
+    auto load_k = [&](int ck) {
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&bar[L::kLk], 2 * kPanel);
+        load_panels(sb + L::k, 2, &maps.k, &bar[L::kLk], 0, gh, ck * kTC, b);
       }
       __syncwarp();
     };
     auto load_v = [&](int ck) {
+      const int at = (ck - c0) & 1;
       if (elect_one()) {
-        mbar_arrive_expect_tx(&bar[L::kLd], L::vt);
-        load_panels(sb + L::v, VP / 64, &maps.v, &bar[L::kLd], 0, h, ck * kTC, b);
+        mbar_arrive_expect_tx(&bar[L::kLv + at], L::vt);
+        load_panels(sb + L::v + at * L::vt, VP / 64, &maps.v, &bar[L::kLv + at], 0, h, ck * kTC, b);
+      }
+      __syncwarp();
+    };
+    // (bulk groups belong to the thread that committed them: the elected one is always the same)
+    auto store_o = [&](int ck) {  // a chunk's o, staged in its tile of v
+      if (elect_one()) {
+        for (int i = 0; i < (p.V + 63) / 64; ++i)
+          tma_store_4d(&maps.o, sb + L::v + ((ck - c0) & 1) * L::vt + i * kPanel, i * 64, h, ck * kTC, b);
+        bulk_commit();
       }
       __syncwarp();
     };
     if (c0 < cend) {
-      load_qk(c0);
       load_v(c0);
+      load_q(c0);
+      load_k(c0);
     }
     for (int ck = c0; ck < cend; ++ck) {
       const uint32_t par = (uint32_t)(ck - c0) & 1u;
+      const uint32_t vtile = L::v + par * L::vt;
       const int valid = len - ck * kTC;
       const bool more = ck + 1 < cend, cut = valid < kTC && ck * kTC + valid < p.L;
-      if (!wait(L::kLq, par)) break;
+      if (!wait(L::kLq, par) || !wait(L::kLk, par)) break;
       if (cut) {  // the row ends inside the tensor: what follows is not its own
         zero_rows(sb + L::q, 4, valid, lane);
         fence_proxy_async_smem();
@@ -237,47 +262,61 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
       }
       __syncwarp();
       if (!wait(L::kSt, par) || !wait(L::kRd, par)) break;
+      if (ck > c0) store_o(ck - 1);
       if (elect_one()) {
         tc_fence_after_sync();
         mma_steps(tm + L::O, Rows{sb + L::q}, Cols{sb + L::s}, mma_idesc(VP, false, true), ks, false);
         mma_commit(&bar[L::kMo]);
-        if (more) {  // the next chunk towards L2
-          prefetch_panels((p.K + 63) / 64, &maps.q, 0, gh, (ck + 1) * kTC, b);
-          prefetch_panels((p.K + 63) / 64, &maps.k, 0, gh, (ck + 1) * kTC, b);
-          prefetch_panels((p.V + 63) / 64, &maps.v, 0, h, (ck + 1) * kTC, b);
-        }
       }
       __syncwarp();
       if (!wait(L::kW, par)) break;
       if (cut) {  // (the v tile's other readers take its dead rows as zero)
-        zero_rows(sb + L::v, VP / 64, valid, lane);
+        zero_rows(sb + vtile, VP / 64, valid, lane);
         fence_proxy_async_smem();
         __syncwarp();
       }
       if (elect_one()) {
         tc_fence_after_sync();
-#pragma unroll
-        for (int t = 2; t >= 0; --t)  // the smallest term first
-          mma_steps(tm + L::Sn, Cols{sb + L::k}, Cols{sb + L::w + t * L::vt}, mma_idesc(VP, true, true), kTC / 16, t < 2);
-        mma_commit(&bar[L::kMs]);
+        if constexpr (VP == 64) {
+          mma_steps(tm + L::Sn, Cols{sb + L::k}, Cols{sb + L::w}, mma_idesc(128, true, true), kTC / 16, false);
+        } else {
+          mma_steps(tm + L::Sn, Cols{sb + L::k}, Cols{sb + L::w + L::vt}, mma_idesc(VP, true, true), kTC / 16, false);
+          mma_steps(tm + L::Sn, Cols{sb + L::k}, Cols{sb + L::w}, mma_idesc(VP, true, true), kTC / 16, true);
+        }
       }
       __syncwarp();
+      if (!wait(L::kMo, par)) break;
+      if (more) {
+        load_q(ck + 1);
+        if (elect_one()) bulk_wait_read();  // v's place held the o of the chunk before
+        __syncwarp();
+        load_v(ck + 1);
+      }
       if (!wait(L::kSc, par)) break;
       if (elect_one()) {
         tc_fence_after_sync();
+        mma_steps(tm + L::Sn + (VP == 64 ? 128 : 0), Cols{sb + L::k}, Cols{sb + L::s}, mma_idesc(VP, true, true), kTC / 16, VP != 64);
+        mma_commit(&bar[L::kMs]);
 #pragma unroll
         for (int s = 0; s < kTC / 16; ++s)
-          mma_ts(tm + L::O, tm + L::Pb + s * 8, desc_cols(sb + L::v, s), mma_idesc(VP, false, true), true);
+          mma_ts(tm + L::O, tm + L::Pb + s * 8, desc_cols(sb + vtile, s), mma_idesc(VP, false, true), true);
         mma_commit(&bar[L::kM1]);
       }
       __syncwarp();
       if (more) {
         if (!wait(L::kMs, par)) break;
-        load_qk(ck + 1);
-        if (!wait(L::kM1, par)) break;
-        load_v(ck + 1);
+        load_k(ck + 1);
+        if (ck + 2 < cend && elect_one()) {  // the chunk after it towards L2
+          prefetch_panels((p.V + 63) / 64, &maps.v, 0, h, (ck + 2) * kTC, b);
+          prefetch_panels((p.K + 63) / 64, &maps.q, 0, gh, (ck + 2) * kTC, b);
+          prefetch_panels((p.K + 63) / 64, &maps.k, 0, gh, (ck + 2) * kTC, b);
+        }
+        __syncwarp();
       }
     }
+    if (ok && c0 < cend && wait(L::kRd, (uint32_t)(cend - c0) & 1u)) store_o(cend - 1);
+    if (elect_one()) bulk_wait();
+    __syncwarp();
   } else if (warp > kLinWarps) {  // ---- the decays' warp: a chunk ahead, stored when the chunk before has read its own
     DecStage ds;
     ds.g.fetch(p, b, h, c0 * kTC, len, lane);
@@ -325,22 +364,28 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
     for (int ck = c0; ck < cend; ++ck) {
       const uint32_t par = (uint32_t)(ck - c0) & 1u;
       const int t0 = ck * kTC, valid = len - t0;
-      if (!wait(L::kDc, par) || !wait(L::kLd, par)) break;
+      const uint32_t vtile = sb + L::v + par * L::vt;
+      if (!wait(L::kDc, par) || !wait(L::kLv + (int)par, (uint32_t)((ck - c0) >> 1) & 1u)) break;
       const Dec last = dec.get(kTC - 1), own = dec.get(row);
       const float elast = dec_exp(last);
       {
         const float wj = dec_exp(dec_sub(last, own));
+        uint32_t third[NU * 4];
 #pragma unroll
         for (int u = 0; u < NU; ++u) {  // w v of this thread's token
           const uint32_t at = tile_at(row, cq * NU + u);
           float x[8];
-          Raw8<__nv_bfloat16>::wide(row < valid ? lds16(sb + L::v + at) : make_uint4(0u, 0u, 0u, 0u), x);
+          Raw8<__nv_bfloat16>::wide(row < valid ? lds16(vtile + at) : make_uint4(0u, 0u, 0u, 0u), x);
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] *= wj;
           sts16(sb + L::w + at, take_term(x));
           sts16(sb + L::w + L::vt + at, take_term(x));
-          sts16(sb + L::w + 2 * L::vt + at, last_term(x));
+          const uint4 t = last_term(x);
+          third[4 * u] = t.x; third[4 * u + 1] = t.y; third[4 * u + 2] = t.z; third[4 * u + 3] = t.w;
         }
+        __syncwarp();
+        tmem_stn(tl + L::Wp + cq * NU * 4, third);
+        tmem_wait_st();
         arrive(L::kW);
       }
       if (!wait(L::kMp, par)) break;
@@ -378,6 +423,14 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
       }
       if (!wait(L::kMo, par)) break;
       tc_fence_after_sync();
+      {  // the state's tile has been read: the third term takes it
+        uint32_t third[NU * 4];
+        tmem_ldn(tl + L::Wp + cq * NU * 4, third);
+        tmem_wait_ld();
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+          sts16(sb + L::s + tile_at(row, cq * NU + u), make_uint4(third[4 * u], third[4 * u + 1], third[4 * u + 2], third[4 * u + 3]));
+      }
       tmem_scale<VQ>(tl + L::O + cq * VQ, dec_exp(own));
       tmem_wait_st();
       arrive(L::kSc);
@@ -391,8 +444,19 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
       tc_fence_after_sync();
       {
         uint32_t r[VQ];
-        tmem_ldn(tl + L::Sn + cq * VQ, r);
-        tmem_wait_ld();
+        if constexpr (VP == 64) {
+          uint32_t r1[VQ], r2[VQ];
+          tmem_ldn(tl + L::Sn + cq * VQ, r);
+          tmem_ldn(tl + L::Sn + 64 + cq * VQ, r1);
+          tmem_ldn(tl + L::Sn + 128 + cq * VQ, r2);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < VQ; ++e)
+            r[e] = __float_as_uint(__uint_as_float(r[e]) + (__uint_as_float(r1[e]) + __uint_as_float(r2[e])));
+        } else {
+          tmem_ldn(tl + L::Sn + cq * VQ, r);
+          tmem_wait_ld();
+        }
 #pragma unroll
         for (int e = 0; e < VQ; ++e) S[e] = fmaf(S[e], elast, __uint_as_float(r[e]));
       }
@@ -402,22 +466,18 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_fwd_tc_kernel(LinAttn 
       }
       if (!wait(L::kM1, par)) break;
       tc_fence_after_sync();
-      {  // o through this warp's part of the first term's tile: a lane's accumulators are one row, whole rows leave
+      {  // o into v's place (P v is done); the issuing warp sends it from there
         uint32_t r[VQ];
         tmem_ldn(tl + L::O + cq * VQ, r);
         tmem_wait_ld();
-        if (ck + 1 < cend) arrive(L::kRd);
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
           float x[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] = row < valid ? p.scale * __uint_as_float(r[8 * u + e]) : 0.f;
-          sts16(sb + L::w + tile_at(row, cq * NU + u), pack8(x));
+          sts16(vtile + tile_at(row, cq * NU + u), pack8(x));
         }
-        __syncwarp();
-        store_rows<NU>(sb + L::w, o + (((long long)b * p.L + t0) * p.H + h) * p.V, (long long)p.H * p.V, (warp & 3) * 32, cq * NU,
-                       p.L - t0, p.V, lane);
-        __syncwarp();
+        arrive(L::kRd);
       }
     }
     if (ok) {
@@ -487,7 +547,7 @@ int fwd_bf16(const FwdPlan& pl, const float* h0, __nv_bfloat16* o, float* ckpt, 
   const unsigned grid = (unsigned)pl.walks * p.nseg;
   FwdMaps maps;
   if (!lin_map(&maps.q, p.q, p.ldq, p.B, p.L, p.G, p.K) || !lin_map(&maps.k, p.k, p.ldk, p.B, p.L, p.G, p.K) ||
-      !lin_map(&maps.v, p.v, p.ldv, p.B, p.L, p.H, p.V))
+      !lin_map(&maps.v, p.v, p.ldv, p.B, p.L, p.H, p.V) || !lin_map(&maps.o, o, (long long)p.H * p.V, p.B, p.L, p.H, p.V))
     return SS_ERR_CUDA;
   return fwd_run(
       pl, h0, ws, s,
