@@ -326,7 +326,10 @@ __global__ void __launch_bounds__(256, KP == 64 && VP == 64 ? 2 : 1) linattn_bwd
 // a term of dq, dk or dv is rounded to bf16 once on its way.
 //
 // Sixteen warps compute, one issues the TMA loads and the MMAs, one finds the
-// decays; they meet at mbarriers, as in the forward.
+// decays; they meet at mbarriers, as in the forward.  dv, dq and dk are copied out
+// by way of dP^T's tile, each warp through a part of its own, while the next k and
+// do land (sent by TMA from the tiles of do, dP^T and k they held these for 5000
+// cycles: 377 us for a training step of 4 x 2048 tokens of 32 heads of 128 x 128).
 template <int VP>
 struct BwdTc {
   static constexpr int vt = kTC * VP * 2;  // bytes of a tile VP columns wide
@@ -335,11 +338,12 @@ struct BwdTc {
   static constexpr int y2 = VP == 64 ? y1 + vt : x, dec = VP == 64 ? y2 + vt : y1 + vt;
   // scale e^{c_i - c of the end of the block of 32 before}; column sums of M by (quarter, block of rows up to it); <S_in, U> by
   // warp; dg of a chunk by quarter
-  static constexpr int into = dec + DecTile::bytes, rect = into + kTC * 4, thr = rect + 10 * 32 * 4, hsum = thr + kLinWarps * 4;
-  // barriers: tiles landed, decays stored; MMA groups done; S terms, U terms and scores, last operands stored; the tiles of do
-  // and of k out; accumulators read
-  static constexpr int kLd = 0, kDc = 1, kM0 = 2, kM1 = 3, kM2 = 4, kM3 = 5, kM4 = 6, kR1 = 7, kR3 = 8, kR4 = 9, kRd = 10, kRk = 11, kR6 = 12, nbar = 13;
-  static constexpr int bar = hsum + 64, tm = bar + nbar * 8, bytes = tm + 8;
+  static constexpr int into = dec + DecTile::bytes, rect = into + kTC * 4, thr = rect + 10 * 32 * 4, hsum = thr + kLinWarps * 4;  // hsum: twice
+  // barriers: tiles landed, decays stored; MMA groups done; S terms, U terms and scores, last operands stored; accumulators read;
+  // parts of dg stored; their sums by quarter, and by chunk (warps 0 .. 3)
+  static constexpr int kLd = 0, kDc = 1, kM0 = 2, kM1 = 3, kM2 = 4, kM3 = 5, kM4 = 6, kR1 = 7, kR3 = 8, kR4 = 9, kR6 = 10, kPt = 11, kEx = 12,
+                       kEs = 13, nbar = 14;
+  static constexpr int bar = hsum + 160, tm = bar + nbar * 8, bytes = tm + 8;
   static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
   static constexpr int T0 = 0, T1 = 128, T2 = 256, T3 = 384, Pb = 384, dPb = 448, cols = 512;
 };
@@ -388,7 +392,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
   cend = cend < c0 ? c0 : cend < c1 ? cend : c1;
 
   if (tid == 0) {
-    for (int i = 0; i < L::nbar; ++i) mbar_init(&bar[i], i >= L::kR1 ? kLinWarps : 1);
+    for (int i = 0; i < L::nbar; ++i) mbar_init(&bar[i], i >= L::kEx ? 4 : i >= L::kR1 ? kLinWarps : 1);
     fence_barrier_init();
   }
   if (warp == 0) {
@@ -406,26 +410,24 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
     const int ks = (p.K + 15) / 16, vs = (p.V + 15) / 16;  // contraction steps over K and V
     const uint32_t id128 = mma_idesc(128, false, false);
     // a chunk's tiles; their readers have passed a barrier that this warp has waited for, with a proxy fence before it
+    auto load_kd = [&](int ck) {
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&bar[L::kLd], 4 * kPanel + 2 * L::vt);  // q and v follow
+        load_panels(sb + L::k, 2, &maps.k, &bar[L::kLd], 0, gh, ck * kTC, b);
+        load_panels(sb + L::d, VP / 64, &maps.d, &bar[L::kLd], 0, h, ck * kTC, b);
+      }
+      __syncwarp();
+    };
     auto load_qv = [&](int ck) {
       if (elect_one()) {
-        mbar_arrive_expect_tx(&bar[L::kLd], 4 * kPanel + 2 * L::vt);  // k and do follow
         load_panels(sb + L::q, 2, &maps.q, &bar[L::kLd], 0, gh, ck * kTC, b);
         load_panels(sb + L::v, VP / 64, &maps.v, &bar[L::kLd], 0, h, ck * kTC, b);
       }
       __syncwarp();
     };
-    auto load_d = [&](int ck) {
-      if (elect_one()) load_panels(sb + L::d, VP / 64, &maps.d, &bar[L::kLd], 0, h, ck * kTC, b);
-      __syncwarp();
-    };
-    auto load_k = [&](int ck) {
-      if (elect_one()) load_panels(sb + L::k, 2, &maps.k, &bar[L::kLd], 0, gh, ck * kTC, b);
-      __syncwarp();
-    };
     if (c0 < cend) {
+      load_kd(cend - 1);
       load_qv(cend - 1);
-      load_d(cend - 1);
-      load_k(cend - 1);
     }
     for (int ck = cend - 1; ck >= c0; --ck) {
       const uint32_t par = (uint32_t)(cend - 1 - ck) & 1u;
@@ -491,12 +493,9 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
       }
       __syncwarp();
       if (ck > c0) {
+        load_kd(ck - 1);
         if (!wait(L::kM4, par)) break;
         load_qv(ck - 1);
-        if (!wait(L::kRd, par)) break;
-        load_d(ck - 1);
-        if (!wait(L::kRk, par)) break;
-        load_k(ck - 1);
       }
     }
   } else if (warp > kLinWarps) {  // ---- the decays' warp
@@ -585,18 +584,74 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
       tmem_st32(tl + t + cq * 32, r);
       return dot;
     };
-    // typed gradients through this warp's part of a tile whose product is done
-    auto stage = [&](const uint32_t* r, int u0, int n, uint32_t tile, bool live) {
+    // typed gradients of this token (this quarter of them), by way of this warp's part of x, whose product is done
+    auto put_rows = [&](void* dst, auto& r, int width, int ck, bool live) {
+      constexpr int n = sizeof(r) / 32;
 #pragma unroll
       for (int u = 0; u < n; ++u) {
         float x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = live ? __uint_as_float(r[8 * u + e]) : 0.f;
-        sts16(sb + tile + tile_at(row, u0 + u), pack8(x));
+        sts16(sb + L::x + tile_at(row, cq * 4 + u), pack8(x));
       }
+      __syncwarp();
+      store_rows<n>(sb + L::x, static_cast<__nv_bfloat16*>(dst) + (((long long)b * p.L + ck * kTC) * p.H + h) * width, (long long)p.H * width,
+                    (warp & 3) * 32, cq * 4, cq * n, p.L - ck * kTC, width, lane);
       __syncwarp();
     };
 
+    // dg of a chunk's tokens t = 32 warp + lane (warps 0 .. 3), from what their warps took when its accumulators were done
+    float in = 0.f, th = 0.f, in_e = 0.f, fa = 0.f, fb = 0.f, q1 = 0.f, q2 = 0.f, q3 = 0.f;
+    auto sum_dg = [&](int ck) {
+      const int t0 = ck * kTC;
+      const uint32_t par = (uint32_t)(cend - 1 - ck) & 1u;
+      const bool live = row < len - t0;
+      float ra = fa, rb = fb + (warp == 0 ? q1 : warp == 1 ? q2 : warp == 2 ? q3 : 0.f);  // running sums within the warp's tokens
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float ua = __shfl_down_sync(0xffffffffu, ra, o), ub = __shfl_up_sync(0xffffffffu, rb, o);
+        if (lane + o < 32) ra += ua;
+        if (lane >= o) rb += ub;
+      }
+      // what other quarters of tokens need of this one: its sum of fa (for those before), of fb and of the paths to quarters after c
+      // (for quarter c after it)
+      float sa = fa, s2 = fb + q2, s3 = fb + q3, s4 = fb;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        sa += __shfl_xor_sync(0xffffffffu, sa, o);
+        s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+        s3 += __shfl_xor_sync(0xffffffffu, s3, o);
+        s4 += __shfl_xor_sync(0xffffffffu, s4, o);
+        th += __shfl_xor_sync(0xffffffffu, th, o);
+      }
+      float* ex = reinterpret_cast<float*>(raw + L::hsum) + par * 20;  // [quarter][4], then the quarters' dg
+      if (lane == 0) {
+        ex[warp * 4] = sa; ex[warp * 4 + 1] = s2; ex[warp * 4 + 2] = s3; ex[warp * 4 + 3] = s4;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[L::kEx]);
+      if (!wait(L::kEx, par)) return;
+      float after = 0.f, before = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        if (w > warp) after += ex[w * 4];
+        if (w < warp) before += ex[w * 4 + warp];  // warp 1, 2, 3: the paths that cross into it
+      }
+      const float up = __shfl_up_sync(0xffffffffu, rb, 1);
+      const float g = in + (after + ra) + (before + (lane > 0 ? up : 0.f)) + in_e * th;
+      if (!p.g_head) {
+        if (t0 + row < p.L) out.dg[((long long)b * p.L + t0 + row) * p.H + h] = live ? g : 0.f;
+      } else {
+        float s = live ? g : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) ex[16 + warp] = s;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[L::kEs]);
+        if (warp == 0 && wait(L::kEs, par) && lane == 0)
+          out.dg[((long long)b * p.nck + ck) * p.H + h] = (ex[16] + ex[17]) + (ex[18] + ex[19]);
+      }
+    };
     for (int ck = cend; ck < c1; ++ck) {  // past the row's end
       const int rows = p.L - ck * kTC < kTC ? p.L - ck * kTC : kTC;
       const long long at = ((long long)b * p.L + ck * kTC) * p.H + h;
@@ -660,33 +715,42 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
           tmem_wait_ld();
           if (!diag) {
 #pragma unroll
-            for (int e = 14; e >= 0; e -= 2) {
-              const float2 f = *reinterpret_cast<const float2*>(into_block + i0 + e);
-              const float w0 = f.x * from, w1 = f.y * from;
-              const float d0 = __uint_as_float(t[e]), d1 = __uint_as_float(t[e + 1]);
-              const float p0 = __uint_as_float(s[e]) * w0, p1 = __uint_as_float(s[e + 1]) * w1;
-              w[e / 2] = pack_bf16(p0, p1);
-              z[e / 2] = pack_bf16(d0 * w0, d1 * w1);
-              tot = fmaf(p1, d1, tot);  // paths from j to this query token or a later one of the quarter
-              m[e + 1] = tot;
-              tot = fmaf(p0, d0, tot);
-              m[e] = tot;
+            for (int e = 12; e >= 0; e -= 4) {
+              const float4 f = *reinterpret_cast<const float4*>(into_block + i0 + e);
+              const float wt[4] = {f.x * from, f.y * from, f.z * from, f.w * from};
+              float pp[4], dp[4];
+#pragma unroll
+              for (int n = 3; n >= 0; --n) {
+                const float d = __uint_as_float(t[e + n]);
+                pp[n] = __uint_as_float(s[e + n]) * wt[n];
+                dp[n] = d * wt[n];
+                tot = fmaf(pp[n], d, tot);  // paths from j to this query token or a later one of the quarter
+                m[e + n] = tot;
+              }
+              w[e / 2] = pack_bf16(pp[0], pp[1]);
+              w[e / 2 + 1] = pack_bf16(pp[2], pp[3]);
+              z[e / 2] = pack_bf16(dp[0], dp[1]);
+              z[e / 2 + 1] = pack_bf16(dp[2], dp[3]);
             }
           } else {
 #pragma unroll
-            for (int e = 14; e >= 0; e -= 2) {
-              const int i = g * 16 + e;
-              const Dec a = dec.rel(i0 + e), c = dec.rel(i0 + e + 1);
-              const float w0 = i >= lane ? p.scale * dec_diff(a.hi, a.lo, orel.hi, orel.lo) : 0.f;
-              const float w1 = i + 1 >= lane ? p.scale * dec_diff(c.hi, c.lo, orel.hi, orel.lo) : 0.f;
-              const float d0 = i >= lane ? __uint_as_float(t[e]) : 0.f, d1 = i + 1 >= lane ? __uint_as_float(t[e + 1]) : 0.f;
-              const float p0 = i >= lane ? __uint_as_float(s[e]) * w0 : 0.f, p1 = i + 1 >= lane ? __uint_as_float(s[e + 1]) * w1 : 0.f;
-              w[e / 2] = pack_bf16(p0, p1);
-              z[e / 2] = pack_bf16(d0 * w0, d1 * w1);
-              tot = fmaf(p1, d1, tot);
-              m[e + 1] = i + 1 > lane ? tot : 0.f;
-              tot = fmaf(p0, d0, tot);
-              m[e] = i > lane ? tot : 0.f;
+            for (int e = 12; e >= 0; e -= 4) {
+              float hi[4], lo[4], pp[4], dp[4];
+              dec.rel4(i0 + e, hi, lo);
+#pragma unroll
+              for (int n = 3; n >= 0; --n) {
+                const int i = g * 16 + e + n;
+                const float wt = i >= lane ? p.scale * dec_diff(hi[n], lo[n], orel.hi, orel.lo) : 0.f;
+                const float d = i >= lane ? __uint_as_float(t[e + n]) : 0.f;
+                pp[n] = (i >= lane ? __uint_as_float(s[e + n]) : 0.f) * wt;
+                dp[n] = d * wt;
+                tot = fmaf(pp[n], d, tot);
+                m[e + n] = i > lane ? tot : 0.f;
+              }
+              w[e / 2] = pack_bf16(pp[0], pp[1]);
+              w[e / 2 + 1] = pack_bf16(pp[2], pp[3]);
+              z[e / 2] = pack_bf16(dp[0], dp[1]);
+              z[e / 2 + 1] = pack_bf16(dp[2], dp[3]);
             }
           }
           tmem_st8u(tl + L::Pb + i0 / 2, w);
@@ -707,7 +771,8 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
       tmem_wait_st();
       arrive(L::kR3);
       const float dot_a = scale_dot(L::T2, L::q, into, live);  // under the products of U
-      if (!wait(L::kM2, par)) break;
+      if (warp < 4 && ck < cend - 1) sum_dg(ck + 1);
+      if (!ok || !wait(L::kM2, par)) break;
       tc_fence_after_sync();
       // operands of the last products: dP^T in shared memory, scale e^{c_i} do in three terms (the third in v's place)
       {
@@ -744,23 +809,14 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
         uint32_t r[VQ];
         tmem_ldn(tl + L::T0 + cq * VQ, r);
         tmem_wait_ld();
-        stage(r, cq * NU, NU, L::d, live);
-        store_rows<NU>(sb + L::d, static_cast<__nv_bfloat16*>(out.dv) + (((long long)b * p.L + t0) * p.H + h) * p.V, (long long)p.H * p.V,
-                       (warp & 3) * 32, cq * NU, p.L - t0, p.V, lane);
+        put_rows(out.dv, r, p.V, ck, live);
       }
-      arrive(L::kRd);
       {
-        const long long at = (((long long)b * p.L + t0) * p.H + h) * p.K;
         uint32_t r[32];
         tmem_ld32(tl + L::T2 + cq * 32, r);
         tmem_wait_ld();
-        if (shared) {
-          put_part(out.dqp, ck, r, live);
-        } else {
-          stage(r, cq * 4, 4, L::k, live);
-          store_rows<4>(sb + L::k, static_cast<__nv_bfloat16*>(out.dq) + at, (long long)p.H * p.K, (warp & 3) * 32, cq * 4, p.L - t0, p.K, lane);
-        }
-        arrive(L::kRk);
+        if (shared) put_part(out.dqp, ck, r, live);
+        else put_rows(out.dq, r, p.K, ck, live);
         {  // this token's parts of dg to the warps that sum it, in the place just read
           const uint32_t e[8] = {__float_as_uint(dot_a), __float_as_uint(dot_b), __float_as_uint(tot), 0u, 0u, 0u, 0u, 0u};
           tmem_st8u(tl + L::T2 + cq * 32, e);
@@ -769,20 +825,16 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
         tmem_wait_ld();
         tmem_wait_st();
         tc_fence_before_sync();
-        if (warp >= 4) asm volatile("bar.arrive 1, 512;" ::: "memory");
-        if (shared) {
-          put_part(out.dkp, ck, r, live);
-        } else {
-          stage(r, cq * 4, 4, L::x, live);
-          store_rows<4>(sb + L::x, static_cast<__nv_bfloat16*>(out.dk) + at, (long long)p.H * p.K, (warp & 3) * 32, cq * 4, p.L - t0, p.K, lane);
-        }
         __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[L::kPt]);
+        if (shared) put_part(out.dkp, ck, r, live);
+        else put_rows(out.dk, r, p.K, ck, live);
       }
-      // dg of tokens t = 32 warp + lane (warps 0 .. 3): what it is summed from now, the sums when the accumulators are free
-      float in = 0.f, th = 0.f, fa = 0.f, fb = 0.f, q1 = 0.f, q2 = 0.f, q3 = 0.f;
-      if (warp < 4) {
-        asm volatile("bar.sync 1, 512;" ::: "memory");
+      if (warp < 4) {  // what dg is summed from; the sums under the next chunk's products
+        if (!wait(L::kPt, par)) break;
         tc_fence_after_sync();
+        in = 0.f;
+        in_e = elast;
 #pragma unroll
         for (int w = 0; w < 4; ++w)  // the blocks of rows up to this quarter
           if (w <= warp) in += rect[(warp * (warp + 1) / 2 + w) * 32 + lane];
@@ -808,53 +860,8 @@ __global__ void __launch_bounds__(kLinThreads, 1) linattn_bwd_tc_kernel(LinAttn 
         for (int e = 0; e < VQ; ++e) U[e] = fmaf(U[e], elast, __uint_as_float(r[e]));
       }
       arrive(L::kR6);
-      if (warp < 4) {
-        float ra = fa, rb = fb + (warp == 0 ? q1 : warp == 1 ? q2 : warp == 2 ? q3 : 0.f);  // running sums within the warp's tokens
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float ua = __shfl_down_sync(0xffffffffu, ra, o), ub = __shfl_up_sync(0xffffffffu, rb, o);
-          if (lane + o < 32) ra += ua;
-          if (lane >= o) rb += ub;
-        }
-        // what other quarters of tokens need of this one: its sum of fa (for those before), of fb and of the paths to quarters after c
-        // (for quarter c after it)
-        float sa = fa, s2 = fb + q2, s3 = fb + q3, s4 = fb;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          sa += __shfl_xor_sync(0xffffffffu, sa, o);
-          s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-          s3 += __shfl_xor_sync(0xffffffffu, s3, o);
-          s4 += __shfl_xor_sync(0xffffffffu, s4, o);
-          th += __shfl_xor_sync(0xffffffffu, th, o);
-        }
-        float* ex = reinterpret_cast<float*>(raw + L::hsum);  // [quarter][4]
-        if (lane == 0) {
-          ex[warp * 4] = sa; ex[warp * 4 + 1] = s2; ex[warp * 4 + 2] = s3; ex[warp * 4 + 3] = s4;
-        }
-        asm volatile("bar.sync 2, 128;" ::: "memory");
-        float after = 0.f, before = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          if (w > warp) after += ex[w * 4];
-          if (w < warp) before += ex[w * 4 + warp];  // warp 1, 2, 3: the paths that cross into it
-        }
-        const float up = __shfl_up_sync(0xffffffffu, rb, 1);
-        const float g = in + (after + ra) + (before + (lane > 0 ? up : 0.f)) + elast * th;
-        if (!p.g_head) {
-          if (t0 + row < p.L) out.dg[((long long)b * p.L + t0 + row) * p.H + h] = live ? g : 0.f;
-          asm volatile("bar.sync 2, 128;" ::: "memory");
-        } else {
-          float s = live ? g : 0.f;
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          asm volatile("bar.sync 2, 128;" ::: "memory");
-          if (lane == 0) ex[warp] = s;
-          asm volatile("bar.sync 2, 128;" ::: "memory");
-          if (tid == 0) out.dg[((long long)b * p.nck + ck) * p.H + h] = (ex[0] + ex[1]) + (ex[2] + ex[3]);
-          asm volatile("bar.sync 2, 128;" ::: "memory");
-        }
-      }
     }
+    if (ok && cend > c0 && warp < 4) sum_dg(c0);
     if (out.dh0 != nullptr && seg == 0 && row < p.K) {
       float* dst = out.dh0 + (bh * p.K + row) * p.V + cq * VQ;
 #pragma unroll

@@ -136,9 +136,9 @@ struct ChunkGates {
   }
 };
 
-constexpr int kLinMaxHead = 128;  // widest K, V
-constexpr int kLinChunkF32 = 64;    // tokens of a chunk: fp32 (FMA pipe)
-constexpr int kLinChunkBf16 = 128;  // bf16 (tensor cores: 128 rows of an MMA)
+constexpr int kLinMaxHead = 128;    // widest K, V
+constexpr int kLinChunkF32 = 64;    // tokens of a chunk: fp32 (its tiles fit shared memory)
+constexpr int kLinChunkBf16 = 128;  // bf16 (the 128 rows of an MMA)
 
 inline int linattn_chunk(int dtype) { return dtype == SS_F32 ? kLinChunkF32 : kLinChunkBf16; }
 
@@ -147,10 +147,9 @@ inline int linattn_chunk(int dtype) { return dtype == SS_F32 ? kLinChunkF32 : kL
 // four chunks whose end states are found first, at the price of a second read of
 // half the inputs.  The tensor-core kernels hold an SM each: as many pieces as
 // leave every one of them its own.  The fp32 kernels share an SM (three forward,
-// two backward) and their time is arithmetic: pieces
-// for three CTAs an SM, so that no SM is left with far more than its share (a
-// training step of the 130M layer, 192 walks: 1458 us for three pieces, 1594 for
-// six, 1862 for two).
+// two backward) and their time is arithmetic: pieces for three CTAs an SM, so that
+// no SM is left with far more than its share (a training step of 192 walks of
+// 2048 tokens, 64 x 64: 1458 us for three pieces, 1594 for six, 1862 for two).
 inline void linattn_segments(LinAttn& p, int dtype, long long walks) {
   const int chunk = linattn_chunk(dtype);
   p.nck = (p.L + chunk - 1) / chunk;

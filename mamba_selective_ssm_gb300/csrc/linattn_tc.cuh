@@ -15,7 +15,6 @@ namespace ssk {
 
 constexpr int kTC = kLinChunkBf16;        // tokens of a chunk = rows of a tile
 constexpr int kPanel = kTC * 128;         // bytes of a panel of kTC rows
-constexpr int kTcThreads = 256;
 constexpr int kLinWarps = 16, kLinThreads = 32 * (kLinWarps + 2);  // computing warps, one that issues, one for the decays
 
 // byte offset of 16-byte unit `u` (8 columns) of row r in a tile of kTC rows
@@ -35,7 +34,6 @@ struct DecTile {
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(a));
     return x;
   }
-  // one warp; incl: the running sum through this lane's four tokens, x[e] that of its own first tokens
   __device__ __forceinline__ void put(int i, Dec r) const {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 4 * i), "f"(r.hi) : "memory");
     const __nv_bfloat16 l = __float2bfloat16_rn(r.lo);
@@ -64,11 +62,19 @@ struct DecTile {
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at + 4 * j));
     return v;
   }
+  // both parts of them
+  __device__ __forceinline__ void rel4(int j, float (&hi)[4], float (&lo)[4]) const {
+    const float4 v = r4(j);
+    uint32_t a, b;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(at + 4 * kTC + 2 * j));
+    hi[0] = v.x; hi[1] = v.y; hi[2] = v.z; hi[3] = v.w;
+    lo[0] = bf16_lo(a); lo[1] = bf16_hi(a); lo[2] = bf16_lo(b); lo[3] = bf16_hi(b);
+  }
 };
 __device__ __forceinline__ Dec dec_sub(Dec a, Dec b) { return dec_add(a, Dec{-b.hi, -b.lo}); }
 __device__ __forceinline__ float dec_exp(Dec d) { return dec_exp(d.hi, d.lo); }
 
-// A chunk's decays, in one warp: take() reads the gates ahead and finds the sums
+// A chunk's decays, in one warp: the gates are read ahead, scan() finds the sums
 // in registers, put() stores them once the tile's readers are done.
 struct DecStage {
   ChunkGates<kTC> g;
@@ -80,19 +86,9 @@ struct DecStage {
     if (lane < kTC / 32) t.put_base(lane, base);
   }
 };
-__device__ __forceinline__ void put_decays(const ChunkGates<kTC>& g, const DecTile& t, int lane) {
-  DecStage s;
-  s.base = g.scan_rel(lane, s.rel);
-  s.put(t, lane);
-}
 
 // One 128-byte line into L2, ahead of the loads that will want it.
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-// kTC rows of `width` bf16 (at most 128: two lines and an odd start) from row t0: a lane per row and line
-__device__ __forceinline__ void prefetch_rows(const __nv_bfloat16* src, long long ld, int valid, int width, int tid) {
-  const int r = tid >> 1, c = (tid & 1) * 64;
-  if (r < valid && c < width) prefetch_l2(src + (long long)r * ld + c);
-}
 
 // ---------------------------------------------------------------- descriptors
 // Shared-memory operand descriptor: start address, leading and stride byte
@@ -116,7 +112,8 @@ __device__ __forceinline__ uint32_t mma_idesc(int n, bool a_cols, bool b_cols) {
 
 // True in one thread of a converged warp.  What that thread then issues takes its
 // operands from the warp's uniform registers; behind a test of the lane's number
-// the compiler cannot know that one thread is left (an MMA took 100 cycles to issue).
+// the compiler cannot know that one thread is left: an MMA took 100 cycles to
+// issue, and operands came to hold other lanes' values.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
@@ -232,24 +229,6 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int panels, int valid, 
       asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + n * kPanel + r * 128 + (lane & 7) * 16), "r"(0) : "memory");
 }
 
-// 16 bytes global -> shared, asynchronously; zeros instead (nothing read) when !ok
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-// kTC tokens x (8 * UNITS) columns into a tile; columns past `width` and tokens past `valid` become zero
-template <int UNITS, int THREADS>
-__device__ __forceinline__ void load_tile_tc(const __nv_bfloat16* __restrict__ src, long long ld, int valid, int width, uint32_t tile,
-                                             int tid) {
-#pragma unroll
-  for (int i = 0; i < kTC * UNITS / THREADS; ++i) {
-    const int at = i * THREADS + tid, r = at / UNITS, u = at % UNITS;
-    const bool ok = r < valid && u * 8 < width;
-    cp16(tile + tile_at(r, u), ok ? src + (long long)r * ld + u * 8 : src, ok);
-  }
-}
-
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -264,26 +243,18 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-// A warp's part of a tile (32 rows from r0, NU 16-byte units from u0) to
-// global memory, up to `rows` rows and `width` columns.  A lane's accumulators
-// are one row, so storing them as they are would touch 32 rows with each
-// instruction; through the tile four lanes share a row (the backward's three
-// outputs: 9000 -> 2000 cycles a chunk).
+// A warp's part of a tile (32 rows from r0, NU 16-byte units from u0) to units
+// from `to` of rows in global memory, up to `rows` rows and `width` columns.  A
+// lane's accumulators are one row, so storing them as they are would touch 32
+// rows with each instruction; through the tile four lanes share a row (the
+// backward's three outputs took 9000 cycles a chunk, so 5500).
 template <int NU>  // NU units of each row: 4 or 2
-__device__ __forceinline__ void store_rows(uint32_t tile, __nv_bfloat16* __restrict__ dst, long long ld, int r0, int u0, int rows, int width,
-                                           int lane) {
+__device__ __forceinline__ void store_rows(uint32_t tile, __nv_bfloat16* __restrict__ dst, long long ld, int r0, int u0, int to, int rows,
+                                           int width, int lane) {
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
-    const int r = r0 + i * (32 / NU) + lane / NU, u = u0 + lane % NU;
-    if (r < rows && u * 8 < width) *reinterpret_cast<uint4*>(dst + (long long)r * ld + u * 8) = lds16(tile + tile_at(r, u));
-  }
-}
-template <int UNITS, int THREADS>
-__device__ __forceinline__ void store_tile_tc(uint32_t tile, __nv_bfloat16* __restrict__ dst, long long ld, int rows, int width, int tid) {
-#pragma unroll
-  for (int i = 0; i < kTC * UNITS / THREADS; ++i) {
-    const int at = i * THREADS + tid, r = at / UNITS, u = at % UNITS;
-    if (r < rows && u * 8 < width) *reinterpret_cast<uint4*>(dst + (long long)r * ld + u * 8) = lds16(tile + tile_at(r, u));
+    const int r = r0 + i * (32 / NU) + lane / NU, u = lane % NU;
+    if (r < rows && (to + u) * 8 < width) *reinterpret_cast<uint4*>(dst + (long long)r * ld + (to + u) * 8) = lds16(tile + tile_at(r, u0 + u));
   }
 }
 
