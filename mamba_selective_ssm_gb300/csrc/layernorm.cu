@@ -12,6 +12,8 @@
 //   wider rows                share the columns, one row per step
 // The backward's column sums stay in registers over all the rows a thread
 // visits; the CTAs' partial rows are added in fixed order by colsum_kernel.
+// 1 / sqrt is rsqrtf (2 units in the last place): 262144 rows of 128 took 33 us
+// with a square root and a division, 31 with it.
 #include <type_traits>
 
 #include "common.cuh"
@@ -72,7 +74,7 @@ __global__ void __launch_bounds__(256) ln_fwd_small_kernel(const T* __restrict__
         s = fmaf(v[e], v[e], s);
       }
       if (!cv) s = 0.f;
-      const float rs = 1.0f / sqrtf(fmaf(lanes_sum<G>(s), inv_dim, eps));
+      const float rs = rsqrtf(fmaf(lanes_sum<G>(s), inv_dim, eps));
       if (r < rows) {
         if (c == 0) {
           if (mean != nullptr) mean[r] = m;
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(256) ln_fwd_warp_kernel(const T* __restrict__ 
       for (int e = 0; e < 8; ++e) t = fmaf(v[e] - m, v[e] - m, t);
       if (u * 32 + lane < ng) s += t;
     }
-    const float rs = 1.0f / sqrtf(fmaf(lanes_sum<32>(s), inv_dim, eps));
+    const float rs = rsqrtf(fmaf(lanes_sum<32>(s), inv_dim, eps));
     if (lane == 0) {
       if (mean != nullptr) mean[r] = m;
       if (rstd != nullptr) rstd[r] = rs;
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(const T* __restrict__
       for (int e = 0; e < 8; ++e) t = fmaf(v[e] - m, v[e] - m, t);
       if (c < dim) s += t;
     }
-    const float rs = 1.0f / sqrtf(fmaf(cta_sum2(make_float2(s, 0.f), red, 1).x, inv_dim, eps));
+    const float rs = rsqrtf(fmaf(cta_sum2(make_float2(s, 0.f), red, 1).x, inv_dim, eps));
     if (threadIdx.x == 0) {
       if (mean != nullptr) mean[r] = m;
       if (rstd != nullptr) rstd[r] = rs;
