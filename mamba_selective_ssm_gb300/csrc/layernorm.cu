@@ -7,9 +7,12 @@
 // Both are one pass over memory: a row is held in registers (as loaded, 8
 // columns a lane and group) between the sums and the output, so the variance is
 // taken around the mean that was found, not as a difference of moments.
-//   rows of <= 256 columns    G lanes per row, 32/G rows per warp, U row sets in flight
-//   rows of <= 2048 columns   forward: one warp per row; backward: a CTA's threads
-//   wider rows                share the columns, one row per step
+//   rows of <= 256 columns    G lanes per row, 32/G rows per warp, U row sets in flight (131072 rows of 256 in bf16:
+//                             forward 31 us, backward 49; as wider rows 38 and 59)
+//   rows of <= 4096 bytes     forward: one warp per row (16384 rows of 2048 in bf16: 27 us, as wider rows 29; in fp32
+//                             51 and 47)
+//   wider rows                and the backward's above 256: a CTA's threads share the columns, one row per step
+//                             (backward with a warp per row: 16384 rows of 1024 in bf16 55 us for 33)
 // The backward's column sums stay in registers over all the rows a thread
 // visits; the CTAs' partial rows are added in fixed order by colsum_kernel.
 // 1 / sqrt is rsqrtf (2 units in the last place): 262144 rows of 128 took 33 us
@@ -168,21 +171,39 @@ __device__ __forceinline__ float2 cta_sum2(float2 v, float2 (*red)[32], int par)
   return make_float2(lanes_sum<32>(w.x), lanes_sum<32>(w.y));
 }
 
-template <typename T, int VPT>
-__global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(const T* __restrict__ x, const float* __restrict__ scale,
+// A CTA's threads share a row, the next one in flight.  Two column groups a thread
+// halve the warps that meet at the two barriers (8192 rows of 4096 in bf16: one
+// group 37 us, two 33; without the next row 39).  HOLD: at most 512 threads, whose
+// registers hold scale and bias too; in bf16, where these are four times a row's
+// bytes, 29 us, in fp32 52 for 48.
+template <typename T, int VPT, bool HOLD>
+__global__ void __launch_bounds__(HOLD ? 512 : 1024) ln_fwd_wide_kernel(const T* __restrict__ x, const float* __restrict__ scale,
                                                            const float* __restrict__ bias, float eps, T* __restrict__ y,
                                                            float* __restrict__ mean, float* __restrict__ rstd, int rows, int dim) {
   using R = Raw8<T>;
   __shared__ float2 red[2][32];
   const float inv_dim = 1.0f / (float)dim;
-  for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
-    typename R::V raw[VPT];
-    float s = 0.f;
+  typename R::V raw[VPT], next[VPT];
+  auto load = [&](typename R::V(&v)[VPT], long long r) {
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
       const int c = (u * (int)blockDim.x + (int)threadIdx.x) * 8;
-      raw[u] = c < dim ? R::ld(x + (size_t)r * dim + c) : R::zero();
+      v[u] = c < dim && r < rows ? R::ld(x + (size_t)r * dim + c) : R::zero();
     }
+  };
+  float sc[HOLD ? VPT : 1][8], bi[HOLD ? VPT : 1][8];
+  auto params = [&](int c, float(&ps)[8], float(&pb)[8]) {
+    ld8f(scale + c, c < dim, ps);
+    ld8f(bias + c, c < dim && bias != nullptr, pb);
+  };
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) params((u * (int)blockDim.x + (int)threadIdx.x) * 8, sc[u], bi[u]);
+  }
+  load(raw, blockIdx.x);
+  for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
+    load(next, r + gridDim.x);  // in flight during this row's sums
+    float s = 0.f;
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
       float v[8];
@@ -210,14 +231,15 @@ __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(const T* __restrict__
     for (int u = 0; u < VPT; ++u) {
       const int c = (u * (int)blockDim.x + (int)threadIdx.x) * 8;
       if (c < dim) {
-        float v[8], sc[8], bi[8];
+        float v[8];
         R::wide(raw[u], v);
-        ld8f(scale + c, true, sc);
-        ld8f(bias + c, bias != nullptr, bi);
+        constexpr int hold = HOLD ? 1 : 0;
+        if (!HOLD) params(c, sc[0], bi[0]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fmaf((v[e] - m) * rs, sc[e], bi[e]);
+        for (int e = 0; e < 8; ++e) v[e] = fmaf((v[e] - m) * rs, sc[u * hold][e], bi[u * hold][e]);
         ActT<T>::st8(y + (size_t)r * dim + c, v);
       }
+      raw[u] = next[u];
     }
   }
 }
@@ -447,7 +469,7 @@ int ln_fwd_launch(const T* x, const float* scale, const float* bias, float eps, 
       return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
     });
   }
-  if (dim <= 2048) {
+  if (dim * sizeof(T) <= 4096) {
     auto run = [&](auto kern) -> int {
       const size_t smem = (size_t)dim * 8;
       const int per_sm = resident_ctas(kern, 256, smem);
@@ -458,15 +480,15 @@ int ln_fwd_launch(const T* x, const float* scale, const float* bias, float eps, 
       return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
     };
     if (dim <= 512) return run(ln_fwd_warp_kernel<T, 2>);
-    if (dim <= 1024) return run(ln_fwd_warp_kernel<T, 4>);
-    return run(ln_fwd_warp_kernel<T, 8>);
+    if (sizeof(T) == 4 || dim <= 1024) return run(ln_fwd_warp_kernel<T, 4>);
+    if constexpr (sizeof(T) == 2) return run(ln_fwd_warp_kernel<T, 8>);
   }
-  const int vpt = ln_vpt(dim), threads = ln_threads(dim, vpt);
-  const int cap = 152 * (2048 / threads);
+  const int vpt = dim <= 16384 ? 2 : 4, threads = ln_threads(dim, vpt);
+  const int cap = 152 * (1024 / threads);
   const int grid = rows < cap ? rows : cap;
-  if (vpt == 1) ln_fwd_wide_kernel<T, 1><<<grid, threads, 0, s>>>(x, scale, bias, eps, y, mean, rstd, rows, dim);
-  else if (vpt == 2) ln_fwd_wide_kernel<T, 2><<<grid, threads, 0, s>>>(x, scale, bias, eps, y, mean, rstd, rows, dim);
-  else ln_fwd_wide_kernel<T, 4><<<grid, threads, 0, s>>>(x, scale, bias, eps, y, mean, rstd, rows, dim);
+  if (vpt == 4) ln_fwd_wide_kernel<T, 4, false><<<grid, threads, 0, s>>>(x, scale, bias, eps, y, mean, rstd, rows, dim);
+  else if (sizeof(T) == 2 && threads <= 512) ln_fwd_wide_kernel<T, 2, sizeof(T) == 2><<<grid, threads, 0, s>>>(x, scale, bias, eps, y, mean, rstd, rows, dim);
+  else ln_fwd_wide_kernel<T, 2, false><<<grid, threads, 0, s>>>(x, scale, bias, eps, y, mean, rstd, rows, dim);
   return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
