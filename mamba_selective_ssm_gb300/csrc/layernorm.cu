@@ -417,7 +417,7 @@ int ln_validate(int rows, int dim, int dtype) {
   return SS_OK;
 }
 
-constexpr int kLnU = 4;  // row sets in flight per warp (rows of at most 256 columns)
+constexpr int kLnU = 4;  // row sets in flight per warp of narrow rows (262144 of 128: 33 us, two sets 37, eight 39)
 
 // lanes per row: the power of two that covers dim / 8 groups
 inline int ln_lanes(int dim) {
@@ -464,7 +464,7 @@ int ln_fwd_launch(const T* x, const float* scale, const float* bias, float eps, 
       constexpr int G = decltype(tag)::value;
       const int per = 8 * (32 / G) * kLnU;
       long long grid = ((long long)rows + per - 1) / per;
-      if (grid > 16 * 152) grid = 16 * 152;
+      if (grid > 16 * 152) grid = 16 * 152;  // (33 us for 262144 rows of 128; a CTA for every set 35)
       ln_fwd_small_kernel<T, G, kLnU><<<(int)grid, 256, 0, s>>>(x, scale, bias, eps, y, mean, rstd, rows, dim);
       return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
     });

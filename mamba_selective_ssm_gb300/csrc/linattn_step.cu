@@ -5,9 +5,10 @@
 // columns of one head: a thread owns four neighbouring columns of every RP-th
 // row, so that a warp's 16-byte vectors follow one another in memory, up to eight
 // rows of a thread in flight; the sum over rows for o is a shared-memory tree.
-// All of V in one CTA when the heads fill the GPU (60 us, 6.7 TB/s, at 96
-// sequences of 32 heads of 128 x 128; 80 us with 32 columns a CTA), 32 columns for a few sequences, whose
-// latency is the number of loads one after another.
+// All of V in one CTA when there is a head for every SM (96 sequences of 32 heads of
+// 128 x 128: 62 us, 6.5 TB/s, and 82 with 32 columns a CTA; 8 sequences 6.2 and
+// 9.7), 32 columns for fewer, whose latency is the number of loads one after
+// another (one sequence 4.2 us, and 6.2 with all of V).
 #include "linattn_common.cuh"
 
 namespace {
@@ -87,7 +88,7 @@ extern "C" int linattn_step(const void* q, const void* k, const void* v, const f
     if (!ssh::aligned16(x)) return SS_ERR_ALIGN;
   if (reinterpret_cast<uintptr_t>(g) & 3u) return SS_ERR_ALIGN;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int cw = B * H >= 2 * 152 ? V : 32;
+  const int cw = B * H >= 152 ? V : 32;
   const dim3 grid((unsigned)(B * H), (unsigned)((V + cw - 1) / cw));
   if (dtype == SS_F32)
     linattn_step_kernel<float><<<grid, kLinStepThreads, 0, s>>>(static_cast<const float*>(q), static_cast<const float*>(k),
