@@ -362,8 +362,6 @@ struct BwdMaps {
 // the sum over the warp's lanes of x[l & 15], in lane l
 __device__ __forceinline__ float col_sums16(float (&x)[16], int lane) {
 #pragma unroll
-  for (int e = 0; e < 16; ++e) x[e] += __shfl_xor_sync(0xffffffffu, x[e], 16);
-#pragma unroll
   for (int o = 8; o > 0; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
@@ -372,7 +370,7 @@ __device__ __forceinline__ float col_sums16(float (&x)[16], int lane) {
       x[e] = keep + __shfl_xor_sync(0xffffffffu, give, o);
     }
   }
-  return x[0];
+  return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 16);
 }
 
 template <int VP>
