@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(256, KP == 64 && VP == 64 ? 2 : 1) linattn_bwd
 // by way of dP^T's tile, each warp through a part of its own, while the next k and
 // do land (sent by TMA from the tiles of do, dP^T and k they held these for 5000
 // cycles: 377 us for a training step of 4 x 2048 tokens of 32 heads of 128 x 128).
-// Measured: 235 us of that step's 325.  A chunk takes 29000 cycles, its MMAs 8100:
+// Measured: 233 us of that step's 323.  A chunk takes 29000 cycles, its MMAs 8100:
 // bound by the chain of operands that the computing warps make for the tensor cores
 // (S and U as three terms, the scores, scale e^{c_i} do) and read back, at the 16
 // warps that the registers leave; the tiles fill shared memory, so that no second
