@@ -377,7 +377,12 @@ def linattn_num_chunks(L: int, dtype) -> int:
 
 
 def _raw_stream(dev):
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+    """The current stream's handle.  The library launches on the current device, so that is where the tensors must be: on
+    another one their addresses and their stream would belong to a device that runs nothing here."""
+    current = torch.cuda.current_device()
+    if dev.index != current:
+        raise ValueError(f"the tensors are on {dev}, but the current device is cuda:{current}")
+    return torch._C._cuda_getCurrentRawStream(current)
 
 
 def _at(t, name, shape, dtype, dev):
