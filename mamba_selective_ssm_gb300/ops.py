@@ -458,6 +458,7 @@ def _scratch(workspace, need, dev):
             return None, 0
         workspace = torch.empty(need, device=dev, dtype=torch.uint8)
         return workspace.data_ptr(), need
+    _req(workspace, "workspace", device=dev)  # (the library checks its size and alignment)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

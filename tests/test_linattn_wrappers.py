@@ -100,3 +100,20 @@ def test_tensors_on_another_device_are_refused(ops, name):
     with pytest.raises(ValueError, match="on cuda:1, but the current device is cuda:0"):
         _calls(ops, 1)[name]()
     assert lib.launched == []
+
+
+@pytest.mark.parametrize("name", NAMES[:3])
+def test_workspace_is_a_dense_tensor_of_the_device(ops, name):
+    ops, lib = ops
+    call = _calls(ops, 0)[name]
+    with pytest.raises(TypeError, match="workspace must be a torch.Tensor"):
+        call(workspace=4096)
+    with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
+        call(workspace=torch.zeros(8192, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        call(workspace=_on(0, 64, 256)[:, :128])
+    with pytest.raises(ValueError, match="workspace is on cuda:1"):
+        call(workspace=_on(1, 8192))
+    assert lib.launched == []
+    call(workspace=_on(0, 8192))
+    assert lib.launched == [name]
