@@ -373,7 +373,9 @@ int conv1d_causal_step(const void* x, float* conv_state, const float* w, const f
  *   lengths : [B] int32 on the device, or NULL: tokens t >= lengths[b] neither
  *          decay nor add nor read (their inputs may hold anything; o and all
  *          gradients there are 0); values are clamped to 0 .. L.
- *   K, V : multiples of 8, at most 128;  H a multiple of G.
+ *   K, V : multiples of 8, at most 128;  H a multiple of G;  L at most
+ *          2^31 - 512;  B * H at most 2^24 (2^23 in fp32 with V > 64; the step
+ *          takes up to 2^31 - 1).
  *   states and their gradients are [B, H, K, V] fp32.
  * The sequence is worked through in chunks whose inner products are matrix
  * products; linattn_num_chunks() is their number (the chunk's length goes by

@@ -1030,8 +1030,8 @@ extern "C" int linattn_bwd(const void* q, long long ldq, const void* k, long lon
   BwdPlan pl;
   int rc = bwd_plan(B, L, H, G, K, V, dtype, g_per_head, pl);
   if (rc != SS_OK) return rc;
-  if ((rc = linattn_ld_ok(ldq, G * K)) != SS_OK || (rc = linattn_ld_ok(ldk, G * K)) != SS_OK ||
-      (rc = linattn_ld_ok(ldv, H * V)) != SS_OK)
+  if ((rc = linattn_ld_ok(ldq, G, K)) != SS_OK || (rc = linattn_ld_ok(ldk, G, K)) != SS_OK ||
+      (rc = linattn_ld_ok(ldv, H, V)) != SS_OK)
     return rc;
   const void* ptrs[] = {q, k, v, ckpt, dout, dh_last, dq, dk, dv, dh0};
   for (const void* x : ptrs)

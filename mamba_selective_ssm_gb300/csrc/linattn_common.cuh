@@ -137,6 +137,7 @@ struct ChunkGates {
 };
 
 constexpr int kLinMaxHead = 128;    // widest K, V
+constexpr int kLinMaxLen = 2147483136;  // longest row: token numbers up to three chunks past its end are still an int
 constexpr int kLinChunkF32 = 64;    // tokens of a chunk: fp32 (its tiles fit shared memory)
 constexpr int kLinChunkBf16 = 128;  // bf16 (the 128 rows of an MMA)
 
@@ -162,7 +163,7 @@ inline void linattn_segments(LinAttn& p, int dtype, long long walks) {
 }
 
 inline int linattn_validate(int B, int L, int H, int G, int K, int V, int dtype) {
-  if (B <= 0 || L <= 0 || H <= 0 || G <= 0 || K <= 0 || V <= 0) return SS_ERR_DIM;
+  if (B <= 0 || L <= 0 || H <= 0 || G <= 0 || K <= 0 || V <= 0 || L > kLinMaxLen) return SS_ERR_DIM;
   if (dtype != SS_F32 && dtype != SS_BF16) return SS_ERR_UNSUPPORTED;
   if (H % G != 0) return SS_ERR_DIM;
   if (K % 8 != 0 || V % 8 != 0) return SS_ERR_ALIGN;
@@ -171,8 +172,8 @@ inline int linattn_validate(int B, int L, int H, int G, int K, int V, int dtype)
 }
 
 // a token stride: at least the row it holds, and rows on 16-byte boundaries
-inline int linattn_ld_ok(long long ld, int width) {
-  if (ld < width) return SS_ERR_DIM;
+inline int linattn_ld_ok(long long ld, int heads, int width) {
+  if (ld < (long long)heads * width) return SS_ERR_DIM;
   return ld % 8 != 0 ? SS_ERR_ALIGN : SS_OK;
 }
 

@@ -562,7 +562,7 @@ int fwd_bf16(const FwdPlan& pl, const float* h0, __nv_bfloat16* o, float* ckpt, 
 }  // namespace
 
 extern "C" int linattn_num_chunks(int L, int dtype) {
-  if (L <= 0 || (dtype != SS_F32 && dtype != SS_BF16)) return 0;
+  if (L <= 0 || L > kLinMaxLen || (dtype != SS_F32 && dtype != SS_BF16)) return 0;
   const int c = linattn_chunk(dtype);
   return (L + c - 1) / c;
 }
@@ -580,8 +580,8 @@ extern "C" int linattn_fwd(const void* q, long long ldq, const void* k, long lon
   FwdPlan pl;
   int rc = fwd_plan(B, L, H, G, K, V, dtype, pl);
   if (rc != SS_OK) return rc;
-  if ((rc = linattn_ld_ok(ldq, G * K)) != SS_OK || (rc = linattn_ld_ok(ldk, G * K)) != SS_OK ||
-      (rc = linattn_ld_ok(ldv, H * V)) != SS_OK)
+  if ((rc = linattn_ld_ok(ldq, G, K)) != SS_OK || (rc = linattn_ld_ok(ldk, G, K)) != SS_OK ||
+      (rc = linattn_ld_ok(ldv, H, V)) != SS_OK)
     return rc;
   const void* ptrs[] = {q, k, v, o, h0, ckpt, h_last};
   for (const void* x : ptrs)
