@@ -378,8 +378,13 @@ int conv1d_causal_step(const void* x, float* conv_state, const float* w, const f
  *          takes up to 2^31 - 1).
  *   states and their gradients are [B, H, K, V] fp32.
  * The sequence is worked through in chunks whose inner products are matrix
- * products; linattn_num_chunks() is their number (the chunk's length goes by
- * dtype).  Alignment: 16 bytes for every pointer but g, dg and lengths (4).
+ * products; linattn_num_chunks() is their number (64 tokens each in fp32, 128
+ * in bf16).  A NaN or infinity in a live token can therefore reach, beyond
+ * what the recurrence says, the other tokens of its chunk, earlier ones among
+ * them (a weight of zero on it is a factor of a product), and in the backward
+ * all tokens of its row; an infinity may come out as NaN.  It reaches no
+ * earlier chunk of the forward, no other batch row, and no head that does not
+ * read it.  (The step has no chunk: there it is the recurrence.)  Alignment: 16 bytes for every pointer but g, dg and lengths (4).
  */
 int linattn_num_chunks(int L, int dtype);
 

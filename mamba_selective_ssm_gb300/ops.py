@@ -470,7 +470,9 @@ def linattn_fwd(q, k, v, g, h0=None, scale=None, lengths=None, want_ckpt: bool =
     ``q, k`` [B, L, G, K] are shared by the H/G heads of a group of ``v`` [B, L, H, V]; each may be a column range of
     a wider [B, L, W] tensor.  ``g`` are log decays, fp32 [B, L, H] or one for each head [H].  ``lengths`` (int32 [B])
     ends each row; past it o is 0 and the state stays.  ``scale`` is ``K ** -0.5`` unless given.  ``ckpt`` (None unless
-    ``want_ckpt``) is what ``linattn_bwd`` starts from."""
+    ``want_ckpt``) is what ``linattn_bwd`` starts from.
+
+    A NaN or infinity in a live token can reach the other tokens of its chunk (64 in fp32, 128 in bf16), also earlier ones."""
     B, L, H, G, K, V = _linattn_sizes(q, v)
     dev, dt, f32 = q.device, q.dtype, torch.float32
     sdt = _act_dtype(q)
