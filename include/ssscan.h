@@ -384,7 +384,15 @@ int conv1d_causal_step(const void* x, float* conv_state, const float* w, const f
  * them (a weight of zero on it is a factor of a product), and in the backward
  * all tokens of its row; an infinity may come out as NaN.  It reaches no
  * earlier chunk of the forward, no other batch row, and no head that does not
- * read it.  (The step has no chunk: there it is the recurrence.)  Alignment: 16 bytes for every pointer but g, dg and lengths (4).
+ * read it.  (The step has no chunk: there it is the recurrence.)
+ * Rounding.  All sums, states and decays are held in fp32 or finer.  fp32
+ * activations: the products take operands of 22 bits (two tf32 values each).
+ * bf16 activations: what ends in fp32 (states, dg, dh0) takes its fp32 operands
+ * in full (three bf16 terms); a score of o, dq, dk or dv, and the state as it
+ * enters o and its gradient as it enters dv, are rounded to bf16 once before
+ * the product, beside the output's own rounding: the error of these outputs is
+ * about sqrt(2) of that of one rounding, in calls of a few tokens up to twice
+ * it.  The step works in fp32 throughout and rounds o only.  Alignment: 16 bytes for every pointer but g, dg and lengths (4).
  */
 int linattn_num_chunks(int L, int dtype);
 
@@ -444,6 +452,8 @@ int linattn_step(const void* q, const void* k, const void* v, const float* g, in
  *   scale, bias : [dim] fp32, bias may be NULL (zero)
  *   mean, rstd  : [rows] fp32 outputs, each may be NULL
  * dim a multiple of 8 and at most 32768; eps >= 0; pointers 16-byte aligned.
+ * Statistics are fp32, the deviations taken around the mean found first; the
+ * reciprocal root is the hardware's (2 units in the last place).
  */
 int layernorm_fwd(const void* x, const float* scale, const float* bias, float eps, void* y, float* mean, float* rstd,
                   int rows, int dim, int dtype, void* stream);

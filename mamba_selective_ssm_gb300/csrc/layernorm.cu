@@ -8,15 +8,17 @@
 // columns a lane and group) between the sums and the output, so the variance is
 // taken around the mean that was found, not as a difference of moments.
 //   rows of <= 256 columns    G lanes per row, 32/G rows per warp, U row sets in flight (131072 rows of 256 in bf16:
-//                             forward 31 us, backward 49; as wider rows 38 and 59)
+//                             forward 32 us, backward 50; as wider rows 38 and 59)
 //   rows of <= 4096 bytes     forward: one warp per row (16384 rows of 2048 in bf16: 27 us, as wider rows 29; in fp32
-//                             51 and 47)
+//                             51 and 48)
 //   wider rows                and the backward's above 256: a CTA's threads share the columns, one row per step
-//                             (backward with a warp per row: 16384 rows of 1024 in bf16 55 us for 33)
+//                             (backward with a warp per row: 16384 rows of 1024 in bf16 55 us for 33).  Its column sums
+//                             fit the registers up to 8192 columns (4096 rows of 8192: bf16 70 us, fp32 85); above, they
+//                             spill (4096 rows of 16384: 527 and 300)
 // The backward's column sums stay in registers over all the rows a thread
 // visits; the CTAs' partial rows are added in fixed order by colsum_kernel.
-// 1 / sqrt is rsqrtf (2 units in the last place): 262144 rows of 128 took 33 us
-// with a square root and a division, 31 with it.
+// 1 / sqrt is rsqrtf (2 units in the last place):
+// 262144 rows of 128 take 30 us with it, 32 with a square root and a division.
 #include <type_traits>
 
 #include "common.cuh"
@@ -173,9 +175,9 @@ __device__ __forceinline__ float2 cta_sum2(float2 v, float2 (*red)[32], int par)
 
 // A CTA's threads share a row, the next one in flight.  Two column groups a thread
 // halve the warps that meet at the two barriers (8192 rows of 4096 in bf16: one
-// group 37 us, two 33; without the next row 39).  HOLD: at most 512 threads, whose
+// group 37 us, two 34; without the next row 39).  HOLD: at most 512 threads, whose
 // registers hold scale and bias too; in bf16, where these are four times a row's
-// bytes, 29 us, in fp32 52 for 48.
+// bytes, 30 us, in fp32 52 for 49.
 template <typename T, int VPT, bool HOLD>
 __global__ void __launch_bounds__(HOLD ? 512 : 1024) ln_fwd_wide_kernel(const T* __restrict__ x, const float* __restrict__ scale,
                                                            const float* __restrict__ bias, float eps, T* __restrict__ y,
@@ -417,7 +419,8 @@ int ln_validate(int rows, int dim, int dtype) {
   return SS_OK;
 }
 
-constexpr int kLnU = 4;  // row sets in flight per warp of narrow rows (262144 of 128: 33 us, two sets 37, eight 39)
+// row sets in flight per warp of narrow rows (262144 of 128 in bf16: forward 30 us, backward 49; two sets 30 and 61, eight 35 and 68)
+constexpr int kLnU = 4;
 
 // lanes per row: the power of two that covers dim / 8 groups
 inline int ln_lanes(int dim) {
@@ -479,7 +482,7 @@ int ln_fwd_launch(const T* x, const float* scale, const float* bias, float eps, 
       constexpr int G = decltype(tag)::value;
       const int per = 8 * (32 / G) * kLnU;
       long long grid = ((long long)rows + per - 1) / per;
-      if (grid > 16 * 152) grid = 16 * 152;  // (33 us for 262144 rows of 128; a CTA for every set 35)
+      if (grid > 16 * 152) grid = 16 * 152;  // (30 us for 262144 rows of 128; a CTA for every set 32)
       ln_fwd_small_kernel<T, G, kLnU><<<(int)grid, 256, 0, s>>>(x, scale, bias, eps, y, mean, rstd, rows, dim);
       return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
     });

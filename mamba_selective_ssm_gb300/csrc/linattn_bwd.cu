@@ -332,11 +332,12 @@ __global__ void __launch_bounds__(256, KP == 64 && VP == 64 ? 2 : 1) linattn_bwd
 // by way of dP^T's tile, each warp through a part of its own, while the next k and
 // do land (sent by TMA from the tiles of do, dP^T and k they held these for 5000
 // cycles: 377 us for a training step of 4 x 2048 tokens of 32 heads of 128 x 128).
-// Measured: 233 us of that step's 323.  A chunk takes 29000 cycles, its MMAs 8100:
+// Measured: 235 us of that step's 323.  A chunk takes 29000 cycles, its MMAs 8100:
 // bound by the chain of operands that the computing warps make for the tensor cores
 // (S and U as three terms, the scores, scale e^{c_i} do) and read back, at the 16
 // warps that the registers leave; the tiles fill shared memory, so that no second
-// chunk or CTA runs beside it.
+// chunk or CTA runs beside it.  Five warps on some of the SM's quarters leave a thread
+// 96 registers: 188 bytes of it spill with VP = 128, 128 with VP = 64.
 template <int VP>
 struct BwdTc {
   static constexpr int vt = kTC * VP * 2;  // bytes of a tile VP columns wide
@@ -1051,9 +1052,9 @@ extern "C" int linattn_bwd(const void* q, long long ldq, const void* k, long lon
   BwdOut out = {dq, dk, dv, nullptr, nullptr, nullptr, dh0};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
-  if (dtype == SS_BF16)  // (8192 tokens of 32 heads of 128 x 64, forward and backward: 370 us in tiles of 64 columns, 430 in tiles of 128)
+  if (dtype == SS_BF16)  // (8192 tokens of 32 heads of 128 x 64, forward and backward: 366 us in tiles of 64 columns, 406 in tiles of 128)
     return V <= 64 ? bwd_bf16<64>(pl, dout, ckpt, dh_last, out, dg, ws, s) : bwd_bf16<128>(pl, dout, ckpt, dh_last, out, dg, ws, s);
-  if (K <= 64)  // (24 heads of 64 x 64, forward and backward: 1458 us in tiles of 64 rows, 2369 in tiles of 128)
+  if (K <= 64)  // (24 heads of 64 x 64, forward and backward: 1449 us in tiles of 64 rows, 2352 in tiles of 128)
     return V <= 64 ? bwd_f32<64, 64>(pl, dout, ckpt, dh_last, out, dg, ws, s) : bwd_f32<64, 128>(pl, dout, ckpt, dh_last, out, dg, ws, s);
   return V <= 64 ? bwd_f32<128, 64>(pl, dout, ckpt, dh_last, out, dg, ws, s) : bwd_f32<128, 128>(pl, dout, ckpt, dh_last, out, dg, ws, s);
 }

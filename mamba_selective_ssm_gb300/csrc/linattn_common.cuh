@@ -148,10 +148,14 @@ inline int linattn_chunk(int dtype) { return dtype == SS_F32 ? kLinChunkF32 : kL
 // four chunks whose end states are found first, at the price of a second read of
 // half the inputs.  The tensor-core kernels hold an SM each: as many pieces as
 // leave every one of them its own (16384 tokens of 32 heads of 128 x 64: 152 us,
-// 353 uncut, 153 for twice as many; 8192 forward and backward 370, 918, 393).  The fp32 kernels share an SM (three forward,
+// 349 uncut, 155 for twice as many; 8192 forward and backward 366, 909, 392).  From
+// 77 walks on nothing is cut, so a count a little above the SMs' takes two turns
+// of whole rows (4 x 2048 tokens of 32 heads of 128 x 128, 128 walks: 77 us, 5 x 2048,
+// 160 walks: 141).  The fp32 kernels share an SM (three forward,
 // two backward) and their time is arithmetic: pieces for three CTAs an SM, so that
 // no SM is left with far more than its share (a training step of 192 walks of
-// 2048 tokens, 64 x 64: 1458 us for three pieces, 1594 for six, 1862 for two).
+// 2048 tokens, 64 x 64: 1449 us for three pieces, 1516 for six, 1766 for two, 1741
+// uncut).  The sums are taken over the last piece walked too, whose end no one reads.
 inline void linattn_segments(LinAttn& p, int dtype, long long walks) {
   const int chunk = linattn_chunk(dtype);
   p.nck = (p.L + chunk - 1) / chunk;
@@ -196,9 +200,12 @@ inline int lin_launch(void (*kern)(KArgs...), unsigned grid, int threads, size_t
 // the three products that matter are summed in fp32, the smallest first; what is
 // dropped is 2^-22 of a term.  Each step of 8 is summed by itself and added with a
 // rounding: the tensor core cuts its sums, which into a state carried over 32
-// chunks added up to 1e-5 of it.  These take operands from registers (mma.sync), so
-// that a tile lies in shared memory once and in fp32: tcgen05 reads its operands
-// there, and both halves of q, k, v, do and the states would not fit.  (On the
+// chunks added up to 1e-5 of it.  The outputs are off by 6e-7 of their root mean square
+// over 32 chunks (2e-7 for plain fp32 products).  These take operands from registers
+// (mma.sync), so that a tile lies in shared memory once and in fp32, and are split
+// again for every product.  tcgen05 reads its operands from shared memory: both
+// halves of q, k, v, do and two states are 192 KB for heads of 64 x 64 and do not fit
+// for wider ones; that form has not been built.  (On the
 // FMA pipe the same kernels were bound by shared memory: 8 x 4 products a thread
 // read 16 vectors for every 128 multiplies.)
 //

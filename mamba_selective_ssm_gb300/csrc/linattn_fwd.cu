@@ -153,7 +153,10 @@ __global__ void __launch_bounds__(FwdSmem<KP>::NT) linattn_fwd_kernel(LinAttn p,
 // 54 % of the copy bandwidth; a chunk takes 9100 cycles of which the chain
 // w v -> Sn -> S -> its tile -> q S -> o binds 6400.  All of V in one CTA: with 64 columns a CTA and two CTAs an SM
 // the scores were made and scaled twice and the narrow products waited for
-// shared memory (114 us).
+// shared memory (114 us).  Five warps on some of the SM's quarters leave a thread 96
+// registers; with VP = 128 56 bytes of it spill.  Tiles of q and k are 128 columns wide
+// whatever K is: with K <= 64 half of the computing threads hold no row of the state
+// (8 x 2048 tokens of 24 heads of 64 x 64: 94 us for 30 of copying).
 template <int VP>
 struct FwdTc {
   static constexpr int vt = kTC * VP * 2;  // bytes of a tile VP columns wide
@@ -598,10 +601,10 @@ extern "C" int linattn_fwd(const void* q, long long ldq, const void* k, long lon
   p.lengths = lengths;
   p.scale = scale;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == SS_F32)  // (24 heads of 64 x 64, forward and backward: 1458 us in tiles of 64 rows, 2067 in tiles of 128)
+  if (dtype == SS_F32)  // (24 heads of 64 x 64, forward and backward: 1449 us in tiles of 64 rows, 2051 in tiles of 128)
     return K <= 64 ? fwd_f32<64>(pl, h0, static_cast<float*>(o), ckpt, h_last, workspace, s)
                    : fwd_f32<128>(pl, h0, static_cast<float*>(o), ckpt, h_last, workspace, s);
-  // (16384 tokens of 32 heads of 128 x 64: 152 us in tiles of 64 columns, 188 in tiles of 128)
+  // (16384 tokens of 32 heads of 128 x 64: 152 us in tiles of 64 columns, 187 in tiles of 128)
   return V <= 64 ? fwd_bf16<64>(pl, h0, static_cast<__nv_bfloat16*>(o), ckpt, h_last, workspace, s)
                  : fwd_bf16<128>(pl, h0, static_cast<__nv_bfloat16*>(o), ckpt, h_last, workspace, s);
 }

@@ -4,11 +4,15 @@
 // All the time goes to reading and writing h ([K, V] fp32).  A CTA takes `cw`
 // columns of one head: a thread owns four neighbouring columns of every RP-th
 // row, so that a warp's 16-byte vectors follow one another in memory, up to eight
-// rows of a thread in flight; the sum over rows for o is a shared-memory tree.
+// rows of a thread in flight.  For o each thread leaves its rows' sum in shared
+// memory, and one thread for each group of columns adds the RP of them in order
+// (8 at V = 128, 128 at V = 8).
 // All of V in one CTA when there is a head for every SM (96 sequences of 32 heads of
 // 128 x 128: 62 us, 6.5 TB/s, and 82 with 32 columns a CTA; 8 sequences 6.2 and
 // 9.7), 32 columns for fewer, whose latency is the number of loads one after
-// another (one sequence 4.2 us, and 6.2 with all of V).
+// another (one sequence 4.2 us, and 6.2 with all of V).  The rule was measured at V =
+// 128.  Narrower states, 96 sequences of 32 heads: V = 64 31 us for 30 of copying
+// their bytes, V = 24 21 for 11, V = 8 21 for 4: there the CTAs count, not the bytes.
 #include "linattn_common.cuh"
 
 namespace {
