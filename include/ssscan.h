@@ -392,7 +392,8 @@ int conv1d_causal_step(const void* x, float* conv_state, const float* w, const f
  * enters o and its gradient as it enters dv, are rounded to bf16 once before
  * the product, beside the output's own rounding: the error of these outputs is
  * about sqrt(2) of that of one rounding, in calls of a few tokens up to twice
- * it.  The step works in fp32 throughout and rounds o only.  Alignment: 16 bytes for every pointer but g, dg and lengths (4).
+ * it.  The step works in fp32 throughout and rounds o only.
+ * Alignment: 16 bytes for every pointer but g, dg and lengths (4).
  */
 int linattn_num_chunks(int L, int dtype);
 
