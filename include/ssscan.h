@@ -1,8 +1,8 @@
 /*
  * ssscan.h — C ABI of libssscan.so: the Mamba selective-scan forward and
  * backward, the depthwise causal conv1d backward, the RMSNorm backward, linear
- * attention with a decay for each head and layer norm (each forward and
- * backward), written for NVIDIA GB300 (sm_103a).
+ * attention with a decay for each head, the gated delta rule, layer norm and
+ * group norm (each forward and backward), written for NVIDIA GB300 (sm_103a).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -444,6 +444,82 @@ int linattn_bwd(const void* q, long long ldq, const void* k, long long ldk, cons
  */
 int linattn_step(const void* q, const void* k, const void* v, const float* g, int g_per_head, float* h, void* o,
                  int B, int H, int G, int K, int V, float scale, int dtype, void* stream);
+
+/*
+ * The gated delta rule: linear attention whose write replaces what the state
+ * already holds for the key.  Per batch row b, head h and token t, with a state
+ * S of [K, V] values,
+ *     r_t = v_t - exp(g_t) S_{t-1}^T k_t
+ *     S_t = exp(g_t) S_{t-1} + beta_t k_t r_t^T            (S_{-1} = h0, or 0)
+ *     o_t = scale * S_t^T q_t
+ *   q, k, v, lengths, ldq, ldk, ldv, K, V, H, G: as in linear attention
+ *   g    : [B, L, H] fp32 log decays, or NULL (none); values below -160 count
+ *          as -160
+ *   beta : [B, L, H] fp32.  The state stays bounded for 0 <= beta_t |k_t|^2 <= 2;
+ *          keys are normally of length one (rmsnorm_fwd over the rows of k with
+ *          scale K^-1/2 makes them so).  Elements of k and q of 2^60 and more
+ *          come out as infinities; those of a token below 2^-24 of its largest
+ *          lose bits.
+ *   B * H at most 2^24, and B * H * ceil(L / 64) below 2^28.
+ * The sequence is worked through in chunks of 64 tokens; a NaN or infinity in a
+ * live token can reach the other tokens of its chunk, earlier ones among them,
+ * and in the backward all tokens of its row.
+ * Rounding.  All sums and states are fp32.  Products run in fp16 with fp32
+ * sums: what ends in fp32 (states, dg, dbeta, dh0, and with fp32 activations
+ * every output) takes fp32 operands as two scaled fp16 terms (22 bits); with
+ * bf16 activations the operands of o, dq and dk are one term (11 bits), well
+ * inside the rounding of the output itself.
+ * Alignment: 16 bytes for every pointer but g, beta, lengths, dg, dbeta (4).
+ *
+ * deltarule_num_states — states a checkpoint holds: one entering each chunk
+ * and the last one, ceil(L / 64) + 1 (0 on an invalid L).
+ */
+int deltarule_num_states(int L);
+
+/*
+ * deltarule_fwd — o [B, L, H, V] (dtype), and where the pointer is given
+ *   ckpt   : [B, H, deltarule_num_states(L), K, V] fp32, from which
+ *            deltarule_bwd starts (the order of the K * V values is the
+ *            library's own; states past a row's last are not written)
+ *   h_last : [B, H, K, V] fp32, the state after the row's last token
+ * h0 may be NULL (zeros).  workspace: deltarule_fwd_workspace_size() bytes.
+ */
+size_t deltarule_fwd_workspace_size(int B, int L, int H, int G, int K, int V, int dtype);
+int deltarule_fwd(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv,
+                  const float* g, const float* beta, const float* h0, const int* lengths, void* o, float* ckpt,
+                  float* h_last, int B, int L, int H, int G, int K, int V, float scale, int dtype,
+                  void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * deltarule_bwd — gradient of sum(o * dout) + sum(h_last * dh_last):
+ *   dq, dk : [B, L, G, K], dv : [B, L, H, V] (dtype; overwritten)
+ *   dg     : [B, L, H] fp32, overwritten (NULL when g is)
+ *   dbeta  : [B, L, H] fp32, overwritten
+ *   dh0    : [B, H, K, V] fp32, overwritten, or NULL
+ * ckpt: the forward's.  dh_last may be NULL (zero).  With U_t = dL/dS_t and
+ * Sd_t = exp(g_t) S_{t-1}:
+ *   dr_t = beta_t U_t^T k_t;  dv_t = dr_t;  dbeta_t = r_t . U_t^T k_t
+ *   dq_t = scale S_t dout_t;  dk_t = beta_t U_t r_t - Sd_t dr_t
+ *   dg_t = <Sd_t, U_t - k_t dr_t^T>;  U_{t-1} = exp(g_t) (U_t - k_t dr_t^T) + scale q_{t-1} dout_{t-1}^T
+ * (dq, dk summed over the heads of a group; past a row's length all are 0).
+ * Sums are in a fixed order: two identical calls give the same bits.
+ */
+size_t deltarule_bwd_workspace_size(int B, int L, int H, int G, int K, int V, int dtype);
+int deltarule_bwd(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv,
+                  const float* g, const float* beta, const int* lengths, const float* ckpt, const void* dout,
+                  const float* dh_last, void* dq, void* dk, void* dv, float* dg, float* dbeta, float* dh0,
+                  int B, int L, int H, int G, int K, int V, float scale, int dtype,
+                  void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * deltarule_step — one token for B sequences (decode), the state in place:
+ *   q, k : [B, G, K], v, o : [B, H, V] (dtype, dense);  g (or NULL), beta : [B, H] fp32
+ *   h    : [B, H, K, V] fp32, read and overwritten
+ * Running it L times from h equals deltarule_fwd over those tokens from h0 = h
+ * (up to rounding order).  It works in fp32 throughout and rounds o only.
+ */
+int deltarule_step(const void* q, const void* k, const void* v, const float* g, const float* beta, float* h, void* o,
+                   int B, int H, int G, int K, int V, float scale, int dtype, void* stream);
 
 /*
  * layernorm_fwd — per row of x [rows, dim]:

@@ -55,6 +55,12 @@ SIGNATURES = {
     "linattn_bwd_workspace_size": (_sz, [_i] * 8),
     "linattn_bwd": (_i, [_vp, _ll] * 3 + [_vp, _i] + [_vp] * 9 + [_i] * 6 + [_f, _i, _vp, _sz, _vp]),
     "linattn_step": (_i, [_vp] * 4 + [_i] + [_vp] * 2 + [_i] * 5 + [_f, _i, _vp]),
+    "deltarule_num_states": (_i, [_i]),
+    "deltarule_fwd_workspace_size": (_sz, [_i] * 7),
+    "deltarule_fwd": (_i, [_vp, _ll] * 3 + [_vp] * 7 + [_i] * 6 + [_f, _i, _vp, _sz, _vp]),
+    "deltarule_bwd_workspace_size": (_sz, [_i] * 7),
+    "deltarule_bwd": (_i, [_vp, _ll] * 3 + [_vp] * 12 + [_i] * 6 + [_f, _i, _vp, _sz, _vp]),
+    "deltarule_step": (_i, [_vp] * 7 + [_i] * 5 + [_f, _i, _vp]),
     "layernorm_fwd": (_i, [_vp] * 3 + [_f] + [_vp] * 3 + [_i] * 3 + [_vp]),
     "layernorm_bwd_workspace_size": (_sz, [_i, _i]),
     "layernorm_bwd": (_i, [_vp] * 8 + [_i] * 4 + [_vp, _sz, _vp]),

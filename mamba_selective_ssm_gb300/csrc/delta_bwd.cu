@@ -1,0 +1,949 @@
+// The gated delta rule's backward (deltarule_bwd) for sm_103a.
+//
+// With U the gradient of the state leaving a chunk (dS1) and every formula in the scaled tokens of delta_common.cuh:
+//   du0 = scale P^T do + e^{c_last - c} K dS1      du = du0 - M^T (beta du0)      dv = dR = beta du      dbeta = <du, r>
+//   dS0 = e^{c_last} dS1 + scale (e^c Q)^T do - (e^c K)^T dR                               (the chain from chunk to chunk)
+//   dq = scale (e^c do S0^T + E K),   E_ts = D_ts do_t.u_s
+//   dk = -e^c dR S0^T + e^{c_last - c} u dS1^T + scale E^T Q - (F + F^T) K,   F_ts = D_ts dR_t.u_s (s < t)
+// A log decay multiplies whatever crosses it.  Every factor e^{c_t} comes with a query or a reading key and every e^{-c_s}
+// with a writing key, and their sums over a chunk meet in o, v and the state that leaves it:
+//   dg_t = sum_{s >= t} (do_s.o_s - dv_s.v_s) + <S1, dS1>        (s within the chunk)
+// so the fp32 gradients dg and dbeta need no product over V but sums along its columns, which the warps that hold o, u and du
+// have in fp32; what enters dq and dk alone is rounded to their type's terms.
+#include <stddef.h>
+
+#include "delta_common.cuh"
+
+namespace {
+
+using namespace ssk;
+
+// ---------------------------------------------------------------- the chain
+// As in the forward, a warp carries 16 columns of dS, transposed, from the last chunk to the first.  It leaves dS1 and du of
+// every chunk ([V][K] and [V][64], fp32) and dv.
+template <typename T, int KP>
+struct BackStage {
+  static constexpr int k = 0, q = k + DTile<KP, kTerms<T>>::bytes, m = q + DTile<KP, kTerms<T>>::bytes, p = m + kDMBytes,
+                       vec = p + DTile<kDC, 2>::bytes, up = vec + kDVec * 4, slices = up + 2 * kDC * 4;
+  static int bytes(int warps) { return slices + warps * DSlice<T>::bytes; }
+};
+
+constexpr int kWalkThreads = 256;
+
+template <typename T, int KP>
+__global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const T* __restrict__ dout, const float* __restrict__ dh_last,
+                                                                 T* __restrict__ dv, float* __restrict__ dS, float* __restrict__ du,
+                                                                 float* __restrict__ dh0, int stages, int stage_bytes) {
+  using St = BackStage<T, KP>;
+  constexpr int N = kTerms<T>, KT = KP / 8;
+  extern __shared__ __align__(128) unsigned char raw[];
+  const uint32_t sb = smem_u32(raw);
+  const LinAttn& a = p.a;
+  const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t2 = 2 * (lane & 3);
+  const int nvt = (a.V + nt / 2 - 1) / (nt / 2);
+  const int vt = (int)(blockIdx.x % nvt);
+  const long long bh = blockIdx.x / nvt;
+  const int h = (int)(bh % a.H), b = (int)(bh / a.H), gh = h / (a.H / a.G);
+  const int v0 = vt * (nt / 2) + warp * 16, vw = a.V - v0;
+  const int len = a.len(b), nck = (len + kDC - 1) / kDC;
+  const T* q = static_cast<const T*>(a.q) + (long long)b * a.L * a.ldq + (long long)gh * a.K;
+  const T* k = static_cast<const T*>(a.k) + (long long)b * a.L * a.ldk + (long long)gh * a.K;
+  const long long ldo = (long long)a.H * a.V;
+  const long long row0 = ((long long)b * a.L * a.H + h) * a.V + v0;
+
+  auto fetch = [&](int ck) {
+    const uint32_t at = sb + (stages == 2 ? (ck & 1) * stage_bytes : 0);
+    const long long t0 = (long long)ck * kDC;
+    const int valid = len - (int)t0 < kDC ? len - (int)t0 : kDC;
+    const long long item = bh * a.nck + ck;
+    tile_load<T, KP>(at + St::k, k + t0 * a.ldk, a.ldk, valid, a.K, tid, nt);
+    tile_load<T, KP>(at + St::q, q + t0 * a.ldq, a.ldq, valid, a.K, tid, nt);
+    tile_copy(at + St::m, p.M + item * kDMBytes, kDMBytes, tid, nt);
+    tile_copy(at + St::p, p.P + item * DTile<kDC, 2>::bytes, DTile<kDC, 2>::bytes, tid, nt);
+    tile_copy(at + St::vec, reinterpret_cast<const unsigned char*>(p.vec + item * kDVec), kDVec * 4, tid, nt);
+    DSlice<T>::load(at + St::slices + warp * DSlice<T>::bytes, dout + row0 + t0 * ldo, ldo, valid, vw, lane);
+    cp_commit();
+  };
+
+  float U[KT][4];
+#pragma unroll
+  for (int j = 0; j < KT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int kk = 8 * j + t2 + (e & 1), vv = g + (e >> 1) * 8;
+      U[j][e] = dh_last != nullptr && kk < a.K && vv < vw ? dh_last[(bh * a.K + kk) * a.V + v0 + vv] : 0.f;
+    }
+
+  if (nck > 0) fetch(nck - 1);
+  for (int ck = nck - 1; ck >= 0; --ck) {
+    const uint32_t off = stages == 2 ? (uint32_t)((ck & 1) * stage_bytes) : 0u, at = sb + off;
+    const float* vec = reinterpret_cast<const float*>(raw + off + St::vec);
+    float* up = reinterpret_cast<float*>(raw + off + St::up);
+    const uint32_t mine = at + St::slices + warp * DSlice<T>::bytes;
+    const long long item = bh * a.nck + ck;
+    cp_wait<0>();
+    __syncthreads();
+    tile_scale<T, KP>(at + St::k, up, tid, nt);
+    tile_scale<T, KP>(at + St::q, up + kDC, tid, nt);
+    __syncthreads();
+    if (stages == 2 && ck > 0) fetch(ck - 1);
+#pragma unroll
+    for (int j = 0; j < KT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const int kk = 8 * j + t2, vv = g + (e >> 1) * 8;
+        if (kk < a.K && vv < vw)
+          *reinterpret_cast<float2*>(dS + (item * a.V + v0 + vv) * a.K + kk) = make_float2(U[j][e], U[j][e + 1]);
+      }
+    // du0^T = (rest K dS1)^T + scale do^T P
+    float D[8][4];
+    {
+      const RowScale us = row_scale(U);
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) D[n][e] = 0.f;
+#pragma unroll
+      for (int kb = 0; kb < KP / 16; ++kb) {
+        uint32_t hi[4], lo[4];
+        left_terms(hi, lo, U[2 * kb], U[2 * kb + 1], us);
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+          uint32_t bb[N][4];
+#pragma unroll
+          for (int n = 0; n < N; ++n) right_rows<KP, N>(bb[n], at + St::k, np, kb, n, lane);
+          mma_terms<N>(D[2 * np], D[2 * np + 1], hi, lo, bb[0], bb[N - 1]);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const float2 re = *reinterpret_cast<const float2*>(vec + kDC + 8 * n + t2);
+        D[n][0] *= re.x * us.r[0].up;
+        D[n][1] *= re.y * us.r[0].up;
+        D[n][2] *= re.x * us.r[1].up;
+        D[n][3] *= re.y * us.r[1].up;
+      }
+    }
+    uint32_t hi[4][4], lo[4][4];
+    {  // (do scaled by powers of two only: one exact term in bf16)
+      float x[8][4];
+#pragma unroll
+      for (int np = 0; np < 4; ++np) DSlice<T>::read(mine, np, lane, x[2 * np], x[2 * np + 1]);
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const float2 qu = *reinterpret_cast<const float2*>(up + kDC + 8 * n + t2);
+        x[n][0] *= qu.x;
+        x[n][1] *= qu.y;
+        x[n][2] *= qu.x;
+        x[n][3] *= qu.y;
+      }
+      const RowScale xs = row_scale(x);
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) {
+        if constexpr (N == 1) left_first(hi[kb], x[2 * kb], x[2 * kb + 1], xs);
+        else left_terms(hi[kb], lo[kb], x[2 * kb], x[2 * kb + 1], xs);
+      }
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int kb = np; kb < 4; ++kb) {  // tokens from this one on
+          uint32_t b0[4], b1[4];
+          right_cols<kDC, 2>(b0, at + St::p, np, kb, 0, lane);
+          right_cols<kDC, 2>(b1, at + St::p, np, kb, 1, lane);
+          if constexpr (N == 1) {
+            mma_f16(c[0], hi[kb], b1[0], b1[1]);
+            mma_f16(c[1], hi[kb], b1[2], b1[3]);
+            mma_f16(c[0], hi[kb], b0[0], b0[1]);
+            mma_f16(c[1], hi[kb], b0[2], b0[3]);
+          } else {
+            mma_terms<2>(c[0], c[1], hi[kb], lo[kb], b0, b1);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) D[2 * np + i][e] = fmaf(a.scale * xs.r[e >> 1].up, c[i][e], D[2 * np + i][e]);
+      }
+    }
+    {  // du^T = du0^T - (beta du0)^T M
+      float w[8][4];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const int t = 8 * n + t2;
+        const float2 em = *reinterpret_cast<const float2*>(vec + 3 * kDC + t), be = *reinterpret_cast<const float2*>(vec + 2 * kDC + t);
+        w[n][0] = be.x * em.x * D[n][0];
+        w[n][1] = be.y * em.y * D[n][1];
+        w[n][2] = be.x * em.x * D[n][2];
+        w[n][3] = be.y * em.y * D[n][3];
+      }
+      const RowScale ws = row_scale(w);
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) left_terms(hi[kb], lo[kb], w[2 * kb], w[2 * kb + 1], ws);
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int kb = np; kb < 4; ++kb) {
+          uint32_t b0[4], b1[4];
+          right_cols<kDC, 2>(b0, at + St::m, np, kb, 0, lane);
+          right_cols<kDC, 2>(b1, at + St::m, np, kb, 1, lane);
+          mma_terms<2>(c[0], c[1], hi[kb], lo[kb], b0, b1);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) D[2 * np + i][e] = fmaf(-ws.r[e >> 1].up, c[i][e], D[2 * np + i][e]);
+      }
+    }
+    const int t0 = ck * kDC, rows = a.L - t0 < kDC ? a.L - t0 : kDC;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const int t = 8 * n + t2;
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const int vv = g + (e >> 1) * 8;
+        if (vv < vw) *reinterpret_cast<float2*>(du + (item * a.V + v0 + vv) * kDC + t) = make_float2(D[n][e], D[n][e + 1]);
+      }
+      const float2 be = *reinterpret_cast<const float2*>(vec + 2 * kDC + t), ku = *reinterpret_cast<const float2*>(up + t);
+      const float d0 = __frcp_rn(ku.x), d1 = __frcp_rn(ku.y);
+      D[n][0] *= be.x;
+      D[n][1] *= be.y;
+      D[n][2] *= be.x;
+      D[n][3] *= be.y;
+      const bool on0 = t0 + t < len, on1 = t0 + t + 1 < len;
+      const float x[4] = {on0 ? D[n][0] * d0 : 0.f, on1 ? D[n][1] * d1 : 0.f, on0 ? D[n][2] * d0 : 0.f, on1 ? D[n][3] * d1 : 0.f};
+      store_tokens(dv + row0 + (long long)t0 * ldo, ldo, 8 * n, rows, vw, x, lane);
+    }
+    {  // dS0^T = e^{c_last} dS1^T + (scale e^c do)^T Q - (e^c dR)^T K, the two left operands in one scale
+      float x[8][4];
+#pragma unroll
+      for (int np = 0; np < 4; ++np) DSlice<T>::read(mine, np, lane, x[2 * np], x[2 * np + 1]);
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const int t = 8 * n + t2;
+        const float2 in = *reinterpret_cast<const float2*>(vec + t), qu = *reinterpret_cast<const float2*>(up + kDC + t);
+        const float f0 = a.scale * in.x * qu.x, f1 = a.scale * in.y * qu.y;
+        x[n][0] *= f0;
+        x[n][1] *= f1;
+        x[n][2] *= f0;
+        x[n][3] *= f1;
+        D[n][0] *= -in.x;
+        D[n][1] *= -in.y;
+        D[n][2] *= -in.x;
+        D[n][3] *= -in.y;
+      }
+      RowScale xs = row_scale(x);
+      const RowScale ds = row_scale(D);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (ds.r[i].up > xs.r[i].up) xs.r[i] = ds.r[i];
+      uint32_t dh[4][4], dl[4][4];
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) {
+        left_terms(hi[kb], lo[kb], x[2 * kb], x[2 * kb + 1], xs);
+        left_terms(dh[kb], dl[kb], D[2 * kb], D[2 * kb + 1], xs);
+      }
+      const float whole = vec[4 * kDC];
+#pragma unroll
+      for (int jp = 0; jp < KP / 16; ++jp) {
+        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+          uint32_t bb[N][4];
+#pragma unroll
+          for (int n = 0; n < N; ++n) right_cols<KP, N>(bb[n], at + St::q, jp, kb, n, lane);
+          mma_terms<N>(c[0], c[1], hi[kb], lo[kb], bb[0], bb[N - 1]);
+#pragma unroll
+          for (int n = 0; n < N; ++n) right_cols<KP, N>(bb[n], at + St::k, jp, kb, n, lane);
+          mma_terms<N>(c[0], c[1], dh[kb], dl[kb], bb[0], bb[N - 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) U[2 * jp + i][e] = fmaf(U[2 * jp + i][e], whole, c[i][e] * xs.r[e >> 1].up);
+      }
+    }
+    if (stages == 1) {
+      __syncthreads();
+      if (ck > 0) fetch(ck - 1);
+    }
+  }
+  if (dh0 != nullptr) {
+#pragma unroll
+    for (int j = 0; j < KT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int kk = 8 * j + t2 + (e & 1), vv = g + (e >> 1) * 8;
+        if (kk < a.K && vv < vw) dh0[(bh * a.K + kk) * a.V + v0 + vv] = U[j][e];
+      }
+  }
+  const int w = vw < 16 ? vw : 16;  // tokens of chunks past the row's end
+  for (long long i = (long long)nck * kDC * 16 + lane; i < (long long)a.L * 16; i += 32)
+    if ((int)(i & 15) < w) ActT<T>::st1(dv + row0 + (i >> 4) * ldo + (i & 15), 0.f);
+}
+
+// ---------------------------------------------------------------- the other gradients, chunk by chunk
+// A CTA takes one (batch row, head, chunk).  First each warp takes 16 columns of V: it finds u and o as the forward does, and
+// what the columns add to dg and dbeta.  Then the warps share the products that contract over V, from tiles in shared memory
+// scaled as a whole: u, dR, S0, dS1 lie [V][..].
+template <typename T, int KP, int VP>
+struct GradSmem {
+  static constexpr int N = kTerms<T>, tile = DTile<KP, N>::bytes;
+  static constexpr int vk = VP * KP * 2 * N, vt = VP * kDC * 2 * N, tt = DTile<kDC, N>::bytes;
+  static constexpr int doo = 0, u = doo + DTile<VP, N>::bytes, r = u + vt, front = r + vt;
+  // bf16: everything has a place, but M and P lie where S0 and dS1 come.  fp32: k, q and then S0, dS1, and k, q again
+  // take turns, E and F lie where M and P were.
+  static constexpr bool turns = N == 2;
+  static constexpr int both = 2 * tile > vk ? 2 * tile : vk;  // k with q, or one of S0 and dS1
+  static constexpr int k = front, q = k + tile;
+  static constexpr int s0 = turns ? front : q + tile, s1 = turns ? s0 : s0 + vk;
+  static constexpr int mp = 2 * kDMBytes;
+  static constexpr int m = turns ? front + both : s0, p = m + kDMBytes;
+  static constexpr int e = turns ? m : s0 + (2 * vk > mp ? 2 * vk : mp), f = e + tt;
+  static constexpr int end = turns ? m + (mp > 2 * tt ? mp : 2 * tt) : f + tt;
+  static constexpr int vec = end, up = vec + kDVec * 4, red = up + 3 * kDC * 4, bytes = red + (2 * 8 * kDC + 64) * 4;
+};
+
+constexpr int kGradThreads = 256;
+
+// 2^13 .. 2^14 for the largest of eight warps' maxima
+__device__ __forceinline__ Pow2 warps_scale(const float* m, int stride) {
+  float x = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) x = fmaxf(x, m[w * stride]);
+  return operand_scale(x);
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+template <int NJ>
+__device__ __forceinline__ float abs_max(const float (&x)[NJ][4]) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(x[j][e]));
+  return warp_max(m);
+}
+// accumulators to a tile of rows of W columns: rows r0 + lane / 4 (+ 8), column tile j
+template <int W, int N>
+__device__ __forceinline__ void store_acc(uint32_t tile, int r0, int j, const float (&x)[4], float f, int lane) {
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {
+    const int r = r0 + (lane >> 2) + (e >> 1) * 8;
+    uint32_t hi, lo;
+    split_half(x[e] * f, x[e + 1] * f, hi, lo);
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(tile + DTile<W, N>::at(r, j, 0) + 4 * (lane & 3)), "r"(hi) : "memory");
+    if constexpr (N == 2)
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(tile + DTile<W, N>::at(r, j, 1) + 4 * (lane & 3)), "r"(lo) : "memory");
+  }
+}
+// c += a b over one step, the terms that N asks for
+template <int N>
+__device__ __forceinline__ void mma_pair(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[N][4], const uint32_t (&b)[N][4]) {
+  if constexpr (N == 1) {
+    mma_f16(c0, a[0], b[0][0], b[0][1]);
+    mma_f16(c1, a[0], b[0][2], b[0][3]);
+  } else {
+    mma_terms<2>(c0, c1, a[0], a[1], b[0], b[1]);
+  }
+}
+
+template <typename T, typename TO, int KP, int VP>
+__global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const float* __restrict__ ckpt, const T* __restrict__ dout,
+                                                                  const float* __restrict__ dS, const float* __restrict__ du,
+                                                                  TO* __restrict__ dq, TO* __restrict__ dk, int heads,
+                                                                  float* __restrict__ dg, float* __restrict__ dbeta) {
+  using Sm = GradSmem<T, KP, VP>;
+  constexpr int N = kTerms<T>, KT = KP / 8, VB = VP / 16, NC = KP / 16;  // NC: column tiles of a warp's half of K
+  extern __shared__ __align__(128) unsigned char raw[];
+  const uint32_t sb = smem_u32(raw);
+  const LinAttn& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t2 = 2 * (lane & 3);
+  const long long item = blockIdx.x, bh = item / a.nck;
+  const int ck = (int)(item % a.nck), h = (int)(bh % a.H), b = (int)(bh / a.H), gh = h / (a.H / a.G);
+  const long long t0 = (long long)ck * kDC;
+  const int len = a.len(b), rows = a.L - (int)t0 < kDC ? a.L - (int)t0 : kDC;
+  const int valid = len - (int)t0 < 0 ? 0 : len - (int)t0 < kDC ? len - (int)t0 : kDC;
+  const long long tok = (long long)b * a.L + t0;
+  // rows of dq and dk: `heads` of them to a token (the groups', or every head's own part)
+  const long long ldg = (long long)heads * a.K;
+  TO* dqb = dq + (tok * heads + (heads == a.G ? gh : h)) * a.K;
+  TO* dkb = dk + (tok * heads + (heads == a.G ? gh : h)) * a.K;
+  if (valid == 0) {
+    for (int i = tid; i < rows * a.K; i += kGradThreads) {
+      ActT<TO>::st1(dqb + i / a.K * ldg + i % a.K, 0.f);
+      ActT<TO>::st1(dkb + i / a.K * ldg + i % a.K, 0.f);
+    }
+    if (tid < rows) {
+      if (dg != nullptr) dg[(tok + tid) * a.H + h] = 0.f;
+      dbeta[(tok + tid) * a.H + h] = 0.f;
+    }
+    return;
+  }
+  const T* q = static_cast<const T*>(a.q) + tok * a.ldq + (long long)gh * a.K;
+  const T* k = static_cast<const T*>(a.k) + tok * a.ldk + (long long)gh * a.K;
+  const T* v = static_cast<const T*>(a.v) + tok * a.ldv + (long long)h * a.V;
+  const long long ldo = (long long)a.H * a.V;
+  const T* dob = dout + (tok * a.H + h) * a.V;
+  float *vec = reinterpret_cast<float*>(raw + Sm::vec), *up = reinterpret_cast<float*>(raw + Sm::up), *red = reinterpret_cast<float*>(raw + Sm::red);
+  float* mx = red + 2 * 8 * kDC;  // eight warps' maxima: S0, u, dR, dS1, E, F, and the state's product
+  tile_load<T, KP>(sb + Sm::k, k, a.ldk, valid, a.K, tid, kGradThreads);
+  tile_load<T, KP>(sb + Sm::q, q, a.ldq, valid, a.K, tid, kGradThreads);
+  tile_load<T, VP>(sb + Sm::doo, dob, ldo, valid, a.V, tid, kGradThreads);
+  tile_copy(sb + Sm::m, p.M + item * kDMBytes, kDMBytes, tid, kGradThreads);
+  tile_copy(sb + Sm::p, p.P + item * kDMBytes, kDMBytes, tid, kGradThreads);
+  tile_copy(sb + Sm::vec, reinterpret_cast<const unsigned char*>(p.vec + item * kDVec), kDVec * 4, tid, kGradThreads);
+  cp_commit();
+  if (tid < 64) mx[tid] = 0.f;
+  const int v0 = warp * 16, vw = a.V - v0;  // this warp's columns
+  // a [V][K] state in the order of accumulators
+  auto state = [&](const float* src, float (&x)[KT][4]) {
+#pragma unroll
+    for (int j = 0; j < KT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const int kk = 8 * j + t2, vv = g + (e >> 1) * 8;
+        float2 y = make_float2(0.f, 0.f);
+        if (kk < a.K && vv < vw) y = *reinterpret_cast<const float2*>(src + (long long)(v0 + vv) * a.K + kk);
+        x[j][e] = y.x;
+        x[j][e + 1] = y.y;
+      }
+  };
+  float S[KT][4];
+  const float* s0 = ckpt + (bh * (a.nck + 1) + ck) * a.V * a.K;
+  if (warp < VB) state(s0, S);
+  cp_wait<0>();
+  __syncthreads();
+  tile_scale<T, KP>(sb + Sm::k, up, tid, kGradThreads);
+  tile_scale<T, KP>(sb + Sm::q, up + kDC, tid, kGradThreads);
+  // do of this warp's columns (before it is scaled in place), v and du, all tokens by columns
+  float X[8][4], R[8][4], D[8][4];
+  if (warp < VB) {
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = 8 * n + t2 + (e & 1), vv = g + (e >> 1) * 8;
+        const bool on = t < valid && vv < vw;
+        X[n][e] = on ? ActT<T>::ld(v + (long long)t * a.ldv + v0 + vv) : 0.f;
+        D[n][e] = vv < vw ? du[(item * a.V + v0 + vv) * kDC + t] : 0.f;
+      }
+  }
+  tile_scale<T, VP>(sb + Sm::doo, up + 2 * kDC, tid, kGradThreads);
+  __syncthreads();
+  if (warp < VB) {
+    float O[8][4];
+    uint32_t hi[4][4], lo[4][4];
+    const RowScale ss = row_scale(S);
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) R[n][e] = O[n][e] = 0.f;
+#pragma unroll
+    for (int kb = 0; kb < KP / 16; ++kb) {
+      uint32_t sh[4], sl[4];
+      left_terms(sh, sl, S[2 * kb], S[2 * kb + 1], ss);
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        uint32_t bb[N][4];
+#pragma unroll
+        for (int n = 0; n < N; ++n) right_rows<KP, N>(bb[n], sb + Sm::k, np, kb, n, lane);
+        mma_terms<N>(R[2 * np], R[2 * np + 1], sh, sl, bb[0], bb[N - 1]);
+#pragma unroll
+        for (int n = 0; n < N; ++n) right_rows<KP, N>(bb[n], sb + Sm::q, np, kb, n, lane);
+        mma_terms<N>(O[2 * np], O[2 * np + 1], sh, sl, bb[0], bb[N - 1]);
+      }
+    }
+    float w[8][4];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const int t = 8 * n + t2;
+      const float2 in = *reinterpret_cast<const float2*>(vec + t), ku = *reinterpret_cast<const float2*>(up + t);
+      const float2 be = *reinterpret_cast<const float2*>(vec + 2 * kDC + t);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float f = (e & 1 ? in.y : in.x) * ss.r[e >> 1].up;
+        X[n][e] *= __frcp_rn(e & 1 ? ku.y : ku.x);
+        R[n][e] = fmaf(-f, R[n][e], X[n][e]);
+        O[n][e] *= f;
+        w[n][e] = (e & 1 ? be.y : be.x) * R[n][e];
+      }
+    }
+    {
+      const RowScale ws = row_scale(w);
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) left_terms(hi[kb], lo[kb], w[2 * kb], w[2 * kb + 1], ws);
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int kb = 0; kb <= np; ++kb) {
+          uint32_t b0[4], b1[4];
+          right_rows<kDC, 2>(b0, sb + Sm::m, np, kb, 0, lane);
+          right_rows<kDC, 2>(b1, sb + Sm::m, np, kb, 1, lane);
+          mma_terms<2>(c[0], c[1], hi[kb], lo[kb], b0, b1);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 em = *reinterpret_cast<const float2*>(vec + 3 * kDC + 16 * np + 8 * i + t2);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) R[2 * np + i][e] = fmaf(-(e & 1 ? em.y : em.x) * ws.r[e >> 1].up, c[i][e], R[2 * np + i][e]);
+        }
+      }
+    }
+    // R is r: dbeta; then u and dR
+    float db[16], af[16];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const int t = 8 * n + t2;
+      const float2 be = *reinterpret_cast<const float2*>(vec + 2 * kDC + t);
+      db[2 * n] = D[n][0] * R[n][0] + D[n][2] * R[n][2];
+      db[2 * n + 1] = D[n][1] * R[n][1] + D[n][3] * R[n][3];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        R[n][e] *= e & 1 ? be.y : be.x;
+        D[n][e] *= e & 1 ? be.y : be.x;
+      }
+      af[2 * n] = -(D[n][0] * X[n][0] + D[n][2] * X[n][2]);
+      af[2 * n + 1] = -(D[n][1] * X[n][1] + D[n][3] * X[n][3]);
+    }
+    {
+      const RowScale us = row_scale(R);
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) left_terms(hi[kb], lo[kb], R[2 * kb], R[2 * kb + 1], us);
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int kb = 0; kb <= np; ++kb) {
+          uint32_t b0[4], b1[4];
+          right_rows<kDC, 2>(b0, sb + Sm::p, np, kb, 0, lane);
+          right_rows<kDC, 2>(b1, sb + Sm::p, np, kb, 1, lane);
+          mma_terms<2>(c[0], c[1], hi[kb], lo[kb], b0, b1);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int n = 2 * np + i, t = 8 * n + t2;
+          const float2 qu = *reinterpret_cast<const float2*>(up + kDC + t);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tt = t + (e & 1), vv = g + (e >> 1) * 8;
+            const float x = tt < valid && vv < vw ? ActT<T>::ld(dob + (long long)tt * ldo + v0 + vv) : 0.f;
+            const float oo = a.scale * (e & 1 ? qu.y : qu.x) * fmaf(c[i][e], us.r[e >> 1].up, O[n][e]);
+            if (tt < valid) af[2 * n + (e & 1)] = fmaf(x, oo, af[2 * n + (e & 1)]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        db[i] += __shfl_xor_sync(0xffffffffu, db[i], o);
+        af[i] += __shfl_xor_sync(0xffffffffu, af[i], o);
+      }
+      if (g == 0) {
+        const int t = (i >> 1) * 8 + t2 + (i & 1);
+        red[warp * kDC + t] = db[i];
+        red[(8 + warp) * kDC + t] = af[i];
+      }
+    }
+    const float ms = abs_max(S), mu = abs_max(R), md = abs_max(D);
+    if (lane == 0) {
+      mx[warp * 8] = ms;
+      mx[warp * 8 + 1] = mu;
+      mx[warp * 8 + 2] = md;
+    }
+  }
+  __syncthreads();
+  const Pow2 scS = warps_scale(mx, 8), scU = warps_scale(mx + 1, 8), scR = warps_scale(mx + 2, 8);
+  if (warp < VB) {
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      store_acc<kDC, N>(sb + Sm::u, v0, n, R[n], scU.down, lane);
+      store_acc<kDC, N>(sb + Sm::r, v0, n, D[n], scR.down, lane);
+    }
+    if constexpr (!Sm::turns) {
+#pragma unroll
+      for (int j = 0; j < KT; ++j) store_acc<KP, N>(sb + Sm::s0, v0, j, S[j], scS.down, lane);
+    }
+    // <S1, dS1> of these columns, and dS1's largest
+    float x = 0.f;
+    state(dS + item * a.V * a.K, S);
+    const float* s1 = s0 + (long long)a.V * a.K;
+#pragma unroll
+    for (int j = 0; j < KT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const int kk = 8 * j + t2, vv = g + (e >> 1) * 8;
+        if (kk < a.K && vv < vw) {
+          const float2 y = *reinterpret_cast<const float2*>(s1 + (long long)(v0 + vv) * a.K + kk);
+          x = fmaf(y.x, S[j][e], fmaf(y.y, S[j][e + 1], x));
+        }
+      }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    const float m = abs_max(S);
+    if (lane == 0) {
+      mx[warp * 8 + 3] = m;
+      mx[warp * 8 + 6] = x;
+    }
+  }
+  __syncthreads();
+  const Pow2 scT = warps_scale(mx + 3, 8);
+  if (!Sm::turns && warp < VB) {
+#pragma unroll
+    for (int j = 0; j < KT; ++j) store_acc<KP, N>(sb + Sm::s1, v0, j, S[j], scT.down, lane);
+  }
+  if (warp == 0) {  // dbeta, and the sums from each token on
+    float s[2], d[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = 2 * lane + i;
+      s[i] = d[i] = 0.f;
+      for (int w = 0; w < VB; ++w) {
+        d[i] += red[w * kDC + t];
+        s[i] += red[(8 + w) * kDC + t];
+      }
+      if (t < rows) dbeta[(tok + t) * a.H + h] = t < valid ? d[i] * up[t] * up[t] : 0.f;
+    }
+    s[0] += s[1];
+    float x = 0.f;
+    for (int w = 0; w < VB; ++w) x += mx[w * 8 + 6];
+    float incl = s[0];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float y = __shfl_down_sync(0xffffffffu, incl, o);
+      if (lane + o < 32) incl += y;
+    }
+    float after = __shfl_down_sync(0xffffffffu, incl, 1);
+    if (lane == 31) after = 0.f;
+    if (dg != nullptr) {
+      if (2 * lane < rows) dg[(tok + 2 * lane) * a.H + h] = 2 * lane < valid ? x + incl : 0.f;
+      if (2 * lane + 1 < rows) dg[(tok + 2 * lane + 1) * a.H + h] = 2 * lane + 1 < valid ? x + (s[1] + after) : 0.f;
+    }
+  }
+  // E and F, a warp's 16 tokens t against half of the tokens s
+  const int mb = warp & 3, half = warp >> 2, vb = (a.V + 15) / 16;
+  {
+    float E[4][4], F[4][4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) E[n][e] = F[n][e] = 0.f;
+    if (2 * half <= mb) {
+      for (int kb = 0; kb < vb; ++kb) {
+        uint32_t ea[N][4], fa[N][4];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          left_rows<VP, N>(ea[n], sb + Sm::doo, mb, kb, n, lane);
+          left_cols<kDC, N>(fa[n], sb + Sm::r, mb, kb, n, lane);
+        }
+#pragma unroll
+        for (int np = 0; np < 2; ++np) {
+          uint32_t bb[N][4];
+#pragma unroll
+          for (int n = 0; n < N; ++n) right_cols<kDC, N>(bb[n], sb + Sm::u, 2 * half + np, kb, n, lane);
+          mma_pair<N>(E[2 * np], E[2 * np + 1], ea, bb);
+          mma_pair<N>(F[2 * np], F[2 * np + 1], fa, bb);
+        }
+      }
+    }
+    // D_ts = e^{c_t - c_s} again from the scalars: e^{c_t} / e^{c_s} would lose small ones, so the gates are summed anew
+    float* cc = red;  // (the sums in it have been taken by warp 0 before the barrier below)
+    __syncthreads();
+    if (warp == 0) {
+      ChunkGates<kDC> gates;
+      if (a.g != nullptr) gates.fetch(a, b, h, (int)t0, (int)t0 + valid, lane);
+      else gates.g[0] = gates.g[1] = 0.f;
+      gates.scan(lane, [&](int i, Dec e) { cc[i] = e.hi; cc[kDC + i] = e.lo; });
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = 16 * mb + g + (e >> 1) * 8, s = 32 * half + 8 * n + t2 + (e & 1);
+        const float d = s <= t ? dec_diff(cc[t], cc[kDC + t], cc[s], cc[kDC + s]) : 0.f;
+        E[n][e] = s <= t ? a.scale * up[kDC + t] * up[2 * kDC + t] * scU.up * d * E[n][e] : 0.f;
+        F[n][e] = s < t ? -scR.up * scU.up * d * F[n][e] : 0.f;
+      }
+    const float me = abs_max(E), mf = abs_max(F);
+    if (lane == 0) {
+      mx[warp * 8 + 4] = me;
+      mx[warp * 8 + 5] = mf;
+    }
+    __syncthreads();
+    const Pow2 scE = warps_scale(mx + 4, 8), scF = warps_scale(mx + 5, 8);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      store_acc<kDC, N>(sb + Sm::e, 16 * mb, 4 * half + n, E[n], scE.down, lane);
+      store_acc<kDC, N>(sb + Sm::f, 16 * mb, 4 * half + n, F[n], scF.down, lane);
+    }
+  }
+  const Pow2 scE = warps_scale(mx + 4, 8), scF = warps_scale(mx + 5, 8);
+  // dq and dk: a warp's 16 tokens and half of the columns of K
+  float Q[NC][4], Kg[NC][4], C[NC][4];
+  const int ta = 16 * mb + g, tb = ta + 8;
+  auto zero = [&] {
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) C[j][e] = 0.f;
+  };
+  auto add = [&](float (&to)[NC][4], float fa, float fb, bool first) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) to[j][e] = fmaf(e < 2 ? fa : fb, C[j][e], first ? 0.f : to[j][e]);
+  };
+  // C += (left operand at step kb) x (the tile's rows 16 kb .., this warp's columns)
+  auto step = [&](uint32_t tile, int kb, const uint32_t (&la)[N][4]) {
+#pragma unroll
+    for (int jp = 0; jp < NC / 2; ++jp) {
+      uint32_t bb[N][4];
+#pragma unroll
+      for (int n = 0; n < N; ++n) right_cols<KP, N>(bb[n], tile, half * (NC / 2) + jp, kb, n, lane);
+      mma_pair<N>(C[2 * jp], C[2 * jp + 1], la, bb);
+    }
+  };
+  auto put_state = [&](uint32_t tile, const float* src, float f) {
+    if (warp < VB) {
+      state(src, S);
+#pragma unroll
+      for (int j = 0; j < KT; ++j) store_acc<KP, N>(tile, v0, j, S[j], f, lane);
+    }
+  };
+  __syncthreads();  // E, F; bf16: S0, dS1; fp32: k, q have been read
+  if constexpr (Sm::turns) {
+    put_state(sb + Sm::s0, s0, scS.down);
+    __syncthreads();
+  }
+  zero();
+  for (int kb = 0; kb < vb; ++kb) {
+    uint32_t la[N][4];
+#pragma unroll
+    for (int n = 0; n < N; ++n) left_rows<VP, N>(la[n], sb + Sm::doo, mb, kb, n, lane);
+    step(sb + Sm::s0, kb, la);
+  }
+  const float fs = a.scale * scS.up;
+  add(Q, fs * vec[ta] * up[2 * kDC + ta], fs * vec[tb] * up[2 * kDC + tb], true);
+  zero();
+  for (int kb = 0; kb < vb; ++kb) {
+    uint32_t la[N][4];
+#pragma unroll
+    for (int n = 0; n < N; ++n) left_cols<kDC, N>(la[n], sb + Sm::r, mb, kb, n, lane);
+    step(sb + Sm::s0, kb, la);
+  }
+  add(Kg, -vec[ta] * scR.up * scS.up, -vec[tb] * scR.up * scS.up, true);
+  if constexpr (Sm::turns) {
+    __syncthreads();
+    put_state(sb + Sm::s1, dS + item * a.V * a.K, scT.down);
+    __syncthreads();
+  }
+  zero();
+  for (int kb = 0; kb < vb; ++kb) {
+    uint32_t la[N][4];
+#pragma unroll
+    for (int n = 0; n < N; ++n) left_cols<kDC, N>(la[n], sb + Sm::u, mb, kb, n, lane);
+    step(sb + Sm::s1, kb, la);
+  }
+  add(Kg, vec[kDC + ta] * scU.up * scT.up, vec[kDC + tb] * scU.up * scT.up, false);
+  if constexpr (Sm::turns) {
+    __syncthreads();
+    tile_load<T, KP>(sb + Sm::k, k, a.ldk, valid, a.K, tid, kGradThreads);
+    tile_load<T, KP>(sb + Sm::q, q, a.ldq, valid, a.K, tid, kGradThreads);
+    cp_commit();
+    cp_wait<0>();
+    __syncthreads();
+    tile_scale<T, KP>(sb + Sm::k, up, tid, kGradThreads);
+    tile_scale<T, KP>(sb + Sm::q, up + kDC, tid, kGradThreads);
+    __syncthreads();
+  }
+  zero();
+#pragma unroll
+  for (int kb = 0; kb < 4; ++kb) {
+    uint32_t la[N][4];
+    if (kb > mb) continue;
+#pragma unroll
+    for (int n = 0; n < N; ++n) left_rows<kDC, N>(la[n], sb + Sm::e, mb, kb, n, lane);
+    step(sb + Sm::k, kb, la);
+  }
+  add(Q, scE.up * __frcp_rn(up[kDC + ta]), scE.up * __frcp_rn(up[kDC + tb]), false);
+  zero();
+#pragma unroll
+  for (int kb = 0; kb < 4; ++kb) {
+    uint32_t la[N][4];
+    if (kb < mb) continue;
+#pragma unroll
+    for (int n = 0; n < N; ++n) left_cols<kDC, N>(la[n], sb + Sm::e, mb, kb, n, lane);
+    step(sb + Sm::q, kb, la);
+  }
+  add(Kg, scE.up, scE.up, false);
+  zero();
+#pragma unroll
+  for (int kb = 0; kb < 4; ++kb) {
+    uint32_t la[N][4];
+    if (kb <= mb) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) left_rows<kDC, N>(la[n], sb + Sm::f, mb, kb, n, lane);
+      step(sb + Sm::k, kb, la);
+    }
+    if (kb >= mb) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) left_cols<kDC, N>(la[n], sb + Sm::f, mb, kb, n, lane);
+      step(sb + Sm::k, kb, la);
+    }
+  }
+  add(Kg, scF.up, scF.up, false);
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {
+    const int t = e == 0 ? ta : tb;
+    if (t >= rows) continue;
+    const float f = __frcp_rn(up[t]);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = half * (KP / 2) + 8 * j + t2;
+      if (c >= a.K) continue;
+      ActT<TO>::st2(dqb + (long long)t * ldg + c, t < valid ? Q[j][e] : 0.f, t < valid ? Q[j][e + 1] : 0.f);
+      ActT<TO>::st2(dkb + (long long)t * ldg + c, t < valid ? Kg[j][e] * f : 0.f, t < valid ? Kg[j][e + 1] * f : 0.f);
+    }
+  }
+}
+
+// dq and dk of a group from its heads' parts, added in order: [tokens, G, R, K] -> [tokens, G, K], four columns a thread
+template <typename T>
+__global__ void __launch_bounds__(256) delta_share_kernel(const float* __restrict__ pq, const float* __restrict__ pk, T* __restrict__ dq,
+                                                          T* __restrict__ dk, long long n4, int R, int K) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  const float* src = (blockIdx.y == 0 ? pq : pk) + i * 4 / K * R * K + i * 4 % K;
+  T* dst = (blockIdx.y == 0 ? dq : dk) + i * 4;
+  float4 s = *reinterpret_cast<const float4*>(src);
+  for (int r = 1; r < R; ++r) {
+    const float4 x = *reinterpret_cast<const float4*>(src + (long long)r * K);
+    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+  }
+  ActT<T>::st2(dst, s.x, s.y);
+  ActT<T>::st2(dst + 2, s.z, s.w);
+}
+
+struct BwdPlan {
+  Delta p;
+  size_t m, pp, vec, ds, du, part, bytes;
+};
+
+int bwd_plan(int B, int L, int H, int G, int K, int V, int dtype, BwdPlan& pl) {
+  const int rc = delta_validate(B, L, H, G, K, V, dtype);
+  if (rc != SS_OK) return rc;
+  pl.p = Delta{};
+  LinAttn& a = pl.p.a;
+  a.B = B; a.L = L; a.H = H; a.G = G; a.K = K; a.V = V;
+  a.nck = (L + kDC - 1) / kDC;
+  pl.p.pterms = 2;
+  const size_t items = (size_t)B * H * a.nck;
+  pl.m = pl.pp = items * kDMBytes;
+  pl.vec = items * kDVec * sizeof(float);
+  pl.ds = items * K * V * sizeof(float);
+  pl.du = items * kDC * V * sizeof(float);
+  pl.part = H > G ? (size_t)B * L * H * K * sizeof(float) : 0;
+  pl.bytes = pl.m + pl.pp + pl.vec + pl.ds + pl.du + 2 * pl.part;
+  return SS_OK;
+}
+
+struct BwdArgs {
+  const float *ckpt, *dh_last;
+  const void* dout;
+  void *dq, *dk, *dv;
+  float *dg, *dbeta, *dh0, *dS, *du, *pq, *pk;
+};
+
+template <typename T, int KP>
+int chain(const BwdPlan& pl, const BwdArgs& x, cudaStream_t s) {
+  using St = BackStage<T, KP>;
+  const LinAttn& a = pl.p.a;
+  const long long bh = (long long)a.B * a.H;
+  int warps = (a.V + 15) / 16;
+  while (warps > 1 && bh * ((a.V + 16 * warps - 1) / (16 * warps)) < 100) warps = (warps + 1) / 2;
+  const int nvt = (a.V + 16 * warps - 1) / (16 * warps);
+  const int sb = St::bytes(warps), stages = 2 * sb <= 227 * 1024 ? 2 : 1;
+  return lin_launch(delta_bwd_kernel<T, KP>, (unsigned)(bh * nvt), 32 * warps, (size_t)sb * stages, s, pl.p, static_cast<const T*>(x.dout), x.dh_last,
+                    static_cast<T*>(x.dv), x.dS, x.du, x.dh0, stages, sb);
+}
+
+template <typename T, int KP, int VP>
+int grads(const BwdPlan& pl, const BwdArgs& x, cudaStream_t s) {
+  const LinAttn& a = pl.p.a;
+  const unsigned grid = (unsigned)((long long)a.B * a.H * a.nck);
+  constexpr size_t smem = GradSmem<T, KP, VP>::bytes;
+  static_assert(smem <= 227 * 1024, "a chunk's tiles fit shared memory");
+  const T* dout = static_cast<const T*>(x.dout);
+  if (a.H == a.G)
+    return lin_launch(delta_grad_kernel<T, T, KP, VP>, grid, kGradThreads, smem, s, pl.p, x.ckpt, dout, x.dS, x.du, static_cast<T*>(x.dq),
+                      static_cast<T*>(x.dk), a.G, x.dg, x.dbeta);
+  const int rc = lin_launch(delta_grad_kernel<T, float, KP, VP>, grid, kGradThreads, smem, s, pl.p, x.ckpt, dout, x.dS, x.du, x.pq, x.pk, a.H, x.dg,
+                            x.dbeta);
+  if (rc != SS_OK) return rc;
+  const long long n4 = (long long)a.B * a.L * a.G * a.K / 4;
+  delta_share_kernel<T><<<dim3((unsigned)((n4 + 255) / 256), 2), 256, 0, s>>>(x.pq, x.pk, static_cast<T*>(x.dq), static_cast<T*>(x.dk), n4,
+                                                                              a.H / a.G, a.K);
+  return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+template <typename T, int KP>
+int run(const BwdPlan& pl, const BwdArgs& x, cudaStream_t s) {
+  const int rc = chain<T, KP>(pl, x, s);
+  if (rc != SS_OK) return rc;
+  return pl.p.a.V <= 64 ? grads<T, KP, 64>(pl, x, s) : grads<T, KP, 128>(pl, x, s);
+}
+
+}  // namespace
+
+extern "C" size_t deltarule_bwd_workspace_size(int B, int L, int H, int G, int K, int V, int dtype) {
+  BwdPlan pl;
+  return bwd_plan(B, L, H, G, K, V, dtype, pl) == SS_OK ? pl.bytes : 0;
+}
+
+extern "C" int deltarule_bwd(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv, const float* g,
+                             const float* beta, const int* lengths, const float* ckpt, const void* dout, const float* dh_last, void* dq,
+                             void* dk, void* dv, float* dg, float* dbeta, float* dh0, int B, int L, int H, int G, int K, int V, float scale,
+                             int dtype, void* workspace, size_t ws_bytes, void* stream) {
+  if (!q || !k || !v || !beta || !ckpt || !dout || !dq || !dk || !dv || !dbeta || (g && !dg)) return SS_ERR_NULL;
+  BwdPlan pl;
+  int rc = bwd_plan(B, L, H, G, K, V, dtype, pl);
+  if (rc != SS_OK) return rc;
+  if ((rc = linattn_ld_ok(ldq, G, K)) != SS_OK || (rc = linattn_ld_ok(ldk, G, K)) != SS_OK || (rc = linattn_ld_ok(ldv, H, V)) != SS_OK)
+    return rc;
+  const void* ptrs[] = {q, k, v, ckpt, dout, dh_last, dq, dk, dv, dh0};
+  for (const void* x : ptrs)
+    if (x != nullptr && !ssh::aligned16(x)) return SS_ERR_ALIGN;
+  const void* words[] = {g, beta, lengths, dg, dbeta};
+  for (const void* x : words)
+    if (reinterpret_cast<uintptr_t>(x) & 3u) return SS_ERR_ALIGN;
+  if (workspace == nullptr || ws_bytes < pl.bytes) return SS_ERR_WORKSPACE;
+  if (!ssh::aligned16(workspace)) return SS_ERR_ALIGN;
+  LinAttn& a = pl.p.a;
+  a.q = q; a.k = k; a.v = v;
+  a.ldq = ldq; a.ldk = ldk; a.ldv = ldv;
+  a.g = g;
+  a.lengths = lengths;
+  a.scale = scale;
+  pl.p.beta = beta;
+  char* w = static_cast<char*>(workspace);
+  BwdArgs x{ckpt, dh_last, dout, dq, dk, dv, g ? dg : nullptr, dbeta, dh0, nullptr, nullptr, nullptr, nullptr};
+  pl.p.M = reinterpret_cast<unsigned char*>(w);
+  pl.p.P = reinterpret_cast<unsigned char*>(w += pl.m);
+  pl.p.vec = reinterpret_cast<float*>(w += pl.pp);
+  x.dS = reinterpret_cast<float*>(w += pl.vec);
+  x.du = reinterpret_cast<float*>(w += pl.ds);
+  x.pq = reinterpret_cast<float*>(w += pl.du);
+  x.pk = reinterpret_cast<float*>(w += pl.part);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((rc = ssh::delta_prep(pl.p, dtype, s)) != SS_OK) return rc;
+  if (dtype == SS_F32) return K <= 64 ? run<float, 64>(pl, x, s) : run<float, 128>(pl, x, s);
+  return K <= 64 ? run<__nv_bfloat16, 64>(pl, x, s) : run<__nv_bfloat16, 128>(pl, x, s);
+}

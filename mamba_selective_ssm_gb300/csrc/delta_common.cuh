@@ -1,0 +1,333 @@
+// Shared pieces of the gated delta rule's kernels (delta_prep.cu, delta_fwd.cu, delta_bwd.cu): the call's arguments,
+// operand tiles and the products of a warp.
+//
+//   r_t = v_t - e^{g_t} S_{t-1}^T k_t,   S_t = e^{g_t} S_{t-1} + beta_t k_t r_t^T,   o_t = scale * S_t^T q_t
+//
+// A chunk of 64 tokens that starts in state S0, with running log decay c_t and D_ts = e^{c_t - c_s}:
+//   A_ts = D_ts k_t.k_s (s < t)      M = (I + A beta)^{-1} A      P_ts = D_ts q_t.k_s (s <= t)
+//   R = V - e^c K S0      r = R - M (beta R)      u = beta r
+//   o = scale (e^c Q S0 + P u)      S1 = e^{c_last} S0 + K^T (e^{c_last - c} u)
+// M and P depend on no state: delta_prep_kernel finds them for all chunks at once.  What passes from chunk to chunk is a
+// chain of three products (K S0, M (beta R), K^T u), and every column of V is a chain of its own.
+//
+// Products run on the tensor cores in fp16 with fp32 sums.  Whatever ends in fp32 takes its fp32 operands as two fp16
+// terms (22 bits), scaled by a power of two to the range of fp16; k and q are scaled token by token:
+//   k'_t = 2^{-e_t} k_t (largest element in [1, 2)),   beta' = 4^{e} beta,   v' = 2^{-e} v,   r' = 2^{-e} r,   u' = 2^{e} u
+// leaves every formula above as it is, so that bf16 keys and queries are one exact fp16 term (fp32 ones are two).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "linattn_common.cuh"
+
+namespace ssk {
+
+constexpr int kDC = 64;        // tokens of a chunk
+constexpr int kDVec = 272;     // floats of a chunk's scalars: into, rest, beta', M's row scales (64 each), e^{c_last}
+constexpr int kDMBytes = kDC * kDC * 4;  // M of a chunk: two fp16 terms
+
+// One call's arguments.  a: q, k, v, g (null: no decay), lengths, sizes as in linear attention.
+struct Delta {
+  LinAttn a;
+  const float* beta;  // [B, L, H]
+  // what delta_prep_kernel leaves for each (batch row, head, chunk)
+  unsigned char *M, *P;  // operand tiles
+  float* vec;
+  int pterms;  // terms of P
+};
+
+template <typename T>
+constexpr int kTerms = sizeof(T) == 4 ? 2 : 1;  // fp16 terms of an activation
+
+inline int delta_validate(int B, int L, int H, int G, int K, int V, int dtype) {
+  const int rc = linattn_validate(B, L, H, G, K, V, dtype);
+  if (rc != SS_OK) return rc;
+  return (long long)B * H > (1ll << 24) || (long long)B * H * ((L + kDC - 1) / kDC) > 2147483647ll / 8 ? SS_ERR_DIM : SS_OK;
+}
+
+// ---------------------------------------------------------------- operand tiles
+// Rows of W columns of fp16 in N terms: 16-byte unit u (8 columns) of term n lies at unit (u N + n) ^ (row & 7) of its
+// row, so that the eight rows an ldmatrix reads fall on different banks.  A raw tile (activations as they are in memory)
+// takes the same bytes: unit u of bf16, or of fp32 as its two halves.
+template <int W, int N>
+struct DTile {
+  static constexpr int row = W * 2 * N, bytes = kDC * row;
+  __device__ __forceinline__ static uint32_t at(int r, int u, int n) { return (uint32_t)(r * row + (((u * N + n) ^ (r & 7)) << 4)); }
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
+  const int n = on ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// kDC rows of `width` columns of activations, `ld` elements apart, as a raw tile; rows from `valid` and columns from
+// `width` on are zero (their memory is not read)
+template <typename T, int W>
+__device__ __forceinline__ void tile_load(uint32_t tile, const T* __restrict__ src, long long ld, int valid, int width, int tid, int nt) {
+  constexpr int N = kTerms<T>, U = W / 8;
+  for (int i = tid; i < kDC * U * N; i += nt) {
+    const int r = i / (U * N), x = i % (U * N), u = x / N, n = x % N;
+    const bool on = r < valid && u * 8 < width;
+    cp16(tile + DTile<W, N>::at(r, u, n), src + (on ? (long long)r * ld + u * 8 + n * 4 : 0), on);
+  }
+}
+// a finished tile of `bytes` bytes from memory
+__device__ __forceinline__ void tile_copy(uint32_t tile, const unsigned char* __restrict__ src, int bytes, int tid, int nt) {
+  for (int i = tid * 16; i < bytes; i += nt * 16) cp16(tile + i, src + i, true);
+}
+
+// 2^-e and 2^e for e = the exponent of m >= 0, kept where both are normal numbers (and e at most 2^60 from 1)
+struct Pow2 {
+  float down, up;
+};
+template <int SHIFT, int MIN, int MAX>
+__device__ __forceinline__ Pow2 pow2_of(float m) {
+  int e = (int)(__float_as_uint(m) >> 23) & 0xff;
+  e = e < MIN ? MIN : e > MAX ? MAX : e;
+  Pow2 p;
+  p.down = __uint_as_float((uint32_t)(254 - e + SHIFT) << 23);
+  p.up = __uint_as_float((uint32_t)(e - SHIFT) << 23);
+  return p;
+}
+// an operand of a product: its largest value into [2^13, 2^14)
+__device__ __forceinline__ Pow2 operand_scale(float m) { return pow2_of<13, 14, 253>(m); }
+// a key or query: its largest element into [1, 2); elements of 2^60 and more overflow
+__device__ __forceinline__ Pow2 token_scale(float m) { return m == 0.f ? Pow2{1.f, 1.f} : pow2_of<0, 127 - 60, 127 + 60>(m); }
+
+__device__ __forceinline__ uint32_t pack_half(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 wide_half(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+// x, y as two fp16 terms: the first is off by 2^-11 of the value at most, both by 2^-22
+__device__ __forceinline__ void split_half(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_half(x, y);
+  const float2 f = wide_half(hi);
+  lo = pack_half(x - f.x, y - f.y);
+}
+__device__ __forceinline__ void store_terms(uint32_t hi_at, uint32_t lo_at, const float (&x)[8]) {
+  uint4 h, l;
+  split_half(x[0], x[1], h.x, l.x);
+  split_half(x[2], x[3], h.y, l.y);
+  split_half(x[4], x[5], h.z, l.z);
+  split_half(x[6], x[7], h.w, l.w);
+  sts128(hi_at, h);
+  sts128(lo_at, l);
+}
+
+// Raw rows become scaled fp16 operands in place; up[r] = the row's 2^e.  W / 8 neighbouring lanes hold a row.
+template <typename T, int W>
+__device__ __forceinline__ void tile_scale(uint32_t tile, float* up, int tid, int nt) {
+  constexpr int N = kTerms<T>, U = W / 8;
+  for (int i = tid; i < kDC * U; i += nt) {  // nt and kDC * U are multiples of 32: whole warps
+    const int r = i / U, u = i % U;
+    const uint32_t a0 = tile + DTile<W, N>::at(r, u, 0), a1 = tile + DTile<W, N>::at(r, u, N - 1);
+    float x[8];
+    if constexpr (N == 1) {
+      Raw8<__nv_bfloat16>::wide(lds128(a0), x);
+    } else {
+      const uint4 p = lds128(a0), q = lds128(a1);
+      x[0] = __uint_as_float(p.x); x[1] = __uint_as_float(p.y); x[2] = __uint_as_float(p.z); x[3] = __uint_as_float(p.w);
+      x[4] = __uint_as_float(q.x); x[5] = __uint_as_float(q.y); x[6] = __uint_as_float(q.z); x[7] = __uint_as_float(q.w);
+    }
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+#pragma unroll
+    for (int o = 1; o < U; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const Pow2 s = token_scale(m);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= s.down;
+    if constexpr (N == 1) {
+      sts128(a0, make_uint4(pack_half(x[0], x[1]), pack_half(x[2], x[3]), pack_half(x[4], x[5]), pack_half(x[6], x[7])));
+    } else {
+      store_terms(a0, a1, x);
+    }
+    if (u == 0) up[r] = s.up;
+  }
+}
+
+// ---------------------------------------------------------------- a warp's products
+// m16n8k16: a warp's accumulators of a 16 x 8 tile are c[0..1] of row lane / 4 and c[2..3] of row lane / 4 + 8, columns
+// 2 (lane % 4) and the next.  As the left operand of the next product they are where they have to be: a chain of products
+// whose rows are columns of V stays in registers.
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ uint32_t trans8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Right operands from a tile, for two neighbouring column tiles of 8: b[0], b[1] of the first, b[2], b[3] of the second.
+// The contraction runs along the tile's columns (16 from 16 kb), the product's columns are its rows (16 from 16 np):
+template <int W, int N>
+__device__ __forceinline__ void right_rows(uint32_t (&b)[4], uint32_t tile, int np, int kb, int n, int lane) {
+  const int mi = lane >> 3;
+  ldsm(b, tile + DTile<W, N>::at(16 * np + (mi >> 1) * 8 + (lane & 7), 2 * kb + (mi & 1), n));
+}
+// ... down the tile's rows (16 from 16 kb), the product's columns are its columns (16 from 16 jp):
+template <int W, int N>
+__device__ __forceinline__ void right_cols(uint32_t (&b)[4], uint32_t tile, int jp, int kb, int n, int lane) {
+  const int mi = lane >> 3;
+  ldsm_t(b, tile + DTile<W, N>::at(16 * kb + (mi & 1) * 8 + (lane & 7), 2 * jp + (mi >> 1), n));
+}
+// Left operands: 16 rows from 16 mb, contraction along the columns (16 from 16 kb)
+template <int W, int N>
+__device__ __forceinline__ void left_rows(uint32_t (&a)[4], uint32_t tile, int mb, int kb, int n, int lane) {
+  const int mi = lane >> 3;
+  ldsm(a, tile + DTile<W, N>::at(16 * mb + (mi & 1) * 8 + (lane & 7), 2 * kb + (mi >> 1), n));
+}
+// ... rows are the tile's columns (16 from 16 mb), contraction down its rows (16 from 16 kb)
+template <int W, int N>
+__device__ __forceinline__ void left_cols(uint32_t (&a)[4], uint32_t tile, int mb, int kb, int n, int lane) {
+  const int mi = lane >> 3;
+  ldsm_t(a, tile + DTile<W, N>::at(16 * kb + (mi >> 1) * 8 + (lane & 7), 2 * mb + (mi & 1), n));
+}
+
+// The scale of each of a thread's two rows of accumulators: [0] row lane / 4, [1] row lane / 4 + 8
+struct RowScale {
+  Pow2 r[2];
+};
+template <int N>
+__device__ __forceinline__ RowScale row_scale(const float (&x)[N][4]) {
+  float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    m0 = fmaxf(m0, fmaxf(fabsf(x[j][0]), fabsf(x[j][1])));
+    m1 = fmaxf(m1, fmaxf(fabsf(x[j][2]), fabsf(x[j][3])));
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+  }
+  return RowScale{{operand_scale(m0), operand_scale(m1)}};
+}
+// accumulators of two neighbouring column tiles as the left operand of a product that contracts over them, in two terms
+__device__ __forceinline__ void left_terms(uint32_t (&h)[4], uint32_t (&l)[4], const float (&x)[4], const float (&y)[4], const RowScale& s) {
+  split_half(x[0] * s.r[0].down, x[1] * s.r[0].down, h[0], l[0]);
+  split_half(x[2] * s.r[1].down, x[3] * s.r[1].down, h[1], l[1]);
+  split_half(y[0] * s.r[0].down, y[1] * s.r[0].down, h[2], l[2]);
+  split_half(y[2] * s.r[1].down, y[3] * s.r[1].down, h[3], l[3]);
+}
+__device__ __forceinline__ void left_first(uint32_t (&h)[4], const float (&x)[4], const float (&y)[4], const RowScale& s) {
+  h[0] = pack_half(x[0] * s.r[0].down, x[1] * s.r[0].down);
+  h[1] = pack_half(x[2] * s.r[1].down, x[3] * s.r[1].down);
+  h[2] = pack_half(y[0] * s.r[0].down, y[1] * s.r[0].down);
+  h[3] = pack_half(y[2] * s.r[1].down, y[3] * s.r[1].down);
+}
+
+// c0, c1 += (h + l) B over one step of 16, B of N terms at b (and bl); the lowest terms' product is dropped (2^-22)
+template <int N>
+__device__ __forceinline__ void mma_terms(float (&c0)[4], float (&c1)[4], const uint32_t (&h)[4], const uint32_t (&l)[4], const uint32_t (&b)[4],
+                                          const uint32_t (&bl)[4]) {
+  mma_f16(c0, l, b[0], b[1]);
+  mma_f16(c1, l, b[2], b[3]);
+  if constexpr (N == 2) {
+    mma_f16(c0, h, bl[0], bl[1]);
+    mma_f16(c1, h, bl[2], bl[3]);
+  }
+  mma_f16(c0, h, b[0], b[1]);
+  mma_f16(c1, h, b[2], b[3]);
+}
+
+// A warp's own 16 columns of V of a chunk (v or do), as it lies in memory: bf16 rows of 32 bytes, the two halves swapped in
+// every second group of four rows (banks); fp32 rows of 80 bytes.
+template <typename T>
+struct DSlice;
+template <>
+struct DSlice<__nv_bfloat16> {
+  static constexpr int bytes = kDC * 32;
+  __device__ __forceinline__ static uint32_t at(int t, int u) { return (uint32_t)(t * 32 + ((u ^ ((t >> 2) & 1)) << 4)); }
+  __device__ __forceinline__ static void load(uint32_t s, const __nv_bfloat16* __restrict__ src, long long ld, int valid, int width, int lane) {
+#pragma unroll
+    for (int i = lane; i < kDC * 2; i += 32) {
+      const int t = i >> 1, u = i & 1;
+      const bool on = t < valid && u * 8 < width;
+      cp16(s + at(t, u), src + (on ? (long long)t * ld + u * 8 : 0), on);
+    }
+  }
+  // tokens of column tiles 2 p and 2 p + 1 in the order of accumulators whose rows are the slice's columns
+  __device__ __forceinline__ static void read(uint32_t s, int p, int lane, float (&x)[4], float (&y)[4]) {
+    const int mi = lane >> 3;
+    uint32_t r[4];
+    ldsm_t(r, s + at(16 * p + (mi >> 1) * 8 + (lane & 7), mi & 1));
+    x[0] = bf16_lo(r[0]); x[1] = bf16_hi(r[0]); x[2] = bf16_lo(r[1]); x[3] = bf16_hi(r[1]);
+    y[0] = bf16_lo(r[2]); y[1] = bf16_hi(r[2]); y[2] = bf16_lo(r[3]); y[3] = bf16_hi(r[3]);
+  }
+};
+template <>
+struct DSlice<float> {
+  static constexpr int bytes = kDC * 80;
+  __device__ __forceinline__ static void load(uint32_t s, const float* __restrict__ src, long long ld, int valid, int width, int lane) {
+#pragma unroll
+    for (int i = lane; i < kDC * 4; i += 32) {
+      const int t = i >> 2, u = i & 3;
+      const bool on = t < valid && u * 4 < width;
+      cp16(s + t * 80 + u * 16, src + (on ? (long long)t * ld + u * 4 : 0), on);
+    }
+  }
+  __device__ __forceinline__ static float get(uint32_t s, int t, int v) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(s + t * 80 + v * 4) : "memory");
+    return x;
+  }
+  __device__ __forceinline__ static void read(uint32_t s, int p, int lane, float (&x)[4], float (&y)[4]) {
+    const int g = lane >> 2, t = 16 * p + 2 * (lane & 3);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = get(s, t + (e & 1), g + (e >> 1) * 8);
+      y[e] = get(s, t + 8 + (e & 1), g + (e >> 1) * 8);
+    }
+  }
+};
+
+// Accumulators (rows = 16 columns of V from v0, columns = 8 tokens from t) to rows of a [.., ld] array
+__device__ __forceinline__ void store_tokens(__nv_bfloat16* __restrict__ dst, long long ld, int t, int rows, int width, const float (&x)[4], int lane) {
+  const uint32_t a = trans8(ActT<__nv_bfloat16>::pack2(x[0], x[1])), b = trans8(ActT<__nv_bfloat16>::pack2(x[2], x[3]));
+  const int r = t + (lane >> 2), c = 2 * (lane & 3);
+  if (r < rows) {
+    if (c < width) *reinterpret_cast<uint32_t*>(dst + (long long)r * ld + c) = a;
+    if (8 + c < width) *reinterpret_cast<uint32_t*>(dst + (long long)r * ld + 8 + c) = b;
+  }
+}
+__device__ __forceinline__ void store_tokens(float* __restrict__ dst, long long ld, int t, int rows, int width, const float (&x)[4], int lane) {
+  const int g = lane >> 2, r = t + 2 * (lane & 3);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int c = g + (e >> 1) * 8;
+    if (r + (e & 1) < rows && c < width) dst[(long long)(r + (e & 1)) * ld + c] = x[e];
+  }
+}
+
+}  // namespace ssk
+
+namespace ssh {
+// Launches delta_prep_kernel for all chunks of a call; P in p.pterms terms.
+int delta_prep(const ssk::Delta& p, int dtype, cudaStream_t s);
+}  // namespace ssh

@@ -21,6 +21,9 @@ Names and argument order follow include/ssscan.h:
 * ``linattn_fwd(q, k, v, g, h0=None, scale=None, lengths=None)`` -> ``(o, ckpt, h_last)``
 * ``linattn_bwd(q, k, v, g, ckpt, do, dh_last=None, scale=None, lengths=None)`` -> dict of gradients
 * ``linattn_step(q, k, v, g, h, scale=None)`` -> ``o`` (h updated in place)
+* ``deltarule_fwd(q, k, v, g, beta, h0=None, scale=None, lengths=None)`` -> ``(o, ckpt, h_last)``
+* ``deltarule_bwd(q, k, v, g, beta, ckpt, do, dh_last=None, scale=None, lengths=None)`` -> dict of gradients
+* ``deltarule_step(q, k, v, g, beta, h, scale=None)`` -> ``o`` (h updated in place)
 * ``layernorm_fwd(x, scale, bias, eps)`` -> ``(y, mean, rstd)``
 * ``layernorm_bwd(dy, x, scale, mean, rstd, dscale=None, dbias=None)`` -> ``(dx, dscale, dbias)``
 
@@ -543,6 +546,99 @@ def linattn_step(q, k, v, g, h, scale=None):
                              sdt, _raw_stream(dev))
     if rc:
         check(rc, "linattn_step")
+    return o
+
+
+def deltarule_num_states(L: int) -> int:
+    """States a row of L tokens has in ``ckpt`` ([B, H, that, K, V])."""
+    return load().deltarule_num_states(L)
+
+
+@functools.lru_cache(maxsize=1024)
+def _deltarule_plan(B, L, H, G, K, V, sdt):
+    """(states, forward scratch, backward scratch) of a call's sizes."""
+    lib = load()
+    return (lib.deltarule_num_states(L), lib.deltarule_fwd_workspace_size(B, L, H, G, K, V, sdt),
+            lib.deltarule_bwd_workspace_size(B, L, H, G, K, V, sdt))
+
+
+def deltarule_fwd(q, k, v, g, beta, h0=None, scale=None, lengths=None, want_ckpt: bool = True, want_h_last: bool = True,
+                  workspace=None):
+    """The gated delta rule -> ``(o, ckpt, h_last)``: ``r_t = v_t - exp(g_t) S_{t-1}^T k_t``,
+    ``S_t = exp(g_t) S_{t-1} + beta_t k_t r_t^T``, ``o_t = scale * S_t^T q_t`` from ``S = h0``.
+
+    ``q, k`` [B, L, G, K], ``v`` [B, L, H, V] and ``lengths`` are as in ``linattn_fwd``; ``g`` (log decays, or None) and
+    ``beta`` are fp32 [B, L, H]; keys are normally of length one.  ``scale`` is ``K ** -0.5`` unless given.  ``ckpt``
+    (None unless ``want_ckpt``) is what ``deltarule_bwd`` starts from.
+
+    A NaN or infinity in a live token can reach the other tokens of its chunk of 64, also earlier ones."""
+    B, L, H, G, K, V = _linattn_sizes(q, v)
+    dev, dt, f32 = q.device, q.dtype, torch.float32
+    sdt = _act_dtype(q)
+    pq, ldq = _rows(q, "q", (B, L, G, K), dt, dev)
+    pk, ldk = _rows(k, "k", (B, L, G, K), dt, dev)
+    pv, ldv = _rows(v, "v", (B, L, H, V), dt, dev)
+    pg, pb = _opt_at(g, "g", (B, L, H), f32, dev), _at(beta, "beta", (B, L, H), f32, dev)
+    ph = _opt_at(h0, "h0", (B, H, K, V), f32, dev)
+    pn = _opt_at(lengths, "lengths", (B,), torch.int32, dev)
+    states, need, _ = _deltarule_plan(B, L, H, G, K, V, sdt)
+    o = torch.empty((B, L, H, V), device=dev, dtype=dt)
+    ckpt = torch.empty((B, H, states, K, V), device=dev, dtype=f32) if want_ckpt else None
+    h_last = torch.empty((B, H, K, V), device=dev, dtype=f32) if want_h_last else None
+    pw, have = _scratch(workspace, need, dev)
+    rc = load().deltarule_fwd(pq, ldq, pk, ldk, pv, ldv, pg, pb, ph, pn, o.data_ptr(), ckpt.data_ptr() if want_ckpt else None,
+                              h_last.data_ptr() if want_h_last else None, B, L, H, G, K, V, K ** -0.5 if scale is None else scale,
+                              sdt, pw, have, _raw_stream(dev))
+    if rc:
+        check(rc, "deltarule_fwd")
+    return o, ckpt, h_last
+
+
+def deltarule_bwd(q, k, v, g, beta, ckpt, do, dh_last=None, scale=None, lengths=None, want_dh0: bool = True, workspace=None):
+    """Gradients of ``sum(o * do)`` (+ ``sum(h_last * dh_last)``) through ``deltarule_fwd`` called with the same q, k, v, g,
+    beta, scale and lengths -> dict ``dq, dk, dv`` (q's type), ``dg`` (None when g is), ``dbeta``, ``dh0`` (fp32)."""
+    B, L, H, G, K, V = _linattn_sizes(q, v)
+    dev, dt, f32 = q.device, q.dtype, torch.float32
+    sdt = _act_dtype(q)
+    pq, ldq = _rows(q, "q", (B, L, G, K), dt, dev)
+    pk, ldk = _rows(k, "k", (B, L, G, K), dt, dev)
+    pv, ldv = _rows(v, "v", (B, L, H, V), dt, dev)
+    pg, pb = _opt_at(g, "g", (B, L, H), f32, dev), _at(beta, "beta", (B, L, H), f32, dev)
+    states, _, need = _deltarule_plan(B, L, H, G, K, V, sdt)
+    pc = _at(ckpt, "ckpt", (B, H, states, K, V), f32, dev)
+    pd = _at(do, "do", (B, L, H, V), dt, dev)
+    pl = _opt_at(dh_last, "dh_last", (B, H, K, V), f32, dev)
+    pn = _opt_at(lengths, "lengths", (B,), torch.int32, dev)
+    dg = None if g is None else torch.empty((B, L, H), device=dev, dtype=f32)
+    dbeta = torch.empty((B, L, H), device=dev, dtype=f32)
+    dq = torch.empty((B, L, G, K), device=dev, dtype=dt)
+    dk = torch.empty((B, L, G, K), device=dev, dtype=dt)
+    dv = torch.empty((B, L, H, V), device=dev, dtype=dt)
+    dh0 = torch.empty((B, H, K, V), device=dev, dtype=f32) if want_dh0 else None
+    pw, have = _scratch(workspace, need, dev)
+    rc = load().deltarule_bwd(pq, ldq, pk, ldk, pv, ldv, pg, pb, pn, pc, pd, pl, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                              None if dg is None else dg.data_ptr(), dbeta.data_ptr(), dh0.data_ptr() if want_dh0 else None,
+                              B, L, H, G, K, V, K ** -0.5 if scale is None else scale, sdt, pw, have, _raw_stream(dev))
+    if rc:
+        check(rc, "deltarule_bwd")
+    return {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dbeta": dbeta, "dh0": dh0}
+
+
+def deltarule_step(q, k, v, g, beta, h, scale=None):
+    """One token for B sequences: updates ``h`` [B, H, K, V] in place and returns o [B, H, V].
+    ``q, k`` [B, G, K], ``v`` [B, H, V], ``g`` (or None) and ``beta`` fp32 [B, H]."""
+    B, G, K = q.shape
+    _, H, V = v.shape
+    dev, dt, f32 = q.device, q.dtype, torch.float32
+    sdt = _act_dtype(q)
+    pq, pk = _at(q, "q", (B, G, K), dt, dev), _at(k, "k", (B, G, K), dt, dev)
+    pv, ph = _at(v, "v", (B, H, V), dt, dev), _at(h, "h", (B, H, K, V), f32, dev)
+    pg, pb = _opt_at(g, "g", (B, H), f32, dev), _at(beta, "beta", (B, H), f32, dev)
+    o = torch.empty_like(v)
+    rc = load().deltarule_step(pq, pk, pv, pg, pb, ph, o.data_ptr(), B, H, G, K, V, K ** -0.5 if scale is None else scale, sdt,
+                               _raw_stream(dev))
+    if rc:
+        check(rc, "deltarule_step")
     return o
 
 
