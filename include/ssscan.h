@@ -549,6 +549,41 @@ int layernorm_bwd(const void* dy, const void* x, const float* scale, const float
                   void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * groupnorm_fwd — group norm with an activation, channels last: x [N, M, C] in
+ * `groups` groups of C / groups neighbouring channels; per sample n and group,
+ * over its M positions and its channels,
+ *   mean, rstd = 1 / sqrt(mean (x - mean)^2 + eps)
+ *   y = act((x - mean) * rstd * scale + bias)     act: SiLU (silu != 0) or nothing
+ *   x, y : [N, M, C] (dtype; y overwritten, bf16 rounded to nearest even)
+ *   scale, bias : [C] fp32, bias may be NULL (zero)
+ *   mean, rstd  : [N, groups] fp32 outputs, each may be NULL
+ * M = 1 is the norm of each token's groups (the heads of a layer's output),
+ * M = L that of whole sequences.  C a multiple of 8 and of groups, at most
+ * 32768; N * groups below 2^31, N * M * C at most 2^40; eps >= 0.  x, y, scale,
+ * bias 16-byte aligned, mean and rstd 4.
+ * Statistics are fp32, the deviations taken around a mean; the reciprocal root
+ * is the hardware's (2 units in the last place).  Sums are in a fixed order.
+ * workspace: groupnorm_fwd_workspace_size() bytes (0 when a CTA holds a sample).
+ */
+size_t groupnorm_fwd_workspace_size(int N, int M, int C, int groups, int dtype);
+int groupnorm_fwd(const void* x, const float* scale, const float* bias, float eps, void* y, float* mean, float* rstd,
+                  int N, int M, int C, int groups, int silu, int dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * groupnorm_bwd — with xh = (x - mean) * rstd, t = xh * scale + bias,
+ * da = dy * act'(t) and w = da * scale:
+ *   dx = rstd * (w - mean w - xh * mean(w * xh))           [N, M, C] fp32, overwritten
+ *   dscale += sum_{n,m} da * xh;  dbias += sum_{n,m} da     [C] fp32
+ * accumulate: 1 adds to dscale, 2 to dbias, 3 to both; where its bit is 0 the
+ * array is overwritten.  dy, x (dtype); mean, rstd as groupnorm_fwd saved them;
+ * bias (NULL: zero) and silu as there; sizes and alignment as there.
+ */
+size_t groupnorm_bwd_workspace_size(int N, int M, int C, int groups, int dtype);
+int groupnorm_bwd(const void* dy, const void* x, const float* scale, const float* bias, const float* mean,
+                  const float* rstd, float* dx, float* dscale, float* dbias, int accumulate, int N, int M, int C,
+                  int groups, int silu, int dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * ss_count_nonfinite — failure detection: writes to `count` (a device
  * uint64) the number of NaN and +-Inf values among the n elements of `p`
  * (dtype SS_F32 or SS_BF16; a value counts when its exponent field is all

@@ -64,6 +64,10 @@ SIGNATURES = {
     "layernorm_fwd": (_i, [_vp] * 3 + [_f] + [_vp] * 3 + [_i] * 3 + [_vp]),
     "layernorm_bwd_workspace_size": (_sz, [_i, _i]),
     "layernorm_bwd": (_i, [_vp] * 8 + [_i] * 4 + [_vp, _sz, _vp]),
+    "groupnorm_fwd_workspace_size": (_sz, [_i] * 5),
+    "groupnorm_fwd": (_i, [_vp] * 3 + [_f] + [_vp] * 3 + [_i] * 6 + [_vp, _sz, _vp]),
+    "groupnorm_bwd_workspace_size": (_sz, [_i] * 5),
+    "groupnorm_bwd": (_i, [_vp] * 9 + [_i] * 7 + [_vp, _sz, _vp]),
     "ss_count_nonfinite_workspace_size": (_sz, []),
     "ss_count_nonfinite": (_i, [_vp, _sz, _i, _vp, _vp, _sz, _vp]),
     "ss_device_status": (_i, [_vp]),

@@ -1,0 +1,883 @@
+// Group norm with an activation, channels last, forward and backward (groupnorm_fwd, groupnorm_bwd) for sm_103a.
+//
+//   x [N, M, C], C in `groups` groups of cg channels; per sample n and group, over its M * cg values:
+//   mean, rstd = 1 / sqrt(mean (x - mean)^2 + eps);   xh = (x - mean) rstd,   t = xh scale + bias,   y = act(t)
+//   da = dy act'(t),  w = da scale;   dx = rstd (w - mean w - xh mean(w xh));   dscale += sum da xh;   dbias += sum da
+// act is SiLU (t sigmoid(t), derivative p (1 + t (1 - p)) with p = sigmoid(t)) or nothing; t is found again in the backward.
+//
+// Three forms, by what a group's values are:
+//   M = 1, cg <= 256 in eights   G lanes hold a row of a group, 32 / G groups (or rows) a warp, U rows in flight, the
+//                                values in registers between the sums and the output: one pass over memory.
+//   a sample of few values       a CTA holds one in registers (eight 16-byte units a thread), per-channel sums meet in
+//                                shared memory: one pass too.
+//   else                         sums by (sample, channels, rows) in fixed parts, a kernel that joins them, and a second
+//                                pass for the output, which takes the rows from the last: L2 still holds those.
+// The variance is taken around the mean (parts around their own first row, joined with their means), never as a difference
+// of moments.  The backward's column sums are joined by colsum_kernel in fixed order.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace {
+
+using namespace ssk;
+
+constexpr int kGnMaxDim = 32768;
+constexpr int kGnThreads = 256;
+constexpr int kGnSampleDim = 8192;  // widest sample of the one-CTA form
+
+template <int G>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = 1; o < G; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ void ld8f(const float* p, bool ok, float* o) {
+  const float4 a = ok ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4 b = ok ? __ldg(reinterpret_cast<const float4*>(p + 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w; o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+}
+template <bool SILU>
+__device__ __forceinline__ float act(float t) {
+  return SILU ? t * sigmoid(t) : t;
+}
+// dy act'(t)
+template <bool SILU>
+__device__ __forceinline__ float dact(float dy, float t) {
+  if (!SILU) return dy;
+  const float p = sigmoid(t);
+  return dy * (p * fmaf(t, 1.f - p, 1.f));
+}
+
+struct Gn {
+  int N, M, C, groups, cg;
+  float eps;
+};
+
+// ---------------------------------------------------------------- rows of a group in lanes (M = 1)
+
+template <typename T, int G, int U, bool SILU>
+__global__ void __launch_bounds__(kGnThreads) gn_fwd_lanes_kernel(Gn p, int gp, const T* __restrict__ x, const float* __restrict__ scale,
+                                                                  const float* __restrict__ bias, T* __restrict__ y, float* __restrict__ mean,
+                                                                  float* __restrict__ rstd) {
+  using R = Raw8<T>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / G, rs = 32 / G / gp;  // rs rows of gp groups a warp
+  const int g = (int)blockIdx.y * gp + slot % gp, i = (lane % G) * 8, c = g * p.cg + i;
+  const bool cv = g < p.groups && i < p.cg;
+  float sc[8], bi[8];
+  ld8f(scale + c, cv, sc);
+  ld8f(bias + c, cv && bias != nullptr, bi);
+  const float inv = 1.0f / (float)p.cg;
+  const long long step = (long long)gridDim.x * 8 * rs * U;
+  for (long long r0 = ((long long)blockIdx.x * 8 + warp) * rs * U; r0 < p.N; r0 += step) {
+    typename R::V raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long r = r0 + u * rs + slot / gp;
+      raw[u] = cv && r < p.N ? R::ld(x + r * p.C + c) : R::zero();
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long r = r0 + u * rs + slot / gp;
+      float v[8], s = 0.f;
+      R::wide(raw[u], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += v[e];
+      const float m = lanes_sum<G>(s) * inv;
+      s = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] -= m;
+        s = fmaf(v[e], v[e], s);
+      }
+      if (!cv) s = 0.f;
+      const float rv = rsqrtf(fmaf(lanes_sum<G>(s), inv, p.eps));
+      if (cv && r < p.N) {
+        if (i == 0) {
+          if (mean != nullptr) mean[r * p.groups + g] = m;
+          if (rstd != nullptr) rstd[r * p.groups + g] = rv;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = act<SILU>(fmaf(v[e] * rv, sc[e], bi[e]));
+        ActT<T>::st8(y + r * p.C + c, v);
+      }
+    }
+  }
+}
+
+template <typename T, int G, int U, bool SILU>
+__global__ void __launch_bounds__(kGnThreads) gn_bwd_lanes_kernel(Gn p, int gp, const T* __restrict__ dy, const T* __restrict__ x,
+                                                                  const float* __restrict__ scale, const float* __restrict__ bias,
+                                                                  const float* __restrict__ mean, const float* __restrict__ rstd,
+                                                                  float* __restrict__ dx, float* __restrict__ part) {
+  using R = Raw8<T>;
+  __shared__ float4 red[4][kGnThreads];
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / G, rs = 32 / G / gp;
+  const int g = (int)blockIdx.y * gp + slot % gp, i = (lane % G) * 8, c = g * p.cg + i;
+  const bool cv = g < p.groups && i < p.cg;
+  float sc[8], bi[8], as[8], ab[8];
+  ld8f(scale + c, cv, sc);
+  ld8f(bias + c, cv && SILU && bias != nullptr, bi);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) as[e] = ab[e] = 0.f;
+  const float inv = 1.0f / (float)p.cg;
+  const long long step = (long long)gridDim.x * 8 * rs * U;
+  for (long long r0 = ((long long)blockIdx.x * 8 + warp) * rs * U; r0 < p.N; r0 += step) {
+    typename R::V rx[U], ry[U];
+    float mu[U], rv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long r = r0 + u * rs + slot / gp;
+      const bool on = cv && r < p.N;
+      rx[u] = on ? R::ld(x + r * p.C + c) : R::zero();
+      ry[u] = on ? R::ld(dy + r * p.C + c) : R::zero();
+      mu[u] = on ? mean[r * p.groups + g] : 0.f;
+      rv[u] = on ? rstd[r * p.groups + g] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long r = r0 + u * rs + slot / gp;
+      float xh[8], w[8], s1 = 0.f, s2 = 0.f;
+      R::wide(rx[u], xh);
+      R::wide(ry[u], w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        xh[e] = (xh[e] - mu[u]) * rv[u];
+        const float da = dact<SILU>(w[e], fmaf(xh[e], sc[e], bi[e]));
+        as[e] = fmaf(da, xh[e], as[e]);
+        ab[e] += da;
+        w[e] = da * sc[e];
+        s1 += w[e];
+        s2 = fmaf(w[e], xh[e], s2);
+      }
+      s1 = lanes_sum<G>(s1) * inv;
+      s2 = lanes_sum<G>(s2) * inv;
+      if (cv && r < p.N) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = rv[u] * (w[e] - s1 - xh[e] * s2);
+        ActT<float>::st8(dx + r * p.C + c, w);
+      }
+    }
+  }
+  red[0][threadIdx.x] = make_float4(as[0], as[1], as[2], as[3]);
+  red[1][threadIdx.x] = make_float4(as[4], as[5], as[6], as[7]);
+  red[2][threadIdx.x] = make_float4(ab[0], ab[1], ab[2], ab[3]);
+  red[3][threadIdx.x] = make_float4(ab[4], ab[5], ab[6], ab[7]);
+  __syncthreads();
+  // the block's rows in order: a thread adds one of the four parts of a lane of a group
+  const int w = threadIdx.x >> 6, l = threadIdx.x & 63;  // (gp * G <= 32 lanes hold different channels)
+  if (l < gp * G && (int)blockIdx.y * gp + l / G < p.groups && (l % G) * 8 < p.cg) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int v = 0; v < 8; ++v)
+      for (int o = 0; o < rs; ++o) {
+        const float4 z = red[w][v * 32 + o * gp * G + l];
+        s.x += z.x; s.y += z.y; s.z += z.z; s.w += z.w;
+      }
+    const int cc = ((int)blockIdx.y * gp + l / G) * p.cg + (l % G) * 8 + (w & 1) * 4;
+    *reinterpret_cast<float4*>(part + (size_t)blockIdx.x * 2 * p.C + (w >> 1) * p.C + cc) = s;
+  }
+}
+
+// ---------------------------------------------------------------- a sample in a CTA
+
+// Which of a sample's units (8 channels of one position) a thread holds: its i-th is unit u of position m.
+struct Mine {
+  int units, rl, lanes;  // units of a position; this thread's position among `lanes` that share them
+  __device__ __forceinline__ Mine(const Gn& p) {
+    units = p.C / 8;
+    lanes = units < kGnThreads ? kGnThreads / units : 1;
+    rl = units < kGnThreads ? (int)threadIdx.x / units : 0;
+  }
+  __device__ __forceinline__ bool at(const Gn& p, int i, int& m, int& u) const {
+    if (units < kGnThreads) {
+      m = rl + i * lanes;
+      u = (int)threadIdx.x % units;
+      return rl < lanes && m < p.M;
+    }
+    const int per = (units + kGnThreads - 1) / kGnThreads;
+    m = i / per;
+    u = i % per * kGnThreads + (int)threadIdx.x;
+    return m < p.M && u < units;
+  }
+};
+inline int gn_sample_items(const Gn& p) {
+  const int units = p.C / 8;
+  if (units < kGnThreads) return (p.M + kGnThreads / units - 1) / (kGnThreads / units);
+  const long long n = (long long)((units + kGnThreads - 1) / kGnThreads) * p.M;
+  return n > 1000 ? 1000 : (int)n;
+}
+template <typename T>
+constexpr int kGnItems = 16 / sizeof(T);  // units a thread holds: 128 bytes of x
+
+// dst[g] = f(sum over the group's channels and the `lanes` rows of part), a warp to a group
+template <typename F>
+__device__ __forceinline__ void group_sums(const Gn& p, const float* part, int lanes, F f) {
+  const int lane = threadIdx.x & 31;
+  for (int g = threadIdx.x >> 5; g < p.groups; g += kGnThreads / 32) {
+    float s = 0.f;
+    for (int l = 0; l < lanes; ++l)
+      for (int j = lane; j < p.cg; j += 32) s += part[l * p.C + g * p.cg + j];
+    s = lanes_sum<32>(s);
+    if (lane == 0) f(g, s);
+  }
+}
+// per-channel sums of a thread's units into part[lanes][C]; val(i, e) its values
+template <int IT, typename V>
+__device__ __forceinline__ void channel_sums(const Gn& p, const Mine& my, float* part, V val) {
+  float s[8];
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    int m, u;
+    const bool on = my.at(p, i, m, u);
+    if (my.units < kGnThreads) {  // one unit: summed over its positions
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = on ? val(i, e) : 0.f;
+        s[e] = i == 0 ? x : s[e] + x;
+      }
+      if (i == IT - 1 && my.rl < my.lanes) ActT<float>::st8(part + my.rl * p.C + u * 8, s);
+    } else if (on) {
+      float* at = part + u * 8;
+      if (m == 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = val(i, e);
+      } else {
+        ActT<float>::ld8(at, s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] += val(i, e);
+      }
+      ActT<float>::st8(at, s);
+    }
+  }
+}
+
+inline size_t gn_part_floats(const Gn& p) { return p.C < 8 * kGnThreads ? 8 * kGnThreads : p.C; }
+
+template <typename T, bool SILU>
+__global__ void __launch_bounds__(kGnThreads) gn_fwd_sample_kernel(Gn p, const T* __restrict__ x, const float* __restrict__ scale,
+                                                                   const float* __restrict__ bias, T* __restrict__ y, float* __restrict__ mean,
+                                                                   float* __restrict__ rstd) {
+  using R = Raw8<T>;
+  constexpr int IT = kGnItems<T>;
+  extern __shared__ float4 sm4[];
+  float* part = reinterpret_cast<float*>(sm4);
+  float* st = part + (p.C < 8 * kGnThreads ? 8 * kGnThreads : p.C);  // mean, rstd of each group
+  const Mine my(p);
+  const float inv = 1.0f / ((float)p.M * (float)p.cg);
+  for (long long n = blockIdx.x; n < p.N; n += gridDim.x) {
+    const T* xn = x + n * p.M * p.C;
+    typename R::V raw[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      int m, u;
+      raw[i] = my.at(p, i, m, u) ? R::ld(xn + (long long)m * p.C + u * 8) : R::zero();
+    }
+    float v[8];
+    channel_sums<IT>(p, my, part, [&](int i, int e) {
+      if (e == 0) R::wide(raw[i], v);
+      return v[e];
+    });
+    __syncthreads();
+    group_sums(p, part, my.lanes, [&](int g, float s) { st[g] = s * inv; });
+    __syncthreads();
+    channel_sums<IT>(p, my, part, [&](int i, int e) {
+      int m, u;
+      my.at(p, i, m, u);
+      if (e == 0) R::wide(raw[i], v);
+      const float d = v[e] - st[(u * 8 + e) / p.cg];
+      return d * d;
+    });
+    __syncthreads();
+    group_sums(p, part, my.lanes, [&](int g, float s) {
+      const float r = rsqrtf(fmaf(s, inv, p.eps));
+      st[p.groups + g] = r;
+      if (mean != nullptr) mean[n * p.groups + g] = st[g];
+      if (rstd != nullptr) rstd[n * p.groups + g] = r;
+    });
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      int m, u;
+      if (!my.at(p, i, m, u)) continue;
+      float sc[8], bi[8];
+      ld8f(scale + u * 8, true, sc);
+      ld8f(bias + u * 8, bias != nullptr, bi);
+      R::wide(raw[i], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int g = (u * 8 + e) / p.cg;
+        v[e] = act<SILU>(fmaf((v[e] - st[g]) * st[p.groups + g], sc[e], bi[e]));
+      }
+      ActT<T>::st8(y + (n * p.M + m) * p.C + u * 8, v);
+    }
+    __syncthreads();  // the next sample's sums
+  }
+}
+
+template <typename T, bool SILU>
+__global__ void __launch_bounds__(kGnThreads) gn_bwd_sample_kernel(Gn p, const T* __restrict__ dy, const T* __restrict__ x,
+                                                                   const float* __restrict__ scale, const float* __restrict__ bias,
+                                                                   const float* __restrict__ mean, const float* __restrict__ rstd,
+                                                                   float* __restrict__ dx, float* __restrict__ out) {
+  using R = Raw8<T>;
+  constexpr int IT = kGnItems<T>;
+  extern __shared__ float4 sm4[];
+  const int pf = p.C < 8 * kGnThreads ? 8 * kGnThreads : p.C;
+  float *part = reinterpret_cast<float*>(sm4), *acc = part + pf, *st = acc + 2 * p.C;
+  pdl_trigger();
+  for (int c = threadIdx.x; c < 2 * p.C; c += kGnThreads) acc[c] = 0.f;
+  const Mine my(p);
+  const float inv = 1.0f / ((float)p.M * (float)p.cg);
+  for (long long n = blockIdx.x; n < p.N; n += gridDim.x) {
+    typename R::V rx[IT], ry[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      int m, u;
+      const bool on = my.at(p, i, m, u);
+      const long long at = (n * p.M + m) * p.C + u * 8;
+      rx[i] = on ? R::ld(x + at) : R::zero();
+      ry[i] = on ? R::ld(dy + at) : R::zero();
+    }
+    const float *mu = mean + n * p.groups, *rv = rstd + n * p.groups;
+    float sc[8], bi[8], xh[8], da[8];
+    auto unit = [&](int i, int u) {  // xh and da of a unit
+      ld8f(scale + u * 8, true, sc);
+      ld8f(bias + u * 8, SILU && bias != nullptr, bi);
+      R::wide(rx[i], xh);
+      R::wide(ry[i], da);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int g = (u * 8 + e) / p.cg;
+        xh[e] = (xh[e] - mu[g]) * rv[g];
+        da[e] = dact<SILU>(da[e], fmaf(xh[e], sc[e], bi[e]));
+      }
+    };
+    // sums of da, then of da xh: per channel into the column sums, per group with the scale
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      channel_sums<IT>(p, my, part, [&](int i, int e) {
+        int m, u;
+        my.at(p, i, m, u);
+        if (e == 0) unit(i, u);
+        return k == 0 ? da[e] : da[e] * xh[e];
+      });
+      __syncthreads();
+      for (int c = threadIdx.x; c < p.C; c += kGnThreads) {
+        float s = 0.f;
+        for (int l = 0; l < my.lanes; ++l) s += part[l * p.C + c];
+        acc[(1 - k) * p.C + c] += s;
+        part[c] = s * scale[c];
+      }
+      __syncthreads();
+      group_sums(p, part, 1, [&](int g, float s) { st[k * p.groups + g] = s * inv; });
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      int m, u;
+      if (!my.at(p, i, m, u)) continue;
+      unit(i, u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int g = (u * 8 + e) / p.cg;
+        da[e] = rv[g] * (da[e] * sc[e] - st[g] - xh[e] * st[p.groups + g]);
+      }
+      ActT<float>::st8(dx + (n * p.M + m) * p.C + u * 8, da);
+    }
+    __syncthreads();
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * p.C; c += kGnThreads) out[(size_t)blockIdx.x * 2 * p.C + c] = acc[c];
+}
+
+// ---------------------------------------------------------------- long samples, in parts
+
+// A CTA's part: `ut` units of channels from u0, rows m0 .. m1 of sample n; thread = (unit, row lane)
+struct Part {
+  int ut, tiles, splits, per;  // units a CTA, CTAs across C, parts of the rows, rows of a part
+};
+struct Where {
+  long long n;
+  int split, c, rl, lanes, m0, m1;
+  bool on;
+  __device__ __forceinline__ Where(const Gn& p, const Part& q) {
+    long long id = blockIdx.x;
+    const int tile = (int)(id % q.tiles);
+    id /= q.tiles;
+    split = (int)(id % q.splits);
+    n = id / q.splits;
+    lanes = kGnThreads / q.ut;
+    rl = (int)threadIdx.x / q.ut;
+    c = (tile * q.ut + (int)threadIdx.x % q.ut) * 8;
+    on = rl < lanes && c < p.C;
+    m0 = split * q.per;
+    m1 = m0 + q.per < p.M ? m0 + q.per : p.M;
+  }
+};
+// the row lanes' sums, added in order: red[thread][8] -> the first lane
+__device__ __forceinline__ void lanes_add(float4 (*red)[kGnThreads], int ut, int lanes, float (&s)[8]) {
+  __syncthreads();
+  red[0][threadIdx.x] = make_float4(s[0], s[1], s[2], s[3]);
+  red[1][threadIdx.x] = make_float4(s[4], s[5], s[6], s[7]);
+  __syncthreads();
+  if ((int)threadIdx.x < ut)
+    for (int l = 1; l < lanes; ++l) {
+      const float4 a = red[0][l * ut + threadIdx.x], b = red[1][l * ut + threadIdx.x];
+      s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w; s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
+    }
+}
+constexpr int kGnAhead = 4;  // rows of a thread in flight
+
+// part[n][split][c] = the rows' sum, and after all of those the sum of squares around their mean.  The sum is taken of the
+// values themselves (a mean near zero would keep the rounding of whatever it is taken around), the squares around the first
+// row's value.
+template <typename T>
+__global__ void __launch_bounds__(kGnThreads) gn_stats_kernel(Gn p, Part q, const T* __restrict__ x, float* __restrict__ part) {
+  using R = Raw8<T>;
+  __shared__ float4 red[2][kGnThreads];
+  pdl_trigger();
+  const Where w(p, q);
+  float base[8], s0[8], s1[8], s2[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) base[e] = s0[e] = s1[e] = s2[e] = 0.f;
+  const T* src = x + w.n * p.M * p.C + w.c;
+  if (w.on) {
+    R::wide(R::ld(src + (long long)w.m0 * p.C), base);
+    for (int m = w.m0 + w.rl; m < w.m1; m += kGnAhead * w.lanes) {
+      typename R::V raw[kGnAhead];
+#pragma unroll
+      for (int u = 0; u < kGnAhead; ++u)
+        if (m + u * w.lanes < w.m1) raw[u] = R::ld(src + (long long)(m + u * w.lanes) * p.C);
+#pragma unroll
+      for (int u = 0; u < kGnAhead; ++u) {
+        if (m + u * w.lanes >= w.m1) break;
+        float v[8];
+        R::wide(raw[u], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          s0[e] += v[e];
+          v[e] -= base[e];
+          s1[e] += v[e];
+          s2[e] = fmaf(v[e], v[e], s2[e]);
+        }
+      }
+    }
+  }
+  lanes_add(red, q.ut, w.lanes, s0);
+  lanes_add(red, q.ut, w.lanes, s1);
+  lanes_add(red, q.ut, w.lanes, s2);
+  if (w.on && w.rl == 0) {
+    const float cnt = (float)(w.m1 - w.m0);
+    float* at = part + (w.n * q.splits + w.split) * p.C + w.c;
+    float sq[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sq[e] = fmaxf(fmaf(-s1[e], s1[e] / cnt, s2[e]), 0.f);
+    ActT<float>::st8(at, s0);
+    ActT<float>::st8(at + (long long)p.N * q.splits * p.C, sq);
+  }
+}
+
+__device__ __forceinline__ float block_sum(float* red, float v) {
+  v = lanes_sum<32>(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int w = 0; w < kGnThreads / 32; ++w) s += red[w];
+  return s;
+}
+
+// a CTA joins the parts of one (sample, group)
+__global__ void __launch_bounds__(kGnThreads) gn_join_kernel(Gn p, Part q, const float* __restrict__ part, float* __restrict__ mean,
+                                                             float* __restrict__ rstd) {
+  __shared__ float red[kGnThreads / 32];
+  pdl_trigger();
+  const long long n = blockIdx.x / p.groups;
+  const int g = blockIdx.x % p.groups, cnt = q.splits * p.cg;
+  const float inv = 1.0f / ((float)p.M * (float)p.cg);
+  const float* sum = part + n * q.splits * p.C + g * p.cg;
+  const float* sq = sum + (long long)p.N * q.splits * p.C;
+  auto rows = [&](int i) { return (float)(min(p.M, (i / p.cg + 1) * q.per) - i / p.cg * q.per); };
+  auto at = [&](int i) { return (long long)(i / p.cg) * p.C + i % p.cg; };
+  pdl_wait();
+  float s = 0.f;
+  for (int i = threadIdx.x; i < cnt; i += kGnThreads) s += sum[at(i)];
+  const float m = block_sum(red, s) * inv;
+  s = 0.f;
+  for (int i = threadIdx.x; i < cnt; i += kGnThreads) {
+    const float d = sum[at(i)] / rows(i) - m;
+    s += fmaf(d * d, rows(i), sq[at(i)]);
+  }
+  s = block_sum(red, s);
+  if (threadIdx.x == 0) {
+    mean[blockIdx.x] = m;
+    rstd[blockIdx.x] = rsqrtf(fmaf(s, inv, p.eps));
+  }
+}
+
+template <typename T, bool SILU>
+__global__ void __launch_bounds__(kGnThreads) gn_apply_kernel(Gn p, Part q, const T* __restrict__ x, const float* __restrict__ scale,
+                                                              const float* __restrict__ bias, const float* __restrict__ mean,
+                                                              const float* __restrict__ rstd, T* __restrict__ y) {
+  using R = Raw8<T>;
+  const Where w(p, q);
+  if (!w.on) return;
+  float sc[8], bi[8], mu[8];
+  ld8f(scale + w.c, true, sc);
+  ld8f(bias + w.c, bias != nullptr, bi);
+  pdl_wait();
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const long long g = w.n * p.groups + (w.c + e) / p.cg;
+    mu[e] = mean[g];
+    sc[e] *= rstd[g];
+  }
+  const long long base = w.n * p.M * p.C + w.c;
+  for (int m = w.m1 - 1 - w.rl; m >= w.m0; m -= kGnAhead * w.lanes) {
+    typename R::V raw[kGnAhead];
+#pragma unroll
+    for (int u = 0; u < kGnAhead; ++u)
+      if (m - u * w.lanes >= w.m0) raw[u] = R::ld(x + base + (long long)(m - u * w.lanes) * p.C);
+#pragma unroll
+    for (int u = 0; u < kGnAhead; ++u) {
+      if (m - u * w.lanes < w.m0) break;
+      float v[8];
+      R::wide(raw[u], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = act<SILU>(fmaf(v[e] - mu[e], sc[e], bi[e]));
+      ActT<T>::st8(y + base + (long long)(m - u * w.lanes) * p.C, v);
+    }
+  }
+}
+
+// part[n][split][2 C]: the rows' sums of da xh and of da
+template <typename T, bool SILU>
+__global__ void __launch_bounds__(kGnThreads) gn_bwd_sums_kernel(Gn p, Part q, const T* __restrict__ dy, const T* __restrict__ x,
+                                                                 const float* __restrict__ scale, const float* __restrict__ bias,
+                                                                 const float* __restrict__ mean, const float* __restrict__ rstd,
+                                                                 float* __restrict__ part) {
+  using R = Raw8<T>;
+  __shared__ float4 red[2][kGnThreads];
+  pdl_trigger();
+  const Where w(p, q);
+  float s1[8], s2[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s1[e] = s2[e] = 0.f;
+  if (w.on) {
+    float sc[8], bi[8], mu[8], rv[8];
+    ld8f(scale + w.c, true, sc);
+    ld8f(bias + w.c, SILU && bias != nullptr, bi);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const long long g = w.n * p.groups + (w.c + e) / p.cg;
+      mu[e] = mean[g];
+      rv[e] = rstd[g];
+    }
+    const long long base = w.n * p.M * p.C + w.c;
+    for (int m = w.m0 + w.rl; m < w.m1; m += kGnAhead * w.lanes) {
+      typename R::V rx[kGnAhead], ry[kGnAhead];
+#pragma unroll
+      for (int u = 0; u < kGnAhead; ++u)
+        if (m + u * w.lanes < w.m1) {
+          const long long at = base + (long long)(m + u * w.lanes) * p.C;
+          rx[u] = R::ld(x + at);
+          ry[u] = R::ld(dy + at);
+        }
+#pragma unroll
+      for (int u = 0; u < kGnAhead; ++u) {
+        if (m + u * w.lanes >= w.m1) break;
+        float xh[8], da[8];
+        R::wide(rx[u], xh);
+        R::wide(ry[u], da);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          xh[e] = (xh[e] - mu[e]) * rv[e];
+          da[e] = dact<SILU>(da[e], fmaf(xh[e], sc[e], bi[e]));
+          s1[e] += da[e];
+          s2[e] = fmaf(da[e], xh[e], s2[e]);
+        }
+      }
+    }
+  }
+  lanes_add(red, q.ut, w.lanes, s1);
+  lanes_add(red, q.ut, w.lanes, s2);
+  if (w.on && w.rl == 0) {
+    float* at = part + (w.n * q.splits + w.split) * 2 * p.C + w.c;
+    ActT<float>::st8(at, s2);
+    ActT<float>::st8(at + p.C, s1);
+  }
+}
+
+// means[n][g] of w and of w xh from the parts
+__global__ void __launch_bounds__(kGnThreads) gn_bwd_join_kernel(Gn p, Part q, const float* __restrict__ part, const float* __restrict__ scale,
+                                                                 float2* __restrict__ means) {
+  __shared__ float red[kGnThreads / 32];
+  pdl_trigger();
+  const long long n = blockIdx.x / p.groups;
+  const int g = blockIdx.x % p.groups, cnt = q.splits * p.cg;
+  const float inv = 1.0f / ((float)p.M * (float)p.cg);
+  const float* at = part + n * q.splits * 2 * p.C + g * p.cg;
+  pdl_wait();
+  float a = 0.f, b = 0.f;
+  for (int i = threadIdx.x; i < cnt; i += kGnThreads) {
+    const float s = scale[g * p.cg + i % p.cg];
+    const float* y = at + (long long)(i / p.cg) * 2 * p.C + i % p.cg;
+    b = fmaf(y[0], s, b);
+    a = fmaf(y[p.C], s, a);
+  }
+  a = block_sum(red, a);
+  b = block_sum(red, b);
+  if (threadIdx.x == 0) means[blockIdx.x] = make_float2(a * inv, b * inv);
+}
+
+template <typename T, bool SILU>
+__global__ void __launch_bounds__(kGnThreads) gn_bwd_apply_kernel(Gn p, Part q, const T* __restrict__ dy, const T* __restrict__ x,
+                                                                  const float* __restrict__ scale, const float* __restrict__ bias,
+                                                                  const float* __restrict__ mean, const float* __restrict__ rstd,
+                                                                  const float2* __restrict__ means, float* __restrict__ dx) {
+  using R = Raw8<T>;
+  const Where w(p, q);
+  if (!w.on) return;
+  float sc[8], bi[8], mu[8], rv[8];
+  float2 av[8];
+  ld8f(scale + w.c, true, sc);
+  ld8f(bias + w.c, SILU && bias != nullptr, bi);
+  pdl_wait();
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const long long g = w.n * p.groups + (w.c + e) / p.cg;
+    mu[e] = mean[g];
+    rv[e] = rstd[g];
+    av[e] = means[g];
+  }
+  constexpr int A = kGnAhead / 2;
+  const long long base = w.n * p.M * p.C + w.c;
+  for (int m = w.m1 - 1 - w.rl; m >= w.m0; m -= A * w.lanes) {
+    typename R::V rx[A], ry[A];
+#pragma unroll
+    for (int u = 0; u < A; ++u)
+      if (m - u * w.lanes >= w.m0) {
+        const long long at = base + (long long)(m - u * w.lanes) * p.C;
+        rx[u] = R::ld(x + at);
+        ry[u] = R::ld(dy + at);
+      }
+#pragma unroll
+    for (int u = 0; u < A; ++u) {
+      if (m - u * w.lanes < w.m0) break;
+      float xh[8], da[8];
+      R::wide(rx[u], xh);
+      R::wide(ry[u], da);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        xh[e] = (xh[e] - mu[e]) * rv[e];
+        da[e] = dact<SILU>(da[e], fmaf(xh[e], sc[e], bi[e])) * sc[e];
+        da[e] = rv[e] * (da[e] - av[e].x - xh[e] * av[e].y);
+      }
+      ActT<float>::st8(dx + base + (long long)(m - u * w.lanes) * p.C, da);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+enum GnForm { kLanes, kSample, kParts };
+
+struct GnPlan {
+  Gn p;
+  GnForm form;
+  int G, gp, segs, grid;  // lanes
+  Part q;                 // parts
+  size_t fwd, bwd;        // workspace
+  int rows;               // partial rows of the backward's column sums
+};
+
+int gn_plan(int N, int M, int C, int groups, int dtype, GnPlan& pl) {
+  if (N <= 0 || M <= 0 || C <= 0 || groups <= 0 || C > kGnMaxDim || C % groups != 0) return SS_ERR_DIM;
+  if (dtype != SS_F32 && dtype != SS_BF16) return SS_ERR_UNSUPPORTED;
+  if (C % 8 != 0) return SS_ERR_ALIGN;
+  if ((long long)N * groups > 2147483647ll || (long long)N * M > (1ll << 40) / C) return SS_ERR_DIM;
+  Gn& p = pl.p;
+  p.N = N; p.M = M; p.C = C; p.groups = groups; p.cg = C / groups;
+  pl.fwd = pl.bwd = 0;
+  const int items = gn_sample_items(p);
+  if (M == 1 && p.cg % 8 == 0 && p.cg <= 256) {
+    pl.form = kLanes;
+    pl.G = 1;
+    while (pl.G * 8 < p.cg) pl.G *= 2;
+    pl.gp = 1;
+    while (pl.gp < groups && pl.gp < 32 / pl.G) pl.gp *= 2;
+    pl.segs = (groups + pl.gp - 1) / pl.gp;
+    const long long sets = ((long long)N + 32 / pl.G / pl.gp * 8 - 1) / (32 / pl.G / pl.gp * 8);  // one set of rows for each warp
+    pl.grid = (int)std::min<long long>(sets, std::max(1, 152 * 8 / pl.segs));
+    pl.rows = pl.grid;
+    pl.bwd = (size_t)pl.rows * 2 * C * sizeof(float);
+  } else if (C <= kGnSampleDim && items <= (dtype == SS_F32 ? kGnItems<float> : kGnItems<__nv_bfloat16>)) {
+    pl.form = kSample;
+    pl.grid = std::min(N, 152 * 4);
+    pl.rows = pl.grid;
+    pl.bwd = (size_t)pl.rows * 2 * C * sizeof(float);
+  } else {
+    pl.form = kParts;
+    Part& q = pl.q;
+    q.ut = std::min(32, C / 8);
+    q.tiles = (C / 8 + q.ut - 1) / q.ut;
+    const int lanes = kGnThreads / q.ut;
+    const long long want = std::max<long long>(1, 152ll * 8 / ((long long)N * q.tiles));
+    const long long most = std::max(1, M / (lanes * kGnAhead));
+    const int splits = (int)std::min(want, most);
+    q.per = (M + splits - 1) / splits;
+    q.splits = (M + q.per - 1) / q.per;
+    if ((long long)N * q.splits * q.tiles > 2147483647ll) return SS_ERR_DIM;
+    pl.rows = N * q.splits;
+    pl.fwd = (size_t)N * q.splits * 2 * C * sizeof(float) + (size_t)N * groups * 2 * sizeof(float);
+    pl.bwd = (size_t)N * q.splits * 2 * C * sizeof(float) + (size_t)N * groups * 2 * sizeof(float);
+  }
+  return SS_OK;
+}
+
+template <typename T, int G, bool SILU>
+void fwd_lanes(const GnPlan& pl, const T* x, const float* scale, const float* bias, T* y, float* mean, float* rstd, cudaStream_t s) {
+  gn_fwd_lanes_kernel<T, G, 4, SILU><<<dim3(pl.grid, pl.segs), kGnThreads, 0, s>>>(pl.p, pl.gp, x, scale, bias, y, mean, rstd);
+}
+template <typename T, int G, bool SILU>
+void bwd_lanes(const GnPlan& pl, const T* dy, const T* x, const float* scale, const float* bias, const float* mean, const float* rstd, float* dx,
+               float* part, cudaStream_t s) {
+  gn_bwd_lanes_kernel<T, G, 2, SILU><<<dim3(pl.grid, pl.segs), kGnThreads, 0, s>>>(pl.p, pl.gp, dy, x, scale, bias, mean, rstd, dx, part);
+}
+#define GN_LANES(f, ...)                             \
+  switch (pl.G) {                                    \
+    case 1: f<T, 1, SILU>(__VA_ARGS__); break;       \
+    case 2: f<T, 2, SILU>(__VA_ARGS__); break;       \
+    case 4: f<T, 4, SILU>(__VA_ARGS__); break;       \
+    case 8: f<T, 8, SILU>(__VA_ARGS__); break;       \
+    case 16: f<T, 16, SILU>(__VA_ARGS__); break;     \
+    default: f<T, 32, SILU>(__VA_ARGS__); break;     \
+  }
+
+template <typename T, bool SILU>
+int fwd(const GnPlan& pl, const T* x, const float* scale, const float* bias, T* y, float* mean, float* rstd, void* ws, cudaStream_t s) {
+  const Gn& p = pl.p;
+  if (pl.form == kLanes) {
+    GN_LANES(fwd_lanes, pl, x, scale, bias, y, mean, rstd, s)
+  } else if (pl.form == kSample) {
+    const size_t smem = (gn_part_floats(p) + 2 * p.groups) * sizeof(float);
+    if (cudaFuncSetAttribute(gn_fwd_sample_kernel<T, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SS_ERR_CUDA;
+    gn_fwd_sample_kernel<T, SILU><<<pl.grid, kGnThreads, smem, s>>>(p, x, scale, bias, y, mean, rstd);
+  } else {
+    const Part& q = pl.q;
+    float* part = static_cast<float*>(ws);
+    float* st = part + (size_t)p.N * q.splits * 2 * p.C;
+    float* mu = mean != nullptr ? mean : st;
+    float* rv = rstd != nullptr ? rstd : st + (size_t)p.N * p.groups;
+    const unsigned grid = (unsigned)((long long)p.N * q.splits * q.tiles);
+    gn_stats_kernel<T><<<grid, kGnThreads, 0, s>>>(p, q, x, part);
+    if (launch_dependent(gn_join_kernel, dim3((unsigned)((long long)p.N * p.groups)), dim3(kGnThreads), 0, s, p, q, (const float*)part, mu, rv) !=
+            cudaSuccess ||
+        launch_dependent(gn_apply_kernel<T, SILU>, dim3(grid), dim3(kGnThreads), 0, s, p, q, x, scale, bias, (const float*)mu, (const float*)rv, y) !=
+            cudaSuccess)
+      return SS_ERR_CUDA;
+  }
+  return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+struct StoreColumns {  // [dscale | dbias]
+  float *ds, *db;
+  int C, add;
+  __device__ __forceinline__ void put(long long i, float v) const {
+    float* at = i < C ? ds + i : db + (i - C);
+    *at = (add & (i < C ? 1 : 2)) ? *at + v : v;
+  }
+};
+
+template <typename T, bool SILU>
+int bwd(const GnPlan& pl, const T* dy, const T* x, const float* scale, const float* bias, const float* mean, const float* rstd, float* dx,
+        float* dscale, float* dbias, int accumulate, void* ws, cudaStream_t s) {
+  const Gn& p = pl.p;
+  float* part = static_cast<float*>(ws);
+  const StoreColumns st{dscale, dbias, p.C, accumulate};
+  if (pl.form == kLanes) {
+    GN_LANES(bwd_lanes, pl, dy, x, scale, bias, mean, rstd, dx, part, s)
+  } else if (pl.form == kSample) {
+    const size_t smem = (gn_part_floats(p) + 2 * p.C + 2 * p.groups) * sizeof(float);
+    if (cudaFuncSetAttribute(gn_bwd_sample_kernel<T, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SS_ERR_CUDA;
+    gn_bwd_sample_kernel<T, SILU><<<pl.grid, kGnThreads, smem, s>>>(p, dy, x, scale, bias, mean, rstd, dx, part);
+  } else {
+    const Part& q = pl.q;
+    float2* means = reinterpret_cast<float2*>(part + (size_t)p.N * q.splits * 2 * p.C);
+    const unsigned grid = (unsigned)((long long)p.N * q.splits * q.tiles);
+    gn_bwd_sums_kernel<T, SILU><<<grid, kGnThreads, 0, s>>>(p, q, dy, x, scale, bias, mean, rstd, part);
+    if (launch_dependent(gn_bwd_join_kernel, dim3((unsigned)((long long)p.N * p.groups)), dim3(kGnThreads), 0, s, p, q, (const float*)part, scale,
+                         means) != cudaSuccess ||
+        launch_dependent(gn_bwd_apply_kernel<T, SILU>, dim3(grid), dim3(kGnThreads), 0, s, p, q, dy, x, scale, bias, mean, rstd,
+                         (const float2*)means, dx) != cudaSuccess)
+      return SS_ERR_CUDA;
+  }
+  if (cudaGetLastError() != cudaSuccess) return SS_ERR_CUDA;
+  return colsum(part, 2ll * p.C, pl.rows, st, s) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" size_t groupnorm_fwd_workspace_size(int N, int M, int C, int groups, int dtype) {
+  GnPlan pl;
+  return gn_plan(N, M, C, groups, dtype, pl) == SS_OK ? pl.fwd : 0;
+}
+
+extern "C" int groupnorm_fwd(const void* x, const float* scale, const float* bias, float eps, void* y, float* mean, float* rstd, int N, int M,
+                             int C, int groups, int silu, int dtype, void* workspace, size_t ws_bytes, void* stream) {
+  if (!x || !scale || !y) return SS_ERR_NULL;
+  GnPlan pl;
+  const int rc = gn_plan(N, M, C, groups, dtype, pl);
+  if (rc != SS_OK) return rc;
+  if (!(eps >= 0.f)) return SS_ERR_DIM;
+  const void* ptrs[] = {x, scale, bias, y};
+  for (const void* q : ptrs)
+    if (!ssh::aligned16(q)) return SS_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(mean) & 3u) || (reinterpret_cast<uintptr_t>(rstd) & 3u)) return SS_ERR_ALIGN;
+  if (pl.fwd > 0) {
+    if (workspace == nullptr || ws_bytes < pl.fwd) return SS_ERR_WORKSPACE;
+    if (!ssh::aligned16(workspace)) return SS_ERR_ALIGN;
+  }
+  pl.p.eps = eps;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto go = [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    const T* xt = static_cast<const T*>(x);
+    return silu ? fwd<T, true>(pl, xt, scale, bias, static_cast<T*>(y), mean, rstd, workspace, s)
+                : fwd<T, false>(pl, xt, scale, bias, static_cast<T*>(y), mean, rstd, workspace, s);
+  };
+  return dtype == SS_F32 ? go(static_cast<float*>(nullptr)) : go(static_cast<__nv_bfloat16*>(nullptr));
+}
+
+extern "C" size_t groupnorm_bwd_workspace_size(int N, int M, int C, int groups, int dtype) {
+  GnPlan pl;
+  return gn_plan(N, M, C, groups, dtype, pl) == SS_OK ? pl.bwd : 0;
+}
+
+extern "C" int groupnorm_bwd(const void* dy, const void* x, const float* scale, const float* bias, const float* mean, const float* rstd, float* dx,
+                             float* dscale, float* dbias, int accumulate, int N, int M, int C, int groups, int silu, int dtype, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  if (!dy || !x || !scale || !mean || !rstd || !dx || !dscale || !dbias) return SS_ERR_NULL;
+  GnPlan pl;
+  const int rc = gn_plan(N, M, C, groups, dtype, pl);
+  if (rc != SS_OK) return rc;
+  const void* ptrs[] = {dy, x, scale, bias, dx};
+  for (const void* q : ptrs)
+    if (!ssh::aligned16(q)) return SS_ERR_ALIGN;
+  const void* words[] = {mean, rstd, dscale, dbias};
+  for (const void* q : words)
+    if (reinterpret_cast<uintptr_t>(q) & 3u) return SS_ERR_ALIGN;
+  if (workspace == nullptr || ws_bytes < pl.bwd) return SS_ERR_WORKSPACE;
+  if (!ssh::aligned16(workspace)) return SS_ERR_ALIGN;
+  pl.p.eps = 0.f;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto go = [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    const T *yt = static_cast<const T*>(dy), *xt = static_cast<const T*>(x);
+    return silu ? bwd<T, true>(pl, yt, xt, scale, bias, mean, rstd, dx, dscale, dbias, accumulate, workspace, s)
+                : bwd<T, false>(pl, yt, xt, scale, bias, mean, rstd, dx, dscale, dbias, accumulate, workspace, s);
+  };
+  return dtype == SS_F32 ? go(static_cast<float*>(nullptr)) : go(static_cast<__nv_bfloat16*>(nullptr));
+}

@@ -26,6 +26,8 @@ Names and argument order follow include/ssscan.h:
 * ``deltarule_step(q, k, v, g, beta, h, scale=None)`` -> ``o`` (h updated in place)
 * ``layernorm_fwd(x, scale, bias, eps)`` -> ``(y, mean, rstd)``
 * ``layernorm_bwd(dy, x, scale, mean, rstd, dscale=None, dbias=None)`` -> ``(dx, dscale, dbias)``
+* ``groupnorm_fwd(x, scale, bias, groups, eps, silu=False)`` -> ``(y, mean, rstd)``
+* ``groupnorm_bwd(dy, x, scale, bias, mean, rstd, groups, silu=False, dscale=None, dbias=None)`` -> ``(dx, dscale, dbias)``
 
 Activations are ``torch.float32`` or ``torch.bfloat16`` CUDA tensors, contiguous;
 parameters, states and gradients are ``torch.float32``.
@@ -35,6 +37,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 
 import torch
 
@@ -680,6 +683,67 @@ def layernorm_bwd(dy, x, scale, mean, rstd, dscale=None, dbias=None, workspace=N
                               _at(dbias, "dbias", (N,), f32, dev), add, R, N, dt, pw, have, _raw_stream(dev))
     if rc:
         check(rc, "layernorm_bwd")
+    return dx, dscale, dbias
+
+
+@functools.lru_cache(maxsize=1024)
+def _groupnorm_plan(N, M, C, groups, sdt):
+    """(forward scratch, backward scratch) of a call's sizes."""
+    lib = load()
+    return lib.groupnorm_fwd_workspace_size(N, M, C, groups, sdt), lib.groupnorm_bwd_workspace_size(N, M, C, groups, sdt)
+
+
+def _groupnorm_sizes(x):
+    """(samples, positions, channels) of x [N, ..., C]."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dim() < 2:
+        raise ValueError(f"x must be [N, ..., C], got {tuple(x.shape)}")
+    return x.shape[0], math.prod(x.shape[1:-1]), x.shape[-1]
+
+
+def groupnorm_fwd(x, scale, bias, groups: int, eps: float, silu: bool = False, want_stats: bool = True, workspace=None):
+    """Group norm of x [N, ..., C] over each sample's positions and each of ``groups`` groups of neighbouring channels, with
+    SiLU on its output when ``silu``: ``(y, mean, rstd)`` with y in x's dtype and the statistics fp32 [N, groups] (None unless
+    ``want_stats``); ``bias`` may be None."""
+    N, M, C = _groupnorm_sizes(x)
+    dev, f32 = x.device, torch.float32
+    dt = _act_dtype(x)
+    px, ps = _at(x, "x", x.shape, x.dtype, dev), _at(scale, "scale", (C,), f32, dev)
+    pb = _opt_at(bias, "bias", (C,), f32, dev)
+    y = torch.empty_like(x)
+    mean = torch.empty((N, groups), device=dev, dtype=f32) if want_stats else None
+    rstd = torch.empty((N, groups), device=dev, dtype=f32) if want_stats else None
+    pw, have = _scratch(workspace, _groupnorm_plan(N, M, C, groups, dt)[0], dev)
+    rc = load().groupnorm_fwd(px, ps, pb, eps, y.data_ptr(), mean.data_ptr() if want_stats else None,
+                              rstd.data_ptr() if want_stats else None, N, M, C, groups, 1 if silu else 0, dt, pw, have,
+                              _raw_stream(dev))
+    if rc:
+        check(rc, "groupnorm_fwd")
+    return y, mean, rstd
+
+
+def groupnorm_bwd(dy, x, scale, bias, mean, rstd, groups: int, silu: bool = False, dscale=None, dbias=None, workspace=None):
+    """Group norm backward -> ``(dx, dscale, dbias)``, all fp32; dscale and dbias accumulate into the given tensors and are
+    made when None.  ``bias`` and ``silu`` as in ``groupnorm_fwd``."""
+    N, M, C = _groupnorm_sizes(x)
+    dev, f32 = x.device, torch.float32
+    dt = _act_dtype(x)
+    py, px = _at(dy, "dy", x.shape, x.dtype, dev), _at(x, "x", x.shape, x.dtype, dev)
+    ps, pb = _at(scale, "scale", (C,), f32, dev), _opt_at(bias, "bias", (C,), f32, dev)
+    pm, pr = _at(mean, "mean", (N, groups), f32, dev), _at(rstd, "rstd", (N, groups), f32, dev)
+    add = (1 if dscale is not None else 0) | (2 if dbias is not None else 0)
+    if dscale is None:
+        dscale = torch.empty((C,), device=dev, dtype=f32)
+    if dbias is None:
+        dbias = torch.empty((C,), device=dev, dtype=f32)
+    dx = torch.empty(x.shape, device=dev, dtype=f32)
+    pw, have = _scratch(workspace, _groupnorm_plan(N, M, C, groups, dt)[1], dev)
+    rc = load().groupnorm_bwd(py, px, ps, pb, pm, pr, dx.data_ptr(), _at(dscale, "dscale", (C,), f32, dev),
+                              _at(dbias, "dbias", (C,), f32, dev), add, N, M, C, groups, 1 if silu else 0, dt, pw, have,
+                              _raw_stream(dev))
+    if rc:
+        check(rc, "groupnorm_bwd")
     return dx, dscale, dbias
 
 
