@@ -471,16 +471,17 @@ int linattn_step(const void* q, const void* k, const void* v, const float* g, in
  * inside the rounding of the output itself.
  * Alignment: 16 bytes for every pointer but g, beta, lengths, dg, dbeta (4).
  *
- * deltarule_num_states — states a checkpoint holds: one entering each chunk
- * and the last one, ceil(L / 64) + 1 (0 on an invalid L).
+ * deltarule_ckpt_size — floats that a checkpoint holds for each batch row and
+ * head (0 on invalid sizes): the states entering each chunk and the last one,
+ * and in bf16 two values for every element of v, which the fp32 gradients need.
  */
-int deltarule_num_states(int L);
+size_t deltarule_ckpt_size(int L, int K, int V, int dtype);
 
 /*
  * deltarule_fwd — o [B, L, H, V] (dtype), and where the pointer is given
- *   ckpt   : [B, H, deltarule_num_states(L), K, V] fp32, from which
- *            deltarule_bwd starts (the order of the K * V values is the
- *            library's own; states past a row's last are not written)
+ *   ckpt   : [B, H, deltarule_ckpt_size(L, K, V, dtype)] fp32, from which
+ *            deltarule_bwd starts (its order is the library's own; what lies
+ *            past a row's length is not written)
  *   h_last : [B, H, K, V] fp32, the state after the row's last token
  * h0 may be NULL (zeros).  workspace: deltarule_fwd_workspace_size() bytes.
  */

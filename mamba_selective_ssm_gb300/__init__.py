@@ -9,7 +9,7 @@ calls the library on the current CUDA stream.
 
 from ._build import build
 from ._capi import SSError, load
-from .ops import (conv1d_causal_bwd, conv1d_causal_fwd, conv1d_causal_silu_bwd, conv1d_causal_step, count_nonfinite, deltarule_bwd, deltarule_fwd, deltarule_num_states,
+from .ops import (conv1d_causal_bwd, conv1d_causal_fwd, conv1d_causal_silu_bwd, conv1d_causal_step, count_nonfinite, deltarule_bwd, deltarule_ckpt_size, deltarule_fwd,
                   deltarule_step, device_status, groupnorm_bwd, groupnorm_fwd,
                   layernorm_bwd, layernorm_fwd, linattn_bwd, linattn_fwd, linattn_num_chunks, linattn_step, num_chunks, rmsnorm_bwd, rmsnorm_fwd,
                   scan_bwd_workspace_size, scan_fwd_workspace_size, ss_scan_bwd, ss_scan_bwd_summary, ss_scan_carries,
@@ -19,6 +19,6 @@ __all__ = [
     "build", "load", "SSError", "ss_scan_fwd", "ss_scan_bwd", "scan_fwd_workspace_size", "scan_bwd_workspace_size",
     "ss_scan_step", "ss_scan_fwd_summary", "ss_scan_bwd_summary", "ss_scan_carries", "conv1d_causal_step", "conv1d_causal_fwd", "conv1d_causal_bwd", "conv1d_causal_silu_bwd", "rmsnorm_fwd", "rmsnorm_bwd", "num_chunks", "count_nonfinite", "device_status",
     "linattn_fwd", "linattn_bwd", "linattn_step", "linattn_num_chunks",
-    "deltarule_fwd", "deltarule_bwd", "deltarule_step", "deltarule_num_states", "layernorm_fwd", "layernorm_bwd",
+    "deltarule_fwd", "deltarule_bwd", "deltarule_step", "deltarule_ckpt_size", "layernorm_fwd", "layernorm_bwd",
     "groupnorm_fwd", "groupnorm_bwd",
 ]

@@ -55,7 +55,7 @@ SIGNATURES = {
     "linattn_bwd_workspace_size": (_sz, [_i] * 8),
     "linattn_bwd": (_i, [_vp, _ll] * 3 + [_vp, _i] + [_vp] * 9 + [_i] * 6 + [_f, _i, _vp, _sz, _vp]),
     "linattn_step": (_i, [_vp] * 4 + [_i] + [_vp] * 2 + [_i] * 5 + [_f, _i, _vp]),
-    "deltarule_num_states": (_i, [_i]),
+    "deltarule_ckpt_size": (_sz, [_i] * 4),
     "deltarule_fwd_workspace_size": (_sz, [_i] * 7),
     "deltarule_fwd": (_i, [_vp, _ll] * 3 + [_vp] * 7 + [_i] * 6 + [_f, _i, _vp, _sz, _vp]),
     "deltarule_bwd_workspace_size": (_sz, [_i] * 7),

@@ -14,6 +14,9 @@ int read_clear_rms_err(cudaStream_t s, unsigned* out);
 int read_clear_rmsf_err(cudaStream_t s, unsigned* out);
 int read_clear_linf_err(cudaStream_t s, unsigned* out);
 int read_clear_linb_err(cudaStream_t s, unsigned* out);
+int read_clear_delf_err(cudaStream_t s, unsigned* out);
+int read_clear_delb_err(cudaStream_t s, unsigned* out);
+int read_clear_delg_err(cudaStream_t s, unsigned* out);
 
 namespace {
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
@@ -65,12 +68,14 @@ extern "C" const char* ss_strerror(int code) {
 
 extern "C" int ss_device_status(void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  unsigned a = 0, b = 0, c = 0, d = 0, e = 0, f = 0;
-  if (ssh::read_clear_fwd_err(s, &a) != SS_OK) return SS_ERR_CUDA;
-  if (ssh::read_clear_bwd_err(s, &b) != SS_OK) return SS_ERR_CUDA;
-  if (ssh::read_clear_rms_err(s, &c) != SS_OK) return SS_ERR_CUDA;
-  if (ssh::read_clear_rmsf_err(s, &d) != SS_OK) return SS_ERR_CUDA;
-  if (ssh::read_clear_linf_err(s, &e) != SS_OK) return SS_ERR_CUDA;
-  if (ssh::read_clear_linb_err(s, &f) != SS_OK) return SS_ERR_CUDA;
-  return (a | b | c | d | e | f) ? SS_ERR_DEVICE : SS_OK;
+  int (*const words[])(cudaStream_t, unsigned*) = {ssh::read_clear_fwd_err,  ssh::read_clear_bwd_err,  ssh::read_clear_rms_err,
+                                                   ssh::read_clear_rmsf_err, ssh::read_clear_linf_err, ssh::read_clear_linb_err,
+                                                   ssh::read_clear_delf_err, ssh::read_clear_delb_err, ssh::read_clear_delg_err};
+  unsigned any = 0;
+  for (auto read : words) {
+    unsigned w = 0;
+    if (read(s, &w) != SS_OK) return SS_ERR_CUDA;
+    any |= w;
+  }
+  return any ? SS_ERR_DEVICE : SS_OK;
 }

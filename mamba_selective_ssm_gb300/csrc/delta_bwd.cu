@@ -844,9 +844,10 @@ int bwd_plan(int B, int L, int H, int G, int K, int V, int dtype, BwdPlan& pl) {
   LinAttn& a = pl.p.a;
   a.B = B; a.L = L; a.H = H; a.G = G; a.K = K; a.V = V;
   a.nck = (L + kDC - 1) / kDC;
-  pl.p.pterms = 2;
+  pl.p.pterms = dtype == SS_F32 ? 2 : 3;
   const size_t items = (size_t)B * H * a.nck;
-  pl.m = pl.pp = items * kDMBytes;
+  pl.m = items * (dtype == SS_F32 ? kDMBytes : kDMTerms);
+  pl.pp = items * (kDC * kDC * 2) * pl.p.pterms;
   pl.vec = items * kDVec * sizeof(float);
   pl.ds = items * K * V * sizeof(float);
   pl.du = items * kDC * V * sizeof(float);
@@ -875,30 +876,41 @@ int chain(const BwdPlan& pl, const BwdArgs& x, cudaStream_t s) {
                     static_cast<T*>(x.dv), x.dS, x.du, x.dh0, stages, sb);
 }
 
-template <typename T, int KP, int VP>
-int grads(const BwdPlan& pl, const BwdArgs& x, cudaStream_t s) {
+// a group's dq and dk from its heads' parts
+template <typename T>
+int share(const BwdPlan& pl, const BwdArgs& x, cudaStream_t s) {
   const LinAttn& a = pl.p.a;
-  const unsigned grid = (unsigned)((long long)a.B * a.H * a.nck);
-  constexpr size_t smem = GradSmem<T, KP, VP>::bytes;
-  static_assert(smem <= 227 * 1024, "a chunk's tiles fit shared memory");
-  const T* dout = static_cast<const T*>(x.dout);
-  if (a.H == a.G)
-    return lin_launch(delta_grad_kernel<T, T, KP, VP>, grid, kGradThreads, smem, s, pl.p, x.ckpt, dout, x.dS, x.du, static_cast<T*>(x.dq),
-                      static_cast<T*>(x.dk), a.G, x.dg, x.dbeta);
-  const int rc = lin_launch(delta_grad_kernel<T, float, KP, VP>, grid, kGradThreads, smem, s, pl.p, x.ckpt, dout, x.dS, x.du, x.pq, x.pk, a.H, x.dg,
-                            x.dbeta);
-  if (rc != SS_OK) return rc;
   const long long n4 = (long long)a.B * a.L * a.G * a.K / 4;
   delta_share_kernel<T><<<dim3((unsigned)((n4 + 255) / 256), 2), 256, 0, s>>>(x.pq, x.pk, static_cast<T*>(x.dq), static_cast<T*>(x.dk), n4,
                                                                               a.H / a.G, a.K);
   return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
-template <typename T, int KP>
+template <int KP, int VP>
+int grads(const BwdPlan& pl, const BwdArgs& x, cudaStream_t s) {
+  const LinAttn& a = pl.p.a;
+  const unsigned grid = (unsigned)((long long)a.B * a.H * a.nck);
+  constexpr size_t smem = GradSmem<float, KP, VP>::bytes;
+  static_assert(smem <= 227 * 1024, "a chunk's tiles fit shared memory");
+  const bool parts = a.H > a.G;
+  const int rc = lin_launch(delta_grad_kernel<float, float, KP, VP>, grid, kGradThreads, smem, s, pl.p, x.ckpt, static_cast<const float*>(x.dout), x.dS, x.du,
+                            parts ? x.pq : static_cast<float*>(x.dq), parts ? x.pk : static_cast<float*>(x.dk), parts ? a.H : a.G, x.dg, x.dbeta);
+  return rc != SS_OK || !parts ? rc : share<float>(pl, x, s);
+}
+
+template <int KP>
 int run(const BwdPlan& pl, const BwdArgs& x, cudaStream_t s) {
-  const int rc = chain<T, KP>(pl, x, s);
+  const int rc = chain<float, KP>(pl, x, s);
   if (rc != SS_OK) return rc;
-  return pl.p.a.V <= 64 ? grads<T, KP, 64>(pl, x, s) : grads<T, KP, 128>(pl, x, s);
+  return pl.p.a.V <= 64 ? grads<KP, 64>(pl, x, s) : grads<KP, 128>(pl, x, s);
+}
+
+int run_bf16(const BwdPlan& pl, const BwdArgs& x, cudaStream_t s) {
+  int rc = ssh::delta_back_bf16(pl.p, x.dout, x.dh_last, x.dv, x.dS, x.du, x.dh0, s);
+  if (rc != SS_OK) return rc;
+  const bool parts = pl.p.a.H > pl.p.a.G;
+  rc = ssh::delta_grad_bf16(pl.p, x.ckpt, x.dout, x.dS, x.du, parts ? x.pq : x.dq, parts ? x.pk : x.dk, parts, x.dg, x.dbeta, s);
+  return rc != SS_OK || !parts ? rc : share<__nv_bfloat16>(pl, x, s);
 }
 
 }  // namespace
@@ -944,6 +956,6 @@ extern "C" int deltarule_bwd(const void* q, long long ldq, const void* k, long l
   x.pk = reinterpret_cast<float*>(w += pl.part);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if ((rc = ssh::delta_prep(pl.p, dtype, s)) != SS_OK) return rc;
-  if (dtype == SS_F32) return K <= 64 ? run<float, 64>(pl, x, s) : run<float, 128>(pl, x, s);
-  return K <= 64 ? run<__nv_bfloat16, 64>(pl, x, s) : run<__nv_bfloat16, 128>(pl, x, s);
+  if (dtype == SS_BF16) return run_bf16(pl, x, s);
+  return K <= 64 ? run<64>(pl, x, s) : run<128>(pl, x, s);
 }

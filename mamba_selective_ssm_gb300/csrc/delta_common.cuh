@@ -24,7 +24,8 @@ namespace ssk {
 
 constexpr int kDC = 64;        // tokens of a chunk
 constexpr int kDVec = 272;     // floats of a chunk's scalars: into, rest, beta', M's row scales (64 each), e^{c_last}
-constexpr int kDMBytes = kDC * kDC * 4;  // M of a chunk: two fp16 terms
+constexpr int kDMBytes = kDC * kDC * 4;  // M of a chunk: two fp16 terms,
+constexpr int kDMTerms = kDC * kDC * 6;  // or three of bf16
 
 // One call's arguments.  a: q, k, v, g (null: no decay), lengths, sizes as in linear attention.
 struct Delta {
@@ -38,6 +39,12 @@ struct Delta {
 
 template <typename T>
 constexpr int kTerms = sizeof(T) == 4 ? 2 : 1;  // fp16 terms of an activation
+
+// What the forward leaves for the backward, floats of one (batch row, head): the state entering each chunk and the last one;
+// in bf16 also r and o of every chunk in fp32 ([16][V][4]: four tokens of a column together), which dg and dbeta need.
+__host__ __device__ inline long long delta_ckpt_floats(int nck, int K, int V, bool bf16) {
+  return (long long)(nck + 1) * K * V + (bf16 ? 2ll * nck * kDC * V : 0);
+}
 
 inline int delta_validate(int B, int L, int H, int G, int K, int V, int dtype) {
   const int rc = linattn_validate(B, L, H, G, K, V, dtype);
@@ -330,4 +337,12 @@ __device__ __forceinline__ void store_tokens(float* __restrict__ dst, long long 
 namespace ssh {
 // Launches delta_prep_kernel for all chunks of a call; P in p.pterms terms.
 int delta_prep(const ssk::Delta& p, int dtype, cudaStream_t s);
+// The chunks' walk in bf16, after delta_prep with P in two terms, or three with ckpt.
+int delta_fwd_bf16(const ssk::Delta& p, const float* h0, void* o, float* ckpt, float* h_last, cudaStream_t s);
+// The backward's walk in bf16, after delta_prep with P in three terms: dv, dh0, and dS ([K / 4][V][4]) and du ([16][V][4]) of
+// every chunk.
+int delta_back_bf16(const ssk::Delta& p, const void* dout, const float* dh_last, void* dv, float* dS, float* du, float* dh0, cudaStream_t s);
+// The other gradients in bf16, chunk by chunk.  dq, dk: rows of `heads` heads, bf16 or (parts) fp32
+int delta_grad_bf16(const ssk::Delta& p, const float* ckpt, const void* dout, const float* dS, const float* du, void* dq, void* dk, bool parts,
+                    float* dg, float* dbeta, cudaStream_t s);
 }  // namespace ssh

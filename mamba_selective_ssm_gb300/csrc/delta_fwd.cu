@@ -283,9 +283,9 @@ int fwd_plan(int B, int L, int H, int G, int K, int V, int dtype, FwdPlan& pl) {
   LinAttn& a = pl.p.a;
   a.B = B; a.L = L; a.H = H; a.G = G; a.K = K; a.V = V;
   a.nck = (L + kDC - 1) / kDC;
-  pl.p.pterms = dtype == SS_F32 ? 2 : 1;
+  pl.p.pterms = dtype == SS_F32 ? 2 : 3;
   const size_t items = (size_t)B * H * a.nck;
-  pl.m = items * kDMBytes;
+  pl.m = items * (dtype == SS_F32 ? kDMBytes : kDMTerms);
   pl.pp = items * (kDC * kDC * 2) * pl.p.pterms;
   pl.bytes = pl.m + pl.pp + items * kDVec * sizeof(float);
   return SS_OK;
@@ -306,7 +306,9 @@ int walk(const FwdPlan& pl, const float* h0, void* o, float* ckpt, float* h_last
 
 }  // namespace
 
-extern "C" int deltarule_num_states(int L) { return L <= 0 || L > kLinMaxLen ? 0 : (L + kDC - 1) / kDC + 1; }
+extern "C" size_t deltarule_ckpt_size(int L, int K, int V, int dtype) {
+  return delta_validate(1, L, 1, 1, K, V, dtype) == SS_OK ? (size_t)delta_ckpt_floats((L + kDC - 1) / kDC, K, V, dtype == SS_BF16) : 0;
+}
 
 extern "C" size_t deltarule_fwd_workspace_size(int B, int L, int H, int G, int K, int V, int dtype) {
   FwdPlan pl;
@@ -340,7 +342,8 @@ extern "C" int deltarule_fwd(const void* q, long long ldq, const void* k, long l
   pl.p.P = pl.p.M + pl.m;
   pl.p.vec = reinterpret_cast<float*>(pl.p.P + pl.pp);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == SS_BF16 && ckpt == nullptr) pl.p.pterms = 2;  // (o alone)
   if ((rc = ssh::delta_prep(pl.p, dtype, s)) != SS_OK) return rc;
   if (dtype == SS_F32) return K <= 64 ? walk<float, 64>(pl, h0, o, ckpt, h_last, s) : walk<float, 128>(pl, h0, o, ckpt, h_last, s);
-  return K <= 64 ? walk<__nv_bfloat16, 64>(pl, h0, o, ckpt, h_last, s) : walk<__nv_bfloat16, 128>(pl, h0, o, ckpt, h_last, s);
+  return ssh::delta_fwd_bf16(pl.p, h0, o, ckpt, h_last, s);
 }

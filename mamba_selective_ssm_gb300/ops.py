@@ -552,16 +552,16 @@ def linattn_step(q, k, v, g, h, scale=None):
     return o
 
 
-def deltarule_num_states(L: int) -> int:
-    """States a row of L tokens has in ``ckpt`` ([B, H, that, K, V])."""
-    return load().deltarule_num_states(L)
+def deltarule_ckpt_size(L: int, K: int, V: int, dtype) -> int:
+    """Floats of ``ckpt`` [B, H, that] for rows of L tokens."""
+    return load().deltarule_ckpt_size(L, K, V, _DT[dtype])
 
 
 @functools.lru_cache(maxsize=1024)
 def _deltarule_plan(B, L, H, G, K, V, sdt):
-    """(states, forward scratch, backward scratch) of a call's sizes."""
+    """(floats of a checkpoint's row and head, forward scratch, backward scratch) of a call's sizes."""
     lib = load()
-    return (lib.deltarule_num_states(L), lib.deltarule_fwd_workspace_size(B, L, H, G, K, V, sdt),
+    return (lib.deltarule_ckpt_size(L, K, V, sdt), lib.deltarule_fwd_workspace_size(B, L, H, G, K, V, sdt),
             lib.deltarule_bwd_workspace_size(B, L, H, G, K, V, sdt))
 
 
@@ -584,9 +584,9 @@ def deltarule_fwd(q, k, v, g, beta, h0=None, scale=None, lengths=None, want_ckpt
     pg, pb = _opt_at(g, "g", (B, L, H), f32, dev), _at(beta, "beta", (B, L, H), f32, dev)
     ph = _opt_at(h0, "h0", (B, H, K, V), f32, dev)
     pn = _opt_at(lengths, "lengths", (B,), torch.int32, dev)
-    states, need, _ = _deltarule_plan(B, L, H, G, K, V, sdt)
+    marks, need, _ = _deltarule_plan(B, L, H, G, K, V, sdt)
     o = torch.empty((B, L, H, V), device=dev, dtype=dt)
-    ckpt = torch.empty((B, H, states, K, V), device=dev, dtype=f32) if want_ckpt else None
+    ckpt = torch.empty((B, H, marks), device=dev, dtype=f32) if want_ckpt else None
     h_last = torch.empty((B, H, K, V), device=dev, dtype=f32) if want_h_last else None
     pw, have = _scratch(workspace, need, dev)
     rc = load().deltarule_fwd(pq, ldq, pk, ldk, pv, ldv, pg, pb, ph, pn, o.data_ptr(), ckpt.data_ptr() if want_ckpt else None,
@@ -607,8 +607,8 @@ def deltarule_bwd(q, k, v, g, beta, ckpt, do, dh_last=None, scale=None, lengths=
     pk, ldk = _rows(k, "k", (B, L, G, K), dt, dev)
     pv, ldv = _rows(v, "v", (B, L, H, V), dt, dev)
     pg, pb = _opt_at(g, "g", (B, L, H), f32, dev), _at(beta, "beta", (B, L, H), f32, dev)
-    states, _, need = _deltarule_plan(B, L, H, G, K, V, sdt)
-    pc = _at(ckpt, "ckpt", (B, H, states, K, V), f32, dev)
+    marks, _, need = _deltarule_plan(B, L, H, G, K, V, sdt)
+    pc = _at(ckpt, "ckpt", (B, H, marks), f32, dev)
     pd = _at(do, "do", (B, L, H, V), dt, dev)
     pl = _opt_at(dh_last, "dh_last", (B, H, K, V), f32, dev)
     pn = _opt_at(lengths, "lengths", (B,), torch.int32, dev)
