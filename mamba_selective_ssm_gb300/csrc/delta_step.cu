@@ -2,7 +2,7 @@
 //   h <- e^{g} h,   r = v - h^T k,   h <- h + beta k r^T,   o = scale * h^T q        per (batch row, head), h in place
 //
 // All the time goes to reading and writing h ([K, V] fp32), once each: a CTA takes `cw` columns of one head and holds them in
-// registers (a thread owns four neighbouring columns of every RP-th row, at most 16 rows).  Both products over K are taken of
+// registers (a thread owns four neighbouring columns of every RP-th row, at most ROWS of them).  Both products over K are taken of
 // the decayed state at once, since o = scale * (h^T q + (k.q) beta r); each thread leaves its rows' sums in shared memory,
 // and they are added in order.
 #include "linattn_common.cuh"
@@ -11,21 +11,21 @@ namespace {
 
 using namespace ssk;
 
-constexpr int kStepThreads = 256;
 
-template <typename T, int ROWS>
-__global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+
+template <typename T, int ROWS, int NT>
+__global__ void __launch_bounds__(NT, ROWS > 8 ? 2 : 4) delta_step_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                                                                   const float* __restrict__ g, const float* __restrict__ beta,
                                                                   float* __restrict__ st, T* __restrict__ o, int H, int G, int K, int V, int cw,
                                                                   float scale) {
   __shared__ float2 kq[kLinMaxHead];
-  __shared__ float4 red[2][kStepThreads];
+  __shared__ float4 red[2][NT];
   __shared__ float dots[4];
   const int tid = threadIdx.x;
   const long long bh = blockIdx.x, b = bh / H;
   const int h = (int)(bh % H), gh = h / (H / G);
   const int c0 = (int)blockIdx.y * cw, n4 = (V - c0 < cw ? V - c0 : cw) / 4;  // this CTA's groups of four columns
-  const int RP = kStepThreads / n4, c = c0 + tid % n4 * 4, r0 = tid / n4;
+  const int RP = NT / n4, c = c0 + tid % n4 * 4, r0 = tid / n4;
   const bool on = r0 < RP;
   float4* at = reinterpret_cast<float4*>(st + (bh * K + r0) * V + c);
   const long long step = (long long)RP * V / 4;
@@ -85,11 +85,11 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const T* __res
   }
 }
 
-template <typename T, int ROWS>
+template <typename T, int ROWS, int NT>
 int launch(const void* q, const void* k, const void* v, const float* g, const float* beta, float* h, void* o, int B, int H, int G, int K, int V,
            int cw, float scale, cudaStream_t s) {
   const dim3 grid((unsigned)(B * H), (unsigned)((V + cw - 1) / cw));
-  delta_step_kernel<T, ROWS><<<grid, kStepThreads, 0, s>>>(static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), g, beta, h,
+  delta_step_kernel<T, ROWS, NT><<<grid, NT, 0, s>>>(static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), g, beta, h,
                                                            static_cast<T*>(o), H, G, K, V, cw, scale);
   return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
@@ -110,8 +110,8 @@ extern "C" int deltarule_step(const void* q, const void* k, const void* v, const
   const bool whole = (long long)B * H >= 152 && V > 32;
   const int cw = whole ? V : 32;
   if (dtype == SS_F32)
-    return whole ? launch<float, 16>(q, k, v, g, beta, h, o, B, H, G, K, V, cw, scale, s)
-                 : launch<float, 4>(q, k, v, g, beta, h, o, B, H, G, K, V, cw, scale, s);
-  return whole ? launch<__nv_bfloat16, 16>(q, k, v, g, beta, h, o, B, H, G, K, V, cw, scale, s)
-               : launch<__nv_bfloat16, 4>(q, k, v, g, beta, h, o, B, H, G, K, V, cw, scale, s);
+    return whole ? launch<float, 16, 256>(q, k, v, g, beta, h, o, B, H, G, K, V, cw, scale, s)
+                 : launch<float, 4, 256>(q, k, v, g, beta, h, o, B, H, G, K, V, cw, scale, s);
+  return whole ? launch<__nv_bfloat16, 16, 256>(q, k, v, g, beta, h, o, B, H, G, K, V, cw, scale, s)
+               : launch<__nv_bfloat16, 4, 256>(q, k, v, g, beta, h, o, B, H, G, K, V, cw, scale, s);
 }

@@ -24,6 +24,7 @@ using namespace ssk;
 
 constexpr int kGnMaxDim = 32768;
 constexpr int kGnThreads = 256;
+constexpr int kGnMost = 2147483647 - (1 << 22);  // samples or positions: a thread's next ones are still an int
 constexpr int kGnSampleDim = 8192;  // widest sample of the one-CTA form
 
 template <int G>
@@ -37,6 +38,44 @@ __device__ __forceinline__ void ld8f(const float* p, bool ok, float* o) {
   const float4 b = ok ? __ldg(reinterpret_cast<const float4*>(p + 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
   o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w; o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
 }
+// pairs of channels: packed arithmetic halves the instructions, which is what short rows are bound by
+__device__ __forceinline__ void ld8p(const float* p, bool ok, float2 (&o)[4]) {
+  float x[8];
+  ld8f(p, ok, x);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = f2(x[2 * e], x[2 * e + 1]);
+}
+template <typename T>
+__device__ __forceinline__ void wide4(const typename Raw8<T>::V& v, float2 (&o)[4]) {
+  float x[8];
+  Raw8<T>::wide(v, x);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = f2(x[2 * e], x[2 * e + 1]);
+}
+template <typename T>
+__device__ __forceinline__ void st4p(T* p, const float2 (&o)[4]) {
+  const float x[8] = {o[0].x, o[0].y, o[1].x, o[1].y, o[2].x, o[2].y, o[3].x, o[3].y};
+  ActT<T>::st8(p, x);
+}
+__device__ __forceinline__ float2 sigmoid2(float2 t) {
+  const float2 e = ex2_2(mul2(t, bc2(-kLog2e))), d = add2(e, bc2(1.f));
+  return f2(rcp(d.x), rcp(d.y));
+}
+template <bool SILU>
+__device__ __forceinline__ float2 act2(float2 t) {
+  return SILU ? mul2(t, sigmoid2(t)) : t;
+}
+template <bool SILU>
+__device__ __forceinline__ float2 dact2(float2 dy, float2 t) {
+  if (!SILU) return dy;
+  const float2 p = sigmoid2(t);
+  return mul2(mul2(dy, p), fma2(t, fma2(p, bc2(-1.f), bc2(1.f)), bc2(1.f)));
+}
+__device__ __forceinline__ float sum4p(const float2 (&x)[4]) {
+  const float2 s = add2(add2(x[0], x[1]), add2(x[2], x[3]));
+  return s.x + s.y;
+}
+
 template <bool SILU>
 __device__ __forceinline__ float act(float t) {
   return SILU ? t * sigmoid(t) : t;
@@ -64,49 +103,44 @@ __global__ void __launch_bounds__(kGnThreads) gn_fwd_lanes_kernel(Gn p, int gp, 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / G, rs = 32 / G / gp;  // rs rows of gp groups a warp
   const int g = (int)blockIdx.y * gp + slot % gp, i = (lane % G) * 8, c = g * p.cg + i;
   const bool cv = g < p.groups && i < p.cg;
-  float sc[8], bi[8];
-  ld8f(scale + c, cv, sc);
-  ld8f(bias + c, cv && bias != nullptr, bi);
+  float2 sc[4], bi[4];
+  ld8p(scale + c, cv, sc);
+  ld8p(bias + c, cv && bias != nullptr, bi);
   const float inv = 1.0f / (float)p.cg;
-  const long long step = (long long)gridDim.x * 8 * rs * U;
-  for (long long r0 = ((long long)blockIdx.x * 8 + warp) * rs * U; r0 < p.N; r0 += step) {
+  const int step = (int)gridDim.x * 8 * rs * U;
+  for (int r0 = ((int)blockIdx.x * 8 + warp) * rs * U + slot / gp; r0 < p.N; r0 += step) {  // this lane's rows: r0 + u rs
+    const T* src = x + (long long)r0 * p.C + c;
     typename R::V raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const long long r = r0 + u * rs + slot / gp;
-      raw[u] = cv && r < p.N ? R::ld(x + r * p.C + c) : R::zero();
-    }
+    for (int u = 0; u < U; ++u) raw[u] = cv && u * rs < p.N - r0 ? R::ld(src + (long long)(u * rs) * p.C) : R::zero();
+    T* dst = y + (long long)r0 * p.C + c;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const long long r = r0 + u * rs + slot / gp;
-      float v[8], s = 0.f;
-      R::wide(raw[u], v);
+      float2 v[4], q[4];
+      wide4<T>(raw[u], v);
+      const float m = lanes_sum<G>(sum4p(v)) * inv;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += v[e];
-      const float m = lanes_sum<G>(s) * inv;
-      s = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[e] -= m;
-        s = fmaf(v[e], v[e], s);
+      for (int e = 0; e < 4; ++e) {
+        v[e] = add2(v[e], bc2(-m));
+        q[e] = mul2(v[e], v[e]);
       }
-      if (!cv) s = 0.f;
-      const float rv = rsqrtf(fmaf(lanes_sum<G>(s), inv, p.eps));
-      if (cv && r < p.N) {
+      const float rv = rsqrtf(fmaf(lanes_sum<G>(cv ? sum4p(q) : 0.f), inv, p.eps));
+      if (cv && u * rs < p.N - r0) {
         if (i == 0) {
-          if (mean != nullptr) mean[r * p.groups + g] = m;
-          if (rstd != nullptr) rstd[r * p.groups + g] = rv;
+          const long long at = (long long)(r0 + u * rs) * p.groups + g;
+          if (mean != nullptr) mean[at] = m;
+          if (rstd != nullptr) rstd[at] = rv;
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = act<SILU>(fmaf(v[e] * rv, sc[e], bi[e]));
-        ActT<T>::st8(y + r * p.C + c, v);
+        for (int e = 0; e < 4; ++e) v[e] = act2<SILU>(fma2(mul2(v[e], bc2(rv)), sc[e], bi[e]));
+        st4p<T>(dst + (long long)(u * rs) * p.C, v);
       }
     }
   }
 }
 
 template <typename T, int G, int U, bool SILU>
-__global__ void __launch_bounds__(kGnThreads) gn_bwd_lanes_kernel(Gn p, int gp, const T* __restrict__ dy, const T* __restrict__ x,
+__global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_lanes_kernel(Gn p, int gp, const T* __restrict__ dy, const T* __restrict__ x,
                                                                   const float* __restrict__ scale, const float* __restrict__ bias,
                                                                   const float* __restrict__ mean, const float* __restrict__ rstd,
                                                                   float* __restrict__ dx, float* __restrict__ part) {
@@ -116,54 +150,53 @@ __global__ void __launch_bounds__(kGnThreads) gn_bwd_lanes_kernel(Gn p, int gp, 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / G, rs = 32 / G / gp;
   const int g = (int)blockIdx.y * gp + slot % gp, i = (lane % G) * 8, c = g * p.cg + i;
   const bool cv = g < p.groups && i < p.cg;
-  float sc[8], bi[8], as[8], ab[8];
-  ld8f(scale + c, cv, sc);
-  ld8f(bias + c, cv && SILU && bias != nullptr, bi);
+  float2 sc[4], bi[4], as[4], ab[4];
+  ld8p(scale + c, cv, sc);
+  ld8p(bias + c, cv && SILU && bias != nullptr, bi);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) as[e] = ab[e] = 0.f;
+  for (int e = 0; e < 4; ++e) as[e] = ab[e] = f2(0.f, 0.f);
   const float inv = 1.0f / (float)p.cg;
-  const long long step = (long long)gridDim.x * 8 * rs * U;
-  for (long long r0 = ((long long)blockIdx.x * 8 + warp) * rs * U; r0 < p.N; r0 += step) {
+  const int step = (int)gridDim.x * 8 * rs * U;
+  for (int r0 = ((int)blockIdx.x * 8 + warp) * rs * U + slot / gp; r0 < p.N; r0 += step) {
+    const long long first = (long long)r0 * p.C + c;
     typename R::V rx[U], ry[U];
     float mu[U], rv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const long long r = r0 + u * rs + slot / gp;
-      const bool on = cv && r < p.N;
-      rx[u] = on ? R::ld(x + r * p.C + c) : R::zero();
-      ry[u] = on ? R::ld(dy + r * p.C + c) : R::zero();
-      mu[u] = on ? mean[r * p.groups + g] : 0.f;
-      rv[u] = on ? rstd[r * p.groups + g] : 0.f;
+      const bool on = cv && u * rs < p.N - r0;
+      const long long at = (long long)(r0 + u * rs) * p.groups + g;
+      rx[u] = on ? R::ld(x + first + (long long)(u * rs) * p.C) : R::zero();
+      ry[u] = on ? R::ld(dy + first + (long long)(u * rs) * p.C) : R::zero();
+      mu[u] = on ? mean[at] : 0.f;
+      rv[u] = on ? rstd[at] : 0.f;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const long long r = r0 + u * rs + slot / gp;
-      float xh[8], w[8], s1 = 0.f, s2 = 0.f;
-      R::wide(rx[u], xh);
-      R::wide(ry[u], w);
+      float2 xh[4], w[4], q[4];
+      wide4<T>(rx[u], xh);
+      wide4<T>(ry[u], w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        xh[e] = (xh[e] - mu[u]) * rv[u];
-        const float da = dact<SILU>(w[e], fmaf(xh[e], sc[e], bi[e]));
-        as[e] = fmaf(da, xh[e], as[e]);
-        ab[e] += da;
-        w[e] = da * sc[e];
-        s1 += w[e];
-        s2 = fmaf(w[e], xh[e], s2);
+      for (int e = 0; e < 4; ++e) {
+        xh[e] = mul2(add2(xh[e], bc2(-mu[u])), bc2(rv[u]));
+        const float2 da = dact2<SILU>(w[e], fma2(xh[e], sc[e], bi[e]));
+        as[e] = fma2(da, xh[e], as[e]);
+        ab[e] = add2(ab[e], da);
+        w[e] = mul2(da, sc[e]);
+        q[e] = mul2(w[e], xh[e]);
       }
-      s1 = lanes_sum<G>(s1) * inv;
-      s2 = lanes_sum<G>(s2) * inv;
-      if (cv && r < p.N) {
+      const float s1 = lanes_sum<G>(sum4p(w)) * inv, s2 = lanes_sum<G>(sum4p(q)) * inv;
+      if (cv && u * rs < p.N - r0) {
+        const float2 k0 = bc2(-s1 * rv[u]), k1 = bc2(-s2 * rv[u]), k2 = bc2(rv[u]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = rv[u] * (w[e] - s1 - xh[e] * s2);
-        ActT<float>::st8(dx + r * p.C + c, w);
+        for (int e = 0; e < 4; ++e) w[e] = fma2(k2, w[e], fma2(xh[e], k1, k0));
+        st4p<float>(dx + first + (long long)(u * rs) * p.C, w);
       }
     }
   }
-  red[0][threadIdx.x] = make_float4(as[0], as[1], as[2], as[3]);
-  red[1][threadIdx.x] = make_float4(as[4], as[5], as[6], as[7]);
-  red[2][threadIdx.x] = make_float4(ab[0], ab[1], ab[2], ab[3]);
-  red[3][threadIdx.x] = make_float4(ab[4], ab[5], ab[6], ab[7]);
+  red[0][threadIdx.x] = make_float4(as[0].x, as[0].y, as[1].x, as[1].y);
+  red[1][threadIdx.x] = make_float4(as[2].x, as[2].y, as[3].x, as[3].y);
+  red[2][threadIdx.x] = make_float4(ab[0].x, ab[0].y, ab[1].x, ab[1].y);
+  red[3][threadIdx.x] = make_float4(ab[2].x, ab[2].y, ab[3].x, ab[3].y);
   __syncthreads();
   // the block's rows in order: a thread adds one of the four parts of a lane of a group
   const int w = threadIdx.x >> 6, l = threadIdx.x & 63;  // (gp * G <= 32 lanes hold different channels)
@@ -416,50 +449,55 @@ struct Where {
   }
 };
 // the row lanes' sums, added in order: red[thread][8] -> the first lane
-__device__ __forceinline__ void lanes_add(float4 (*red)[kGnThreads], int ut, int lanes, float (&s)[8]) {
+__device__ __forceinline__ void lanes_add(float4 (*red)[kGnThreads], int ut, int lanes, float2 (&s)[4]) {
   __syncthreads();
-  red[0][threadIdx.x] = make_float4(s[0], s[1], s[2], s[3]);
-  red[1][threadIdx.x] = make_float4(s[4], s[5], s[6], s[7]);
+  red[0][threadIdx.x] = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
+  red[1][threadIdx.x] = make_float4(s[2].x, s[2].y, s[3].x, s[3].y);
   __syncthreads();
   if ((int)threadIdx.x < ut)
     for (int l = 1; l < lanes; ++l) {
       const float4 a = red[0][l * ut + threadIdx.x], b = red[1][l * ut + threadIdx.x];
-      s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w; s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
+      s[0] = add2(s[0], f2(a.x, a.y));
+      s[1] = add2(s[1], f2(a.z, a.w));
+      s[2] = add2(s[2], f2(b.x, b.y));
+      s[3] = add2(s[3], f2(b.z, b.w));
     }
 }
-constexpr int kGnAhead = 4;  // rows of a thread in flight
+template <typename T>
+constexpr int kGnAhead = 16 / sizeof(T);  // rows of a thread in flight: 128 bytes
 
 // part[n][split][c] = the rows' sum, and after all of those the sum of squares around their mean.  The sum is taken of the
 // values themselves (a mean near zero would keep the rounding of whatever it is taken around), the squares around the first
 // row's value.
 template <typename T>
-__global__ void __launch_bounds__(kGnThreads) gn_stats_kernel(Gn p, Part q, const T* __restrict__ x, float* __restrict__ part) {
+__global__ void __launch_bounds__(kGnThreads, 2) gn_stats_kernel(Gn p, Part q, const T* __restrict__ x, float* __restrict__ part) {
   using R = Raw8<T>;
   __shared__ float4 red[2][kGnThreads];
   pdl_trigger();
   const Where w(p, q);
-  float base[8], s0[8], s1[8], s2[8];
+  float2 base[4], s0[4], s1[4], s2[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) base[e] = s0[e] = s1[e] = s2[e] = 0.f;
+  for (int e = 0; e < 4; ++e) base[e] = s0[e] = s1[e] = s2[e] = f2(0.f, 0.f);
   const T* src = x + w.n * p.M * p.C + w.c;
+  constexpr int A = kGnAhead<T>;
   if (w.on) {
-    R::wide(R::ld(src + (long long)w.m0 * p.C), base);
-    for (int m = w.m0 + w.rl; m < w.m1; m += kGnAhead * w.lanes) {
-      typename R::V raw[kGnAhead];
+    wide4<T>(R::ld(src + (long long)w.m0 * p.C), base);
+    for (int m = w.m0 + w.rl; m < w.m1; m += A * w.lanes) {
+      typename R::V raw[A];
 #pragma unroll
-      for (int u = 0; u < kGnAhead; ++u)
+      for (int u = 0; u < A; ++u)
         if (m + u * w.lanes < w.m1) raw[u] = R::ld(src + (long long)(m + u * w.lanes) * p.C);
 #pragma unroll
-      for (int u = 0; u < kGnAhead; ++u) {
+      for (int u = 0; u < A; ++u) {
         if (m + u * w.lanes >= w.m1) break;
-        float v[8];
-        R::wide(raw[u], v);
+        float2 v[4];
+        wide4<T>(raw[u], v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s0[e] += v[e];
-          v[e] -= base[e];
-          s1[e] += v[e];
-          s2[e] = fmaf(v[e], v[e], s2[e]);
+        for (int e = 0; e < 4; ++e) {
+          s0[e] = add2(s0[e], v[e]);
+          v[e] = fma2(base[e], bc2(-1.f), v[e]);
+          s1[e] = add2(s1[e], v[e]);
+          s2[e] = fma2(v[e], v[e], s2[e]);
         }
       }
     }
@@ -468,13 +506,15 @@ __global__ void __launch_bounds__(kGnThreads) gn_stats_kernel(Gn p, Part q, cons
   lanes_add(red, q.ut, w.lanes, s1);
   lanes_add(red, q.ut, w.lanes, s2);
   if (w.on && w.rl == 0) {
-    const float cnt = (float)(w.m1 - w.m0);
+    const float inv = 1.f / (float)(w.m1 - w.m0);
     float* at = part + (w.n * q.splits + w.split) * p.C + w.c;
-    float sq[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sq[e] = fmaxf(fmaf(-s1[e], s1[e] / cnt, s2[e]), 0.f);
-    ActT<float>::st8(at, s0);
-    ActT<float>::st8(at + (long long)p.N * q.splits * p.C, sq);
+    for (int e = 0; e < 4; ++e) {
+      const float2 d = fma2(mul2(s1[e], bc2(-inv)), s1[e], s2[e]);
+      s2[e] = f2(fmaxf(d.x, 0.f), fmaxf(d.y, 0.f));
+    }
+    st4p<float>(at, s0);
+    st4p<float>(at + (long long)p.N * q.splits * p.C, s2);
   }
 }
 
@@ -489,27 +529,37 @@ __device__ __forceinline__ float block_sum(float* red, float v) {
   return s;
 }
 
+// f(channel of the group, part) over all of them, by the threads of a CTA
+template <typename F>
+__device__ __forceinline__ void each_part(const Gn& p, const Part& q, F f) {
+  const int w = p.cg < kGnThreads ? p.cg : kGnThreads, l = kGnThreads / w, r = (int)threadIdx.x / w;
+  if (r < l)
+    for (int c = (int)threadIdx.x % w; c < p.cg; c += w)
+#pragma unroll 4
+      for (int s = r; s < q.splits; s += l) f(c, s);
+}
+
 // a CTA joins the parts of one (sample, group)
 __global__ void __launch_bounds__(kGnThreads) gn_join_kernel(Gn p, Part q, const float* __restrict__ part, float* __restrict__ mean,
                                                              float* __restrict__ rstd) {
   __shared__ float red[kGnThreads / 32];
   pdl_trigger();
   const long long n = blockIdx.x / p.groups;
-  const int g = blockIdx.x % p.groups, cnt = q.splits * p.cg;
+  const int g = blockIdx.x % p.groups;
   const float inv = 1.0f / ((float)p.M * (float)p.cg);
   const float* sum = part + n * q.splits * p.C + g * p.cg;
   const float* sq = sum + (long long)p.N * q.splits * p.C;
-  auto rows = [&](int i) { return (float)(min(p.M, (i / p.cg + 1) * q.per) - i / p.cg * q.per); };
-  auto at = [&](int i) { return (long long)(i / p.cg) * p.C + i % p.cg; };
+  const float full = (float)q.per, last = (float)(p.M - (q.splits - 1) * q.per), fi = 1.f / full, li = 1.f / last;
   pdl_wait();
   float s = 0.f;
-  for (int i = threadIdx.x; i < cnt; i += kGnThreads) s += sum[at(i)];
+  each_part(p, q, [&](int c, int i) { s += sum[(long long)i * p.C + c]; });
   const float m = block_sum(red, s) * inv;
   s = 0.f;
-  for (int i = threadIdx.x; i < cnt; i += kGnThreads) {
-    const float d = sum[at(i)] / rows(i) - m;
-    s += fmaf(d * d, rows(i), sq[at(i)]);
-  }
+  each_part(p, q, [&](int c, int i) {
+    const bool end = i == q.splits - 1;
+    const float d = fmaf(sum[(long long)i * p.C + c], end ? li : fi, -m);
+    s += fmaf(d * d, end ? last : full, sq[(long long)i * p.C + c]);
+  });
   s = block_sum(red, s);
   if (threadIdx.x == 0) {
     mean[blockIdx.x] = m;
@@ -518,43 +568,44 @@ __global__ void __launch_bounds__(kGnThreads) gn_join_kernel(Gn p, Part q, const
 }
 
 template <typename T, bool SILU>
-__global__ void __launch_bounds__(kGnThreads) gn_apply_kernel(Gn p, Part q, const T* __restrict__ x, const float* __restrict__ scale,
+__global__ void __launch_bounds__(kGnThreads, 2) gn_apply_kernel(Gn p, Part q, const T* __restrict__ x, const float* __restrict__ scale,
                                                               const float* __restrict__ bias, const float* __restrict__ mean,
                                                               const float* __restrict__ rstd, T* __restrict__ y) {
   using R = Raw8<T>;
   const Where w(p, q);
   if (!w.on) return;
-  float sc[8], bi[8], mu[8];
-  ld8f(scale + w.c, true, sc);
-  ld8f(bias + w.c, bias != nullptr, bi);
+  float2 sc[4], bi[4], mu[4];
+  ld8p(scale + w.c, true, sc);
+  ld8p(bias + w.c, bias != nullptr, bi);
   pdl_wait();
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const long long g = w.n * p.groups + (w.c + e) / p.cg;
-    mu[e] = mean[g];
-    sc[e] *= rstd[g];
+  for (int e = 0; e < 4; ++e) {
+    const long long g = w.n * p.groups + (w.c + 2 * e) / p.cg, h = w.n * p.groups + (w.c + 2 * e + 1) / p.cg;
+    mu[e] = f2(-mean[g], -mean[h]);
+    sc[e] = mul2(sc[e], f2(rstd[g], rstd[h]));
   }
   const long long base = w.n * p.M * p.C + w.c;
-  for (int m = w.m1 - 1 - w.rl; m >= w.m0; m -= kGnAhead * w.lanes) {
-    typename R::V raw[kGnAhead];
+  constexpr int A = kGnAhead<T> / 2;
+  for (int m = w.m1 - 1 - w.rl; m >= w.m0; m -= A * w.lanes) {
+    typename R::V raw[A];
 #pragma unroll
-    for (int u = 0; u < kGnAhead; ++u)
+    for (int u = 0; u < A; ++u)
       if (m - u * w.lanes >= w.m0) raw[u] = R::ld(x + base + (long long)(m - u * w.lanes) * p.C);
 #pragma unroll
-    for (int u = 0; u < kGnAhead; ++u) {
+    for (int u = 0; u < A; ++u) {
       if (m - u * w.lanes < w.m0) break;
-      float v[8];
-      R::wide(raw[u], v);
+      float2 v[4];
+      wide4<T>(raw[u], v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = act<SILU>(fmaf(v[e] - mu[e], sc[e], bi[e]));
-      ActT<T>::st8(y + base + (long long)(m - u * w.lanes) * p.C, v);
+      for (int e = 0; e < 4; ++e) v[e] = act2<SILU>(fma2(add2(v[e], mu[e]), sc[e], bi[e]));
+      st4p<T>(y + base + (long long)(m - u * w.lanes) * p.C, v);
     }
   }
 }
 
 // part[n][split][2 C]: the rows' sums of da xh and of da
 template <typename T, bool SILU>
-__global__ void __launch_bounds__(kGnThreads) gn_bwd_sums_kernel(Gn p, Part q, const T* __restrict__ dy, const T* __restrict__ x,
+__global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_sums_kernel(Gn p, Part q, const T* __restrict__ dy, const T* __restrict__ x,
                                                                  const float* __restrict__ scale, const float* __restrict__ bias,
                                                                  const float* __restrict__ mean, const float* __restrict__ rstd,
                                                                  float* __restrict__ part) {
@@ -562,41 +613,42 @@ __global__ void __launch_bounds__(kGnThreads) gn_bwd_sums_kernel(Gn p, Part q, c
   __shared__ float4 red[2][kGnThreads];
   pdl_trigger();
   const Where w(p, q);
-  float s1[8], s2[8];
+  float2 s1[4], s2[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) s1[e] = s2[e] = 0.f;
+  for (int e = 0; e < 4; ++e) s1[e] = s2[e] = f2(0.f, 0.f);
   if (w.on) {
-    float sc[8], bi[8], mu[8], rv[8];
-    ld8f(scale + w.c, true, sc);
-    ld8f(bias + w.c, SILU && bias != nullptr, bi);
+    float2 sc[4], bi[4], mu[4], rv[4];
+    ld8p(scale + w.c, true, sc);
+    ld8p(bias + w.c, SILU && bias != nullptr, bi);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const long long g = w.n * p.groups + (w.c + e) / p.cg;
-      mu[e] = mean[g];
-      rv[e] = rstd[g];
+    for (int e = 0; e < 4; ++e) {
+      const long long g = w.n * p.groups + (w.c + 2 * e) / p.cg, h = w.n * p.groups + (w.c + 2 * e + 1) / p.cg;
+      mu[e] = f2(-mean[g], -mean[h]);
+      rv[e] = f2(rstd[g], rstd[h]);
     }
     const long long base = w.n * p.M * p.C + w.c;
-    for (int m = w.m0 + w.rl; m < w.m1; m += kGnAhead * w.lanes) {
-      typename R::V rx[kGnAhead], ry[kGnAhead];
+    constexpr int A = kGnAhead<T> / 2;
+    for (int m = w.m0 + w.rl; m < w.m1; m += A * w.lanes) {
+      typename R::V rx[A], ry[A];
 #pragma unroll
-      for (int u = 0; u < kGnAhead; ++u)
+      for (int u = 0; u < A; ++u)
         if (m + u * w.lanes < w.m1) {
           const long long at = base + (long long)(m + u * w.lanes) * p.C;
           rx[u] = R::ld(x + at);
           ry[u] = R::ld(dy + at);
         }
 #pragma unroll
-      for (int u = 0; u < kGnAhead; ++u) {
+      for (int u = 0; u < A; ++u) {
         if (m + u * w.lanes >= w.m1) break;
-        float xh[8], da[8];
-        R::wide(rx[u], xh);
-        R::wide(ry[u], da);
+        float2 xh[4], da[4];
+        wide4<T>(rx[u], xh);
+        wide4<T>(ry[u], da);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          xh[e] = (xh[e] - mu[e]) * rv[e];
-          da[e] = dact<SILU>(da[e], fmaf(xh[e], sc[e], bi[e]));
-          s1[e] += da[e];
-          s2[e] = fmaf(da[e], xh[e], s2[e]);
+        for (int e = 0; e < 4; ++e) {
+          xh[e] = mul2(add2(xh[e], mu[e]), rv[e]);
+          da[e] = dact2<SILU>(da[e], fma2(xh[e], sc[e], bi[e]));
+          s1[e] = add2(s1[e], da[e]);
+          s2[e] = fma2(da[e], xh[e], s2[e]);
         }
       }
     }
@@ -605,8 +657,8 @@ __global__ void __launch_bounds__(kGnThreads) gn_bwd_sums_kernel(Gn p, Part q, c
   lanes_add(red, q.ut, w.lanes, s2);
   if (w.on && w.rl == 0) {
     float* at = part + (w.n * q.splits + w.split) * 2 * p.C + w.c;
-    ActT<float>::st8(at, s2);
-    ActT<float>::st8(at + p.C, s1);
+    st4p<float>(at, s2);
+    st4p<float>(at + p.C, s1);
   }
 }
 
@@ -616,43 +668,44 @@ __global__ void __launch_bounds__(kGnThreads) gn_bwd_join_kernel(Gn p, Part q, c
   __shared__ float red[kGnThreads / 32];
   pdl_trigger();
   const long long n = blockIdx.x / p.groups;
-  const int g = blockIdx.x % p.groups, cnt = q.splits * p.cg;
+  const int g = blockIdx.x % p.groups;
   const float inv = 1.0f / ((float)p.M * (float)p.cg);
   const float* at = part + n * q.splits * 2 * p.C + g * p.cg;
   pdl_wait();
   float a = 0.f, b = 0.f;
-  for (int i = threadIdx.x; i < cnt; i += kGnThreads) {
-    const float s = scale[g * p.cg + i % p.cg];
-    const float* y = at + (long long)(i / p.cg) * 2 * p.C + i % p.cg;
+  each_part(p, q, [&](int c, int i) {
+    const float s = scale[g * p.cg + c];
+    const float* y = at + (long long)i * 2 * p.C + c;
     b = fmaf(y[0], s, b);
     a = fmaf(y[p.C], s, a);
-  }
+  });
   a = block_sum(red, a);
   b = block_sum(red, b);
   if (threadIdx.x == 0) means[blockIdx.x] = make_float2(a * inv, b * inv);
 }
 
 template <typename T, bool SILU>
-__global__ void __launch_bounds__(kGnThreads) gn_bwd_apply_kernel(Gn p, Part q, const T* __restrict__ dy, const T* __restrict__ x,
+__global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_apply_kernel(Gn p, Part q, const T* __restrict__ dy, const T* __restrict__ x,
                                                                   const float* __restrict__ scale, const float* __restrict__ bias,
                                                                   const float* __restrict__ mean, const float* __restrict__ rstd,
                                                                   const float2* __restrict__ means, float* __restrict__ dx) {
   using R = Raw8<T>;
   const Where w(p, q);
   if (!w.on) return;
-  float sc[8], bi[8], mu[8], rv[8];
-  float2 av[8];
-  ld8f(scale + w.c, true, sc);
-  ld8f(bias + w.c, SILU && bias != nullptr, bi);
+  float2 sc[4], bi[4], mu[4], rv[4], k0[4], k1[4];
+  ld8p(scale + w.c, true, sc);
+  ld8p(bias + w.c, SILU && bias != nullptr, bi);
   pdl_wait();
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const long long g = w.n * p.groups + (w.c + e) / p.cg;
-    mu[e] = mean[g];
-    rv[e] = rstd[g];
-    av[e] = means[g];
+  for (int e = 0; e < 4; ++e) {
+    const long long g = w.n * p.groups + (w.c + 2 * e) / p.cg, h = w.n * p.groups + (w.c + 2 * e + 1) / p.cg;
+    const float2 a = means[g], b = means[h];
+    mu[e] = f2(-mean[g], -mean[h]);
+    rv[e] = f2(rstd[g], rstd[h]);
+    k0[e] = mul2(rv[e], f2(-a.x, -b.x));
+    k1[e] = mul2(rv[e], f2(-a.y, -b.y));
   }
-  constexpr int A = kGnAhead / 2;
+  constexpr int A = kGnAhead<T> / 2;
   const long long base = w.n * p.M * p.C + w.c;
   for (int m = w.m1 - 1 - w.rl; m >= w.m0; m -= A * w.lanes) {
     typename R::V rx[A], ry[A];
@@ -666,16 +719,16 @@ __global__ void __launch_bounds__(kGnThreads) gn_bwd_apply_kernel(Gn p, Part q, 
 #pragma unroll
     for (int u = 0; u < A; ++u) {
       if (m - u * w.lanes < w.m0) break;
-      float xh[8], da[8];
-      R::wide(rx[u], xh);
-      R::wide(ry[u], da);
+      float2 xh[4], da[4];
+      wide4<T>(rx[u], xh);
+      wide4<T>(ry[u], da);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        xh[e] = (xh[e] - mu[e]) * rv[e];
-        da[e] = dact<SILU>(da[e], fmaf(xh[e], sc[e], bi[e])) * sc[e];
-        da[e] = rv[e] * (da[e] - av[e].x - xh[e] * av[e].y);
+      for (int e = 0; e < 4; ++e) {
+        xh[e] = mul2(add2(xh[e], mu[e]), rv[e]);
+        da[e] = mul2(dact2<SILU>(da[e], fma2(xh[e], sc[e], bi[e])), sc[e]);
+        da[e] = fma2(rv[e], da[e], fma2(xh[e], k1[e], k0[e]));
       }
-      ActT<float>::st8(dx + base + (long long)(m - u * w.lanes) * p.C, da);
+      st4p<float>(dx + base + (long long)(m - u * w.lanes) * p.C, da);
     }
   }
 }
@@ -697,6 +750,7 @@ int gn_plan(int N, int M, int C, int groups, int dtype, GnPlan& pl) {
   if (N <= 0 || M <= 0 || C <= 0 || groups <= 0 || C > kGnMaxDim || C % groups != 0) return SS_ERR_DIM;
   if (dtype != SS_F32 && dtype != SS_BF16) return SS_ERR_UNSUPPORTED;
   if (C % 8 != 0) return SS_ERR_ALIGN;
+  if (N > kGnMost || M > kGnMost) return SS_ERR_DIM;
   if ((long long)N * groups > 2147483647ll || (long long)N * M > (1ll << 40) / C) return SS_ERR_DIM;
   Gn& p = pl.p;
   p.N = N; p.M = M; p.C = C; p.groups = groups; p.cg = C / groups;
@@ -724,8 +778,8 @@ int gn_plan(int N, int M, int C, int groups, int dtype, GnPlan& pl) {
     q.ut = std::min(32, C / 8);
     q.tiles = (C / 8 + q.ut - 1) / q.ut;
     const int lanes = kGnThreads / q.ut;
-    const long long want = std::max<long long>(1, 152ll * 8 / ((long long)N * q.tiles));
-    const long long most = std::max(1, M / (lanes * kGnAhead));
+    const long long want = std::max<long long>(1, 152ll * 4 / ((long long)N * q.tiles));
+    const long long most = std::max(1, M / (lanes * 4));
     const int splits = (int)std::min(want, most);
     q.per = (M + splits - 1) / splits;
     q.splits = (M + q.per - 1) / q.per;
@@ -744,7 +798,7 @@ void fwd_lanes(const GnPlan& pl, const T* x, const float* scale, const float* bi
 template <typename T, int G, bool SILU>
 void bwd_lanes(const GnPlan& pl, const T* dy, const T* x, const float* scale, const float* bias, const float* mean, const float* rstd, float* dx,
                float* part, cudaStream_t s) {
-  gn_bwd_lanes_kernel<T, G, 2, SILU><<<dim3(pl.grid, pl.segs), kGnThreads, 0, s>>>(pl.p, pl.gp, dy, x, scale, bias, mean, rstd, dx, part);
+  gn_bwd_lanes_kernel<T, G, 3, SILU><<<dim3(pl.grid, pl.segs), kGnThreads, 0, s>>>(pl.p, pl.gp, dy, x, scale, bias, mean, rstd, dx, part);
 }
 #define GN_LANES(f, ...)                             \
   switch (pl.G) {                                    \
