@@ -14,7 +14,6 @@ namespace {
 using namespace ssk;
 
 constexpr int kGT = 512;
-
 template <int KP>
 struct GradTc {
   static constexpr int NKP = KP / 64, ST = NKP * kPanel;  // bytes of a term of a state
@@ -93,6 +92,13 @@ __global__ void __launch_bounds__(kGT, 1) delta_grad_tc_kernel(Delta p, const __
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tm = *tma;
+  auto state = [&](const float4* src, float4 (&x)[SC / 4]) {
+#pragma unroll
+    for (int e = 0; e < SC / 4; ++e)
+      x[e] = mine && cq * SC + 4 * e < a.K ? __ldcg(src + (long long)(cq * (SC / 4) + e) * a.V) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  float4 X[SC / 4];
+  state(s0, X);
   bool ok = chain_wait(&bar[L::kIn], 0);
   if (valid < kDC && t0 + valid < a.L) {  // the row ends inside the tensor: what follows is not its own
     if (warp == 0) tok_clear(sb + L::dy, vp, valid, lane);
@@ -146,13 +152,6 @@ __global__ void __launch_bounds__(kGT, 1) delta_grad_tc_kernel(Delta p, const __
       put_terms<2>(sb + L::S + unit_at(kPanel, row, cq * (SC / 8) + e), L::ST, y);
     }
   };
-  auto state = [&](const float4* src, float4 (&x)[SC / 4]) {
-#pragma unroll
-    for (int e = 0; e < SC / 4; ++e)
-      x[e] = mine && cq * SC + 4 * e < a.K ? __ldcg(src + (long long)(cq * (SC / 4) + e) * a.V) : make_float4(0.f, 0.f, 0.f, 0.f);
-  };
-  float4 X[SC / 4];
-  state(s0, X);
   // sums over a warp's 32 columns: each step adds a half of the values to the other lane's and keeps the half
 #pragma unroll
   for (int n = 16; n > 0; n >>= 1) {

@@ -35,41 +35,43 @@ template <>
 struct Substitute<0> {
   __device__ __forceinline__ static void go(const float*, const float*, float (&m)[16], float (&y)[16]) { m[0] = y[0] = 0.f; }
 };
-// x[i] -= sum_{s < S} a[i][s] z[s] for R rows, z[s] = be[s] * col[s * kPrepLA]
+// x[i] -= sum_{s < S} a[i][s] z[s] for R rows and two neighbouring columns, z[s] = be[s] * col[s * kPrepLA]
 template <int S, int R>
-__device__ __forceinline__ void below(const float* __restrict__ a, const float* __restrict__ be, const float* __restrict__ col, float (&x)[R]) {
+__device__ __forceinline__ void below(const float* __restrict__ a, const float* __restrict__ be, const float* __restrict__ col, float2 (&x)[R]) {
 #pragma unroll 2
   for (int s = 0; s < S; s += 4) {
-    float z[4];
+    const float4 b = *reinterpret_cast<const float4*>(be + s);
+    const float bb[4] = {-b.x, -b.y, -b.z, -b.w};
+    float2 z[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z[e] = be[s + e] * col[(s + e) * kPrepLA];
+    for (int e = 0; e < 4; ++e) z[e] = mul2(bc2(bb[e]), *reinterpret_cast<const float2*>(col + (s + e) * kPrepLA));
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const float4 v = *reinterpret_cast<const float4*>(a + i * kPrepLA + s);
-      x[i] = fmaf(-v.x, z[0], x[i]);
-      x[i] = fmaf(-v.y, z[1], x[i]);
-      x[i] = fmaf(-v.z, z[2], x[i]);
-      x[i] = fmaf(-v.w, z[3], x[i]);
+      x[i] = fma2(bc2(v.x), z[0], x[i]);
+      x[i] = fma2(bc2(v.y), z[1], x[i]);
+      x[i] = fma2(bc2(v.z), z[2], x[i]);
+      x[i] = fma2(bc2(v.w), z[3], x[i]);
     }
   }
 }
-// the S x S block below the diagonal at tokens t0 .. t0 + 2 S: this thread's R rows from r and column c of it
+// the S x S block below the diagonal at tokens t0 .. t0 + 2 S: this thread's R rows from r and two columns from c of it
 template <int S, int R>
 __device__ __forceinline__ void join(float* A, const float* be, int t0, int r, int c) {
   float* d = A + t0 * (kPrepLA + 1);
   float* row = d + (S + r) * kPrepLA;
-  float x[R];
+  float2 x[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) x[i] = row[i * kPrepLA + c];
+  for (int i = 0; i < R; ++i) x[i] = *reinterpret_cast<const float2*>(row + i * kPrepLA + c);
   below<S, R>(row, be + t0, d + c, x);
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < R; ++i) row[i * kPrepLA + c] = x[i];
+  for (int i = 0; i < R; ++i) *reinterpret_cast<float2*>(row + i * kPrepLA + c) = x[i];
   __syncthreads();
   below<S, R>(row + S, be + t0 + S, d + S * kPrepLA + c, x);
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < R; ++i) row[i * kPrepLA + c] = x[i];
+  for (int i = 0; i < R; ++i) *reinterpret_cast<float2*>(row + i * kPrepLA + c) = x[i];
   __syncthreads();
 }
 __device__ __forceinline__ void solve(float* A, const float* be, int tid) {
@@ -85,8 +87,8 @@ __device__ __forceinline__ void solve(float* A, const float* be, int tid) {
     for (int t = 0; t < 16; ++t) a[t * kPrepLA + lane] = m[t];
   }
   __syncthreads();
-  join<16, 4>(A, be, (tid >> 6) * 32, (tid >> 4 & 3) * 4, tid & 15);
-  join<32, 8>(A, be, 0, warp * 8, lane);
+  join<16, 2>(A, be, (tid >> 6) * 32, (tid >> 3 & 7) * 2, (tid & 7) * 2);
+  join<32, 4>(A, be, 0, (tid >> 4) * 4, (tid & 15) * 2);
 }
 
 template <typename T, int KP>

@@ -741,7 +741,7 @@ struct GnPlan {
   Gn p;
   GnForm form;
   int G, gp, segs, grid;  // lanes
-  Part q;                 // parts
+  Part q, qa;             // parts of the sums, and of the forward's second pass
   size_t fwd, bwd;        // workspace
   int rows;               // partial rows of the backward's column sums
 };
@@ -774,16 +774,23 @@ int gn_plan(int N, int M, int C, int groups, int dtype, GnPlan& pl) {
     pl.bwd = (size_t)pl.rows * 2 * C * sizeof(float);
   } else {
     pl.form = kParts;
-    Part& q = pl.q;
-    q.ut = std::min(32, C / 8);
-    q.tiles = (C / 8 + q.ut - 1) / q.ut;
-    const int lanes = kGnThreads / q.ut;
-    const long long want = std::max<long long>(1, 152ll * 4 / ((long long)N * q.tiles));
-    const long long most = std::max(1, M / (lanes * 4));
-    const int splits = (int)std::min(want, most);
-    q.per = (M + splits - 1) / splits;
-    q.splits = (M + q.per - 1) / q.per;
-    if ((long long)N * q.splits * q.tiles > 2147483647ll) return SS_ERR_DIM;
+    // one turn of two CTAs an SM for the sums (17.8 -> 15.9 us for 4 x 2048 x 4096 in bf16 against two turns), three turns
+    // for the forward's output (25 -> 22)
+    auto parts = [&](int turns) {
+      Part q;
+      q.ut = std::min(32, C / 8);
+      q.tiles = (C / 8 + q.ut - 1) / q.ut;
+      const int lanes = kGnThreads / q.ut;
+      const long long want = std::max<long long>(1, 152ll * 2 * turns / ((long long)N * q.tiles));
+      const int splits = (int)std::min<long long>(want, std::max(1, M / (lanes * 4)));
+      q.per = (M + splits - 1) / splits;
+      q.splits = (M + q.per - 1) / q.per;
+      return q;
+    };
+    pl.qa = parts(3);
+    pl.q = parts(1);
+    const Part& q = pl.q;
+    if ((long long)N * pl.qa.splits * q.tiles > 2147483647ll) return SS_ERR_DIM;
     pl.rows = N * q.splits;
     pl.fwd = (size_t)N * q.splits * 2 * C * sizeof(float) + (size_t)N * groups * 2 * sizeof(float);
     pl.bwd = (size_t)N * q.splits * 2 * C * sizeof(float) + (size_t)N * groups * 2 * sizeof(float);
@@ -829,7 +836,7 @@ int fwd(const GnPlan& pl, const T* x, const float* scale, const float* bias, T* 
     gn_stats_kernel<T><<<grid, kGnThreads, 0, s>>>(p, q, x, part);
     if (launch_dependent(gn_join_kernel, dim3((unsigned)((long long)p.N * p.groups)), dim3(kGnThreads), 0, s, p, q, (const float*)part, mu, rv) !=
             cudaSuccess ||
-        launch_dependent(gn_apply_kernel<T, SILU>, dim3(grid), dim3(kGnThreads), 0, s, p, q, x, scale, bias, (const float*)mu, (const float*)rv, y) !=
+        launch_dependent(gn_apply_kernel<T, SILU>, dim3((unsigned)((long long)p.N * pl.qa.splits * q.tiles)), dim3(kGnThreads), 0, s, p, pl.qa, x, scale, bias, (const float*)mu, (const float*)rv, y) !=
             cudaSuccess)
       return SS_ERR_CUDA;
   }
