@@ -4,7 +4,7 @@
 //   dbeta = <du, r>      dg_t = sum_{s >= t} (do_s.o_s - dR_s.v_s) + <S1, dS>           along columns of V, in fp32
 //   E = scale D do u^T,  F = -D dR u^T (strict)                                          [t, s]
 //   dq = scale e^c do S0^T + E K      dk = -e^c dR S0^T + e^{c_last - c} u dS^T + E^T Q + (F + F^T) K
-// dq and dk are rounded to bf16; their fp32 operands are two bf16 terms (16 bits).  Products run with the columns of K as the
+// dq and dk are rounded to bf16; their fp32 operands are two bf16 terms (2^-15).  Products run with the columns of K as the
 // 128 rows of an MMA; S0, dS, u and dR lie in shared memory by columns of V, as they come from memory, and are contracted down
 // their rows.
 #include "delta_tc.cuh"

@@ -108,7 +108,8 @@ __global__ void __launch_bounds__(kGnThreads) gn_fwd_lanes_kernel(Gn p, int gp, 
   ld8p(bias + c, cv && bias != nullptr, bi);
   const float inv = 1.0f / (float)p.cg;
   const int step = (int)gridDim.x * 8 * rs * U;
-  for (int r0 = ((int)blockIdx.x * 8 + warp) * rs * U + slot / gp; r0 < p.N; r0 += step) {  // this lane's rows: r0 + u rs
+  for (int w0 = ((int)blockIdx.x * 8 + warp) * rs * U; w0 < p.N; w0 += step) {  // (a warp goes round together: it shuffles)
+    const int r0 = w0 + slot / gp;  // this lane's rows: r0 + u rs
     const T* src = x + (long long)r0 * p.C + c;
     typename R::V raw[U];
 #pragma unroll
@@ -157,7 +158,8 @@ __global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_lanes_kernel(Gn p, int g
   for (int e = 0; e < 4; ++e) as[e] = ab[e] = f2(0.f, 0.f);
   const float inv = 1.0f / (float)p.cg;
   const int step = (int)gridDim.x * 8 * rs * U;
-  for (int r0 = ((int)blockIdx.x * 8 + warp) * rs * U + slot / gp; r0 < p.N; r0 += step) {
+  for (int w0 = ((int)blockIdx.x * 8 + warp) * rs * U; w0 < p.N; w0 += step) {
+    const int r0 = w0 + slot / gp;
     const long long first = (long long)r0 * p.C + c;
     typename R::V rx[U], ry[U];
     float mu[U], rv[U];

@@ -30,6 +30,8 @@ and RMSNorm scale invariance.
 
 from .conv1d import (conv1d_causal_bwd_ref, conv1d_causal_fwd_ref, conv1d_causal_silu_bwd_ref,
                      conv1d_causal_silu_fwd_ref, conv1d_step_bwd_ref, conv1d_step_fwd_ref, dsilu_ref, silu_ref)
+from .deltarule import deltarule_bwd_ref, deltarule_fwd_ref, deltarule_step_ref
+from .groupnorm import groupnorm_bwd_ref, groupnorm_fwd_ref
 from .layernorm import layernorm_bwd_ref, layernorm_fwd_ref
 from .linattn import linattn_bwd_ref, linattn_fwd_ref, linattn_step_ref
 from .rmsnorm import rmsnorm_bwd_ref, rmsnorm_fwd_ref
@@ -43,4 +45,5 @@ __all__ = [
     "conv1d_causal_silu_bwd_ref", "conv1d_step_bwd_ref",
     "rmsnorm_fwd_ref", "rmsnorm_bwd_ref", "layernorm_fwd_ref", "layernorm_bwd_ref",
     "linattn_fwd_ref", "linattn_bwd_ref", "linattn_step_ref",
+    "deltarule_fwd_ref", "deltarule_bwd_ref", "deltarule_step_ref", "groupnorm_fwd_ref", "groupnorm_bwd_ref",
 ]
