@@ -29,7 +29,8 @@ struct BackMaps {
 };
 
 template <int KP>
-__global__ void __launch_bounds__(kDThreads, 1) delta_back_tc_kernel(Delta p, const __grid_constant__ BackMaps maps, const float* __restrict__ dh_last,
+__global__ void __launch_bounds__(kDThreads, 1) delta_back_tc_kernel(Delta p, const __grid_constant__ BackMaps maps,
+                                                                     const float* __restrict__ dh_last,
                                                                      __nv_bfloat16* __restrict__ dv, float* __restrict__ dS, float* __restrict__ du,
                                                                      float* __restrict__ dh0) {
   using L = BackTc<KP>;
@@ -121,7 +122,8 @@ __global__ void __launch_bounds__(kDThreads, 1) delta_back_tc_kernel(Delta p, co
         for (int n = 2; n >= 0; --n)
 #pragma unroll
           for (int s = 3; s >= 0; --s)
-            mma_ss(tm + L::D2, cols_desc(sb + L::dy, kTok, s), cols_desc(sb + L::p + n * kDTerm, kTok, s), mma_idesc(16 * (s + 1), true, true), n < 2 || s < 3);
+            mma_ss(tm + L::D2, cols_desc(sb + L::dy, kTok, s), cols_desc(sb + L::p + n * kDTerm, kTok, s),
+                   mma_idesc(16 * (s + 1), true, true), n < 2 || s < 3);
         mma_commit(&bar[L::kD2]);
       }
       __syncwarp();
@@ -156,7 +158,8 @@ __global__ void __launch_bounds__(kDThreads, 1) delta_back_tc_kernel(Delta p, co
         for (int n = 2; n >= 0; --n)
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            mma_ss(tm + L::D5, rows_desc(sb + L::a1 + n * kPanel, kPanel, s), cols_desc(kt + kTok, kPanel, s), mma_idesc(KP, false, true), n < 2 || s > 0);
+            mma_ss(tm + L::D5, rows_desc(sb + L::a1 + n * kPanel, kPanel, s), cols_desc(kt + kTok, kPanel, s), mma_idesc(KP, false, true),
+                   n < 2 || s > 0);
       }
       __syncwarp();
       if (!wait(L::kMr, par) || !wait(L::kW, 0u)) break;
@@ -168,7 +171,8 @@ __global__ void __launch_bounds__(kDThreads, 1) delta_back_tc_kernel(Delta p, co
           const uint32_t l = pairs & 3u, r = sb + L::m + (pairs >> 2 & 3u) * kDTerm;
 #pragma unroll
           for (int s = 3; s >= 0; --s) {
-            if (l == 2) mma_ss(tm + L::D1, rows_desc(sb + L::w2, kPanel, s), cols_desc(r, kTok, s), mma_idesc(16 * (s + 1), false, true), n > 0 || s < 3);
+            if (l == 2)
+              mma_ss(tm + L::D1, rows_desc(sb + L::w2, kPanel, s), cols_desc(r, kTok, s), mma_idesc(16 * (s + 1), false, true), n > 0 || s < 3);
             else mma_ts(tm + L::D1, tm + L::W + l * 32 + s * 8, cols_desc(r, kTok, s), mma_idesc(16 * (s + 1), false, true), n > 0 || s < 3);
           }
         }

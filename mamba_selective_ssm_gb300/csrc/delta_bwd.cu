@@ -1,4 +1,5 @@
-// The gated delta rule's backward (deltarule_bwd) for sm_103a.
+// The gated delta rule's backward (deltarule_bwd) for sm_103a: its plan, and its kernels for fp32 (bf16: delta_back_tc.cu,
+// delta_grad_tc.cu).
 //
 // With U the gradient of the state leaving a chunk (dS1) and every formula in the scaled tokens of delta_common.cuh:
 //   du0 = scale P^T do + e^{c_last - c} K dS1      du = du0 - M^T (beta du0)      dv = dR = beta du      dbeta = <du, r>
@@ -9,7 +10,7 @@
 // with a writing key, and their sums over a chunk meet in o, v and the state that leaves it:
 //   dg_t = sum_{s >= t} (do_s.o_s - dv_s.v_s) + <S1, dS1>        (s within the chunk)
 // so the fp32 gradients dg and dbeta need no product over V but sums along its columns, which the warps that hold o, u and du
-// have in fp32; what enters dq and dk alone is rounded to their type's terms.
+// have in fp32.
 #include <stddef.h>
 
 #include "delta_common.cuh"
@@ -21,21 +22,21 @@ using namespace ssk;
 // ---------------------------------------------------------------- the chain
 // As in the forward, a warp carries 16 columns of dS, transposed, from the last chunk to the first.  It leaves dS1 and du of
 // every chunk ([V][K] and [V][64], fp32) and dv.
-template <typename T, int KP>
+template <int KP>
 struct BackStage {
-  static constexpr int k = 0, q = k + DTile<KP, kTerms<T>>::bytes, m = q + DTile<KP, kTerms<T>>::bytes, p = m + kDMBytes,
+  static constexpr int k = 0, q = k + DTile<KP, 2>::bytes, m = q + DTile<KP, 2>::bytes, p = m + kDMBytes,
                        vec = p + DTile<kDC, 2>::bytes, up = vec + kDVec * 4, slices = up + 2 * kDC * 4;
-  static int bytes(int warps) { return slices + warps * DSlice<T>::bytes; }
+  static int bytes(int warps) { return slices + warps * DSlice::bytes; }
 };
 
 constexpr int kWalkThreads = 256;
 
-template <typename T, int KP>
-__global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const T* __restrict__ dout, const float* __restrict__ dh_last,
-                                                                 T* __restrict__ dv, float* __restrict__ dS, float* __restrict__ du,
+template <int KP>
+__global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const float* __restrict__ dout, const float* __restrict__ dh_last,
+                                                                 float* __restrict__ dv, float* __restrict__ dS, float* __restrict__ du,
                                                                  float* __restrict__ dh0, int stages, int stage_bytes) {
-  using St = BackStage<T, KP>;
-  constexpr int N = kTerms<T>, KT = KP / 8;
+  using St = BackStage<KP>;
+  constexpr int N = 2, KT = KP / 8;
   extern __shared__ __align__(128) unsigned char raw[];
   const uint32_t sb = smem_u32(raw);
   const LinAttn& a = p.a;
@@ -46,8 +47,8 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
   const int h = (int)(bh % a.H), b = (int)(bh / a.H), gh = h / (a.H / a.G);
   const int v0 = vt * (nt / 2) + warp * 16, vw = a.V - v0;
   const int len = a.len(b), nck = (len + kDC - 1) / kDC;
-  const T* q = static_cast<const T*>(a.q) + (long long)b * a.L * a.ldq + (long long)gh * a.K;
-  const T* k = static_cast<const T*>(a.k) + (long long)b * a.L * a.ldk + (long long)gh * a.K;
+  const float* q = static_cast<const float*>(a.q) + (long long)b * a.L * a.ldq + (long long)gh * a.K;
+  const float* k = static_cast<const float*>(a.k) + (long long)b * a.L * a.ldk + (long long)gh * a.K;
   const long long ldo = (long long)a.H * a.V;
   const long long row0 = ((long long)b * a.L * a.H + h) * a.V + v0;
 
@@ -56,12 +57,12 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
     const long long t0 = (long long)ck * kDC;
     const int valid = len - (int)t0 < kDC ? len - (int)t0 : kDC;
     const long long item = bh * a.nck + ck;
-    tile_load<T, KP>(at + St::k, k + t0 * a.ldk, a.ldk, valid, a.K, tid, nt);
-    tile_load<T, KP>(at + St::q, q + t0 * a.ldq, a.ldq, valid, a.K, tid, nt);
+    tile_load<float, KP>(at + St::k, k + t0 * a.ldk, a.ldk, valid, a.K, tid, nt);
+    tile_load<float, KP>(at + St::q, q + t0 * a.ldq, a.ldq, valid, a.K, tid, nt);
     tile_copy(at + St::m, p.M + item * kDMBytes, kDMBytes, tid, nt);
     tile_copy(at + St::p, p.P + item * DTile<kDC, 2>::bytes, DTile<kDC, 2>::bytes, tid, nt);
     tile_copy(at + St::vec, reinterpret_cast<const unsigned char*>(p.vec + item * kDVec), kDVec * 4, tid, nt);
-    DSlice<T>::load(at + St::slices + warp * DSlice<T>::bytes, dout + row0 + t0 * ldo, ldo, valid, vw, lane);
+    DSlice::load(at + St::slices + warp * DSlice::bytes, dout + row0 + t0 * ldo, ldo, valid, vw, lane);
     cp_commit();
   };
 
@@ -79,12 +80,12 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
     const uint32_t off = stages == 2 ? (uint32_t)((ck & 1) * stage_bytes) : 0u, at = sb + off;
     const float* vec = reinterpret_cast<const float*>(raw + off + St::vec);
     float* up = reinterpret_cast<float*>(raw + off + St::up);
-    const uint32_t mine = at + St::slices + warp * DSlice<T>::bytes;
+    const uint32_t mine = at + St::slices + warp * DSlice::bytes;
     const long long item = bh * a.nck + ck;
     cp_wait<0>();
     __syncthreads();
-    tile_scale<T, KP>(at + St::k, up, tid, nt);
-    tile_scale<T, KP>(at + St::q, up + kDC, tid, nt);
+    tile_scale<KP>(at + St::k, up, tid, nt);
+    tile_scale<KP>(at + St::q, up + kDC, tid, nt);
     __syncthreads();
     if (stages == 2 && ck > 0) fetch(ck - 1);
 #pragma unroll
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
           uint32_t bb[N][4];
 #pragma unroll
           for (int n = 0; n < N; ++n) right_rows<KP, N>(bb[n], at + St::k, np, kb, n, lane);
-          mma_terms<N>(D[2 * np], D[2 * np + 1], hi, lo, bb[0], bb[N - 1]);
+          mma_terms(D[2 * np], D[2 * np + 1], hi, lo, bb[0], bb[N - 1]);
         }
       }
 #pragma unroll
@@ -125,10 +126,10 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
       }
     }
     uint32_t hi[4][4], lo[4][4];
-    {  // (do scaled by powers of two only: one exact term in bf16)
+    {  // scale do^T P
       float x[8][4];
 #pragma unroll
-      for (int np = 0; np < 4; ++np) DSlice<T>::read(mine, np, lane, x[2 * np], x[2 * np + 1]);
+      for (int np = 0; np < 4; ++np) DSlice::read(mine, np, lane, x[2 * np], x[2 * np + 1]);
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
         const float2 qu = *reinterpret_cast<const float2*>(up + kDC + 8 * n + t2);
@@ -140,8 +141,7 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
       const RowScale xs = row_scale(x);
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb) {
-        if constexpr (N == 1) left_first(hi[kb], x[2 * kb], x[2 * kb + 1], xs);
-        else left_terms(hi[kb], lo[kb], x[2 * kb], x[2 * kb + 1], xs);
+        left_terms(hi[kb], lo[kb], x[2 * kb], x[2 * kb + 1], xs);
       }
 #pragma unroll
       for (int np = 0; np < 4; ++np) {
@@ -151,14 +151,7 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
           uint32_t b0[4], b1[4];
           right_cols<kDC, 2>(b0, at + St::p, np, kb, 0, lane);
           right_cols<kDC, 2>(b1, at + St::p, np, kb, 1, lane);
-          if constexpr (N == 1) {
-            mma_f16(c[0], hi[kb], b1[0], b1[1]);
-            mma_f16(c[1], hi[kb], b1[2], b1[3]);
-            mma_f16(c[0], hi[kb], b0[0], b0[1]);
-            mma_f16(c[1], hi[kb], b0[2], b0[3]);
-          } else {
-            mma_terms<2>(c[0], c[1], hi[kb], lo[kb], b0, b1);
-          }
+          mma_terms(c[0], c[1], hi[kb], lo[kb], b0, b1);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -188,7 +181,7 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
           uint32_t b0[4], b1[4];
           right_cols<kDC, 2>(b0, at + St::m, np, kb, 0, lane);
           right_cols<kDC, 2>(b1, at + St::m, np, kb, 1, lane);
-          mma_terms<2>(c[0], c[1], hi[kb], lo[kb], b0, b1);
+          mma_terms(c[0], c[1], hi[kb], lo[kb], b0, b1);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -218,7 +211,7 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
     {  // dS0^T = e^{c_last} dS1^T + (scale e^c do)^T Q - (e^c dR)^T K, the two left operands in one scale
       float x[8][4];
 #pragma unroll
-      for (int np = 0; np < 4; ++np) DSlice<T>::read(mine, np, lane, x[2 * np], x[2 * np + 1]);
+      for (int np = 0; np < 4; ++np) DSlice::read(mine, np, lane, x[2 * np], x[2 * np + 1]);
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
         const int t = 8 * n + t2;
@@ -253,10 +246,10 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
           uint32_t bb[N][4];
 #pragma unroll
           for (int n = 0; n < N; ++n) right_cols<KP, N>(bb[n], at + St::q, jp, kb, n, lane);
-          mma_terms<N>(c[0], c[1], hi[kb], lo[kb], bb[0], bb[N - 1]);
+          mma_terms(c[0], c[1], hi[kb], lo[kb], bb[0], bb[N - 1]);
 #pragma unroll
           for (int n = 0; n < N; ++n) right_cols<KP, N>(bb[n], at + St::k, jp, kb, n, lane);
-          mma_terms<N>(c[0], c[1], dh[kb], dl[kb], bb[0], bb[N - 1]);
+          mma_terms(c[0], c[1], dh[kb], dl[kb], bb[0], bb[N - 1]);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -280,28 +273,23 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
   }
   const int w = vw < 16 ? vw : 16;  // tokens of chunks past the row's end
   for (long long i = (long long)nck * kDC * 16 + lane; i < (long long)a.L * 16; i += 32)
-    if ((int)(i & 15) < w) ActT<T>::st1(dv + row0 + (i >> 4) * ldo + (i & 15), 0.f);
+    if ((int)(i & 15) < w) dv[row0 + (i >> 4) * ldo + (i & 15)] = 0.f;
 }
 
 // ---------------------------------------------------------------- the other gradients, chunk by chunk
 // A CTA takes one (batch row, head, chunk).  First each warp takes 16 columns of V: it finds u and o as the forward does, and
 // what the columns add to dg and dbeta.  Then the warps share the products that contract over V, from tiles in shared memory
 // scaled as a whole: u, dR, S0, dS1 lie [V][..].
-template <typename T, int KP, int VP>
+template <int KP, int VP>
 struct GradSmem {
-  static constexpr int N = kTerms<T>, tile = DTile<KP, N>::bytes;
+  static constexpr int N = 2, tile = DTile<KP, N>::bytes;
   static constexpr int vk = VP * KP * 2 * N, vt = VP * kDC * 2 * N, tt = DTile<kDC, N>::bytes;
   static constexpr int doo = 0, u = doo + DTile<VP, N>::bytes, r = u + vt, front = r + vt;
-  // bf16: everything has a place, but M and P lie where S0 and dS1 come.  fp32: k, q and then S0, dS1, and k, q again
-  // take turns, E and F lie where M and P were.
-  static constexpr bool turns = N == 2;
-  static constexpr int both = 2 * tile > vk ? 2 * tile : vk;  // k with q, or one of S0 and dS1
-  static constexpr int k = front, q = k + tile;
-  static constexpr int s0 = turns ? front : q + tile, s1 = turns ? s0 : s0 + vk;
-  static constexpr int mp = 2 * kDMBytes;
-  static constexpr int m = turns ? front + both : s0, p = m + kDMBytes;
-  static constexpr int e = turns ? m : s0 + (2 * vk > mp ? 2 * vk : mp), f = e + tt;
-  static constexpr int end = turns ? m + (mp > 2 * tt ? mp : 2 * tt) : f + tt;
+  // k with q, S0, dS1, and k with q again take turns; E and F lie where M and P were
+  static constexpr int both = 2 * tile > vk ? 2 * tile : vk;
+  static constexpr int k = front, q = k + tile, st = front;
+  static constexpr int m = front + both, p = m + kDMBytes, e = m, f = e + tt;
+  static constexpr int end = m + 2 * (kDMBytes > tt ? kDMBytes : tt);
   static constexpr int vec = end, up = vec + kDVec * 4, red = up + 3 * kDC * 4, bytes = red + (2 * 8 * kDC + 64) * 4;
 };
 
@@ -329,36 +317,29 @@ __device__ __forceinline__ float abs_max(const float (&x)[NJ][4]) {
   return warp_max(m);
 }
 // accumulators to a tile of rows of W columns: rows r0 + lane / 4 (+ 8), column tile j
-template <int W, int N>
+template <int W>
 __device__ __forceinline__ void store_acc(uint32_t tile, int r0, int j, const float (&x)[4], float f, int lane) {
 #pragma unroll
   for (int e = 0; e < 4; e += 2) {
     const int r = r0 + (lane >> 2) + (e >> 1) * 8;
     uint32_t hi, lo;
     split_half(x[e] * f, x[e + 1] * f, hi, lo);
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(tile + DTile<W, N>::at(r, j, 0) + 4 * (lane & 3)), "r"(hi) : "memory");
-    if constexpr (N == 2)
-      asm volatile("st.shared.b32 [%0], %1;" ::"r"(tile + DTile<W, N>::at(r, j, 1) + 4 * (lane & 3)), "r"(lo) : "memory");
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(tile + DTile<W, 2>::at(r, j, 0) + 4 * (lane & 3)), "r"(hi) : "memory");
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(tile + DTile<W, 2>::at(r, j, 1) + 4 * (lane & 3)), "r"(lo) : "memory");
   }
 }
-// c += a b over one step, the terms that N asks for
-template <int N>
-__device__ __forceinline__ void mma_pair(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[N][4], const uint32_t (&b)[N][4]) {
-  if constexpr (N == 1) {
-    mma_f16(c0, a[0], b[0][0], b[0][1]);
-    mma_f16(c1, a[0], b[0][2], b[0][3]);
-  } else {
-    mma_terms<2>(c0, c1, a[0], a[1], b[0], b[1]);
-  }
+// c += a b over one step
+__device__ __forceinline__ void mma_pair(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[2][4], const uint32_t (&b)[2][4]) {
+  mma_terms(c0, c1, a[0], a[1], b[0], b[1]);
 }
 
-template <typename T, typename TO, int KP, int VP>
-__global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const float* __restrict__ ckpt, const T* __restrict__ dout,
+template <int KP, int VP>
+__global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const float* __restrict__ ckpt, const float* __restrict__ dout,
                                                                   const float* __restrict__ dS, const float* __restrict__ du,
-                                                                  TO* __restrict__ dq, TO* __restrict__ dk, int heads,
+                                                                  float* __restrict__ dq, float* __restrict__ dk, int heads,
                                                                   float* __restrict__ dg, float* __restrict__ dbeta) {
-  using Sm = GradSmem<T, KP, VP>;
-  constexpr int N = kTerms<T>, KT = KP / 8, VB = VP / 16, NC = KP / 16;  // NC: column tiles of a warp's half of K
+  using Sm = GradSmem<KP, VP>;
+  constexpr int N = 2, KT = KP / 8, VB = VP / 16, NC = KP / 16;  // NC: column tiles of a warp's half of K
   extern __shared__ __align__(128) unsigned char raw[];
   const uint32_t sb = smem_u32(raw);
   const LinAttn& a = p.a;
@@ -371,12 +352,12 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
   const long long tok = (long long)b * a.L + t0;
   // rows of dq and dk: `heads` of them to a token (the groups', or every head's own part)
   const long long ldg = (long long)heads * a.K;
-  TO* dqb = dq + (tok * heads + (heads == a.G ? gh : h)) * a.K;
-  TO* dkb = dk + (tok * heads + (heads == a.G ? gh : h)) * a.K;
+  float* dqb = dq + (tok * heads + (heads == a.G ? gh : h)) * a.K;
+  float* dkb = dk + (tok * heads + (heads == a.G ? gh : h)) * a.K;
   if (valid == 0) {
     for (int i = tid; i < rows * a.K; i += kGradThreads) {
-      ActT<TO>::st1(dqb + i / a.K * ldg + i % a.K, 0.f);
-      ActT<TO>::st1(dkb + i / a.K * ldg + i % a.K, 0.f);
+      dqb[i / a.K * ldg + i % a.K] = 0.f;
+      dkb[i / a.K * ldg + i % a.K] = 0.f;
     }
     if (tid < rows) {
       if (dg != nullptr) dg[(tok + tid) * a.H + h] = 0.f;
@@ -384,16 +365,16 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
     }
     return;
   }
-  const T* q = static_cast<const T*>(a.q) + tok * a.ldq + (long long)gh * a.K;
-  const T* k = static_cast<const T*>(a.k) + tok * a.ldk + (long long)gh * a.K;
-  const T* v = static_cast<const T*>(a.v) + tok * a.ldv + (long long)h * a.V;
+  const float* q = static_cast<const float*>(a.q) + tok * a.ldq + (long long)gh * a.K;
+  const float* k = static_cast<const float*>(a.k) + tok * a.ldk + (long long)gh * a.K;
+  const float* v = static_cast<const float*>(a.v) + tok * a.ldv + (long long)h * a.V;
   const long long ldo = (long long)a.H * a.V;
-  const T* dob = dout + (tok * a.H + h) * a.V;
+  const float* dob = dout + (tok * a.H + h) * a.V;
   float *vec = reinterpret_cast<float*>(raw + Sm::vec), *up = reinterpret_cast<float*>(raw + Sm::up), *red = reinterpret_cast<float*>(raw + Sm::red);
   float* mx = red + 2 * 8 * kDC;  // eight warps' maxima: S0, u, dR, dS1, E, F, and the state's product
-  tile_load<T, KP>(sb + Sm::k, k, a.ldk, valid, a.K, tid, kGradThreads);
-  tile_load<T, KP>(sb + Sm::q, q, a.ldq, valid, a.K, tid, kGradThreads);
-  tile_load<T, VP>(sb + Sm::doo, dob, ldo, valid, a.V, tid, kGradThreads);
+  tile_load<float, KP>(sb + Sm::k, k, a.ldk, valid, a.K, tid, kGradThreads);
+  tile_load<float, KP>(sb + Sm::q, q, a.ldq, valid, a.K, tid, kGradThreads);
+  tile_load<float, VP>(sb + Sm::doo, dob, ldo, valid, a.V, tid, kGradThreads);
   tile_copy(sb + Sm::m, p.M + item * kDMBytes, kDMBytes, tid, kGradThreads);
   tile_copy(sb + Sm::p, p.P + item * kDMBytes, kDMBytes, tid, kGradThreads);
   tile_copy(sb + Sm::vec, reinterpret_cast<const unsigned char*>(p.vec + item * kDVec), kDVec * 4, tid, kGradThreads);
@@ -418,8 +399,8 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
   if (warp < VB) state(s0, S);
   cp_wait<0>();
   __syncthreads();
-  tile_scale<T, KP>(sb + Sm::k, up, tid, kGradThreads);
-  tile_scale<T, KP>(sb + Sm::q, up + kDC, tid, kGradThreads);
+  tile_scale<KP>(sb + Sm::k, up, tid, kGradThreads);
+  tile_scale<KP>(sb + Sm::q, up + kDC, tid, kGradThreads);
   // do of this warp's columns (before it is scaled in place), v and du, all tokens by columns
   float X[8][4], R[8][4], D[8][4];
   if (warp < VB) {
@@ -429,11 +410,11 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
       for (int e = 0; e < 4; ++e) {
         const int t = 8 * n + t2 + (e & 1), vv = g + (e >> 1) * 8;
         const bool on = t < valid && vv < vw;
-        X[n][e] = on ? ActT<T>::ld(v + (long long)t * a.ldv + v0 + vv) : 0.f;
+        X[n][e] = on ? v[(long long)t * a.ldv + v0 + vv] : 0.f;
         D[n][e] = vv < vw ? du[(item * a.V + v0 + vv) * kDC + t] : 0.f;
       }
   }
-  tile_scale<T, VP>(sb + Sm::doo, up + 2 * kDC, tid, kGradThreads);
+  tile_scale<VP>(sb + Sm::doo, up + 2 * kDC, tid, kGradThreads);
   __syncthreads();
   if (warp < VB) {
     float O[8][4];
@@ -452,10 +433,10 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
         uint32_t bb[N][4];
 #pragma unroll
         for (int n = 0; n < N; ++n) right_rows<KP, N>(bb[n], sb + Sm::k, np, kb, n, lane);
-        mma_terms<N>(R[2 * np], R[2 * np + 1], sh, sl, bb[0], bb[N - 1]);
+        mma_terms(R[2 * np], R[2 * np + 1], sh, sl, bb[0], bb[N - 1]);
 #pragma unroll
         for (int n = 0; n < N; ++n) right_rows<KP, N>(bb[n], sb + Sm::q, np, kb, n, lane);
-        mma_terms<N>(O[2 * np], O[2 * np + 1], sh, sl, bb[0], bb[N - 1]);
+        mma_terms(O[2 * np], O[2 * np + 1], sh, sl, bb[0], bb[N - 1]);
       }
     }
     float w[8][4];
@@ -485,7 +466,7 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
           uint32_t b0[4], b1[4];
           right_rows<kDC, 2>(b0, sb + Sm::m, np, kb, 0, lane);
           right_rows<kDC, 2>(b1, sb + Sm::m, np, kb, 1, lane);
-          mma_terms<2>(c[0], c[1], hi[kb], lo[kb], b0, b1);
+          mma_terms(c[0], c[1], hi[kb], lo[kb], b0, b1);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -523,7 +504,7 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
           uint32_t b0[4], b1[4];
           right_rows<kDC, 2>(b0, sb + Sm::p, np, kb, 0, lane);
           right_rows<kDC, 2>(b1, sb + Sm::p, np, kb, 1, lane);
-          mma_terms<2>(c[0], c[1], hi[kb], lo[kb], b0, b1);
+          mma_terms(c[0], c[1], hi[kb], lo[kb], b0, b1);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -532,7 +513,7 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int tt = t + (e & 1), vv = g + (e >> 1) * 8;
-            const float x = tt < valid && vv < vw ? ActT<T>::ld(dob + (long long)tt * ldo + v0 + vv) : 0.f;
+            const float x = tt < valid && vv < vw ? dob[(long long)tt * ldo + v0 + vv] : 0.f;
             const float oo = a.scale * (e & 1 ? qu.y : qu.x) * fmaf(c[i][e], us.r[e >> 1].up, O[n][e]);
             if (tt < valid) af[2 * n + (e & 1)] = fmaf(x, oo, af[2 * n + (e & 1)]);
           }
@@ -564,12 +545,8 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
   if (warp < VB) {
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
-      store_acc<kDC, N>(sb + Sm::u, v0, n, R[n], scU.down, lane);
-      store_acc<kDC, N>(sb + Sm::r, v0, n, D[n], scR.down, lane);
-    }
-    if constexpr (!Sm::turns) {
-#pragma unroll
-      for (int j = 0; j < KT; ++j) store_acc<KP, N>(sb + Sm::s0, v0, j, S[j], scS.down, lane);
+      store_acc<kDC>(sb + Sm::u, v0, n, R[n], scU.down, lane);
+      store_acc<kDC>(sb + Sm::r, v0, n, D[n], scR.down, lane);
     }
     // <S1, dS1> of these columns, and dS1's largest
     float x = 0.f;
@@ -595,10 +572,6 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
   }
   __syncthreads();
   const Pow2 scT = warps_scale(mx + 3, 8);
-  if (!Sm::turns && warp < VB) {
-#pragma unroll
-    for (int j = 0; j < KT; ++j) store_acc<KP, N>(sb + Sm::s1, v0, j, S[j], scT.down, lane);
-  }
   if (warp == 0) {  // dbeta, and the sums from each token on
     float s[2], d[2];
 #pragma unroll
@@ -648,8 +621,8 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
           uint32_t bb[N][4];
 #pragma unroll
           for (int n = 0; n < N; ++n) right_cols<kDC, N>(bb[n], sb + Sm::u, 2 * half + np, kb, n, lane);
-          mma_pair<N>(E[2 * np], E[2 * np + 1], ea, bb);
-          mma_pair<N>(F[2 * np], F[2 * np + 1], fa, bb);
+          mma_pair(E[2 * np], E[2 * np + 1], ea, bb);
+          mma_pair(F[2 * np], F[2 * np + 1], fa, bb);
         }
       }
     }
@@ -681,8 +654,8 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
     const Pow2 scE = warps_scale(mx + 4, 8), scF = warps_scale(mx + 5, 8);
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-      store_acc<kDC, N>(sb + Sm::e, 16 * mb, 4 * half + n, E[n], scE.down, lane);
-      store_acc<kDC, N>(sb + Sm::f, 16 * mb, 4 * half + n, F[n], scF.down, lane);
+      store_acc<kDC>(sb + Sm::e, 16 * mb, 4 * half + n, E[n], scE.down, lane);
+      store_acc<kDC>(sb + Sm::f, 16 * mb, 4 * half + n, F[n], scF.down, lane);
     }
   }
   const Pow2 scE = warps_scale(mx + 4, 8), scF = warps_scale(mx + 5, 8);
@@ -708,27 +681,25 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
       uint32_t bb[N][4];
 #pragma unroll
       for (int n = 0; n < N; ++n) right_cols<KP, N>(bb[n], tile, half * (NC / 2) + jp, kb, n, lane);
-      mma_pair<N>(C[2 * jp], C[2 * jp + 1], la, bb);
+      mma_pair(C[2 * jp], C[2 * jp + 1], la, bb);
     }
   };
   auto put_state = [&](uint32_t tile, const float* src, float f) {
     if (warp < VB) {
       state(src, S);
 #pragma unroll
-      for (int j = 0; j < KT; ++j) store_acc<KP, N>(tile, v0, j, S[j], f, lane);
+      for (int j = 0; j < KT; ++j) store_acc<KP>(tile, v0, j, S[j], f, lane);
     }
   };
-  __syncthreads();  // E, F; bf16: S0, dS1; fp32: k, q have been read
-  if constexpr (Sm::turns) {
-    put_state(sb + Sm::s0, s0, scS.down);
-    __syncthreads();
-  }
+  __syncthreads();  // E and F; k and q have been read
+  put_state(sb + Sm::st, s0, scS.down);
+  __syncthreads();
   zero();
   for (int kb = 0; kb < vb; ++kb) {
     uint32_t la[N][4];
 #pragma unroll
     for (int n = 0; n < N; ++n) left_rows<VP, N>(la[n], sb + Sm::doo, mb, kb, n, lane);
-    step(sb + Sm::s0, kb, la);
+    step(sb + Sm::st, kb, la);
   }
   const float fs = a.scale * scS.up;
   add(Q, fs * vec[ta] * up[2 * kDC + ta], fs * vec[tb] * up[2 * kDC + tb], true);
@@ -737,33 +708,29 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
     uint32_t la[N][4];
 #pragma unroll
     for (int n = 0; n < N; ++n) left_cols<kDC, N>(la[n], sb + Sm::r, mb, kb, n, lane);
-    step(sb + Sm::s0, kb, la);
+    step(sb + Sm::st, kb, la);
   }
   add(Kg, -vec[ta] * scR.up * scS.up, -vec[tb] * scR.up * scS.up, true);
-  if constexpr (Sm::turns) {
-    __syncthreads();
-    put_state(sb + Sm::s1, dS + item * a.V * a.K, scT.down);
-    __syncthreads();
-  }
+  __syncthreads();
+  put_state(sb + Sm::st, dS + item * a.V * a.K, scT.down);
+  __syncthreads();
   zero();
   for (int kb = 0; kb < vb; ++kb) {
     uint32_t la[N][4];
 #pragma unroll
     for (int n = 0; n < N; ++n) left_cols<kDC, N>(la[n], sb + Sm::u, mb, kb, n, lane);
-    step(sb + Sm::s1, kb, la);
+    step(sb + Sm::st, kb, la);
   }
   add(Kg, vec[kDC + ta] * scU.up * scT.up, vec[kDC + tb] * scU.up * scT.up, false);
-  if constexpr (Sm::turns) {
-    __syncthreads();
-    tile_load<T, KP>(sb + Sm::k, k, a.ldk, valid, a.K, tid, kGradThreads);
-    tile_load<T, KP>(sb + Sm::q, q, a.ldq, valid, a.K, tid, kGradThreads);
-    cp_commit();
-    cp_wait<0>();
-    __syncthreads();
-    tile_scale<T, KP>(sb + Sm::k, up, tid, kGradThreads);
-    tile_scale<T, KP>(sb + Sm::q, up + kDC, tid, kGradThreads);
-    __syncthreads();
-  }
+  __syncthreads();
+  tile_load<float, KP>(sb + Sm::k, k, a.ldk, valid, a.K, tid, kGradThreads);
+  tile_load<float, KP>(sb + Sm::q, q, a.ldq, valid, a.K, tid, kGradThreads);
+  cp_commit();
+  cp_wait<0>();
+  __syncthreads();
+  tile_scale<KP>(sb + Sm::k, up, tid, kGradThreads);
+  tile_scale<KP>(sb + Sm::q, up + kDC, tid, kGradThreads);
+  __syncthreads();
   zero();
 #pragma unroll
   for (int kb = 0; kb < 4; ++kb) {
@@ -809,8 +776,9 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
     for (int j = 0; j < NC; ++j) {
       const int c = half * (KP / 2) + 8 * j + t2;
       if (c >= a.K) continue;
-      ActT<TO>::st2(dqb + (long long)t * ldg + c, t < valid ? Q[j][e] : 0.f, t < valid ? Q[j][e + 1] : 0.f);
-      ActT<TO>::st2(dkb + (long long)t * ldg + c, t < valid ? Kg[j][e] * f : 0.f, t < valid ? Kg[j][e + 1] * f : 0.f);
+      const bool on = t < valid;
+      *reinterpret_cast<float2*>(dqb + (long long)t * ldg + c) = on ? make_float2(Q[j][e], Q[j][e + 1]) : make_float2(0.f, 0.f);
+      *reinterpret_cast<float2*>(dkb + (long long)t * ldg + c) = on ? make_float2(Kg[j][e] * f, Kg[j][e + 1] * f) : make_float2(0.f, 0.f);
     }
   }
 }
@@ -863,17 +831,17 @@ struct BwdArgs {
   float *dg, *dbeta, *dh0, *dS, *du, *pq, *pk;
 };
 
-template <typename T, int KP>
+template <int KP>
 int chain(const BwdPlan& pl, const BwdArgs& x, cudaStream_t s) {
-  using St = BackStage<T, KP>;
+  using St = BackStage<KP>;
   const LinAttn& a = pl.p.a;
   const long long bh = (long long)a.B * a.H;
   int warps = (a.V + 15) / 16;
   while (warps > 1 && bh * ((a.V + 16 * warps - 1) / (16 * warps)) < 100) warps = (warps + 1) / 2;
   const int nvt = (a.V + 16 * warps - 1) / (16 * warps);
   const int sb = St::bytes(warps), stages = 2 * sb <= 227 * 1024 ? 2 : 1;
-  return lin_launch(delta_bwd_kernel<T, KP>, (unsigned)(bh * nvt), 32 * warps, (size_t)sb * stages, s, pl.p, static_cast<const T*>(x.dout), x.dh_last,
-                    static_cast<T*>(x.dv), x.dS, x.du, x.dh0, stages, sb);
+  return lin_launch(delta_bwd_kernel<KP>, (unsigned)(bh * nvt), 32 * warps, (size_t)sb * stages, s, pl.p, static_cast<const float*>(x.dout),
+                    x.dh_last, static_cast<float*>(x.dv), x.dS, x.du, x.dh0, stages, sb);
 }
 
 // a group's dq and dk from its heads' parts
@@ -890,17 +858,17 @@ template <int KP, int VP>
 int grads(const BwdPlan& pl, const BwdArgs& x, cudaStream_t s) {
   const LinAttn& a = pl.p.a;
   const unsigned grid = (unsigned)((long long)a.B * a.H * a.nck);
-  constexpr size_t smem = GradSmem<float, KP, VP>::bytes;
+  constexpr size_t smem = GradSmem<KP, VP>::bytes;
   static_assert(smem <= 227 * 1024, "a chunk's tiles fit shared memory");
   const bool parts = a.H > a.G;
-  const int rc = lin_launch(delta_grad_kernel<float, float, KP, VP>, grid, kGradThreads, smem, s, pl.p, x.ckpt, static_cast<const float*>(x.dout), x.dS, x.du,
+  const int rc = lin_launch(delta_grad_kernel<KP, VP>, grid, kGradThreads, smem, s, pl.p, x.ckpt, static_cast<const float*>(x.dout), x.dS, x.du,
                             parts ? x.pq : static_cast<float*>(x.dq), parts ? x.pk : static_cast<float*>(x.dk), parts ? a.H : a.G, x.dg, x.dbeta);
   return rc != SS_OK || !parts ? rc : share<float>(pl, x, s);
 }
 
 template <int KP>
 int run(const BwdPlan& pl, const BwdArgs& x, cudaStream_t s) {
-  const int rc = chain<float, KP>(pl, x, s);
+  const int rc = chain<KP>(pl, x, s);
   if (rc != SS_OK) return rc;
   return pl.p.a.V <= 64 ? grads<KP, 64>(pl, x, s) : grads<KP, 128>(pl, x, s);
 }

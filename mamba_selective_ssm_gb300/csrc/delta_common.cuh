@@ -10,10 +10,11 @@
 // M and P depend on no state: delta_prep_kernel finds them for all chunks at once.  What passes from chunk to chunk is a
 // chain of three products (K S0, M (beta R), K^T u), and every column of V is a chain of its own.
 //
-// Products run on the tensor cores in fp16 with fp32 sums.  Whatever ends in fp32 takes its fp32 operands as two fp16
-// terms (22 bits), scaled by a power of two to the range of fp16; k and q are scaled token by token:
+// fp32 inputs (this file's tiles and products; bf16 ones: delta_tc.cuh): products run on the tensor cores in fp16 with fp32
+// sums, every operand as two fp16 terms (22 bits) scaled by a power of two to the range of fp16; k and q are scaled token by
+// token:
 //   k'_t = 2^{-e_t} k_t (largest element in [1, 2)),   beta' = 4^{e} beta,   v' = 2^{-e} v,   r' = 2^{-e} r,   u' = 2^{e} u
-// leaves every formula above as it is, so that bf16 keys and queries are one exact fp16 term (fp32 ones are two).
+// leaves every formula above as it is.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -135,21 +136,16 @@ __device__ __forceinline__ void store_terms(uint32_t hi_at, uint32_t lo_at, cons
   sts128(lo_at, l);
 }
 
-// Raw rows become scaled fp16 operands in place; up[r] = the row's 2^e.  W / 8 neighbouring lanes hold a row.
-template <typename T, int W>
+// Raw fp32 rows become scaled fp16 operands in place; up[r] = the row's 2^e.  W / 8 neighbouring lanes hold a row.
+template <int W>
 __device__ __forceinline__ void tile_scale(uint32_t tile, float* up, int tid, int nt) {
-  constexpr int N = kTerms<T>, U = W / 8;
+  constexpr int U = W / 8;
   for (int i = tid; i < kDC * U; i += nt) {  // nt and kDC * U are multiples of 32: whole warps
     const int r = i / U, u = i % U;
-    const uint32_t a0 = tile + DTile<W, N>::at(r, u, 0), a1 = tile + DTile<W, N>::at(r, u, N - 1);
-    float x[8];
-    if constexpr (N == 1) {
-      Raw8<__nv_bfloat16>::wide(lds128(a0), x);
-    } else {
-      const uint4 p = lds128(a0), q = lds128(a1);
-      x[0] = __uint_as_float(p.x); x[1] = __uint_as_float(p.y); x[2] = __uint_as_float(p.z); x[3] = __uint_as_float(p.w);
-      x[4] = __uint_as_float(q.x); x[5] = __uint_as_float(q.y); x[6] = __uint_as_float(q.z); x[7] = __uint_as_float(q.w);
-    }
+    const uint32_t a0 = tile + DTile<W, 2>::at(r, u, 0), a1 = tile + DTile<W, 2>::at(r, u, 1);
+    const uint4 p = lds128(a0), q = lds128(a1);
+    float x[8] = {__uint_as_float(p.x), __uint_as_float(p.y), __uint_as_float(p.z), __uint_as_float(p.w),
+                  __uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z), __uint_as_float(q.w)};
     float m = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
@@ -158,11 +154,7 @@ __device__ __forceinline__ void tile_scale(uint32_t tile, float* up, int tid, in
     const Pow2 s = token_scale(m);
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] *= s.down;
-    if constexpr (N == 1) {
-      sts128(a0, make_uint4(pack_half(x[0], x[1]), pack_half(x[2], x[3]), pack_half(x[4], x[5]), pack_half(x[6], x[7])));
-    } else {
-      store_terms(a0, a1, x);
-    }
+    store_terms(a0, a1, x);
     if (u == 0) up[r] = s.up;
   }
 }
@@ -183,11 +175,6 @@ __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t at) {
 __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
-}
-__device__ __forceinline__ uint32_t trans8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
 }
 
 // Right operands from a tile, for two neighbouring column tiles of 8: b[0], b[1] of the first, b[2], b[3] of the second.
@@ -242,54 +229,20 @@ __device__ __forceinline__ void left_terms(uint32_t (&h)[4], uint32_t (&l)[4], c
   split_half(y[0] * s.r[0].down, y[1] * s.r[0].down, h[2], l[2]);
   split_half(y[2] * s.r[1].down, y[3] * s.r[1].down, h[3], l[3]);
 }
-__device__ __forceinline__ void left_first(uint32_t (&h)[4], const float (&x)[4], const float (&y)[4], const RowScale& s) {
-  h[0] = pack_half(x[0] * s.r[0].down, x[1] * s.r[0].down);
-  h[1] = pack_half(x[2] * s.r[1].down, x[3] * s.r[1].down);
-  h[2] = pack_half(y[0] * s.r[0].down, y[1] * s.r[0].down);
-  h[3] = pack_half(y[2] * s.r[1].down, y[3] * s.r[1].down);
-}
 
-// c0, c1 += (h + l) B over one step of 16, B of N terms at b (and bl); the lowest terms' product is dropped (2^-22)
-template <int N>
+// c0, c1 += (h + l) (b + bl) over one step of 16; the lowest terms' product is dropped (2^-22)
 __device__ __forceinline__ void mma_terms(float (&c0)[4], float (&c1)[4], const uint32_t (&h)[4], const uint32_t (&l)[4], const uint32_t (&b)[4],
                                           const uint32_t (&bl)[4]) {
   mma_f16(c0, l, b[0], b[1]);
   mma_f16(c1, l, b[2], b[3]);
-  if constexpr (N == 2) {
-    mma_f16(c0, h, bl[0], bl[1]);
-    mma_f16(c1, h, bl[2], bl[3]);
-  }
+  mma_f16(c0, h, bl[0], bl[1]);
+  mma_f16(c1, h, bl[2], bl[3]);
   mma_f16(c0, h, b[0], b[1]);
   mma_f16(c1, h, b[2], b[3]);
 }
 
-// A warp's own 16 columns of V of a chunk (v or do), as it lies in memory: bf16 rows of 32 bytes, the two halves swapped in
-// every second group of four rows (banks); fp32 rows of 80 bytes.
-template <typename T>
-struct DSlice;
-template <>
-struct DSlice<__nv_bfloat16> {
-  static constexpr int bytes = kDC * 32;
-  __device__ __forceinline__ static uint32_t at(int t, int u) { return (uint32_t)(t * 32 + ((u ^ ((t >> 2) & 1)) << 4)); }
-  __device__ __forceinline__ static void load(uint32_t s, const __nv_bfloat16* __restrict__ src, long long ld, int valid, int width, int lane) {
-#pragma unroll
-    for (int i = lane; i < kDC * 2; i += 32) {
-      const int t = i >> 1, u = i & 1;
-      const bool on = t < valid && u * 8 < width;
-      cp16(s + at(t, u), src + (on ? (long long)t * ld + u * 8 : 0), on);
-    }
-  }
-  // tokens of column tiles 2 p and 2 p + 1 in the order of accumulators whose rows are the slice's columns
-  __device__ __forceinline__ static void read(uint32_t s, int p, int lane, float (&x)[4], float (&y)[4]) {
-    const int mi = lane >> 3;
-    uint32_t r[4];
-    ldsm_t(r, s + at(16 * p + (mi >> 1) * 8 + (lane & 7), mi & 1));
-    x[0] = bf16_lo(r[0]); x[1] = bf16_hi(r[0]); x[2] = bf16_lo(r[1]); x[3] = bf16_hi(r[1]);
-    y[0] = bf16_lo(r[2]); y[1] = bf16_hi(r[2]); y[2] = bf16_lo(r[3]); y[3] = bf16_hi(r[3]);
-  }
-};
-template <>
-struct DSlice<float> {
+// A warp's own 16 columns of V of a chunk of fp32 (v or do), rows of 80 bytes (banks)
+struct DSlice {
   static constexpr int bytes = kDC * 80;
   __device__ __forceinline__ static void load(uint32_t s, const float* __restrict__ src, long long ld, int valid, int width, int lane) {
 #pragma unroll
@@ -315,14 +268,6 @@ struct DSlice<float> {
 };
 
 // Accumulators (rows = 16 columns of V from v0, columns = 8 tokens from t) to rows of a [.., ld] array
-__device__ __forceinline__ void store_tokens(__nv_bfloat16* __restrict__ dst, long long ld, int t, int rows, int width, const float (&x)[4], int lane) {
-  const uint32_t a = trans8(ActT<__nv_bfloat16>::pack2(x[0], x[1])), b = trans8(ActT<__nv_bfloat16>::pack2(x[2], x[3]));
-  const int r = t + (lane >> 2), c = 2 * (lane & 3);
-  if (r < rows) {
-    if (c < width) *reinterpret_cast<uint32_t*>(dst + (long long)r * ld + c) = a;
-    if (8 + c < width) *reinterpret_cast<uint32_t*>(dst + (long long)r * ld + 8 + c) = b;
-  }
-}
 __device__ __forceinline__ void store_tokens(float* __restrict__ dst, long long ld, int t, int rows, int width, const float (&x)[4], int lane) {
   const int g = lane >> 2, r = t + 2 * (lane & 3);
 #pragma unroll

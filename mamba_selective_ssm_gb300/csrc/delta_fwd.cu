@@ -1,4 +1,4 @@
-// The gated delta rule, chunked forward (deltarule_fwd) for sm_103a.
+// The gated delta rule, chunked forward (deltarule_fwd) for sm_103a: its plan, and the chain for fp32 (bf16: delta_fwd_tc.cu).
 #include <stddef.h>
 
 #include "delta_common.cuh"
@@ -10,22 +10,21 @@ using namespace ssk;
 // A warp walks the chunks of one (batch row, head) with 16 columns of the state in registers, transposed: rows are columns
 // of V, so that K S0, M (beta R), K^T u and o are products whose left operand is the accumulators of the one before, and the
 // warps of a CTA share nothing but the tiles of the chunk (k, q, M, P).
-template <typename T, int KP>
+template <int KP>
 struct WalkStage {
-  static constexpr int NP = kTerms<T>;  // terms of P: it ends in o only, which has the activations' type
-  static constexpr int k = 0, q = k + DTile<KP, kTerms<T>>::bytes, m = q + DTile<KP, kTerms<T>>::bytes, p = m + kDMBytes,
-                       vec = p + DTile<kDC, NP>::bytes, up = vec + kDVec * 4, slices = up + 2 * kDC * 4;
-  static int bytes(int warps) { return slices + warps * DSlice<T>::bytes; }
+  static constexpr int k = 0, q = k + DTile<KP, 2>::bytes, m = q + DTile<KP, 2>::bytes, p = m + kDMBytes,
+                       vec = p + DTile<kDC, 2>::bytes, up = vec + kDVec * 4, slices = up + 2 * kDC * 4;
+  static int bytes(int warps) { return slices + warps * DSlice::bytes; }
 };
 
 constexpr int kWalkThreads = 256;
 
-template <typename T, int KP>
-__global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const float* __restrict__ h0, T* __restrict__ o,
+template <int KP>
+__global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const float* __restrict__ h0, float* __restrict__ o,
                                                                  float* __restrict__ ckpt, float* __restrict__ h_last, int stages,
                                                                  int stage_bytes) {
-  using St = WalkStage<T, KP>;
-  constexpr int N = kTerms<T>, KT = KP / 8;
+  using St = WalkStage<KP>;
+  constexpr int N = 2, KT = KP / 8;
   extern __shared__ __align__(128) unsigned char raw[];
   const uint32_t sb = smem_u32(raw);
   const LinAttn& a = p.a;
@@ -36,10 +35,10 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
   const int h = (int)(bh % a.H), b = (int)(bh / a.H), gh = h / (a.H / a.G);
   const int v0 = vt * (nt / 2) + warp * 16, vw = a.V - v0;  // (a warp past V walks along with zeros)
   const int len = a.len(b), nck = (len + kDC - 1) / kDC;
-  const T* q = static_cast<const T*>(a.q) + (long long)b * a.L * a.ldq + (long long)gh * a.K;
-  const T* k = static_cast<const T*>(a.k) + (long long)b * a.L * a.ldk + (long long)gh * a.K;
-  const T* v = static_cast<const T*>(a.v) + (long long)b * a.L * a.ldv + (long long)h * a.V + v0;
-  T* ob = o + ((long long)b * a.L * a.H + h) * a.V + v0;
+  const float* q = static_cast<const float*>(a.q) + (long long)b * a.L * a.ldq + (long long)gh * a.K;
+  const float* k = static_cast<const float*>(a.k) + (long long)b * a.L * a.ldk + (long long)gh * a.K;
+  const float* v = static_cast<const float*>(a.v) + (long long)b * a.L * a.ldv + (long long)h * a.V + v0;
+  float* ob = o + ((long long)b * a.L * a.H + h) * a.V + v0;
   const long long ldo = (long long)a.H * a.V;
 
   auto fetch = [&](int ck) {
@@ -47,12 +46,12 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
     const long long t0 = (long long)ck * kDC;
     const int valid = len - (int)t0 < kDC ? len - (int)t0 : kDC;
     const long long item = bh * a.nck + ck;
-    tile_load<T, KP>(at + St::k, k + t0 * a.ldk, a.ldk, valid, a.K, tid, nt);
-    tile_load<T, KP>(at + St::q, q + t0 * a.ldq, a.ldq, valid, a.K, tid, nt);
+    tile_load<float, KP>(at + St::k, k + t0 * a.ldk, a.ldk, valid, a.K, tid, nt);
+    tile_load<float, KP>(at + St::q, q + t0 * a.ldq, a.ldq, valid, a.K, tid, nt);
     tile_copy(at + St::m, p.M + item * kDMBytes, kDMBytes, tid, nt);
-    tile_copy(at + St::p, p.P + item * DTile<kDC, St::NP>::bytes, DTile<kDC, St::NP>::bytes, tid, nt);
+    tile_copy(at + St::p, p.P + item * DTile<kDC, 2>::bytes, DTile<kDC, 2>::bytes, tid, nt);
     tile_copy(at + St::vec, reinterpret_cast<const unsigned char*>(p.vec + item * kDVec), kDVec * 4, tid, nt);
-    DSlice<T>::load(at + St::slices + warp * DSlice<T>::bytes, v + t0 * a.ldv, a.ldv, valid, vw, lane);
+    DSlice::load(at + St::slices + warp * DSlice::bytes, v + t0 * a.ldv, a.ldv, valid, vw, lane);
     cp_commit();
   };
 
@@ -82,8 +81,8 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
     float* up = reinterpret_cast<float*>(raw + off + St::up);
     cp_wait<0>();
     __syncthreads();
-    tile_scale<T, KP>(at + St::k, up, tid, nt);
-    tile_scale<T, KP>(at + St::q, up + kDC, tid, nt);
+    tile_scale<KP>(at + St::k, up, tid, nt);
+    tile_scale<KP>(at + St::q, up + kDC, tid, nt);
     __syncthreads();
     if (stages == 2 && ck + 1 < nck) fetch(ck + 1);  // its place was read in the chunk before
     if (ckpt != nullptr) save(ck);
@@ -103,13 +102,13 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
         uint32_t bb[N][4];
 #pragma unroll
         for (int n = 0; n < N; ++n) right_rows<KP, N>(bb[n], at + St::k, np, kb, n, lane);
-        mma_terms<N>(R[2 * np], R[2 * np + 1], hi, lo, bb[0], bb[N - 1]);
+        mma_terms(R[2 * np], R[2 * np + 1], hi, lo, bb[0], bb[N - 1]);
       }
     }
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
       float x[2][4];
-      DSlice<T>::read(at + St::slices + warp * DSlice<T>::bytes, np, lane, x[0], x[1]);
+      DSlice::read(at + St::slices + warp * DSlice::bytes, np, lane, x[0], x[1]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int n = 2 * np + i, t = 8 * n + t2;
@@ -143,7 +142,7 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
           uint32_t b0[4], b1[4];
           right_rows<kDC, 2>(b0, at + St::m, np, kb, 0, lane);
           right_rows<kDC, 2>(b1, at + St::m, np, kb, 1, lane);
-          mma_terms<2>(c[0], c[1], hi[kb], lo[kb], b0, b1);
+          mma_terms(c[0], c[1], hi[kb], lo[kb], b0, b1);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -165,26 +164,19 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
 #pragma unroll
       for (int kb = 0; kb < KP / 16; ++kb) {
         uint32_t sh[4], sl[4];
-        if constexpr (N == 1) left_first(sh, S[2 * kb], S[2 * kb + 1], ss);
-        else left_terms(sh, sl, S[2 * kb], S[2 * kb + 1], ss);
+        left_terms(sh, sl, S[2 * kb], S[2 * kb + 1], ss);
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
           uint32_t bb[N][4];
 #pragma unroll
           for (int n = 0; n < N; ++n) right_rows<KP, N>(bb[n], at + St::q, np, kb, n, lane);
-          if constexpr (N == 1) {
-            mma_f16(O[2 * np], sh, bb[0][0], bb[0][1]);
-            mma_f16(O[2 * np + 1], sh, bb[0][2], bb[0][3]);
-          } else {
-            mma_terms<N>(O[2 * np], O[2 * np + 1], sh, sl, bb[0], bb[N - 1]);
-          }
+          mma_terms(O[2 * np], O[2 * np + 1], sh, sl, bb[0], bb[N - 1]);
         }
       }
       const RowScale us = row_scale(R);
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb) {
-        if constexpr (N == 1) left_first(hi[kb], R[2 * kb], R[2 * kb + 1], us);
-        else left_terms(hi[kb], lo[kb], R[2 * kb], R[2 * kb + 1], us);
+        left_terms(hi[kb], lo[kb], R[2 * kb], R[2 * kb + 1], us);
       }
       const int t0 = ck * kDC, rows = a.L - t0 < kDC ? a.L - t0 : kDC;
 #pragma unroll
@@ -195,12 +187,7 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
           uint32_t bb[N][4];
 #pragma unroll
           for (int n = 0; n < N; ++n) right_rows<kDC, N>(bb[n], at + St::p, np, kb, n, lane);
-          if constexpr (N == 1) {
-            mma_f16(c[0], hi[kb], bb[0][0], bb[0][1]);
-            mma_f16(c[1], hi[kb], bb[0][2], bb[0][3]);
-          } else {
-            mma_terms<N>(c[0], c[1], hi[kb], lo[kb], bb[0], bb[N - 1]);
-          }
+          mma_terms(c[0], c[1], hi[kb], lo[kb], bb[0], bb[N - 1]);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -238,7 +225,7 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
           uint32_t bb[N][4];
 #pragma unroll
           for (int n = 0; n < N; ++n) right_cols<KP, N>(bb[n], at + St::k, jp, kb, n, lane);
-          mma_terms<N>(c[0], c[1], hi[kb], lo[kb], bb[0], bb[N - 1]);
+          mma_terms(c[0], c[1], hi[kb], lo[kb], bb[0], bb[N - 1]);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -268,7 +255,7 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
   // tokens of chunks past the row's end
   const int w = vw < 16 ? vw : 16;
   for (long long i = (long long)nck * kDC * 16 + lane; i < (long long)a.L * 16; i += 32)
-    if ((int)(i & 15) < w) ActT<T>::st1(ob + (i >> 4) * ldo + (i & 15), 0.f);
+    if ((int)(i & 15) < w) ob[(i >> 4) * ldo + (i & 15)] = 0.f;
 }
 
 struct FwdPlan {
@@ -291,16 +278,16 @@ int fwd_plan(int B, int L, int H, int G, int K, int V, int dtype, FwdPlan& pl) {
   return SS_OK;
 }
 
-template <typename T, int KP>
+template <int KP>
 int walk(const FwdPlan& pl, const float* h0, void* o, float* ckpt, float* h_last, cudaStream_t s) {
-  using St = WalkStage<T, KP>;
+  using St = WalkStage<KP>;
   const LinAttn& a = pl.p.a;
   const long long bh = (long long)a.B * a.H;
   int warps = (a.V + 15) / 16;
   while (warps > 1 && bh * ((a.V + 16 * warps - 1) / (16 * warps)) < 100) warps = (warps + 1) / 2;
   const int nvt = (a.V + 16 * warps - 1) / (16 * warps);
   const int sb = St::bytes(warps), stages = 2 * sb <= 227 * 1024 ? 2 : 1;
-  return lin_launch(delta_fwd_kernel<T, KP>, (unsigned)(bh * nvt), 32 * warps, (size_t)sb * stages, s, pl.p, h0, static_cast<T*>(o), ckpt, h_last,
+  return lin_launch(delta_fwd_kernel<KP>, (unsigned)(bh * nvt), 32 * warps, (size_t)sb * stages, s, pl.p, h0, static_cast<float*>(o), ckpt, h_last,
                     stages, sb);
 }
 
@@ -344,6 +331,6 @@ extern "C" int deltarule_fwd(const void* q, long long ldq, const void* k, long l
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == SS_BF16 && ckpt == nullptr) pl.p.pterms = 2;  // (o alone)
   if ((rc = ssh::delta_prep(pl.p, dtype, s)) != SS_OK) return rc;
-  if (dtype == SS_F32) return K <= 64 ? walk<float, 64>(pl, h0, o, ckpt, h_last, s) : walk<float, 128>(pl, h0, o, ckpt, h_last, s);
+  if (dtype == SS_F32) return K <= 64 ? walk<64>(pl, h0, o, ckpt, h_last, s) : walk<128>(pl, h0, o, ckpt, h_last, s);
   return ssh::delta_fwd_bf16(pl.p, h0, o, ckpt, h_last, s);
 }

@@ -19,7 +19,8 @@ template <int KP, bool TRAIN>
 struct DeltaTc {
   static constexpr int UT = TRAIN ? 3 : 2;  // terms of u and P: o's own rounding needs two, its sum with do in dg three
   static constexpr int NKP = KP / 64;  // panels of K
-  static constexpr int kq = 0, place = NKP * kPanel, v = kq + 2 * place, m = v + 2 * kTok, p = m + 3 * kDTerm, u = p + UT * kDTerm, vec = u + UT * kPanel, bar = vec + 2 * kDVec * 4;
+  static constexpr int kq = 0, place = NKP * kPanel, v = kq + 2 * place, m = v + 2 * kTok, p = m + 3 * kDTerm,
+                       u = p + UT * kDTerm, vec = u + UT * kPanel, bar = vec + 2 * kDVec * 4;
   // barriers: k and q (two), v, scalars (two), M, P landed; S, w / weighted u, u stored, o staged; products done
   static constexpr int kK = 0, kV = 2, kX = 3, kMr = 5, kPr = 6, kS = 7, kW = 8, kU = 9, kO = 10, kD1 = 11, kD3 = 12, kD4 = 13, kD5 = 14,
                        nbar = 15;
@@ -416,7 +417,8 @@ int walk(const Delta& p, const float* h0, __nv_bfloat16* o, float* ckpt, float* 
   if (!delta_map(&maps.q, a.q, a.ldq, a.B, a.L, a.G, a.K) || !delta_map(&maps.k, a.k, a.ldk, a.B, a.L, a.G, a.K) ||
       !delta_map(&maps.v, a.v, a.ldv, a.B, a.L, a.H, a.V) || !delta_map(&maps.o, o, (long long)a.H * a.V, a.B, a.L, a.H, a.V))
     return SS_ERR_CUDA;
-  return lin_launch(delta_fwd_tc_kernel<KP, TRAIN>, (unsigned)((long long)a.B * a.H), kDThreads, DeltaTc<KP, TRAIN>::bytes, s, p, maps, h0, o, ckpt, h_last);
+  return lin_launch(delta_fwd_tc_kernel<KP, TRAIN>, (unsigned)((long long)a.B * a.H), kDThreads, DeltaTc<KP, TRAIN>::bytes, s, p, maps, h0, o,
+                    ckpt, h_last);
 }
 
 }  // namespace

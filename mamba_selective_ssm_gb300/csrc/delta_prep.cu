@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(Delta p) {
   cp_wait<0>();
   __syncthreads();
   if constexpr (N == 2) {
-    tile_scale<T, KP>(sb + S::k, kup, tid, kPrepThreads);
-    tile_scale<T, KP>(sb + S::q, qup, tid, kPrepThreads);
+    tile_scale<KP>(sb + S::k, kup, tid, kPrepThreads);
+    tile_scale<KP>(sb + S::q, qup, tid, kPrepThreads);
     __syncthreads();
   }
   float* vec = p.vec + item * kDVec;
@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(Delta p) {
         mma_bf16(qk[0], qa[0], bb[0][0], bb[0][1]);
         mma_bf16(qk[1], qa[0], bb[0][2], bb[0][3]);
       } else {
-        mma_terms<2>(kk[2 * np], kk[2 * np + 1], ka[0], ka[N - 1], bb[0], bb[N - 1]);
-        mma_terms<2>(qk[0], qk[1], qa[0], qa[N - 1], bb[0], bb[N - 1]);
+        mma_terms(kk[2 * np], kk[2 * np + 1], ka[0], ka[N - 1], bb[0], bb[N - 1]);
+        mma_terms(qk[0], qk[1], qa[0], qa[N - 1], bb[0], bb[N - 1]);
       }
     }
 #pragma unroll

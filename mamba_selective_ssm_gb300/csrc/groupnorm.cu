@@ -826,7 +826,8 @@ int fwd(const GnPlan& pl, const T* x, const float* scale, const float* bias, T* 
     GN_LANES(fwd_lanes, pl, x, scale, bias, y, mean, rstd, s)
   } else if (pl.form == kSample) {
     const size_t smem = (gn_part_floats(p) + 2 * p.groups) * sizeof(float);
-    if (cudaFuncSetAttribute(gn_fwd_sample_kernel<T, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SS_ERR_CUDA;
+    if (cudaFuncSetAttribute(gn_fwd_sample_kernel<T, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      return SS_ERR_CUDA;
     gn_fwd_sample_kernel<T, SILU><<<pl.grid, kGnThreads, smem, s>>>(p, x, scale, bias, y, mean, rstd);
   } else {
     const Part& q = pl.q;
@@ -838,7 +839,8 @@ int fwd(const GnPlan& pl, const T* x, const float* scale, const float* bias, T* 
     gn_stats_kernel<T><<<grid, kGnThreads, 0, s>>>(p, q, x, part);
     if (launch_dependent(gn_join_kernel, dim3((unsigned)((long long)p.N * p.groups)), dim3(kGnThreads), 0, s, p, q, (const float*)part, mu, rv) !=
             cudaSuccess ||
-        launch_dependent(gn_apply_kernel<T, SILU>, dim3((unsigned)((long long)p.N * pl.qa.splits * q.tiles)), dim3(kGnThreads), 0, s, p, pl.qa, x, scale, bias, (const float*)mu, (const float*)rv, y) !=
+        launch_dependent(gn_apply_kernel<T, SILU>, dim3((unsigned)((long long)p.N * pl.qa.splits * q.tiles)), dim3(kGnThreads), 0, s, p, pl.qa, x,
+                         scale, bias, (const float*)mu, (const float*)rv, y) !=
             cudaSuccess)
       return SS_ERR_CUDA;
   }
@@ -864,7 +866,8 @@ int bwd(const GnPlan& pl, const T* dy, const T* x, const float* scale, const flo
     GN_LANES(bwd_lanes, pl, dy, x, scale, bias, mean, rstd, dx, part, s)
   } else if (pl.form == kSample) {
     const size_t smem = (gn_part_floats(p) + 2 * p.C + 2 * p.groups) * sizeof(float);
-    if (cudaFuncSetAttribute(gn_bwd_sample_kernel<T, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SS_ERR_CUDA;
+    if (cudaFuncSetAttribute(gn_bwd_sample_kernel<T, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      return SS_ERR_CUDA;
     gn_bwd_sample_kernel<T, SILU><<<pl.grid, kGnThreads, smem, s>>>(p, dy, x, scale, bias, mean, rstd, dx, part);
   } else {
     const Part& q = pl.q;
