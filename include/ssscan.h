@@ -458,32 +458,35 @@ int linattn_step(const void* q, const void* k, const void* v, const float* g, in
  *   beta : [B, L, H] fp32.  The state stays bounded for 0 <= beta_t |k_t|^2 <= 2;
  *          keys are normally of length one (rmsnorm_fwd over the rows of k with
  *          scale K^-1/2 makes them so).  Elements of k and q of 2^60 and more
- *          come out as infinities; those of a token below 2^-24 of its largest
- *          lose bits.
+ *          come out as infinities with fp32 activations; those of a token below
+ *          2^-24 of its largest lose bits there.
  *   B * H at most 2^24, and B * H * ceil(L / 64) below 2^28.
  * The sequence is worked through in chunks of 64 tokens; a NaN or infinity in a
  * live token can reach the other tokens of its chunk, earlier ones among them,
  * and in the backward all tokens of its row.
- * Rounding.  All sums and states are fp32.  Products run in fp16 with fp32
- * sums: what ends in fp32 (states, dg, dbeta, dh0, and with fp32 activations
- * every output) takes fp32 operands as two scaled fp16 terms (22 bits); with
- * bf16 activations the operands of o, dq and dk are one term (11 bits), well
- * inside the rounding of the output itself.
+ * Rounding.  All sums and states are fp32.  Products run in 16 bits with fp32
+ * sums.  With bf16 activations these are operands as they are, and an fp32
+ * operand is three bf16 terms (all its 24 bits) where the result ends in fp32
+ * (states, dg, dbeta, dh0, the states' way into o), two (2^-15) where it is
+ * rounded to bf16 alone (u in o without ckpt, dq, dk).  With fp32 activations
+ * every operand is two scaled fp16 terms (22 bits).
  * Alignment: 16 bytes for every pointer but g, beta, lengths, dg, dbeta (4).
  *
  * deltarule_ckpt_size — floats that a checkpoint holds for each batch row and
  * head (0 on invalid sizes): the states entering each chunk and the last one,
- * and in bf16 two values for every element of v, which the fp32 gradients need.
+ * two operands of 64 x 64 for each chunk, and in bf16 two values for every
+ * element of v, which the fp32 gradients need.
  */
 size_t deltarule_ckpt_size(int L, int K, int V, int dtype);
 
 /*
  * deltarule_fwd — o [B, L, H, V] (dtype), and where the pointer is given
  *   ckpt   : [B, H, deltarule_ckpt_size(L, K, V, dtype)] fp32, from which
- *            deltarule_bwd starts (its order is the library's own; what lies
- *            past a row's length is not written)
+ *            deltarule_bwd starts (one array, its order is the library's
+ *            own; what lies past a row's length is not written)
  *   h_last : [B, H, K, V] fp32, the state after the row's last token
- * h0 may be NULL (zeros).  workspace: deltarule_fwd_workspace_size() bytes.
+ * h0 may be NULL (zeros).  workspace: deltarule_fwd_workspace_size() bytes; with
+ * ckpt it is not used and may be NULL.
  */
 size_t deltarule_fwd_workspace_size(int B, int L, int H, int G, int K, int V, int dtype);
 int deltarule_fwd(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv,

@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(256) delta_share_kernel(const float* __restric
 
 struct BwdPlan {
   Delta p;
-  size_t m, pp, vec, ds, du, part, bytes;
+  size_t ds, du, part, bytes;
 };
 
 int bwd_plan(int B, int L, int H, int G, int K, int V, int dtype, BwdPlan& pl) {
@@ -813,14 +813,11 @@ int bwd_plan(int B, int L, int H, int G, int K, int V, int dtype, BwdPlan& pl) {
   a.B = B; a.L = L; a.H = H; a.G = G; a.K = K; a.V = V;
   a.nck = (L + kDC - 1) / kDC;
   pl.p.pterms = dtype == SS_F32 ? 2 : 3;
-  const size_t items = (size_t)B * H * a.nck;
-  pl.m = items * (dtype == SS_F32 ? kDMBytes : kDMTerms);
-  pl.pp = items * (kDC * kDC * 2) * pl.p.pterms;
-  pl.vec = items * kDVec * sizeof(float);
+  const size_t items = pl.p.items();
   pl.ds = items * K * V * sizeof(float);
   pl.du = items * kDC * V * sizeof(float);
   pl.part = H > G ? (size_t)B * L * H * K * sizeof(float) : 0;
-  pl.bytes = pl.m + pl.pp + pl.vec + pl.ds + pl.du + 2 * pl.part;
+  pl.bytes = pl.ds + pl.du + 2 * pl.part;
   return SS_OK;
 }
 
@@ -915,15 +912,12 @@ extern "C" int deltarule_bwd(const void* q, long long ldq, const void* k, long l
   pl.p.beta = beta;
   char* w = static_cast<char*>(workspace);
   BwdArgs x{ckpt, dh_last, dout, dq, dk, dv, g ? dg : nullptr, dbeta, dh0, nullptr, nullptr, nullptr, nullptr};
-  pl.p.M = reinterpret_cast<unsigned char*>(w);
-  pl.p.P = reinterpret_cast<unsigned char*>(w += pl.m);
-  pl.p.vec = reinterpret_cast<float*>(w += pl.pp);
-  x.dS = reinterpret_cast<float*>(w += pl.vec);
+  pl.p.place(const_cast<float*>(ckpt) + (long long)B * H * delta_ckpt_floats(a.nck, K, V, dtype == SS_BF16), dtype == SS_BF16);  // (only read)
+  x.dS = reinterpret_cast<float*>(w);
   x.du = reinterpret_cast<float*>(w += pl.ds);
   x.pq = reinterpret_cast<float*>(w += pl.du);
   x.pk = reinterpret_cast<float*>(w += pl.part);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((rc = ssh::delta_prep(pl.p, dtype, s)) != SS_OK) return rc;
   if (dtype == SS_BF16) return run_bf16(pl, x, s);
   return K <= 64 ? run<64>(pl, x, s) : run<128>(pl, x, s);
 }

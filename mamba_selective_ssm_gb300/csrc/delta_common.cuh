@@ -36,13 +36,25 @@ struct Delta {
   unsigned char *M, *P;  // operand tiles
   float* vec;
   int pterms;  // terms of P
+
+  // the room they take, in bytes, and their places in it
+  size_t prep_bytes(bool bf16) const { return items() * (m_bytes(bf16) + (size_t)kDC * kDC * 2 * pterms + kDVec * sizeof(float)); }
+  void place(void* at, bool bf16) {
+    M = static_cast<unsigned char*>(at);
+    P = M + items() * m_bytes(bf16);
+    vec = reinterpret_cast<float*>(P + items() * ((size_t)kDC * kDC * 2 * pterms));
+  }
+  size_t items() const { return (size_t)a.B * a.H * a.nck; }
+  static size_t m_bytes(bool bf16) { return bf16 ? kDMTerms : kDMBytes; }
 };
 
 template <typename T>
 constexpr int kTerms = sizeof(T) == 4 ? 2 : 1;  // fp16 terms of an activation
 
 // What the forward leaves for the backward, floats of one (batch row, head): the state entering each chunk and the last one;
-// in bf16 also r and o of every chunk in fp32 ([16][V][4]: four tokens of a column together), which dg and dbeta need.
+// in bf16 also r and o of every chunk in fp32 ([16][V][4]: four tokens of a column together), which dg and dbeta need.  Behind
+// all heads' lie M, P and the scalars of all chunks, so that the backward need not find them again (78 of 420 us of its kernels
+// before the gradients at 4 x 2048 tokens of 32 heads of 128 x 128).
 __host__ __device__ inline long long delta_ckpt_floats(int nck, int K, int V, bool bf16) {
   return (long long)(nck + 1) * K * V + (bf16 ? 2ll * nck * kDC * V : 0);
 }

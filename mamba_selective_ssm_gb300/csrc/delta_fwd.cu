@@ -260,21 +260,18 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
 
 struct FwdPlan {
   Delta p;
-  size_t m, pp, bytes;
+  size_t bytes;
 };
 
-int fwd_plan(int B, int L, int H, int G, int K, int V, int dtype, FwdPlan& pl) {
+int fwd_plan(int B, int L, int H, int G, int K, int V, int dtype, bool train, FwdPlan& pl) {
   const int rc = delta_validate(B, L, H, G, K, V, dtype);
   if (rc != SS_OK) return rc;
   pl.p = Delta{};
   LinAttn& a = pl.p.a;
   a.B = B; a.L = L; a.H = H; a.G = G; a.K = K; a.V = V;
   a.nck = (L + kDC - 1) / kDC;
-  pl.p.pterms = dtype == SS_F32 ? 2 : 3;
-  const size_t items = (size_t)B * H * a.nck;
-  pl.m = items * (dtype == SS_F32 ? kDMBytes : kDMTerms);
-  pl.pp = items * (kDC * kDC * 2) * pl.p.pterms;
-  pl.bytes = pl.m + pl.pp + items * kDVec * sizeof(float);
+  pl.p.pterms = dtype == SS_BF16 && train ? 3 : 2;  // (two for o alone)
+  pl.bytes = pl.p.prep_bytes(dtype == SS_BF16);
   return SS_OK;
 }
 
@@ -294,12 +291,14 @@ int walk(const FwdPlan& pl, const float* h0, void* o, float* ckpt, float* h_last
 }  // namespace
 
 extern "C" size_t deltarule_ckpt_size(int L, int K, int V, int dtype) {
-  return delta_validate(1, L, 1, 1, K, V, dtype) == SS_OK ? (size_t)delta_ckpt_floats((L + kDC - 1) / kDC, K, V, dtype == SS_BF16) : 0;
+  FwdPlan pl;
+  if (fwd_plan(1, L, 1, 1, K, V, dtype, true, pl) != SS_OK) return 0;
+  return (size_t)delta_ckpt_floats(pl.p.a.nck, K, V, dtype == SS_BF16) + pl.bytes / sizeof(float);
 }
 
 extern "C" size_t deltarule_fwd_workspace_size(int B, int L, int H, int G, int K, int V, int dtype) {
   FwdPlan pl;
-  return fwd_plan(B, L, H, G, K, V, dtype, pl) == SS_OK ? pl.bytes : 0;
+  return fwd_plan(B, L, H, G, K, V, dtype, false, pl) == SS_OK ? pl.bytes : 0;
 }
 
 extern "C" int deltarule_fwd(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv, const float* g,
@@ -307,7 +306,7 @@ extern "C" int deltarule_fwd(const void* q, long long ldq, const void* k, long l
                              int H, int G, int K, int V, float scale, int dtype, void* workspace, size_t ws_bytes, void* stream) {
   if (!q || !k || !v || !beta || !o) return SS_ERR_NULL;
   FwdPlan pl;
-  int rc = fwd_plan(B, L, H, G, K, V, dtype, pl);
+  int rc = fwd_plan(B, L, H, G, K, V, dtype, ckpt != nullptr, pl);
   if (rc != SS_OK) return rc;
   if ((rc = linattn_ld_ok(ldq, G, K)) != SS_OK || (rc = linattn_ld_ok(ldk, G, K)) != SS_OK || (rc = linattn_ld_ok(ldv, H, V)) != SS_OK)
     return rc;
@@ -316,8 +315,10 @@ extern "C" int deltarule_fwd(const void* q, long long ldq, const void* k, long l
     if (x != nullptr && !ssh::aligned16(x)) return SS_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(g) & 3u) || (reinterpret_cast<uintptr_t>(beta) & 3u) || (reinterpret_cast<uintptr_t>(lengths) & 3u))
     return SS_ERR_ALIGN;
-  if (workspace == nullptr || ws_bytes < pl.bytes) return SS_ERR_WORKSPACE;
-  if (!ssh::aligned16(workspace)) return SS_ERR_ALIGN;
+  if (ckpt == nullptr) {
+    if (workspace == nullptr || ws_bytes < pl.bytes) return SS_ERR_WORKSPACE;
+    if (!ssh::aligned16(workspace)) return SS_ERR_ALIGN;
+  }
   LinAttn& a = pl.p.a;
   a.q = q; a.k = k; a.v = v;
   a.ldq = ldq; a.ldk = ldk; a.ldv = ldv;
@@ -325,11 +326,8 @@ extern "C" int deltarule_fwd(const void* q, long long ldq, const void* k, long l
   a.lengths = lengths;
   a.scale = scale;
   pl.p.beta = beta;
-  pl.p.M = static_cast<unsigned char*>(workspace);
-  pl.p.P = pl.p.M + pl.m;
-  pl.p.vec = reinterpret_cast<float*>(pl.p.P + pl.pp);
+  pl.p.place(ckpt != nullptr ? ckpt + (long long)B * H * delta_ckpt_floats(a.nck, K, V, dtype == SS_BF16) : workspace, dtype == SS_BF16);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == SS_BF16 && ckpt == nullptr) pl.p.pterms = 2;  // (o alone)
   if ((rc = ssh::delta_prep(pl.p, dtype, s)) != SS_OK) return rc;
   if (dtype == SS_F32) return K <= 64 ? walk<64>(pl, h0, o, ckpt, h_last, s) : walk<128>(pl, h0, o, ckpt, h_last, s);
   return ssh::delta_fwd_bf16(pl.p, h0, o, ckpt, h_last, s);

@@ -588,7 +588,7 @@ def deltarule_fwd(q, k, v, g, beta, h0=None, scale=None, lengths=None, want_ckpt
     o = torch.empty((B, L, H, V), device=dev, dtype=dt)
     ckpt = torch.empty((B, H, marks), device=dev, dtype=f32) if want_ckpt else None
     h_last = torch.empty((B, H, K, V), device=dev, dtype=f32) if want_h_last else None
-    pw, have = _scratch(workspace, need, dev)
+    pw, have = _scratch(workspace, 0 if want_ckpt else need, dev)  # (with ckpt that has the place)
     rc = load().deltarule_fwd(pq, ldq, pk, ldk, pv, ldv, pg, pb, ph, pn, o.data_ptr(), ckpt.data_ptr() if want_ckpt else None,
                               h_last.data_ptr() if want_h_last else None, B, L, H, G, K, V, K ** -0.5 if scale is None else scale,
                               sdt, pw, have, _raw_stream(dev))

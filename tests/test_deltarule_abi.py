@@ -34,9 +34,10 @@ def _sizes(**kw):
 
 def test_ckpt_size(lib):
     from mamba_selective_ssm_gb300 import _capi as c
-    assert lib.deltarule_ckpt_size(64, 32, 40, c.SS_F32) == 2 * 32 * 40  # the state entering the chunk and the last
-    assert lib.deltarule_ckpt_size(65, 32, 40, c.SS_F32) == 3 * 32 * 40
-    assert lib.deltarule_ckpt_size(65, 32, 40, c.SS_BF16) == 3 * 32 * 40 + 2 * 128 * 40
+    mp32, mp16 = 2 * 64 * 64 + 272, 3 * 64 * 64 + 272  # a chunk's two 64 x 64 operands and scalars
+    assert lib.deltarule_ckpt_size(64, 32, 40, c.SS_F32) == 2 * 32 * 40 + mp32  # the state entering the chunk and the last
+    assert lib.deltarule_ckpt_size(65, 32, 40, c.SS_F32) == 3 * 32 * 40 + 2 * mp32
+    assert lib.deltarule_ckpt_size(65, 32, 40, c.SS_BF16) == 3 * 32 * 40 + 2 * 128 * 40 + 2 * mp16
     for bad in ((0, 32, 40, 0), (64, 30, 40, 0), (64, 32, 136, 0), (64, 32, 40, 2)):
         assert lib.deltarule_ckpt_size(*bad) == 0
 
@@ -74,9 +75,9 @@ def test_fwd_refusals(lib, dt):
         assert call(_fake(0x100002), at) == c.SS_ERR_ALIGN
     need = lib.deltarule_fwd_workspace_size(*_sizes(), dt)
     assert need > 0 and lib.deltarule_fwd_workspace_size(*_sizes(K=4), dt) == 0
-    assert call(ws=None) == c.SS_ERR_WORKSPACE
-    assert call(wsz=need - 1) == c.SS_ERR_WORKSPACE
-    assert call(ws=_fake(0x900008)) == c.SS_ERR_ALIGN
+    assert call(None, 8, ws=None) == c.SS_ERR_WORKSPACE  # (with ckpt there is no workspace)
+    assert call(None, 8, wsz=need - 1) == c.SS_ERR_WORKSPACE
+    assert call(None, 8, ws=_fake(0x900008)) == c.SS_ERR_ALIGN
 
 
 @pytest.mark.parametrize("dt", [0, 1])

@@ -367,10 +367,14 @@ def test_workspace_contents_do_not_matter(ss, dtype):
     g = _bwd(ss, d, ckpt)
     for fill in (0xFF, 0x7F):
         ws = torch.full((64 << 20,), fill, dtype=torch.uint8, device="cuda")
-        o2, ckpt2, h2 = _fwd(ss, d, workspace=ws)
-        ws.fill_(fill)
+        ckpt.view(torch.uint8).fill_(fill)
+        o2, ckpt2, h2 = _fwd(ss, d)
         g2 = _bwd(ss, d, ckpt2, workspace=ws)
         assert torch.equal(o, o2) and torch.equal(h, h2) and all(torch.equal(g[n], g2[n]) for n in g)
+        ws.fill_(fill)
+        o3, _, h3 = _fwd(ss, d, want_ckpt=False, workspace=ws)
+        assert torch.equal(h, h3)  # (o differs with and without ckpt in bf16, by its operands' last term)
+        ckpt = ckpt2
 
 
 def test_offsets_past_32_bits(ss):
@@ -420,6 +424,6 @@ def test_refusals(ss):
     with pytest.raises(ValueError, match="ckpt"):
         ss.deltarule_bwd(q, q, v, g, g, z(1), v)
     with pytest.raises(ss.SSError, match="status -5"):
-        ss.deltarule_fwd(q, q, v, g, g, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+        ss.deltarule_fwd(q, q, v, g, g, want_ckpt=False, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError, match="h has shape"):
         ss.deltarule_step(q[:, 0].contiguous(), q[:, 0].contiguous(), v[:, 0].contiguous(), None, g[:, 0].contiguous(), z(2, 4, 16, 8))
