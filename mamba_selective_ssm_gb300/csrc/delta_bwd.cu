@@ -277,20 +277,21 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
 }
 
 // ---------------------------------------------------------------- the other gradients, chunk by chunk
-// A CTA takes one (batch row, head, chunk).  First each warp takes 16 columns of V: it finds u and o as the forward does, and
-// what the columns add to dg and dbeta.  Then the warps share the products that contract over V, from tiles in shared memory
-// scaled as a whole: u, dR, S0, dS1 lie [V][..].
+// A CTA takes one (batch row, head, chunk).  First its warps take 16 columns of V each (with half of the tokens where V is 64
+// and less): what they add to dg and dbeta, from r and o (the forward's), du, v and do.  Then they share the products that
+// contract over V, from tiles in shared memory scaled as a whole: u, dR, S0, dS1 lie [V][..].
 template <int KP, int VP>
 struct GradSmem {
   static constexpr int N = 2, tile = DTile<KP, N>::bytes;
   static constexpr int vk = VP * KP * 2 * N, vt = VP * kDC * 2 * N, tt = DTile<kDC, N>::bytes;
-  static constexpr int doo = 0, u = doo + DTile<VP, N>::bytes, r = u + vt, front = r + vt;
-  // k with q, S0, dS1, and k with q again take turns; E and F lie where M and P were
-  static constexpr int both = 2 * tile > vk ? 2 * tile : vk;
-  static constexpr int k = front, q = k + tile, st = front;
-  static constexpr int m = front + both, p = m + kDMBytes, e = m, f = e + tt;
-  static constexpr int end = m + 2 * (kDMBytes > tt ? kDMBytes : tt);
-  static constexpr int vec = end, up = vec + kDVec * 4, red = up + 3 * kDC * 4, bytes = red + (2 * 8 * kDC + 64) * 4;
+  static constexpr int doo = 0, u = doo + DTile<VP, N>::bytes, r = u + vt, k = r + vt, q = k + tile;
+  // S0 and dS1 take turns, and where there is no room for one beside k and q these come a second time
+  static constexpr bool turns = r + vt + 2 * tile + vk > 220 * 1024;
+  static constexpr int st = turns ? k : q + tile, e = doo, f = e + tt;  // (E and F after do, u and dR)
+  static constexpr int end = turns ? k + (2 * tile > vk ? 2 * tile : vk) : st + vk;
+  static constexpr int vec = end, up = vec + kDVec * 4, red = up + 3 * kDC * 4, bytes = red + (2 * 8 * kDC + 64 + 2 * kDC) * 4;
+  static constexpr int ctas = 2 * (bytes + 1024) <= 228 * 1024 ? 2 : 1;
+  static_assert(f + tt <= k, "E and F where do, u and dR were");
 };
 
 constexpr int kGradThreads = 256;
@@ -334,12 +335,13 @@ __device__ __forceinline__ void mma_pair(float (&c0)[4], float (&c1)[4], const u
 }
 
 template <int KP, int VP>
-__global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const float* __restrict__ ckpt, const float* __restrict__ dout,
+__global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_grad_kernel(Delta p, const float* __restrict__ ckpt, const float* __restrict__ dout,
                                                                   const float* __restrict__ dS, const float* __restrict__ du,
                                                                   float* __restrict__ dq, float* __restrict__ dk, int heads,
                                                                   float* __restrict__ dg, float* __restrict__ dbeta) {
   using Sm = GradSmem<KP, VP>;
-  constexpr int N = 2, KT = KP / 8, VB = VP / 16, NC = KP / 16;  // NC: column tiles of a warp's half of K
+  constexpr int N = 2, VB = VP / 16, NC = KP / 16;  // NC: column tiles of a warp's half of K
+  constexpr int NW = 8 / VB, KT = KP / 8 / NW, NT = 8 / NW;  // warps of 16 columns of V; a warp's tiles of K, of tokens
   extern __shared__ __align__(128) unsigned char raw[];
   const uint32_t sb = smem_u32(raw);
   const LinAttn& a = p.a;
@@ -375,203 +377,148 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
   tile_load<float, KP>(sb + Sm::k, k, a.ldk, valid, a.K, tid, kGradThreads);
   tile_load<float, KP>(sb + Sm::q, q, a.ldq, valid, a.K, tid, kGradThreads);
   tile_load<float, VP>(sb + Sm::doo, dob, ldo, valid, a.V, tid, kGradThreads);
-  tile_copy(sb + Sm::m, p.M + item * kDMBytes, kDMBytes, tid, kGradThreads);
-  tile_copy(sb + Sm::p, p.P + item * kDMBytes, kDMBytes, tid, kGradThreads);
   tile_copy(sb + Sm::vec, reinterpret_cast<const unsigned char*>(p.vec + item * kDVec), kDVec * 4, tid, kGradThreads);
   cp_commit();
-  if (tid < 64) mx[tid] = 0.f;
-  const int v0 = warp * 16, vw = a.V - v0;  // this warp's columns
+  float* cc = mx + 64;  // running log2 decays: D_ts = e^{c_t - c_s} from the scalars, e^{c_t} / e^{c_s}, would lose small ones
+  if (warp == 7) {
+    ChunkGates<kDC> gates;
+    if (a.g != nullptr) gates.fetch(a, b, h, (int)t0, (int)t0 + valid, lane);
+    else gates.g[0] = gates.g[1] = 0.f;
+    gates.scan(lane, [&](int i, Dec e) { cc[i] = e.hi; cc[kDC + i] = e.lo; });
+  }
+  const int v0 = warp % VB * 16, part = warp / VB, vw = a.V - v0;  // this warp's columns, its part of the other axis
   // a [V][K] state in the order of accumulators
   auto state = [&](const float* src, float (&x)[KT][4]) {
 #pragma unroll
     for (int j = 0; j < KT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
-        const int kk = 8 * j + t2, vv = g + (e >> 1) * 8;
+        const int kk = 8 * (part * KT + j) + t2, vv = g + (e >> 1) * 8;
         float2 y = make_float2(0.f, 0.f);
         if (kk < a.K && vv < vw) y = *reinterpret_cast<const float2*>(src + (long long)(v0 + vv) * a.K + kk);
         x[j][e] = y.x;
         x[j][e + 1] = y.y;
       }
   };
-  float S[KT][4];
-  const float* s0 = ckpt + (bh * (a.nck + 1) + ck) * a.V * a.K;
-  if (warp < VB) state(s0, S);
+  // [V][64] values, and rows of v and do
+  auto tokens = [&](const float* src, float (&x)[NT][4]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const int t = 8 * (part * NT + n) + t2, vv = g + (e >> 1) * 8;
+        float2 y = make_float2(0.f, 0.f);
+        if (vv < vw) y = *reinterpret_cast<const float2*>(src + (long long)(v0 + vv) * kDC + t);
+        x[n][e] = y.x;
+        x[n][e + 1] = y.y;
+      }
+  };
+  auto rows_of = [&](const float* src, long long ld, float (&x)[NT][4]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = 8 * (part * NT + n) + t2 + (e & 1), vv = g + (e >> 1) * 8;
+        x[n][e] = t < valid && vv < vw ? src[(long long)t * ld + v0 + vv] : 0.f;
+      }
+  };
+  const float* base = ckpt + bh * delta_ckpt_floats(a.nck, a.K, a.V);
+  const float* s0 = base + (long long)ck * a.K * a.V;
+  const float* ro = base + (long long)(a.nck + 1) * a.K * a.V + (long long)ck * kDC * a.V;
+  float R[NT][4], D[NT][4];  // r, then u; du, then dR
+  float db[2 * NT], af[2 * NT];
+  tokens(ro, R);
+  tokens(du + item * kDC * a.V, D);
+  {
+    float x[NT][4], o[NT][4];
+    rows_of(dob, ldo, x);
+    tokens(ro + (long long)a.nck * kDC * a.V, o);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int t = 8 * (part * NT + n) + t2;
+      af[2 * n] = t < valid ? fmaf(x[n][0], o[n][0], x[n][2] * o[n][2]) : 0.f;
+      af[2 * n + 1] = t + 1 < valid ? fmaf(x[n][1], o[n][1], x[n][3] * o[n][3]) : 0.f;
+    }
+  }
+  float X[NT][4];
+  rows_of(v, a.ldv, X);
   cp_wait<0>();
   __syncthreads();
   tile_scale<KP>(sb + Sm::k, up, tid, kGradThreads);
   tile_scale<KP>(sb + Sm::q, up + kDC, tid, kGradThreads);
-  // do of this warp's columns (before it is scaled in place), v and du, all tokens by columns
-  float X[8][4], R[8][4], D[8][4];
-  if (warp < VB) {
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = 8 * n + t2 + (e & 1), vv = g + (e >> 1) * 8;
-        const bool on = t < valid && vv < vw;
-        X[n][e] = on ? v[(long long)t * a.ldv + v0 + vv] : 0.f;
-        D[n][e] = vv < vw ? du[(item * a.V + v0 + vv) * kDC + t] : 0.f;
-      }
-  }
   tile_scale<VP>(sb + Sm::doo, up + 2 * kDC, tid, kGradThreads);
   __syncthreads();
-  if (warp < VB) {
-    float O[8][4];
-    uint32_t hi[4][4], lo[4][4];
-    const RowScale ss = row_scale(S);
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
+  for (int n = 0; n < NT; ++n) {
+    const int t = 8 * (part * NT + n) + t2;
+    const float2 be = *reinterpret_cast<const float2*>(vec + 2 * kDC + t), ku = *reinterpret_cast<const float2*>(up + t);
+    db[2 * n] = fmaf(D[n][0], R[n][0], D[n][2] * R[n][2]);
+    db[2 * n + 1] = fmaf(D[n][1], R[n][1], D[n][3] * R[n][3]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) R[n][e] = O[n][e] = 0.f;
-#pragma unroll
-    for (int kb = 0; kb < KP / 16; ++kb) {
-      uint32_t sh[4], sl[4];
-      left_terms(sh, sl, S[2 * kb], S[2 * kb + 1], ss);
-#pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        uint32_t bb[N][4];
-#pragma unroll
-        for (int n = 0; n < N; ++n) right_rows<KP, N>(bb[n], sb + Sm::k, np, kb, n, lane);
-        mma_terms(R[2 * np], R[2 * np + 1], sh, sl, bb[0], bb[N - 1]);
-#pragma unroll
-        for (int n = 0; n < N; ++n) right_rows<KP, N>(bb[n], sb + Sm::q, np, kb, n, lane);
-        mma_terms(O[2 * np], O[2 * np + 1], sh, sl, bb[0], bb[N - 1]);
-      }
+    for (int e = 0; e < 4; ++e) {
+      R[n][e] *= e & 1 ? be.y : be.x;
+      D[n][e] *= e & 1 ? be.y : be.x;
     }
-    float w[8][4];
+    // (v in its token's scale, as dR)
+    af[2 * n] -= fmaf(D[n][0], X[n][0], D[n][2] * X[n][2]) * __frcp_rn(ku.x);
+    af[2 * n + 1] -= fmaf(D[n][1], X[n][1], D[n][3] * X[n][3]) * __frcp_rn(ku.y);
+  }
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const int t = 8 * n + t2;
-      const float2 in = *reinterpret_cast<const float2*>(vec + t), ku = *reinterpret_cast<const float2*>(up + t);
-      const float2 be = *reinterpret_cast<const float2*>(vec + 2 * kDC + t);
+  for (int i = 0; i < 2 * NT; ++i) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float f = (e & 1 ? in.y : in.x) * ss.r[e >> 1].up;
-        X[n][e] *= __frcp_rn(e & 1 ? ku.y : ku.x);
-        R[n][e] = fmaf(-f, R[n][e], X[n][e]);
-        O[n][e] *= f;
-        w[n][e] = (e & 1 ? be.y : be.x) * R[n][e];
-      }
+    for (int o = 4; o < 32; o <<= 1) {
+      db[i] += __shfl_xor_sync(0xffffffffu, db[i], o);
+      af[i] += __shfl_xor_sync(0xffffffffu, af[i], o);
     }
-    {
-      const RowScale ws = row_scale(w);
-#pragma unroll
-      for (int kb = 0; kb < 4; ++kb) left_terms(hi[kb], lo[kb], w[2 * kb], w[2 * kb + 1], ws);
-#pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-        for (int kb = 0; kb <= np; ++kb) {
-          uint32_t b0[4], b1[4];
-          right_rows<kDC, 2>(b0, sb + Sm::m, np, kb, 0, lane);
-          right_rows<kDC, 2>(b1, sb + Sm::m, np, kb, 1, lane);
-          mma_terms(c[0], c[1], hi[kb], lo[kb], b0, b1);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float2 em = *reinterpret_cast<const float2*>(vec + 3 * kDC + 16 * np + 8 * i + t2);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) R[2 * np + i][e] = fmaf(-(e & 1 ? em.y : em.x) * ws.r[e >> 1].up, c[i][e], R[2 * np + i][e]);
-        }
-      }
-    }
-    // R is r: dbeta; then u and dR
-    float db[16], af[16];
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const int t = 8 * n + t2;
-      const float2 be = *reinterpret_cast<const float2*>(vec + 2 * kDC + t);
-      db[2 * n] = D[n][0] * R[n][0] + D[n][2] * R[n][2];
-      db[2 * n + 1] = D[n][1] * R[n][1] + D[n][3] * R[n][3];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        R[n][e] *= e & 1 ? be.y : be.x;
-        D[n][e] *= e & 1 ? be.y : be.x;
-      }
-      af[2 * n] = -(D[n][0] * X[n][0] + D[n][2] * X[n][2]);
-      af[2 * n + 1] = -(D[n][1] * X[n][1] + D[n][3] * X[n][3]);
-    }
-    {
-      const RowScale us = row_scale(R);
-#pragma unroll
-      for (int kb = 0; kb < 4; ++kb) left_terms(hi[kb], lo[kb], R[2 * kb], R[2 * kb + 1], us);
-#pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-        for (int kb = 0; kb <= np; ++kb) {
-          uint32_t b0[4], b1[4];
-          right_rows<kDC, 2>(b0, sb + Sm::p, np, kb, 0, lane);
-          right_rows<kDC, 2>(b1, sb + Sm::p, np, kb, 1, lane);
-          mma_terms(c[0], c[1], hi[kb], lo[kb], b0, b1);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int n = 2 * np + i, t = 8 * n + t2;
-          const float2 qu = *reinterpret_cast<const float2*>(up + kDC + t);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tt = t + (e & 1), vv = g + (e >> 1) * 8;
-            const float x = tt < valid && vv < vw ? dob[(long long)tt * ldo + v0 + vv] : 0.f;
-            const float oo = a.scale * (e & 1 ? qu.y : qu.x) * fmaf(c[i][e], us.r[e >> 1].up, O[n][e]);
-            if (tt < valid) af[2 * n + (e & 1)] = fmaf(x, oo, af[2 * n + (e & 1)]);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        db[i] += __shfl_xor_sync(0xffffffffu, db[i], o);
-        af[i] += __shfl_xor_sync(0xffffffffu, af[i], o);
-      }
-      if (g == 0) {
-        const int t = (i >> 1) * 8 + t2 + (i & 1);
-        red[warp * kDC + t] = db[i];
-        red[(8 + warp) * kDC + t] = af[i];
-      }
-    }
-    const float ms = abs_max(S), mu = abs_max(R), md = abs_max(D);
-    if (lane == 0) {
-      mx[warp * 8] = ms;
-      mx[warp * 8 + 1] = mu;
-      mx[warp * 8 + 2] = md;
+    if (g == 0) {
+      const int t = 8 * (part * NT + (i >> 1)) + t2 + (i & 1);
+      red[warp % VB * kDC + t] = db[i];
+      red[(8 + warp % VB) * kDC + t] = af[i];
     }
   }
-  __syncthreads();
-  const Pow2 scS = warps_scale(mx, 8), scU = warps_scale(mx + 1, 8), scR = warps_scale(mx + 2, 8);
-  if (warp < VB) {
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      store_acc<kDC>(sb + Sm::u, v0, n, R[n], scU.down, lane);
-      store_acc<kDC>(sb + Sm::r, v0, n, D[n], scR.down, lane);
-    }
-    // <S1, dS1> of these columns, and dS1's largest
-    float x = 0.f;
-    state(dS + item * a.V * a.K, S);
+  // dS1: its largest and <S1, dS1>; S0
+  float S[KT][4];
+  float dot = 0.f;
+  state(dS + item * a.V * a.K, S);
+  {
     const float* s1 = s0 + (long long)a.V * a.K;
 #pragma unroll
     for (int j = 0; j < KT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
-        const int kk = 8 * j + t2, vv = g + (e >> 1) * 8;
+        const int kk = 8 * (part * KT + j) + t2, vv = g + (e >> 1) * 8;
         if (kk < a.K && vv < vw) {
           const float2 y = *reinterpret_cast<const float2*>(s1 + (long long)(v0 + vv) * a.K + kk);
-          x = fmaf(y.x, S[j][e], fmaf(y.y, S[j][e + 1], x));
+          dot = fmaf(y.x, S[j][e], fmaf(y.y, S[j][e + 1], dot));
         }
       }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    const float m = abs_max(S);
+    for (int o = 1; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+  }
+  {
+    const float mt = abs_max(S);
+    state(s0, S);
+    const float ms = abs_max(S), mu = abs_max(R), md = abs_max(D);
     if (lane == 0) {
-      mx[warp * 8 + 3] = m;
-      mx[warp * 8 + 6] = x;
+      mx[warp * 8] = ms;
+      mx[warp * 8 + 1] = mu;
+      mx[warp * 8 + 2] = md;
+      mx[warp * 8 + 3] = mt;
+      mx[warp * 8 + 6] = dot;
     }
   }
   __syncthreads();
-  const Pow2 scT = warps_scale(mx + 3, 8);
+  const Pow2 scS = warps_scale(mx, 8), scU = warps_scale(mx + 1, 8), scR = warps_scale(mx + 2, 8), scT = warps_scale(mx + 3, 8);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    store_acc<kDC>(sb + Sm::u, v0, part * NT + n, R[n], scU.down, lane);
+    store_acc<kDC>(sb + Sm::r, v0, part * NT + n, D[n], scR.down, lane);
+  }
+  auto put_state = [&](float f) {
+#pragma unroll
+    for (int j = 0; j < KT; ++j) store_acc<KP>(sb + Sm::st, v0, part * KT + j, S[j], f, lane);
+  };
+  if (!Sm::turns) put_state(scS.down);
   if (warp == 0) {  // dbeta, and the sums from each token on
     float s[2], d[2];
 #pragma unroll
@@ -586,7 +533,7 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
     }
     s[0] += s[1];
     float x = 0.f;
-    for (int w = 0; w < VB; ++w) x += mx[w * 8 + 6];
+    for (int w = 0; w < 8; ++w) x += mx[w * 8 + 6];
     float incl = s[0];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -602,8 +549,9 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
   }
   // E and F, a warp's 16 tokens t against half of the tokens s
   const int mb = warp & 3, half = warp >> 2, vb = (a.V + 15) / 16;
+  float E[4][4], F[4][4];
+  __syncthreads();  // u and dR
   {
-    float E[4][4], F[4][4];
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -626,16 +574,6 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
         }
       }
     }
-    // D_ts = e^{c_t - c_s} again from the scalars: e^{c_t} / e^{c_s} would lose small ones, so the gates are summed anew
-    float* cc = red;  // (the sums in it have been taken by warp 0 before the barrier below)
-    __syncthreads();
-    if (warp == 0) {
-      ChunkGates<kDC> gates;
-      if (a.g != nullptr) gates.fetch(a, b, h, (int)t0, (int)t0 + valid, lane);
-      else gates.g[0] = gates.g[1] = 0.f;
-      gates.scan(lane, [&](int i, Dec e) { cc[i] = e.hi; cc[kDC + i] = e.lo; });
-    }
-    __syncthreads();
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -650,15 +588,7 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
       mx[warp * 8 + 4] = me;
       mx[warp * 8 + 5] = mf;
     }
-    __syncthreads();
-    const Pow2 scE = warps_scale(mx + 4, 8), scF = warps_scale(mx + 5, 8);
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      store_acc<kDC>(sb + Sm::e, 16 * mb, 4 * half + n, E[n], scE.down, lane);
-      store_acc<kDC>(sb + Sm::f, 16 * mb, 4 * half + n, F[n], scF.down, lane);
-    }
   }
-  const Pow2 scE = warps_scale(mx + 4, 8), scF = warps_scale(mx + 5, 8);
   // dq and dk: a warp's 16 tokens and half of the columns of K
   float Q[NC][4], Kg[NC][4], C[NC][4];
   const int ta = 16 * mb + g, tb = ta + 8;
@@ -684,16 +614,11 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
       mma_pair(C[2 * jp], C[2 * jp + 1], la, bb);
     }
   };
-  auto put_state = [&](uint32_t tile, const float* src, float f) {
-    if (warp < VB) {
-      state(src, S);
-#pragma unroll
-      for (int j = 0; j < KT; ++j) store_acc<KP>(tile, v0, j, S[j], f, lane);
-    }
-  };
-  __syncthreads();  // E and F; k and q have been read
-  put_state(sb + Sm::st, s0, scS.down);
-  __syncthreads();
+  if constexpr (Sm::turns) {
+    __syncthreads();  // (k and q were read by tile_scale alone; all are past that)
+    put_state(scS.down);
+    __syncthreads();
+  }
   zero();
   for (int kb = 0; kb < vb; ++kb) {
     uint32_t la[N][4];
@@ -711,8 +636,9 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
     step(sb + Sm::st, kb, la);
   }
   add(Kg, -vec[ta] * scR.up * scS.up, -vec[tb] * scR.up * scS.up, true);
+  state(dS + item * a.V * a.K, S);
   __syncthreads();
-  put_state(sb + Sm::st, dS + item * a.V * a.K, scT.down);
+  put_state(scT.down);
   __syncthreads();
   zero();
   for (int kb = 0; kb < vb; ++kb) {
@@ -722,14 +648,24 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(Delta p, const
     step(sb + Sm::st, kb, la);
   }
   add(Kg, vec[kDC + ta] * scU.up * scT.up, vec[kDC + tb] * scU.up * scT.up, false);
-  __syncthreads();
-  tile_load<float, KP>(sb + Sm::k, k, a.ldk, valid, a.K, tid, kGradThreads);
-  tile_load<float, KP>(sb + Sm::q, q, a.ldq, valid, a.K, tid, kGradThreads);
-  cp_commit();
-  cp_wait<0>();
-  __syncthreads();
-  tile_scale<KP>(sb + Sm::k, up, tid, kGradThreads);
-  tile_scale<KP>(sb + Sm::q, up + kDC, tid, kGradThreads);
+  __syncthreads();  // do, u, dR and dS1 have been read
+  if constexpr (Sm::turns) {
+    tile_load<float, KP>(sb + Sm::k, k, a.ldk, valid, a.K, tid, kGradThreads);
+    tile_load<float, KP>(sb + Sm::q, q, a.ldq, valid, a.K, tid, kGradThreads);
+    cp_commit();
+  }
+  const Pow2 scE = warps_scale(mx + 4, 8), scF = warps_scale(mx + 5, 8);
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    store_acc<kDC>(sb + Sm::e, 16 * mb, 4 * half + n, E[n], scE.down, lane);
+    store_acc<kDC>(sb + Sm::f, 16 * mb, 4 * half + n, F[n], scF.down, lane);
+  }
+  if constexpr (Sm::turns) {
+    cp_wait<0>();
+    __syncthreads();
+    tile_scale<KP>(sb + Sm::k, up, tid, kGradThreads);
+    tile_scale<KP>(sb + Sm::q, up + kDC, tid, kGradThreads);
+  }
   __syncthreads();
   zero();
 #pragma unroll
@@ -912,7 +848,7 @@ extern "C" int deltarule_bwd(const void* q, long long ldq, const void* k, long l
   pl.p.beta = beta;
   char* w = static_cast<char*>(workspace);
   BwdArgs x{ckpt, dh_last, dout, dq, dk, dv, g ? dg : nullptr, dbeta, dh0, nullptr, nullptr, nullptr, nullptr};
-  pl.p.place(const_cast<float*>(ckpt) + (long long)B * H * delta_ckpt_floats(a.nck, K, V, dtype == SS_BF16), dtype == SS_BF16);  // (only read)
+  pl.p.place(const_cast<float*>(ckpt) + (long long)B * H * delta_ckpt_floats(a.nck, K, V), dtype == SS_BF16);  // (only read)
   x.dS = reinterpret_cast<float*>(w);
   x.du = reinterpret_cast<float*>(w += pl.ds);
   x.pq = reinterpret_cast<float*>(w += pl.du);

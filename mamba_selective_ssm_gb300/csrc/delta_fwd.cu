@@ -63,6 +63,15 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
       const int kk = 8 * j + t2 + (e & 1), vv = g + (e >> 1) * 8;
       S[j][e] = h0 != nullptr && kk < a.K && vv < vw ? h0[(bh * a.K + kk) * a.V + v0 + vv] : 0.f;
     }
+  if (ckpt != nullptr) ckpt += bh * delta_ckpt_floats(a.nck, a.K, a.V);
+  float* ro = ckpt + (long long)(a.nck + 1) * a.K * a.V;  // r of every chunk, [V][64], and then o
+  auto keep = [&](float* dst, int t, const float (&x)[4]) {  // two tokens of two columns
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      const int vv = g + (e >> 1) * 8;
+      if (vv < vw) *reinterpret_cast<float2*>(dst + (long long)(v0 + vv) * kDC + t) = make_float2(x[e], x[e + 1]);
+    }
+  };
   auto save = [&](int ck) {  // the state entering chunk ck: [V][K]
 #pragma unroll
     for (int j = 0; j < KT; ++j)
@@ -70,7 +79,7 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
       for (int e = 0; e < 4; e += 2) {
         const int kk = 8 * j + t2, vv = g + (e >> 1) * 8;
         if (kk < a.K && vv < vw)
-          *reinterpret_cast<float2*>(ckpt + ((bh * (a.nck + 1) + ck) * a.V + v0 + vv) * a.K + kk) = make_float2(S[j][e], S[j][e + 1]);
+          *reinterpret_cast<float2*>(ckpt + ((long long)ck * a.V + v0 + vv) * a.K + kk) = make_float2(S[j][e], S[j][e + 1]);
       }
   };
 
@@ -148,10 +157,15 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
         for (int i = 0; i < 2; ++i) {
           const int n = 2 * np + i, t = 8 * n + t2;
           const float2 em = *reinterpret_cast<const float2*>(vec + 3 * kDC + t), be = *reinterpret_cast<const float2*>(vec + 2 * kDC + t);
-          R[n][0] = be.x * fmaf(-em.x * ws.r[0].up, c[i][0], R[n][0]);
-          R[n][1] = be.y * fmaf(-em.y * ws.r[0].up, c[i][1], R[n][1]);
-          R[n][2] = be.x * fmaf(-em.x * ws.r[1].up, c[i][2], R[n][2]);
-          R[n][3] = be.y * fmaf(-em.y * ws.r[1].up, c[i][3], R[n][3]);
+          R[n][0] = fmaf(-em.x * ws.r[0].up, c[i][0], R[n][0]);
+          R[n][1] = fmaf(-em.y * ws.r[0].up, c[i][1], R[n][1]);
+          R[n][2] = fmaf(-em.x * ws.r[1].up, c[i][2], R[n][2]);
+          R[n][3] = fmaf(-em.y * ws.r[1].up, c[i][3], R[n][3]);
+          if (ckpt != nullptr) keep(ro + (long long)ck * kDC * a.V, t, R[n]);
+          R[n][0] *= be.x;
+          R[n][1] *= be.y;
+          R[n][2] *= be.x;
+          R[n][3] *= be.y;
         }
       }
     }
@@ -200,6 +214,7 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
           O[n][3] = f1 * fmaf(O[n][3], in.y * ss.r[1].up, c[i][3] * us.r[1].up);
           if (t0 + t >= len) O[n][0] = O[n][2] = 0.f;  // (not 0 * NaN)
           if (t0 + t + 1 >= len) O[n][1] = O[n][3] = 0.f;
+          if (ckpt != nullptr) keep(ro + (long long)(a.nck + ck) * kDC * a.V, t, O[n]);
           store_tokens(ob + (long long)t0 * ldo, ldo, 8 * n, rows, vw, O[n], lane);
         }
       }
@@ -293,7 +308,7 @@ int walk(const FwdPlan& pl, const float* h0, void* o, float* ckpt, float* h_last
 extern "C" size_t deltarule_ckpt_size(int L, int K, int V, int dtype) {
   FwdPlan pl;
   if (fwd_plan(1, L, 1, 1, K, V, dtype, true, pl) != SS_OK) return 0;
-  return (size_t)delta_ckpt_floats(pl.p.a.nck, K, V, dtype == SS_BF16) + pl.bytes / sizeof(float);
+  return (size_t)delta_ckpt_floats(pl.p.a.nck, K, V) + pl.bytes / sizeof(float);
 }
 
 extern "C" size_t deltarule_fwd_workspace_size(int B, int L, int H, int G, int K, int V, int dtype) {
@@ -326,7 +341,7 @@ extern "C" int deltarule_fwd(const void* q, long long ldq, const void* k, long l
   a.lengths = lengths;
   a.scale = scale;
   pl.p.beta = beta;
-  pl.p.place(ckpt != nullptr ? ckpt + (long long)B * H * delta_ckpt_floats(a.nck, K, V, dtype == SS_BF16) : workspace, dtype == SS_BF16);
+  pl.p.place(ckpt != nullptr ? ckpt + (long long)B * H * delta_ckpt_floats(a.nck, K, V) : workspace, dtype == SS_BF16);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if ((rc = ssh::delta_prep(pl.p, dtype, s)) != SS_OK) return rc;
   if (dtype == SS_F32) return K <= 64 ? walk<64>(pl, h0, o, ckpt, h_last, s) : walk<128>(pl, h0, o, ckpt, h_last, s);

@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kDThreads, 1) delta_fwd_tc_kernel(Delta p, con
     // r and o of a chunk, [16][V][4]: this thread's first vector
     float4* keep = nullptr;
     if (TRAIN) {
-      ckpt += bh * delta_ckpt_floats(a.nck, a.K, a.V, true);
+      ckpt += bh * delta_ckpt_floats(a.nck, a.K, a.V);
       keep = reinterpret_cast<float4*>(ckpt + (long long)(a.nck + 1) * a.K * a.V) + (long long)(cq * TC / 4) * a.V + row;
     }
     if (nck > 0) read_v(0);

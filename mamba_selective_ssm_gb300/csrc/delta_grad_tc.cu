@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kGT, 1) delta_grad_tc_kernel(Delta p, const __
     tok_load(sb + L::q, kp, &maps.q, &bar[L::kIn], gh, t0, b);
   };
   auto marks = [&](long long it) {  // the forward's states, and after them r and o, of a chunk's batch row and head
-    return ckpt + it / a.nck * delta_ckpt_floats(a.nck, a.K, a.V, true);
+    return ckpt + it / a.nck * delta_ckpt_floats(a.nck, a.K, a.V);
   };
   // r, o and du of a chunk towards L2, a line of 128 bytes at a time (with dS1 as well: 481 us where this gives 442, as the
   // states' lines come back out of L2 before they are read)

@@ -35,8 +35,8 @@ def _sizes(**kw):
 def test_ckpt_size(lib):
     from mamba_selective_ssm_gb300 import _capi as c
     mp32, mp16 = 2 * 64 * 64 + 272, 3 * 64 * 64 + 272  # a chunk's two 64 x 64 operands and scalars
-    assert lib.deltarule_ckpt_size(64, 32, 40, c.SS_F32) == 2 * 32 * 40 + mp32  # the state entering the chunk and the last
-    assert lib.deltarule_ckpt_size(65, 32, 40, c.SS_F32) == 3 * 32 * 40 + 2 * mp32
+    assert lib.deltarule_ckpt_size(64, 32, 40, c.SS_F32) == 2 * 32 * 40 + 2 * 64 * 40 + mp32  # two states, r and o
+    assert lib.deltarule_ckpt_size(65, 32, 40, c.SS_F32) == 3 * 32 * 40 + 2 * 128 * 40 + 2 * mp32
     assert lib.deltarule_ckpt_size(65, 32, 40, c.SS_BF16) == 3 * 32 * 40 + 2 * 128 * 40 + 2 * mp16
     for bad in ((0, 32, 40, 0), (64, 30, 40, 0), (64, 32, 136, 0), (64, 32, 40, 2)):
         assert lib.deltarule_ckpt_size(*bad) == 0
