@@ -772,7 +772,9 @@ int chain(const BwdPlan& pl, const BwdArgs& x, cudaStream_t s) {
   int warps = (a.V + 15) / 16;
   while (warps > 1 && bh * ((a.V + 16 * warps - 1) / (16 * warps)) < 100) warps = (warps + 1) / 2;
   const int nvt = (a.V + 16 * warps - 1) / (16 * warps);
-  const int sb = St::bytes(warps), stages = 2 * sb <= 227 * 1024 ? 2 : 1;
+  // A chunk's tiles have two places where these fit and the CTAs are no more than the SMs; with more CTAs two an SM, each with
+  // one place, are faster than one with two.
+  const int sb = St::bytes(warps), stages = 2 * sb <= 226 * 1024 && bh * nvt <= 152 ? 2 : 1;
   return lin_launch(delta_bwd_kernel<KP>, (unsigned)(bh * nvt), 32 * warps, (size_t)sb * stages, s, pl.p, static_cast<const float*>(x.dout),
                     x.dh_last, static_cast<float*>(x.dv), x.dS, x.du, x.dh0, stages, sb);
 }
