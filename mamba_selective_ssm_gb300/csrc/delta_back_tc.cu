@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(kDThreads, 1) delta_back_tc_kernel(Delta p, co
     for (int i = 0; i < L::nbar; ++i) mbar_init(&bar[i], i >= L::kS && i <= L::kO ? 4 * quarters : 1);
     fence_barrier_init();
   }
+  pdl_trigger();
   if (warp == 0) {
     tmem_alloc(tma, L::cols);
     tmem_relinquish();

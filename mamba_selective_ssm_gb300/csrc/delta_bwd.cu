@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
       U[j][e] = dh_last != nullptr && kk < a.K && vv < vw ? dh_last[(bh * a.K + kk) * a.V + v0 + vv] : 0.f;
     }
 
+  pdl_trigger();
   if (nck > 0) fetch(nck - 1);
   for (int ck = nck - 1; ck >= 0; --ck) {
     const uint32_t off = stages == 2 ? (uint32_t)((ck & 1) * stage_bytes) : 0u, at = sb + off;
@@ -357,6 +358,7 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
   float* dqb = dq + (tok * heads + (heads == a.G ? gh : h)) * a.K;
   float* dkb = dk + (tok * heads + (heads == a.G ? gh : h)) * a.K;
   if (valid == 0) {
+    pdl_wait();
     for (int i = tid; i < rows * a.K; i += kGradThreads) {
       dqb[i / a.K * ldg + i % a.K] = 0.f;
       dkb[i / a.K * ldg + i % a.K] = 0.f;
@@ -422,6 +424,7 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
         x[n][e] = t < valid && vv < vw ? src[(long long)t * ld + v0 + vv] : 0.f;
       }
   };
+  pdl_wait();  // dS and du are delta_bwd_kernel's
   const float* base = ckpt + bh * delta_ckpt_floats(a.nck, a.K, a.V);
   const float* s0 = base + (long long)ck * a.K * a.V;
   const float* ro = base + (long long)(a.nck + 1) * a.K * a.V + (long long)ck * kDC * a.V;
@@ -796,7 +799,7 @@ int grads(const BwdPlan& pl, const BwdArgs& x, cudaStream_t s) {
   constexpr size_t smem = GradSmem<KP, VP>::bytes;
   static_assert(smem <= 227 * 1024, "a chunk's tiles fit shared memory");
   const bool parts = a.H > a.G;
-  const int rc = lin_launch(delta_grad_kernel<KP, VP>, grid, kGradThreads, smem, s, pl.p, x.ckpt, static_cast<const float*>(x.dout), x.dS, x.du,
+  const int rc = delta_launch_next(delta_grad_kernel<KP, VP>, grid, kGradThreads, smem, s, pl.p, x.ckpt, static_cast<const float*>(x.dout), x.dS, x.du,
                             parts ? x.pq : static_cast<float*>(x.dq), parts ? x.pk : static_cast<float*>(x.dk), parts ? a.H : a.G, x.dg, x.dbeta);
   return rc != SS_OK || !parts ? rc : share<float>(pl, x, s);
 }

@@ -58,6 +58,14 @@ __host__ __device__ inline long long delta_ckpt_floats(int nck, int K, int V) {
   return (long long)(nck + 1) * K * V + 2ll * nck * kDC * V;
 }
 
+// Launches a kernel that may start while the one before it ends (each CTA of it calls pdl_wait): its first tiles, its barriers
+// and its tensor memory are then ready when that is done (3 to 5 us a pair).
+template <typename... KArgs, typename... Args>
+inline int delta_launch_next(void (*kern)(KArgs...), unsigned grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SS_ERR_CUDA;
+  return launch_dependent(kern, dim3(grid), dim3((unsigned)threads), smem, s, args...) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
 inline int delta_validate(int B, int L, int H, int G, int K, int V, int dtype) {
   const int rc = linattn_validate(B, L, H, G, K, V, dtype);
   if (rc != SS_OK) return rc;

@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
       }
   };
 
+  pdl_wait();  // M, P and the scalars are delta_prep_kernel's
   if (nck > 0) fetch(0);
   for (int ck = 0; ck < nck; ++ck) {
     const uint32_t off = stages == 2 ? (uint32_t)((ck & 1) * stage_bytes) : 0u, at = sb + off;
@@ -301,7 +302,7 @@ int walk(const FwdPlan& pl, const float* h0, void* o, float* ckpt, float* h_last
   // A chunk's tiles have two places where these fit and the CTAs are no more than the SMs; with more CTAs two an SM, each with
   // one place, are faster than one with two.
   const int sb = St::bytes(warps), stages = 2 * sb <= 226 * 1024 && bh * nvt <= 152 ? 2 : 1;
-  return lin_launch(delta_fwd_kernel<KP>, (unsigned)(bh * nvt), 32 * warps, (size_t)sb * stages, s, pl.p, h0, static_cast<float*>(o), ckpt, h_last,
+  return delta_launch_next(delta_fwd_kernel<KP>, (unsigned)(bh * nvt), 32 * warps, (size_t)sb * stages, s, pl.p, h0, static_cast<float*>(o), ckpt, h_last,
                     stages, sb);
 }
 

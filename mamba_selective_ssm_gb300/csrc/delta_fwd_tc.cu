@@ -128,8 +128,11 @@ __global__ void __launch_bounds__(kDThreads, 1) delta_fwd_tc_kernel(Delta p, con
     };
     if (nck > 0) {
       load_kq(0);
-      load_x(0);
       load_v(0);
+    }
+    pdl_wait();  // M, P and the scalars are delta_prep_kernel's
+    if (nck > 0) {
+      load_x(0);
       load_m(0);
       load_p(0);
     }
@@ -417,7 +420,7 @@ int walk(const Delta& p, const float* h0, __nv_bfloat16* o, float* ckpt, float* 
   if (!delta_map(&maps.q, a.q, a.ldq, a.B, a.L, a.G, a.K) || !delta_map(&maps.k, a.k, a.ldk, a.B, a.L, a.G, a.K) ||
       !delta_map(&maps.v, a.v, a.ldv, a.B, a.L, a.H, a.V) || !delta_map(&maps.o, o, (long long)a.H * a.V, a.B, a.L, a.H, a.V))
     return SS_ERR_CUDA;
-  return lin_launch(delta_fwd_tc_kernel<KP, TRAIN>, (unsigned)((long long)a.B * a.H), kDThreads, DeltaTc<KP, TRAIN>::bytes, s, p, maps, h0, o,
+  return delta_launch_next(delta_fwd_tc_kernel<KP, TRAIN>, (unsigned)((long long)a.B * a.H), kDThreads, DeltaTc<KP, TRAIN>::bytes, s, p, maps, h0, o,
                     ckpt, h_last);
 }
 

@@ -98,7 +98,10 @@ __global__ void __launch_bounds__(kGT, 1) delta_grad_tc_kernel(Delta p, const __
     const long long first = following(blockIdx.x);
     if (first < items) {
       if (tid == 0) load(first);
+      pdl_wait();  // dS and du are delta_back_tc_kernel's
       ahead(first);
+    } else {
+      pdl_wait();
     }
   }
   uint32_t par = 0;
@@ -419,7 +422,7 @@ int run(const Delta& p, const float* ckpt, const void* dout, const float* dS, co
     return SS_ERR_CUDA;
   static_assert(GradTc<KP>::bytes <= 227 * 1024, "a chunk's tiles fit shared memory");
   const unsigned grid = (unsigned)std::min<long long>(kGGrid, (long long)a.B * a.H * a.nck);
-  return lin_launch(delta_grad_tc_kernel<KP, TO>, grid, kGT, GradTc<KP>::bytes, s, p, maps, ckpt, dS, du, static_cast<TO*>(dq), static_cast<TO*>(dk),
+  return delta_launch_next(delta_grad_tc_kernel<KP, TO>, grid, kGT, GradTc<KP>::bytes, s, p, maps, ckpt, dS, du, static_cast<TO*>(dq), static_cast<TO*>(dk),
                     kTile ? a.G : a.H, dg, dbeta);
 }
 

@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(Delta p) {
   const long long item = blockIdx.x, bh = item / a.nck;
   const int ck = (int)(item % a.nck), h = (int)(bh % a.H), b = (int)(bh / a.H), gh = h / (a.H / a.G);
   const int t0 = ck * kDC, left = a.len(b) - t0, valid = left < kDC ? left : kDC;
+  pdl_trigger();
   if (valid <= 0) return;  // the chunk is not walked
   const T* q = static_cast<const T*>(a.q) + ((long long)b * a.L + t0) * a.ldq + (long long)gh * a.K;
   const T* k = static_cast<const T*>(a.k) + ((long long)b * a.L + t0) * a.ldk + (long long)gh * a.K;
