@@ -1,7 +1,7 @@
 """GB300-native Mamba selective scan: forward and backward of the diagonal
 selective SSM, the depthwise causal conv1d (+SiLU), RMSNorm, linear attention
-with a decay for each head and layer norm forward and backward, as hand-written sm_103a CUDA kernels behind the C ABI in
-include/ssscan.h.
+with a decay for each head, the gated delta rule, layer norm and group norm forward and backward, as hand-written sm_103a
+CUDA kernels behind the C ABI in include/ssscan.h.
 
 The Python layer only checks arguments, allocates outputs with PyTorch and
 calls the library on the current CUDA stream.

@@ -21,7 +21,7 @@ using namespace ssk;
 
 // ---------------------------------------------------------------- the chain
 // As in the forward, a warp carries 16 columns of dS, transposed, from the last chunk to the first.  It leaves dS1 and du of
-// every chunk ([V][K] and [V][64], fp32) and dv.
+// every chunk ([V][K] and [V][64], fp32) and dv.  8 x 2048 tokens of 24 heads of 64 x 64: 334 us.
 template <int KP>
 struct BackStage {
   static constexpr int k = 0, q = k + DTile<KP, 2>::bytes, m = q + DTile<KP, 2>::bytes, p = m + kDMBytes,
@@ -280,7 +280,9 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
 // ---------------------------------------------------------------- the other gradients, chunk by chunk
 // A CTA takes one (batch row, head, chunk).  First its warps take 16 columns of V each (with half of the tokens where V is 64
 // and less): what they add to dg and dbeta, from r and o (the forward's), du, v and do.  Then they share the products that
-// contract over V, from tiles in shared memory scaled as a whole: u, dR, S0, dS1 lie [V][..].
+// contract over V, from tiles in shared memory scaled as a whole: u, dR, S0, dS1 lie [V][..].  8 x 2048 tokens of 24 heads of
+// 64 x 64: 502 us (tensor pipe 21 %, memory a quarter of its rate: the steps between barriers, at two CTAs an SM); 997 when r and
+// o were found again here.
 template <int KP, int VP>
 struct GradSmem {
   static constexpr int N = 2, tile = DTile<KP, N>::bytes;
@@ -775,8 +777,7 @@ int chain(const BwdPlan& pl, const BwdArgs& x, cudaStream_t s) {
   int warps = (a.V + 15) / 16;
   while (warps > 1 && bh * ((a.V + 16 * warps - 1) / (16 * warps)) < 100) warps = (warps + 1) / 2;
   const int nvt = (a.V + 16 * warps - 1) / (16 * warps);
-  // A chunk's tiles have two places where these fit and the CTAs are no more than the SMs; with more CTAs two an SM, each with
-  // one place, are faster than one with two.
+  // as in the forward (192 heads of 64 x 64: 334 us for 445)
   const int sb = St::bytes(warps), stages = 2 * sb <= 226 * 1024 && bh * nvt <= 152 ? 2 : 1;
   return lin_launch(delta_bwd_kernel<KP>, (unsigned)(bh * nvt), 32 * warps, (size_t)sb * stages, s, pl.p, static_cast<const float*>(x.dout),
                     x.dh_last, static_cast<float*>(x.dv), x.dS, x.du, x.dh0, stages, sb);

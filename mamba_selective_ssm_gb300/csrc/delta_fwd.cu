@@ -9,7 +9,8 @@ using namespace ssk;
 
 // A warp walks the chunks of one (batch row, head) with 16 columns of the state in registers, transposed: rows are columns
 // of V, so that K S0, M (beta R), K^T u and o are products whose left operand is the accumulators of the one before, and the
-// warps of a CTA share nothing but the tiles of the chunk (k, q, M, P).
+// warps of a CTA share nothing but the tiles of the chunk (k, q, M, P).  8 x 2048 tokens of 24 heads of 64 x 64: 363 us with r, o
+// and the states for the backward; the chain's latency bounds it at four warps a CTA (tensor pipe 18 %, issue slots 26 %).
 template <int KP>
 struct WalkStage {
   static constexpr int k = 0, q = k + DTile<KP, 2>::bytes, m = q + DTile<KP, 2>::bytes, p = m + kDMBytes,
@@ -300,7 +301,7 @@ int walk(const FwdPlan& pl, const float* h0, void* o, float* ckpt, float* h_last
   while (warps > 1 && bh * ((a.V + 16 * warps - 1) / (16 * warps)) < 100) warps = (warps + 1) / 2;
   const int nvt = (a.V + 16 * warps - 1) / (16 * warps);
   // A chunk's tiles have two places where these fit and the CTAs are no more than the SMs; with more CTAs two an SM, each with
-  // one place, are faster than one with two.
+  // one place, are faster than one with two (192 heads of 64 x 64: 363 us for 497).
   const int sb = St::bytes(warps), stages = 2 * sb <= 226 * 1024 && bh * nvt <= 152 ? 2 : 1;
   return delta_launch_next(delta_fwd_kernel<KP>, (unsigned)(bh * nvt), 32 * warps, (size_t)sb * stages, s, pl.p, h0, static_cast<float*>(o), ckpt, h_last,
                     stages, sb);

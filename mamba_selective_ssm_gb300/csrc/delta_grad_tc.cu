@@ -6,7 +6,9 @@
 //   dq = scale e^c do S0^T + E K      dk = -e^c dR S0^T + e^{c_last - c} u dS^T + E^T Q + (F + F^T) K
 // dq and dk are rounded to bf16; their fp32 operands are two bf16 terms (2^-15).  Products run with the columns of K as the
 // 128 rows of an MMA; S0, dS, u and dR lie in shared memory by columns of V, as they come from memory, and are contracted down
-// their rows.
+// their rows.  4 x 2048 tokens of 32 heads of 128 x 128: 422 us, 3.2 TB/s.  A CTA an SM (208 KB; tensor memory is taken whole),
+// whose steps wait for one another: the sums and operands along V a third of a chunk's time, the states' loads and terms a third.
+// A CTA for each chunk took 438 us, and where the heads' parts are added up (32 heads on 4, 128 x 64) 384 for 351.
 #include <algorithm>
 
 #include "delta_tc.cuh"

@@ -14,6 +14,12 @@
 //                                pass for the output, which takes the rows from the last: L2 still holds those.
 // The variance is taken around the mean (parts around their own first row, joined with their means), never as a difference
 // of moments.  The backward's column sums are joined by colsum_kernel in fixed order.
+//
+// bf16 with SiLU, floors at 6.7 TB/s in brackets: 8192 x 1 x 4096 in 32 groups, forward 28 us (20; instructions of short rows:
+// 61 % of the issue slots), backward 50 + 6 (40); 4 x 2048 x 4096 forward 44 (20; x is read twice, the second time from L2 in
+// part).  fp32, 8 x 2048 x 1536 in 24 groups, backward 90 (45; dy and x twice).  The forms at each other's sizes: the first of
+// these with a sample in a CTA 105 and 283 us; 4096 x 4 x 512 with a sample in a CTA 34 and 60, in parts 203 and 184;
+// 16 x 4 x 512 5.1 and 10, in parts 12.4 and 15; 8000 x 2 x 4096 136 and 410, in parts 1750 and 1890.
 #include <algorithm>
 
 #include "common.cuh"
@@ -216,25 +222,41 @@ __global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_lanes_kernel(Gn p, int g
 
 // ---------------------------------------------------------------- a sample in a CTA
 
-// Which of a sample's units (8 channels of one position) a thread holds: its i-th is unit u of position m.
+// Which of a sample's units (8 channels of one position) a thread holds.  Up to 256 units a position: one of them, of every
+// `lanes`-th position; more: every 256th unit of all positions.  Walked with next(), which divides nothing (with the divisions that
+// a unit's place and its channels' groups take otherwise, 4096 samples of 4 x 512 took 124 us).
 struct Mine {
-  int units, rl, lanes;  // units of a position; this thread's position among `lanes` that share them
-  __device__ __forceinline__ Mine(const Gn& p) {
+  int units, lanes, rl, items;  // units of a position; threads that share one, this one's place among them; units held, at most
+  int per, step, m0, u0;        // units of a position held, positions from one to the next
+  uint32_t magic;               // 2^26 / cg, rounded up: exact quotients below 2^13 (kGnSampleDim)
+  int m, u, k;
+  __device__ __forceinline__ Mine(const Gn& p, int n) {
     units = p.C / 8;
-    lanes = units < kGnThreads ? kGnThreads / units : 1;
-    rl = units < kGnThreads ? (int)threadIdx.x / units : 0;
+    items = n;
+    const bool narrow = units < kGnThreads;
+    lanes = narrow ? kGnThreads / units : 1;
+    rl = narrow ? (int)threadIdx.x / units : 0;
+    u0 = narrow ? (int)threadIdx.x % units : (int)threadIdx.x;
+    per = narrow ? 1 : (units + kGnThreads - 1) / kGnThreads;
+    step = lanes;
+    m0 = rl < lanes ? rl : p.M;
+    magic = (1u << 26) / (uint32_t)p.cg + 1u;
   }
-  __device__ __forceinline__ bool at(const Gn& p, int i, int& m, int& u) const {
-    if (units < kGnThreads) {
-      m = rl + i * lanes;
-      u = (int)threadIdx.x % units;
-      return rl < lanes && m < p.M;
+  __device__ __forceinline__ void first() {
+    m = m0;
+    u = u0;
+    k = 0;
+  }
+  __device__ __forceinline__ bool on(const Gn& p) const { return m < p.M && u < units; }
+  __device__ __forceinline__ void next() {
+    u += kGnThreads;
+    if (++k == per) {
+      k = 0;
+      u = u0;
+      m += step;
     }
-    const int per = (units + kGnThreads - 1) / kGnThreads;
-    m = i / per;
-    u = i % per * kGnThreads + (int)threadIdx.x;
-    return m < p.M && u < units;
   }
+  __device__ __forceinline__ int group(int e) const { return (int)__umulhi((uint32_t)(u * 8 + e) << 6, magic); }
 };
 inline int gn_sample_items(const Gn& p) {
   const int units = p.C / 8;
@@ -244,6 +266,16 @@ inline int gn_sample_items(const Gn& p) {
 }
 template <typename T>
 constexpr int kGnItems = 16 / sizeof(T);  // units a thread holds: 128 bytes of x
+
+// A unit goes to its thread's own place in shared memory (registers would have to be indexed by constants: a kernel that
+// unrolled its eight units held 230 of them, and one CTA an SM, or spilled).
+template <typename V, typename T>
+__device__ __forceinline__ void hold_copy(V* dst, const T* src) {
+#pragma unroll
+  for (int e = 0; e < (int)sizeof(V); e += 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst) + e), "l"(reinterpret_cast<const char*>(src) + e) : "memory");
+}
+__device__ __forceinline__ void hold_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // dst[g] = f(sum over the group's channels and the `lanes` rows of part), a warp to a group
 template <typename F>
@@ -258,23 +290,19 @@ __device__ __forceinline__ void group_sums(const Gn& p, const float* part, int l
   }
 }
 // per-channel sums of a thread's units into part[lanes][C]; val(i, e) its values
-template <int IT, typename V>
-__device__ __forceinline__ void channel_sums(const Gn& p, const Mine& my, float* part, V val) {
-  float s[8];
-#pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    int m, u;
-    const bool on = my.at(p, i, m, u);
+template <typename V>
+__device__ __forceinline__ void channel_sums(const Gn& p, Mine& my, float* part, V val) {
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  my.first();
+  for (int i = 0; i < my.items; ++i, my.next()) {
     if (my.units < kGnThreads) {  // one unit: summed over its positions
+      if (my.on(p)) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float x = on ? val(i, e) : 0.f;
-        s[e] = i == 0 ? x : s[e] + x;
+        for (int e = 0; e < 8; ++e) s[e] += val(i, e);
       }
-      if (i == IT - 1 && my.rl < my.lanes) ActT<float>::st8(part + my.rl * p.C + u * 8, s);
-    } else if (on) {
-      float* at = part + u * 8;
-      if (m == 0) {
+    } else if (my.on(p)) {
+      float* at = part + my.u * 8;
+      if (my.m == 0) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] = val(i, e);
       } else {
@@ -285,42 +313,39 @@ __device__ __forceinline__ void channel_sums(const Gn& p, const Mine& my, float*
       ActT<float>::st8(at, s);
     }
   }
+  if (my.units < kGnThreads && my.rl < my.lanes) ActT<float>::st8(part + my.rl * p.C + my.u0 * 8, s);
 }
 
 inline size_t gn_part_floats(const Gn& p) { return p.C < 8 * kGnThreads ? 8 * kGnThreads : p.C; }
 
 template <typename T, bool SILU>
-__global__ void __launch_bounds__(kGnThreads) gn_fwd_sample_kernel(Gn p, const T* __restrict__ x, const float* __restrict__ scale,
+__global__ void __launch_bounds__(kGnThreads, 4) gn_fwd_sample_kernel(Gn p, int items, const T* __restrict__ x, const float* __restrict__ scale,
                                                                    const float* __restrict__ bias, T* __restrict__ y, float* __restrict__ mean,
                                                                    float* __restrict__ rstd) {
   using R = Raw8<T>;
-  constexpr int IT = kGnItems<T>;
   extern __shared__ float4 sm4[];
-  float* part = reinterpret_cast<float*>(sm4);
+  typename R::V* hold = reinterpret_cast<typename R::V*>(sm4) + threadIdx.x;  // this thread's units of x
+  float* part = reinterpret_cast<float*>(sm4) + items * kGnThreads * (int)(sizeof(typename R::V) / 4);
   float* st = part + (p.C < 8 * kGnThreads ? 8 * kGnThreads : p.C);  // mean, rstd of each group
-  const Mine my(p);
+  Mine my(p, items);
   const float inv = 1.0f / ((float)p.M * (float)p.cg);
   for (long long n = blockIdx.x; n < p.N; n += gridDim.x) {
     const T* xn = x + n * p.M * p.C;
-    typename R::V raw[IT];
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      int m, u;
-      raw[i] = my.at(p, i, m, u) ? R::ld(xn + (long long)m * p.C + u * 8) : R::zero();
-    }
+    my.first();
+    for (int i = 0; i < items; ++i, my.next())
+      if (my.on(p)) hold_copy(hold + i * kGnThreads, xn + (long long)my.m * p.C + my.u * 8);
+    hold_wait();
     float v[8];
-    channel_sums<IT>(p, my, part, [&](int i, int e) {
-      if (e == 0) R::wide(raw[i], v);
+    channel_sums(p, my, part, [&](int i, int e) {
+      if (e == 0) R::wide(hold[i * kGnThreads], v);
       return v[e];
     });
     __syncthreads();
     group_sums(p, part, my.lanes, [&](int g, float s) { st[g] = s * inv; });
     __syncthreads();
-    channel_sums<IT>(p, my, part, [&](int i, int e) {
-      int m, u;
-      my.at(p, i, m, u);
-      if (e == 0) R::wide(raw[i], v);
-      const float d = v[e] - st[(u * 8 + e) / p.cg];
+    channel_sums(p, my, part, [&](int i, int e) {
+      if (e == 0) R::wide(hold[i * kGnThreads], v);
+      const float d = v[e] - st[my.group(e)];
       return d * d;
     });
     __syncthreads();
@@ -331,59 +356,57 @@ __global__ void __launch_bounds__(kGnThreads) gn_fwd_sample_kernel(Gn p, const T
       if (rstd != nullptr) rstd[n * p.groups + g] = r;
     });
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      int m, u;
-      if (!my.at(p, i, m, u)) continue;
+    my.first();
+    for (int i = 0; i < items; ++i, my.next()) {
+      if (!my.on(p)) continue;
       float sc[8], bi[8];
-      ld8f(scale + u * 8, true, sc);
-      ld8f(bias + u * 8, bias != nullptr, bi);
-      R::wide(raw[i], v);
+      ld8f(scale + my.u * 8, true, sc);
+      ld8f(bias + my.u * 8, bias != nullptr, bi);
+      R::wide(hold[i * kGnThreads], v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int g = (u * 8 + e) / p.cg;
+        const int g = my.group(e);
         v[e] = act<SILU>(fmaf((v[e] - st[g]) * st[p.groups + g], sc[e], bi[e]));
       }
-      ActT<T>::st8(y + (n * p.M + m) * p.C + u * 8, v);
+      ActT<T>::st8(y + (n * p.M + my.m) * p.C + my.u * 8, v);
     }
     __syncthreads();  // the next sample's sums
   }
 }
 
 template <typename T, bool SILU>
-__global__ void __launch_bounds__(kGnThreads) gn_bwd_sample_kernel(Gn p, const T* __restrict__ dy, const T* __restrict__ x,
+__global__ void __launch_bounds__(kGnThreads, 3) gn_bwd_sample_kernel(Gn p, int items, const T* __restrict__ dy, const T* __restrict__ x,
                                                                    const float* __restrict__ scale, const float* __restrict__ bias,
                                                                    const float* __restrict__ mean, const float* __restrict__ rstd,
                                                                    float* __restrict__ dx, float* __restrict__ out) {
   using R = Raw8<T>;
-  constexpr int IT = kGnItems<T>;
   extern __shared__ float4 sm4[];
   const int pf = p.C < 8 * kGnThreads ? 8 * kGnThreads : p.C;
-  float *part = reinterpret_cast<float*>(sm4), *acc = part + pf, *st = acc + 2 * p.C;
+  typename R::V* hold = reinterpret_cast<typename R::V*>(sm4) + threadIdx.x;  // this thread's units of x, then of dy
+  float *part = reinterpret_cast<float*>(sm4) + 2 * items * kGnThreads * (int)(sizeof(typename R::V) / 4), *acc = part + pf, *st = acc + 2 * p.C;
   pdl_trigger();
   for (int c = threadIdx.x; c < 2 * p.C; c += kGnThreads) acc[c] = 0.f;
-  const Mine my(p);
+  Mine my(p, items);
   const float inv = 1.0f / ((float)p.M * (float)p.cg);
   for (long long n = blockIdx.x; n < p.N; n += gridDim.x) {
-    typename R::V rx[IT], ry[IT];
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      int m, u;
-      const bool on = my.at(p, i, m, u);
-      const long long at = (n * p.M + m) * p.C + u * 8;
-      rx[i] = on ? R::ld(x + at) : R::zero();
-      ry[i] = on ? R::ld(dy + at) : R::zero();
+    my.first();
+    for (int i = 0; i < items; ++i, my.next()) {
+      if (!my.on(p)) continue;
+      const long long at = (n * p.M + my.m) * p.C + my.u * 8;
+      hold_copy(hold + i * kGnThreads, x + at);
+      hold_copy(hold + (items + i) * kGnThreads, dy + at);
     }
+    hold_wait();
     const float *mu = mean + n * p.groups, *rv = rstd + n * p.groups;
     float sc[8], bi[8], xh[8], da[8];
-    auto unit = [&](int i, int u) {  // xh and da of a unit
-      ld8f(scale + u * 8, true, sc);
-      ld8f(bias + u * 8, SILU && bias != nullptr, bi);
-      R::wide(rx[i], xh);
-      R::wide(ry[i], da);
+    auto unit = [&](int i) {  // xh and da of a unit
+      ld8f(scale + my.u * 8, true, sc);
+      ld8f(bias + my.u * 8, SILU && bias != nullptr, bi);
+      R::wide(hold[i * kGnThreads], xh);
+      R::wide(hold[(items + i) * kGnThreads], da);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int g = (u * 8 + e) / p.cg;
+        const int g = my.group(e);
         xh[e] = (xh[e] - mu[g]) * rv[g];
         da[e] = dact<SILU>(da[e], fmaf(xh[e], sc[e], bi[e]));
       }
@@ -391,10 +414,8 @@ __global__ void __launch_bounds__(kGnThreads) gn_bwd_sample_kernel(Gn p, const T
     // sums of da, then of da xh: per channel into the column sums, per group with the scale
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      channel_sums<IT>(p, my, part, [&](int i, int e) {
-        int m, u;
-        my.at(p, i, m, u);
-        if (e == 0) unit(i, u);
+      channel_sums(p, my, part, [&](int i, int e) {
+        if (e == 0) unit(i);
         return k == 0 ? da[e] : da[e] * xh[e];
       });
       __syncthreads();
@@ -408,17 +429,16 @@ __global__ void __launch_bounds__(kGnThreads) gn_bwd_sample_kernel(Gn p, const T
       group_sums(p, part, 1, [&](int g, float s) { st[k * p.groups + g] = s * inv; });
       __syncthreads();
     }
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      int m, u;
-      if (!my.at(p, i, m, u)) continue;
-      unit(i, u);
+    my.first();
+    for (int i = 0; i < items; ++i, my.next()) {
+      if (!my.on(p)) continue;
+      unit(i);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int g = (u * 8 + e) / p.cg;
+        const int g = my.group(e);
         da[e] = rv[g] * (da[e] * sc[e] - st[g] - xh[e] * st[p.groups + g]);
       }
-      ActT<float>::st8(dx + (n * p.M + m) * p.C + u * 8, da);
+      ActT<float>::st8(dx + (n * p.M + my.m) * p.C + my.u * 8, da);
     }
     __syncthreads();
   }
@@ -743,6 +763,7 @@ struct GnPlan {
   Gn p;
   GnForm form;
   int G, gp, segs, grid;  // lanes
+  int items;              // a sample's units in a thread
   Part q, qa;             // parts of the sums, and of the forward's second pass
   size_t fwd, bwd;        // workspace
   int rows;               // partial rows of the backward's column sums
@@ -757,7 +778,7 @@ int gn_plan(int N, int M, int C, int groups, int dtype, GnPlan& pl) {
   Gn& p = pl.p;
   p.N = N; p.M = M; p.C = C; p.groups = groups; p.cg = C / groups;
   pl.fwd = pl.bwd = 0;
-  const int items = gn_sample_items(p);
+  const int items = pl.items = gn_sample_items(p);
   if (M == 1 && p.cg % 8 == 0 && p.cg <= 256) {
     pl.form = kLanes;
     pl.G = 1;
@@ -771,7 +792,7 @@ int gn_plan(int N, int M, int C, int groups, int dtype, GnPlan& pl) {
     pl.bwd = (size_t)pl.rows * 2 * C * sizeof(float);
   } else if (C <= kGnSampleDim && items <= (dtype == SS_F32 ? kGnItems<float> : kGnItems<__nv_bfloat16>)) {
     pl.form = kSample;
-    pl.grid = std::min(N, 152 * 4);
+    pl.grid = std::min(N, 152 * 8);
     pl.rows = pl.grid;
     pl.bwd = (size_t)pl.rows * 2 * C * sizeof(float);
   } else {
@@ -825,10 +846,10 @@ int fwd(const GnPlan& pl, const T* x, const float* scale, const float* bias, T* 
   if (pl.form == kLanes) {
     GN_LANES(fwd_lanes, pl, x, scale, bias, y, mean, rstd, s)
   } else if (pl.form == kSample) {
-    const size_t smem = (gn_part_floats(p) + 2 * p.groups) * sizeof(float);
-    if (cudaFuncSetAttribute(gn_fwd_sample_kernel<T, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-      return SS_ERR_CUDA;
-    gn_fwd_sample_kernel<T, SILU><<<pl.grid, kGnThreads, smem, s>>>(p, x, scale, bias, y, mean, rstd);
+    const size_t smem = pl.items * kGnThreads * sizeof(typename Raw8<T>::V) + (gn_part_floats(p) + 2 * p.groups) * sizeof(float);
+    const auto kernel = gn_fwd_sample_kernel<T, SILU>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SS_ERR_CUDA;
+    kernel<<<pl.grid, kGnThreads, smem, s>>>(p, pl.items, x, scale, bias, y, mean, rstd);
   } else {
     const Part& q = pl.q;
     float* part = static_cast<float*>(ws);
@@ -865,10 +886,10 @@ int bwd(const GnPlan& pl, const T* dy, const T* x, const float* scale, const flo
   if (pl.form == kLanes) {
     GN_LANES(bwd_lanes, pl, dy, x, scale, bias, mean, rstd, dx, part, s)
   } else if (pl.form == kSample) {
-    const size_t smem = (gn_part_floats(p) + 2 * p.C + 2 * p.groups) * sizeof(float);
-    if (cudaFuncSetAttribute(gn_bwd_sample_kernel<T, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-      return SS_ERR_CUDA;
-    gn_bwd_sample_kernel<T, SILU><<<pl.grid, kGnThreads, smem, s>>>(p, dy, x, scale, bias, mean, rstd, dx, part);
+    const size_t smem = 2 * pl.items * kGnThreads * sizeof(typename Raw8<T>::V) + (gn_part_floats(p) + 2 * p.C + 2 * p.groups) * sizeof(float);
+    const auto kernel = gn_bwd_sample_kernel<T, SILU>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SS_ERR_CUDA;
+    kernel<<<pl.grid, kGnThreads, smem, s>>>(p, pl.items, dy, x, scale, bias, mean, rstd, dx, part);
   } else {
     const Part& q = pl.q;
     float2* means = reinterpret_cast<float2*>(part + (size_t)p.N * q.splits * 2 * p.C);

@@ -20,7 +20,9 @@ reordering beyond what the definition states:
   depthwise causal conv1d backward, full-sequence and per-step (mamba-rs
   ``backward_ops.rs``, ``backward_conv1d_step``);
 * ``rmsnorm.rmsnorm_bwd_ref`` — the RMSNorm backward (mamba-rs
-  ``backward_ops.rs``, ``backward_rms_norm``).
+  ``backward_ops.rs``, ``backward_rms_norm``);
+* ``deltarule`` — the gated delta rule token by token, its gradient and its
+  single step; ``groupnorm`` — group norm (+ SiLU) and its gradient.
 
 Pins (tests/test_oracle_*.py, CPU only): central finite differences, the L=1
 closed form, the A->0 cumulative-sum limit, the constant-input geometric

@@ -254,7 +254,8 @@ def test_tokens_of_very_different_lengths(ss):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("B,H,G,K,V,decay", [(1, 1, 1, 8, 8, True), (3, 4, 2, 40, 72, False), (2, 32, 32, 128, 128, True),
-                                             (300, 2, 1, 64, 128, True), (1, 3, 3, 120, 8, True), (200, 1, 1, 128, 40, False)])
+                                             (300, 2, 1, 64, 128, True), (1, 3, 3, 120, 8, True), (200, 1, 1, 128, 40, False),
+                                             (40, 24, 8, 128, 104, True), (520, 1, 1, 64, 64, True), (513, 2, 2, 8, 8, True)])
 def test_step(ss, B, H, G, K, V, decay, dtype):
     """Every term of the new state passes two sums of K products in fp32 and five roundings: (2 sqrt(K) + 5) 2^-24 of the norm, and
     o one more sum."""
@@ -397,6 +398,34 @@ def test_offsets_past_32_bits(ss):
     tol = 2 * _tol(tail, "bf16", False, 1)
     _near(o[:, -100:], _np(o2[:, -100:]), 2.0 ** -7 + tol, "o")  # two results that round apart
     _near(h, _np(h2), tol, "h")
+
+
+@pytest.mark.parametrize("dtype,L,H,V,K,tail", [("bf16", 270_080, 64, 128, 8, 320), ("f32", 65_600, 512, 64, 8, 320)])
+def test_gradient_offsets_past_32_bits(ss, dtype, L, H, V, K, tail):
+    """As above for the backward: v, do, dv, r and o of over 2^31 elements.  Nothing comes back from the tail, and into its last
+    100 tokens comes nothing from before it, so all of their gradients equal those of a call on the tail alone."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    unit = lambda t: t / t.norm(dim=-1, keepdim=True)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    assert L * H * V > 2 ** 31
+    q, k = (unit(torch.randn(1, L, 1, K, device="cuda", generator=gen)).to(dt) for _ in range(2))
+    v, do = (torch.ones(1, L, H, V, device="cuda", dtype=dt) for _ in range(2))
+    for t in (v, do):
+        t[:, -tail:] = torch.randn(1, tail, H, V, device="cuda", generator=gen).to(dt)
+    g = torch.full((1, L, H), -2.0, device="cuda")
+    beta = torch.rand(1, L, H, device="cuda", generator=gen)
+    _, ckpt, _ = ss.deltarule_fwd(q, k, v, g, beta)
+    got = ss.deltarule_bwd(q, k, v, g, beta, ckpt, do, want_dh0=False)
+    del ckpt
+    cut = lambda t: t[:, -tail:].contiguous()
+    c = [cut(t) for t in (q, k, v, g, beta)]
+    _, ckpt, _ = ss.deltarule_fwd(*c)
+    ref = ss.deltarule_bwd(*c, ckpt, cut(do), want_dh0=False)
+    typed = 2.0 ** -7 if dtype == "bf16" else 0.0  # two results that round apart
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        tol = 2 * _tol(tail, dtype, False, 3) * 64 ** 0.5 + (typed if n in ("dq", "dk", "dv") else 0.0)  # (dg: sums over a chunk)
+        _near(got[n][:, -100:], _np(ref[n][:, -100:]), tol, n)
 
 
 def test_refusals(ss):
