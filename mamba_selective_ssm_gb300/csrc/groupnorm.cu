@@ -16,8 +16,8 @@
 // of moments.  The backward's column sums are joined by colsum_kernel in fixed order.
 //
 // bf16 with SiLU, floors at 6.7 TB/s in brackets: 8192 x 1 x 4096 in 32 groups, forward 28 us (20; instructions of short rows:
-// 61 % of the issue slots), backward 50 + 6 (40); 4 x 2048 x 4096 forward 44 (20; x is read twice, the second time from L2 in
-// part).  fp32, 8 x 2048 x 1536 in 24 groups, backward 90 (45; dy and x twice).  The forms at each other's sizes: the first of
+// 61 % of the issue slots), backward 50 + 6 (40); 4 x 2048 x 4096 forward 43 (20; x is read twice, the second time from L2 in
+// part).  fp32, 8 x 2048 x 1536 in 24 groups, backward 89 (45; dy and x twice).  The forms at each other's sizes: the first of
 // these with a sample in a CTA 105 and 283 us; 4096 x 4 x 512 with a sample in a CTA 34 and 60, in parts 203 and 184;
 // 16 x 4 x 512 5.1 and 10, in parts 12.4 and 15; 8000 x 2 x 4096 136 and 410, in parts 1750 and 1890.
 #include <algorithm>
@@ -62,6 +62,24 @@ template <typename T>
 __device__ __forceinline__ void st4p(T* p, const float2 (&o)[4]) {
   const float x[8] = {o[0].x, o[0].y, o[1].x, o[1].y, o[2].x, o[2].y, o[3].x, o[3].y};
   ActT<T>::st8(p, x);
+}
+// In the second pass of the parts' form x (and dy) are read for the last time and the output is not read again: marked so, more of
+// them is still in L2 from the first pass (4 x 2048 x 4096 in bf16: 45.0 -> 42.9 us; backward of 8 x 2048 x 1536 in fp32 90.4 ->
+// 88.6).
+template <typename T>
+__device__ __forceinline__ typename Raw8<T>::V ld_last(const T* p) {
+  if constexpr (sizeof(T) == 4) return typename Raw8<T>::V{__ldcs(reinterpret_cast<const float4*>(p)), __ldcs(reinterpret_cast<const float4*>(p) + 1)};
+  else return __ldcs(reinterpret_cast<const uint4*>(p));
+}
+template <typename T>
+__device__ __forceinline__ void st4_last(T* p, const float2 (&o)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(o[0].x, o[0].y, o[1].x, o[1].y));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(o[2].x, o[2].y, o[3].x, o[3].y));
+  } else {
+    using A = ActT<__nv_bfloat16>;
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(A::pack2(o[0].x, o[0].y), A::pack2(o[1].x, o[1].y), A::pack2(o[2].x, o[2].y), A::pack2(o[3].x, o[3].y)));
+  }
 }
 __device__ __forceinline__ float2 sigmoid2(float2 t) {
   const float2 e = ex2_2(mul2(t, bc2(-kLog2e))), d = add2(e, bc2(1.f));
@@ -612,7 +630,7 @@ __global__ void __launch_bounds__(kGnThreads, 2) gn_apply_kernel(Gn p, Part q, c
     typename R::V raw[A];
 #pragma unroll
     for (int u = 0; u < A; ++u)
-      if (m - u * w.lanes >= w.m0) raw[u] = R::ld(x + base + (long long)(m - u * w.lanes) * p.C);
+      if (m - u * w.lanes >= w.m0) raw[u] = ld_last<T>(x + base + (long long)(m - u * w.lanes) * p.C);
 #pragma unroll
     for (int u = 0; u < A; ++u) {
       if (m - u * w.lanes < w.m0) break;
@@ -620,7 +638,7 @@ __global__ void __launch_bounds__(kGnThreads, 2) gn_apply_kernel(Gn p, Part q, c
       wide4<T>(raw[u], v);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = act2<SILU>(fma2(add2(v[e], mu[e]), sc[e], bi[e]));
-      st4p<T>(y + base + (long long)(m - u * w.lanes) * p.C, v);
+      st4_last<T>(y + base + (long long)(m - u * w.lanes) * p.C, v);
     }
   }
 }
@@ -735,8 +753,8 @@ __global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_apply_kernel(Gn p, Part 
     for (int u = 0; u < A; ++u)
       if (m - u * w.lanes >= w.m0) {
         const long long at = base + (long long)(m - u * w.lanes) * p.C;
-        rx[u] = R::ld(x + at);
-        ry[u] = R::ld(dy + at);
+        rx[u] = ld_last<T>(x + at);
+        ry[u] = ld_last<T>(dy + at);
       }
 #pragma unroll
     for (int u = 0; u < A; ++u) {
@@ -750,7 +768,7 @@ __global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_apply_kernel(Gn p, Part 
         da[e] = mul2(dact2<SILU>(da[e], fma2(xh[e], sc[e], bi[e])), sc[e]);
         da[e] = fma2(rv[e], da[e], fma2(xh[e], k1[e], k0[e]));
       }
-      st4p<float>(dx + base + (long long)(m - u * w.lanes) * p.C, da);
+      st4_last<float>(dx + base + (long long)(m - u * w.lanes) * p.C, da);
     }
   }
 }

@@ -49,6 +49,7 @@ CASES = [
     (1, 1, 8, 1), (1, 1, 8, 8), (3, 1, 16, 4), (5, 1, 4096, 32), (700, 1, 768, 6), (9, 1, 2048, 8), (2, 1, 24, 3), (40, 1, 520, 13),  # tokens
     (1000, 1, 4096, 1), (3, 1, 8192, 16), (6, 1, 512, 128), (4, 1, 1024, 1),  # tokens, groups past the lanes or below a vector
     (3, 7, 128, 32), (100, 20, 24, 3), (64, 2, 768, 6), (7, 3, 40, 10), (300, 16, 64, 8),  # samples that a CTA holds
+    (3, 2, 8192, 8192), (2, 1, 8192, 4096), (5, 4, 2056, 257), (1300, 2, 1024, 16), (3, 5, 72, 9), (4, 60, 200, 25),
     (2, 500, 64, 4), (1, 5000, 512, 1), (9, 33, 4096, 32), (2, 300, 1536, 24), (1, 4, 32768, 8), (1, 1, 32768, 2), (3, 1000, 8, 2),  # in parts
     (2, 129, 4104, 27), (1, 20000, 8, 1), (4, 100, 96, 32),
 ]
