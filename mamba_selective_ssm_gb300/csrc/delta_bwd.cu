@@ -338,7 +338,8 @@ __device__ __forceinline__ void mma_pair(float (&c0)[4], float (&c1)[4], const u
 }
 
 template <int KP, int VP>
-__global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_grad_kernel(Delta p, const float* __restrict__ ckpt, const float* __restrict__ dout,
+__global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_grad_kernel(Delta p, const float* __restrict__ ckpt,
+                                                                  const float* __restrict__ dout,
                                                                   const float* __restrict__ dS, const float* __restrict__ du,
                                                                   float* __restrict__ dq, float* __restrict__ dk, int heads,
                                                                   float* __restrict__ dg, float* __restrict__ dbeta) {
@@ -800,7 +801,8 @@ int grads(const BwdPlan& pl, const BwdArgs& x, cudaStream_t s) {
   constexpr size_t smem = GradSmem<KP, VP>::bytes;
   static_assert(smem <= 227 * 1024, "a chunk's tiles fit shared memory");
   const bool parts = a.H > a.G;
-  const int rc = delta_launch_next(delta_grad_kernel<KP, VP>, grid, kGradThreads, smem, s, pl.p, x.ckpt, static_cast<const float*>(x.dout), x.dS, x.du,
+  const int rc = delta_launch_next(delta_grad_kernel<KP, VP>, grid, kGradThreads, smem, s, pl.p, x.ckpt, static_cast<const float*>(x.dout), x.dS,
+                            x.du,
                             parts ? x.pq : static_cast<float*>(x.dq), parts ? x.pk : static_cast<float*>(x.dk), parts ? a.H : a.G, x.dg, x.dbeta);
   return rc != SS_OK || !parts ? rc : share<float>(pl, x, s);
 }

@@ -303,8 +303,8 @@ int walk(const FwdPlan& pl, const float* h0, void* o, float* ckpt, float* h_last
   // A chunk's tiles have two places where these fit and the CTAs are no more than the SMs; with more CTAs two an SM, each with
   // one place, are faster than one with two (192 heads of 64 x 64: 363 us for 497).
   const int sb = St::bytes(warps), stages = 2 * sb <= 226 * 1024 && bh * nvt <= 152 ? 2 : 1;
-  return delta_launch_next(delta_fwd_kernel<KP>, (unsigned)(bh * nvt), 32 * warps, (size_t)sb * stages, s, pl.p, h0, static_cast<float*>(o), ckpt, h_last,
-                    stages, sb);
+  return delta_launch_next(delta_fwd_kernel<KP>, (unsigned)(bh * nvt), 32 * warps, (size_t)sb * stages, s, pl.p, h0, static_cast<float*>(o), ckpt,
+                           h_last, stages, sb);
 }
 
 }  // namespace

@@ -6,9 +6,9 @@
 //   dq = scale e^c do S0^T + E K      dk = -e^c dR S0^T + e^{c_last - c} u dS^T + E^T Q + (F + F^T) K
 // dq and dk are rounded to bf16; their fp32 operands are two bf16 terms (2^-15).  Products run with the columns of K as the
 // 128 rows of an MMA; S0, dS, u and dR lie in shared memory by columns of V, as they come from memory, and are contracted down
-// their rows.  4 x 2048 tokens of 32 heads of 128 x 128: 422 us, 3.2 TB/s.  A CTA an SM (208 KB; tensor memory is taken whole),
+// their rows.  4 x 2048 tokens of 32 heads of 128 x 128: 415 us, 3.2 TB/s.  A CTA an SM (208 KB; tensor memory is taken whole),
 // whose steps wait for one another: the sums and operands along V a third of a chunk's time, the states' loads and terms a third.
-// A CTA for each chunk took 438 us, and where the heads' parts are added up (32 heads on 4, 128 x 64) 384 for 351.
+// A CTA for each chunk took 438 us, and where the heads' parts are added up (32 heads on 4, 128 x 64) 384 for 346.
 #include <algorithm>
 
 #include "delta_tc.cuh"
@@ -70,8 +70,15 @@ __global__ void __launch_bounds__(kGT, 1) delta_grad_tc_kernel(Delta p, const __
   auto marks = [&](long long it) {  // the forward's states, and after them r and o, of a chunk's batch row and head
     return ckpt + it / a.nck * delta_ckpt_floats(a.nck, a.K, a.V);
   };
-  // r, o and du of a chunk towards L2, a line of 128 bytes at a time (with dS1 as well: 481 us where this gives 442, as the
-  // states' lines come back out of L2 before they are read)
+  // r, o and du of a chunk towards L2, a line of 128 bytes at a time, under the first products; its states under the second.  (427 us
+  // without the states or with r, o and du asked for earlier, 415 so; all of it before this chunk's own loads: 481.)
+  auto states_ahead = [&](long long it) {
+    const float* st = marks(it) + it % a.nck * a.K * a.V;
+    for (int i = tid; i < a.K * a.V / 32; i += kGT) {
+      prefetch_l2(st + i * 32);
+      prefetch_l2(dS + it * a.K * a.V + i * 32);
+    }
+  };
   auto ahead = [&](long long it) {
     const long long ck = it % a.nck;
     const float* ro = marks(it) + (long long)(a.nck + 1) * a.K * a.V + ck * kDC * a.V;
@@ -150,7 +157,6 @@ __global__ void __launch_bounds__(kGT, 1) delta_grad_tc_kernel(Delta p, const __
     float4 X[SC / 4];
     state(s0, X);
     ok = chain_wait(&bar[L::kIn], par);
-    if (next < items) ahead(next);
     if (valid < kDC && t0 + valid < a.L) {  // the row ends inside the tensor: what follows is not its own
       if (warp == 0) tok_clear(sb + L::dy, vp, valid, lane);
       if (warp == 1) tok_clear(sb + L::k, kp, valid, lane);
@@ -282,6 +288,7 @@ __global__ void __launch_bounds__(kGT, 1) delta_grad_tc_kernel(Delta p, const __
         if (2 * lane + 1 < rows) dg[(tok + 2 * lane + 1) * a.H + h] = 2 * lane + 1 < valid ? x + (s[1] + after) : 0.f;
       }
     }
+    if (next < items) ahead(next);
     ok = chain_wait(&bar[L::kM0], par) && ok;
     tc_fence_after_sync();
     put_state(X);  // dS where S0 was
@@ -337,6 +344,7 @@ __global__ void __launch_bounds__(kGT, 1) delta_grad_tc_kernel(Delta p, const __
       }
       __syncwarp();
     }
+    if (next < items) states_ahead(next);
     ok = chain_wait(&bar[L::kM1], par) && ok;
     tc_fence_after_sync();
     if (tid == 0 && next < items && ok) load(next);  // (their places have been read)
@@ -424,8 +432,8 @@ int run(const Delta& p, const float* ckpt, const void* dout, const float* dS, co
     return SS_ERR_CUDA;
   static_assert(GradTc<KP>::bytes <= 227 * 1024, "a chunk's tiles fit shared memory");
   const unsigned grid = (unsigned)std::min<long long>(kGGrid, (long long)a.B * a.H * a.nck);
-  return delta_launch_next(delta_grad_tc_kernel<KP, TO>, grid, kGT, GradTc<KP>::bytes, s, p, maps, ckpt, dS, du, static_cast<TO*>(dq), static_cast<TO*>(dk),
-                    kTile ? a.G : a.H, dg, dbeta);
+  return delta_launch_next(delta_grad_tc_kernel<KP, TO>, grid, kGT, GradTc<KP>::bytes, s, p, maps, ckpt, dS, du, static_cast<TO*>(dq),
+                           static_cast<TO*>(dk), kTile ? a.G : a.H, dg, dbeta);
 }
 
 }  // namespace

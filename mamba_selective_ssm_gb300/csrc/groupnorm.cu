@@ -68,8 +68,12 @@ __device__ __forceinline__ void st4p(T* p, const float2 (&o)[4]) {
 // 88.6).
 template <typename T>
 __device__ __forceinline__ typename Raw8<T>::V ld_last(const T* p) {
-  if constexpr (sizeof(T) == 4) return typename Raw8<T>::V{__ldcs(reinterpret_cast<const float4*>(p)), __ldcs(reinterpret_cast<const float4*>(p) + 1)};
-  else return __ldcs(reinterpret_cast<const uint4*>(p));
+  if constexpr (sizeof(T) == 4) {
+    const float4* f = reinterpret_cast<const float4*>(p);
+    return typename Raw8<T>::V{__ldcs(f), __ldcs(f + 1)};
+  } else {
+    return __ldcs(reinterpret_cast<const uint4*>(p));
+  }
 }
 template <typename T>
 __device__ __forceinline__ void st4_last(T* p, const float2 (&o)[4]) {
@@ -78,7 +82,8 @@ __device__ __forceinline__ void st4_last(T* p, const float2 (&o)[4]) {
     __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(o[2].x, o[2].y, o[3].x, o[3].y));
   } else {
     using A = ActT<__nv_bfloat16>;
-    __stcs(reinterpret_cast<uint4*>(p), make_uint4(A::pack2(o[0].x, o[0].y), A::pack2(o[1].x, o[1].y), A::pack2(o[2].x, o[2].y), A::pack2(o[3].x, o[3].y)));
+    __stcs(reinterpret_cast<uint4*>(p),
+           make_uint4(A::pack2(o[0].x, o[0].y), A::pack2(o[1].x, o[1].y), A::pack2(o[2].x, o[2].y), A::pack2(o[3].x, o[3].y)));
   }
 }
 __device__ __forceinline__ float2 sigmoid2(float2 t) {

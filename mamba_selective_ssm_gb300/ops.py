@@ -572,7 +572,7 @@ def deltarule_fwd(q, k, v, g, beta, h0=None, scale=None, lengths=None, want_ckpt
 
     ``q, k`` [B, L, G, K], ``v`` [B, L, H, V] and ``lengths`` are as in ``linattn_fwd``; ``g`` (log decays, or None) and
     ``beta`` are fp32 [B, L, H]; keys are normally of length one.  ``scale`` is ``K ** -0.5`` unless given.  ``ckpt``
-    (None unless ``want_ckpt``) is what ``deltarule_bwd`` starts from.
+    (None unless ``want_ckpt``) is what ``deltarule_bwd`` starts from; a call that makes one uses no workspace.
 
     A NaN or infinity in a live token can reach the other tokens of its chunk of 64, also earlier ones."""
     B, L, H, G, K, V = _linattn_sizes(q, v)
