@@ -467,9 +467,9 @@ int linattn_step(const void* q, const void* k, const void* v, const float* g, in
  * Rounding.  All sums and states are fp32.  Products run in 16 bits with fp32
  * sums.  With bf16 activations these are operands as they are, and an fp32
  * operand is three bf16 terms (all its 24 bits) where the result ends in fp32
- * (states, dg, dbeta, dh0, the states' way into o), two (2^-15) where it is
- * rounded to bf16 alone (u in o without ckpt, dq, dk).  With fp32 activations
- * every operand is two scaled fp16 terms (22 bits).
+ * (states, dg, dbeta, dh0) or in o, which has the same bits with and without
+ * ckpt, and two (2^-15) in dq and dk.  With fp32 activations every operand is
+ * two scaled fp16 terms (22 bits).
  * Alignment: 16 bytes for every pointer but g, beta, lengths, dg, dbeta (4).
  *
  * deltarule_ckpt_size — floats that a checkpoint holds for each batch row and

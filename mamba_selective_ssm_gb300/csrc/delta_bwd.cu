@@ -754,7 +754,6 @@ int bwd_plan(int B, int L, int H, int G, int K, int V, int dtype, BwdPlan& pl) {
   LinAttn& a = pl.p.a;
   a.B = B; a.L = L; a.H = H; a.G = G; a.K = K; a.V = V;
   a.nck = (L + kDC - 1) / kDC;
-  pl.p.pterms = dtype == SS_F32 ? 2 : 3;
   const size_t items = pl.p.items();
   pl.ds = items * K * V * sizeof(float);
   pl.du = items * kDC * V * sizeof(float);

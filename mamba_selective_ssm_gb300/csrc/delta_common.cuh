@@ -26,7 +26,7 @@ namespace ssk {
 constexpr int kDC = 64;        // tokens of a chunk
 constexpr int kDVec = 272;     // floats of a chunk's scalars: into, rest, beta', M's row scales (64 each), e^{c_last}
 constexpr int kDMBytes = kDC * kDC * 4;  // M of a chunk: two fp16 terms,
-constexpr int kDMTerms = kDC * kDC * 6;  // or three of bf16
+constexpr int kDMTerms = kDC * kDC * 6;  // or three of bf16; P alike
 
 // One call's arguments.  a: q, k, v, g (null: no decay), lengths, sizes as in linear attention.
 struct Delta {
@@ -35,17 +35,16 @@ struct Delta {
   // what delta_prep_kernel leaves for each (batch row, head, chunk)
   unsigned char *M, *P;  // operand tiles
   float* vec;
-  int pterms;  // terms of P
 
   // the room they take, in bytes, and their places in it
-  size_t prep_bytes(bool bf16) const { return items() * (m_bytes(bf16) + (size_t)kDC * kDC * 2 * pterms + kDVec * sizeof(float)); }
+  size_t prep_bytes(bool bf16) const { return items() * (2 * tile_bytes(bf16) + kDVec * sizeof(float)); }
   void place(void* at, bool bf16) {
     M = static_cast<unsigned char*>(at);
-    P = M + items() * m_bytes(bf16);
-    vec = reinterpret_cast<float*>(P + items() * ((size_t)kDC * kDC * 2 * pterms));
+    P = M + items() * tile_bytes(bf16);
+    vec = reinterpret_cast<float*>(P + items() * tile_bytes(bf16));
   }
   size_t items() const { return (size_t)a.B * a.H * a.nck; }
-  static size_t m_bytes(bool bf16) { return bf16 ? kDMTerms : kDMBytes; }
+  static size_t tile_bytes(bool bf16) { return bf16 ? kDMTerms : kDMBytes; }
 };
 
 template <typename T>
@@ -300,11 +299,11 @@ __device__ __forceinline__ void store_tokens(float* __restrict__ dst, long long 
 }  // namespace ssk
 
 namespace ssh {
-// Launches delta_prep_kernel for all chunks of a call; P in p.pterms terms.
+// Launches delta_prep_kernel for all chunks of a call.
 int delta_prep(const ssk::Delta& p, int dtype, cudaStream_t s);
-// The chunks' walk in bf16, after delta_prep with P in two terms, or three with ckpt.
+// The chunks' walk in bf16, after delta_prep.
 int delta_fwd_bf16(const ssk::Delta& p, const float* h0, void* o, float* ckpt, float* h_last, cudaStream_t s);
-// The backward's walk in bf16, after delta_prep with P in three terms: dv, dh0, and dS ([K / 4][V][4]) and du ([16][V][4]) of
+// The backward's walk in bf16: dv, dh0, and dS ([K / 4][V][4]) and du ([16][V][4]) of
 // every chunk.
 int delta_back_bf16(const ssk::Delta& p, const void* dout, const float* dh_last, void* dv, float* dS, float* du, float* dh0, cudaStream_t s);
 // The other gradients in bf16, chunk by chunk.  dq, dk: rows of `heads` heads, bf16 or (parts) fp32

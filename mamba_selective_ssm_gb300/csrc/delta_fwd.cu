@@ -280,14 +280,13 @@ struct FwdPlan {
   size_t bytes;
 };
 
-int fwd_plan(int B, int L, int H, int G, int K, int V, int dtype, bool train, FwdPlan& pl) {
+int fwd_plan(int B, int L, int H, int G, int K, int V, int dtype, FwdPlan& pl) {
   const int rc = delta_validate(B, L, H, G, K, V, dtype);
   if (rc != SS_OK) return rc;
   pl.p = Delta{};
   LinAttn& a = pl.p.a;
   a.B = B; a.L = L; a.H = H; a.G = G; a.K = K; a.V = V;
   a.nck = (L + kDC - 1) / kDC;
-  pl.p.pterms = dtype == SS_BF16 && train ? 3 : 2;  // (two for o alone)
   pl.bytes = pl.p.prep_bytes(dtype == SS_BF16);
   return SS_OK;
 }
@@ -311,13 +310,13 @@ int walk(const FwdPlan& pl, const float* h0, void* o, float* ckpt, float* h_last
 
 extern "C" size_t deltarule_ckpt_size(int L, int K, int V, int dtype) {
   FwdPlan pl;
-  if (fwd_plan(1, L, 1, 1, K, V, dtype, true, pl) != SS_OK) return 0;
+  if (fwd_plan(1, L, 1, 1, K, V, dtype, pl) != SS_OK) return 0;
   return (size_t)delta_ckpt_floats(pl.p.a.nck, K, V) + pl.bytes / sizeof(float);
 }
 
 extern "C" size_t deltarule_fwd_workspace_size(int B, int L, int H, int G, int K, int V, int dtype) {
   FwdPlan pl;
-  return fwd_plan(B, L, H, G, K, V, dtype, false, pl) == SS_OK ? pl.bytes : 0;
+  return fwd_plan(B, L, H, G, K, V, dtype, pl) == SS_OK ? pl.bytes : 0;
 }
 
 extern "C" int deltarule_fwd(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv, const float* g,
@@ -325,7 +324,7 @@ extern "C" int deltarule_fwd(const void* q, long long ldq, const void* k, long l
                              int H, int G, int K, int V, float scale, int dtype, void* workspace, size_t ws_bytes, void* stream) {
   if (!q || !k || !v || !beta || !o) return SS_ERR_NULL;
   FwdPlan pl;
-  int rc = fwd_plan(B, L, H, G, K, V, dtype, ckpt != nullptr, pl);
+  int rc = fwd_plan(B, L, H, G, K, V, dtype, pl);
   if (rc != SS_OK) return rc;
   if ((rc = linattn_ld_ok(ldq, G, K)) != SS_OK || (rc = linattn_ld_ok(ldk, G, K)) != SS_OK || (rc = linattn_ld_ok(ldv, H, V)) != SS_OK)
     return rc;

@@ -2,7 +2,7 @@
 // (batch row, head) with the state in registers (thread = one column of V and a quarter of K) and, as three bf16 terms, in tensor
 // memory, where it is the left operand of K S0 and Q S0.
 //   D1 = S K^T       R = v - e^c D1,  w = beta R  (three terms, tensor memory)
-//   D3 = w M^T       r = R - D3,  u = beta r,  e^{c_last - c} u (three terms, w's place),  u (two terms, shared memory)
+//   D3 = w M^T       r = R - D3,  u = beta r,  e^{c_last - c} u (three terms, w's place),  u (three terms, shared memory)
 //   D5 = .. K        S = e^{c_last} S + D5  (three terms, tensor memory)
 //   D2 = S Q^T, D4 = u P^T:  o = scale e^c D2 + D4, under the next chunk's D1
 // Sixteen warps compute, one issues the copies and MMAs; they meet at mbarriers with bounded waits.  With the left operand in
@@ -18,9 +18,10 @@ using namespace ssk;
 
 constexpr int kDW = 16, kDThreads = 32 * (kDW + 1);  // computing warps; one that issues
 
-template <int KP, bool TRAIN>
+template <int KP>
 struct DeltaTc {
-  static constexpr int UT = TRAIN ? 3 : 2;  // terms of u and P: o's own rounding needs two, its sum with do in dg three
+  // terms of u and P: with two, o was 2e-4 of its size from the rounded fp32 result, for 4e-5, and had other bits than with ckpt
+  static constexpr int UT = 3;
   static constexpr int NKP = KP / 64;  // panels of K
   static constexpr int kq = 0, place = NKP * kPanel, v = kq + 2 * place, m = v + 2 * kTok, p = m + 3 * kDTerm,
                        u = p + UT * kDTerm, vec = u + UT * kPanel, bar = vec + 2 * kDVec * 4;
@@ -40,7 +41,7 @@ template <int KP, bool TRAIN>
 __global__ void __launch_bounds__(kDThreads, 1) delta_fwd_tc_kernel(Delta p, const __grid_constant__ DeltaMaps maps, const float* __restrict__ h0,
                                                                     __nv_bfloat16* __restrict__ o, float* __restrict__ ckpt,
                                                                     float* __restrict__ h_last) {
-  using L = DeltaTc<KP, TRAIN>;
+  using L = DeltaTc<KP>;
   constexpr int UT = L::UT;
   constexpr int SC = KP / 4, TC = kDC / 4;  // a thread's columns of the state, its tokens of a product
   extern __shared__ __align__(1024) unsigned char raw[];
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(kDThreads, 1) delta_fwd_tc_kernel(Delta p, con
       if (!wait(L::kPr, par) || !wait(L::kU, par)) break;
       if (elect_one()) {
         tc_fence_after_sync();
-        lower(sb + L::p, TRAIN ? 0x041852u : 0x041u, TRAIN ? 6 : 3,
+        lower(sb + L::p, 0x041852u, 6,
               [&](uint32_t l, int s, uint64_t r, uint32_t id, bool add) {
                 mma_ss(tm + L::D4 + 16 * s, rows_desc(sb + L::u + l * kPanel, kPanel, s), r, id, add);
               });
@@ -423,7 +424,7 @@ int walk(const Delta& p, const float* h0, __nv_bfloat16* o, float* ckpt, float* 
   if (!delta_map(&maps.q, a.q, a.ldq, a.B, a.L, a.G, a.K) || !delta_map(&maps.k, a.k, a.ldk, a.B, a.L, a.G, a.K) ||
       !delta_map(&maps.v, a.v, a.ldv, a.B, a.L, a.H, a.V) || !delta_map(&maps.o, o, (long long)a.H * a.V, a.B, a.L, a.H, a.V))
     return SS_ERR_CUDA;
-  return delta_launch_next(delta_fwd_tc_kernel<KP, TRAIN>, (unsigned)((long long)a.B * a.H), kDThreads, DeltaTc<KP, TRAIN>::bytes, s, p, maps, h0, o,
+  return delta_launch_next(delta_fwd_tc_kernel<KP, TRAIN>, (unsigned)((long long)a.B * a.H), kDThreads, DeltaTc<KP>::bytes, s, p, maps, h0, o,
                     ckpt, h_last);
 }
 

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(Delta p) {
     if (tid == 0) vec[4 * kDC] = dec_exp(chi[kDC - 1], clo[kDC - 1]);
   }
   // A and P, a warp's 16 rows against the tokens up to its own
-  unsigned char* P = p.P + item * (long long)(kDC * kDC * 2) * p.pterms;
+  unsigned char* P = p.P + item * (long long)(N == 1 ? kDMTerms : kDMBytes);
   float kk[8][4];
   const int g = lane >> 2, c2 = 2 * (lane & 3);
   const float ps = N == 2 ? 1.f : a.scale;
@@ -211,7 +211,6 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(Delta p) {
         } else {
 #pragma unroll
           for (int m = 0; m < 3; ++m) {
-            if (m >= p.pterms) break;
             const uint32_t w = ActT<__nv_bfloat16>::pack2(y0, y1);
             *reinterpret_cast<uint32_t*>(P + m * (kDC * kDC * 2) + DTile<kDC, 1>::at(t, n, 0) + 2 * c2) = w;
             y0 -= bf16_lo(w);
