@@ -468,7 +468,7 @@ int linattn_step(const void* q, const void* k, const void* v, const float* g, in
  * sums.  With bf16 activations these are operands as they are, and an fp32
  * operand is three bf16 terms (all its 24 bits) where the result ends in fp32
  * (states, dg, dbeta, dh0) or in o, which has the same bits with and without
- * ckpt, and two (2^-15) in dq and dk.  With fp32 activations every operand is
+ * ckpt, and two (2^-16) in dq and dk.  With fp32 activations every operand is
  * two scaled fp16 terms (22 bits).
  * Alignment: 16 bytes for every pointer but g, beta, lengths, dg, dbeta (4).
  *

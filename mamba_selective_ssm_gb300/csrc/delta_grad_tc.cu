@@ -4,7 +4,7 @@
 //   dbeta = <du, r>      dg_t = sum_{s >= t} (do_s.o_s - dR_s.v_s) + <S1, dS>           along columns of V, in fp32
 //   E = scale D do u^T,  F = -D dR u^T (strict)                                          [t, s]
 //   dq = scale e^c do S0^T + E K      dk = -e^c dR S0^T + e^{c_last - c} u dS^T + E^T Q + (F + F^T) K
-// dq and dk are rounded to bf16; their fp32 operands are two bf16 terms (2^-15).  Products run with the columns of K as the
+// dq and dk are rounded to bf16; their fp32 operands are two rounded bf16 terms (2^-16).  Products run with the columns of K as the
 // 128 rows of an MMA; S0, dS, u and dR lie in shared memory by columns of V, as they come from memory, and are contracted down
 // their rows.  4 x 2048 tokens of 32 heads of 128 x 128: 415 us, 3.2 TB/s.  A CTA an SM (208 KB; tensor memory is taken whole),
 // whose steps wait for one another: the sums and operands along V a third of a chunk's time, the states' loads and terms a third.
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kGT, 1) delta_grad_tc_kernel(Delta p, const __
         if (on[3]) sums[7] += fmaf(y[3], o4.w, -d1.y * v[3]);
         const uint32_t w = (uint32_t)(c * 128 + (((warp >> 1) ^ (c & 7)) << 4) + (warp & 1) * 8);
         auto put = [&](uint32_t tile, float2 x, float2 z) {
-          const uint32_t a0 = take_pair(x), a1 = take_pair(z);
+          const uint32_t a0 = round_pair(x), a1 = round_pair(z);
           asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(tile + w), "r"(a0), "r"(a1) : "memory");
           asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(tile + kPanel + w), "r"(pack_bf16(x.x, x.y)), "r"(pack_bf16(z.x, z.y)) : "memory");
         };

@@ -92,17 +92,29 @@ __device__ __forceinline__ uint32_t take_pair(float2& x) {
   x = fma2(f2(bf16_lo(w), bf16_hi(w)), bc2(-1.f), x);
   return w;
 }
+// The nearest bf16 of a pair, packed; the pair becomes what is left.  Of two terms the first is this one: what is left is half as much
+// and of either sign, so that the pair is off by 2^-16 at most where a cut one is by 2^-15, and the product of two second terms,
+// which is dropped, is 2^-16 of any sign for 2^-14 of one sign (dq and dk were 1.6e-4 and 2e-4 of their size from the rounded
+// fp32 result).
+__device__ __forceinline__ uint32_t round_pair(float2& x) {
+  const uint32_t w = pack_bf16(x.x, x.y);
+  x = fma2(f2(bf16_lo(w), bf16_hi(w)), bc2(-1.f), x);
+  return w;
+}
 __device__ __forceinline__ uint32_t last_pair(float2 x) { return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632); }
-// eight values as NT terms to 16-byte units `step` bytes apart.  Three terms are the value (what is left after two has eight
-// bits); the second of two is rounded.
+// eight values as NT terms to 16-byte units `step` bytes apart.  Three cut terms are the value (what is left after two has
+// eight bits); two are rounded.
 template <int NT>
 __device__ __forceinline__ void put_terms(uint32_t at, int step, float2 (&x)[4]) {
+  static_assert(NT == 2 || NT == 3, "two terms or three");
+  if constexpr (NT == 3) {
 #pragma unroll
-  for (int n = 0; n + 1 < NT; ++n) sts16(at + n * step, make_uint4(take_pair(x[0]), take_pair(x[1]), take_pair(x[2]), take_pair(x[3])));
-  if (NT == 3) sts16(at + 2 * step, make_uint4(last_pair(x[0]), last_pair(x[1]), last_pair(x[2]), last_pair(x[3])));
-  else
-    sts16(at + (NT - 1) * step,
-          make_uint4(pack_bf16(x[0].x, x[0].y), pack_bf16(x[1].x, x[1].y), pack_bf16(x[2].x, x[2].y), pack_bf16(x[3].x, x[3].y)));
+    for (int n = 0; n < 2; ++n) sts16(at + n * step, make_uint4(take_pair(x[0]), take_pair(x[1]), take_pair(x[2]), take_pair(x[3])));
+    sts16(at + 2 * step, make_uint4(last_pair(x[0]), last_pair(x[1]), last_pair(x[2]), last_pair(x[3])));
+  } else {
+    sts16(at, make_uint4(round_pair(x[0]), round_pair(x[1]), round_pair(x[2]), round_pair(x[3])));
+    sts16(at + step, make_uint4(pack_bf16(x[0].x, x[0].y), pack_bf16(x[1].x, x[1].y), pack_bf16(x[2].x, x[2].y), pack_bf16(x[3].x, x[3].y)));
+  }
 }
 __device__ __forceinline__ float2 u2f(uint32_t a, uint32_t b) { return f2(__uint_as_float(a), __uint_as_float(b)); }
 
