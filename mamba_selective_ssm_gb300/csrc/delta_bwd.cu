@@ -6,11 +6,13 @@
 //   dS0 = e^{c_last} dS1 + scale (e^c Q)^T do - (e^c K)^T dR                               (the chain from chunk to chunk)
 //   dq = scale (e^c do S0^T + E K),   E_ts = D_ts do_t.u_s
 //   dk = -e^c dR S0^T + e^{c_last - c} u dS1^T + scale E^T Q - (F + F^T) K,   F_ts = D_ts dR_t.u_s (s < t)
-// A log decay multiplies whatever crosses it.  Every factor e^{c_t} comes with a query or a reading key and every e^{-c_s}
-// with a writing key, and their sums over a chunk meet in o, v and the state that leaves it:
-//   dg_t = sum_{s >= t} (do_s.o_s - dv_s.v_s) + <S1, dS1>        (s within the chunk)
-// so the fp32 gradients dg and dbeta need no product over V but sums along its columns, which the warps that hold o, u and du
-// have in fp32.
+// A log decay multiplies whatever crosses it: what tokens from t on read of the state (a) and of writes before t (X), what writes
+// before t leave to the end (b), and the state that passes through:
+//   dg_t = sum_{i >= t} a_i + sum_{s < t <= i} X_is + sum_{s < t} b_s + e^{c_last} <S0, dS1>
+//   a_i = scale e^{c_i} do_i.S0^T q_i - e^{c_i} dR_i.S0^T k_i      b_s = e^{c_last - c_s} u_s.dS1^T k_s      X_is = E_is q_i.k_s - F_is k_i.k_s
+// Each of these terms carries e^{g_t}, so the sum is as good for a head that forgets as for one that remembers.  (The same
+// sum is that of do_i.o_i - dv_i.v_i over i >= t and of <S1, dS1>, in which every token's own write cancels: 3e-6 of dg was lost at
+// g = -1, all of it at -14.)  do.S0^T q is the forward's; the other products with q and k are taken of the parts of dk.
 #include <stddef.h>
 
 #include "delta_common.cuh"
@@ -279,10 +281,9 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
 
 // ---------------------------------------------------------------- the other gradients, chunk by chunk
 // A CTA takes one (batch row, head, chunk).  First its warps take 16 columns of V each (with half of the tokens where V is 64
-// and less): what they add to dg and dbeta, from r and o (the forward's), du, v and do.  Then they share the products that
-// contract over V, from tiles in shared memory scaled as a whole: u, dR, S0, dS1 lie [V][..].  8 x 2048 tokens of 24 heads of
-// 64 x 64: 502 us (tensor pipe 21 %, memory a quarter of its rate: the steps between barriers, at two CTAs an SM); 997 when r and
-// o were found again here.
+// and less): what they add to dg and dbeta, from r and the state's part of o (the forward's), du and do.  Then they share the
+// products that contract over V, from tiles in shared memory scaled as a whole: u, dR, S0, dS1 lie [V][..].  8 x 2048 tokens of 24
+// heads of 64 x 64: 480 us, with decays 575 (tensor pipe 21 %, memory a quarter of its rate: the steps between barriers, at two CTAs an SM).
 template <int KP, int VP>
 struct GradSmem {
   static constexpr int N = 2, tile = DTile<KP, N>::bytes;
@@ -294,7 +295,7 @@ struct GradSmem {
   static constexpr int end = turns ? k + (2 * tile > vk ? 2 * tile : vk) : st + vk;
   static constexpr int vec = end, up = vec + kDVec * 4, red = up + 3 * kDC * 4, bytes = red + (2 * 8 * kDC + 64 + 2 * kDC) * 4;
   static constexpr int ctas = 2 * (bytes + 1024) <= 228 * 1024 ? 2 : 1;
-  static_assert(f + tt <= k, "E and F where do, u and dR were");
+  static_assert(f + tt <= r && vt >= kDC * kDC * 4, "E, F and X where do, u and dR were");
 };
 
 constexpr int kGradThreads = 256;
@@ -331,6 +332,15 @@ __device__ __forceinline__ void store_acc(uint32_t tile, int r0, int j, const fl
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(tile + DTile<W, 2>::at(r, j, 0) + 4 * (lane & 3)), "r"(hi) : "memory");
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(tile + DTile<W, 2>::at(r, j, 1) + 4 * (lane & 3)), "r"(lo) : "memory");
   }
+}
+// columns 2 (lane % 4) and the next of unit u of a row, from its two terms
+template <int W>
+__device__ __forceinline__ float2 tile_pair(uint32_t tile, int r, int u, int lane) {
+  uint32_t hi, lo;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(hi) : "r"(tile + DTile<W, 2>::at(r, u, 0) + 4 * (lane & 3)) : "memory");
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(lo) : "r"(tile + DTile<W, 2>::at(r, u, 1) + 4 * (lane & 3)) : "memory");
+  const float2 h = wide_half(hi), l = wide_half(lo);
+  return make_float2(h.x + l.x, h.y + l.y);
 }
 // c += a b over one step
 __device__ __forceinline__ void mma_pair(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[2][4], const uint32_t (&b)[2][4]) {
@@ -374,7 +384,6 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
   }
   const float* q = static_cast<const float*>(a.q) + tok * a.ldq + (long long)gh * a.K;
   const float* k = static_cast<const float*>(a.k) + tok * a.ldk + (long long)gh * a.K;
-  const float* v = static_cast<const float*>(a.v) + tok * a.ldv + (long long)h * a.V;
   const long long ldo = (long long)a.H * a.V;
   const float* dob = dout + (tok * a.H + h) * a.V;
   float *vec = reinterpret_cast<float*>(raw + Sm::vec), *up = reinterpret_cast<float*>(raw + Sm::up), *red = reinterpret_cast<float*>(raw + Sm::red);
@@ -405,7 +414,7 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
         x[j][e + 1] = y.y;
       }
   };
-  // [V][64] values, and rows of v and do
+  // [V][64] values, and rows of do
   auto tokens = [&](const float* src, float (&x)[NT][4]) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -446,8 +455,6 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
       af[2 * n + 1] = t + 1 < valid ? fmaf(x[n][1], o[n][1], x[n][3] * o[n][3]) : 0.f;
     }
   }
-  float X[NT][4];
-  rows_of(v, a.ldv, X);
   cp_wait<0>();
   __syncthreads();
   tile_scale<KP>(sb + Sm::k, up, tid, kGradThreads);
@@ -457,7 +464,7 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int t = 8 * (part * NT + n) + t2;
-    const float2 be = *reinterpret_cast<const float2*>(vec + 2 * kDC + t), ku = *reinterpret_cast<const float2*>(up + t);
+    const float2 be = *reinterpret_cast<const float2*>(vec + 2 * kDC + t);
     db[2 * n] = fmaf(D[n][0], R[n][0], D[n][2] * R[n][2]);
     db[2 * n + 1] = fmaf(D[n][1], R[n][1], D[n][3] * R[n][3]);
 #pragma unroll
@@ -465,9 +472,6 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
       R[n][e] *= e & 1 ? be.y : be.x;
       D[n][e] *= e & 1 ? be.y : be.x;
     }
-    // (v in its token's scale, as dR)
-    af[2 * n] -= fmaf(D[n][0], X[n][0], D[n][2] * X[n][2]) * __frcp_rn(ku.x);
-    af[2 * n + 1] -= fmaf(D[n][1], X[n][1], D[n][3] * X[n][3]) * __frcp_rn(ku.y);
   }
 #pragma unroll
   for (int i = 0; i < 2 * NT; ++i) {
@@ -482,19 +486,18 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
       red[(8 + warp % VB) * kDC + t] = af[i];
     }
   }
-  // dS1: its largest and <S1, dS1>; S0
+  // dS1: its largest and <S0, dS1>; S0
   float S[KT][4];
   float dot = 0.f;
   state(dS + item * a.V * a.K, S);
   {
-    const float* s1 = s0 + (long long)a.V * a.K;
 #pragma unroll
     for (int j = 0; j < KT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
         const int kk = 8 * (part * KT + j) + t2, vv = g + (e >> 1) * 8;
         if (kk < a.K && vv < vw) {
-          const float2 y = *reinterpret_cast<const float2*>(s1 + (long long)(v0 + vv) * a.K + kk);
+          const float2 y = *reinterpret_cast<const float2*>(s0 + (long long)(v0 + vv) * a.K + kk);
           dot = fmaf(y.x, S[j][e], fmaf(y.y, S[j][e + 1], dot));
         }
       }
@@ -525,37 +528,22 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
     for (int j = 0; j < KT; ++j) store_acc<KP>(sb + Sm::st, v0, part * KT + j, S[j], f, lane);
   };
   if (!Sm::turns) put_state(scS.down);
-  if (warp == 0) {  // dbeta, and the sums from each token on
-    float s[2], d[2];
+  if (warp == 0) {  // dbeta, and a's part of q
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
-      s[i] = d[i] = 0.f;
+      float s = 0.f, d = 0.f;
       for (int w = 0; w < VB; ++w) {
-        d[i] += red[w * kDC + t];
-        s[i] += red[(8 + w) * kDC + t];
+        d += red[w * kDC + t];
+        s += red[(8 + w) * kDC + t];
       }
-      if (t < rows) dbeta[(tok + t) * a.H + h] = t < valid ? d[i] * up[t] * up[t] : 0.f;
-    }
-    s[0] += s[1];
-    float x = 0.f;
-    for (int w = 0; w < 8; ++w) x += mx[w * 8 + 6];
-    float incl = s[0];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const float y = __shfl_down_sync(0xffffffffu, incl, o);
-      if (lane + o < 32) incl += y;
-    }
-    float after = __shfl_down_sync(0xffffffffu, incl, 1);
-    if (lane == 31) after = 0.f;
-    if (dg != nullptr) {
-      if (2 * lane < rows) dg[(tok + 2 * lane) * a.H + h] = 2 * lane < valid ? x + incl : 0.f;
-      if (2 * lane + 1 < rows) dg[(tok + 2 * lane + 1) * a.H + h] = 2 * lane + 1 < valid ? x + (s[1] + after) : 0.f;
+      if (t < rows) dbeta[(tok + t) * a.H + h] = t < valid ? d * up[t] * up[t] : 0.f;
+      red[8 * kDC + t] = s;
     }
   }
   // E and F, a warp's 16 tokens t against half of the tokens s
   const int mb = warp & 3, half = warp >> 2, vb = (a.V + 15) / 16;
-  float E[4][4], F[4][4];
+  float E[4][4], F[4][4], Xr[4][4];
   __syncthreads();  // u and dR
   {
 #pragma unroll
@@ -589,6 +577,36 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
         E[n][e] = s <= t ? a.scale * up[kDC + t] * up[2 * kDC + t] * scU.up * d * E[n][e] : 0.f;
         F[n][e] = s < t ? -scR.up * scU.up * d * F[n][e] : 0.f;
       }
+    // X: its values wait here for the place of dR (and are made of these, not of E's and F's tiles: in those a token's own values
+    // set the scale, and what a strong decay left is lost)
+    if (dg != nullptr) {
+#pragma unroll
+      for (int np = 0; np < 2; ++np) {
+        float qk[2][4], kk[2][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) qk[0][e] = qk[1][e] = kk[0][e] = kk[1][e] = 0.f;
+        if (2 * half + np <= mb)
+#pragma unroll 1
+          for (int kb = 0; kb < KP / 16; ++kb) {
+            uint32_t qa[N][4], ka[N][4], bb[N][4];
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+              left_rows<KP, N>(qa[n], sb + Sm::q, mb, kb, n, lane);
+              left_rows<KP, N>(ka[n], sb + Sm::k, mb, kb, n, lane);
+              right_rows<KP, N>(bb[n], sb + Sm::k, 2 * half + np, kb, n, lane);
+            }
+            mma_pair(qk[0], qk[1], qa, bb);
+            mma_pair(kk[0], kk[1], ka, bb);
+          }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int n = 2 * np + i, t = 16 * mb + g + (e >> 1) * 8, s = 32 * half + 8 * n + t2 + (e & 1);
+            Xr[n][e] = s < t ? fmaf(E[n][e], qk[i][e], F[n][e] * kk[i][e]) : 0.f;
+          }
+      }
+    }
     const float me = abs_max(E), mf = abs_max(F);
     if (lane == 0) {
       mx[warp * 8 + 4] = me;
@@ -609,6 +627,28 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
     for (int j = 0; j < NC; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) to[j][e] = fmaf(e < 2 ? fa : fb, C[j][e], first ? 0.f : to[j][e]);
+  };
+  // red[row + half][t] = f C.k of this warp's tokens, over its columns of K, in the tokens' scale
+  auto meet = [&](int row, float fa, float fb) {
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = i == 0 ? ta : tb;
+      const float* kt = k + (long long)(t < valid ? t : 0) * a.ldk;
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const int c = half * (KP / 2) + 8 * j + t2;
+        if (c >= a.K) continue;
+        float2 y;
+        if constexpr (Sm::turns) y = *reinterpret_cast<const float2*>(kt + c);  // (a state is where k was)
+        else y = tile_pair<KP>(sb + Sm::k, t, half * (KP / 16) + j, lane);
+        s[i] = fmaf(C[j][2 * i], y.x, fmaf(C[j][2 * i + 1], y.y, s[i]));
+      }
+      s[i] *= (i == 0 ? fa : fb) * (Sm::turns ? __frcp_rn(up[t]) : 1.f);
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+      if ((lane & 3) == 0) red[(row + half) * kDC + t] = t < valid ? s[i] : 0.f;
+    }
   };
   // C += (left operand at step kb) x (the tile's rows 16 kb .., this warp's columns)
   auto step = [&](uint32_t tile, int kb, const uint32_t (&la)[N][4]) {
@@ -642,6 +682,7 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
     step(sb + Sm::st, kb, la);
   }
   add(Kg, -vec[ta] * scR.up * scS.up, -vec[tb] * scR.up * scS.up, true);
+  if (dg != nullptr) meet(0, -vec[ta] * scR.up * scS.up, -vec[tb] * scR.up * scS.up);
   state(dS + item * a.V * a.K, S);
   __syncthreads();
   put_state(scT.down);
@@ -654,6 +695,7 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
     step(sb + Sm::st, kb, la);
   }
   add(Kg, vec[kDC + ta] * scU.up * scT.up, vec[kDC + tb] * scU.up * scT.up, false);
+  if (dg != nullptr) meet(2, vec[kDC + ta] * scU.up * scT.up, vec[kDC + tb] * scU.up * scT.up);
   __syncthreads();  // do, u, dR and dS1 have been read
   if constexpr (Sm::turns) {
     tile_load<float, KP>(sb + Sm::k, k, a.ldk, valid, a.K, tid, kGradThreads);
@@ -666,6 +708,14 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
     store_acc<kDC>(sb + Sm::e, 16 * mb, 4 * half + n, E[n], scE.down, lane);
     store_acc<kDC>(sb + Sm::f, 16 * mb, 4 * half + n, F[n], scF.down, lane);
   }
+  // X, whose sums over s < t <= i follow between the products
+  float* X = reinterpret_cast<float*>(raw + Sm::r);  // [t][s], s's eights turned by t (banks)
+  auto xat = [](int t, int s) { return t * kDC + (s ^ ((t & 7) << 3)); };
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; e += 2)
+      if (dg != nullptr) *reinterpret_cast<float2*>(X + xat(e == 0 ? ta : tb, 32 * half + 8 * n + t2)) = make_float2(Xr[n][e], Xr[n][e + 1]);
   if constexpr (Sm::turns) {
     cp_wait<0>();
     __syncthreads();
@@ -673,6 +723,15 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
     tile_scale<KP>(sb + Sm::q, up + kDC, tid, kGradThreads);
   }
   __syncthreads();
+  if (dg != nullptr) {
+    float run = 0.f;  // X[t][s] becomes its sum over the tokens from t to the end of t's 16
+#pragma unroll
+    for (int t = 15; t >= 0; --t) {
+      float* at = X + xat(16 * (tid >> 6) + t, tid & 63);
+      run += *at;
+      *at = run;
+    }
+  }
   zero();
 #pragma unroll
   for (int kb = 0; kb < 4; ++kb) {
@@ -683,6 +742,20 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
     step(sb + Sm::k, kb, la);
   }
   add(Q, scE.up * __frcp_rn(up[kDC + ta]), scE.up * __frcp_rn(up[kDC + tb]), false);
+  if (dg != nullptr) {
+    __syncthreads();
+    const int j = tid >> 2;
+    float s = 0.f;
+#pragma unroll 1
+    for (int c = tid & 3; c < j; c += 4) {
+      s += X[xat(j, c)];
+#pragma unroll 1
+      for (int later = (j >> 4) + 1; later < 4; ++later) s += X[xat(16 * later, c)];
+    }
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    if ((tid & 3) == 0) red[9 * kDC + j] = s;
+  }
   zero();
 #pragma unroll
   for (int kb = 0; kb < 4; ++kb) {
@@ -693,6 +766,36 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
     step(sb + Sm::q, kb, la);
   }
   add(Kg, scE.up, scE.up, false);
+  if (dg != nullptr) {
+    __syncthreads();
+    if (warp == 0) {
+      float x = 0.f, after[2], before[2];
+      for (int w = 0; w < 8; ++w) x += mx[w * 8 + 6];
+      x *= vec[4 * kDC];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i;
+        after[i] = red[8 * kDC + t] + (red[t] + red[kDC + t]);
+        before[i] = red[2 * kDC + t] + red[3 * kDC + t];
+      }
+      float from = after[0] + after[1], upto = before[0] + before[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_down_sync(0xffffffffu, from, o), z = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane + o < 32) from += y;
+        if (lane >= o) upto += z;
+      }
+      float rest = __shfl_down_sync(0xffffffffu, from, 1), past = __shfl_up_sync(0xffffffffu, upto, 1);
+      if (lane == 31) rest = 0.f;
+      if (lane == 0) past = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i;
+        const float y = ((i == 0 ? from : after[1] + rest) + (i == 0 ? past : past + before[0])) + (x + red[9 * kDC + t]);
+        if (t < rows) dg[(tok + t) * a.H + h] = t < valid ? y : 0.f;
+      }
+    }
+  }
   zero();
 #pragma unroll
   for (int kb = 0; kb < 4; ++kb) {

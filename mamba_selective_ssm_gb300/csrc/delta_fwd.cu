@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
       S[j][e] = h0 != nullptr && kk < a.K && vv < vw ? h0[(bh * a.K + kk) * a.V + v0 + vv] : 0.f;
     }
   if (ckpt != nullptr) ckpt += bh * delta_ckpt_floats(a.nck, a.K, a.V);
-  float* ro = ckpt + (long long)(a.nck + 1) * a.K * a.V;  // r of every chunk, [V][64], and then o
+  float* ro = ckpt + (long long)(a.nck + 1) * a.K * a.V;  // r of every chunk, [V][64], and then the state's part of o
   auto keep = [&](float* dst, int t, const float (&x)[4]) {  // two tokens of two columns
 #pragma unroll
     for (int e = 0; e < 4; e += 2) {
@@ -210,13 +210,18 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
           const int n = 2 * np + i, t = 8 * n + t2;
           const float2 in = *reinterpret_cast<const float2*>(vec + t), qu = *reinterpret_cast<const float2*>(up + kDC + t);
           const float f0 = t0 + t < len ? a.scale * qu.x : 0.f, f1 = t0 + t + 1 < len ? a.scale * qu.y : 0.f;
+          if (ckpt != nullptr) {
+            const bool on0 = t0 + t < len, on1 = t0 + t + 1 < len;  // (not 0 * NaN)
+            const float x0 = f0 * in.x * ss.r[0].up, x1 = f1 * in.y * ss.r[0].up, x2 = f0 * in.x * ss.r[1].up, x3 = f1 * in.y * ss.r[1].up;
+            const float st[4] = {on0 ? x0 * O[n][0] : 0.f, on1 ? x1 * O[n][1] : 0.f, on0 ? x2 * O[n][2] : 0.f, on1 ? x3 * O[n][3] : 0.f};
+            keep(ro + (long long)(a.nck + ck) * kDC * a.V, t, st);
+          }
           O[n][0] = f0 * fmaf(O[n][0], in.x * ss.r[0].up, c[i][0] * us.r[0].up);
           O[n][1] = f1 * fmaf(O[n][1], in.y * ss.r[0].up, c[i][1] * us.r[0].up);
           O[n][2] = f0 * fmaf(O[n][2], in.x * ss.r[1].up, c[i][2] * us.r[1].up);
           O[n][3] = f1 * fmaf(O[n][3], in.y * ss.r[1].up, c[i][3] * us.r[1].up);
           if (t0 + t >= len) O[n][0] = O[n][2] = 0.f;  // (not 0 * NaN)
           if (t0 + t + 1 >= len) O[n][1] = O[n][3] = 0.f;
-          if (ckpt != nullptr) keep(ro + (long long)(a.nck + ck) * kDC * a.V, t, O[n]);
           store_tokens(ob + (long long)t0 * ldo, ldo, 8 * n, rows, vw, O[n], lane);
         }
       }

@@ -2,6 +2,10 @@
 // the state S0 that enters it, its r and o (from the forward), the gradient dS of the state that leaves it and its du (from
 // the backward chain); u = beta r, dR = beta du.
 //   dbeta = <du, r>      dg_t = sum_{s >= t} (do_s.o_s - dR_s.v_s) + <S1, dS>           along columns of V, in fp32
+// In this dg each token's own write cancels, which leaves an error of 3e-7 of the terms, and dg is e^{g_t} of them.  A token that
+// forgets (g_t below kForget) takes the sum of what crosses it instead, as the fp32 kernel does (delta_bwd.cu), of the products
+// below: their operands of two terms leave 2 to 4e-6 of dg at any g, the other form 9e-7 at g = -1, 3e-6 at -2, 3e-5 at -4 and all at
+// -14.
 //   E = scale D do u^T,  F = -D dR u^T (strict)                                          [t, s]
 //   dq = scale e^c do S0^T + E K      dk = -e^c dR S0^T + e^{c_last - c} u dS^T + E^T Q + (F + F^T) K
 // dq and dk are rounded to bf16; their fp32 operands are two rounded bf16 terms (2^-16).  Products run with the columns of K as the
@@ -18,15 +22,17 @@ namespace {
 using namespace ssk;
 
 constexpr int kGT = 512, kGGrid = 152;  // a CTA an SM, which goes from chunk to chunk
+constexpr float kForget = -2.f;
 template <int KP>
 struct GradTc {
   static constexpr int NKP = KP / 64, ST = NKP * kPanel;  // bytes of a term of a state
   static constexpr int S = 0, u = S + 2 * ST, r = u + 2 * kPanel, dy = r + 2 * kPanel, k = dy + 2 * kTok, q = k + NKP * kTok, e = q + NKP * kTok,
-                       f = e + 2 * kDTerm, vec = f + 2 * kDTerm, dec = vec + kDVec * 4, red = dec + 2 * kDC * 4, bar = red + (16 * 8 + 16) * 4;
+                       f = e + 2 * kDTerm, vec = f + 2 * kDTerm, dec = vec + kDVec * 4, red = dec + 2 * kDC * 4, fg = red + (16 * 8 + 32) * 4, bar = fg + 4 * 4;
   static constexpr int v = e;  // (v's tile, before E and F)
+  static constexpr int x = r, cross = r + kPanel;  // X, and the sums of a, b and X, where dR's terms were
   static constexpr int kIn = 0, kM0 = 1, kM1 = 2, nbar = 3, tm = bar + nbar * 8, bytes = tm + 8;
-  // tensor memory: do S0^T, dR S0^T, u dS^T, E, F, E K, E^T Q + (F + F^T) K
-  static constexpr int G1 = 0, G2 = 64, G3 = 128, E = 192, F = 256, H1 = 320, H2 = 384, cols = 512;
+  // tensor memory: do S0^T, dR S0^T, u dS^T, E, F, E K, E^T Q + (F + F^T) K; before the last two in their places q k^T, k k^T
+  static constexpr int G1 = 0, G2 = 64, G3 = 128, E = 192, F = 256, H1 = 320, H2 = 384, QK = H1, KK = H2, cols = 512;
 };
 
 struct GradMaps {
@@ -114,6 +120,22 @@ __global__ void __launch_bounds__(kGT, 1) delta_grad_tc_kernel(Delta p, const __
     }
   }
   uint32_t par = 0;
+  uint32_t* forgets = reinterpret_cast<uint32_t*>(raw + L::fg);  // a chunk's tokens that forget: the even ones, the odd ones
+  float *X = reinterpret_cast<float*>(raw + L::x), *as = reinterpret_cast<float*>(raw + L::cross), *bs = as + 4 * kDC, *xs = bs + 4 * kDC;
+  auto xat = [](int t, int s) { return t * kDC + (s ^ ((t & 7) << 2)); };
+  // a warp's sums of sixteen tokens over its lanes: token lane % 16 of them ends in x[0]
+  auto lanes_tokens = [&](float (&x)[TC]) {
+#pragma unroll
+    for (int n = TC / 2; n > 0; n >>= 1) {
+      const bool upper = lane & n;
+#pragma unroll
+      for (int e = 0; e < n; ++e) {
+        const float keep = upper ? x[e + n] : x[e], give = upper ? x[e] : x[e + n];
+        x[e] = keep + __shfl_xor_sync(0xffffffffu, give, n);
+      }
+    }
+    x[0] += __shfl_xor_sync(0xffffffffu, x[0], TC);
+  };
   for (long long item = blockIdx.x; item < items && ok; item += gridDim.x) {
     const long long bh = item / a.nck;
     const int ck = (int)(item % a.nck), h = (int)(bh % a.H), b = (int)(bh / a.H), gh = h / (a.H / a.G);
@@ -147,15 +169,22 @@ __global__ void __launch_bounds__(kGT, 1) delta_grad_tc_kernel(Delta p, const __
       if (a.g != nullptr) gates.fetch(a, b, h, t0, t0 + valid, lane);
       else gates.g[0] = gates.g[1] = 0.f;
       gates.scan(lane, [&](int i, Dec e) { dec[i] = e.hi; dec[kDC + i] = e.lo; });
+      const uint32_t even = __ballot_sync(0xffffffffu, gates.g[0] < kForget), odd = __ballot_sync(0xffffffffu, gates.g[1] < kForget);
+      if (lane == 0) {
+        forgets[0] = even;
+        forgets[1] = odd;
+      }
     }
     __syncthreads();
+    const uint32_t forget[2] = {forgets[0], forgets[1]};
+    const bool crossing = (forget[0] | forget[1]) != 0u;
     auto state = [&](const float4* src, float4 (&x)[SC / 4]) {
 #pragma unroll
       for (int e = 0; e < SC / 4; ++e)
         x[e] = mine && cq * SC + 4 * e < a.K ? __ldcg(src + (long long)(cq * (SC / 4) + e) * a.V) : make_float4(0.f, 0.f, 0.f, 0.f);
     };
-    float4 X[SC / 4];
-    state(s0, X);
+    float4 X4[SC / 4];
+    state(s0, X4);
     ok = chain_wait(&bar[L::kIn], par);
     if (valid < kDC && t0 + valid < a.L) {  // the row ends inside the tensor: what follows is not its own
       if (warp == 0) tok_clear(sb + L::dy, vp, valid, lane);
@@ -226,7 +255,7 @@ __global__ void __launch_bounds__(kGT, 1) delta_grad_tc_kernel(Delta p, const __
     sums[0] += __shfl_xor_sync(0xffffffffu, sums[0], 8);
     sums[0] += __shfl_xor_sync(0xffffffffu, sums[0], 16);
     if (lane < 8) red[warp * 8 + lane] = sums[0];
-    put_state(X);
+    put_state(X4);
     fence_proxy_async_smem();
     __syncthreads();
     if (warp == 0) {
@@ -248,22 +277,38 @@ __global__ void __launch_bounds__(kGT, 1) delta_grad_tc_kernel(Delta p, const __
             mma_ss(tm + L::G2, cols_desc(sb + L::S + i * L::ST, kPanel, s), cols_desc(sb + L::r + j * kPanel, kPanel, s), cc, n > 0 || s > 0);
           }
         }
+        if (crossing) {
+          const uint32_t rr = mma_idesc(64, false, false);
+#pragma unroll 1
+          for (int s = 0; s < (a.K + 15) / 16; ++s) {
+            const uint64_t kd = rows_desc(sb + L::k, kTok, s);
+            mma_ss(tm + L::QK, rows_desc(sb + L::q, kTok, s), kd, rr, s > 0);
+            mma_ss(tm + L::KK, kd, kd, rr, s > 0);
+          }
+        }
         mma_commit(&bar[L::kM0]);
       }
       __syncwarp();
     }
     // ---- under the products: <S1, dS>, and dg and dbeta
-    float dot = 0.f;
     {
       float4 Y[SC / 4];
+      auto dot = [&](int at) {
+        float d = 0.f;
+#pragma unroll
+        for (int e = 0; e < SC / 4; ++e) d = fmaf(X4[e].x, Y[e].x, fmaf(X4[e].y, Y[e].y, fmaf(X4[e].z, Y[e].z, fmaf(X4[e].w, Y[e].w, d))));
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        if (lane == 0) red[at + warp] = d;
+      };
       state(s1, Y);
-      state(reinterpret_cast<const float4*>(dS + item * a.K * a.V) + row, X);
-#pragma unroll
-      for (int e = 0; e < SC / 4; ++e) dot = fmaf(X[e].x, Y[e].x, fmaf(X[e].y, Y[e].y, fmaf(X[e].z, Y[e].z, fmaf(X[e].w, Y[e].w, dot))));
+      state(reinterpret_cast<const float4*>(dS + item * a.K * a.V) + row, X4);
+      dot(16 * 8);
+      if (crossing) {
+        state(s0, Y);
+        dot(16 * 8 + 16);
+      }
     }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if (lane == 0) red[16 * 8 + warp] = dot;
     __syncthreads();
     if (warp == 15) {
       float s[2], x = 0.f;
@@ -291,7 +336,7 @@ __global__ void __launch_bounds__(kGT, 1) delta_grad_tc_kernel(Delta p, const __
     if (next < items) ahead(next);
     ok = chain_wait(&bar[L::kM0], par) && ok;
     tc_fence_after_sync();
-    put_state(X);  // dS where S0 was
+    put_state(X4);  // dS where S0 was
     if ((warp & 3) < 2) {  // E and F: row = token t, this warp's 16 tokens s
       uint32_t d[16], f[16];
       tmem_ld16(tl + L::E + cq * TC, d);
@@ -309,6 +354,20 @@ __global__ void __launch_bounds__(kGT, 1) delta_grad_tc_kernel(Delta p, const __
           const float xe = s <= row ? a.scale * c * __uint_as_float(d[e]) : 0.f, ye = s < row ? -c * __uint_as_float(f[e]) : 0.f;
           (z & 1 ? x[z / 2].y : x[z / 2].x) = xe;
           (z & 1 ? y[z / 2].y : y[z / 2].x) = ye;
+        }
+        if (crossing) {
+          uint32_t qk[8], kk[8];
+          tmem_ld8u(tl + L::QK + cq * TC + 8 * u, qk);
+          tmem_ld8u(tl + L::KK + cq * TC + 8 * u, kk);
+          tmem_done(qk);
+          tmem_done(kk);
+          float w[8];
+#pragma unroll
+          for (int z = 0; z < 8; ++z)
+            w[z] = cq * TC + 8 * u + z < row ? fmaf(z & 1 ? x[z / 2].y : x[z / 2].x, __uint_as_float(qk[z]),
+                                                    (z & 1 ? y[z / 2].y : y[z / 2].x) * __uint_as_float(kk[z])) : 0.f;
+          *reinterpret_cast<float4*>(X + xat(row, cq * TC + 8 * u)) = make_float4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<float4*>(X + xat(row, cq * TC + 8 * u + 4)) = make_float4(w[4], w[5], w[6], w[7]);
         }
         const uint32_t at = unit_at(kTok, row, cq * (TC / 8) + u);
         put_terms<2>(sb + L::e + at, kDTerm, x);
@@ -345,8 +404,80 @@ __global__ void __launch_bounds__(kGT, 1) delta_grad_tc_kernel(Delta p, const __
       __syncwarp();
     }
     if (next < items) states_ahead(next);
+    if (crossing) {  // ---- under the products: a, and the sums of X over s < t <= i
+      float sa[TC];
+#pragma unroll
+      for (int e = 0; e < TC; ++e) sa[e] = 0.f;
+      if ((warp & 3) * 32 < a.K) {
+        float2 qc[TC / 2], kc[TC / 2];
+        ColRead<TC>::go(col_at(sb + L::q, row) + cq * TC * 128, qc);
+        ColRead<TC>::go(col_at(sb + L::k, row) + cq * TC * 128, kc);
+        tc_fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < TC; c += 8) {
+          uint32_t g1[8], g2[8];
+          tmem_ld8u(tl + L::G1 + cq * TC + c, g1);
+          tmem_ld8u(tl + L::G2 + cq * TC + c, g2);
+          tmem_done(g1);
+          tmem_done(g2);
+          float2 in[4];
+          pairs4(vec + cq * TC + c, in);
+#pragma unroll
+          for (int z = 0; z < 8; ++z) {
+            const float qv = z & 1 ? qc[(c + z) / 2].y : qc[(c + z) / 2].x, kv = z & 1 ? kc[(c + z) / 2].y : kc[(c + z) / 2].x;
+            sa[c + z] = (z & 1 ? in[z / 2].y : in[z / 2].x) * (a.scale * qv * __uint_as_float(g1[z]) - kv * __uint_as_float(g2[z]));
+          }
+        }
+      }
+      lanes_tokens(sa);
+      if (lane < TC) as[(warp & 3) * kDC + cq * TC + lane] = sa[0];
+      float run = 0.f;  // X[t][s] becomes its sum over the tokens from t to the end of t's eight
+#pragma unroll
+      for (int t = 7; t >= 0; --t) {
+        float* at = X + xat(8 * (tid >> 6) + t, tid & 63);
+        run += *at;
+        *at = run;
+      }
+      __syncthreads();
+      const int j = tid >> 3;
+      float s = 0.f;
+#pragma unroll 1  // (unrolled, its instructions cost every chunk 4 %, those that skip them too)
+      for (int c = tid & 7; c < j; c += 8) {
+        s += X[xat(j, c)];
+#pragma unroll 1
+        for (int later = (j >> 3) + 1; later < 8; ++later) s += X[xat(8 * later, c)];
+      }
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if ((tid & 7) == 0) xs[j] = s;
+    }
+    const float whole = vec[4 * kDC];
     ok = chain_wait(&bar[L::kM1], par) && ok;
     tc_fence_after_sync();
+    if (crossing) {  // ---- b
+      float sw[TC];
+#pragma unroll
+      for (int e = 0; e < TC; ++e) sw[e] = 0.f;
+      if ((warp & 3) * 32 < a.K) {
+        float2 kc[TC / 2];
+        ColRead<TC>::go(col_at(sb + L::k, row) + cq * TC * 128, kc);
+#pragma unroll
+        for (int c = 0; c < TC; c += 8) {
+          uint32_t g3[8];
+          tmem_ld8u(tl + L::G3 + cq * TC + c, g3);
+          tmem_done(g3);
+          float2 re[4];
+          pairs4(vec + kDC + cq * TC + c, re);
+#pragma unroll
+          for (int z = 0; z < 8; ++z)
+            sw[c + z] = (z & 1 ? re[z / 2].y * kc[(c + z) / 2].y : re[z / 2].x * kc[(c + z) / 2].x) * __uint_as_float(g3[z]);
+        }
+      }
+      lanes_tokens(sw);
+      if (lane < TC) bs[(warp & 3) * kDC + cq * TC + lane] = sw[0];
+      fence_proxy_async_smem();
+      __syncthreads();  // (the columns of k and q were read before the copies that follow)
+    }
     if (tid == 0 && next < items && ok) load(next);  // (their places have been read)
     par ^= 1u;
     constexpr bool kTile = sizeof(TO) == 2;  // bf16 leaves by TMA from tiles of tokens, where the states were
@@ -413,6 +544,32 @@ __global__ void __launch_bounds__(kGT, 1) delta_grad_tc_kernel(Delta p, const __
     tc_fence_before_sync();
     ok = __syncthreads_and(ok);  // the sums, the scalars and the tiles have been read; all go on or none does
     tc_fence_after_sync();
+    if (crossing && warp == 15) {  // (what it reads is written again behind the next chunk's first barrier)
+      float after[2], before[2], x = 0.f;
+      for (int w = 0; w < 16; ++w) x += red[16 * 8 + 16 + w];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i;
+        after[i] = (as[t] + as[kDC + t]) + (as[2 * kDC + t] + as[3 * kDC + t]);
+        before[i] = (bs[t] + bs[kDC + t]) + (bs[2 * kDC + t] + bs[3 * kDC + t]);
+      }
+      float from = after[0] + after[1], upto = before[0] + before[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_down_sync(0xffffffffu, from, o), z = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane + o < 32) from += y;
+        if (lane >= o) upto += z;
+      }
+      float rest = __shfl_down_sync(0xffffffffu, from, 1), past = __shfl_up_sync(0xffffffffu, upto, 1);
+      if (lane == 31) rest = 0.f;
+      if (lane == 0) past = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i;
+        const float y = ((i == 0 ? from : after[1] + rest) + (i == 0 ? past : past + before[0])) + fmaf(whole, x, xs[t]);
+        if ((forget[i] >> lane & 1u) && t < valid) dg[(tok + t) * a.H + h] = y;
+      }
+    }
   }
   if (tid == 0) bulk_wait();
   lin_leave(ok, bar, L::nbar, tm, L::cols, warp, lane);

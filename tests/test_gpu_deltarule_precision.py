@@ -53,3 +53,73 @@ def test_operands_of_dq_are_rounded_not_cut(ss):
             own[at] = W ** -0.5 * np.exp(c)[:, None] * (do[at] @ two(S[t, h]).T) + two(E) @ k[at]
     exact = bf16(deltarule_bwd_ref(q, k, v, g, beta, do)["dq"])
     assert np.linalg.norm(got - bf16(own)) <= 0.5 * np.linalg.norm(bf16(own) - exact)
+
+
+LEVELS = [-0.01, -0.3, -1.0, -1.9, -2.1, -4.0, -8.0, -12.0, -16.0, -30.0, -200.0]
+
+
+def _forgetting(L, dtype, mixed, K=48, V=40, seed=0):
+    """A head for each level of its log decays, within a tenth; or among weak ones with now and then a token at the level."""
+    import torch
+    r = np.random.default_rng(seed)
+    d = _case(2, L, len(LEVELS), 1, K, V, dtype, seed=seed)
+    g = np.array(LEVELS) * r.uniform(0.9, 1.1, (2, L, len(LEVELS)))
+    if mixed:
+        at = r.random(g.shape) < 0.1
+        g = np.where(at, g, -np.exp(r.uniform(np.log(1e-3), np.log(0.3), g.shape)))
+    else:
+        at = np.ones(g.shape, bool)
+    d["g"] = torch.from_numpy(g).float().cuda()
+    return d, at
+
+
+@pytest.mark.parametrize("mixed", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("L", [1, 3, 64, 200])
+def test_decay_gradients_of_heads_that_forget(ss, L, dtype, mixed):
+    """dg of each level by itself.  dg_t carries e^{g_t}; a form in which each token's own write cancels keeps the rounding of terms
+    of any size.  fp32: the three-fold bound of a gradient, 3 F, at every level.  bf16: where g is below -2 the sum of what
+    crosses the token, with products of two operands that are off by 2^-16 each and drop as much, 3 * 2^-16; above, the other form,
+    whose terms are at most e^2 of the result: 3 F e^2."""
+    from oracle.deltarule import deltarule_bwd_ref
+    from tests.test_gpu_deltarule import _bwd, _near, _np, _tol
+    d, at = _forgetting(L, dtype, mixed, seed=L)
+    got = _np(_bwd(ss, d, _fwd(ss, d)[1])["dg"])
+    ref = deltarule_bwd_ref(*[_np(d[x]) for x in ("q", "k", "v", "g", "beta", "do", "h0", "dh_last")])["dg"]
+    tol = _tol(L, dtype, False, 3) * (np.exp(2) if dtype == "bf16" else 1.0) + (3 * 2.0 ** -16 if dtype == "bf16" else 0.0)
+    for i, level in enumerate(LEVELS):
+        for group in (at[..., i], ~at[..., i]):
+            if group.any():
+                a, b = got[..., i][group], ref[..., i][group]
+                off, size = np.linalg.norm(a - b), np.linalg.norm(b)
+                assert off <= tol * size + 1e-30, (level, off / max(size, 1e-300), tol)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_decay_gradients_that_forget_in_every_layout(ss, dtype):
+    """The sizes, strides, shared heads, lengths and dead tokens of the other tests, each head with its own level; NaN past the ends;
+    twice the same bits."""
+    import torch
+    from oracle.deltarule import deltarule_bwd_ref
+    from tests.test_gpu_deltarule import _bwd, _np, _tol
+    for B, L, H, G, K, V, opt in CASES:
+        if opt.get("decay") is False or opt.get("strong"):
+            continue
+        d = _case(B, L, H, G, K, V, dtype, seed=L, **opt)
+        d["g"] = torch.tensor(([-9.0, -0.5, -20.0] * H)[:H], device="cuda") * (0.9 + 0.2 * torch.rand(B, L, H, device="cuda"))
+        n = None if d["lengths"] is None else np.clip(_np(d["lengths"]), 0, L)
+        dead = None
+        if n is not None:
+            dead = torch.arange(L, device="cuda")[None, :] >= torch.tensor(n, device="cuda")[:, None]
+            for name in ("q", "k", "v", "do", "g", "beta"):
+                d[name] = torch.where(dead.view(B, L, *[1] * (d[name].dim() - 2)), torch.full_like(d[name], float("nan")), d[name])
+        ckpt = _fwd(ss, d)[1]
+        got = _bwd(ss, d, ckpt)["dg"]
+        assert torch.equal(got, _bwd(ss, d, ckpt)["dg"])
+        assert dead is None or (got[dead] == 0).all()
+        ref = deltarule_bwd_ref(*[np.nan_to_num(_np(d[x])) if d[x] is not None else None for x in ("q", "k", "v", "g", "beta", "do", "h0", "dh_last")], lengths=n)["dg"]
+        tol = _tol(L, dtype, False, 3) * (np.exp(2) if dtype == "bf16" else 1.0) + (3 * 2.0 ** -16 if dtype == "bf16" else 0.0)
+        for h in range(H):
+            off, size = np.linalg.norm(_np(got)[..., h] - ref[..., h]), np.linalg.norm(ref[..., h])
+            assert off <= tol * size + 1e-30, (B, L, H, K, V, h, off / max(size, 1e-300), tol)
+    assert ss.device_status() == 0
