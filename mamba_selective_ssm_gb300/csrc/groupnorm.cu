@@ -12,8 +12,8 @@
 //                                shared memory: one pass too.
 //   else                         sums by (sample, channels, rows) in fixed parts, a kernel that joins them, and a second
 //                                pass for the output, which takes the rows from the last: L2 still holds those.
-// The variance is taken around the mean (parts around their own first row, joined with their means), never as a difference
-// of moments.  The backward's column sums are joined by colsum_kernel in fixed order.
+// The variance is taken around the mean (in parts around the mean of a few rows at a time, joined with their means), never as a
+// difference of moments.  The backward's column sums are joined by colsum_kernel in fixed order.
 //
 // bf16 with SiLU, floors at 6.7 TB/s in brackets: 8192 x 1 x 4096 in 32 groups, forward 28 us (20; instructions of short rows:
 // 61 % of the issue slots), backward 50 + 6 (40); 4 x 2048 x 4096 forward 43 (20; x is read twice, the second time from L2 in
@@ -493,73 +493,113 @@ struct Where {
     m1 = m0 + q.per < p.M ? m0 + q.per : p.M;
   }
 };
-// the row lanes' sums, added in order: red[thread][8] -> the first lane
+// the row lanes' sums, in pairs: red[thread][8] -> the first lane, and there
 __device__ __forceinline__ void lanes_add(float4 (*red)[kGnThreads], int ut, int lanes, float2 (&s)[4]) {
+  const int tid = threadIdx.x, rl = tid / ut;
   __syncthreads();
-  red[0][threadIdx.x] = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
-  red[1][threadIdx.x] = make_float4(s[2].x, s[2].y, s[3].x, s[3].y);
-  __syncthreads();
-  if ((int)threadIdx.x < ut)
-    for (int l = 1; l < lanes; ++l) {
-      const float4 a = red[0][l * ut + threadIdx.x], b = red[1][l * ut + threadIdx.x];
+  red[0][tid] = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
+  red[1][tid] = make_float4(s[2].x, s[2].y, s[3].x, s[3].y);
+  int h = 1;
+  while (h < lanes) h *= 2;
+  for (h /= 2; h > 0; h /= 2) {
+    __syncthreads();
+    if (rl < h && rl + h < lanes) {
+      const float4 a = red[0][tid + h * ut], b = red[1][tid + h * ut];
       s[0] = add2(s[0], f2(a.x, a.y));
       s[1] = add2(s[1], f2(a.z, a.w));
       s[2] = add2(s[2], f2(b.x, b.y));
       s[3] = add2(s[3], f2(b.z, b.w));
+      red[0][tid] = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
+      red[1][tid] = make_float4(s[2].x, s[2].y, s[3].x, s[3].y);
     }
+  }
 }
 template <typename T>
 constexpr int kGnAhead = 16 / sizeof(T);  // rows of a thread in flight: 128 bytes
 
-// part[n][split][c] = the rows' sum, and after all of those the sum of squares around their mean.  The sum is taken of the
-// values themselves (a mean near zero would keep the rounding of whatever it is taken around), the squares around the first
-// row's value.
+// part[n][split][c] = the rows' sum, and after all of those the sum of squares around their mean.  A thread's rows come in sets
+// of a few: a set's squares are taken around its own mean, and sets, then threads, are joined as
+//   m2 = m2_a + m2_b + (mean_a - mean_b)^2 n_a n_b / (n_a + n_b),
+// sums of squares all, so that no row (a first one of zeros, one far from the others) costs the variance its digits, as it did when
+// the squares were taken around the first row: 1e-4 of rstd for 4096 rows a thread's part of deviation 1 and mean 100 behind one of
+// zeros.  A thread's sum carries what its additions drop (kahan), since a thread may have most of a long sample.
 template <typename T>
 __global__ void __launch_bounds__(kGnThreads, 2) gn_stats_kernel(Gn p, Part q, const T* __restrict__ x, float* __restrict__ part) {
   using R = Raw8<T>;
   __shared__ float4 red[2][kGnThreads];
   pdl_trigger();
   const Where w(p, q);
-  float2 base[4], s0[4], s1[4], s2[4];
+  float2 s[4], lost[4], m2[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) base[e] = s0[e] = s1[e] = s2[e] = f2(0.f, 0.f);
+  for (int e = 0; e < 4; ++e) s[e] = lost[e] = m2[e] = f2(0.f, 0.f);
   const T* src = x + w.n * p.M * p.C + w.c;
   constexpr int A = kGnAhead<T>;
+  float n = 0.f;  // rows so far
   if (w.on) {
-    wide4<T>(R::ld(src + (long long)w.m0 * p.C), base);
     for (int m = w.m0 + w.rl; m < w.m1; m += A * w.lanes) {
       typename R::V raw[A];
+      int rows = 0;
 #pragma unroll
       for (int u = 0; u < A; ++u)
-        if (m + u * w.lanes < w.m1) raw[u] = R::ld(src + (long long)(m + u * w.lanes) * p.C);
+        if (m + u * w.lanes < w.m1) {
+          raw[u] = R::ld(src + (long long)(m + u * w.lanes) * p.C);
+          rows = u + 1;
+        }
+      float2 b[4], mb[4], sq[4], v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = sq[e] = f2(0.f, 0.f);
 #pragma unroll
       for (int u = 0; u < A; ++u) {
-        if (m + u * w.lanes >= w.m1) break;
-        float2 v[4];
+        if (u >= rows) break;
+        wide4<T>(raw[u], v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] = add2(b[e], v[e]);
+      }
+      const float nb = (float)rows, ib = rows == A ? 1.f / A : __frcp_rn(nb);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mb[e] = mul2(b[e], bc2(-ib));
+#pragma unroll
+      for (int u = 0; u < A; ++u) {
+        if (u >= rows) break;
         wide4<T>(raw[u], v);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s0[e] = add2(s0[e], v[e]);
-          v[e] = fma2(base[e], bc2(-1.f), v[e]);
-          s1[e] = add2(s1[e], v[e]);
-          s2[e] = fma2(v[e], v[e], s2[e]);
+          v[e] = add2(v[e], mb[e]);
+          sq[e] = fma2(v[e], v[e], sq[e]);
         }
+      }
+      const float in = n > 0.f ? __frcp_rn(n) : 0.f, wt = __fdividef(n * nb, n + nb);
+      n += nb;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 d = fma2(s[e], bc2(in), mb[e]);  // (of the rows before, minus the set's)
+        m2[e] = add2(m2[e], fma2(mul2(d, bc2(wt)), d, sq[e]));
+        const float2 y = fma2(lost[e], bc2(-1.f), b[e]), t = add2(s[e], y);
+        lost[e] = fma2(y, bc2(-1.f), fma2(s[e], bc2(-1.f), t));
+        s[e] = t;
       }
     }
   }
-  lanes_add(red, q.ut, w.lanes, s0);
-  lanes_add(red, q.ut, w.lanes, s1);
-  lanes_add(red, q.ut, w.lanes, s2);
-  if (w.on && w.rl == 0) {
-    const float inv = 1.f / (float)(w.m1 - w.m0);
-    float* at = part + (w.n * q.splits + w.split) * p.C + w.c;
+  float2 own[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) own[e] = s[e];
+  lanes_add(red, q.ut, w.lanes, s);
+  __syncthreads();
+  {
+    const float4 a = red[0][threadIdx.x % q.ut], b = red[1][threadIdx.x % q.ut];
+    const float2 all[4] = {f2(a.x, a.y), f2(a.z, a.w), f2(b.x, b.y), f2(b.z, b.w)};
+    const float inv = -1.f / (float)(w.m1 - w.m0), in = n > 0.f ? __frcp_rn(n) : 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 d = fma2(mul2(s1[e], bc2(-inv)), s1[e], s2[e]);
-      s2[e] = f2(fmaxf(d.x, 0.f), fmaxf(d.y, 0.f));
+      const float2 d = fma2(own[e], bc2(in), mul2(all[e], bc2(inv)));
+      m2[e] = fma2(mul2(d, bc2(n)), d, m2[e]);
     }
-    st4p<float>(at, s0);
-    st4p<float>(at + (long long)p.N * q.splits * p.C, s2);
+  }
+  lanes_add(red, q.ut, w.lanes, m2);
+  if (w.on && w.rl == 0) {
+    float* at = part + (w.n * q.splits + w.split) * p.C + w.c;
+    st4p<float>(at, s);
+    st4p<float>(at + (long long)p.N * q.splits * p.C, m2);
   }
 }
 

@@ -1,0 +1,67 @@
+"""Group norm's statistics where rows are unlike one another: a first position of zeros before data with a mean, a position far from
+all others, values that are all alike.
+
+Tolerances as in test_gpu_groupnorm.py, and no wider for any of these: statistics to STEP (2 sqrt(M + 32) + 24), the mean of the
+values' root mean square and rstd of itself (an error d of the mean, in deviations, adds d^2 / 2 to it); y is off by the same, and by
+the mean's error in deviations."""
+
+import numpy as np
+import pytest
+
+from tests.gpu_util import ss_module
+from tests.test_gpu_groupnorm import STEP, _near, _np
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ss():
+    return ss_module()
+
+
+SHAPES = [(3, 1, 512, 4), (4, 1, 1024, 2), (3, 8, 64, 4), (200, 6, 128, 8),  # in lanes, and a sample in a CTA
+          (2, 600, 64, 4), (4, 2048, 256, 8), (64, 16384, 64, 8), (320, 4096, 8, 1), (1, 30000, 24, 3), (310, 700, 520, 13)]  # in parts
+
+
+@pytest.mark.parametrize("kind", ["zeros first", "zeros last", "spike first", "spike inside", "one channel", "alike"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,M,C,groups", SHAPES)
+def test_statistics_of_rows_unlike_one_another(ss, N, M, C, groups, dtype, kind):
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(M + C)
+    x = torch.randn(N, M, C, device="cuda", generator=gen) + 100.0
+    if kind == "zeros first":
+        x[:, 0] = 0.0
+    elif kind == "zeros last":
+        x[:, -1] = 0.0
+    elif kind == "spike first":
+        x = x - 100.0
+        x[:, 0] = 700.0
+    elif kind == "spike inside":
+        x = x - 100.0
+        x[:, M // 2, ::2] = -300.0
+    elif kind == "one channel":
+        x[..., 1] = 5000.0
+    else:
+        x = torch.full_like(x, 0.1) + (torch.arange(C, device="cuda") % 2) * 0.25
+    x = x.to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    scale = torch.ones(C, device="cuda")
+    y, mean, rstd = ss.groupnorm_fwd(x, scale, None, groups, 1e-3)
+    means, rstds, off = [], [], 0.0
+    tol = STEP * (2 * (M + 32) ** 0.5 + 24)
+    total = size = 0.0
+    for n in range(N):  # float64, a sample at a time
+        f = x[n].double().view(M, groups, C // groups)
+        m = f.mean((0, 2))
+        d = f - m[:, None]
+        r = ((d * d).mean((0, 2)) + 1e-3).rsqrt()
+        e = d * r[:, None]
+        total += float(((y[n].double().view_as(e) - e) ** 2).sum())
+        size += float((e * e).sum())
+        off = max(off, float((f.square().mean((0, 2)).sqrt() * r).max()))
+        means.append(m)
+        rstds.append(r)
+    _near(mean, _np(torch.stack(means)), tol, "mean", size=float(x.double().square().mean().sqrt()))
+    _near(rstd, _np(torch.stack(rstds)), tol + (off * tol) ** 2, "rstd")
+    typed = 2.0 ** -8 if dtype == "bf16" else 0.0
+    assert total ** 0.5 <= (tol * (1 + off) + typed) * max(size, N * M * C * 1e-6) ** 0.5, (total ** 0.5, size ** 0.5)
