@@ -52,6 +52,15 @@ inline int resident_ctas(K kern, int threads, size_t smem) {
   return n;
 }
 
+// How much dynamic shared memory a kernel may be launched with.  That is a property of the kernel, not of a launch, so a kernel
+// whose launches differ in it is always given the same: set to each launch's own size, it could be lowered by a call of
+// another host thread between this one's setting and its launch, which then failed.
+constexpr int kSmemMost = 227 * 1024;
+template <typename K>
+inline bool allow_smem(K kern, int most = kSmemMost) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) == cudaSuccess;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

@@ -381,7 +381,7 @@ int walk(const Delta& p, const __nv_bfloat16* dout, const float* dh_last, __nv_b
       !delta_map(&maps.dy, dout, ldo, a.B, a.L, a.H, a.V) || !delta_map(&maps.dv, dv, ldo, a.B, a.L, a.H, a.V))
     return SS_ERR_CUDA;
   static_assert(BackTc<KP>::bytes <= 227 * 1024, "a chunk's tiles fit shared memory");
-  return lin_launch(delta_back_tc_kernel<KP>, (unsigned)((long long)a.B * a.H), kDThreads, BackTc<KP>::bytes, s, p, maps, dh_last, dv, dS, du, dh0);
+  return delta_launch(delta_back_tc_kernel<KP>, (unsigned)((long long)a.B * a.H), kDThreads, BackTc<KP>::bytes, s, p, maps, dh_last, dv, dS, du, dh0);
 }
 
 }  // namespace

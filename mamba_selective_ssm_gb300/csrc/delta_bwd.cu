@@ -882,7 +882,7 @@ int chain(const BwdPlan& pl, const BwdArgs& x, cudaStream_t s) {
   const int nvt = (a.V + 16 * warps - 1) / (16 * warps);
   // as in the forward (192 heads of 64 x 64: 334 us for 445)
   const int sb = St::bytes(warps), stages = 2 * sb <= 226 * 1024 && bh * nvt <= 152 ? 2 : 1;
-  return lin_launch(delta_bwd_kernel<KP>, (unsigned)(bh * nvt), 32 * warps, (size_t)sb * stages, s, pl.p, static_cast<const float*>(x.dout),
+  return delta_launch(delta_bwd_kernel<KP>, (unsigned)(bh * nvt), 32 * warps, (size_t)sb * stages, s, pl.p, static_cast<const float*>(x.dout),
                     x.dh_last, static_cast<float*>(x.dv), x.dS, x.du, x.dh0, stages, sb);
 }
 

@@ -62,8 +62,15 @@ __host__ __device__ inline long long delta_ckpt_floats(int nck, int K, int V) {
 // and its tensor memory are then ready when that is done (3 to 5 us a pair).
 template <typename... KArgs, typename... Args>
 inline int delta_launch_next(void (*kern)(KArgs...), unsigned grid, int threads, size_t smem, cudaStream_t s, Args... args) {
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SS_ERR_CUDA;
+  if (!allow_smem(kern)) return SS_ERR_CUDA;
   return launch_dependent(kern, dim3(grid), dim3((unsigned)threads), smem, s, args...) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+}
+
+template <typename... KArgs, typename... Args>
+inline int delta_launch(void (*kern)(KArgs...), unsigned grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+  if (!allow_smem(kern)) return SS_ERR_CUDA;
+  kern<<<grid, threads, smem, s>>>(args...);
+  return cudaGetLastError() == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
 
 inline int delta_validate(int B, int L, int H, int G, int K, int V, int dtype) {

@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(Delta p) {
 
 template <typename T, int KP>
 int prep(const Delta& p, cudaStream_t s) {
-  return lin_launch(delta_prep_kernel<T, KP>, (unsigned)((long long)p.a.B * p.a.H * p.a.nck), kPrepThreads, PrepSmem<T, KP>::bytes, s, p);
+  return delta_launch(delta_prep_kernel<T, KP>, (unsigned)((long long)p.a.B * p.a.H * p.a.nck), kPrepThreads, PrepSmem<T, KP>::bytes, s, p);
 }
 
 }  // namespace

@@ -911,7 +911,7 @@ int fwd(const GnPlan& pl, const T* x, const float* scale, const float* bias, T* 
   } else if (pl.form == kSample) {
     const size_t smem = pl.items * kGnThreads * sizeof(typename Raw8<T>::V) + (gn_part_floats(p) + 2 * p.groups) * sizeof(float);
     const auto kernel = gn_fwd_sample_kernel<T, SILU>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SS_ERR_CUDA;
+    if (!allow_smem(kernel)) return SS_ERR_CUDA;
     kernel<<<pl.grid, kGnThreads, smem, s>>>(p, pl.items, x, scale, bias, y, mean, rstd);
   } else {
     const Part& q = pl.q;
@@ -951,7 +951,7 @@ int bwd(const GnPlan& pl, const T* dy, const T* x, const float* scale, const flo
   } else if (pl.form == kSample) {
     const size_t smem = 2 * pl.items * kGnThreads * sizeof(typename Raw8<T>::V) + (gn_part_floats(p) + 2 * p.C + 2 * p.groups) * sizeof(float);
     const auto kernel = gn_bwd_sample_kernel<T, SILU>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SS_ERR_CUDA;
+    if (!allow_smem(kernel)) return SS_ERR_CUDA;
     kernel<<<pl.grid, kGnThreads, smem, s>>>(p, pl.items, dy, x, scale, bias, mean, rstd, dx, part);
   } else {
     const Part& q = pl.q;

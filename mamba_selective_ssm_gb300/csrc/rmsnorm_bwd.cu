@@ -359,7 +359,7 @@ int rms_tma_launch(const void* dy, const void* x, const float* scale, const floa
   const T* g = static_cast<const T*>(dy);
   const T* xx = static_cast<const T*>(x);
   auto run = [&](auto kern) -> int {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SS_ERR_CUDA;
+    if (!allow_smem(kern, kSmemMost - 1024)) return SS_ERR_CUDA;  // (less a kernel's static arrays)
   // prefer the largest shared-memory carveout, so that residency (and the occupancy
   // query the segment and grid choices rely on) is limited by the CTAs' own needs
   cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);

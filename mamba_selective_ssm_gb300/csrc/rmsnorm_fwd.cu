@@ -260,7 +260,7 @@ int rms_fwd_warp_launch(const void* x, const float* scale, float eps, void* y, f
   if (nst < 2) nst = 2;
   const size_t smem = (size_t)kRmsFWarps * nst * rb + (size_t)kRmsFWarps * nst * sizeof(uint64_t);
   auto run = [&](auto kern) -> int {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SS_ERR_CUDA;
+    if (!allow_smem(kern, kSmemMost - 1024)) return SS_ERR_CUDA;  // (less a kernel's static arrays)
     cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
     const int per_sm = resident_ctas(kern, 32 * kRmsFWarps, smem);
     if (per_sm < 1) return SS_ERR_CUDA;
@@ -444,7 +444,7 @@ int rms_fwd_launch(const void* x, const float* scale, float eps, void* y, float*
     const int threads = (groups + 31) / 32 * 32;
     const size_t smem = (size_t)nst * dim * sizeof(T) + (size_t)nst * sizeof(uint64_t);
     auto kern = rms_fwd_tma_kernel<T>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SS_ERR_CUDA;
+    if (!allow_smem(kern, kSmemMost - 1024)) return SS_ERR_CUDA;  // (less a kernel's static arrays)
   // prefer the largest shared-memory carveout, so that residency (and the occupancy
   // query the segment and grid choices rely on) is limited by the CTAs' own needs
   cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);

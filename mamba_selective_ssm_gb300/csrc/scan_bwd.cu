@@ -922,7 +922,7 @@ int launch_bwd_f(BwdParams p, const void* x, const void* delta, const void* Bm, 
   // allocation would wait for another CTA to finish.  Ask for enough shared
   // memory per CTA to keep the residency within that bound.
   size_t smem_launch = smem;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SS_ERR_CUDA;
+  if (!allow_smem(kern)) return SS_ERR_CUDA;
   // prefer the largest shared-memory carveout, so that residency (and the occupancy
   // query the segment and grid choices rely on) is limited by the CTAs' own needs
   cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
@@ -934,8 +934,6 @@ int launch_bwd_f(BwdParams p, const void* x, const void* delta, const void* Bm, 
     smem_launch = (size_t)(227 * 1024) / (size_t)(max_ctas + 1) + 1024;
     if (smem_launch < smem) smem_launch = smem;
     if (smem_launch > 227 * 1024) smem_launch = 227 * 1024;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_launch) != cudaSuccess)
-      return SS_ERR_CUDA;
     per_sm = resident_ctas(kern, Geo<N, DT>::NT, smem_launch);
     if (per_sm < 1) return SS_ERR_CUDA;
     if ((uint32_t)per_sm * p.tcols > 512u) return SS_ERR_UNSUPPORTED;
