@@ -90,7 +90,7 @@ def ss_scan_fwd(x, delta, A, Bm, Cm, Dv, z, h0=None, chunk: int = 64, want_h_las
     """Forward scan -> ``(y, ckpt, h_last)``.  With ``dt_bias`` / ``delta_softplus`` the
     recurrence uses softplus(delta + dt_bias) (or delta + dt_bias), computed in the kernel."""
     lib = load()
-    B, L, D = x.shape
+    B, L, D = _int_sizes(*x.shape)
     N = A.shape[1]
     dev, dt = x.device, x.dtype
     _act_dtype(x)
@@ -131,7 +131,7 @@ def ss_scan_bwd(x, delta, A, Bm, Cm, Dv, z, ckpt, dy, dh_last=None, chunk: int =
     With the fused discretisation (same ``dt_bias`` / ``delta_softplus`` as the forward),
     ``ddelta`` is the gradient of the raw delta and ``d_dt_bias`` accumulates (zeros when None)."""
     lib = load()
-    B, L, D = x.shape
+    B, L, D = _int_sizes(*x.shape)
     N = A.shape[1]
     dev, dt = x.device, x.dtype
     _act_dtype(x)
@@ -176,7 +176,7 @@ def ss_scan_fwd_summary(x, delta, A, Bm, dt_bias=None, delta_softplus: bool = Fa
     """Forward summary of one piece of a sequence -> ``(h_end [B,D,N], delta_sum [B,D])``:
     the state the piece reaches from a zero start and its sum of (discretised) delta."""
     lib = load()
-    B, L, D = x.shape
+    B, L, D = _int_sizes(*x.shape)
     N = A.shape[1]
     dev, dt = x.device, x.dtype
     _act_dtype(x)
@@ -237,7 +237,7 @@ def ss_scan_carries(A, delta_sum, summ, init=None, reverse: bool = False):
 
 def conv1d_causal_bwd(dout, x, w, dw=None, db=None, workspace=None):
     lib = load()
-    B, L, D = x.shape
+    B, L, D = _int_sizes(*x.shape)
     K = w.shape[1]
     dev = x.device
     xdt = _act_dtype(x)
@@ -259,7 +259,7 @@ def conv1d_causal_bwd(dout, x, w, dw=None, db=None, workspace=None):
 def conv1d_causal_silu_bwd(dact, x, w, bias=None, dw=None, db=None, workspace=None):
     """Backward through silu(conv1d(x) + bias) given dL/d(silu output); dw, db accumulate."""
     lib = load()
-    B, L, D = x.shape
+    B, L, D = _int_sizes(*x.shape)
     K = w.shape[1]
     dev = x.device
     xdt = _act_dtype(x)
@@ -282,7 +282,7 @@ def conv1d_causal_silu_bwd(dact, x, w, bias=None, dw=None, db=None, workspace=No
 
 def rmsnorm_bwd(dy, x, scale, rms, dscale=None, workspace=None):
     lib = load()
-    R, H = x.shape
+    R, H = _int_sizes(*x.shape)
     dev = x.device
     dt = _act_dtype(x)
     _req(dy, "dy", (R, H), x.dtype, dev)
@@ -304,7 +304,7 @@ def rmsnorm_bwd(dy, x, scale, rms, dscale=None, workspace=None):
 def conv1d_causal_fwd(x, w, bias=None, silu: bool = False, out=None):
     """Depthwise causal conv1d (+ optional SiLU); ``out`` has x's dtype."""
     lib = load()
-    B, L, D = x.shape
+    B, L, D = _int_sizes(*x.shape)
     K = w.shape[1]
     dev = x.device
     xdt = _act_dtype(x)
@@ -321,7 +321,7 @@ def conv1d_causal_fwd(x, w, bias=None, silu: bool = False, out=None):
 def rmsnorm_fwd(x, scale, eps: float, want_rms: bool = True):
     """RMSNorm forward: ``(y, rms)`` with y in x's dtype and rms fp32 (None unless ``want_rms``)."""
     lib = load()
-    R, H = x.shape
+    R, H = _int_sizes(*x.shape)
     dev = x.device
     dt = _act_dtype(x)
     _req(x, "x", (R, H), x.dtype, dev)
@@ -336,7 +336,7 @@ def rmsnorm_fwd(x, scale, eps: float, want_rms: bool = True):
 def ss_scan_step(x, delta, A, Bm, Cm, Dv, z, h):
     """One decode step for B sequences: updates ``h`` [B,D,N] in place and returns y [B,D]."""
     lib = load()
-    B, D = x.shape
+    B, D = _int_sizes(*x.shape)
     N = A.shape[1]
     dev, dt = x.device, x.dtype
     _act_dtype(x)
@@ -357,7 +357,7 @@ def ss_scan_step(x, delta, A, Bm, Cm, Dv, z, h):
 def conv1d_causal_step(x, conv_state, w, bias=None, silu: bool = False):
     """One conv step for B sequences: shifts ``conv_state`` [B,D,K] in place and returns out [B,D]."""
     lib = load()
-    B, D = x.shape
+    B, D = _int_sizes(*x.shape)
     K = w.shape[1]
     dev = x.device
     xdt = _act_dtype(x)
@@ -442,13 +442,20 @@ def _layernorm_plan(R, N):
     return load().layernorm_bwd_workspace_size(R, N)
 
 
+def _int_sizes(*sizes):
+    """The library takes sizes as 32-bit integers, and ctypes cuts a longer one without a word."""
+    if max(sizes) > 2147483647:
+        raise ValueError(f"sizes {sizes} reach 2^31, more than a call takes")
+    return sizes
+
+
 def _linattn_sizes(q, v):
     if not isinstance(q, torch.Tensor) or not isinstance(v, torch.Tensor):
         raise TypeError("q, k, v must be torch.Tensor")
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError(f"q, k must be [B, L, G, K] and v [B, L, H, V], got {tuple(q.shape)} and {tuple(v.shape)}")
     B, L, G, K = q.shape
-    return B, L, v.shape[2], G, K, v.shape[3]
+    return _int_sizes(B, L, v.shape[2], G, K, v.shape[3])
 
 
 def _linattn_gate(g, B, L, H, dev):
@@ -648,7 +655,7 @@ def deltarule_step(q, k, v, g, beta, h, scale=None):
 def layernorm_fwd(x, scale, bias, eps: float, want_stats: bool = True):
     """Layer norm of the rows of x [rows, dim]: ``(y, mean, rstd)`` with y in x's dtype and the statistics fp32 (None
     unless ``want_stats``); ``bias`` may be None."""
-    R, N = x.shape
+    R, N = _int_sizes(*x.shape)
     dev, f32 = x.device, torch.float32
     dt = _act_dtype(x)
     px, ps = _at(x, "x", (R, N), x.dtype, dev), _at(scale, "scale", (N,), f32, dev)
@@ -666,7 +673,7 @@ def layernorm_fwd(x, scale, bias, eps: float, want_stats: bool = True):
 def layernorm_bwd(dy, x, scale, mean, rstd, dscale=None, dbias=None, workspace=None):
     """Layer norm backward -> ``(dx, dscale, dbias)``, all fp32; dscale and dbias accumulate into the given tensors
     and are made when None."""
-    R, N = x.shape
+    R, N = _int_sizes(*x.shape)
     dev, f32 = x.device, torch.float32
     dt = _act_dtype(x)
     py, px = _at(dy, "dy", (R, N), x.dtype, dev), _at(x, "x", (R, N), x.dtype, dev)
@@ -699,7 +706,7 @@ def _groupnorm_sizes(x):
         raise TypeError("x must be a torch.Tensor")
     if x.dim() < 2:
         raise ValueError(f"x must be [N, ..., C], got {tuple(x.shape)}")
-    return x.shape[0], math.prod(x.shape[1:-1]), x.shape[-1]
+    return _int_sizes(x.shape[0], math.prod(x.shape[1:-1]), x.shape[-1])
 
 
 def groupnorm_fwd(x, scale, bias, groups: int, eps: float, silu: bool = False, want_stats: bool = True, workspace=None):
