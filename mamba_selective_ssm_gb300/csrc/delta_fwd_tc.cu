@@ -120,8 +120,9 @@ __global__ void __launch_bounds__(kDThreads, 1) delta_fwd_tc_kernel(Delta p, con
       }
       __syncwarp();
     };
-    // a product with M or P, of which the column tiles from 16 s on are not zero.  `pairs`: its pairs of terms from the
-    // smallest, left in the low and right in the high bits of four
+    // a product with M or P, of which the column tiles from 16 s on are not zero (products of whole tiles give the same bits at all
+    // sizes of the tests, and take 4 % longer in the forward).  `pairs`: its pairs of terms from the smallest, left in the low and
+    // right in the high bits of four
     auto lower = [&](uint32_t right, uint32_t pairs, int n, auto mma) {
 #pragma unroll 1
       for (int i = 0; i < n; ++i, pairs >>= 4) {
@@ -201,7 +202,8 @@ __global__ void __launch_bounds__(kDThreads, 1) delta_fwd_tc_kernel(Delta p, con
         mma_commit(&bar[L::kD5]);
       }
       __syncwarp();
-      if (!wait(L::kPr, par) || !wait(L::kU, par)) break;
+      // (D4's place is that of w, which D5 reads; the wait costs 0.5 % of 4 x 2048 tokens, 1.7 % of 1 x 16384)
+      if (!wait(L::kPr, par) || !wait(L::kU, par) || !wait(L::kD5, par)) break;
       if (elect_one()) {
         tc_fence_after_sync();
         lower(sb + L::p, 0x041852u, 6,
