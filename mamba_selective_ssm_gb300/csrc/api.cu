@@ -72,6 +72,7 @@ extern "C" int ss_device_status(void* stream) {
                                                    ssh::read_clear_rmsf_err, ssh::read_clear_linf_err, ssh::read_clear_linb_err,
                                                    ssh::read_clear_delf_err, ssh::read_clear_delb_err, ssh::read_clear_delg_err};
   unsigned any = 0;
+  if (cudaStreamSynchronize(s) != cudaSuccess) return SS_ERR_CUDA;
   for (auto read : words) {
     unsigned w = 0;
     if (read(s, &w) != SS_OK) return SS_ERR_CUDA;

@@ -284,10 +284,7 @@ using namespace ssk;
 __device__ unsigned g_lin_err;  // this translation unit's error word: a wait for its own MMAs ran out
 
 inline int read_clear_lin_err(cudaStream_t s, unsigned* out) {
-  unsigned zero = 0;
-  if (cudaMemcpyFromSymbolAsync(out, g_lin_err, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess) return SS_ERR_CUDA;
-  if (cudaMemcpyToSymbolAsync(g_lin_err, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s) != cudaSuccess) return SS_ERR_CUDA;
-  return cudaStreamSynchronize(s) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+  return ssk::read_clear_word(g_lin_err, s, out);
 }
 
 // A whole warp waits for a phase of a barrier, and leaves together: tensor-memory

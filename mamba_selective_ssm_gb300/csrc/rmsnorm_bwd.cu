@@ -565,10 +565,7 @@ int noalloc_scratch(float** out) {
 
 namespace ssh {
 int read_clear_rms_err(cudaStream_t s, unsigned* out) {
-  unsigned zero = 0;
-  if (cudaMemcpyFromSymbolAsync(out, g_rms_err, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess) return SS_ERR_CUDA;
-  if (cudaMemcpyToSymbolAsync(g_rms_err, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s) != cudaSuccess) return SS_ERR_CUDA;
-  return cudaStreamSynchronize(s) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+  return ssk::read_clear_word(g_rms_err, s, out);
 }
 }  // namespace ssh
 

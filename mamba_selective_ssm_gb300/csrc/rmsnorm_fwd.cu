@@ -472,12 +472,7 @@ int rms_fwd_launch(const void* x, const float* scale, float eps, void* y, float*
 
 namespace ssh {
 int read_clear_rmsf_err(cudaStream_t s, unsigned* out) {
-  unsigned zero = 0;
-  if (cudaMemcpyFromSymbolAsync(out, g_rmsf_err, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess)
-    return SS_ERR_CUDA;
-  if (cudaMemcpyToSymbolAsync(g_rmsf_err, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s) != cudaSuccess)
-    return SS_ERR_CUDA;
-  return cudaStreamSynchronize(s) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+  return ssk::read_clear_word(g_rmsf_err, s, out);
 }
 }  // namespace ssh
 

@@ -1048,10 +1048,7 @@ int bwd_summary_fuse(const BwdParams& p, const void* delta, const void* Cm, cons
 
 namespace ssh {
 int read_clear_bwd_err(cudaStream_t s, unsigned* out) {
-  unsigned zero = 0;
-  if (cudaMemcpyFromSymbolAsync(out, g_bwd_err, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess) return SS_ERR_CUDA;
-  if (cudaMemcpyToSymbolAsync(g_bwd_err, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s) != cudaSuccess) return SS_ERR_CUDA;
-  return cudaStreamSynchronize(s) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+  return ssk::read_clear_word(g_bwd_err, s, out);
 }
 }  // namespace ssh
 

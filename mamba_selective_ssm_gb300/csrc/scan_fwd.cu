@@ -398,10 +398,7 @@ int fwd_summary_fuse(const FwdParams& p, const void* x, const void* delta, const
 
 namespace ssh {
 int read_clear_fwd_err(cudaStream_t s, unsigned* out) {
-  unsigned zero = 0;
-  if (cudaMemcpyFromSymbolAsync(out, g_fwd_err, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess) return SS_ERR_CUDA;
-  if (cudaMemcpyToSymbolAsync(g_fwd_err, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s) != cudaSuccess) return SS_ERR_CUDA;
-  return cudaStreamSynchronize(s) == cudaSuccess ? SS_OK : SS_ERR_CUDA;
+  return ssk::read_clear_word(g_fwd_err, s, out);
 }
 }  // namespace ssh
 
