@@ -457,9 +457,11 @@ int linattn_step(const void* q, const void* k, const void* v, const float* g, in
  *          as -160
  *   beta : [B, L, H] fp32.  The state stays bounded for 0 <= beta_t |k_t|^2 <= 2;
  *          keys are normally of length one (rmsnorm_fwd over the rows of k with
- *          scale K^-1/2 makes them so).  Elements of k and q of 2^60 and more
- *          come out as infinities with fp32 activations; those of a token below
- *          2^-24 of its largest lose bits there.
+ *          scale K^-1/2 makes them so).  With fp32 activations, elements of k
+ *          of 2^60 and more come out as infinities and keys below 2^-60 lose
+ *          bits, as do elements of a token's k, q or dout below 2^-24 of its
+ *          largest, and the gradients of a token whose k, q or dout is below
+ *          2^-16 of the largest in its chunk.
  *   B * H at most 2^24, and B * H * ceil(L / 64) below 2^28.
  * The sequence is worked through in chunks of 64 tokens; a NaN or infinity in a
  * live token can reach the other tokens of its chunk, earlier ones among them,

@@ -87,8 +87,8 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
     const long long item = bh * a.nck + ck;
     cp_wait<0>();
     __syncthreads();
-    tile_scale<KP>(at + St::k, up, tid, nt);
-    tile_scale<KP>(at + St::q, up + kDC, tid, nt);
+    tile_scale<KP, true>(at + St::k, up, tid, nt);
+    tile_scale<KP, false>(at + St::q, up + kDC, tid, nt);
     __syncthreads();
     if (stages == 2 && ck > 0) fetch(ck - 1);
 #pragma unroll
@@ -457,9 +457,9 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
   }
   cp_wait<0>();
   __syncthreads();
-  tile_scale<KP>(sb + Sm::k, up, tid, kGradThreads);
-  tile_scale<KP>(sb + Sm::q, up + kDC, tid, kGradThreads);
-  tile_scale<VP>(sb + Sm::doo, up + 2 * kDC, tid, kGradThreads);
+  tile_scale<KP, true>(sb + Sm::k, up, tid, kGradThreads);
+  tile_scale<KP, false>(sb + Sm::q, up + kDC, tid, kGradThreads);
+  tile_scale<VP, false>(sb + Sm::doo, up + 2 * kDC, tid, kGradThreads);
   __syncthreads();
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -719,8 +719,8 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
   if constexpr (Sm::turns) {
     cp_wait<0>();
     __syncthreads();
-    tile_scale<KP>(sb + Sm::k, up, tid, kGradThreads);
-    tile_scale<KP>(sb + Sm::q, up + kDC, tid, kGradThreads);
+    tile_scale<KP, true>(sb + Sm::k, up, tid, kGradThreads);
+    tile_scale<KP, false>(sb + Sm::q, up + kDC, tid, kGradThreads);
   }
   __syncthreads();
   if (dg != nullptr) {

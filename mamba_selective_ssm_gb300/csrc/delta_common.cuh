@@ -138,8 +138,12 @@ __device__ __forceinline__ Pow2 pow2_of(float m) {
 }
 // an operand of a product: its largest value into [2^13, 2^14)
 __device__ __forceinline__ Pow2 operand_scale(float m) { return pow2_of<13, 14, 253>(m); }
-// a key or query: its largest element into [1, 2); elements of 2^60 and more overflow
-__device__ __forceinline__ Pow2 token_scale(float m) { return m == 0.f ? Pow2{1.f, 1.f} : pow2_of<0, 127 - 60, 127 + 60>(m); }
+// a token's row: its largest element into [1, 2).  A key's scale is squared in beta', so keys have it within 2^60 of 1: elements
+// of 2^60 and more overflow, those of keys below 2^-60 lose bits.
+template <bool KEY>
+__device__ __forceinline__ Pow2 token_scale(float m) {
+  return m == 0.f ? Pow2{1.f, 1.f} : KEY ? pow2_of<0, 127 - 60, 127 + 60>(m) : pow2_of<0, 1, 253>(m);
+}
 
 __device__ __forceinline__ uint32_t pack_half(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
@@ -163,7 +167,7 @@ __device__ __forceinline__ void store_terms(uint32_t hi_at, uint32_t lo_at, cons
 }
 
 // Raw fp32 rows become scaled fp16 operands in place; up[r] = the row's 2^e.  W / 8 neighbouring lanes hold a row.
-template <int W>
+template <int W, bool KEY>
 __device__ __forceinline__ void tile_scale(uint32_t tile, float* up, int tid, int nt) {
   constexpr int U = W / 8;
   for (int i = tid; i < kDC * U; i += nt) {  // nt and kDC * U are multiples of 32: whole warps
@@ -177,7 +181,7 @@ __device__ __forceinline__ void tile_scale(uint32_t tile, float* up, int tid, in
     for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
 #pragma unroll
     for (int o = 1; o < U; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const Pow2 s = token_scale(m);
+    const Pow2 s = token_scale<KEY>(m);
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] *= s.down;
     store_terms(a0, a1, x);

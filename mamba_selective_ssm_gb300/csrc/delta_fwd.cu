@@ -92,8 +92,8 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
     float* up = reinterpret_cast<float*>(raw + off + St::up);
     cp_wait<0>();
     __syncthreads();
-    tile_scale<KP>(at + St::k, up, tid, nt);
-    tile_scale<KP>(at + St::q, up + kDC, tid, nt);
+    tile_scale<KP, true>(at + St::k, up, tid, nt);
+    tile_scale<KP, false>(at + St::q, up + kDC, tid, nt);
     __syncthreads();
     if (stages == 2 && ck + 1 < nck) fetch(ck + 1);  // its place was read in the chunk before
     if (ckpt != nullptr) save(ck);

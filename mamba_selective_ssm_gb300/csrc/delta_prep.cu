@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(Delta p) {
   cp_wait<0>();
   __syncthreads();
   if constexpr (N == 2) {
-    tile_scale<KP>(sb + S::k, kup, tid, kPrepThreads);
-    tile_scale<KP>(sb + S::q, qup, tid, kPrepThreads);
+    tile_scale<KP, true>(sb + S::k, kup, tid, kPrepThreads);
+    tile_scale<KP, false>(sb + S::q, qup, tid, kPrepThreads);
     __syncthreads();
   }
   float* vec = p.vec + item * kDVec;

@@ -123,3 +123,34 @@ def test_decay_gradients_that_forget_in_every_layout(ss, dtype):
             off, size = np.linalg.norm(_np(got)[..., h] - ref[..., h]), np.linalg.norm(ref[..., h])
             assert off <= tol * size + 1e-30, (B, L, H, K, V, h, off / max(size, 1e-300), tol)
     assert ss.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("power", [-100, -80, -66, -30, 30, 66, 90])
+def test_values_and_gradients_of_any_size(ss, dtype, power):
+    """The forward is linear in q and in (v, h0), the backward in (do, dh_last): scaled by a power of two, each gives its results scaled
+    alike.  Beside 2^-100 the smallest terms of an operand, 2^-24 of it, are near the least normal number, and bf16 ones past
+    it: 2^-8 and 2^-16 of them are subnormal."""
+    import torch
+    from tests.test_gpu_deltarule import _bwd, _near, _np, _tol
+    d = _case(2, 150, 4, 2, 48, 40, dtype, seed=4)
+    f = 2.0 ** power
+    o, ckpt, h = _fwd(ss, d)
+    g = _bwd(ss, d, ckpt)
+    alone = _bwd(ss, d | {"dh_last": None}, ckpt)
+    tol = _tol(150, dtype, False, 3) * 2 + (2.0 ** -7 if dtype == "bf16" else 0.0)  # two results that round apart
+    e = d | {"do": d["do"] * f, "dh_last": d["dh_last"] * f}
+    for n, t in _bwd(ss, e, ckpt).items():
+        _near(t.double() / f, _np(g[n]), tol, f"do: {n}")
+    e = d | {"q": d["q"] * f}
+    o2, ckpt2, h2 = _fwd(ss, e)
+    assert torch.equal(h2, h)
+    _near(o2.double() / f, _np(o), tol, "q: o")
+    for n, t in _bwd(ss, e | {"dh_last": None}, ckpt2).items():
+        _near(t.double() / (1.0 if n == "dq" else f), _np(alone[n]), tol, f"q: {n}")
+    e = d | {"v": d["v"] * f, "h0": d["h0"] * f}
+    o2, ckpt2, h2 = _fwd(ss, e)
+    _near(o2.double() / f, _np(o), tol, "v: o")
+    _near(h2.double() / f, _np(h), tol, "v: h")
+    for n, t in _bwd(ss, e, ckpt2).items():
+        _near(t.double() / (1.0 if n in ("dv", "dh0") else f), _np(g[n]), tol, f"v: {n}")
