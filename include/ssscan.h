@@ -477,9 +477,12 @@ int linattn_step(const void* q, const void* k, const void* v, const float* g, in
  * Alignment: 16 bytes for every pointer but g, beta, lengths, dg, dbeta (4).
  *
  * deltarule_ckpt_size — floats that a checkpoint holds for each batch row and
- * head (0 on invalid sizes): the states entering each chunk and the last one,
- * two operands of 64 x 64 for each chunk, and in bf16 two values for every
- * element of v, which the fp32 gradients need.
+ * head (0 on invalid sizes).  With n = ceil(L / 64) chunks, for both types:
+ * n + 1 states of K * V, two values for every element of v of the n chunks, and
+ * for each chunk two operands of 64 x 64 and 272 scalars; an element of an
+ * operand is one float with fp32 activations, one and a half with bf16 ones:
+ *   (n + 1) K V + 128 n V + n (8192 + 272)     fp32
+ *   (n + 1) K V + 128 n V + n (12288 + 272)    bf16
  */
 size_t deltarule_ckpt_size(int L, int K, int V, int dtype);
 
