@@ -432,6 +432,7 @@ def _rows(t, name, shape, dtype, dev):
 @functools.lru_cache(maxsize=1024)
 def _linattn_plan(B, L, H, G, K, V, per_head, sdt):
     """(chunks, forward scratch, backward scratch) of a call's sizes."""
+    _int_sizes(B, L, H, G, K, V)
     lib = load()
     return (lib.linattn_num_chunks(L, sdt), lib.linattn_fwd_workspace_size(B, L, H, G, K, V, sdt),
             lib.linattn_bwd_workspace_size(B, L, H, G, K, V, per_head, sdt))
@@ -455,7 +456,7 @@ def _linattn_sizes(q, v):
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError(f"q, k must be [B, L, G, K] and v [B, L, H, V], got {tuple(q.shape)} and {tuple(v.shape)}")
     B, L, G, K = q.shape
-    return _int_sizes(B, L, v.shape[2], G, K, v.shape[3])
+    return B, L, v.shape[2], G, K, v.shape[3]
 
 
 def _linattn_gate(g, B, L, H, dev):
@@ -567,6 +568,7 @@ def deltarule_ckpt_size(L: int, K: int, V: int, dtype) -> int:
 @functools.lru_cache(maxsize=1024)
 def _deltarule_plan(B, L, H, G, K, V, sdt):
     """(floats of a checkpoint's row and head, forward scratch, backward scratch) of a call's sizes."""
+    _int_sizes(B, L, H, G, K, V)
     lib = load()
     return (lib.deltarule_ckpt_size(L, K, V, sdt), lib.deltarule_fwd_workspace_size(B, L, H, G, K, V, sdt),
             lib.deltarule_bwd_workspace_size(B, L, H, G, K, V, sdt))
@@ -696,6 +698,7 @@ def layernorm_bwd(dy, x, scale, mean, rstd, dscale=None, dbias=None, workspace=N
 @functools.lru_cache(maxsize=1024)
 def _groupnorm_plan(N, M, C, groups, sdt):
     """(forward scratch, backward scratch) of a call's sizes."""
+    _int_sizes(N, M, C, groups)
     lib = load()
     return lib.groupnorm_fwd_workspace_size(N, M, C, groups, sdt), lib.groupnorm_bwd_workspace_size(N, M, C, groups, sdt)
 
@@ -706,7 +709,7 @@ def _groupnorm_sizes(x):
         raise TypeError("x must be a torch.Tensor")
     if x.dim() < 2:
         raise ValueError(f"x must be [N, ..., C], got {tuple(x.shape)}")
-    return _int_sizes(x.shape[0], math.prod(x.shape[1:-1]), x.shape[-1])
+    return x.shape[0], math.prod(x.shape[1:-1]), x.shape[-1]
 
 
 def groupnorm_fwd(x, scale, bias, groups: int, eps: float, silu: bool = False, want_stats: bool = True, workspace=None):
@@ -718,10 +721,11 @@ def groupnorm_fwd(x, scale, bias, groups: int, eps: float, silu: bool = False, w
     dt = _act_dtype(x)
     px, ps = _at(x, "x", x.shape, x.dtype, dev), _at(scale, "scale", (C,), f32, dev)
     pb = _opt_at(bias, "bias", (C,), f32, dev)
+    need, _ = _groupnorm_plan(N, M, C, groups, dt)
     y = torch.empty_like(x)
     mean = torch.empty((N, groups), device=dev, dtype=f32) if want_stats else None
     rstd = torch.empty((N, groups), device=dev, dtype=f32) if want_stats else None
-    pw, have = _scratch(workspace, _groupnorm_plan(N, M, C, groups, dt)[0], dev)
+    pw, have = _scratch(workspace, need, dev)
     rc = load().groupnorm_fwd(px, ps, pb, eps, y.data_ptr(), mean.data_ptr() if want_stats else None,
                               rstd.data_ptr() if want_stats else None, N, M, C, groups, 1 if silu else 0, dt, pw, have,
                               _raw_stream(dev))
@@ -736,6 +740,7 @@ def groupnorm_bwd(dy, x, scale, bias, mean, rstd, groups: int, silu: bool = Fals
     N, M, C = _groupnorm_sizes(x)
     dev, f32 = x.device, torch.float32
     dt = _act_dtype(x)
+    _, need = _groupnorm_plan(N, M, C, groups, dt)
     py, px = _at(dy, "dy", x.shape, x.dtype, dev), _at(x, "x", x.shape, x.dtype, dev)
     ps, pb = _at(scale, "scale", (C,), f32, dev), _opt_at(bias, "bias", (C,), f32, dev)
     pm, pr = _at(mean, "mean", (N, groups), f32, dev), _at(rstd, "rstd", (N, groups), f32, dev)
@@ -745,7 +750,7 @@ def groupnorm_bwd(dy, x, scale, bias, mean, rstd, groups: int, silu: bool = Fals
     if dbias is None:
         dbias = torch.empty((C,), device=dev, dtype=f32)
     dx = torch.empty(x.shape, device=dev, dtype=f32)
-    pw, have = _scratch(workspace, _groupnorm_plan(N, M, C, groups, dt)[1], dev)
+    pw, have = _scratch(workspace, need, dev)
     rc = load().groupnorm_bwd(py, px, ps, pb, pm, pr, dx.data_ptr(), _at(dscale, "dscale", (C,), f32, dev),
                               _at(dbias, "dbias", (C,), f32, dev), add, N, M, C, groups, 1 if silu else 0, dt, pw, have,
                               _raw_stream(dev))
