@@ -23,7 +23,7 @@ using namespace ssk;
 
 // ---------------------------------------------------------------- the chain
 // As in the forward, a warp carries 16 columns of dS, transposed, from the last chunk to the first.  It leaves dS1 and du of
-// every chunk ([V][K] and [V][64], fp32) and dv.  8 x 2048 tokens of 24 heads of 64 x 64: 334 us.
+// every chunk ([V][K] and [V][64], fp32) and dv.  8 x 2048 tokens of 24 heads of 64 x 64: 338 us.
 template <int KP>
 struct BackStage {
   static constexpr int k = 0, q = k + DTile<KP, 2>::bytes, m = q + DTile<KP, 2>::bytes, p = m + kDMBytes,
@@ -283,7 +283,8 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
 // A CTA takes one (batch row, head, chunk).  First its warps take 16 columns of V each (with half of the tokens where V is 64
 // and less): what they add to dg and dbeta, from r and the state's part of o (the forward's), du and do.  Then they share the
 // products that contract over V, from tiles in shared memory scaled as a whole: u, dR, S0, dS1 lie [V][..].  8 x 2048 tokens of 24
-// heads of 64 x 64: 480 us, with decays 575 (tensor pipe 21 %, memory a quarter of its rate: the steps between barriers, at two CTAs an SM).
+// heads of 64 x 64: 470 us, with decays 565 (tensor pipe 24 %, memory a quarter of its rate: the steps between barriers, at two
+// CTAs an SM).
 template <int KP, int VP>
 struct GradSmem {
   static constexpr int N = 2, tile = DTile<KP, N>::bytes;

@@ -52,8 +52,8 @@ constexpr int kTerms = sizeof(T) == 4 ? 2 : 1;  // fp16 terms of an activation
 
 // What the forward leaves for the backward, floats of one (batch row, head): the state entering each chunk and the last one
 // (fp32: [V][K]; bf16: [K / 4][V][4]), then of every chunk r and, in bf16, o, else the state's part of o, all in fp32 (fp32:
-// [V][64]; bf16: [16][V][4]).  Behind all heads' lie M, P and the scalars of all chunks, so that the backward need not find them again (78 us at 4 x 2048 tokens of 32 heads of
-// 128 x 128, of a training step's 948).
+// [V][64]; bf16: [16][V][4]).  Behind all heads' lie M, P and the scalars of all chunks, so that the backward need not find them
+// again (78 us at 4 x 2048 tokens of 32 heads of 128 x 128, of a training step's 948 then).
 __host__ __device__ inline long long delta_ckpt_floats(int nck, int K, int V) {
   return (long long)(nck + 1) * K * V + 2ll * nck * kDC * V;
 }

@@ -9,8 +9,8 @@ using namespace ssk;
 
 // A warp walks the chunks of one (batch row, head) with 16 columns of the state in registers, transposed: rows are columns
 // of V, so that K S0, M (beta R), K^T u and o are products whose left operand is the accumulators of the one before, and the
-// warps of a CTA share nothing but the tiles of the chunk (k, q, M, P).  8 x 2048 tokens of 24 heads of 64 x 64: 363 us with r, o
-// and the states for the backward; the chain's latency bounds it at four warps a CTA (tensor pipe 18 %, issue slots 26 %).
+// warps of a CTA share nothing but the tiles of the chunk (k, q, M, P).  8 x 2048 tokens of 24 heads of 64 x 64: 378 us with r,
+// the state's part of o and the states for the backward; the chain's latency bounds it at four warps a CTA (tensor pipe 18 %, issue slots 26 %).
 template <int KP>
 struct WalkStage {
   static constexpr int k = 0, q = k + DTile<KP, 2>::bytes, m = q + DTile<KP, 2>::bytes, p = m + kDMBytes,

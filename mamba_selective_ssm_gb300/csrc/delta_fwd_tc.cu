@@ -7,8 +7,8 @@
 //   D2 = S Q^T, D4 = u P^T:  o = scale e^c D2 + D4, under the next chunk's D1
 // Sixteen warps compute, one issues the copies and MMAs; they meet at mbarriers with bounded waits.  With the left operand in
 // tensor memory an MMA of 64 columns takes 36 cycles, in shared memory 51.
-// 4 x 2048 tokens of 32 heads of 128 x 128: 143 us, with ckpt 191 (128 CTAs of 32 chunks, 4.5 and 6.0 us a chunk; tensor pipe
-// 22 %, memory 57 % with ckpt): the chain of a chunk's steps bounds it, reading sums and making terms of operands between the
+// 4 x 2048 tokens of 32 heads of 128 x 128: 145 us, with ckpt 192 (128 CTAs of 32 chunks, 4.5 and 6.0 us a chunk; with ckpt tensor
+// pipe 27 %, memory 57 %): the chain of a chunk's steps bounds it, reading sums and making terms of operands between the
 // products.
 #include "delta_tc.cuh"
 

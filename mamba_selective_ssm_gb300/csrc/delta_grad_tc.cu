@@ -4,13 +4,13 @@
 //   dbeta = <du, r>      dg_t = sum_{s >= t} (do_s.o_s - dR_s.v_s) + <S1, dS>           along columns of V, in fp32
 // In this dg each token's own write cancels, which leaves an error of 3e-7 of the terms, and dg is e^{g_t} of them.  A token that
 // forgets (g_t below kForget) takes the sum of what crosses it instead, as the fp32 kernel does (delta_bwd.cu), of the products
-// below: their operands of two terms leave 2 to 4e-6 of dg at any g, the other form 9e-7 at g = -1, 3e-6 at -2, 3e-5 at -4 and all at
-// -14.
+// below: their operands of two terms leave 2 to 4e-6 of dg at any g, the other form 9e-7 at g = -1, 3e-6 at -2, 3e-5 at -4 and
+// all at -14.  If every chunk has such a token the kernel takes 505 us for 420; chunks without one skip the work.
 //   E = scale D do u^T,  F = -D dR u^T (strict)                                          [t, s]
 //   dq = scale e^c do S0^T + E K      dk = -e^c dR S0^T + e^{c_last - c} u dS^T + E^T Q + (F + F^T) K
 // dq and dk are rounded to bf16; their fp32 operands are two rounded bf16 terms (2^-16).  Products run with the columns of K as the
 // 128 rows of an MMA; S0, dS, u and dR lie in shared memory by columns of V, as they come from memory, and are contracted down
-// their rows.  4 x 2048 tokens of 32 heads of 128 x 128: 415 us, 3.2 TB/s.  A CTA an SM (208 KB; tensor memory is taken whole),
+// their rows.  4 x 2048 tokens of 32 heads of 128 x 128: 420 us, 3.2 TB/s.  A CTA an SM (210 KB; tensor memory is taken whole),
 // whose steps wait for one another: the sums and operands along V a third of a chunk's time, the states' loads and terms a third.
 // A CTA for each chunk took 438 us, and where the heads' parts are added up (32 heads on 4, 128 x 64) 384 for 346.
 #include <algorithm>
@@ -22,12 +22,13 @@ namespace {
 using namespace ssk;
 
 constexpr int kGT = 512, kGGrid = 152;  // a CTA an SM, which goes from chunk to chunk
-constexpr float kForget = -2.f;
+constexpr float kForget = -2.f;  // where the two forms of dg are off by the same
 template <int KP>
 struct GradTc {
   static constexpr int NKP = KP / 64, ST = NKP * kPanel;  // bytes of a term of a state
   static constexpr int S = 0, u = S + 2 * ST, r = u + 2 * kPanel, dy = r + 2 * kPanel, k = dy + 2 * kTok, q = k + NKP * kTok, e = q + NKP * kTok,
-                       f = e + 2 * kDTerm, vec = f + 2 * kDTerm, dec = vec + kDVec * 4, red = dec + 2 * kDC * 4, fg = red + (16 * 8 + 32) * 4, bar = fg + 4 * 4;
+                       f = e + 2 * kDTerm, vec = f + 2 * kDTerm, dec = vec + kDVec * 4, red = dec + 2 * kDC * 4, fg = red + (16 * 8 + 32) * 4,
+                       bar = fg + 4 * 4;
   static constexpr int v = e;  // (v's tile, before E and F)
   static constexpr int x = r, cross = r + kPanel;  // X, and the sums of a, b and X, where dR's terms were
   static constexpr int kIn = 0, kM0 = 1, kM1 = 2, nbar = 3, tm = bar + nbar * 8, bytes = tm + 8;

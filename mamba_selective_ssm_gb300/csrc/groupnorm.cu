@@ -15,8 +15,8 @@
 // The variance is taken around the mean (in parts around the mean of a few rows at a time, joined with their means), never as a
 // difference of moments.  The backward's column sums are joined by colsum_kernel in fixed order.
 //
-// bf16 with SiLU, floors at 6.7 TB/s in brackets: 8192 x 1 x 4096 in 32 groups, forward 28 us (20; instructions of short rows:
-// 61 % of the issue slots), backward 50 + 6 (40); 4 x 2048 x 4096 forward 43 (20; x is read twice, the second time from L2 in
+// bf16 with SiLU, floors at 6.7 TB/s in brackets: 8192 x 1 x 4096 in 32 groups, forward 29 us (20; latency at four rows in flight a
+// lane: 61 % of the issue slots, 38 % of memory), backward 50 + 6 (40); 4 x 2048 x 4096 forward 43 (20; x is read twice, the second time from L2 in
 // part).  fp32, 8 x 2048 x 1536 in 24 groups, backward 89 (45; dy and x twice).  The forms at each other's sizes: the first of
 // these with a sample in a CTA 105 and 283 us; 4096 x 4 x 512 with a sample in a CTA 34 and 60, in parts 203 and 184;
 // 16 x 4 x 512 5.1 and 10, in parts 12.4 and 15; 8000 x 2 x 4096 136 and 410, in parts 1750 and 1890.
