@@ -472,7 +472,7 @@ int linattn_step(const void* q, const void* k, const void* v, const float* g, in
  * (states, dg, dbeta, dh0) or in o, which has the same bits with and without
  * ckpt, and two (2^-16) in dq and dk and in dg of tokens whose g is below -2.
  * With fp32 activations every operand is two scaled fp16 terms (22 bits).
- * dg_t carries e^{g_t}, and what it is off by does too: 5e-7 of a head's dg in
+ * dg_t carries e^{g_t}, and what it is off by does too: 8e-7 of a head's dg in
  * fp32 at any decay; in bf16 4e-7 e^{-g} down to g = -2, 4e-6 below.
  * Alignment: 16 bytes for every pointer but g, beta, lengths, dg, dbeta (4).
  *

@@ -23,7 +23,7 @@ using namespace ssk;
 
 // ---------------------------------------------------------------- the chain
 // As in the forward, a warp carries 16 columns of dS, transposed, from the last chunk to the first.  It leaves dS1 and du of
-// every chunk ([V][K] and [V][64], fp32) and dv.  8 x 2048 tokens of 24 heads of 64 x 64: 338 us.
+// every chunk ([V][K] and [V][64], fp32) and dv.  8 x 2048 tokens of 24 heads of 64 x 64: 348 us.
 template <int KP>
 struct BackStage {
   static constexpr int k = 0, q = k + DTile<KP, 2>::bytes, m = q + DTile<KP, 2>::bytes, p = m + kDMBytes,
@@ -103,10 +103,9 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
     float D[8][4];
     {
       const RowScale us = row_scale(U);
-#pragma unroll
-      for (int n = 0; n < 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) D[n][e] = 0.f;
+      float low[8][4];
+      clear(D);
+      clear(low);
 #pragma unroll
       for (int kb = 0; kb < KP / 16; ++kb) {
         uint32_t hi[4], lo[4];
@@ -116,9 +115,10 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
           uint32_t bb[N][4];
 #pragma unroll
           for (int n = 0; n < N; ++n) right_rows<KP, N>(bb[n], at + St::k, np, kb, n, lane);
-          mma_terms(D[2 * np], D[2 * np + 1], hi, lo, bb[0], bb[N - 1]);
+          mma_terms(D[2 * np], D[2 * np + 1], low[2 * np], low[2 * np + 1], hi, lo, bb[0], bb[N - 1]);
         }
       }
+      fold(D, low);
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
         const float2 re = *reinterpret_cast<const float2*>(vec + kDC + 8 * n + t2);
@@ -148,14 +148,17 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
       }
 #pragma unroll
       for (int np = 0; np < 4; ++np) {
-        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float c[2][4], d[2][4];
+        clear(c);
+        clear(d);
 #pragma unroll
         for (int kb = np; kb < 4; ++kb) {  // tokens from this one on
           uint32_t b0[4], b1[4];
           right_cols<kDC, 2>(b0, at + St::p, np, kb, 0, lane);
           right_cols<kDC, 2>(b1, at + St::p, np, kb, 1, lane);
-          mma_terms(c[0], c[1], hi[kb], lo[kb], b0, b1);
+          mma_terms(c[0], c[1], d[0], d[1], hi[kb], lo[kb], b0, b1);
         }
+        fold(c, d);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -178,14 +181,17 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
       for (int kb = 0; kb < 4; ++kb) left_terms(hi[kb], lo[kb], w[2 * kb], w[2 * kb + 1], ws);
 #pragma unroll
       for (int np = 0; np < 4; ++np) {
-        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float c[2][4], d[2][4];
+        clear(c);
+        clear(d);
 #pragma unroll
         for (int kb = np; kb < 4; ++kb) {
           uint32_t b0[4], b1[4];
           right_cols<kDC, 2>(b0, at + St::m, np, kb, 0, lane);
           right_cols<kDC, 2>(b1, at + St::m, np, kb, 1, lane);
-          mma_terms(c[0], c[1], hi[kb], lo[kb], b0, b1);
+          mma_terms(c[0], c[1], d[0], d[1], hi[kb], lo[kb], b0, b1);
         }
+        fold(c, d);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -243,17 +249,20 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
       const float whole = vec[4 * kDC];
 #pragma unroll
       for (int jp = 0; jp < KP / 16; ++jp) {
-        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float c[2][4], d[2][4];
+        clear(c);
+        clear(d);
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb) {
           uint32_t bb[N][4];
 #pragma unroll
           for (int n = 0; n < N; ++n) right_cols<KP, N>(bb[n], at + St::q, jp, kb, n, lane);
-          mma_terms(c[0], c[1], hi[kb], lo[kb], bb[0], bb[N - 1]);
+          mma_terms(c[0], c[1], d[0], d[1], hi[kb], lo[kb], bb[0], bb[N - 1]);
 #pragma unroll
           for (int n = 0; n < N; ++n) right_cols<KP, N>(bb[n], at + St::k, jp, kb, n, lane);
-          mma_terms(c[0], c[1], dh[kb], dl[kb], bb[0], bb[N - 1]);
+          mma_terms(c[0], c[1], d[0], d[1], dh[kb], dl[kb], bb[0], bb[N - 1]);
         }
+        fold(c, d);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -283,7 +292,7 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
 // A CTA takes one (batch row, head, chunk).  First its warps take 16 columns of V each (with half of the tokens where V is 64
 // and less): what they add to dg and dbeta, from r and the state's part of o (the forward's), du and do.  Then they share the
 // products that contract over V, from tiles in shared memory scaled as a whole: u, dR, S0, dS1 lie [V][..].  8 x 2048 tokens of 24
-// heads of 64 x 64: 470 us, with decays 565 (tensor pipe 24 %, memory a quarter of its rate: the steps between barriers, at two
+// heads of 64 x 64: 495 us, with decays 600 (tensor pipe 24 %, memory a quarter of its rate: the steps between barriers, at two
 // CTAs an SM).
 template <int KP, int VP>
 struct GradSmem {
@@ -343,11 +352,6 @@ __device__ __forceinline__ float2 tile_pair(uint32_t tile, int r, int u, int lan
   const float2 h = wide_half(hi), l = wide_half(lo);
   return make_float2(h.x + l.x, h.y + l.y);
 }
-// c += a b over one step
-__device__ __forceinline__ void mma_pair(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[2][4], const uint32_t (&b)[2][4]) {
-  mma_terms(c0, c1, a[0], a[1], b[0], b[1]);
-}
-
 template <int KP, int VP>
 __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_grad_kernel(Delta p, const float* __restrict__ ckpt,
                                                                   const float* __restrict__ dout,
@@ -551,23 +555,30 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
     for (int n = 0; n < 4; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) E[n][e] = F[n][e] = 0.f;
-    if (2 * half <= mb) {
+#pragma unroll
+    for (int np = 0; np < 2; ++np) {
+      if (2 * half + np > mb) continue;
+      float el[2][4], fl[2][4];
+      clear(el);
+      clear(fl);
       for (int kb = 0; kb < vb; ++kb) {
-        uint32_t ea[N][4], fa[N][4];
+        uint32_t ea[N][4], fa[N][4], bb[N][4];
 #pragma unroll
         for (int n = 0; n < N; ++n) {
           left_rows<VP, N>(ea[n], sb + Sm::doo, mb, kb, n, lane);
           left_cols<kDC, N>(fa[n], sb + Sm::r, mb, kb, n, lane);
+          right_cols<kDC, N>(bb[n], sb + Sm::u, 2 * half + np, kb, n, lane);
         }
-#pragma unroll
-        for (int np = 0; np < 2; ++np) {
-          uint32_t bb[N][4];
-#pragma unroll
-          for (int n = 0; n < N; ++n) right_cols<kDC, N>(bb[n], sb + Sm::u, 2 * half + np, kb, n, lane);
-          mma_pair(E[2 * np], E[2 * np + 1], ea, bb);
-          mma_pair(F[2 * np], F[2 * np + 1], fa, bb);
-        }
+        mma_terms(E[2 * np], E[2 * np + 1], el[0], el[1], ea[0], ea[1], bb[0], bb[1]);
+        mma_terms(F[2 * np], F[2 * np + 1], fl[0], fl[1], fa[0], fa[1], bb[0], bb[1]);
       }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          E[2 * np + i][e] += el[i][e];
+          F[2 * np + i][e] += fl[i][e];
+        }
     }
 #pragma unroll
     for (int n = 0; n < 4; ++n)
@@ -583,9 +594,11 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
     if (dg != nullptr) {
 #pragma unroll
       for (int np = 0; np < 2; ++np) {
-        float qk[2][4], kk[2][4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) qk[0][e] = qk[1][e] = kk[0][e] = kk[1][e] = 0.f;
+        float qk[2][4], kk[2][4], ql[2][4], kl[2][4];
+        clear(qk);
+        clear(kk);
+        clear(ql);
+        clear(kl);
         if (2 * half + np <= mb)
 #pragma unroll 1
           for (int kb = 0; kb < KP / 16; ++kb) {
@@ -596,9 +609,11 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
               left_rows<KP, N>(ka[n], sb + Sm::k, mb, kb, n, lane);
               right_rows<KP, N>(bb[n], sb + Sm::k, 2 * half + np, kb, n, lane);
             }
-            mma_pair(qk[0], qk[1], qa, bb);
-            mma_pair(kk[0], kk[1], ka, bb);
+            mma_terms(qk[0], qk[1], ql[0], ql[1], qa[0], qa[1], bb[0], bb[1]);
+            mma_terms(kk[0], kk[1], kl[0], kl[1], ka[0], ka[1], bb[0], bb[1]);
           }
+        fold(qk, ql);
+        fold(kk, kl);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -615,15 +630,14 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
     }
   }
   // dq and dk: a warp's 16 tokens and half of the columns of K
-  float Q[NC][4], Kg[NC][4], C[NC][4];
+  float Q[NC][4], Kg[NC][4], C[NC][4], Cl[NC][4];
   const int ta = 16 * mb + g, tb = ta + 8;
   auto zero = [&] {
-#pragma unroll
-    for (int j = 0; j < NC; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) C[j][e] = 0.f;
+    clear(C);
+    clear(Cl);
   };
   auto add = [&](float (&to)[NC][4], float fa, float fb, bool first) {
+    fold(C, Cl);
 #pragma unroll
     for (int j = 0; j < NC; ++j)
 #pragma unroll
@@ -658,7 +672,7 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
       uint32_t bb[N][4];
 #pragma unroll
       for (int n = 0; n < N; ++n) right_cols<KP, N>(bb[n], tile, half * (NC / 2) + jp, kb, n, lane);
-      mma_pair(C[2 * jp], C[2 * jp + 1], la, bb);
+      mma_terms(C[2 * jp], C[2 * jp + 1], Cl[2 * jp], Cl[2 * jp + 1], la[0], la[1], bb[0], bb[1]);
     }
   };
   if constexpr (Sm::turns) {

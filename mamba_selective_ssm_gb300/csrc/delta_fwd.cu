@@ -99,11 +99,9 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
     if (ckpt != nullptr) save(ck);
     const RowScale ss = row_scale(S);
     // R^T = v^T - e^c (K S0)^T
-    float R[8][4];
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) R[n][e] = 0.f;
+    float R[8][4], low[8][4];
+    clear(R);
+    clear(low);
 #pragma unroll
     for (int kb = 0; kb < KP / 16; ++kb) {
       uint32_t hi[4], lo[4];
@@ -113,9 +111,10 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
         uint32_t bb[N][4];
 #pragma unroll
         for (int n = 0; n < N; ++n) right_rows<KP, N>(bb[n], at + St::k, np, kb, n, lane);
-        mma_terms(R[2 * np], R[2 * np + 1], hi, lo, bb[0], bb[N - 1]);
+        mma_terms(R[2 * np], R[2 * np + 1], low[2 * np], low[2 * np + 1], hi, lo, bb[0], bb[N - 1]);
       }
     }
+    fold(R, low);
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
       float x[2][4];
@@ -147,14 +146,17 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
       for (int kb = 0; kb < 4; ++kb) left_terms(hi[kb], lo[kb], w[2 * kb], w[2 * kb + 1], ws);
 #pragma unroll
       for (int np = 0; np < 4; ++np) {
-        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float c[2][4], d[2][4];
+        clear(c);
+        clear(d);
 #pragma unroll
         for (int kb = 0; kb <= np; ++kb) {  // tokens up to this one
           uint32_t b0[4], b1[4];
           right_rows<kDC, 2>(b0, at + St::m, np, kb, 0, lane);
           right_rows<kDC, 2>(b1, at + St::m, np, kb, 1, lane);
-          mma_terms(c[0], c[1], hi[kb], lo[kb], b0, b1);
+          mma_terms(c[0], c[1], d[0], d[1], hi[kb], lo[kb], b0, b1);
         }
+        fold(c, d);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int n = 2 * np + i, t = 8 * n + t2;
@@ -172,11 +174,9 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
       }
     }
     {  // o^T = scale (e^c (Q S0)^T + u^T P^T)
-      float O[8][4];
-#pragma unroll
-      for (int n = 0; n < 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) O[n][e] = 0.f;
+      float O[8][4], low[8][4];
+      clear(O);
+      clear(low);
 #pragma unroll
       for (int kb = 0; kb < KP / 16; ++kb) {
         uint32_t sh[4], sl[4];
@@ -186,9 +186,10 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
           uint32_t bb[N][4];
 #pragma unroll
           for (int n = 0; n < N; ++n) right_rows<KP, N>(bb[n], at + St::q, np, kb, n, lane);
-          mma_terms(O[2 * np], O[2 * np + 1], sh, sl, bb[0], bb[N - 1]);
+          mma_terms(O[2 * np], O[2 * np + 1], low[2 * np], low[2 * np + 1], sh, sl, bb[0], bb[N - 1]);
         }
       }
+      fold(O, low);
       const RowScale us = row_scale(R);
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb) {
@@ -197,14 +198,17 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
       const int t0 = ck * kDC, rows = a.L - t0 < kDC ? a.L - t0 : kDC;
 #pragma unroll
       for (int np = 0; np < 4; ++np) {
-        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float c[2][4], d[2][4];
+        clear(c);
+        clear(d);
 #pragma unroll
         for (int kb = 0; kb <= np; ++kb) {
           uint32_t bb[N][4];
 #pragma unroll
           for (int n = 0; n < N; ++n) right_rows<kDC, N>(bb[n], at + St::p, np, kb, n, lane);
-          mma_terms(c[0], c[1], hi[kb], lo[kb], bb[0], bb[N - 1]);
+          mma_terms(c[0], c[1], d[0], d[1], hi[kb], lo[kb], bb[0], bb[N - 1]);
         }
+        fold(c, d);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int n = 2 * np + i, t = 8 * n + t2;
@@ -241,14 +245,17 @@ __global__ void __launch_bounds__(kWalkThreads) delta_fwd_kernel(Delta p, const 
       const float whole = vec[4 * kDC];
 #pragma unroll
       for (int jp = 0; jp < KP / 16; ++jp) {
-        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float c[2][4], d[2][4];
+        clear(c);
+        clear(d);
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb) {
           uint32_t bb[N][4];
 #pragma unroll
           for (int n = 0; n < N; ++n) right_cols<KP, N>(bb[n], at + St::k, jp, kb, n, lane);
-          mma_terms(c[0], c[1], hi[kb], lo[kb], bb[0], bb[N - 1]);
+          mma_terms(c[0], c[1], d[0], d[1], hi[kb], lo[kb], bb[0], bb[N - 1]);
         }
+        fold(c, d);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float(&s)[4] = S[2 * jp + i];

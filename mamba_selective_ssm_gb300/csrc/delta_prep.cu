@@ -159,7 +159,9 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(Delta p) {
   const float ps = N == 2 ? 1.f : a.scale;
 #pragma unroll
   for (int np = 0; np < 4; ++np) {
-    float qk[2][4];
+    float qk[2][4], kl[2][4], ql[2][4];
+    clear(kl);
+    clear(ql);
 #pragma unroll
     for (int e = 0; e < 4; ++e) kk[2 * np][e] = kk[2 * np + 1][e] = qk[0][e] = qk[1][e] = 0.f;
     if (np > warp) {
@@ -188,8 +190,16 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(Delta p) {
         mma_bf16(qk[0], qa[0], bb[0][0], bb[0][1]);
         mma_bf16(qk[1], qa[0], bb[0][2], bb[0][3]);
       } else {
-        mma_terms(kk[2 * np], kk[2 * np + 1], ka[0], ka[N - 1], bb[0], bb[N - 1]);
-        mma_terms(qk[0], qk[1], qa[0], qa[N - 1], bb[0], bb[N - 1]);
+        mma_terms(kk[2 * np], kk[2 * np + 1], kl[0], kl[1], ka[0], ka[N - 1], bb[0], bb[N - 1]);
+        mma_terms(qk[0], qk[1], ql[0], ql[1], qa[0], qa[N - 1], bb[0], bb[N - 1]);
+      }
+    }
+    if constexpr (N == 2) {
+      fold(qk, ql);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        kk[2 * np][e] += kl[0][e];
+        kk[2 * np + 1][e] += kl[1][e];
       }
     }
 #pragma unroll

@@ -154,3 +154,21 @@ def test_values_and_gradients_of_any_size(ss, dtype, power):
     _near(h2.double() / f, _np(h), tol, "v: h")
     for n, t in _bwd(ss, e, ckpt2).items():
         _near(t.double() / (1.0 if n in ("dv", "dh0") else f), _np(g[n]), tol, f"v: {n}")
+
+
+@pytest.mark.parametrize("seed", [1, 2, 3])
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 128)])
+def test_fp32_sums_are_cut_once_a_step(ss, K, V, seed):
+    """fp32, no decay, beta up to 2.  A product of K = 128 is 8 steps, each cut once, by 2^-24 of the sum on average, and its two
+    operands' terms leave four times that in the mean square (2^-22 at most, 2^-23 on average, each); three products a chunk, over n
+    chunks and one more, as independent errors: (3 (8 + 4) (n + 1))^(1/2) 2^-24.  (Cut three times a step, 24 for 8.)"""
+    from oracle.deltarule import deltarule_fwd_ref
+    from tests.test_gpu_deltarule import _np
+    L = 256
+    d = _case(2, L, 4, 4, K, V, "f32", decay=False, carry=False, seed=seed)
+    o, _, h = _fwd(ss, d)
+    ro, rS = deltarule_fwd_ref(*[_np(d[x]) for x in ("q", "k", "v", "g", "beta")])
+    tol = (3 * (8 + 4) * (L // 64 + 1)) ** 0.5 * 2.0 ** -24
+    for name, got, ref in (("o", o, ro), ("h_last", h, rS[:, -1])):
+        off = np.linalg.norm(_np(got) - ref) / np.linalg.norm(ref)
+        assert off <= tol, (name, off, tol)
