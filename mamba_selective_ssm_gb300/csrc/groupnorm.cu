@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_bwd_sample_kernel(Gn p, int 
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int g = my.group(e);
-        da[e] = rv[g] * (da[e] * sc[e] - st[g] - xh[e] * st[p.groups + g]);
+        // (w and its mean, each rounded, first: in a group of one value they are the same, and dx is 0)
+        da[e] = rv[g] * fmaf(-xh[e], st[p.groups + g], __fsub_rn(__fmul_rn(da[e], sc[e]), st[g]));
       }
       ActT<float>::st8(dx + (n * p.M + my.m) * p.C + my.u * 8, da);
     }
@@ -787,8 +788,8 @@ __global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_apply_kernel(Gn p, Part 
     const float2 a = means[g], b = means[h];
     mu[e] = f2(-mean[g], -mean[h]);
     rv[e] = f2(rstd[g], rstd[h]);
-    k0[e] = mul2(rv[e], f2(-a.x, -b.x));
-    k1[e] = mul2(rv[e], f2(-a.y, -b.y));
+    k0[e] = f2(-a.x, -b.x);
+    k1[e] = f2(-a.y, -b.y);
   }
   constexpr int A = kGnAhead<T> / 2;
   const long long base = w.n * p.M * p.C + w.c;
@@ -810,8 +811,10 @@ __global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_apply_kernel(Gn p, Part 
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         xh[e] = mul2(add2(xh[e], mu[e]), rv[e]);
-        da[e] = mul2(dact2<SILU>(da[e], fma2(xh[e], sc[e], bi[e])), sc[e]);
-        da[e] = fma2(rv[e], da[e], fma2(xh[e], k1[e], k0[e]));
+        da[e] = dact2<SILU>(da[e], fma2(xh[e], sc[e], bi[e]));
+        // w - mean w first, as above (in scalars: a packed product and sum are made one)
+        da[e] = f2(__fadd_rn(__fmul_rn(da[e].x, sc[e].x), k0[e].x), __fadd_rn(__fmul_rn(da[e].y, sc[e].y), k0[e].y));
+        da[e] = mul2(rv[e], fma2(xh[e], k1[e], da[e]));
       }
       st4_last<float>(dx + base + (long long)(m - u * w.lanes) * p.C, da);
     }

@@ -65,3 +65,23 @@ def test_statistics_of_rows_unlike_one_another(ss, N, M, C, groups, dtype, kind)
     _near(rstd, _np(torch.stack(rstds)), tol + (off * tol) ** 2, "rstd")
     typed = 2.0 ** -8 if dtype == "bf16" else 0.0
     assert total ** 0.5 <= (tol * (1 + off) + typed) * max(size, N * M * C * 1e-6) ** 0.5, (total ** 0.5, size ** 0.5)
+
+
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,C", [(1, 8), (1834, 8), (300, 520), (3, 8192), (5, 16384)])
+def test_groups_of_one_value(ss, N, C, dtype, silu):
+    """A group of one value: y is act(bias) whatever x is, so dx and dscale are 0 and nothing near it, and rstd is eps^(-1/2)."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(C + N)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x, dy = (3 * torch.randn(N, 1, C, device="cuda", generator=gen).to(dt) for _ in range(2))
+    scale, bias = (torch.randn(C, device="cuda", generator=gen) for _ in range(2))
+    y, mean, rstd = ss.groupnorm_fwd(x, scale, bias, C, 1e-5, silu=silu)
+    b = bias.double()
+    want = (b / (1 + torch.exp(-b)) if silu else b).expand(N, 1, C)
+    assert torch.equal(mean, x.float()[:, 0])
+    assert ((rstd.double() - 1e-5 ** -0.5).abs() <= 4 * 2.0 ** -24 * 1e-5 ** -0.5).all()
+    assert ((y.double() - want).abs() <= (2.0 ** -20 + (2.0 ** -8 if dtype == "bf16" else 0.0)) * want.abs()).all()
+    dx, dscale, _ = ss.groupnorm_bwd(dy, x, scale, bias, mean, rstd, C, silu=silu)
+    assert (dx == 0).all() and (dscale == 0).all()
