@@ -570,8 +570,9 @@ int layernorm_bwd(const void* dy, const void* x, const float* scale, const float
  *   mean, rstd  : [N, groups] fp32 outputs, each may be NULL
  * M = 1 is the norm of each token's groups (the heads of a layer's output),
  * M = L that of whole sequences.  C a multiple of 8 and of groups, at most
- * 32768; N * groups below 2^31, N * M * C at most 2^40; eps >= 0.  x, y, scale,
- * bias 16-byte aligned, mean and rstd 4.
+ * 32768, or 2^20 in groups of at most 256 channels; N * groups below 2^31,
+ * N * M * C at most 2^40; eps >= 0.  x, y, scale, bias 16-byte aligned, mean
+ * and rstd 4.
  * Statistics are fp32, the deviations taken around a mean; the reciprocal root
  * is the hardware's (2 units in the last place).  Sums are in a fixed order.
  * workspace: groupnorm_fwd_workspace_size() bytes (0 when a CTA holds a sample).

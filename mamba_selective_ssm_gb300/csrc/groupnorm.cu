@@ -28,7 +28,7 @@ namespace {
 
 using namespace ssk;
 
-constexpr int kGnMaxDim = 32768;
+constexpr int kGnMaxDim = 32768, kGnNarrow = 256, kGnMaxNarrow = 1 << 20;  // widest samples: in any groups, in groups of at most 256 channels
 constexpr int kGnThreads = 256;
 constexpr int kGnMost = 2147483647 - (1 << 22);  // samples or positions: a thread's next ones are still an int
 constexpr int kGnSampleDim = 8192;  // widest sample of the one-CTA form
@@ -836,7 +836,8 @@ struct GnPlan {
 };
 
 int gn_plan(int N, int M, int C, int groups, int dtype, GnPlan& pl) {
-  if (N <= 0 || M <= 0 || C <= 0 || groups <= 0 || C > kGnMaxDim || C % groups != 0) return SS_ERR_DIM;
+  if (N <= 0 || M <= 0 || C <= 0 || groups <= 0 || C % groups != 0) return SS_ERR_DIM;
+  if (C > (C / groups <= kGnNarrow ? kGnMaxNarrow : kGnMaxDim)) return SS_ERR_DIM;
   if (dtype != SS_F32 && dtype != SS_BF16) return SS_ERR_UNSUPPORTED;
   if (C % 8 != 0) return SS_ERR_ALIGN;
   if (N > kGnMost || M > kGnMost) return SS_ERR_DIM;

@@ -85,3 +85,27 @@ def test_groups_of_one_value(ss, N, C, dtype, silu):
     assert ((y.double() - want).abs() <= (2.0 ** -20 + (2.0 ** -8 if dtype == "bf16" else 0.0)) * want.abs()).all()
     dx, dscale, _ = ss.groupnorm_bwd(dy, x, scale, bias, mean, rstd, C, silu=silu)
     assert (dx == 0).all() and (dscale == 0).all()
+
+
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,M,C,groups", [(3, 1, 259080, 1016), (2, 1, 65536, 256), (5, 1, 1 << 20, 1 << 17), (2, 3, 40000, 5000), (1, 40, 100000, 2500),
+                                          (2, 2, 32776, 8194)])
+def test_wide_samples_in_narrow_groups(ss, N, M, C, groups, dtype, silu):
+    """More than 32768 channels in groups of at most 256, forward and backward."""
+    from oracle.groupnorm import groupnorm_bwd_ref, groupnorm_fwd_ref
+    from tests.test_gpu_groupnorm import _case
+    d = _case(N, M, C, dtype, seed=C, bias=silu)
+    x = _np(d["x"])
+    y, mean, rstd = ss.groupnorm_fwd(d["x"], d["scale"], d["bias"], groups, 1e-2, silu=silu)
+    ry, rm, rr = groupnorm_fwd_ref(x, _np(d["scale"]), _np(d["bias"]), groups, 1e-2, silu)
+    tol, typed = STEP * (2 * (M + 32) ** 0.5 + 24), 2.0 ** -8 if dtype == "bf16" else 0.0
+    _near(y, ry, tol + typed, "y")
+    _near(mean, rm, tol, "mean", size=np.sqrt(np.mean(x * x)))
+    _near(rstd, rr, tol, "rstd")
+    dx, ds, db = ss.groupnorm_bwd(d["dy"], d["x"], d["scale"], d["bias"], mean, rstd, groups, silu=silu)
+    rdx, rds, rdb = groupnorm_bwd_ref(_np(d["dy"]), x, _np(d["scale"]), _np(d["bias"]), _np(mean), _np(rstd), silu)
+    cols = STEP * (4 * (N * M) ** 0.5 + 64)
+    _near(dx, rdx, 2 * tol, "dx", size=max(np.sqrt(np.mean(rdx ** 2)), np.sqrt(np.mean(_np(d["dy"]) ** 2)) * np.abs(_np(rstd)).max() if M * (C // groups) < 8 else 0.0))
+    _near(ds, rds, cols, "dscale")
+    _near(db, rdb, cols, "dbias")
