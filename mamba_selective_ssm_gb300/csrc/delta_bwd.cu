@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kWalkThreads) delta_bwd_kernel(Delta p, const 
 // A CTA takes one (batch row, head, chunk).  First its warps take 16 columns of V each (with half of the tokens where V is 64
 // and less): what they add to dg and dbeta, from r and the state's part of o (the forward's), du and do.  Then they share the
 // products that contract over V, from tiles in shared memory scaled as a whole: u, dR, S0, dS1 lie [V][..].  8 x 2048 tokens of 24
-// heads of 64 x 64: 495 us, with decays 600 (tensor pipe 24 %, memory a quarter of its rate: the steps between barriers, at two
+// heads of 64 x 64: 495 us, with decays 600 (tensor pipe 22 %, memory a quarter of its rate: the steps between barriers, at two
 // CTAs an SM).
 template <int KP, int VP>
 struct GradSmem {
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(kGradThreads, (GradSmem<KP, VP>::ctas)) delta_
     }
   };
   if constexpr (Sm::turns) {
-    __syncthreads();  // (k and q were read by tile_scale alone; all are past that)
+    __syncthreads();  // (k and q have been read by tile_scale and for X)
     put_state(scS.down);
     __syncthreads();
   }

@@ -1,7 +1,7 @@
 // What the gated delta rule's chunks need and no state enters: M, P and the scalars of every chunk (delta_common.cuh).
 // A CTA takes one (batch row, head, chunk): 4096 chunks with K = 128 in bf16 take 78 us, 6144 with K = 64 in fp32 140 us.  What
-// bounds it is instructions and their latency at the six CTAs of four warps an SM that shared memory leaves for these (half of the
-// issue slots; the substitution a third of the time, the 64 x 64 decays a fifth), not memory (150 MB, a quarter of its rate).
+// bounds it is instructions and their latency at six CTAs of four warps an SM (shared memory) and five (registers): half of the issue
+// slots; the substitution a third of the time, the 64 x 64 decays a fifth.  Memory is at a quarter of its rate (150 MB).
 #include "delta_common.cuh"
 
 namespace {
